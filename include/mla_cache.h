@@ -12,7 +12,11 @@
  *      with the conditional dtype cast, then the fused [k_nope | k_pe] key and V
  *      pack ("PR #51772 [Attention][MLA] Fuse Kimi-K3 chunked-context K/V
  *      packing", Implementation items 1-2 and Source snippets:
- *      fused_mla_kv_concat / fused_mla_kv_concat_quant_fp8).
+ *      fused_mla_kv_concat / fused_mla_kv_concat_quant_fp8);
+ *   3. what a serving loop runs on these caches next: the attention of new
+ *      tokens over the paged latent rows, the join of attention results over
+ *      parts of the context, and the copying, forking, compacting and clearing
+ *      of cache blocks.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -74,7 +78,13 @@ typedef struct CUstream_st* mla_stream_t;
  * kv_b_proj output into the pack, and the gather's widening for an fp16
  * kv_b_proj input ("PR #51772", Review: bf16 and fp16 inputs); the grouped
  * insert takes bf16 input and bf16 / fp8 caches only. */
-typedef enum { MLA_BF16 = 0, MLA_FP8_E4M3 = 1, MLA_FP8_E5M2 = 2, MLA_FP16 = 3 } mla_dtype_t;
+typedef enum {
+  MLA_BF16 = 0,
+  MLA_FP8_E4M3 = 1,
+  MLA_FP8_E5M2 = 2,
+  MLA_FP16 = 3,
+  MLA_FP32 = 4 /* the states of mla_merge_attn_states only */
+} mla_dtype_t;
 
 typedef enum {
   MLA_OK = 0,
@@ -504,6 +514,150 @@ mla_status_t mla_norm_rope_grouped(
  */
 mla_status_t mla_rope_cos_sin_cache(float* out, int64_t max_position, int32_t rot_dim,
                                     double base, mla_stream_t stream);
+
+/*
+ * Copy, fork, compact or clear whole blocks of the paged caches of every layer
+ * in ONE launch, next to the grouped insert that fills them ("PR #55356",
+ * Source snippets: the per-layer cache pointer array and the shared block
+ * layout).  For every layer l < num_layers and copy i < num_copies, with
+ * n = row_counts[i] (block_size when row_counts is NULL): the entries
+ *   cache_l[dst_blocks[i] * block_stride + r * entry_stride + e],
+ *   r < n, e < entry_dim,
+ * become those of src_blocks[i], or zero bytes where src_blocks[i] == -1.
+ * Everything else (rows n.., padding between entries and blocks, other blocks)
+ * is left as it was.
+ *   - copying / compacting: whole blocks to free ones (the caller rewrites its
+ *     block tables);
+ *   - forking: a block may be the source of any number of copies; the last,
+ *     part-filled block of a sequence is copied with its row count;
+ *   - freeing: src -1 clears a block before it is handed out again.
+ * A copy with dst_blocks[i] == -1 or n == 0 is padding and is skipped, and so
+ * is one with dst == src.  A block that is the destination of one copy must
+ * be neither destination nor source of another (its contents are unspecified
+ * otherwise); caches of different layers must not overlap.
+ *
+ *   kv_cache_ptrs       int64 device array [num_layers], as in the grouped
+ *                       insert; a null or misaligned base skips the layer
+ *                       (MLA_ERRBIT_MISALIGNED).  At most 128 layers.
+ *   cache_dtype         MLA_BF16, MLA_FP8_E4M3 or MLA_FP8_E5M2.
+ *   entry_dim           elements of an entry that are copied, a multiple of 16
+ *                       bytes.
+ *   src_blocks, dst_blocks  int32 device [num_copies]; an id below -1 or not
+ *                       below num_blocks skips the copy (MLA_ERRBIT_BLOCK_OOB).
+ *   row_counts          int32 device [num_copies] or NULL; a count outside
+ *                       [0, block_size] skips the copy (MLA_ERRBIT_BLOCK_OOB).
+ */
+mla_status_t mla_cache_copy_blocks(const int64_t* kv_cache_ptrs, int32_t num_layers,
+                                   mla_dtype_t cache_dtype, int64_t num_blocks,
+                                   int32_t block_size, int64_t block_stride,
+                                   int64_t entry_stride, int32_t entry_dim,
+                                   const int32_t* src_blocks, const int32_t* dst_blocks,
+                                   const int32_t* row_counts, int32_t num_copies,
+                                   uint32_t* err_word, mla_stream_t stream);
+
+/*
+ * Attention of new tokens over the paged latent cache, in the absorbed MLA
+ * form: kv_b_proj's key half is already multiplied into the query, so every
+ * head of a token attends to the same cache rows [kv_c | k_pe], and the first
+ * kv_lora_rank columns of a row are also its value ("PR #55356" fills these
+ * rows, "PR #51772" Implementation item 2 reads them through the same block
+ * table).  One call takes any mixture of single-token (decode), few-token
+ * (verification) and many-token (chunked prefill) sequences.
+ *
+ * Sequence s < num_seqs owns the tokens [cu_q_lens[s], cu_q_lens[s+1]), n of
+ * them, and has kv_lens[s] cache rows, its new tokens' own rows included;
+ * row p is entry p % block_size of block block_table[s * block_table_stride +
+ * p / block_size].  Its token number j (from 0) sees the rows
+ *   p < kv_lens[s]                        causal == 0
+ *   p < kv_lens[s] - n + 1 + j            causal != 0
+ * and for each head h, with q = [q_c[t, h] | q_pe[t, h]],
+ *   x_p       = softmax_scale * sum_e q[e] * row_p[e]
+ *   lse[t,h]  = ln(sum_p exp(x_p))
+ *   out[t,h]  = sum_p exp(x_p - lse[t,h]) * row_p[0:kv_lora_rank]
+ * where row_p is the stored bf16 row, or an fp8 row's values times *k_scale.  A
+ * token that sees no row has out = 0 and lse = -infinity.  A row that a token
+ * does not see has no influence on its result, whatever the row holds; the
+ * result of a token that sees a row with a NaN or an infinity is not specified.
+ *
+ * Arithmetic: products of bf16 values (fp8 ones are exact in bf16) summed in
+ * fp32, softmax in fp32; the weights exp(x_p - max) are rounded to bf16 before
+ * they multiply the rows, the sums stay in fp32, and the result is rounded once
+ * to bf16.  Results do not depend on other work on the device; on the call's
+ * shape (num_tokens, num_seqs, num_heads) and lengths they depend through the
+ * order of fp32 sums only.
+ *
+ *   q_c, q_pe           bf16; element (t, h, e) at t * token_stride +
+ *                       h * head_stride + e; rows start on 16-byte boundaries.
+ *                       A [T, H, 576] query: q_c = base, q_pe = base + 512.
+ *   num_tokens          rows of q and out; tokens owned by no sequence, and
+ *                       those numbered num_tokens and above, are not touched.
+ *   num_heads           1 to 1024.
+ *   kv_lora_rank, pe_dim  must be 512 and 64 (else UNSUPPORTED).
+ *   kv_cache ... block_table_stride  the paged cache, as in mla_context_gather;
+ *                       cache_dtype MLA_BF16, MLA_FP8_E4M3 or MLA_FP8_E5M2.  A
+ *                       seen row whose block id is out of range, or whose block
+ *                       index is outside the table's row, is left out of the
+ *                       sums (MLA_ERRBIT_BLOCK_OOB).
+ *   cu_q_lens           int32 device [num_seqs + 1], non-decreasing.
+ *   kv_lens             int32 device [num_seqs].
+ *   num_seqs            1 to 4096.
+ *   softmax_scale       finite; applies to the dequantised product.
+ *   k_scale             device fp32 scalar: required for an fp8 cache, must be
+ *                       NULL for a bf16 cache.
+ *   out                 bf16 [T, H, kv_lora_rank] by strides, rows on 16-byte
+ *                       boundaries.
+ *   lse                 fp32 [T, H] by strides, or NULL.
+ *   workspace           16-byte aligned device memory of workspace_bytes >=
+ *                       what mla_latent_attention_workspace gives.  Its contents before and after a call
+ *                       mean nothing; calls that may run at the same time (on
+ *                       two streams) need one each.
+ */
+mla_status_t mla_latent_attention(
+    const void* q_c, int64_t qc_token_stride, int64_t qc_head_stride, const void* q_pe,
+    int64_t qpe_token_stride, int64_t qpe_head_stride, int32_t num_tokens, int32_t num_heads,
+    int32_t kv_lora_rank, int32_t pe_dim, const void* kv_cache, mla_dtype_t cache_dtype,
+    int64_t num_blocks, int32_t block_size, int64_t block_stride, int64_t entry_stride,
+    const int32_t* block_table, int64_t block_table_stride, const int32_t* cu_q_lens,
+    const int32_t* kv_lens, int32_t num_seqs, float softmax_scale, const float* k_scale,
+    int32_t causal, void* out, int64_t out_token_stride, int64_t out_head_stride, float* lse,
+    int64_t lse_token_stride, int64_t lse_head_stride, void* workspace, int64_t workspace_bytes,
+    uint32_t* err_word, mla_stream_t stream);
+
+/* Writes to *bytes (host memory) the workspace that mla_latent_attention needs
+ * on the current device for any call of at most num_tokens tokens, num_heads
+ * heads and num_seqs sequences.  Host only. */
+mla_status_t mla_latent_attention_workspace(int32_t num_tokens, int32_t num_heads,
+                                            int32_t num_seqs, int64_t* bytes);
+
+/*
+ * Join attention results over disjoint parts of the context: the step that
+ * ends the chunked-context loop ("PR #51772", Implementation items 1-2: each
+ * chunk's packed K/V gives a partial result), and that joins a shared prefix
+ * with each sequence's own suffix (mla_latent_attention over each).  For every
+ * token t, head h, with parts i < num_parts,
+ *   lse_out[t,h]    = ln(sum_i exp(lse_i[t,h]))
+ *   out[t,h,:]      = sum_i exp(lse_i[t,h] - lse_out[t,h]) * part_i[t,h,:]
+ * in fp32, rounded once to dtype.  A part whose lse is -infinity has no
+ * influence, whatever its row holds; when every part's is, out = 0 and lse_out
+ * = -infinity.  A lse of +infinity or NaN gives NaN.
+ *
+ *   parts               element (i, t, h, e) at i * part_stride +
+ *                       t * token_stride + h * head_stride + e, of type dtype;
+ *                       rows start on 16-byte boundaries.
+ *   lse                 fp32, element (i, t, h) at i * lse_part_stride +
+ *                       t * lse_token_stride + h * lse_head_stride.
+ *   dtype               MLA_BF16, MLA_FP16 or MLA_FP32 (parts and out).
+ *   dim                 elements of a row, a multiple of 16 bytes.
+ *   out                 by its own strides, rows on 16-byte boundaries.
+ *   lse_out             fp32 by its own strides, or NULL.
+ *   num_parts           1 to 1024.
+ */
+mla_status_t mla_merge_attn_states(
+    const void* parts, int64_t part_stride, int64_t token_stride, int64_t head_stride,
+    const float* lse, int64_t lse_part_stride, int64_t lse_token_stride, int64_t lse_head_stride,
+    mla_dtype_t dtype, int32_t num_parts, int32_t num_tokens, int32_t num_heads, int32_t dim,
+    void* out, int64_t out_token_stride, int64_t out_head_stride, float* lse_out,
+    int64_t lo_token_stride, int64_t lo_head_stride, mla_stream_t stream);
 
 #ifdef __cplusplus
 }

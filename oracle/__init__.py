@@ -109,6 +109,12 @@ def lib() -> ctypes.CDLL:
                 "orc_context_kv_pack_paged": (u32, [vp, i64, i64, vp, i64, i64, vp, i32, i64, i32,
                                                     i64, i64, i32, vp, i64, vp, vp, i32, i32, i32,
                                                     i32, i32, i32, vp, vp, i32, f32, i32]),
+                "orc_latent_attention": (u32, [vp, i64, i64, vp, i64, i64, i32, i32, i32, i32, vp,
+                                               i32, i64, i32, i64, i64, vp, i64, vp, vp, i32, f32,
+                                               f32, i32, vp, vp]),
+                "orc_merge_attn_states": (None, [vp, vp, i32, i64, i32, vp, vp]),
+                "orc_copy_blocks": (u32, [vp, i32, i32, i64, i32, i64, i64, i32, vp, vp, vp,
+                                          i32]),
                 "orc_split_insert_grouped": (u32, [i32, vp, i64, i64, vp, i64, i64, i32, i32, i32,
                                                    i32, vp, i64, vp, vp, i32, i64, i32, i64, i64,
                                                    vp, i64, f32, vp, vp, i64]),
@@ -437,3 +443,43 @@ def context_kv_pack_split(threads, k_nope_buf, kn_token_stride, kn_head_stride, 
                                     v_dim, _p(key), _p(vout), out_dtype, float(out_scale),
                                     in_dtype)
     return key, vout
+
+
+# ------------------------------------------------- serving operators on the caches
+def latent_attention(q, cache, cache_dtype, num_blocks, block_size, block_stride, entry_stride,
+                     block_table, cu_q_lens, kv_lens, softmax_scale, k_scale=1.0, causal=True,
+                     fill=np.nan):
+    """q uint16 bf16 bits [T, H, 576] (contiguous).  Returns (out f64 [T, H, 512],
+    lse f64 [T, H], error bits); tokens of no sequence keep ``fill``."""
+    _chk(q, np.uint16), _chk(block_table, np.int32), _chk(cu_q_lens, np.int32)
+    _chk(kv_lens, np.int32)
+    T, H, E = q.shape
+    out, lse = np.full((T, H, 512), fill), np.full((T, H), fill)
+    pe = q.reshape(-1)[512:]
+    err = lib().orc_latent_attention(
+        _p(q), H * E, E, _p(pe) if T else None, H * E, E, T, H, 512, E - 512, _p(cache),
+        cache_dtype, num_blocks, block_size, block_stride, entry_stride, _p(block_table),
+        block_table.shape[1], _p(cu_q_lens), _p(kv_lens), kv_lens.shape[0], softmax_scale,
+        k_scale, 1 if causal else 0, _p(out), _p(lse))
+    return out, lse, err
+
+
+def merge_attn_states(parts, lse):
+    """parts f64 [P, T, H, D], lse f64 [P, T, H] -> (out [T, H, D], lse [T, H]) in f64."""
+    _chk(parts, np.float64), _chk(lse, np.float64)
+    P, T, H, D = parts.shape
+    out, lo = np.empty((T, H, D)), np.empty((T, H))
+    lib().orc_merge_attn_states(_p(parts), _p(lse), P, T * H, D, _p(out), _p(lo))
+    return out, lo
+
+
+def copy_blocks(caches, elt_size, num_blocks, block_size, block_stride, entry_stride, entry_dim,
+                src_blocks, dst_blocks, row_counts=None):
+    """``caches``: a list of flat numpy buffers, modified in place; returns the error bits."""
+    _chk(src_blocks, np.int32), _chk(dst_blocks, np.int32)
+    if row_counts is not None:
+        _chk(row_counts, np.int32)
+    ptrs = (ctypes.c_void_p * len(caches))(*[c.ctypes.data for c in caches])
+    return lib().orc_copy_blocks(ctypes.cast(ptrs, ctypes.c_void_p), len(caches), elt_size,
+                                 num_blocks, block_size, block_stride, entry_stride, entry_dim,
+                                 _p(src_blocks), _p(dst_blocks), _p(row_counts), len(dst_blocks))

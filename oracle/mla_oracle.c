@@ -720,3 +720,137 @@ uint32_t orc_context_kv_pack_paged(
   free(v_tmp);
   return err;
 }
+
+/* ======================================================================== */
+/* Serving operators on the caches.                                         */
+/* ======================================================================== */
+
+/*
+ * Attention of new tokens over the paged latent rows, from the definition: token
+ * t of sequence s (its number j = t - cu_q_lens[s] of n) sees the positions
+ * below kv_lens[s] (not causal) or kv_lens[s] - n + 1 + j (causal); x_p =
+ * scale <q, row_p>, lse = ln sum exp(x_p), out = sum exp(x_p - lse) row_p over
+ * the first kv_lora_rank columns.  A seen position whose block cannot be found
+ * is left out and reported.  out [T, H, kv_lora_rank], lse [T, H] in double;
+ * tokens of no sequence are left as they were.
+ */
+uint32_t orc_latent_attention(
+    const uint16_t* q_c, int64_t qc_token_stride, int64_t qc_head_stride, const uint16_t* q_pe,
+    int64_t qpe_token_stride, int64_t qpe_head_stride, int32_t num_tokens, int32_t num_heads,
+    int32_t kv_lora_rank, int32_t pe_dim, const void* cache, int32_t cache_dtype,
+    int64_t num_blocks, int32_t block_size, int64_t block_stride, int64_t entry_stride,
+    const int32_t* block_table, int64_t block_table_stride, const int32_t* cu_q_lens,
+    const int32_t* kv_lens, int32_t num_seqs, float softmax_scale, float k_scale, int32_t causal,
+    double* out, double* lse) {
+  uint32_t err = 0;
+  const int32_t entry = kv_lora_rank + pe_dim;
+  for (int32_t s = 0; s < num_seqs; ++s) {
+    int64_t kv = kv_lens[s] < 0 ? 0 : kv_lens[s];
+    int64_t n = (int64_t)cu_q_lens[s + 1] - cu_q_lens[s];
+    double* rows = (double*)malloc((size_t)(kv + 1) * (size_t)entry * sizeof(double));
+    double* x = (double*)malloc((size_t)(kv + 1) * sizeof(double));
+    char* found = (char*)calloc((size_t)(kv + 1), 1);
+    if (!rows || !x || !found) return 0xFFFFFFFFu;
+    for (int64_t p = 0; p < kv; ++p) { /* the sequence's rows as values */
+      int64_t kb = p / block_size;
+      if (kb >= block_table_stride) continue;
+      int32_t blk = block_table[s * block_table_stride + kb];
+      if (blk < 0 || blk >= num_blocks) continue;
+      found[p] = 1;
+      int64_t at = blk * block_stride + (p % block_size) * entry_stride;
+      for (int32_t e = 0; e < entry; ++e)
+        rows[p * entry + e] =
+            cache_dtype == ORC_BF16
+                ? orc_bf16_to_f64(((const uint16_t*)cache)[at + e])
+                : orc_fp8_to_f64(((const uint8_t*)cache)[at + e], cache_dtype) * (double)k_scale;
+    }
+    for (int64_t t = cu_q_lens[s]; t < cu_q_lens[s + 1] && t < num_tokens; ++t) {
+      int64_t seen = causal ? kv - n + 1 + (t - cu_q_lens[s]) : kv;
+      for (int32_t h = 0; h < num_heads; ++h) {
+        double top = -INFINITY, sum = 0.0;
+        double* o = out + (t * num_heads + h) * kv_lora_rank;
+        for (int64_t p = 0; p < seen; ++p) {
+          if (!found[p]) {
+            err |= ORC_ERR_BLOCK_OOB;
+            continue;
+          }
+          double d = 0.0;
+          for (int32_t e = 0; e < kv_lora_rank; ++e)
+            d += orc_bf16_to_f64(q_c[t * qc_token_stride + h * qc_head_stride + e]) *
+                 rows[p * entry + e];
+          for (int32_t e = 0; e < pe_dim; ++e)
+            d += orc_bf16_to_f64(q_pe[t * qpe_token_stride + h * qpe_head_stride + e]) *
+                 rows[p * entry + kv_lora_rank + e];
+          x[p] = d * (double)softmax_scale;
+          if (x[p] > top) top = x[p];
+        }
+        for (int32_t e = 0; e < kv_lora_rank; ++e) o[e] = 0.0;
+        for (int64_t p = 0; p < seen; ++p) {
+          if (!found[p]) continue;
+          double w = exp(x[p] - top);
+          sum += w;
+          for (int32_t e = 0; e < kv_lora_rank; ++e) o[e] += w * rows[p * entry + e];
+        }
+        if (sum > 0.0)
+          for (int32_t e = 0; e < kv_lora_rank; ++e) o[e] /= sum;
+        lse[t * num_heads + h] = sum > 0.0 ? top + log(sum) : -INFINITY;
+      }
+    }
+    free(rows);
+    free(x);
+    free(found);
+  }
+  return err;
+}
+
+/* Join of attention results over parts of the context, per row:
+ * lse_out = ln sum_i exp(lse_i), out = sum_i exp(lse_i - lse_out) part_i; a part
+ * with lse -inf does not count, and with none left out = 0, lse_out = -inf. */
+void orc_merge_attn_states(const double* parts, const double* lse, int32_t num_parts,
+                           int64_t rows, int32_t dim, double* out, double* lse_out) {
+  for (int64_t r = 0; r < rows; ++r) {
+    double top = -INFINITY, sum = 0.0;
+    for (int32_t i = 0; i < num_parts; ++i)
+      if (lse[i * rows + r] > top) top = lse[i * rows + r];
+    for (int32_t e = 0; e < dim; ++e) out[r * dim + e] = 0.0;
+    for (int32_t i = 0; i < num_parts; ++i) {
+      if (lse[i * rows + r] == -INFINITY) continue;
+      double w = exp(lse[i * rows + r] - top);
+      sum += w;
+      for (int32_t e = 0; e < dim; ++e) out[r * dim + e] += w * parts[(i * rows + r) * dim + e];
+    }
+    for (int32_t e = 0; e < dim && sum > 0.0; ++e) out[r * dim + e] /= sum;
+    lse_out[r] = sum > 0.0 ? top + log(sum) : -INFINITY;
+  }
+}
+
+/* Block copies, one entry at a time in the order of the copies: rows [0, n) of
+ * block dst become those of block src, or zero bytes for src -1. */
+uint32_t orc_copy_blocks(void* const* caches, int32_t num_layers, int32_t elt_size,
+                         int64_t num_blocks, int32_t block_size, int64_t block_stride,
+                         int64_t entry_stride, int32_t entry_dim, const int32_t* src_blocks,
+                         const int32_t* dst_blocks, const int32_t* row_counts,
+                         int32_t num_copies) {
+  uint32_t err = 0;
+  for (int32_t l = 0; l < num_layers; ++l)
+    for (int32_t i = 0; i < num_copies; ++i) {
+      int64_t src = src_blocks[i], dst = dst_blocks[i];
+      int32_t n = row_counts ? row_counts[i] : block_size;
+      if (dst == -1) continue;
+      if (src < -1 || dst < -1 || src >= num_blocks || dst >= num_blocks || n < 0 ||
+          n > block_size) {
+        err |= ORC_ERR_BLOCK_OOB;
+        continue;
+      }
+      char* c = (char*)caches[l];
+      for (int32_t r = 0; r < n; ++r) {
+        char* to = c + (dst * block_stride + r * entry_stride) * elt_size;
+        if (src < 0)
+          memset(to, 0, (size_t)entry_dim * (size_t)elt_size);
+        else
+          memmove(to, c + (src * block_stride + r * entry_stride) * elt_size,
+                  (size_t)entry_dim * (size_t)elt_size);
+      }
+    }
+  return err;
+}

@@ -149,6 +149,28 @@ uint32_t orc_context_kv_pack_paged(
     int32_t num_tokens, int32_t num_heads, int32_t nope_dim, int32_t rope_dim, int32_t v_dim,
     void* key_out, void* v_out, int32_t out_dtype, float out_scale, int32_t in_dtype);
 
+/* ---- serving operators on the caches --------------------------------------
+ * Attention of new tokens over the paged latent cache, the join of attention
+ * results over parts of the context, and block copies.  The two floating point
+ * results are left in double. */
+uint32_t orc_latent_attention(
+    const uint16_t* q_c, int64_t qc_token_stride, int64_t qc_head_stride, const uint16_t* q_pe,
+    int64_t qpe_token_stride, int64_t qpe_head_stride, int32_t num_tokens, int32_t num_heads,
+    int32_t kv_lora_rank, int32_t pe_dim, const void* cache, int32_t cache_dtype,
+    int64_t num_blocks, int32_t block_size, int64_t block_stride, int64_t entry_stride,
+    const int32_t* block_table, int64_t block_table_stride, const int32_t* cu_q_lens,
+    const int32_t* kv_lens, int32_t num_seqs, float softmax_scale, float k_scale, int32_t causal,
+    double* out, double* lse);
+
+void orc_merge_attn_states(const double* parts, const double* lse, int32_t num_parts,
+                           int64_t rows, int32_t dim, double* out, double* lse_out);
+
+uint32_t orc_copy_blocks(void* const* caches, int32_t num_layers, int32_t elt_size,
+                         int64_t num_blocks, int32_t block_size, int64_t block_stride,
+                         int64_t entry_stride, int32_t entry_dim, const int32_t* src_blocks,
+                         const int32_t* dst_blocks, const int32_t* row_counts,
+                         int32_t num_copies);
+
 /* ---- the row loops above split over host threads (mla_oracle_split.c) ---
  * For the multi-core CPU baseline only: each cuts its rows into `threads`
  * contiguous ranges and runs the unchanged function above on each range in its

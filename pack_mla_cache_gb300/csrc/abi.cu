@@ -175,6 +175,40 @@ mla::PagedSrc paged_src(const void* kv_cache, int64_t num_blocks, int32_t block_
   return p;
 }
 
+inline bool cache_dtype_ok(int d) {
+  return d == MLA_BF16 || d == MLA_FP8_E4M3 || d == MLA_FP8_E5M2;
+}
+// Whether block_size entries of `dim` elements fit into a block (no overflow:
+// the product is only formed when it is below block_stride).
+inline bool block_holds(int32_t block_size, int64_t block_stride, int64_t entry_stride,
+                        int64_t dim) {
+  if (block_size > 1 && entry_stride > block_stride / (block_size - 1)) return false;
+  return block_stride - (int64_t)(block_size - 1) * entry_stride >= dim;
+}
+
+mla_status_t check_attention_sizes(int32_t num_tokens, int32_t num_heads, int32_t num_seqs) {
+  if (num_tokens < 0) return fail(MLA_ERR_INVALID_ARG, "num_tokens must be >= 0");
+  if (num_heads <= 0) return fail(MLA_ERR_INVALID_ARG, "num_heads must be >= 1");
+  if (num_heads > 1024) return fail(MLA_ERR_UNSUPPORTED, "at most 1024 heads are built");
+  if (num_seqs <= 0) return fail(MLA_ERR_INVALID_ARG, "num_seqs must be >= 1");
+  if (num_seqs > 4096) return fail(MLA_ERR_UNSUPPORTED, "at most 4096 sequences per call are built");
+  if ((int64_t)num_tokens * num_heads >= (int64_t(1) << 31))
+    return fail(MLA_ERR_UNSUPPORTED, "num_tokens * num_heads is too large for one call");
+  return MLA_OK;
+}
+
+// SMs of the current device.
+mla_status_t current_sms(int* sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    return fail(MLA_ERR_CUDA, "reading the device's SM count failed: %s", cudaGetErrorString(e));
+  }
+  return MLA_OK;
+}
+
 mla_status_t check_paged_ptrs(const int32_t* block_table, const int32_t* cu,
                               const int32_t* starts) {
   MLA_TRY(check_device_ptr(block_table, "block_table"));
@@ -794,6 +828,229 @@ mla_status_t mla_rope_cos_sin_cache(float* out, int64_t max_position, int32_t ro
   MLA_TRY(check_device_ptr(out, "out"));
   return launched(mla::launch_rope_table(out, max_position, rot_dim, base, cfg_for(stream)),
                   "mla_rope_cos_sin_cache");
+}
+
+mla_status_t mla_cache_copy_blocks(const int64_t* kv_cache_ptrs, int32_t num_layers,
+                                   mla_dtype_t cache_dtype, int64_t num_blocks,
+                                   int32_t block_size, int64_t block_stride,
+                                   int64_t entry_stride, int32_t entry_dim,
+                                   const int32_t* src_blocks, const int32_t* dst_blocks,
+                                   const int32_t* row_counts, int32_t num_copies,
+                                   uint32_t* err_word, mla_stream_t stream) {
+  if (num_copies < 0) return fail(MLA_ERR_INVALID_ARG, "num_copies must be >= 0");
+  if (num_layers <= 0) return fail(MLA_ERR_INVALID_ARG, "num_layers must be >= 1");
+  if (num_layers > 128) return fail(MLA_ERR_UNSUPPORTED, "at most 128 layers per call are built");
+  if (!cache_dtype_ok(cache_dtype))
+    return fail(MLA_ERR_INVALID_ARG,
+                "cache_dtype must be MLA_BF16, MLA_FP8_E4M3 or MLA_FP8_E5M2; got %d",
+                (int)cache_dtype);
+  if (block_size <= 0 || num_blocks <= 0)
+    return fail(MLA_ERR_INVALID_ARG, "block_size and num_blocks must be >= 1");
+  if (entry_dim <= 0 || entry_dim > entry_stride)
+    return fail(MLA_ERR_INVALID_ARG, "entry_dim must lie in [1, entry_stride]");
+  if (!block_holds(block_size, block_stride, entry_stride, entry_dim))
+    return fail(MLA_ERR_INVALID_ARG, "block_stride is too small for block_size entries");
+  const int ce = elt_size(cache_dtype);
+  if (!m16(block_stride * ce) || !m16(entry_stride * ce))
+    return fail(MLA_ERR_MISALIGNED, "cache block_stride / entry_stride must be multiples of 16 bytes");
+  if (!m16((int64_t)entry_dim * ce))
+    return fail(MLA_ERR_MISALIGNED, "entry_dim must span a multiple of 16 bytes");
+  const int64_t row_chunks = (int64_t)entry_dim * ce / 16;
+  if (row_chunks * block_size >= (int64_t(1) << 31))
+    return fail(MLA_ERR_UNSUPPORTED, "blocks of 32 GiB and more are not built");
+  if (reinterpret_cast<uintptr_t>(kv_cache_ptrs) & 7)
+    return fail(MLA_ERR_MISALIGNED, "kv_cache_ptrs must be 8-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(src_blocks) | reinterpret_cast<uintptr_t>(dst_blocks) |
+       reinterpret_cast<uintptr_t>(row_counts)) & 3)
+    return fail(MLA_ERR_MISALIGNED, "int32 index arrays must be 4-byte aligned");
+  if (err_word && (reinterpret_cast<uintptr_t>(err_word) & 3))
+    return fail(MLA_ERR_MISALIGNED, "err_word must be 4-byte aligned");
+  if (num_copies == 0) return MLA_OK;  // empty inputs may have null data pointers
+  if (!kv_cache_ptrs || !src_blocks || !dst_blocks)
+    return fail(MLA_ERR_INVALID_ARG, "kv_cache_ptrs, src_blocks and dst_blocks must be non-null");
+  MLA_TRY(check_device_ptr(kv_cache_ptrs, "kv_cache_ptrs"));
+  MLA_TRY(check_device_ptr(src_blocks, "src_blocks"));
+  MLA_TRY(check_device_ptr(dst_blocks, "dst_blocks"));
+  if (row_counts) MLA_TRY(check_device_ptr(row_counts, "row_counts"));
+  if (err_word) MLA_TRY(check_device_ptr(err_word, "err_word"));
+
+  mla::CopyBlocksArgs a{};
+  a.cache_ptrs = kv_cache_ptrs;
+  a.num_layers = num_layers;
+  a.num_blocks = num_blocks;
+  a.block_stride = block_stride * ce;
+  a.entry_stride = entry_stride * ce;
+  a.block_size = block_size;
+  a.row_chunks = (int32_t)row_chunks;
+  a.dense = entry_stride == entry_dim;
+  a.src = src_blocks;
+  a.dst = dst_blocks;
+  a.rows = row_counts;
+  a.num_copies = num_copies;
+  a.err = err_word;
+  return launched(mla::launch_copy_blocks(a, cfg_for(stream)), "mla_cache_copy_blocks");
+}
+
+mla_status_t mla_merge_attn_states(
+    const void* parts, int64_t part_stride, int64_t token_stride, int64_t head_stride,
+    const float* lse, int64_t lse_part_stride, int64_t lse_token_stride, int64_t lse_head_stride,
+    mla_dtype_t dtype, int32_t num_parts, int32_t num_tokens, int32_t num_heads, int32_t dim,
+    void* out, int64_t out_token_stride, int64_t out_head_stride, float* lse_out,
+    int64_t lo_token_stride, int64_t lo_head_stride, mla_stream_t stream) {
+  if (num_tokens < 0) return fail(MLA_ERR_INVALID_ARG, "num_tokens must be >= 0");
+  if (num_heads <= 0) return fail(MLA_ERR_INVALID_ARG, "num_heads must be >= 1");
+  if (num_parts <= 0) return fail(MLA_ERR_INVALID_ARG, "num_parts must be >= 1");
+  if (num_parts > 1024) return fail(MLA_ERR_UNSUPPORTED, "at most 1024 parts per call are built");
+  if (dim <= 0) return fail(MLA_ERR_INVALID_ARG, "dim must be >= 1");
+  if (dtype != MLA_BF16 && dtype != MLA_FP16 && dtype != MLA_FP32)
+    return fail(MLA_ERR_INVALID_ARG, "dtype must be MLA_BF16, MLA_FP16 or MLA_FP32; got %d",
+                (int)dtype);
+  const int es = dtype == MLA_FP32 ? 4 : 2;
+  if (!m16((int64_t)dim * es))
+    return fail(MLA_ERR_MISALIGNED, "dim must span a multiple of 16 bytes");
+  if (!a16(parts) || !m16(part_stride * es) || !m16(token_stride * es) || !m16(head_stride * es))
+    return fail(MLA_ERR_MISALIGNED, "rows of parts must start on 16-byte boundaries");
+  if (!a16(out) || !m16(out_token_stride * es) || !m16(out_head_stride * es))
+    return fail(MLA_ERR_MISALIGNED, "out rows must start on 16-byte boundaries");
+  if ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(lse_out)) & 3)
+    return fail(MLA_ERR_MISALIGNED, "lse and lse_out must be 4-byte aligned");
+  if (num_tokens == 0) return MLA_OK;  // empty inputs may have null data pointers
+  if (!parts || !lse || !out) return fail(MLA_ERR_INVALID_ARG, "parts, lse and out must be non-null");
+  MLA_TRY(check_device_ptr(parts, "parts"));
+  MLA_TRY(check_device_ptr(lse, "lse"));
+  MLA_TRY(check_device_ptr(out, "out"));
+  if (lse_out) MLA_TRY(check_device_ptr(lse_out, "lse_out"));
+
+  mla::MergeArgs a{};
+  a.parts = static_cast<const uint8_t*>(parts);
+  a.ps = part_stride * es;
+  a.ts = token_stride * es;
+  a.hs = head_stride * es;
+  a.lse = lse;
+  a.lps = lse_part_stride;
+  a.lts = lse_token_stride;
+  a.lhs = lse_head_stride;
+  a.num_parts = num_parts;
+  a.num_tokens = num_tokens;
+  a.num_heads = num_heads;
+  a.row_chunks = (int32_t)((int64_t)dim * es / 16);
+  a.out = static_cast<uint8_t*>(out);
+  a.ots = out_token_stride * es;
+  a.ohs = out_head_stride * es;
+  a.lse_out = lse_out;
+  a.lots = lo_token_stride;
+  a.lohs = lo_head_stride;
+  const int fmt = dtype == MLA_FP32 ? mla::kF32 : (int)dtype;
+  return launched(mla::launch_merge(a, fmt, cfg_for(stream)), "mla_merge_attn_states");
+}
+
+mla_status_t mla_latent_attention_workspace(int32_t num_tokens, int32_t num_heads,
+                                            int32_t num_seqs, int64_t* bytes) {
+  MLA_TRY(check_attention_sizes(num_tokens, num_heads, num_seqs));
+  if (!bytes) return fail(MLA_ERR_INVALID_ARG, "bytes must be non-null");
+  int sms = 0;
+  MLA_TRY(current_sms(&sms));
+  *bytes = mla::latent_attention_workspace(num_tokens, num_heads, num_seqs, sms);
+  return MLA_OK;
+}
+
+mla_status_t mla_latent_attention(
+    const void* q_c, int64_t qc_token_stride, int64_t qc_head_stride, const void* q_pe,
+    int64_t qpe_token_stride, int64_t qpe_head_stride, int32_t num_tokens, int32_t num_heads,
+    int32_t kv_lora_rank, int32_t pe_dim, const void* kv_cache, mla_dtype_t cache_dtype,
+    int64_t num_blocks, int32_t block_size, int64_t block_stride, int64_t entry_stride,
+    const int32_t* block_table, int64_t block_table_stride, const int32_t* cu_q_lens,
+    const int32_t* kv_lens, int32_t num_seqs, float softmax_scale, const float* k_scale,
+    int32_t causal, void* out, int64_t out_token_stride, int64_t out_head_stride, float* lse,
+    int64_t lse_token_stride, int64_t lse_head_stride, void* workspace, int64_t workspace_bytes,
+    uint32_t* err_word, mla_stream_t stream) {
+  MLA_TRY(check_attention_sizes(num_tokens, num_heads, num_seqs));
+  if (kv_lora_rank != 512 || pe_dim != 64)
+    return fail(MLA_ERR_UNSUPPORTED,
+                "only kv_lora_rank 512 and pe_dim 64 are built (got %d, %d)", kv_lora_rank,
+                pe_dim);
+  if (!cache_dtype_ok(cache_dtype))
+    return fail(MLA_ERR_INVALID_ARG,
+                "cache_dtype must be MLA_BF16, MLA_FP8_E4M3 or MLA_FP8_E5M2; got %d",
+                (int)cache_dtype);
+  const bool fp8 = cache_dtype != MLA_BF16;
+  if (fp8 && !k_scale) return fail(MLA_ERR_INVALID_ARG, "an fp8 cache requires k_scale");
+  if (!fp8 && k_scale) return fail(MLA_ERR_INVALID_ARG, "a bf16 cache does not use k_scale");
+  if (!(softmax_scale > -3.0e38f) || !(softmax_scale < 3.0e38f))
+    return fail(MLA_ERR_INVALID_ARG, "softmax_scale must be finite");
+  const int ce = elt_size(cache_dtype);
+  MLA_TRY(check_paged(kv_cache, num_blocks, block_size, block_stride, entry_stride, 0,
+                      kv_lora_rank + pe_dim, ce, block_table, block_table_stride, cu_q_lens,
+                      kv_lens, num_seqs));
+  if (!a16(q_c) || !m16(qc_token_stride * 2) || !m16(qc_head_stride * 2))
+    return fail(MLA_ERR_MISALIGNED, "q_c rows must start on 16-byte boundaries");
+  if (!a16(q_pe) || !m16(qpe_token_stride * 2) || !m16(qpe_head_stride * 2))
+    return fail(MLA_ERR_MISALIGNED, "q_pe rows must start on 16-byte boundaries");
+  if (!a16(out) || !m16(out_token_stride * 2) || !m16(out_head_stride * 2))
+    return fail(MLA_ERR_MISALIGNED, "out rows must start on 16-byte boundaries");
+  if (!a16(workspace)) return fail(MLA_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(k_scale) |
+       reinterpret_cast<uintptr_t>(err_word)) & 3)
+    return fail(MLA_ERR_MISALIGNED, "lse, k_scale and err_word must be 4-byte aligned");
+  if (num_tokens == 0) return MLA_OK;  // empty inputs may have null data pointers
+  if (!q_c || !q_pe || !kv_cache || !block_table || !cu_q_lens || !kv_lens || !out || !workspace)
+    return fail(MLA_ERR_INVALID_ARG,
+                "q_c, q_pe, kv_cache, block_table, cu_q_lens, kv_lens, out and workspace must be "
+                "non-null");
+  int sms = 0;
+  MLA_TRY(current_sms(&sms));
+  const int64_t need = mla::latent_attention_workspace(num_tokens, num_heads, num_seqs, sms);
+  if (workspace_bytes < need)
+    return fail(MLA_ERR_INVALID_ARG, "workspace_bytes must be >= %lld (got %lld)", (long long)need,
+                (long long)workspace_bytes);
+  MLA_TRY(check_device_ptr(q_c, "q_c"));
+  MLA_TRY(check_device_ptr(q_pe, "q_pe"));
+  MLA_TRY(check_device_ptr(kv_cache, "kv_cache"));
+  MLA_TRY(check_device_ptr(block_table, "block_table"));
+  MLA_TRY(check_device_ptr(cu_q_lens, "cu_q_lens"));
+  MLA_TRY(check_device_ptr(kv_lens, "kv_lens"));
+  if (fp8) MLA_TRY(check_device_ptr(k_scale, "k_scale"));
+  MLA_TRY(check_device_ptr(out, "out"));
+  if (lse) MLA_TRY(check_device_ptr(lse, "lse"));
+  MLA_TRY(check_device_ptr(workspace, "workspace"));
+  if (err_word) MLA_TRY(check_device_ptr(err_word, "err_word"));
+
+  mla::LatentAttnArgs a{};
+  a.q_c = static_cast<const uint8_t*>(q_c);
+  a.qc_ts = qc_token_stride * 2;
+  a.qc_hs = qc_head_stride * 2;
+  a.q_pe = static_cast<const uint8_t*>(q_pe);
+  a.qp_ts = qpe_token_stride * 2;
+  a.qp_hs = qpe_head_stride * 2;
+  a.num_tokens = num_tokens;
+  a.num_heads = num_heads;
+  a.cache = static_cast<const uint8_t*>(kv_cache);
+  a.block_stride = block_stride * ce;
+  a.entry_stride = entry_stride * ce;
+  a.num_blocks = num_blocks;
+  a.block_size = block_size;
+  a.bs_shift = log2_exact(block_size);
+  a.block_table = block_table;
+  a.bt_stride = block_table_stride;
+  a.room = block_table_stride > INT32_MAX / block_size ? INT32_MAX
+                                                       : (int32_t)(block_table_stride * block_size);
+  a.cu_q = cu_q_lens;
+  a.kv_lens = kv_lens;
+  a.num_seqs = num_seqs;
+  a.softmax_scale = softmax_scale;
+  a.k_scale = k_scale;
+  a.causal = causal != 0;
+  a.out = static_cast<uint8_t*>(out);
+  a.out_ts = out_token_stride * 2;
+  a.out_hs = out_head_stride * 2;
+  a.lse = lse;
+  a.lse_ts = lse_token_stride;
+  a.lse_hs = lse_head_stride;
+  a.workspace = static_cast<uint8_t*>(workspace);
+  a.err = err_word;
+  a.wait_limit_ns = g_wait_ns.load();
+  return launched(mla::launch_latent_attention(a, (int)cache_dtype, cfg_for(stream)),
+                  "mla_latent_attention");
 }
 
 }  // extern "C"

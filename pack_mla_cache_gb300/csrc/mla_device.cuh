@@ -12,7 +12,7 @@
 
 namespace mla {
 
-enum Fmt : int { kBF16 = 0, kE4M3 = 1, kE5M2 = 2, kF16 = 3 };
+enum Fmt : int { kBF16 = 0, kE4M3 = 1, kE5M2 = 2, kF16 = 3, kF32 = 4 };
 
 // Whether a format is a 16-bit float (bf16 or fp16).
 __host__ __device__ constexpr bool is16(int f) { return f == kBF16 || f == kF16; }

@@ -16,7 +16,7 @@ import torch
 
 from .build import LIB_PATH
 
-MLA_BF16, MLA_FP8_E4M3, MLA_FP8_E5M2, MLA_FP16 = 0, 1, 2, 3
+MLA_BF16, MLA_FP8_E4M3, MLA_FP8_E5M2, MLA_FP16, MLA_FP32 = 0, 1, 2, 3, 4
 MLA_OK, MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_MISALIGNED, MLA_ERR_CUDA = range(5)
 MLA_ERRBIT_SLOT_OOB, MLA_ERRBIT_BLOCK_OOB, MLA_ERRBIT_POS_OOB, MLA_ERRBIT_MISALIGNED = 1, 2, 4, 8
 MLA_ERRBIT_TIMEOUT = 16
@@ -98,6 +98,16 @@ SIGNATURES = {
     "mla_rope_cos_sin_cache": (ctypes.c_int, [_vp, _i64, _i32, ctypes.c_double, _vp]),
     "mla_context_kv_pack_gather": (ctypes.c_int, [ctypes.POINTER(KvPack),
                                                   ctypes.POINTER(ContextGather), _vp, _vp]),
+    "mla_cache_copy_blocks": (ctypes.c_int, [
+        _vp, _i32, ctypes.c_int, _i64, _i32, _i64, _i64, _i32, _vp, _vp, _vp, _i32, _vp, _vp]),
+    "mla_latent_attention": (ctypes.c_int, [
+        _vp, _i64, _i64, _vp, _i64, _i64, _i32, _i32, _i32, _i32, _vp, ctypes.c_int, _i64, _i32,
+        _i64, _i64, _vp, _i64, _vp, _vp, _i32, ctypes.c_float, _vp, _i32, _vp, _i64, _i64, _vp,
+        _i64, _i64, _vp, _i64, _vp, _vp]),
+    "mla_latent_attention_workspace": (ctypes.c_int, [_i32, _i32, _i32, ctypes.POINTER(_i64)]),
+    "mla_merge_attn_states": (ctypes.c_int, [
+        _vp, _i64, _i64, _i64, _vp, _i64, _i64, _i64, ctypes.c_int, _i32, _i32, _i32, _i32, _vp,
+        _i64, _i64, _vp, _i64, _i64, _vp]),
 }
 
 
@@ -340,3 +350,58 @@ def mla_context_kv_pack_gather(pack: KvPack, next_gather: ContextGather, *, err_
     must write a workspace the pack does not use."""
     _check(lib().mla_context_kv_pack_gather(ctypes.byref(pack), ctypes.byref(next_gather),
                                             _ptr(err_word), _stream(stream)))
+
+
+def mla_cache_copy_blocks(kv_cache_ptrs, cache_dtype, num_blocks, block_size, block_stride,
+                          entry_stride, entry_dim, src_blocks, dst_blocks, *, row_counts=None,
+                          err_word=None, stream=None):
+    """Copy (fork, compact) or clear (src -1) blocks in every layer's cache:
+    kv_cache_ptrs int64 [L]; src_blocks / dst_blocks / row_counts int32 [N],
+    row_counts None for whole blocks."""
+    _check(lib().mla_cache_copy_blocks(
+        _ptr(kv_cache_ptrs), kv_cache_ptrs.shape[0], dtype_code(cache_dtype), num_blocks,
+        block_size, block_stride, entry_stride, entry_dim, _ptr(src_blocks), _ptr(dst_blocks),
+        _ptr(row_counts), dst_blocks.shape[0], _ptr(err_word), _stream(stream)))
+
+
+def mla_latent_attention_workspace(num_tokens: int, num_heads: int, num_seqs: int) -> int:
+    """Bytes of workspace of ``mla_latent_attention`` on the current device."""
+    n = _i64(0)
+    _check(lib().mla_latent_attention_workspace(num_tokens, num_heads, num_seqs, ctypes.byref(n)))
+    return n.value
+
+
+def mla_latent_attention(q_c, q_pe, kv_cache, cache_dtype, num_blocks, block_size, block_stride,
+                         entry_stride, block_table, cu_q_lens, kv_lens, out, workspace, *,
+                         softmax_scale, k_scale=None, causal=True, lse=None, err_word=None,
+                         stream=None):
+    """Attention of new tokens over the paged latent cache (absorbed form):
+    q_c [T, H, 512] and q_pe [T, H, 64] bf16 views (strided), out bf16
+    [T, H, 512], lse fp32 [T, H] or None; block_table int32 [S, W], cu_q_lens
+    int32 [S + 1], kv_lens int32 [S]; workspace: a uint8 tensor of
+    ``mla_latent_attention_workspace`` bytes."""
+    T, H, R = q_c.shape
+    _check(lib().mla_latent_attention(
+        _ptr(q_c), q_c.stride(0), q_c.stride(1), _ptr(q_pe), q_pe.stride(0), q_pe.stride(1), T, H,
+        R, q_pe.shape[2], _ptr(kv_cache), dtype_code(cache_dtype), num_blocks, block_size,
+        block_stride, entry_stride, _ptr(block_table), _bt_stride(block_table), _ptr(cu_q_lens),
+        _ptr(kv_lens), kv_lens.shape[0], softmax_scale, _ptr(k_scale), 1 if causal else 0,
+        _ptr(out), out.stride(0), out.stride(1), _ptr(lse),
+        0 if lse is None else lse.stride(0), 0 if lse is None else lse.stride(1),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(err_word),
+        _stream(stream)))
+
+
+def mla_merge_attn_states(parts, lse, out, *, lse_out=None, stream=None):
+    """Join attention results over disjoint parts of the context: parts
+    [P, T, H, D] (bf16, fp16 or fp32; strided, unit last stride) with lse fp32
+    [P, T, H] into out [T, H, D] of the same type and lse_out fp32 [T, H]."""
+    P, T, H, Dm = parts.shape
+    if parts.dtype != out.dtype:
+        raise ValueError(f"out must have the parts' dtype ({parts.dtype}, got {out.dtype})")
+    code = MLA_FP32 if parts.dtype == torch.float32 else dtype_code(parts.dtype)
+    _check(lib().mla_merge_attn_states(
+        _ptr(parts), parts.stride(0), parts.stride(1), parts.stride(2), _ptr(lse), lse.stride(0),
+        lse.stride(1), lse.stride(2), code, P, T, H, Dm, _ptr(out), out.stride(0), out.stride(1),
+        _ptr(lse_out), 0 if lse_out is None else lse_out.stride(0),
+        0 if lse_out is None else lse_out.stride(1), _stream(stream)))
