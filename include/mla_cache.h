@@ -100,8 +100,8 @@ enum {
   MLA_ERRBIT_BLOCK_OOB = 2u,  /* block table index or block id out of range */
   MLA_ERRBIT_POS_OOB = 4u,    /* position outside [0, max_position) */
   MLA_ERRBIT_MISALIGNED = 8u, /* a per-layer cache base null or not 16-byte aligned */
-  MLA_ERRBIT_TIMEOUT = 16u     /* a pipeline wait of the grouped insert gave up (see
-                                  mla_cache_insert_grouped) */
+  MLA_ERRBIT_TIMEOUT = 16u     /* a pipeline wait gave up (see mla_cache_insert_grouped
+                                  and mla_latent_attention) */
 };
 
 /* Map a vLLM kv-cache-dtype string to mla_dtype_t; -1 if it is not one of
@@ -599,7 +599,8 @@ mla_status_t mla_cache_copy_blocks(const int64_t* kv_cache_ptrs, int32_t num_lay
  *                       index is outside the table's row, is left out of the
  *                       sums (MLA_ERRBIT_BLOCK_OOB).
  *   cu_q_lens           int32 device [num_seqs + 1], non-decreasing.
- *   kv_lens             int32 device [num_seqs].
+ *   kv_lens             int32 device [num_seqs]; lengths beyond the table's row
+ *                       (or 2^31 - 128) are cut there (MLA_ERRBIT_BLOCK_OOB).
  *   num_seqs            1 to 4096.
  *   softmax_scale       finite; applies to the dequantised product.
  *   k_scale             device fp32 scalar: required for an fp8 cache, must be
@@ -611,6 +612,9 @@ mla_status_t mla_cache_copy_blocks(const int64_t* kv_cache_ptrs, int32_t num_lay
  *                       what mla_latent_attention_workspace gives.  Its contents before and after a call
  *                       mean nothing; calls that may run at the same time (on
  *                       two streams) need one each.
+ * The kernel's internal waits are bounded (2 s, which means a fault or a stalled
+ * GPU); one that runs out leaves rows of out unwritten and sets
+ * MLA_ERRBIT_TIMEOUT.
  */
 mla_status_t mla_latent_attention(
     const void* q_c, int64_t qc_token_stride, int64_t qc_head_stride, const void* q_pe,

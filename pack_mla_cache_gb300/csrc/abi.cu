@@ -1032,8 +1032,9 @@ mla_status_t mla_latent_attention(
   a.bs_shift = log2_exact(block_size);
   a.block_table = block_table;
   a.bt_stride = block_table_stride;
-  a.room = block_table_stride > INT32_MAX / block_size ? INT32_MAX
-                                                       : (int32_t)(block_table_stride * block_size);
+  const int64_t most_rows = INT32_MAX - 127;  // row numbers of a whole tile stay in 32 bits
+  a.room = (int32_t)(block_table_stride > most_rows / block_size ? most_rows
+                                                                 : block_table_stride * block_size);
   a.cu_q = cu_q_lens;
   a.kv_lens = kv_lens;
   a.num_seqs = num_seqs;
@@ -1048,8 +1049,8 @@ mla_status_t mla_latent_attention(
   a.lse_hs = lse_head_stride;
   a.workspace = static_cast<uint8_t*>(workspace);
   a.err = err_word;
-  a.wait_limit_ns = g_wait_ns.load();
-  return launched(mla::launch_latent_attention(a, (int)cache_dtype, cfg_for(stream)),
+  a.wait_limit_ns = kDefaultWaitNs;
+  return launched(mla::launch_latent_attention(a, (int)cache_dtype, sms, cfg_for(stream)),
                   "mla_latent_attention");
 }
 

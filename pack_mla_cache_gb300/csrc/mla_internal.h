@@ -151,7 +151,7 @@ struct LatentAttnArgs {
   int32_t block_size, bs_shift;  // bs_shift = log2(block_size) or -1
   const int32_t* block_table;
   int64_t bt_stride;  // elements
-  int32_t room;       // rows that a table row can hold (at most INT32_MAX)
+  int32_t room;       // rows that a table row can hold (below 2^31 - 127)
   const int32_t* cu_q;
   const int32_t* kv_lens;
   int32_t num_seqs;
@@ -193,7 +193,8 @@ cudaError_t launch_rope_table(float* out, int64_t max_position, int32_t rot_dim,
 cudaError_t launch_copy_blocks(const CopyBlocksArgs& a, const LaunchCfg& cfg);
 // fmt: kBF16, kF16 or kF32.
 cudaError_t launch_merge(const MergeArgs& a, int fmt, const LaunchCfg& cfg);
-cudaError_t launch_latent_attention(const LatentAttnArgs& a, int cache_fmt, const LaunchCfg& cfg);
+cudaError_t launch_latent_attention(const LatentAttnArgs& a, int cache_fmt, int num_sms,
+                                    const LaunchCfg& cfg);
 // Bytes of workspace of such a call on a device of num_sms SMs.
 int64_t latent_attention_workspace(int32_t num_tokens, int32_t num_heads, int32_t num_seqs,
                                    int num_sms);

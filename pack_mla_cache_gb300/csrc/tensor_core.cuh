@@ -1,0 +1,154 @@
+// tensor_core.cuh -- thin wrappers over the 5th-generation tensor core PTX of
+// sm_103a (tcgen05) that the latent attention uses: tensor memory allocation,
+// shared-memory and instruction descriptors, the bf16 matrix instruction with
+// fp32 accumulators in tensor memory, its completion on an mbarrier, and loads
+// and stores of tensor memory.
+#pragma once
+
+#include <cstdint>
+
+#include "mla_device.cuh"
+
+namespace mla {
+namespace tc {
+
+// Tensor memory: `cols` columns (a power of two >= 32) of 128 lanes x 32 bits;
+// the base address is written to shared memory.  One whole warp calls these.
+__device__ __forceinline__ void alloc(uint32_t smem_dst, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst),
+               "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void dealloc(uint32_t tmem, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols)
+               : "memory");
+}
+
+// Order tensor-memory accesses around a synchronisation between threads.
+__device__ __forceinline__ void fence_before_sync() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_after_sync() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+// Make this thread's view of shared memory (ordinary stores, its own or ones it
+// has synchronised with) visible to the tensor core's reads.
+__device__ __forceinline__ void fence_smem_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Shared-memory operand with the 128-byte swizzle: rows of 128 bytes whose
+// 16-byte units are permuted by XOR with the row number mod 8, in groups of 8
+// rows (1024 bytes, 1024-byte aligned).
+//   K-major (a row holds 64 consecutive k of one m or n): sbo = bytes from one
+//     group of 8 rows to the next; lbo unused.
+//   MN-major (a row holds 64 consecutive m of one k): sbo = bytes from one group
+//     of 8 k to the next, lbo = bytes from one run of 64 m to the next.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// Instruction descriptor: bf16 A and B, fp32 accumulator, M x N tile;
+// a_mn: A is MN-major.
+__host__ __device__ constexpr uint32_t instr_desc(int m, int n, bool a_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(m >> 4) << 24);
+}
+
+// D[tmem] (+)= A * B for one k step of 16; issued by one thread.
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         bool accumulate) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
+      "  tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+// Arrive on `bar` when every matrix instruction this thread has issued is done.
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                   bar)
+               : "memory");
+}
+
+__device__ __forceinline__ void wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// The loads wait for their registers in the same statement, so that no use of
+// them can be moved in front of the wait.  Whole warps call them converged.
+//
+// 16 lanes x 8 columns per group of 4 registers: thread t gets, of group j,
+// lane t / 4 columns 8 j + 2 (t % 4) and + 1 in r[4 j], r[4 j + 1], and lane
+// t / 4 + 8 in r[4 j + 2], r[4 j + 3].  G groups.
+template <int G>
+__device__ __forceinline__ void ld_16x256(uint32_t addr, uint32_t* r) {
+  static_assert(G == 2 || G == 4 || G == 8, "groups built");
+  if constexpr (G == 2) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7])
+        : "r"(addr)
+        : "memory");
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15}, [%16];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
+        : "memory");
+    if constexpr (G == 8) ld_16x256<4>(addr + 32, r + 16);
+  }
+}
+
+// 32 lanes x 16 columns: thread t gets lane t's 16 columns.
+__device__ __forceinline__ void ld_32x16(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void st_32x16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// Four 8x8 matrices of 16-bit values stored transposed: thread t holds, of
+// matrix i, row t / 4 columns 2 (t % 4) and + 1 in r_i; column c of matrix i goes
+// to the 16 bytes whose address thread 8 i + c passes.
+__device__ __forceinline__ void st_8x8_t(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2,
+                                         uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+               : "memory");
+}
+
+// 16 bytes global -> shared, asynchronously; zeros when !valid (src is not read).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(valid ? 16u : 0u)
+               : "memory");
+}
+// Arrive on `bar` when this thread's cp_async16 so far are done.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+}  // namespace tc
+}  // namespace mla
