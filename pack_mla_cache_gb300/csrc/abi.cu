@@ -1024,6 +1024,10 @@ mla_status_t mla_latent_attention(
   a.qp_hs = qpe_head_stride * 2;
   a.num_tokens = num_tokens;
   a.num_heads = num_heads;
+  // division by an invariant integer using multiplication (Granlund and
+  // Montgomery, PLDI 1994): shift = ceil(log2 d), mul = floor(2^32 (2^shift - d) / d) + 1
+  while ((int64_t(1) << a.heads_shift) < num_heads) ++a.heads_shift;
+  a.heads_mul = (uint32_t)((((uint64_t(1) << a.heads_shift) - num_heads) << 32) / num_heads + 1);
   a.cache = static_cast<const uint8_t*>(kv_cache);
   a.block_stride = block_stride * ce;
   a.entry_stride = entry_stride * ce;

@@ -11,7 +11,7 @@
 // keys; one unit = (query tile, key tile).  The units of the whole call, in
 // (sequence, query tile, key tile) order, are cut into equal contiguous runs,
 // one per CTA (one CTA per SM), so ragged batches load every SM alike.  A
-// (query tile) whose units fall into several CTAs leaves unnormalised fp32
+// query tile whose units fall into several CTAs leaves unnormalised fp32
 // partial sums in the workspace, which a second small launch joins in the
 // order of the CTAs (no atomics: equal calls give equal bits).
 //
@@ -21,22 +21,39 @@
 //   scores    S^T [64 keys x NR]  = K  [64 x 576] * Q^T   (A = K as loaded)
 //   outputs   O^T [512 x NR]     += V^T [512 x 64] * P^T  (A = the same shared
 //             memory read MN-major: a latent row is key and value)
-// A key tile is 9 chunks of 64 keys x 64 columns bf16 in the 128-byte swizzle.
+// A key tile is a few chunks of 64 keys x 128 bytes in the 128-byte swizzle.
 // S^T (two buffers) and O^T (4 x 128 dims) stay in tensor memory.
 //
-// Roles (13 warps): 8 producer warps load and, for fp8, widen key tiles into a
-// two-stage ring; one thread issues the matrix instructions; 4 warps do the
-// softmax (running maximum per query row, rescaling O^T only when the maximum
-// has grown by more than 2^8) and the output.  The scores of tile i + 1 are
-// issued before the outputs of tile i, so they overlap the softmax.
+// bf16 cache: 9 chunks of 64 columns, two tiles in flight (2 x 72 KB).
+// fp8 cache: the codes themselves are the A operand (5 chunks, the last one
+// columns 448 to 575, four tiles in flight), and the 16-bit operands are split
+// into two e4m3 parts that together hold a bf16's 8 bits: a query row, scaled by
+// a power of two, is q1 + q2 / 16; a weight is p1 + p2 / 512.  The parts are 2 NR
+// columns of one product, added when the sums are read.  (Widening the codes to
+// bf16 in shared memory instead took 4000 cycles per tile of producers' time,
+// against 1570 for its bytes from HBM.)
 //
-// Rows that a token must not see: rows behind every row's view are loaded as
-// zeros; in the tiles where tokens of one query tile see different rows, a row
-// holding a NaN or an infinity is loaded as zeros and marked, and its score
-// becomes NaN for the tokens that do see it.
+// Cost of a tile (measured, cycles per instruction: M = 64, N = 16 / 64 24 / 33;
+// M = 128 40 / 49; the A operand's shared memory reads bound both): bf16 36 + 16
+// instructions, 1500 cycles at NR = 16 and 2000 at NR = 64; fp8 18 + 8, 780 at
+// NR = 16.  HBM delivers a bf16 tile to each SM in 3140 cycles, an fp8 one in 1570.
+//
+// Roles (9 or 13 warps): 4 or 8 warps do the softmax (running maximum per query
+// row, rescaling O^T only when a maximum has grown by more than 2^8, or 2^4 for
+// fp8) and the output; one warp issues the matrix instructions; 4 warps load.
+// Whole tiles come by TMA where a tile is a few boxes of the paged cache (block
+// size a multiple of 8); the others, and the last tile of a sequence, whose rows
+// behind the end are zeros, by 16-byte asynchronous copies.
+//
+// Rows that a token must not see: rows behind every row's view are zeros; in
+// the tiles where tokens of one query tile see different rows, a row holding a
+// NaN or an infinity is stored as zeros and marked, and its score becomes NaN
+// for the tokens that do see it.
 //
 // Waits are bounded (wait_limit_ns): one that runs out marks the CTA as given
 // up, every later wait returns at once, and MLA_ERRBIT_TIMEOUT is set.
+#include <cuda.h>
+
 #include "mla_device.cuh"
 #include "mla_internal.h"
 #include "tensor_core.cuh"
@@ -44,50 +61,65 @@
 namespace mla {
 namespace {
 
-constexpr int kKeys = 64;                    // keys per tile
-constexpr int kChunk = kKeys * 128;          // bytes of a chunk: 64 keys x 64 columns
-constexpr int kChunks = 9;                   // 576 columns
-constexpr int kTile = kChunks * kChunk;      // 73728
-constexpr int kStages = 2;
-constexpr int kSoftWarps = 4;
-constexpr int kMmaWarp = kSoftWarps;
-constexpr int kProdWarp = kMmaWarp + 1;
-constexpr int kProdWarps = 8;
-constexpr int kWarps = kProdWarp + kProdWarps;
-constexpr int kThreads = kWarps * 32;
+constexpr int kKeys = 64;                 // keys per tile
+constexpr int kChunk = kKeys * 128;       // bytes of a chunk
+constexpr int kProdWarps = 4;
 constexpr int kProdThreads = kProdWarps * 32;
 constexpr int kRank = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kGrow = 8.0f;  // rescale when a maximum grows by more than this (log2)
-constexpr int kMinUnits = 2;   // a CTA takes at least this many units
+constexpr int kMinUnits = 2;              // a CTA takes at least this many units
+constexpr float kQ2 = 0.0625f;            // query parts: q = q1 + q2 / 16
+constexpr float kP2 = 1.0f / 512.0f;      // weight parts: p = p1 + p2 / 512
 
 // Key flags of a tile (one byte per key).
 constexpr uint32_t kAbsent = 1;  // its block was not found: left out
 constexpr uint32_t kPoison = 2;  // holds a NaN or an infinity
 
-template <int NR>
+template <int FMT, int NR>
 struct Lay {
-  static constexpr int kQBufs = NR <= 32 ? 2 : 1;
-  static constexpr int kQ = kChunks * NR * 128;
+  static constexpr bool kF8 = FMT != kBF16;
+  static constexpr int kParts = kF8 ? 2 : 1;            // columns per query row
+  static constexpr int kN = kParts * NR;
+  static constexpr int kChunks = kF8 ? 5 : 9;
+  static constexpr int kTile = kChunks * kChunk;
+  static constexpr int kStages = kF8 ? 4 : 2;
+  static constexpr int kQBufs = NR <= (kF8 ? 16 : 32) ? 2 : 1;
+  static constexpr int kQ = kChunks * kN * 128;
+  static constexpr int kSoftWarps = NR == 64 ? 8 : 4;   // 4 warps per 32 query rows
+  static constexpr int kCols = NR == 64 ? 32 : NR;      // query rows of a group of 4 warps
+  static constexpr int kMmaWarp = kSoftWarps;
+  static constexpr int kProdWarp = kMmaWarp + 1;
+  static constexpr int kWarps = kProdWarp + kProdWarps;
+  static constexpr int kThreads = kWarps * 32;
+  // a maximum may grow this much (log2) before the sums are rescaled; the fp8
+  // weights stay below 2^4 (p1 rounds by at most 1/2 there, p2 = 512 (p - p1) fits)
+  static constexpr float kGrow = kF8 ? 4.0f : 8.0f;
+  // shared memory
   static constexpr int q = kStages * kTile;
-  static constexpr int p = q + kQBufs * kQ;          // NR x 64 keys bf16
-  static constexpr int red = p + NR * 128;           // float [2][4][NR]
-  static constexpr int flags = red + 2 * 4 * NR * 4; // uint8 [kStages][64]
-  static constexpr int bars = flags + kStages * 64;
-  static constexpr int kBars = 13;
-  static constexpr int misc = bars + kBars * 8;      // Misc
+  static constexpr int p = q + kQBufs * kQ;              // kN rows x 128 bytes
+  static constexpr int red = p + kN * 128;               // float [2][kSoftWarps][kCols]
+  static constexpr int qs = red + 2 * kSoftWarps * kCols * 4;  // float [kQBufs][NR]
+  static constexpr int flags = qs + (kF8 ? kQBufs * NR * 4 : 0);  // uint8 [kStages][64]
+  static constexpr int bars = flags + kStages * kKeys;
+  // barriers, by index
+  static constexpr int kFull = 0, kEmpty = kStages, kQFull = 2 * kStages, kQEmpty = kQFull + 2,
+                       kSFull = kQEmpty + 2, kPFull = kSFull + 2, kPvDone = kPFull + 1,
+                       kOFree = kPvDone + 1, kBars = kOFree + 1;
+  static constexpr int misc = (bars + kBars * 8 + 15) / 16 * 16;
   static constexpr int bytes = misc + 64;
-  static constexpr int kCols = NR == 16 ? 128 : NR == 32 ? 256 : 512;
+  static_assert(bytes <= 232448, "shared memory of a CTA");
+  // tensor memory columns: two score buffers, then the sums of 4 x 128 dims
+  static constexpr int kO = 2 * kN;
+  static constexpr int kTmem = kN <= 16 ? 128 : kN <= 32 ? 256 : 512;
 };
-enum Bar { kFull = 0, kEmpty = 2, kQFull = 4, kQEmpty = 6, kSFull = 8, kPFull = 10, kPvDone = 11,
-           kOFree = 12 };
 
 struct Misc {
   uint32_t tmem;
   uint32_t abort;
-  int32_t s, qt, kt, ctas;
-  int64_t begin, count, total;
+  int32_t s, qt, kt, count;
+  int64_t begin, run;  // the first unit; units of the CTAs c >= extra (run + 1 of the ones before)
+  int32_t extra;
 };
 static_assert(sizeof(Misc) <= 64, "Misc fits");
 
@@ -102,6 +134,11 @@ struct Seq {
   int32_t nqt;       // query tiles
 };
 
+// Token of a sequence's query row (row < 2^31), by the reciprocal of num_heads.
+__device__ __forceinline__ int token_of(const LatentAttnArgs& a, uint32_t row) {
+  return (int)((__umulhi(row, a.heads_mul) + row) >> a.heads_shift);
+}
+
 template <int NR>
 __device__ __forceinline__ Seq load_seq(const LatentAttnArgs& a, int s) {
   Seq q;
@@ -110,7 +147,7 @@ __device__ __forceinline__ Seq load_seq(const LatentAttnArgs& a, int s) {
   q.kv = __ldg(a.kv_lens + s);
   q.t0 = max(c0, 0);
   q.ntok = max(min(q.c1, a.num_tokens) - q.t0, 0);
-  q.nqt = (int)(((int64_t)q.ntok * a.num_heads + NR - 1) / NR);
+  q.nqt = (int)(((uint32_t)q.ntok * (uint32_t)a.num_heads + NR - 1) / NR);
   return q;
 }
 // Rows that token t of the sequence sees.
@@ -121,8 +158,8 @@ __device__ __forceinline__ int seen_of(const LatentAttnArgs& a, const Seq& q, in
 // Rows that the last (first) row of query tile qt sees: the most (least) of its rows.
 template <int NR>
 __device__ __forceinline__ int most_seen(const LatentAttnArgs& a, const Seq& q, int qt) {
-  const int64_t last = min((int64_t)(qt + 1) * NR, (int64_t)q.ntok * a.num_heads) - 1;
-  return seen_of(a, q, q.t0 + (int)(last / a.num_heads));
+  const uint32_t last = min((uint32_t)(qt + 1) * NR, (uint32_t)q.ntok * (uint32_t)a.num_heads) - 1;
+  return seen_of(a, q, q.t0 + token_of(a, last));
 }
 // Key tiles of a query tile that sees `most` rows (one even when it sees none: its
 // rows are still written).
@@ -132,6 +169,7 @@ struct Tile {
   bool valid, first, last;  // first / last of this CTA's run of the query tile
   int s, qt, kt, nkt;
   int most, least;          // rows seen by the last / first row of the query tile
+  int t0, ntok;             // the sequence's tokens
 };
 
 // Walks a CTA's run of units; every role has its own copy.
@@ -139,33 +177,38 @@ template <int NR>
 struct Walk {
   Seq q;
   int s, qt, kt, nkt, most, least;
-  int64_t left;
+  int left;
   bool fresh;
   __device__ __forceinline__ void item(const LatentAttnArgs& a) {
     most = most_seen<NR>(a, q, qt);
-    least = seen_of(a, q, q.t0 + (int)((int64_t)qt * NR / a.num_heads));
+    least = seen_of(a, q, q.t0 + token_of(a, (uint32_t)qt * NR));
     nkt = key_tiles(most);
     fresh = true;
   }
-  __device__ __forceinline__ void start(const LatentAttnArgs& a, const Misc& m) {
+  __device__ __forceinline__ void start(const Misc& m) {
     s = m.s;
     qt = m.qt;
     kt = m.kt;
     left = m.count;
-    if (left > 0) {
-      q = load_seq<NR>(a, s);
-      item(a);
-    }
+    nkt = 0;
+    q.nqt = 0;
   }
+  // The next unit.  Each role calls this at one place only: 13 warps of different
+  // code share the instruction caches.
   __device__ __forceinline__ Tile next(const LatentAttnArgs& a) {
     Tile t{};
     if (left <= 0) return t;
-    if (kt == nkt) {
-      kt = 0;
-      ++qt;
-      while (qt >= q.nqt && s + 1 < a.num_seqs) {
-        q = load_seq<NR>(a, ++s);
-        qt = 0;
+    if (kt >= nkt) {  // another query tile (the first: nkt is 0)
+      if (nkt > 0) {
+        kt = 0;
+        ++qt;
+        if (qt >= q.nqt) {
+          qt = 0;
+          do q = load_seq<NR>(a, ++s);
+          while (q.nqt == 0 && s + 1 < a.num_seqs);
+        }
+      } else {
+        q = load_seq<NR>(a, s);
       }
       item(a);
     }
@@ -178,6 +221,8 @@ struct Walk {
     t.nkt = nkt;
     t.most = most;
     t.least = least;
+    t.t0 = q.t0;
+    t.ntok = q.ntok;
     --left;
     t.last = kt == nkt || left == 0;
     return t;
@@ -189,19 +234,19 @@ struct Waiter {
   uint32_t abort;  // shared address of Misc::abort
   uint64_t limit;
   __device__ __forceinline__ bool given_up() const { return lds_u32(abort) != 0; }
+  // Called now and then while waiting; since: 0 at first.
+  __device__ __forceinline__ bool expired(uint64_t& since) const {
+    if (given_up()) return true;
+    const uint64_t now = global_ns();
+    if (since == 0) since = now;
+    if (now - since <= limit) return false;
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(abort), "r"(1u) : "memory");
+    return true;
+  }
   __device__ __forceinline__ void operator()(uint32_t bar, uint32_t parity) const {
-    if (mbar_try_wait(bar, parity)) return;
-    const uint64_t t0 = global_ns();
-    for (uint32_t spin = 1;; ++spin) {
-      if (mbar_try_wait(bar, parity)) return;
-      if ((spin & 31u) == 0) {
-        if (given_up()) return;
-        if (global_ns() - t0 > limit) {
-          asm volatile("st.shared.u32 [%0], %1;" ::"r"(abort), "r"(1u) : "memory");
-          return;
-        }
-      }
-    }
+    uint64_t since = 0;
+    for (uint32_t spin = 1; !mbar_try_wait(bar, parity); ++spin)
+      if ((spin & 31u) == 0 && expired(since)) return;
   }
 };
 
@@ -213,13 +258,20 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
 __device__ __forceinline__ void sts_u8(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
+__device__ __forceinline__ void sts_u16(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"((uint16_t)v) : "memory");
+}
+__device__ __forceinline__ void sts_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
 }
-__device__ __forceinline__ void soft_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kSoftWarps * 32) : "memory");
+// A barrier of the four warps of one softmax group.
+__device__ __forceinline__ void soft_sync(int group) {
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -241,32 +293,40 @@ __device__ __forceinline__ bool any_special(uint4 v) {
   return (m & (FMT == kBF16 ? 0x80008000u : 0x80808080u)) != 0;
 }
 
-// The address of row p of sequence s, or nullptr: not seen by any row of the
-// query tile (p >= most), or its block cannot be found (flag kAbsent).
-__device__ __forceinline__ const uint8_t* find_row(const LatentAttnArgs& a, int s, int p, int most,
-                                                   uint32_t& flag) {
-  flag = 0;
-  if (p >= most) return nullptr;
+// The block of row p of sequence s: an id to be checked, or kUnseen when no row of
+// the query tile sees it.  The table's answer is not looked at here, so its load
+// runs on while the tile before is produced.
+constexpr int32_t kUnseen = INT32_MIN;
+__device__ __forceinline__ int32_t find_block(const LatentAttnArgs& a, const Tile& t, int p) {
   const int kb = a.bs_shift >= 0 ? p >> a.bs_shift : p / a.block_size;
-  const int32_t blk = __ldg(a.block_table + (int64_t)s * a.bt_stride + kb);
-  if (blk < 0 || blk >= a.num_blocks) {
-    flag = kAbsent;
-    return nullptr;
-  }
-  return a.cache + (int64_t)blk * a.block_stride + (int64_t)(p - kb * a.block_size) * a.entry_stride;
+  int32_t blk = kUnseen;
+  if (t.valid && p < t.most) blk = __ldg(a.block_table + (int64_t)t.s * a.bt_stride + kb);
+  return blk;
+}
+// The address of row p in that block, or nullptr: unseen, or not found (flag kAbsent).
+__device__ __forceinline__ const uint8_t* row_in(const LatentAttnArgs& a, int p, int32_t blk,
+                                                 uint32_t& flag) {
+  const bool ok = blk >= 0 && blk < a.num_blocks;
+  flag = ok || blk == kUnseen ? 0 : kAbsent;
+  const int off = a.bs_shift >= 0 ? p & (a.block_size - 1) : p % a.block_size;
+  const uint8_t* r = a.cache + (int64_t)blk * a.block_stride + (int64_t)off * a.entry_stride;
+  return ok ? r : nullptr;
 }
 
 // ------------------------------------------------------------------ producers
+// One query tile into shared memory: bf16 rows by asynchronous copies.
 template <int NR>
-__device__ __forceinline__ void load_q(const LatentAttnArgs& a, const Seq& q, int qt, uint32_t dst,
-                                       int pw, int lane) {
-  const int64_t rows = (int64_t)q.ntok * a.num_heads;
+__device__ __forceinline__ void load_q(const LatentAttnArgs& a, const Tile& q, uint32_t dst,
+                                       uint32_t bar, int pw, int lane) {
+  const uint32_t rows = (uint32_t)q.ntok * (uint32_t)a.num_heads;
   const int col = lane & 7;
+#pragma unroll 1
   for (int r = pw * 4 + (lane >> 3); r < NR; r += kProdWarps * 4) {
-    const int64_t row = (int64_t)qt * NR + r;
+    const uint32_t row = (uint32_t)q.qt * NR + r;
     const bool ok = row < rows;
-    const int64_t t = ok ? q.t0 + row / a.num_heads : 0;
-    const int64_t h = ok ? row % a.num_heads : 0;
+    const int tok = ok ? token_of(a, row) : 0;
+    const int64_t t = ok ? q.t0 + tok : 0;
+    const int64_t h = ok ? (int)row - tok * a.num_heads : 0;
     const uint8_t* c = a.q_c + t * a.qc_ts + h * a.qc_hs + col * 16;
     const uint8_t* pe = a.q_pe + t * a.qp_ts + h * a.qp_hs + col * 16;
     const uint32_t d = dst + r * 128 + ((col ^ (r & 7)) << 4);
@@ -274,194 +334,315 @@ __device__ __forceinline__ void load_q(const LatentAttnArgs& a, const Seq& q, in
     for (int ch = 0; ch < 8; ++ch) tc::cp_async16(d + ch * (NR * 128), c + ch * 128, ok);
     tc::cp_async16(d + 8 * (NR * 128), pe, ok);
   }
+  tc::cp_async_arrive(bar);
+}
+// The same as two e4m3 parts of the row times a power of two: with the largest
+// magnitude in [2^7, 2^8), q1 = e4m3(q) rounds by at most 8 and q2 = e4m3(16 (q -
+// q1)).  q1 + q2 / 16 has every bit of a bf16 down to 2^-14 of the largest, and
+// is off by at most 2^-22 of it below.  A row with a NaN or an infinity gets NaN
+// as its inverse scale.  A warp takes a row; lane l has columns 16 l .. 16 l + 15
+// and 512 + 2 l, 513 + 2 l.
+template <int NR>
+__device__ __forceinline__ void split_q(const LatentAttnArgs& a, const Tile& q, uint32_t dst,
+                                        uint32_t scales, uint32_t bar, int pw, int lane) {
+  const uint32_t rows = (uint32_t)q.ntok * (uint32_t)a.num_heads;
+#pragma unroll 1
+  for (int r = pw; r < NR; r += kProdWarps) {
+    const uint32_t row = (uint32_t)q.qt * NR + r;
+    uint32_t w[9] = {};
+    if (row < rows) {
+      const int tok = token_of(a, row);
+      const int64_t t = q.t0 + tok, h = (int)row - tok * a.num_heads;
+      const uint8_t* c = a.q_c + t * a.qc_ts + h * a.qc_hs + lane * 32;
+      const uint4 v0 = ld_stream16(c), v1 = ld_stream16(c + 16);
+      w[8] = *reinterpret_cast<const uint32_t*>(a.q_pe + t * a.qp_ts + h * a.qp_hs + lane * 4);
+      w[0] = v0.x; w[1] = v0.y; w[2] = v0.z; w[3] = v0.w;
+      w[4] = v1.x; w[5] = v1.y; w[6] = v1.z; w[7] = v1.w;
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 9; ++i) top = umax16x2(top, w[i] & 0x7FFF7FFFu);
+    top = __reduce_max_sync(0xFFFFFFFFu, max(top & 0xFFFFu, top >> 16));
+    const uint32_t e = max(top >> 7, 8u);  // exponent field of the largest magnitude
+    const float s = __uint_as_float((261u - e) << 23);  // 2^(134 - e)
+    uint32_t p1[9], p2[9];  // two codes in the low half of each
+#pragma unroll
+    for (int i = 0; i < 9; ++i) {
+      const float x0 = bf16lo(w[i]) * s, x1 = bf16hi(w[i]) * s;
+      p1[i] = pack_fp8x2<kE4M3>(x0, x1);
+      float y0, y1;
+      fp8x2_to_f32x2<kE4M3>(p1[i], y0, y1);
+      p2[i] = pack_fp8x2<kE4M3>((x0 - y0) * 16.0f, (x1 - y1) * 16.0f);
+    }
+    const int ch = lane >> 3;
+    const uint32_t in = (uint32_t)(((lane & 7) ^ (r & 7)) << 4);  // NR is a multiple of 8
+    const uint32_t d = dst + ch * (2 * NR * 128) + r * 128 + in;
+    sts16(d, make_uint4(p1[0] | p1[1] << 16, p1[2] | p1[3] << 16, p1[4] | p1[5] << 16,
+                        p1[6] | p1[7] << 16));
+    sts16(d + NR * 128, make_uint4(p2[0] | p2[1] << 16, p2[2] | p2[3] << 16, p2[4] | p2[5] << 16,
+                                   p2[6] | p2[7] << 16));
+    const uint32_t dr = dst + 4 * (2 * NR * 128) + r * 128 + ((ch ^ (r & 7)) << 4) + 2 * (lane & 7);
+    sts_u16(dr, p1[8]);
+    sts_u16(dr + NR * 128, p2[8]);
+    if (lane == 0)
+      sts_u32(scales + 4 * r, top >= 0x7F80u ? 0x7FC00000u : (e - 7u) << 23);  // 2^(e - 134)
+  }
+  __syncwarp();
+  if (lane == 0) mbar_arrive_n(bar, 32);
 }
 
 template <int FMT, int NR>
-__device__ __forceinline__ void produce(const LatentAttnArgs& a, const Misc& m, uint32_t smem,
-                                        const Waiter& wait, int pw, int lane, uint32_t& errbits) {
-  using L = Lay<NR>;
+__device__ __forceinline__ void produce(const LatentAttnArgs& a, const CUtensorMap* map,
+                                        const Misc& m, uint32_t smem, const Waiter& wait, int pw,
+                                        int lane, uint32_t& errbits) {
+  using L = Lay<FMT, NR>;
   const uint32_t bars = smem + L::bars;
   Walk<NR> walk;
-  walk.start(a, m);
-  // bf16: 8 lanes x 16 bytes per row, rows pw * 8 + lane / 8 and + 4.
-  // fp8: 4 lanes x 16 bytes per row, row pw * 8 + lane / 4.
-  constexpr int kRows = FMT == kBF16 ? 2 : 1;
-  const int row0 = pw * 8 + (FMT == kBF16 ? lane >> 3 : lane >> 2);
-  const int col = FMT == kBF16 ? lane & 7 : lane & 3;
-  const bool marks = col == 0;  // the lane that writes its rows' flags
-  Tile cur = walk.next(a);
-  Seq cq = walk.q;
-  const uint8_t* src[kRows];
-  uint32_t flag[kRows];
+  walk.start(m);
+  // Row copies: 8 lanes x 16 bytes per row and chunk; this thread has the rows
+  // pw * 16 + 4 i + lane / 8.  Boxes: box_rows keys x one chunk; the first warp's
+  // lane l has the boxes of keys (l % boxes) * box_rows.
+  constexpr int kRows = 4;
+  const int row0 = pw * 16 + (lane >> 3), col = lane & 7;
+  const int boxes = a.box_rows ? kKeys / a.box_rows : 0;
+  const int box = boxes ? lane & (boxes - 1) : 0;
+  // whole tiles, whose rows every row of the query tile sees
+  auto by_box = [&](const Tile& t) { return boxes && (t.kt + 1) * kKeys <= t.least; };
+  // Blocks are looked up two tiles ahead.
+  Tile cur{}, nxt{};
+  int32_t blk[kRows] = {}, nblk[kRows] = {};
+  uint32_t item = 0;
+#pragma unroll 1
+  for (int step = -2;; ++step) {
+    const Tile far = walk.next(a);
+    int32_t fblk[kRows];
+    if (by_box(far)) {
+      fblk[0] = pw == 0 ? find_block(a, far, far.kt * kKeys + box * a.box_rows) : kUnseen;
+    } else {
 #pragma unroll
-  for (int i = 0; i < kRows; ++i)
-    src[i] = cur.valid ? find_row(a, cur.s, cur.kt * kKeys + row0 + 4 * i, cur.most, flag[i]) : nullptr;
-  uint4 reg[FMT == kBF16 ? 1 : kChunks];
-  if constexpr (FMT != kBF16) {
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c)
-      reg[c] = src[0] ? ld_stream16(src[0] + col * 16 + c * 64) : make_uint4(0, 0, 0, 0);
-  }
-  uint32_t g = 0, item = 0;
-  for (; cur.valid; ++g) {
-    if (cur.first) {
-      const int b = item % L::kQBufs;
-      const uint32_t n = item / L::kQBufs;
-      if (n > 0) wait(bars + 8 * (kQEmpty + b), (n - 1) & 1);
-      load_q<NR>(a, cq, cur.qt, smem + L::q + b * L::kQ, pw, lane);
-      tc::cp_async_arrive(bars + 8 * (kQFull + b));
-      ++item;
+      for (int i = 0; i < kRows; ++i) fblk[i] = find_block(a, far, far.kt * kKeys + row0 + 4 * i);
     }
-    const Tile nxt = walk.next(a);
-    const uint8_t* nsrc[kRows];
-    uint32_t nflag[kRows];
-#pragma unroll
-    for (int i = 0; i < kRows; ++i)
-      nsrc[i] = nxt.valid ? find_row(a, nxt.s, nxt.kt * kKeys + row0 + 4 * i, nxt.most, nflag[i])
-                          : nullptr;
-    const int st = g & 1;
-    const uint32_t full = bars + 8 * (kFull + st);
-    if (g >= kStages) wait(bars + 8 * (kEmpty + st), ((g >> 1) - 1) & 1);
-    const uint32_t base = smem + st * kTile;
-    // tokens of the query tile see different rows of this key tile
-    const bool mixed = cur.least < cur.most && (cur.kt + 1) * kKeys > cur.least;
-#pragma unroll
-    for (int i = 0; i < kRows; ++i)
-      if (flag[i]) errbits |= kErrBlockOOB;
-    if constexpr (FMT == kBF16) {
-      if (!mixed) {
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-          const int row = row0 + 4 * i;
-          const uint32_t d = base + row * 128 + ((col ^ (row & 7)) << 4);
-          const uint8_t* p = src[i] ? src[i] + col * 16 : a.cache;
-#pragma unroll
-          for (int c = 0; c < kChunks; ++c) tc::cp_async16(d + c * kChunk, p + (src[i] ? c * 128 : 0), src[i] != nullptr);
+    if (cur.valid) {
+      if (cur.first) {
+        const int b = item % L::kQBufs;
+        const uint32_t n = item / L::kQBufs;
+        if (n > 0) wait(bars + 8 * (L::kQEmpty + b), (n - 1) & 1);
+        const uint32_t dst = smem + L::q + b * L::kQ, bar = bars + 8 * (L::kQFull + b);
+        if constexpr (L::kF8) split_q<NR>(a, cur, dst, smem + L::qs + b * NR * 4, bar, pw, lane);
+        else load_q<NR>(a, cur, dst, bar, pw, lane);
+        ++item;
+      }
+      const uint32_t g = step;
+      const int st = g % L::kStages;
+      const uint32_t full = bars + 8 * (L::kFull + st), flags = smem + L::flags + st * kKeys;
+      if (g >= L::kStages) wait(bars + 8 * (L::kEmpty + st), (g / L::kStages - 1) & 1);
+      __syncwarp();
+      const uint32_t base = smem + st * L::kTile;
+      if (by_box(cur)) {
+        if (pw == 0) {
+          const bool ok = blk[0] >= 0 && blk[0] < a.num_blocks;
+          if (!ok) errbits |= kErrBlockOOB;
+          const uint32_t none = __shfl_sync(0xFFFFFFFFu, ok ? 0u : 0x01010101u * kAbsent,
+                                            (lane & 15) * 4 / a.box_rows);
+          if (lane < 16) sts_u32(flags + 4 * lane, none);
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive_expect_tx(full, L::kTile);
+            mbar_arrive_n(full, 32);
+          }
+          __syncwarp();
+          const int p = cur.kt * kKeys + box * a.box_rows;
+          const int off = a.bs_shift >= 0 ? p & (a.block_size - 1) : p % a.block_size;
+          const int z = ok ? blk[0] : (int)a.num_blocks;  // outside the tensor: zeros
+          for (int i = lane / boxes; i < L::kChunks; i += 32 / boxes)
+            tc::tma_load3(base + i * kChunk + box * a.box_rows * 128, map,
+                          L::kF8 ? (i < 4 ? i * 128 : 448) : i * 64, off, z, full);
+        } else if (lane == 0) {
+          mbar_arrive_n(full, 33);
         }
       } else {
-#pragma unroll
+        // tokens of the query tile see different rows of this key tile
+        const bool mixed = cur.least < cur.most && (cur.kt + 1) * kKeys > cur.least;
+#pragma unroll 1
         for (int i = 0; i < kRows; ++i) {
           const int row = row0 + 4 * i;
+          const int32_t bi = i == 0 ? blk[0] : i == 1 ? blk[1] : i == 2 ? blk[2] : blk[3];
+          uint32_t flag;
+          const uint8_t* src = row_in(a, cur.kt * kKeys + row, bi, flag);
+          if (flag) errbits |= kErrBlockOOB;
           const uint32_t d = base + row * 128 + ((col ^ (row & 7)) << 4);
-          uint4 v[kChunks];
-          bool sp = false;
+          // the 16-byte parts of this lane: chunk c, and for fp8 the rotary columns of
+          // the last chunk (its upper half) in lanes 4 to 7
+          auto part = [&](int c) { return !L::kF8 || c < 4 ? c * 128 + col * 16 : 512 + (col - 4) * 16; };
+          auto has = [&](int c) { return !L::kF8 || c < 4 || col >= 4; };
+          if (!mixed) {
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c) {
-            v[c] = src[i] ? ld_stream16(src[i] + col * 16 + c * 128) : make_uint4(0, 0, 0, 0);
-            sp |= any_special<kBF16>(v[c]);
+            for (int c = 0; c < L::kChunks; ++c)
+              if (has(c)) tc::cp_async16(d + c * kChunk, src ? src + part(c) : a.cache, src != nullptr);
+          } else {
+            uint4 v[L::kChunks];
+            bool sp = false;
+#pragma unroll
+            for (int c = 0; c < L::kChunks; ++c) {
+              v[c] = src && has(c) ? ld_stream16(src + part(c)) : make_uint4(0, 0, 0, 0);
+              sp |= any_special<FMT>(v[c]);
+            }
+            const bool drop = __ballot_sync(0xFFFFFFFFu, sp) & (0xFFu << (lane & 24));
+            if (drop) flag = kPoison;
+#pragma unroll
+            for (int c = 0; c < L::kChunks; ++c)
+              if (has(c)) sts16(d + c * kChunk, drop ? make_uint4(0, 0, 0, 0) : v[c]);
           }
-          const uint32_t who = __ballot_sync(0xFFFFFFFFu, sp);
-          if (who & (0xFFu << (lane & 24))) {
-            flag[i] = kPoison;
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c) v[c] = make_uint4(0, 0, 0, 0);
-          }
-#pragma unroll
-          for (int c = 0; c < kChunks; ++c) sts16(d + c * kChunk, v[c]);
+          if (col == 0) sts_u8(flags + row, flag);
         }
-        tc::fence_smem_async();
-      }
-    } else {
-      const int row = row0;
-      if (mixed) {
-        bool sp = false;
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) sp |= any_special<FMT>(reg[c]);
-        const uint32_t who = __ballot_sync(0xFFFFFFFFu, sp);
-        if (who & (0xFu << (lane & 28))) {
-          flag[0] = kPoison;
-#pragma unroll
-          for (int c = 0; c < kChunks; ++c) reg[c] = make_uint4(0, 0, 0, 0);
+        __syncwarp();
+        if (mixed) {
+          if (lane == 0) mbar_arrive_n(full, 33);
+        } else {
+          if (lane == 0) mbar_arrive(full);
+          tc::cp_async_arrive(full);
         }
       }
-      const uint32_t d0 = base + row * 128 + (((2 * col) ^ (row & 7)) << 4);
-      const uint32_t d1 = base + row * 128 + (((2 * col + 1) ^ (row & 7)) << 4);
-#pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        const uint4 v = reg[c];
-        sts16(d0 + c * kChunk, fp8x8_to_x16x8<FMT, kBF16>(make_uint2(v.x, v.y)));
-        sts16(d1 + c * kChunk, fp8x8_to_x16x8<FMT, kBF16>(make_uint2(v.z, v.w)));
-        reg[c] = nsrc[0] ? ld_stream16(nsrc[0] + col * 16 + c * 64) : make_uint4(0, 0, 0, 0);
-      }
-      tc::fence_smem_async();
     }
-    if (marks) {
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) sts_u8(smem + L::flags + st * kKeys + row0 + 4 * i, flag[i]);
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(full);
-    if (FMT == kBF16 && !mixed) tc::cp_async_arrive(full);
-    else mbar_arrive(full);
     cur = nxt;
-    cq = walk.q;
+    nxt = far;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      src[i] = nsrc[i];
-      flag[i] = nflag[i];
+      blk[i] = nblk[i];
+      nblk[i] = fblk[i];
     }
+    if (step >= -1 && !cur.valid) break;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // --------------------------------------------------------------- matrix issue
-template <int NR>
+// The whole warp runs this; one elected lane issues.  Stage and query buffer are
+// template arguments, so every descriptor is the shared base plus a constant
+// (computed per instruction in a branch of one lane they cost ~90 cycles each,
+// three times the instruction).
+template <int FMT, int NR, int ST, int QB>
+__device__ __forceinline__ void issue_scores(uint32_t smem, uint32_t tmem, bool one, bool last) {
+  using L = Lay<FMT, NR>;
+  constexpr uint32_t kId =
+      tc::instr_desc(kKeys, L::kN, false, FMT == kE4M3 ? 0 : 1, L::kF8 ? 0 : 1);
+  const uint64_t ka = tc::smem_desc(smem + ST * L::kTile, 0, 1024);
+  const uint64_t qa = tc::smem_desc(smem + L::q + QB * L::kQ, 0, 1024);
+  const uint32_t d = tmem + (ST & 1) * L::kN;
+#pragma unroll
+  for (int c = 0; c < L::kChunks; ++c)
+#pragma unroll
+    for (int k = 0; k < (L::kF8 && c == 4 ? 2 : 4); ++k) {
+      // a k step is 32 bytes of a row; the fp8 rotary columns are the upper half of
+      // their chunk, the lower half of the query's
+      const uint64_t ak = ka + (c * kChunk >> 4) + 2 * k + (L::kF8 && c == 4 ? 4 : 0);
+      const uint64_t bk = qa + (c * L::kN * 128 >> 4) + 2 * k;
+      if constexpr (L::kF8) tc::mma_fp8(one, d, ak, bk, kId, c + k > 0);
+      else tc::mma_bf16(one, d, ak, bk, kId, c + k > 0);
+    }
+  tc::commit(one, smem + L::bars + 8 * (L::kSFull + (ST & 1)));
+  if (last) tc::commit(one, smem + L::bars + 8 * (L::kQEmpty + QB));
+}
+template <int FMT, int NR, int ST>
+__device__ __forceinline__ void issue_outputs(uint32_t smem, uint32_t tmem, bool one, bool first) {
+  using L = Lay<FMT, NR>;
+  constexpr uint32_t kId = tc::instr_desc(128, L::kN, true, FMT == kE4M3 ? 0 : 1, L::kF8 ? 0 : 1);
+  // The K tile, MN-major.  128 dims are two bf16 chunks or one fp8 chunk; a k step
+  // is 16 keys (2 groups of 8 rows) or 32.
+  const uint64_t va = tc::smem_desc(smem + ST * L::kTile, L::kF8 ? 0 : kChunk, 1024);
+  const uint64_t pa = tc::smem_desc(smem + L::p, 0, 1024);
+  constexpr int kDims = L::kF8 ? kChunk : 2 * kChunk, kStep = L::kF8 ? 4096 : 2048;
+#pragma unroll
+  for (int b = 0; b < 4; ++b)
+#pragma unroll
+    for (int k = 0; k < (L::kF8 ? 2 : 4); ++k) {
+      const uint32_t d = tmem + L::kO + b * L::kN;
+      const uint64_t ak = va + (b * kDims >> 4) + k * (kStep >> 4), bk = pa + 2 * k;
+      if constexpr (L::kF8) tc::mma_fp8(one, d, ak, bk, kId, k > 0 || !first);
+      else tc::mma_bf16(one, d, ak, bk, kId, k > 0 || !first);
+    }
+  tc::commit(one, smem + L::bars + 8 * (L::kEmpty + ST));
+  tc::commit(one, smem + L::bars + 8 * L::kPvDone);
+}
+
+template <int FMT, int NR>
 __device__ __forceinline__ void issue_mma(const LatentAttnArgs& a, const Misc& m, uint32_t smem,
                                           uint32_t tmem, const Waiter& wait) {
-  using L = Lay<NR>;
-  constexpr uint32_t kIdS = tc::instr_desc(kKeys, NR, false);
-  constexpr uint32_t kIdO = tc::instr_desc(128, NR, true);
+  using L = Lay<FMT, NR>;
   const uint32_t bars = smem + L::bars;
-  const uint64_t dk = tc::smem_desc(smem, 0, 1024);            // K tiles, K-major
-  const uint64_t dv = tc::smem_desc(smem, kChunk, 1024);       // the same, MN-major
-  const uint64_t dq = tc::smem_desc(smem + L::q, 0, 1024);
-  const uint64_t dp = tc::smem_desc(smem + L::p, 0, 1024);
   Walk<NR> walk;
-  walk.start(a, m);
-  uint32_t items = 0;  // query tiles whose scores have begun
+  walk.start(m);
+  const bool one = tc::elect();
+  uint32_t items = 0;       // query tiles whose scores have begun
+  uint32_t done_items = 0;  // query tiles whose outputs have begun
+  // whether tile g's rows (and its query) are there
+  auto loaded = [&](const Tile& t, uint32_t g) {
+    return mbar_test(bars + 8 * (L::kFull + g % L::kStages), (g / L::kStages) & 1) &&
+           (!t.first ||
+            mbar_test(bars + 8 * (L::kQFull + items % L::kQBufs), (items / L::kQBufs) & 1));
+  };
   auto scores = [&](const Tile& t, uint32_t g) {
-    if (t.first) {
-      wait(bars + 8 * (kQFull + items % L::kQBufs), (items / L::kQBufs) & 1);
-      ++items;
-    }
-    wait(bars + 8 * (kFull + (g & 1)), (g >> 1) & 1);
+    items += t.first;
+    // Rows may have been written by ordinary and asynchronous stores of the
+    // producers; the fence towards the tensor core's reads stands here, behind the
+    // barrier (in the producers it would also wait for their loads in flight).
     tc::fence_smem_async();
     tc::fence_after_sync();
-    const int qb = (items - 1) % L::kQBufs;
-    const uint64_t ka = dk + ((g & 1) * kTile >> 4);
-    const uint64_t qa = dq + (qb * L::kQ >> 4);
-#pragma unroll 1
-    for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        tc::mma_bf16(tmem + (g & 1) * NR, ka + (c * kChunk >> 4) + 2 * k,
-                     qa + (c * NR * 128 >> 4) + 2 * k, kIdS, c + k > 0);
-    tc::commit(bars + 8 * (kSFull + (g & 1)));
-    if (t.last) tc::commit(bars + 8 * (kQEmpty + qb));
-  };
-  Tile cur = walk.next(a);
-  if (cur.valid) scores(cur, 0);
-  uint32_t done_items = 0;
-  for (uint32_t g = 0; cur.valid; ++g) {
-    const Tile nxt = walk.next(a);
-    const bool ahead = nxt.valid && (!nxt.first || L::kQBufs > 1);
-    if (ahead) scores(nxt, g + 1);
-    wait(bars + 8 * kPFull, g & 1);
-    if (cur.first) {
-      if (done_items > 0) wait(bars + 8 * kOFree, (done_items - 1) & 1);
-      ++done_items;
+    constexpr int kQ1 = L::kQBufs - 1, kS2 = L::kStages - 2, kS3 = L::kStages - 1;
+    const int st = g % L::kStages;
+    if (L::kQBufs == 1 || (items & 1)) {
+      if (st == 0) issue_scores<FMT, NR, 0, 0>(smem, tmem, one, t.last);
+      else if (st == 1) issue_scores<FMT, NR, 1, 0>(smem, tmem, one, t.last);
+      else if (st == 2) issue_scores<FMT, NR, kS2, 0>(smem, tmem, one, t.last);
+      else issue_scores<FMT, NR, kS3, 0>(smem, tmem, one, t.last);
+    } else {
+      if (st == 0) issue_scores<FMT, NR, 0, kQ1>(smem, tmem, one, t.last);
+      else if (st == 1) issue_scores<FMT, NR, 1, kQ1>(smem, tmem, one, t.last);
+      else if (st == 2) issue_scores<FMT, NR, kS2, kQ1>(smem, tmem, one, t.last);
+      else issue_scores<FMT, NR, kS3, kQ1>(smem, tmem, one, t.last);
     }
+  };
+  auto weighted = [&](const Tile& t, uint32_t g) {
+    return mbar_test(bars + 8 * L::kPFull, g & 1) &&
+           (!t.first || done_items == 0 || mbar_test(bars + 8 * L::kOFree, (done_items - 1) & 1));
+  };
+  auto outputs = [&](const Tile& t, uint32_t g) {
+    done_items += t.first;
     tc::fence_after_sync();
-    const uint64_t va = dv + ((g & 1) * kTile >> 4);
+    constexpr int kS2 = L::kStages - 2, kS3 = L::kStages - 1;
+    const int st = g % L::kStages;
+    if (st == 0) issue_outputs<FMT, NR, 0>(smem, tmem, one, t.first);
+    else if (st == 1) issue_outputs<FMT, NR, 1>(smem, tmem, one, t.first);
+    else if (st == 2) issue_outputs<FMT, NR, kS2>(smem, tmem, one, t.first);
+    else issue_outputs<FMT, NR, kS3>(smem, tmem, one, t.first);
+  };
+  Tile cur{};
+  // The scores of tile g and the outputs of tile g - 1 are issued as each
+  // becomes ready, scores first: waiting for rows never holds back outputs (they
+  // free the stage that the rows behind them need).  With one query buffer the
+  // scores of a new query tile come after the outputs before them: their query
+  // is loaded over the old one.
 #pragma unroll 1
-    for (int b = 0; b < 4; ++b)
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        tc::mma_bf16(tmem + 2 * NR + b * NR, va + (2 * b * kChunk >> 4) + k * (2048 >> 4), dp + 2 * k,
-                     kIdO, k > 0 || !cur.first);
-    tc::commit(bars + 8 * (kEmpty + (g & 1)));
-    tc::commit(bars + 8 * kPvDone);
-    if (nxt.valid && !ahead) scores(nxt, g + 1);
+  for (uint32_t g = 0;; ++g) {
+    const Tile nxt = walk.next(a);
+    if (!cur.valid && !nxt.valid) break;
+    bool s_due = nxt.valid, o_due = cur.valid;
+    const bool s_held = L::kQBufs == 1 && nxt.first;
+    uint64_t since = 0;
+#pragma unroll 1
+    for (uint32_t spin = 1; s_due || o_due; ++spin) {
+      const bool lost = (spin & 127u) == 0 && wait.expired(since);
+      const bool s_go = s_due && !(s_held && o_due) && (loaded(nxt, g) || lost);
+      if (__all_sync(0xFFFFFFFFu, s_go)) {
+        scores(nxt, g);
+        s_due = false;
+      }
+      const bool o_go = o_due && (weighted(cur, g - 1) || lost);
+      if (__all_sync(0xFFFFFFFFu, o_go)) {
+        outputs(cur, g - 1);
+        o_due = false;
+      }
+    }
     cur = nxt;
   }
 }
@@ -487,66 +668,91 @@ template <int FMT, int NR>
 __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Misc& m, uint32_t smem,
                                        uint32_t tmem, const Waiter& waiter, int warp, int lane,
                                        const Workspace& ws) {
-  using L = Lay<NR>;
-  constexpr int kG = NR / 8;  // column groups; a thread has columns 8 j + 2 (lane % 4) + {0, 1}
+  using L = Lay<FMT, NR>;
+  constexpr int kC = L::kCols;  // query rows of this group of four warps
+  constexpr int kG = kC / 8;    // a thread has the rows 8 j + 2 (lane % 4) + {0, 1} of them
+  const int group = warp >> 2, w4 = warp & 3, col0 = group * kC;
   const uint32_t bars = smem + L::bars;
   auto wait = [&](uint32_t bar, uint32_t parity) {
     waiter(bar, parity);
     __syncwarp();
   };
-  const uint32_t sub = tmem + ((uint32_t)(warp * 32) << 16);  // this warp's lanes
+  const uint32_t sub = tmem + ((uint32_t)(w4 * 32) << 16);  // this warp's lanes
   const float ks = FMT == kBF16 ? 1.0f : __ldg(a.k_scale);
   const float c = a.softmax_scale * ks * kLog2e;
   const int c2 = 2 * (lane & 3);
-  const int key0 = warp * 16 + (lane >> 2);  // and + 8
+  const int key0 = w4 * 16 + (lane >> 2);  // and + 8
   float* red = reinterpret_cast<float*>(__cvta_shared_to_generic(smem + L::red));
   float mu[kG][2], l[kG][2];
-  int seen[kG][2];
+  float cs[kG][2];  // score of a product: softmax and cache scale, log2 e, the query row's scale
   Walk<NR> walk;
-  walk.start(a, m);
+  walk.start(m);
   int kt_begin = 0;
-  uint32_t g = 0;
-  for (Tile t = walk.next(a); t.valid; t = walk.next(a), ++g) {
+  uint32_t g = 0, item = 0;
+#pragma unroll 1
+  for (;; ++g) {
+    const Tile t = walk.next(a);
+    if (!t.valid) break;
     if (t.first) {
       kt_begin = t.kt;
+      const uint32_t scales = smem + L::qs + (item % L::kQBufs) * NR * 4;
+      if constexpr (L::kF8) wait(bars + 8 * (L::kQFull + item % L::kQBufs), (item / L::kQBufs) & 1);
 #pragma unroll
       for (int j = 0; j < kG; ++j)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          // a row behind the last one (its query is zeros) copies the last one's view
-          const int64_t row = min((int64_t)t.qt * NR + 8 * j + c2 + e,
-                                  (int64_t)walk.q.ntok * a.num_heads - 1);
-          seen[j][e] = seen_of(a, walk.q, walk.q.t0 + (int)(row / a.num_heads));
+          cs[j][e] = c;
+          if constexpr (L::kF8)
+            cs[j][e] = c * __uint_as_float(lds_u32(scales + 4 * (col0 + 8 * j + c2 + e)));
           l[j][e] = 0.0f;
           mu[j][e] = -INFINITY;
         }
+      if constexpr (L::kF8) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + 8 * (L::kQEmpty + item % L::kQBufs));
+      }
+      ++item;
     }
     const int b = g & 1;
-    wait(bars + 8 * (kFull + b), (g >> 1) & 1);  // the key flags
-    wait(bars + 8 * (kSFull + b), (g >> 1) & 1);
+    const int st = g % L::kStages;
+    wait(bars + 8 * (L::kFull + st), (g / L::kStages) & 1);  // the key flags
+    wait(bars + 8 * (L::kSFull + b), (g >> 1) & 1);
     tc::fence_after_sync();
     float x[kG][4];
-    tc::ld_16x256<kG>(sub + b * NR, reinterpret_cast<uint32_t*>(&x[0][0]));
-    const uint32_t f0 = lds_u8(smem + L::flags + b * kKeys + key0);
-    const uint32_t f1 = lds_u8(smem + L::flags + b * kKeys + key0 + 8);
+    tc::ld_16x256<kG>(sub + b * L::kN + col0, reinterpret_cast<uint32_t*>(&x[0][0]));
+    if constexpr (L::kF8) {
+      float y[kG][4];
+      tc::ld_16x256<kG>(sub + b * L::kN + NR + col0, reinterpret_cast<uint32_t*>(&y[0][0]));
+#pragma unroll
+      for (int j = 0; j < kG; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[j][i] = fmaf(y[j][i], kQ2, x[j][i]);
+    }
+    const uint32_t f0 = lds_u8(smem + L::flags + st * kKeys + key0);
+    const uint32_t f1 = lds_u8(smem + L::flags + st * kKeys + key0 + 8);
 #pragma unroll
     for (int j = 0; j < kG; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[j][i] *= c;
+      for (int i = 0; i < 4; ++i) x[j][i] *= cs[j][i & 1];
     if ((t.kt + 1) * kKeys > t.least || __any_sync(0xFFFFFFFFu, (f0 | f1) != 0)) {
       const int p = t.kt * kKeys + key0;
 #pragma unroll
       for (int j = 0; j < kG; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t f = i < 2 ? f0 : f1;
-          if (f == kPoison) x[j][i] = NAN;
-          if (p + (i < 2 ? 0 : 8) >= seen[j][i & 1] || f == kAbsent) x[j][i] = -INFINITY;
+        for (int e = 0; e < 2; ++e) {
+          // a row behind the last one (its query is zeros) copies the last one's view
+          const uint32_t row = min((uint32_t)t.qt * NR + col0 + 8 * j + c2 + e,
+                                   (uint32_t)t.ntok * (uint32_t)a.num_heads - 1);
+          const int seen = seen_of(a, walk.q, t.t0 + token_of(a, row));
+          if (f0 == kPoison) x[j][e] = NAN;
+          if (f1 == kPoison) x[j][e + 2] = NAN;
+          if (p >= seen || f0 == kAbsent) x[j][e] = -INFINITY;
+          if (p + 8 >= seen || f1 == kAbsent) x[j][e + 2] = -INFINITY;
         }
     }
     // maximum over the tile's 64 keys: in the warp, then across the four warps
     float tm[kG][2];
-    float* mine = red + (b * 4 + warp) * NR;
+    float* mine = red + (b * L::kSoftWarps + warp) * kC;
 #pragma unroll
     for (int j = 0; j < kG; ++j)
 #pragma unroll
@@ -560,22 +766,22 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Misc& m, u
 #pragma unroll
       for (int j = 0; j < kG; ++j)
         *reinterpret_cast<float2*>(mine + 8 * j + c2) = make_float2(tm[j][0], tm[j][1]);
-    soft_sync();
+    soft_sync(group);
     bool grown = false;
 #pragma unroll
     for (int j = 0; j < kG; ++j) {
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const float2 v = *reinterpret_cast<const float2*>(red + (b * 4 + w) * NR + 8 * j + c2);
+        const float2 v = *reinterpret_cast<const float2*>(red + (b * L::kSoftWarps + group * 4 + w) * kC + 8 * j + c2);
         tm[j][0] = fmaxf(tm[j][0], v.x);
         tm[j][1] = fmaxf(tm[j][1], v.y);
       }
-      grown |= tm[j][0] > mu[j][0] + kGrow || tm[j][1] > mu[j][1] + kGrow;
+      grown |= tm[j][0] > mu[j][0] + L::kGrow || tm[j][1] > mu[j][1] + L::kGrow;
     }
     // P's buffer, and O^T for the rescaling, are free when the outputs of the tile before are done
-    if (g > 0) wait(bars + 8 * kPvDone, (g - 1) & 1);
-    if (__any_sync(0xFFFFFFFFu, grown)) {  // the same in all four warps
-      float* fac = red + ((b ^ 1) * 4 + warp) * NR;
+    if (g > 0) wait(bars + 8 * L::kPvDone, (g - 1) & 1);
+    if (__any_sync(0xFFFFFFFFu, grown)) {  // the same in the group's four warps
+      float* fac = red + ((b ^ 1) * L::kSoftWarps + warp) * kC;
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < kG; ++j) {
@@ -593,13 +799,15 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Misc& m, u
       if (!t.first) {
         tc::fence_after_sync();
 #pragma unroll 1
-        for (int n = 0; n < 4 * NR; n += 16) {
+        for (int n = 0; n < 4 * L::kParts * kC; n += 16) {
+          // 16 of this group's columns: dims n / (kParts kC), part, columns n % kC
+          const int o = L::kO + n / kC * NR + col0 + n % kC;
           uint32_t r[16];
-          tc::ld_32x16(sub + 2 * NR + n, r);
-  #pragma unroll
+          tc::ld_32x16(sub + o, r);
+#pragma unroll
           for (int i = 0; i < 16; ++i)
-            r[i] = __float_as_uint(__uint_as_float(r[i]) * fac[(n & (NR - 1)) + i]);
-          tc::st_32x16(sub + 2 * NR + n, r);
+            r[i] = __float_as_uint(__uint_as_float(r[i]) * fac[n % kC + i]);
+          tc::st_32x16(sub + o, r);
         }
         tc::wait_st();
       }
@@ -616,22 +824,46 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Misc& m, u
         const float p2 = ex2(x[j + jj][2] - m0), p3 = ex2(x[j + jj][3] - m1);
         l[j + jj][0] += p0 + p2;
         l[j + jj][1] += p1 + p3;
-        w[2 * jj] = pack_bf16x2(p0, p1);
-        w[2 * jj + 1] = pack_bf16x2(p2, p3);
+        if constexpr (!L::kF8) {
+          w[2 * jj] = pack_bf16x2(p0, p1);
+          w[2 * jj + 1] = pack_bf16x2(p2, p3);
+        } else {
+          // each weight as two e4m3 parts, p1 in row n and p2 in row NR + n: 2^-8 of the
+          // weight, or 2^-19 (half of p2's smallest step / 512), as a bf16 would round it
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float u = h ? p2 : p0, v = h ? p3 : p1;
+            const uint32_t hi = pack_fp8x2<kE4M3>(u, v);
+            float uh, vh;
+            fp8x2_to_f32x2<kE4M3>(hi, uh, vh);
+            const uint32_t lo = pack_fp8x2<kE4M3>((u - uh) * (1.0f / kP2), (v - vh) * (1.0f / kP2));
+            const int n = (j + jj) * 8 + c2;  // and n + 1
+            const uint32_t in = (lane >> 2) + 8 * h;
+            const uint32_t d0 = smem + L::p + n * 128 + ((w4 ^ (n & 7)) << 4) + in;
+            const uint32_t d1 = smem + L::p + (n + 1) * 128 + ((w4 ^ ((n + 1) & 7)) << 4) + in;
+            sts_u8(d0, hi);
+            sts_u8(d1, hi >> 8);
+            sts_u8(d0 + NR * 128, lo);
+            sts_u8(d1 + NR * 128, lo >> 8);
+          }
+        }
       }
-      const int n = (j + (lane >> 4)) * 8 + (lane & 7);
-      const int unit = 2 * warp + ((lane >> 3) & 1);
-      tc::st_8x8_t(smem + L::p + n * 128 + ((unit ^ (n & 7)) << 4), w[0], w[1], w[2], w[3]);
+      if constexpr (!L::kF8) {
+        const int n = col0 + (j + (lane >> 4)) * 8 + (lane & 7);
+        const int unit = 2 * w4 + ((lane >> 3) & 1);
+        tc::st_8x8_t(smem + L::p + n * 128 + ((unit ^ (n & 7)) << 4), w[0], w[1], w[2], w[3]);
+      }
     }
     tc::fence_smem_async();
     tc::fence_before_sync();
-    mbar_arrive(bars + 8 * kPFull);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + 8 * L::kPFull);
     if (!t.last) continue;
 
     // ---- the end of this CTA's run of the query tile
-    wait(bars + 8 * kPvDone, g & 1);
+    wait(bars + 8 * L::kPvDone, g & 1);
     tc::fence_after_sync();
-    float* part = red + ((b ^ 1) * 4 + warp) * NR;
+    float* part = red + ((b ^ 1) * L::kSoftWarps + warp) * kC;
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < kG; ++j) {
@@ -643,21 +875,23 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Misc& m, u
       }
       if (lane < 4) *reinterpret_cast<float2*>(part + 8 * j + c2) = make_float2(l[j][0], l[j][1]);
     }
-    soft_sync();
+    soft_sync(group);
     const bool whole = kt_begin == 0 && t.kt + 1 == t.nkt;
     const int64_t slot = 2 * (int64_t)blockIdx.x + (kt_begin == 0 ? 1 : 0);
-    const int64_t rows = (int64_t)walk.q.ntok * a.num_heads;
-    const int64_t first = (int64_t)t.qt * NR;
-    const int nv = (int)min((int64_t)NR, rows - first);
-    const int tok0 = walk.q.t0 + (int)(first / a.num_heads);
-    const int head0 = (int)(first % a.num_heads);
+    const uint32_t first = (uint32_t)t.qt * NR;
+    // rows of this group that exist (none or less: all of them are behind the last row)
+    const int nv =
+        min((int)min((uint32_t)NR, (uint32_t)t.ntok * (uint32_t)a.num_heads - first) - col0, kC);
+    // token and head of this group's first row
+    const int dt0 = token_of(a, first + col0), tok0 = t.t0 + dt0;
+    const int head0 = (int)(first + col0) - dt0 * a.num_heads;
     const bool lost = waiter.given_up();
 #pragma unroll
     for (int j = 0; j < kG; ++j) {
       float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const float2 v = *reinterpret_cast<const float2*>(red + ((b ^ 1) * 4 + w) * NR + 8 * j + c2);
+        const float2 v = *reinterpret_cast<const float2*>(red + ((b ^ 1) * L::kSoftWarps + group * 4 + w) * kC + 8 * j + c2);
         sum.x += v.x;
         sum.y += v.y;
       }
@@ -666,12 +900,12 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Misc& m, u
         const float s = e ? sum.y : sum.x;
         const int n = 8 * j + c2 + e;
         if (lane < 4) mine[n] = s == 0.0f ? 0.0f : ks / s;
-        if (warp == 0 && lane < 4 && n < nv && !lost) {
+        if (w4 == 0 && lane < 4 && n < nv && !lost) {
           if (!whole) {
-            ws.ml[slot * NR + n] = make_float2(mu[j][e], s);
+            ws.ml[slot * NR + col0 + n] = make_float2(mu[j][e], s);
           } else if (a.lse) {
-            const int64_t hh = head0 + n;
-            a.lse[(tok0 + hh / a.num_heads) * a.lse_ts + hh % a.num_heads * a.lse_hs] =
+            const int dt = token_of(a, head0 + n);
+            a.lse[(int64_t)(tok0 + dt) * a.lse_ts + (int64_t)(head0 + n - dt * a.num_heads) * a.lse_hs] =
                 s == 0.0f ? -INFINITY : fmaf(mu[j][e], kLn2, logf(s));
           }
         }
@@ -679,27 +913,39 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Misc& m, u
     }
     __syncwarp();
     if (!whole && kt_begin == 0 && warp == 0 && lane == 0 && !lost) {
-      const int64_t u1 = m.begin + m.count - 1 + (t.nkt - 1 - t.kt);  // the query tile's last unit
-      ws.split[blockIdx.x] = Split{t.s, t.qt, (int)(((u1 + 1) * m.ctas - 1) / m.total), 0};
+      // the CTA of the query tile's last unit
+      const int64_t u1 = m.begin + m.count - 1 + (t.nkt - 1 - t.kt);
+      const int64_t long_end = (m.run + 1) * m.extra;
+      const int64_t last = u1 < long_end ? u1 / (m.run + 1) : m.extra + (u1 - long_end) / m.run;
+      ws.split[blockIdx.x] = Split{t.s, t.qt, (int)last, 0};
     }
 #pragma unroll 1
     for (int blk = 0; blk < 4; ++blk) {
 #pragma unroll 1
       for (int n0 = 0; n0 < nv; n0 += 16) {
         uint32_t r[16];
-        tc::ld_32x16(sub + 2 * NR + blk * NR + n0, r);
+        const uint32_t o = sub + L::kO + blk * L::kN + col0 + n0;
+        tc::ld_32x16(o, r);
+        if constexpr (L::kF8) {
+          uint32_t r2[16];
+          tc::ld_32x16(o + NR, r2);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            r[i] = __float_as_uint(fmaf(__uint_as_float(r2[i]), kP2, __uint_as_float(r[i])));
+        }
         if (lost) continue;
         if (whole) {
           // lanes 2 i and 2 i + 1 exchange, so that each holds two neighbouring columns of out
-          int h = head0 + n0 + (lane & 1), tok = tok0 + h / a.num_heads;
-          h %= a.num_heads;
-          const int d = blk * 128 + warp * 32 + (lane & ~1);
+          int h = head0 + n0 + (lane & 1), tok = token_of(a, h);
+          h -= tok * a.num_heads;
+          tok += tok0;
+          const int d = blk * 128 + w4 * 32 + (lane & ~1);
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
             const float v0 = __uint_as_float(r[i]) * mine[n0 + i];
             const float v1 = __uint_as_float(r[i + 1]) * mine[n0 + i + 1];
-            const float o = __shfl_xor_sync(0xFFFFFFFFu, (lane & 1) ? v0 : v1, 1);
-            const uint32_t w = (lane & 1) ? pack_bf16x2(o, v1) : pack_bf16x2(v0, o);
+            const float x = __shfl_xor_sync(0xFFFFFFFFu, (lane & 1) ? v0 : v1, 1);
+            const uint32_t w = (lane & 1) ? pack_bf16x2(x, v1) : pack_bf16x2(v0, x);
             if (n0 + i + (lane & 1) < nv)
               *reinterpret_cast<uint32_t*>(a.out + (int64_t)tok * a.out_ts + (int64_t)h * a.out_hs + d * 2) = w;
             h += 2;
@@ -709,7 +955,7 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Misc& m, u
             }
           }
         } else {
-          float* dst = ws.o + (slot * NR + n0) * kRank + blk * 128 + warp * 32 + lane;
+          float* dst = ws.o + (slot * NR + col0 + n0) * kRank + blk * 128 + w4 * 32 + lane;
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             if (n0 + i < nv) dst[i * kRank] = __uint_as_float(r[i]);
@@ -717,15 +963,16 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Misc& m, u
       }
     }
     tc::fence_before_sync();
-    mbar_arrive(bars + 8 * kOFree);
-    soft_sync();  // red is read: the next tile may write it
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + 8 * L::kOFree);
+    soft_sync(group);  // red is read: the next tile may write it
   }
 }
 
 // ------------------------------------------------------------------ the kernel
 // Splits the call's units over the CTAs and finds this CTA's first unit; the
 // scratch is the (still unused) first key stage.
-template <int NR>
+template <int NR, int kWarps>
 __device__ __forceinline__ void schedule(const LatentAttnArgs& a, uint8_t* scratch, Misc& m,
                                          uint32_t& errbits) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -745,6 +992,7 @@ __device__ __forceinline__ void schedule(const LatentAttnArgs& a, uint8_t* scrat
   }
   __syncthreads();
   // exclusive prefix sums: each thread a run of sequences, then warps, then all
+  constexpr int kThreads = kWarps * 32;
   const int run = (a.num_seqs + kThreads - 1) / kThreads;
   const int s0 = min((int)threadIdx.x * run, a.num_seqs), s1 = min(s0 + run, a.num_seqs);
   int64_t sum = 0;
@@ -762,14 +1010,21 @@ __device__ __forceinline__ void schedule(const LatentAttnArgs& a, uint8_t* scrat
     if (w < warp) before += part[w];
     total += part[w];
   }
-  const int ctas = (int)max((int64_t)1, min((int64_t)gridDim.x, total / kMinUnits));
-  const int64_t begin = total * blockIdx.x / ctas, end = total * (blockIdx.x + 1) / ctas;
-  const bool works = (int)blockIdx.x < ctas && end > begin;
+  // total units over `ctas` runs: the first `extra` of them one longer than `run`
+  const uint32_t ctas = total >= (int64_t)gridDim.x * kMinUnits
+                            ? gridDim.x
+                            : max(1u, (uint32_t)total / (uint32_t)kMinUnits);
+  int64_t each;
+  if ((total >> 32) == 0) each = (uint32_t)total / ctas;
+  else each = total / ctas;
+  const uint32_t extra = (uint32_t)(total - each * ctas);
+  const int64_t begin = each * blockIdx.x + min(blockIdx.x, extra);
+  const bool works = blockIdx.x < ctas && total > 0;
   if (threadIdx.x == 0) {
     m.begin = begin;
-    m.count = works ? end - begin : 0;
-    m.total = total;
-    m.ctas = ctas;
+    m.count = works ? (int)each + (blockIdx.x < extra ? 1 : 0) : 0;
+    m.run = each;
+    m.extra = (int)extra;
   }
   if (works)
     for (int s = s0; s < s1; ++s) {
@@ -808,41 +1063,50 @@ __device__ __forceinline__ void schedule(const LatentAttnArgs& a, uint8_t* scrat
 }
 
 template <int FMT, int NR>
-__global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const LatentAttnArgs a) {
-  using L = Lay<NR>;
+__global__ void __launch_bounds__(Lay<FMT, NR>::kThreads, 1)
+    latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ CUtensorMap map) {
+  using L = Lay<FMT, NR>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t smem = smem_addr(smem_raw);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // broadcast, so that the compiler knows the roles' branches are uniform in a warp
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   Misc& m = *reinterpret_cast<Misc*>(smem_raw + L::misc);
   pdl_trigger();
-  if (warp == kMmaWarp) tc::alloc(smem_addr(&m.tmem), L::kCols);
+  if (warp == L::kMmaWarp) tc::alloc(smem_addr(&m.tmem), L::kTmem);
   if (threadIdx.x == 0) {
     m.abort = 0;
     const uint32_t bars = smem + L::bars;
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bars + 8 * (kFull + i), kProdThreads + kProdWarps);
-      mbar_init(bars + 8 * (kEmpty + i), 1);
-      mbar_init(bars + 8 * (kQFull + i), kProdThreads);
-      mbar_init(bars + 8 * (kQEmpty + i), 1);
-      mbar_init(bars + 8 * (kSFull + i), 1);
+    for (int i = 0; i < L::kStages; ++i) {
+      // each producer warp's key flags, and each thread's row copies
+      mbar_init(bars + 8 * (L::kFull + i), kProdWarps + kProdThreads);
+      mbar_init(bars + 8 * (L::kEmpty + i), 1);
     }
-    mbar_init(bars + 8 * kPFull, kSoftWarps * 32);
-    mbar_init(bars + 8 * kPvDone, 1);
-    mbar_init(bars + 8 * kOFree, kSoftWarps * 32);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bars + 8 * (L::kQFull + i), kProdThreads);
+      // the last scores of its query tile, and for fp8 the softmax warps' look at the scales
+      mbar_init(bars + 8 * (L::kQEmpty + i), 1 + (L::kF8 ? L::kSoftWarps : 0));
+      mbar_init(bars + 8 * (L::kSFull + i), 1);
+    }
+    mbar_init(bars + 8 * L::kPFull, L::kSoftWarps);
+    mbar_init(bars + 8 * L::kPvDone, 1);
+    mbar_init(bars + 8 * L::kOFree, L::kSoftWarps);
     mbar_fence_init();
   }
   pdl_wait();
   const Workspace ws = workspace_of<NR>(a.workspace, gridDim.x);
   if (threadIdx.x == 0) ws.split[blockIdx.x] = Split{-1, 0, 0, 0};
   uint32_t errbits = 0;
-  schedule<NR>(a, smem_raw, m, errbits);
+  schedule<NR, L::kWarps>(a, smem_raw, m, errbits);
   tc::fence_after_sync();
-  const uint32_t tmem = m.tmem;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, m.tmem, 0);
   const Waiter wait{smem_addr(&m.abort), a.wait_limit_ns};
   if (m.count > 0) {
-    if (warp < kSoftWarps) soften<FMT, NR>(a, m, smem, tmem, wait, warp, lane, ws);
-    else if (warp >= kProdWarp) produce<FMT, NR>(a, m, smem, wait, warp - kProdWarp, lane, errbits);
-    else if (lane == 0) issue_mma<NR>(a, m, smem, tmem, wait);
+    if (warp < L::kSoftWarps)
+      soften<FMT, NR>(a, m, smem, tmem, wait, warp, lane, ws);
+    else if (warp >= L::kProdWarp)
+      produce<FMT, NR>(a, &map, m, smem, wait, warp - L::kProdWarp, lane, errbits);
+    else
+      issue_mma<FMT, NR>(a, m, smem, tmem, wait);
   }
   __syncwarp();
   if (a.err) {
@@ -855,7 +1119,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const Lat
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  if (warp == kMmaWarp) tc::dealloc(tmem, L::kCols);
+  if (warp == L::kMmaWarp) tc::dealloc(tmem, L::kTmem);
 }
 
 // ---------------------------------------------------- join of the split query tiles
@@ -878,8 +1142,8 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentA
   const Split sp = ws.split[c];
   if (sp.s < 0) return;
   const Seq q = load_seq<NR>(a, sp.s);
-  const int64_t row = (int64_t)sp.qt * NR + n;
-  if (row >= (int64_t)q.ntok * a.num_heads) return;
+  const uint32_t row = (uint32_t)sp.qt * NR + n;
+  if (row >= (uint32_t)q.ntok * (uint32_t)a.num_heads) return;
   const int parts = sp.last - c + 1;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto slot = [&](int i) { return (2 * (int64_t)(c + i) + (i == 0 ? 1 : 0)) * NR + n; };
@@ -929,7 +1193,7 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentA
   }
   const float ks = FMT == kBF16 ? 1.0f : __ldg(a.k_scale);
   const float inv = sum == 0.0f ? 0.0f : ks / sum;
-  const int64_t t = q.t0 + row / a.num_heads, h = row % a.num_heads;
+  const int64_t t = q.t0 + token_of(a, row), h = (int)row - token_of(a, row) * a.num_heads;
   st8(a.out + t * a.out_ts + h * a.out_hs + d4 * 8,
       make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv)));
   if (tid == 0 && a.lse)
@@ -937,27 +1201,59 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentA
 }
 
 // Rows of a query tile: the average rows (tokens x heads) per sequence decide.
-inline int tile_rows(int32_t num_tokens, int32_t num_heads, int32_t num_seqs) {
+// fp8 tiles stop at 32: their split sums take two columns of tensor memory each.
+inline int tile_rows(int32_t num_tokens, int32_t num_heads, int32_t num_seqs, bool fp8) {
   const int64_t rows = (int64_t)((num_tokens + num_seqs - 1) / num_seqs) * num_heads;
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  return rows <= 16 ? 16 : rows <= 32 || fp8 ? 32 : 64;
+}
+
+// The cache as a tensor of (column, entry, block), read in boxes of one chunk of
+// box_rows entries.  Without a box (entries per block not a multiple of 8, or
+// sizes that a tensor map does not hold) rows are copied one by one.
+int box_map(const LatentAttnArgs& a, bool fp8, CUtensorMap* map) {
+  int rows = kKeys;
+  while (a.block_size % rows) rows >>= 1;
+  if (rows < 8 || a.num_blocks >= INT32_MAX) return 0;
+  static const auto encode = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    (void)cudaGetLastError();
+    return reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(f);
+  }();
+  if (!encode) return 0;
+  const cuuint64_t dims[3] = {576, (cuuint64_t)a.block_size, (cuuint64_t)a.num_blocks};
+  const cuuint64_t strides[2] = {(cuuint64_t)a.entry_stride, (cuuint64_t)a.block_stride};
+  const cuuint32_t box[3] = {fp8 ? 128u : 64u, (cuuint32_t)rows, 1}, unit[3] = {1, 1, 1};
+  const CUresult r = encode(
+      map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+      const_cast<uint8_t*>(a.cache), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? rows : 0;
 }
 
 template <int FMT, int NR>
-cudaError_t launch_t(const LatentAttnArgs& a, int ctas, const LaunchCfg& cfg) {
+cudaError_t launch_t(const LatentAttnArgs& a, const CUtensorMap& map, int ctas,
+                     const LaunchCfg& cfg) {
+  using L = Lay<FMT, NR>;
   auto kern = latent_attention_kernel<FMT, NR>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<NR>::bytes);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::bytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(ctas);
-  lc.blockDim = dim3(kThreads);
-  lc.dynamicSmemBytes = Lay<NR>::bytes;
+  lc.blockDim = dim3(L::kThreads);
+  lc.dynamicSmemBytes = L::bytes;
   lc.stream = cfg.stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = attr;
   lc.numAttrs = cfg.pdl ? 1 : 0;
-  e = cudaLaunchKernelEx(&lc, kern, a);
+  e = cudaLaunchKernelEx(&lc, kern, a, map);
   if (e != cudaSuccess) return e;
   lc.gridDim = dim3(NR, ctas);
   lc.blockDim = dim3(kJoinThreads);
@@ -966,11 +1262,16 @@ cudaError_t launch_t(const LatentAttnArgs& a, int ctas, const LaunchCfg& cfg) {
 }
 
 template <int FMT>
-cudaError_t launch_f(const LatentAttnArgs& a, int ctas, const LaunchCfg& cfg) {
-  switch (tile_rows(a.num_tokens, a.num_heads, a.num_seqs)) {
-    case 16: return launch_t<FMT, 16>(a, ctas, cfg);
-    case 32: return launch_t<FMT, 32>(a, ctas, cfg);
-    default: return launch_t<FMT, 64>(a, ctas, cfg);
+cudaError_t launch_f(LatentAttnArgs a, int ctas, const LaunchCfg& cfg) {
+  constexpr bool kF8 = FMT != kBF16;
+  CUtensorMap map = {};
+  a.box_rows = box_map(a, kF8, &map);
+  switch (tile_rows(a.num_tokens, a.num_heads, a.num_seqs, kF8)) {
+    case 16: return launch_t<FMT, 16>(a, map, ctas, cfg);
+    case 32: return launch_t<FMT, 32>(a, map, ctas, cfg);
+    default:
+      if constexpr (!kF8) return launch_t<FMT, 64>(a, map, ctas, cfg);
+      else return cudaErrorInvalidValue;
   }
 }
 

@@ -146,9 +146,11 @@ struct LatentAttnArgs {
   const uint8_t* q_pe;
   int64_t qp_ts, qp_hs;
   int32_t num_tokens, num_heads;
+  uint32_t heads_mul, heads_shift;  // n / num_heads = (mulhi(n, mul) + n) >> shift, n < 2^31
   const uint8_t* cache;
   int64_t block_stride, entry_stride, num_blocks;
   int32_t block_size, bs_shift;  // bs_shift = log2(block_size) or -1
+  int32_t box_rows;              // entries of a TMA box (set by the launch), 0 = row copies
   const int32_t* block_table;
   int64_t bt_stride;  // elements
   int32_t room;       // rows that a table row can hold (below 2^31 - 127)

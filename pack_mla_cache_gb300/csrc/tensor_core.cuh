@@ -50,27 +50,48 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
          ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-// Instruction descriptor: bf16 A and B, fp32 accumulator, M x N tile;
-// a_mn: A is MN-major.
-__host__ __device__ constexpr uint32_t instr_desc(int m, int n, bool a_mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | ((uint32_t)(n >> 3) << 17) |
-         ((uint32_t)(m >> 4) << 24);
+// Instruction descriptor: fp32 accumulator, M x N tile, A MN-major or K-major, B
+// K-major.  fa / fb: 1 for bf16 (mma_bf16); 0 for e4m3, 1 for e5m2 (mma_fp8).
+__host__ __device__ constexpr uint32_t instr_desc(int m, int n, bool a_mn, int fa, int fb) {
+  return (1u << 4) | ((uint32_t)fa << 7) | ((uint32_t)fb << 10) | (a_mn ? 1u << 15 : 0u) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-// D[tmem] (+)= A * B for one k step of 16; issued by one thread.
-__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                         bool accumulate) {
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect() {
+  uint32_t one;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(one));
+  return one != 0;
+}
+
+// D[tmem] (+)= A * B for one k step of 16.  The whole (converged) warp runs these
+// two statements and `lane` holds in the one lane that issues: without a branch
+// around them, descriptors that are the same in all lanes are computed in uniform
+// registers, where the instruction wants them.
+__device__ __forceinline__ void mma_bf16(bool lane, uint32_t d, uint64_t a, uint64_t b,
+                                         uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
-      "  tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      "{ .reg .pred p, q; setp.ne.u32 p, %4, 0; setp.ne.u32 q, %5, 0;\n"
+      "  @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(lane ? 1u : 0u)
       : "memory");
 }
-// Arrive on `bar` when every matrix instruction this thread has issued is done.
-__device__ __forceinline__ void commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   bar)
-               : "memory");
+// The same for fp8 operands (of either format each): one k step of 32.
+__device__ __forceinline__ void mma_fp8(bool lane, uint32_t d, uint64_t a, uint64_t b,
+                                        uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.u32 p, %4, 0; setp.ne.u32 q, %5, 0;\n"
+      "  @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(lane ? 1u : 0u)
+      : "memory");
+}
+// Arrive on `bar` when every matrix instruction that lane has issued is done.
+__device__ __forceinline__ void commit(bool lane, uint32_t bar) {
+  asm volatile(
+      "{ .reg .pred q; setp.ne.u32 q, %1, 0;\n"
+      "  @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar),
+      "r"(lane ? 1u : 0u)
+      : "memory");
 }
 
 __device__ __forceinline__ void wait_st() {
@@ -144,6 +165,17 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool v
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(valid ? 16u : 0u)
                : "memory");
+}
+// One tile of a 3-dimensional tensor map to shared memory, completing on `bar`
+// (parts outside the tensor are filled with zeros; x * element size a multiple of
+// 16 bytes).
+__device__ __forceinline__ void tma_load3(uint32_t dst, const void* map, int x, int y, int z,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
 }
 // Arrive on `bar` when this thread's cp_async16 so far are done.
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {

@@ -2,9 +2,8 @@
 attention, the merge of attention states and the block copies.
 
 ``attention`` is the definition in numpy float64 (pinned against the C oracle's
-loops by test_oracle_serving.py).  Beside the result it gives what the error
-bounds need: per output element the weighted mean of |row|, and per (token,
-head) the largest sum of |q * row| * |scale|.
+loops by test_oracle_serving.py); ``attention_bounds`` derives how far a result
+may be from it.
 """
 from __future__ import annotations
 
@@ -78,13 +77,26 @@ def rows_of(pg: Paged, s, n):
     return out, found
 
 
-def attention(pg: Paged, q, cu, kv_lens, scale=SCALE, causal=True):
-    """(out, lse, mean |row|, largest |scale| * sum |q row|), float64; tokens of
-    no sequence are NaN in all."""
+@dataclass
+class Result:
+    """The definition's result in float64 and what its error bounds need; tokens of no
+    sequence are NaN in all."""
+    out: np.ndarray    # [T, H, 512]
+    lse: np.ndarray    # [T, H]
+    mag: np.ndarray    # [T, H, 512]: sum of weight * |row| / sum of weights
+    flat: np.ndarray   # [T, H, 512]: sum of |row| / sum of weights (the largest weight is 1)
+    dot: np.ndarray    # [T, H]: largest |scale| * sum |q row|
+    reach: np.ndarray  # [T, H]: largest |scale| * max |q| * sum |row|
+    longest: int
+    fp8: bool
+
+
+def attention(pg: Paged, q, cu, kv_lens, scale=SCALE, causal=True) -> Result:
     T, H, _ = q.shape
     qv = orc.bf16_bits_to_f64(q).reshape(q.shape)
-    out, mag = np.full((T, H, RANK), np.nan), np.full((T, H, RANK), np.nan)
-    lse, dot = np.full((T, H), np.nan), np.full((T, H), np.nan)
+    wide, flat2 = (T, H, RANK), (T, H)
+    r = Result(*(np.full(sh, np.nan) for sh in (wide, flat2, wide, wide, flat2, flat2)),
+               max(1, max(int(k) for k in kv_lens)), pg.fmt != 0)
     for s, kv in enumerate(kv_lens):
         a, b = int(cu[s]), min(int(cu[s + 1]), T)
         n = int(cu[s + 1]) - a
@@ -93,35 +105,53 @@ def attention(pg: Paged, q, cu, kv_lens, scale=SCALE, causal=True):
         rows, found = rows_of(pg, s, max(0, int(kv)))
         for t in range(a, b):
             seen = max(0, int(kv) - n + 1 + t - a if causal else int(kv))
-            r = rows[:seen][found[:seen]]
-            out[t], mag[t], lse[t], dot[t] = 0.0, 0.0, -np.inf, 0.0
-            if len(r) == 0:
+            k = rows[:seen][found[:seen]]
+            for x in (r.out, r.mag, r.flat, r.dot, r.reach):
+                x[t] = 0.0
+            r.lse[t] = -np.inf
+            if len(k) == 0:
                 continue
-            x = scale * (qv[t] @ r.T)
+            x = scale * (qv[t] @ k.T)
             top = x.max(-1, keepdims=True)
             w = np.exp(x - top)
             total = w.sum(-1, keepdims=True)
+            v = np.abs(k[:, :RANK])
             with np.errstate(invalid="ignore"):
-                out[t], mag[t] = (w / total) @ r[:, :RANK], (w / total) @ np.abs(r[:, :RANK])
-            lse[t] = (top + np.log(total))[:, 0]
-            dot[t] = abs(scale) * (np.abs(qv[t]) @ np.abs(r).T).max(-1)
-    return out, lse, mag, dot
+                r.out[t], r.mag[t] = (w / total) @ k[:, :RANK], (w / total) @ v
+            r.flat[t] = v.sum(0) / total
+            r.lse[t] = (top + np.log(total))[:, 0]
+            r.dot[t] = abs(scale) * (np.abs(qv[t]) @ np.abs(k).T).max(-1)
+            r.reach[t] = abs(scale) * np.abs(qv[t]).max(-1) * np.abs(k).sum(-1).max()
+    return r
 
 
-def attention_bounds(out, lse, mag, dot, longest):
+def attention_bounds(r: Result):
     """How far out and lse may be from the float64 result.
 
     A score is a sum of 576 exact products in fp32: off by at most d = 576 * 2^-23
     * sum |q row| * scale (each addition at most one fp32 step, as a matrix unit
-    that truncates adds).  A weight exp(x - max) is then off by a factor e^(2d)
-    (its score and the maximum), rounded once to bf16 (2^-8), and the sums over
-    `longest` rows add longest * 2^-23 relative to the sum of magnitudes; the sum
-    of the weights is off by the same factors without the bf16 rounding.  The
-    result is rounded once to bf16 (2^-8 of its value).  Exponentials and the
-    final scaling are fp32 operations with errors of a few 2^-22.
+    that truncates adds).  With an fp8 cache the query is two e4m3 parts of itself
+    times a power of two that puts its largest value into [2^7, 2^8): exact, or off
+    by half the second part's smallest step, 2^-10 / 16 = 2^-14, that is by 2^-21 of
+    the largest value at most, so d grows by 2^-21 * scale * max |q| * sum |row|.
+    A weight exp(x - max) is then off by a factor e^(2d) (its score and the
+    maximum) and rounded to 8 bits: by 2^-8 of itself; as two e4m3 parts with an fp8
+    cache by 2^-8 (2^-4 each) or, below the second part's smallest step / 512, by
+    2^-19 of the unit that weights are relative to, which is at most the largest
+    weight (the reference maximum is never above the true one).  The sums over
+    `longest` rows add longest * 2^-23 relative to the sum of magnitudes; the sum of
+    the weights is off by the same factors without the rounding to 8 bits.  The
+    result is rounded once to bf16 (2^-8 of its value).  Exponentials and the final
+    scaling are fp32 operations with errors of a few 2^-22.
     lse is off by d, the relative error of the sum, and fp32 roundings of itself."""
-    d = 576 * 2.0 ** -23 * dot
-    rel = (BF16_HALF + 4 * d + 2 * longest * 2.0 ** -23 + 2.0 ** -18)[..., None]
-    o = rel * mag + BF16_HALF * (np.abs(out) + rel * mag) + 1e-30
-    le = d + longest * 2.0 ** -23 + 2.0 ** -18 + 4 * FP32_HALF * np.abs(np.where(np.isfinite(lse), lse, 0))
+    d = 576 * 2.0 ** -23 * r.dot
+    part = 0.0
+    if r.fp8:
+        d = d + 2.0 ** -21 * r.reach
+        part = 2.0 ** -19 * r.flat
+    rel = (BF16_HALF + 4 * d + 2 * r.longest * 2.0 ** -23 + 2.0 ** -18)[..., None]
+    err = rel * r.mag + part
+    o = err + BF16_HALF * (np.abs(r.out) + err) + 1e-30
+    le = d + r.longest * 2.0 ** -23 + 2.0 ** -18 + \
+        4 * FP32_HALF * np.abs(np.where(np.isfinite(r.lse), r.lse, 0))
     return o, le

@@ -79,12 +79,13 @@ class Call:
 
 def check(call, q, err=0):
     out, lse, e = call.got()
-    ro, rl, mag, dot = R.attention(call.pg, q, call.cu, call.kv, call.scale, call.causal)
+    r = R.attention(call.pg, q, call.cu, call.kv, call.scale, call.causal)
+    ro, rl = r.out, r.lse
     own = ~np.isnan(rl)
     assert (out[~own] == 7).all() and (lse[~own] == 7).all()  # unowned tokens are untouched
     none = np.isneginf(rl)
     assert (out[none] == 0).all() and np.isneginf(lse[none]).all()
-    bo, bl = R.attention_bounds(ro, rl, mag, dot, max(1, max(call.kv)))
+    bo, bl = R.attention_bounds(r)
     live = own & ~none
     assert np.isfinite(out[live]).all() and np.isfinite(lse[live]).all()
     worst = (np.abs(out[live] - ro[live]) / bo[live]).max() if live.any() else 0

@@ -259,8 +259,9 @@ def test_insert_fork_attend_merge(fmt):
                      None if fmt == 0 else float(scales[layer]))
         qh = D.host_u16(q)
         kv = [prompt + new] * samples
-        ro, rl, mag, dot = R.attention(pg, qh, [0, 2, 4, 6], kv)
-        bo, bl = R.attention_bounds(ro, rl, mag, dot, prompt + new)
+        r = R.attention(pg, qh, [0, 2, 4, 6], kv)
+        ro, rl, mag = r.out, r.lse, r.mag
+        bo, bl = R.attention_bounds(r)
         f = lambda t: t.double().cpu().numpy()
         assert (np.abs(f(whole) - ro) <= bo).all() and (np.abs(f(lse_w) - rl) <= bl).all()
         # a part is within the same bounds of its own result, whose magnitudes are at most the rows';

@@ -21,7 +21,8 @@ def test_attention_matches_the_numpy_definition(orc, fmt, causal):
     pg = R.paged(kv, fmt, 16, pad_entry=16, pad_block=32)
     q = R.queries(12, 3)
     out, lse, err = run(orc, pg, q, cu, kv, causal)
-    ro, rl, _, _ = R.attention(pg, q, cu, kv, causal=causal)
+    r = R.attention(pg, q, cu, kv, causal=causal)
+    ro, rl = r.out, r.lse
     assert err == 0
     np.testing.assert_allclose(out[:11], ro[:11], rtol=1e-11, atol=1e-12)
     np.testing.assert_allclose(lse[:11], rl[:11], rtol=1e-12)
@@ -49,7 +50,8 @@ def test_attention_leaves_out_rows_without_a_block(orc):
     pg.table[0, 1] = pg.num_blocks
     q = R.queries(1, 2)
     out, lse, err = run(orc, pg, q, [0, 1], [40])
-    ro, rl, _, _ = R.attention(pg, q, [0, 1], [40])
+    r = R.attention(pg, q, [0, 1], [40])
+    ro, rl = r.out, r.lse
     assert err == 2
     np.testing.assert_allclose(out, ro, rtol=1e-11, atol=1e-12)
     np.testing.assert_allclose(lse, rl, rtol=1e-12)
