@@ -117,15 +117,13 @@ struct Lay {
 struct Misc {
   uint32_t tmem;
   uint32_t abort;
-  int32_t s, qt, kt, count;
-  int64_t begin, run;  // the first unit; units of the CTAs c >= extra (run + 1 of the ones before)
-  int32_t extra;
 };
 static_assert(sizeof(Misc) <= 64, "Misc fits");
 
-// A split query tile that CTA c starts: the partials of CTAs c .. last belong to it.
+// A query tile that CTA c starts and others go on with: rows first_row .. of the
+// sequence, the partials of the CTAs c .. c + parts - 1 (rows 0: none).
 struct Split {
-  int32_t s, qt, last, pad;
+  int32_t tok0, head0, rows, parts;
 };
 
 struct Seq {
@@ -161,6 +159,10 @@ __device__ __forceinline__ int most_seen(const LatentAttnArgs& a, const Seq& q, 
   const uint32_t last = min((uint32_t)(qt + 1) * NR, (uint32_t)q.ntok * (uint32_t)a.num_heads) - 1;
   return seen_of(a, q, q.t0 + token_of(a, last));
 }
+// Whether a token sees rows beyond the block table's.
+__device__ __forceinline__ bool over_room(const LatentAttnArgs& a, const Seq& q) {
+  return (int64_t)q.kv + (a.causal ? (int64_t)q.t0 + q.ntok - q.c1 : 0) > a.room;
+}
 // Key tiles of a query tile that sees `most` rows (one even when it sees none: its
 // rows are still written).
 __device__ __forceinline__ int key_tiles(int most) { return max(1, (most + kKeys - 1) / kKeys); }
@@ -172,7 +174,15 @@ struct Tile {
   int t0, ntok;             // the sequence's tokens
 };
 
-// Walks a CTA's run of units; every role has its own copy.
+// A CTA's run of units: where it starts, and what finds the CTA of another unit.
+struct Run {
+  Seq q;               // of sequence s
+  int s, qt, kt, count;
+  int64_t begin, each; // the first unit; units of the CTAs c >= extra (each + 1 of the ones before)
+  int extra;
+};
+
+// Walks the run; every role has its own copy.
 template <int NR>
 struct Walk {
   Seq q;
@@ -185,13 +195,13 @@ struct Walk {
     nkt = key_tiles(most);
     fresh = true;
   }
-  __device__ __forceinline__ void start(const Misc& m) {
-    s = m.s;
-    qt = m.qt;
-    kt = m.kt;
-    left = m.count;
+  __device__ __forceinline__ void start(const Run& r) {
+    q = r.q;
+    s = r.s;
+    qt = r.qt;
+    kt = r.kt;
+    left = r.count;
     nkt = 0;
-    q.nqt = 0;
   }
   // The next unit.  Each role calls this at one place only: 13 warps of different
   // code share the instruction caches.
@@ -207,8 +217,6 @@ struct Walk {
           do q = load_seq<NR>(a, ++s);
           while (q.nqt == 0 && s + 1 < a.num_seqs);
         }
-      } else {
-        q = load_seq<NR>(a, s);
       }
       item(a);
     }
@@ -255,11 +263,11 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
                "r"(v.z), "r"(v.w)
                : "memory");
 }
+__device__ __forceinline__ void sts8(uint32_t addr, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
+}
 __device__ __forceinline__ void sts_u8(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-__device__ __forceinline__ void sts_u16(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"((uint16_t)v) : "memory");
 }
 __device__ __forceinline__ void sts_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
@@ -272,6 +280,17 @@ __device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
 // A barrier of the four warps of one softmax group.
 __device__ __forceinline__ void soft_sync(int group) {
   asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
+}
+// The same barrier, and whether x holds in any of its threads.
+__device__ __forceinline__ bool soft_any(int group, bool x) {
+  uint32_t any;
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.u32 q, %2, 0;\n"
+      "  barrier.cta.red.or.pred p, %1, 128, q; selp.u32 %0, 1, 0, p; }"
+      : "=r"(any)
+      : "r"(1 + group), "r"(x ? 1u : 0u)
+      : "memory");
+  return any != 0;
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -339,66 +358,76 @@ __device__ __forceinline__ void load_q(const LatentAttnArgs& a, const Tile& q, u
 // The same as two e4m3 parts of the row times a power of two: with the largest
 // magnitude in [2^7, 2^8), q1 = e4m3(q) rounds by at most 8 and q2 = e4m3(16 (q -
 // q1)).  q1 + q2 / 16 has every bit of a bf16 down to 2^-14 of the largest, and
-// is off by at most 2^-22 of it below.  A row with a NaN or an infinity gets NaN
-// as its inverse scale.  A warp takes a row; lane l has columns 16 l .. 16 l + 15
-// and 512 + 2 l, 513 + 2 l.
+// is off by at most 2^-21 of it below.  A row with a NaN or an infinity gets NaN
+// as its inverse scale.  8 lanes take a row, 16 bytes of every chunk each, so a
+// tile of 16 rows costs the four warps one round of loads.
 template <int NR>
 __device__ __forceinline__ void split_q(const LatentAttnArgs& a, const Tile& q, uint32_t dst,
                                         uint32_t scales, uint32_t bar, int pw, int lane) {
   const uint32_t rows = (uint32_t)q.ntok * (uint32_t)a.num_heads;
+  const int col = lane & 7;
 #pragma unroll 1
-  for (int r = pw; r < NR; r += kProdWarps) {
+  for (int r = pw * 4 + (lane >> 3); r < NR; r += kProdWarps * 4) {
     const uint32_t row = (uint32_t)q.qt * NR + r;
-    uint32_t w[9] = {};
+    uint4 v[9] = {};
     if (row < rows) {
       const int tok = token_of(a, row);
       const int64_t t = q.t0 + tok, h = (int)row - tok * a.num_heads;
-      const uint8_t* c = a.q_c + t * a.qc_ts + h * a.qc_hs + lane * 32;
-      const uint4 v0 = ld_stream16(c), v1 = ld_stream16(c + 16);
-      w[8] = *reinterpret_cast<const uint32_t*>(a.q_pe + t * a.qp_ts + h * a.qp_hs + lane * 4);
-      w[0] = v0.x; w[1] = v0.y; w[2] = v0.z; w[3] = v0.w;
-      w[4] = v1.x; w[5] = v1.y; w[6] = v1.z; w[7] = v1.w;
+      const uint8_t* c = a.q_c + t * a.qc_ts + h * a.qc_hs + col * 16;
+#pragma unroll
+      for (int ch = 0; ch < 8; ++ch) v[ch] = ld_stream16(c + ch * 128);
+      v[8] = ld_stream16(a.q_pe + t * a.qp_ts + h * a.qp_hs + col * 16);
     }
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < 9; ++i) top = umax16x2(top, w[i] & 0x7FFF7FFFu);
-    top = __reduce_max_sync(0xFFFFFFFFu, max(top & 0xFFFFu, top >> 16));
+    for (int ch = 0; ch < 9; ++ch)
+      top = umax16x2(top, umax16x2(umax16x2(v[ch].x & 0x7FFF7FFFu, v[ch].y & 0x7FFF7FFFu),
+                                   umax16x2(v[ch].z & 0x7FFF7FFFu, v[ch].w & 0x7FFF7FFFu)));
+    top = max(top & 0xFFFFu, top >> 16);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
     const uint32_t e = max(top >> 7, 8u);  // exponent field of the largest magnitude
     const float s = __uint_as_float((261u - e) << 23);  // 2^(134 - e)
-    uint32_t p1[9], p2[9];  // two codes in the low half of each
+    // columns 64 ch + 8 col ..: 8 bytes at byte 64 (ch % 2) + 8 col of chunk ch / 2
+    const uint32_t d = dst + r * 128 + 8 * (col & 1);
 #pragma unroll
-    for (int i = 0; i < 9; ++i) {
-      const float x0 = bf16lo(w[i]) * s, x1 = bf16hi(w[i]) * s;
-      p1[i] = pack_fp8x2<kE4M3>(x0, x1);
-      float y0, y1;
-      fp8x2_to_f32x2<kE4M3>(p1[i], y0, y1);
-      p2[i] = pack_fp8x2<kE4M3>((x0 - y0) * 16.0f, (x1 - y1) * 16.0f);
+    for (int ch = 0; ch < 9; ++ch) {
+      const uint32_t w[4] = {v[ch].x, v[ch].y, v[ch].z, v[ch].w};
+      uint32_t p1[4], p2[4];  // two codes each
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float x0 = bf16lo(w[i]) * s, x1 = bf16hi(w[i]) * s;
+        p1[i] = pack_fp8x2<kE4M3>(x0, x1);
+        float y0, y1;
+        fp8x2_to_f32x2<kE4M3>(p1[i], y0, y1);
+        p2[i] = pack_fp8x2<kE4M3>((x0 - y0) * 16.0f, (x1 - y1) * 16.0f);
+      }
+      const int unit = (ch & 1) * 4 + (col >> 1);
+      const uint32_t at = d + (ch >> 1) * (2 * NR * 128) + ((unit ^ (r & 7)) << 4);
+      sts8(at, p1[0] | p1[1] << 16, p1[2] | p1[3] << 16);
+      sts8(at + NR * 128, p2[0] | p2[1] << 16, p2[2] | p2[3] << 16);
     }
-    const int ch = lane >> 3;
-    const uint32_t in = (uint32_t)(((lane & 7) ^ (r & 7)) << 4);  // NR is a multiple of 8
-    const uint32_t d = dst + ch * (2 * NR * 128) + r * 128 + in;
-    sts16(d, make_uint4(p1[0] | p1[1] << 16, p1[2] | p1[3] << 16, p1[4] | p1[5] << 16,
-                        p1[6] | p1[7] << 16));
-    sts16(d + NR * 128, make_uint4(p2[0] | p2[1] << 16, p2[2] | p2[3] << 16, p2[4] | p2[5] << 16,
-                                   p2[6] | p2[7] << 16));
-    const uint32_t dr = dst + 4 * (2 * NR * 128) + r * 128 + ((ch ^ (r & 7)) << 4) + 2 * (lane & 7);
-    sts_u16(dr, p1[8]);
-    sts_u16(dr + NR * 128, p2[8]);
-    if (lane == 0)
+    if (col == 0)
       sts_u32(scales + 4 * r, top >= 0x7F80u ? 0x7FC00000u : (e - 7u) << 23);  // 2^(e - 134)
   }
   __syncwarp();
   if (lane == 0) mbar_arrive_n(bar, 32);
 }
 
+// The cache as a tensor of (column, entry, chunk, block): boxes of one chunk of
+// box_rows entries, and of all chunks (fp8: the first four) of a whole tile.
+struct Maps {
+  CUtensorMap chunk, tile;
+};
+
 template <int FMT, int NR>
-__device__ __forceinline__ void produce(const LatentAttnArgs& a, const CUtensorMap* map,
-                                        const Misc& m, uint32_t smem, const Waiter& wait, int pw,
+__device__ __forceinline__ void produce(const LatentAttnArgs& a, const Maps& maps,
+                                        const Run& run, uint32_t smem, const Waiter& wait, int pw,
                                         int lane, uint32_t& errbits) {
   using L = Lay<FMT, NR>;
   const uint32_t bars = smem + L::bars;
   Walk<NR> walk;
-  walk.start(m);
+  walk.start(run);
   // Row copies: 8 lanes x 16 bytes per row and chunk; this thread has the rows
   // pw * 16 + 4 i + lane / 8.  Boxes: box_rows keys x one chunk; the first warp's
   // lane l has the boxes of keys (l % boxes) * box_rows.
@@ -423,15 +452,6 @@ __device__ __forceinline__ void produce(const LatentAttnArgs& a, const CUtensorM
       for (int i = 0; i < kRows; ++i) fblk[i] = find_block(a, far, far.kt * kKeys + row0 + 4 * i);
     }
     if (cur.valid) {
-      if (cur.first) {
-        const int b = item % L::kQBufs;
-        const uint32_t n = item / L::kQBufs;
-        if (n > 0) wait(bars + 8 * (L::kQEmpty + b), (n - 1) & 1);
-        const uint32_t dst = smem + L::q + b * L::kQ, bar = bars + 8 * (L::kQFull + b);
-        if constexpr (L::kF8) split_q<NR>(a, cur, dst, smem + L::qs + b * NR * 4, bar, pw, lane);
-        else load_q<NR>(a, cur, dst, bar, pw, lane);
-        ++item;
-      }
       const uint32_t g = step;
       const int st = g % L::kStages;
       const uint32_t full = bars + 8 * (L::kFull + st), flags = smem + L::flags + st * kKeys;
@@ -454,9 +474,17 @@ __device__ __forceinline__ void produce(const LatentAttnArgs& a, const CUtensorM
           const int p = cur.kt * kKeys + box * a.box_rows;
           const int off = a.bs_shift >= 0 ? p & (a.block_size - 1) : p % a.block_size;
           const int z = ok ? blk[0] : (int)a.num_blocks;  // outside the tensor: zeros
-          for (int i = lane / boxes; i < L::kChunks; i += 32 / boxes)
-            tc::tma_load3(base + i * kChunk + box * a.box_rows * 128, map,
-                          L::kF8 ? (i < 4 ? i * 128 : 448) : i * 64, off, z, full);
+          const uint32_t to = base + box * a.box_rows * 128;
+          if (boxes == 1) {
+            // one box of all chunks (fp8: of four; the last one starts in the middle)
+            if (lane == 0) tc::tma_load4(base, &maps.tile, 0, off, 0, z, full);
+            if (L::kF8 && lane == 1) tc::tma_load4(base + 4 * kChunk, &maps.chunk, 448, off, 0, z, full);
+          } else {
+            for (int i = lane / boxes; i < L::kChunks; i += 32 / boxes) {
+              if (L::kF8 && i == 4) tc::tma_load4(to + i * kChunk, &maps.chunk, 448, off, 0, z, full);
+              else tc::tma_load4(to + i * kChunk, &maps.chunk, 0, off, i, z, full);
+            }
+          }
         } else if (lane == 0) {
           mbar_arrive_n(full, 33);
         }
@@ -503,6 +531,15 @@ __device__ __forceinline__ void produce(const LatentAttnArgs& a, const CUtensorM
           tc::cp_async_arrive(full);
         }
       }
+      if (cur.first) {
+        const int b = item % L::kQBufs;
+        const uint32_t n = item / L::kQBufs;
+        if (n > 0) wait(bars + 8 * (L::kQEmpty + b), (n - 1) & 1);
+        const uint32_t dst = smem + L::q + b * L::kQ, bar = bars + 8 * (L::kQFull + b);
+        if constexpr (L::kF8) split_q<NR>(a, cur, dst, smem + L::qs + b * NR * 4, bar, pw, lane);
+        else load_q<NR>(a, cur, dst, bar, pw, lane);
+        ++item;
+      }
     }
     cur = nxt;
     nxt = far;
@@ -529,17 +566,21 @@ __device__ __forceinline__ void issue_scores(uint32_t smem, uint32_t tmem, bool 
   const uint64_t ka = tc::smem_desc(smem + ST * L::kTile, 0, 1024);
   const uint64_t qa = tc::smem_desc(smem + L::q + QB * L::kQ, 0, 1024);
   const uint32_t d = tmem + (ST & 1) * L::kN;
+  // a k step is 32 bytes of a row
+#pragma unroll 1
+  for (int c = 0; c < (L::kF8 ? 4 : 9); ++c)
 #pragma unroll
-  for (int c = 0; c < L::kChunks; ++c)
-#pragma unroll
-    for (int k = 0; k < (L::kF8 && c == 4 ? 2 : 4); ++k) {
-      // a k step is 32 bytes of a row; the fp8 rotary columns are the upper half of
-      // their chunk, the lower half of the query's
-      const uint64_t ak = ka + (c * kChunk >> 4) + 2 * k + (L::kF8 && c == 4 ? 4 : 0);
-      const uint64_t bk = qa + (c * L::kN * 128 >> 4) + 2 * k;
+    for (int k = 0; k < 4; ++k) {
+      const uint64_t ak = ka + (c * kChunk >> 4) + 2 * k, bk = qa + (c * L::kN * 128 >> 4) + 2 * k;
       if constexpr (L::kF8) tc::mma_fp8(one, d, ak, bk, kId, c + k > 0);
       else tc::mma_bf16(one, d, ak, bk, kId, c + k > 0);
     }
+  // the fp8 rotary columns are the upper half of their chunk, the lower half of the query's
+  if constexpr (L::kF8)
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      tc::mma_fp8(one, d, ka + (4 * kChunk >> 4) + 2 * k + 4, qa + (4 * L::kN * 128 >> 4) + 2 * k, kId,
+                  true);
   tc::commit(one, smem + L::bars + 8 * (L::kSFull + (ST & 1)));
   if (last) tc::commit(one, smem + L::bars + 8 * (L::kQEmpty + QB));
 }
@@ -552,7 +593,7 @@ __device__ __forceinline__ void issue_outputs(uint32_t smem, uint32_t tmem, bool
   const uint64_t va = tc::smem_desc(smem + ST * L::kTile, L::kF8 ? 0 : kChunk, 1024);
   const uint64_t pa = tc::smem_desc(smem + L::p, 0, 1024);
   constexpr int kDims = L::kF8 ? kChunk : 2 * kChunk, kStep = L::kF8 ? 4096 : 2048;
-#pragma unroll
+#pragma unroll 1
   for (int b = 0; b < 4; ++b)
 #pragma unroll
     for (int k = 0; k < (L::kF8 ? 2 : 4); ++k) {
@@ -566,12 +607,12 @@ __device__ __forceinline__ void issue_outputs(uint32_t smem, uint32_t tmem, bool
 }
 
 template <int FMT, int NR>
-__device__ __forceinline__ void issue_mma(const LatentAttnArgs& a, const Misc& m, uint32_t smem,
+__device__ __forceinline__ void issue_mma(const LatentAttnArgs& a, const Run& run, uint32_t smem,
                                           uint32_t tmem, const Waiter& wait) {
   using L = Lay<FMT, NR>;
   const uint32_t bars = smem + L::bars;
   Walk<NR> walk;
-  walk.start(m);
+  walk.start(run);
   const bool one = tc::elect();
   uint32_t items = 0;       // query tiles whose scores have begun
   uint32_t done_items = 0;  // query tiles whose outputs have begun
@@ -649,23 +690,26 @@ __device__ __forceinline__ void issue_mma(const LatentAttnArgs& a, const Misc& m
 
 // ----------------------------------------------------------- softmax and output
 struct Workspace {
-  Split* split;  // [ctas]
-  float2* ml;    // [2 ctas][NR]: running maximum (log2 units) and sum
-  float* o;      // [2 ctas][NR][512]: unnormalised sums
+  Split* split;   // [ctas]
+  float *m, *l;   // [2 ctas][NR]: running maximum (log2 units) and sum
+  float* o;       // [2 ctas][NR][512]: unnormalised sums
 };
 template <int NR>
 __host__ __device__ inline Workspace workspace_of(uint8_t* p, int ctas) {
   Workspace w;
   w.split = reinterpret_cast<Split*>(p);
-  p += (int64_t)ctas * sizeof(Split);
-  w.ml = reinterpret_cast<float2*>(p);
-  p += (int64_t)ctas * 2 * NR * sizeof(float2);
-  w.o = reinterpret_cast<float*>(p);
+  w.m = reinterpret_cast<float*>(p + (int64_t)ctas * sizeof(Split));
+  w.l = w.m + (int64_t)ctas * 2 * NR;
+  w.o = w.l + (int64_t)ctas * 2 * NR;
   return w;
+}
+// n / d where both mostly fit 32 bits.
+__device__ __forceinline__ int quotient(int64_t n, int64_t d) {
+  return ((n | d) >> 32) == 0 ? (int)((uint32_t)n / (uint32_t)d) : (int)(n / d);
 }
 
 template <int FMT, int NR>
-__device__ __forceinline__ void soften(const LatentAttnArgs& a, const Misc& m, uint32_t smem,
+__device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, uint32_t smem,
                                        uint32_t tmem, const Waiter& waiter, int warp, int lane,
                                        const Workspace& ws) {
   using L = Lay<FMT, NR>;
@@ -686,7 +730,7 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Misc& m, u
   float mu[kG][2], l[kG][2];
   float cs[kG][2];  // score of a product: softmax and cache scale, log2 e, the query row's scale
   Walk<NR> walk;
-  walk.start(m);
+  walk.start(run);
   int kt_begin = 0;
   uint32_t g = 0, item = 0;
 #pragma unroll 1
@@ -750,41 +794,44 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Misc& m, u
           if (p + 8 >= seen || f1 == kAbsent) x[j][e + 2] = -INFINITY;
         }
     }
-    // maximum over the tile's 64 keys: in the warp, then across the four warps
-    float tm[kG][2];
-    float* mine = red + (b * L::kSoftWarps + warp) * kC;
+    // Only whether a score passes its row's reference by more than 2^kGrow is asked of
+    // every tile (one barrier that also ORs); the new maxima are found when one does.
+    bool grown = false;
 #pragma unroll
     for (int j = 0; j < kG; ++j)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float v = fmaxf(x[j][e], x[j][e + 2]);
-        v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
-        v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
-        tm[j][e] = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
-      }
-    if (lane < 4)
-#pragma unroll
-      for (int j = 0; j < kG; ++j)
-        *reinterpret_cast<float2*>(mine + 8 * j + c2) = make_float2(tm[j][0], tm[j][1]);
-    soft_sync(group);
-    bool grown = false;
-#pragma unroll
-    for (int j = 0; j < kG; ++j) {
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float2 v = *reinterpret_cast<const float2*>(red + (b * L::kSoftWarps + group * 4 + w) * kC + 8 * j + c2);
-        tm[j][0] = fmaxf(tm[j][0], v.x);
-        tm[j][1] = fmaxf(tm[j][1], v.y);
-      }
-      grown |= tm[j][0] > mu[j][0] + L::kGrow || tm[j][1] > mu[j][1] + L::kGrow;
-    }
+      for (int e = 0; e < 2; ++e)
+        grown |= fmaxf(x[j][e], x[j][e + 2]) > mu[j][e] + L::kGrow;
+    grown = soft_any(group, grown);
     // P's buffer, and O^T for the rescaling, are free when the outputs of the tile before are done
     if (g > 0) wait(bars + 8 * L::kPvDone, (g - 1) & 1);
-    if (__any_sync(0xFFFFFFFFu, grown)) {  // the same in the group's four warps
-      float* fac = red + ((b ^ 1) * L::kSoftWarps + warp) * kC;
-      __syncwarp();
+    if (grown) {
+      // maximum over the tile's 64 keys: in the warp, then across the four warps
+      float* mine = red + warp * kC;
+      float* fac = red + (L::kSoftWarps + warp) * kC;
+      float tm[kG][2];
+#pragma unroll
+      for (int j = 0; j < kG; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float v = fmaxf(x[j][e], x[j][e + 2]);
+          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
+          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
+          tm[j][e] = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
+        }
+      if (lane < 4)
+#pragma unroll
+        for (int j = 0; j < kG; ++j)
+          *reinterpret_cast<float2*>(mine + 8 * j + c2) = make_float2(tm[j][0], tm[j][1]);
+      soft_sync(group);
 #pragma unroll
       for (int j = 0; j < kG; ++j) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float2 v = *reinterpret_cast<const float2*>(red + (group * 4 + w) * kC + 8 * j + c2);
+          tm[j][0] = fmaxf(tm[j][0], v.x);
+          tm[j][1] = fmaxf(tm[j][1], v.y);
+        }
         float f[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -795,7 +842,7 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Misc& m, u
         }
         if (lane < 4) *reinterpret_cast<float2*>(fac + 8 * j + c2) = make_float2(f[0], f[1]);
       }
-      __syncwarp();
+      soft_sync(group);  // the maxima are read, the factors written
       if (!t.first) {
         tc::fence_after_sync();
 #pragma unroll 1
@@ -863,7 +910,10 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Misc& m, u
     // ---- the end of this CTA's run of the query tile
     wait(bars + 8 * L::kPvDone, g & 1);
     tc::fence_after_sync();
-    float* part = red + ((b ^ 1) * L::kSoftWarps + warp) * kC;
+    // the sums of the weights over lanes (and warps, below); row n's sum and maximum
+    // then go to lane n
+    float* part = red + warp * kC;
+    float* mine = red + (L::kSoftWarps + warp) * kC;
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < kG; ++j) {
@@ -876,53 +926,52 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Misc& m, u
       if (lane < 4) *reinterpret_cast<float2*>(part + 8 * j + c2) = make_float2(l[j][0], l[j][1]);
     }
     soft_sync(group);
+    if (lane < 4)
+#pragma unroll
+      for (int j = 0; j < kG; ++j)
+        *reinterpret_cast<float2*>(mine + 8 * j + c2) = make_float2(mu[j][0], mu[j][1]);
+    __syncwarp();
     const bool whole = kt_begin == 0 && t.kt + 1 == t.nkt;
     const int64_t slot = 2 * (int64_t)blockIdx.x + (kt_begin == 0 ? 1 : 0);
     const uint32_t first = (uint32_t)t.qt * NR;
-    // rows of this group that exist (none or less: all of them are behind the last row)
-    const int nv =
-        min((int)min((uint32_t)NR, (uint32_t)t.ntok * (uint32_t)a.num_heads - first) - col0, kC);
+    // rows of the tile that exist, and of them this group's (none or less: not one)
+    const int rows = (int)min((uint32_t)NR, (uint32_t)t.ntok * (uint32_t)a.num_heads - first);
+    const int nv = min(rows - col0, kC);
     // token and head of this group's first row
     const int dt0 = token_of(a, first + col0), tok0 = t.t0 + dt0;
     const int head0 = (int)(first + col0) - dt0 * a.num_heads;
     const bool lost = waiter.given_up();
+    if (lane < kC) {
+      float sum = 0.0f;
 #pragma unroll
-    for (int j = 0; j < kG; ++j) {
-      float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float2 v = *reinterpret_cast<const float2*>(red + ((b ^ 1) * L::kSoftWarps + group * 4 + w) * kC + 8 * j + c2);
-        sum.x += v.x;
-        sum.y += v.y;
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float s = e ? sum.y : sum.x;
-        const int n = 8 * j + c2 + e;
-        if (lane < 4) mine[n] = s == 0.0f ? 0.0f : ks / s;
-        if (w4 == 0 && lane < 4 && n < nv && !lost) {
-          if (!whole) {
-            ws.ml[slot * NR + col0 + n] = make_float2(mu[j][e], s);
-          } else if (a.lse) {
-            const int dt = token_of(a, head0 + n);
-            a.lse[(int64_t)(tok0 + dt) * a.lse_ts + (int64_t)(head0 + n - dt * a.num_heads) * a.lse_hs] =
-                s == 0.0f ? -INFINITY : fmaf(mu[j][e], kLn2, logf(s));
-          }
+      for (int w = 0; w < 4; ++w)
+        sum += red[(group * 4 + w) * kC + lane];
+      const float top = mine[lane];
+      mine[lane] = sum == 0.0f ? 0.0f : ks / sum;
+      if (w4 == 0 && lane < nv && !lost) {
+        if (!whole) {
+          ws.m[slot * NR + col0 + lane] = top;
+          ws.l[slot * NR + col0 + lane] = sum;
+        } else if (a.lse) {
+          const int dt = token_of(a, head0 + lane);
+          a.lse[(int64_t)(tok0 + dt) * a.lse_ts + (int64_t)(head0 + lane - dt * a.num_heads) * a.lse_hs] =
+              sum == 0.0f ? -INFINITY : fmaf(top, kLn2, logf(sum));
         }
       }
     }
     __syncwarp();
     if (!whole && kt_begin == 0 && warp == 0 && lane == 0 && !lost) {
       // the CTA of the query tile's last unit
-      const int64_t u1 = m.begin + m.count - 1 + (t.nkt - 1 - t.kt);
-      const int64_t long_end = (m.run + 1) * m.extra;
-      const int64_t last = u1 < long_end ? u1 / (m.run + 1) : m.extra + (u1 - long_end) / m.run;
-      ws.split[blockIdx.x] = Split{t.s, t.qt, (int)last, 0};
+      const int64_t u1 = run.begin + run.count - 1 + (t.nkt - 1 - t.kt);
+      const int64_t long_end = (run.each + 1) * run.extra;
+      const int last = u1 < long_end ? quotient(u1, run.each + 1)
+                                     : run.extra + quotient(u1 - long_end, run.each);
+      ws.split[blockIdx.x] = Split{tok0, head0, rows, last - (int)blockIdx.x + 1};
     }
 #pragma unroll 1
-    for (int blk = 0; blk < 4; ++blk) {
+    for (int n0 = 0; n0 < nv; n0 += 16) {
 #pragma unroll 1
-      for (int n0 = 0; n0 < nv; n0 += 16) {
+      for (int blk = 0; blk < 4; ++blk) {
         uint32_t r[16];
         const uint32_t o = sub + L::kO + blk * L::kN + col0 + n0;
         tc::ld_32x16(o, r);
@@ -955,6 +1004,8 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Misc& m, u
             }
           }
         } else {
+          // (16 rows of a dim in a run, 16 bytes per store, took three times as long: a
+          // warp's store then touches 32 lines instead of one)
           float* dst = ws.o + (slot * NR + col0 + n0) * kRank + blk * 128 + w4 * 32 + lane;
 #pragma unroll
           for (int i = 0; i < 16; ++i)
@@ -970,39 +1021,110 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Misc& m, u
 }
 
 // ------------------------------------------------------------------ the kernel
-// Splits the call's units over the CTAs and finds this CTA's first unit; the
-// scratch is the (still unused) first key stage.
+// The runs of `total` units: the first `extra` CTAs take one unit more than the
+// others; fewer CTAs than the grid has when each would get less than kMinUnits.
+__device__ __forceinline__ void cut(int64_t total, Run& r) {
+  const uint32_t ctas = total >= (int64_t)gridDim.x * kMinUnits
+                            ? gridDim.x
+                            : max(1u, (uint32_t)total / (uint32_t)kMinUnits);
+  if ((total >> 32) == 0) r.each = (uint32_t)total / ctas;
+  else r.each = total / ctas;
+  r.extra = (int)(total - r.each * ctas);
+  r.begin = r.each * blockIdx.x + min((int)blockIdx.x, r.extra);
+  r.count = blockIdx.x < ctas ? (int)r.each + ((int)blockIdx.x < r.extra ? 1 : 0) : 0;
+}
+__device__ __forceinline__ int64_t scan64(int64_t v, int lane) {  // inclusive, over the warp
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+// This CTA's run.  Up to 128 sequences of at most 8 query tiles: every warp finds
+// it by itself (a lane has four sequences), without a barrier.
+constexpr int kLaneSeqs = 4, kLaneTiles = 8;
+template <int NR>
+__device__ __forceinline__ bool schedule_small(const LatentAttnArgs& a, int lane, Run& r,
+                                               uint32_t& errbits) {
+  const int per = (a.num_seqs + 31) >> 5;
+  Seq q[kLaneSeqs];
+  int64_t u[kLaneSeqs], sum = 0;
+  bool big = a.num_seqs > 32 * kLaneSeqs;
+#pragma unroll
+  for (int i = 0; i < kLaneSeqs; ++i) {
+    const int s = lane * per + i;
+    q[i].nqt = 0;
+    if (!big && i < per && s < a.num_seqs) q[i] = load_seq<NR>(a, s);
+  }
+#pragma unroll
+  for (int i = 0; i < kLaneSeqs; ++i) {
+    big |= q[i].nqt > kLaneTiles;
+    u[i] = 0;
+#pragma unroll 1
+    for (int qt = 0; qt < min(q[i].nqt, kLaneTiles); ++qt) u[i] += key_tiles(most_seen<NR>(a, q[i], qt));
+    sum += u[i];
+    if (q[i].nqt > 0 && over_room(a, q[i])) errbits |= kErrBlockOOB;
+  }
+  if (__any_sync(0xFFFFFFFFu, big)) return false;
+  const int64_t inc = scan64(sum, lane);
+  cut(__shfl_sync(0xFFFFFFFFu, inc, 31), r);
+  int64_t off = r.begin - (inc - sum);  // the first unit among this lane's
+  const uint32_t has = __ballot_sync(0xFFFFFFFFu, r.count > 0 && off >= 0 && off < sum);
+  if (has == 0) return true;
+  int s = lane * per, qt = 0, kt = 0;
+  Seq qq = q[0];
+#pragma unroll
+  for (int i = 0; i + 1 < kLaneSeqs; ++i)
+    if (s == lane * per + i && off >= u[i]) {
+      off -= u[i];
+      ++s;
+      qq = q[i + 1];
+    }
+  if (has >> lane & 1) {
+#pragma unroll 1
+    for (;; ++qt) {
+      const int k = key_tiles(most_seen<NR>(a, qq, qt));
+      if (off < k) break;
+      off -= k;
+    }
+    kt = (int)off;
+  }
+  const int from = __ffs(has) - 1;
+  auto all = [&](int v) { return __shfl_sync(0xFFFFFFFFu, v, from); };
+  r.s = all(s);
+  r.qt = all(qt);
+  r.kt = all(kt);
+  r.q = Seq{all(qq.t0), all(qq.ntok), all(qq.c1), all(qq.kv), all(qq.nqt)};
+  return true;
+}
+
+// Any number of sequences and query tiles, by the whole CTA; the scratch is the
+// (still unused) first key stage.
 template <int NR, int kWarps>
-__device__ __forceinline__ void schedule(const LatentAttnArgs& a, uint8_t* scratch, Misc& m,
-                                         uint32_t& errbits) {
+__device__ __noinline__ void schedule_large(const LatentAttnArgs& a, uint8_t* scratch, Run& r) {
+  constexpr int kThreads = kWarps * 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int64_t* pre = reinterpret_cast<int64_t*>(scratch);  // [num_seqs + 1]
-  int64_t* part = pre + a.num_seqs + 1;                // [kWarps]
+  int64_t* pre = reinterpret_cast<int64_t*>(scratch);  // [num_seqs]
+  int64_t* part = pre + a.num_seqs;                    // [kWarps]
+  int64_t* at = part + kWarps;                         // sequence, unit in it, query tile, key tile
   for (int s = warp; s < a.num_seqs; s += kWarps) {
     const Seq q = load_seq<NR>(a, s);
     int64_t u = 0;
     for (int qt = lane; qt < q.nqt; qt += 32) u += key_tiles(most_seen<NR>(a, q, qt));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
-    if (lane == 0) {
-      pre[s] = u;
-      const int64_t most = (int64_t)q.kv + (a.causal ? (int64_t)q.t0 + q.ntok - q.c1 : 0);
-      if (q.ntok > 0 && most > a.room) errbits |= kErrBlockOOB;
-    }
+    if (lane == 0) pre[s] = u;
+    if (lane == 0 && q.nqt > 0 && over_room(a, q) && a.err) atomicOr(a.err, kErrBlockOOB);
   }
   __syncthreads();
-  // exclusive prefix sums: each thread a run of sequences, then warps, then all
-  constexpr int kThreads = kWarps * 32;
+  // prefix sums: each thread a run of sequences, then warps, then all
   const int run = (a.num_seqs + kThreads - 1) / kThreads;
   const int s0 = min((int)threadIdx.x * run, a.num_seqs), s1 = min(s0 + run, a.num_seqs);
   int64_t sum = 0;
   for (int s = s0; s < s1; ++s) sum += pre[s];
-  int64_t inc = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-    if (lane >= o) inc += v;
-  }
+  const int64_t inc = scan64(sum, lane);
   if (lane == 31) part[warp] = inc;
   __syncthreads();
   int64_t before = inc - sum, total = 0;
@@ -1010,49 +1132,32 @@ __device__ __forceinline__ void schedule(const LatentAttnArgs& a, uint8_t* scrat
     if (w < warp) before += part[w];
     total += part[w];
   }
-  // total units over `ctas` runs: the first `extra` of them one longer than `run`
-  const uint32_t ctas = total >= (int64_t)gridDim.x * kMinUnits
-                            ? gridDim.x
-                            : max(1u, (uint32_t)total / (uint32_t)kMinUnits);
-  int64_t each;
-  if ((total >> 32) == 0) each = (uint32_t)total / ctas;
-  else each = total / ctas;
-  const uint32_t extra = (uint32_t)(total - each * ctas);
-  const int64_t begin = each * blockIdx.x + min(blockIdx.x, extra);
-  const bool works = blockIdx.x < ctas && total > 0;
-  if (threadIdx.x == 0) {
-    m.begin = begin;
-    m.count = works ? (int)each + (blockIdx.x < extra ? 1 : 0) : 0;
-    m.run = each;
-    m.extra = (int)extra;
-  }
-  if (works)
+  cut(total, r);
+  if (r.count > 0)
     for (int s = s0; s < s1; ++s) {
       const int64_t u = pre[s];
-      if (before <= begin && begin < before + u) {
-        m.s = s;
-        part[kWarps] = begin - before;
+      if (before <= r.begin && r.begin < before + u) {
+        at[0] = s;
+        at[1] = r.begin - before;
       }
       before += u;
     }
   __syncthreads();
-  if (works && warp == 0) {
-    const Seq q = load_seq<NR>(a, m.s);
-    const int64_t off = part[kWarps];
+  if (r.count > 0) {
+    r.s = (int)at[0];
+    r.q = load_seq<NR>(a, r.s);
+  }
+  if (r.count > 0 && warp == 0) {
+    const int64_t off = at[1];
     int64_t base = 0;
-    for (int q0 = 0; q0 < q.nqt; q0 += 32) {
-      const int64_t u = q0 + lane < q.nqt ? key_tiles(most_seen<NR>(a, q, q0 + lane)) : 0;
-      int64_t in = u;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, in, o);
-        if (lane >= o) in += v;
-      }
+    for (int q0 = 0; q0 < r.q.nqt; q0 += 32) {
+      const int64_t u = q0 + lane < r.q.nqt ? key_tiles(most_seen<NR>(a, r.q, q0 + lane)) : 0;
+      const int64_t in = scan64(u, lane);
       const uint32_t hit = __ballot_sync(0xFFFFFFFFu, off < base + in);
       if (hit) {
         if (lane == __ffs(hit) - 1) {
-          m.qt = q0 + lane;
-          m.kt = (int)(off - (base + in - u));
+          at[2] = q0 + lane;
+          at[3] = off - (base + in - u);
         }
         break;
       }
@@ -1060,11 +1165,16 @@ __device__ __forceinline__ void schedule(const LatentAttnArgs& a, uint8_t* scrat
     }
   }
   __syncthreads();
+  if (r.count > 0) {
+    r.qt = (int)at[2];
+    r.kt = (int)at[3];
+  }
+  __syncthreads();  // the scratch is read
 }
 
 template <int FMT, int NR>
 __global__ void __launch_bounds__(Lay<FMT, NR>::kThreads, 1)
-    latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ CUtensorMap map) {
+    latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps maps) {
   using L = Lay<FMT, NR>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t smem = smem_addr(smem_raw);
@@ -1092,21 +1202,28 @@ __global__ void __launch_bounds__(Lay<FMT, NR>::kThreads, 1)
     mbar_init(bars + 8 * L::kOFree, L::kSoftWarps);
     mbar_fence_init();
   }
-  pdl_wait();
-  const Workspace ws = workspace_of<NR>(a.workspace, gridDim.x);
-  if (threadIdx.x == 0) ws.split[blockIdx.x] = Split{-1, 0, 0, 0};
-  uint32_t errbits = 0;
-  schedule<NR, L::kWarps>(a, smem_raw, m, errbits);
+  tc::fence_before_sync();
+  __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, m.tmem, 0);
   const Waiter wait{smem_addr(&m.abort), a.wait_limit_ns};
-  if (m.count > 0) {
+  pdl_wait();
+  const Workspace ws = workspace_of<NR>(a.workspace, gridDim.x);
+  if (threadIdx.x == 0) ws.split[blockIdx.x] = Split{0, 0, 0, 0};
+  uint32_t errbits = 0;
+  Run run;
+  if (!schedule_small<NR>(a, lane, run, errbits)) {
+    Run large;  // apart, so that only this branch has it in memory
+    schedule_large<NR, L::kWarps>(a, smem_raw, large);
+    run = large;
+  }
+  if (run.count > 0) {
     if (warp < L::kSoftWarps)
-      soften<FMT, NR>(a, m, smem, tmem, wait, warp, lane, ws);
+      soften<FMT, NR>(a, run, smem, tmem, wait, warp, lane, ws);
     else if (warp >= L::kProdWarp)
-      produce<FMT, NR>(a, &map, m, smem, wait, warp - L::kProdWarp, lane, errbits);
+      produce<FMT, NR>(a, maps, run, smem, wait, warp - L::kProdWarp, lane, errbits);
     else
-      issue_mma<FMT, NR>(a, m, smem, tmem, wait);
+      issue_mma<FMT, NR>(a, run, smem, tmem, wait);
   }
   __syncwarp();
   if (a.err) {
@@ -1123,81 +1240,118 @@ __global__ void __launch_bounds__(Lay<FMT, NR>::kThreads, 1)
 }
 
 // ---------------------------------------------------- join of the split query tiles
-// Block (n, c): row n of the query tile that CTA c started and others went on
-// with.  Four groups of 128 threads take the partials in turn, a float4 per
-// thread, and are added in order.
+// A step is one row of a split: 128 threads, four dims each.  With up to kFewParts
+// partials the block's four groups of 128 threads take four rows; with more they
+// share one, a quarter of the partials each, added in order.  The steps of all
+// splits are dealt to the blocks in turn.
 constexpr int kJoinGroups = 4;
 constexpr int kJoinThreads = kJoinGroups * 128;
+constexpr int kFewParts = 8;
 constexpr int kMaxCtas = 1024;
 
 template <int FMT, int NR>
-__global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentAttnArgs a) {
-  __shared__ float wt[kMaxCtas];
-  __shared__ float red[2][kJoinThreads / 32];
+__global__ void __launch_bounds__(kJoinThreads, 2) latent_join_kernel(const LatentAttnArgs a, int ctas) {
+  __shared__ int ends[kMaxCtas];  // steps of the splits up to c
+  __shared__ int warp_sum_s[kJoinThreads / 32];
   __shared__ float4 acc_s[kJoinGroups][128];
+  __shared__ float2 sum_s[kJoinGroups];
   pdl_trigger();
   pdl_wait();
-  const Workspace ws = workspace_of<NR>(a.workspace, gridDim.y);
-  const int c = blockIdx.y, n = blockIdx.x;
-  const Split sp = ws.split[c];
-  if (sp.s < 0) return;
-  const Seq q = load_seq<NR>(a, sp.s);
-  const uint32_t row = (uint32_t)sp.qt * NR + n;
-  if (row >= (uint32_t)q.ntok * (uint32_t)a.num_heads) return;
-  const int parts = sp.last - c + 1;
+  const Workspace ws = workspace_of<NR>(a.workspace, ctas);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  auto slot = [&](int i) { return (2 * (int64_t)(c + i) + (i == 0 ? 1 : 0)) * NR + n; };
-  // the largest maximum, the weights relative to it, and the whole sum
-  float mx = -INFINITY;
-  for (int i = tid; i < parts; i += kJoinThreads) mx = fmaxf(mx, ws.ml[slot(i)].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-  if (lane == 0) red[0][warp] = mx;
-  __syncthreads();
-  mx = red[0][0];
-  for (int w = 1; w < kJoinThreads / 32; ++w) mx = fmaxf(mx, red[0][w]);
-  const float m0 = mx == -INFINITY ? 0.0f : mx;
-  float sum = 0.0f;
-  for (int i = tid; i < parts; i += kJoinThreads) {
-    const float2 v = ws.ml[slot(i)];
-    const float w = ex2(v.x - m0);
-    wt[i] = w;
-    sum += w * v.y;
-  }
-  sum = warp_sum(sum);
-  if (lane == 0) red[1][warp] = sum;
-  __syncthreads();
-  sum = 0.0f;
-  for (int w = 0; w < kJoinThreads / 32; ++w) sum += red[1][w];
   const int grp = tid >> 7, d4 = tid & 127;
-  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-  for (int i = grp; i < parts; i += kJoinGroups) {
-    const float4 v = *reinterpret_cast<const float4*>(ws.o + slot(i) * kRank + d4 * 4);
-    const float w = wt[i];
-    acc.x = fmaf(w, v.x, acc.x);
-    acc.y = fmaf(w, v.y, acc.y);
-    acc.z = fmaf(w, v.z, acc.z);
-    acc.w = fmaf(w, v.w, acc.w);
-  }
-  acc_s[grp][d4] = acc;
-  __syncthreads();
-  if (grp != 0) return;
+  // steps of each split, and their running sums
+  int total = 0;
+#pragma unroll 1
+  for (int c0 = 0; c0 < ctas; c0 += kJoinThreads) {
+    const Split sp = c0 + tid < ctas ? ws.split[c0 + tid] : Split{0, 0, 0, 0};
+    int v = sp.parts > kFewParts ? sp.rows : (sp.rows + kJoinGroups - 1) / kJoinGroups;
 #pragma unroll
-  for (int k = 1; k < kJoinGroups; ++k) {
-    const float4 v = acc_s[k][d4];
-    acc.x += v.x;
-    acc.y += v.y;
-    acc.z += v.z;
-    acc.w += v.w;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+      if (lane >= o) v += u;
+    }
+    if (lane == 31) warp_sum_s[warp] = v;
+    __syncthreads();
+    int sum = 0;
+#pragma unroll 1
+    for (int w = 0; w < kJoinThreads / 32; ++w) {
+      if (w < warp) v += warp_sum_s[w];
+      sum += warp_sum_s[w];
+    }
+    if (c0 + tid < ctas) ends[c0 + tid] = total + v;
+    total += sum;
+    __syncthreads();
   }
   const float ks = FMT == kBF16 ? 1.0f : __ldg(a.k_scale);
-  const float inv = sum == 0.0f ? 0.0f : ks / sum;
-  const int64_t t = q.t0 + token_of(a, row), h = (int)row - token_of(a, row) * a.num_heads;
-  st8(a.out + t * a.out_ts + h * a.out_hs + d4 * 8,
-      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv)));
-  if (tid == 0 && a.lse)
-    a.lse[t * a.lse_ts + h * a.lse_hs] = sum == 0.0f ? -INFINITY : fmaf(m0, kLn2, logf(sum));
+#pragma unroll 1
+  for (int step = blockIdx.x; step < total; step += gridDim.x) {
+    int lo = 0, hi = ctas - 1;  // the split: the first with ends[c] > step
+#pragma unroll 1
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (ends[mid] > step) hi = mid;
+      else lo = mid + 1;
+    }
+    const int c = lo, in = step - (c > 0 ? ends[c - 1] : 0);
+    const Split sp = ws.split[c];
+    const bool shared = sp.parts > kFewParts;
+    const int n = shared ? in : in * kJoinGroups + grp;
+    float4 acc = make_float4(0, 0, 0, 0);
+    float sum = 0.0f, top = -INFINITY;
+    // joins `v` with weight sum lv and maximum mv to what is there
+    auto add = [&](const float4& v, float lv, float mv) {
+      const float m = fmaxf(top, mv), m0 = m == -INFINITY ? 0.0f : m;
+      const float f = ex2(top - m0), w = ex2(mv - m0);
+      acc.x = fmaf(acc.x, f, w * v.x);
+      acc.y = fmaf(acc.y, f, w * v.y);
+      acc.z = fmaf(acc.z, f, w * v.z);
+      acc.w = fmaf(acc.w, f, w * v.w);
+      sum = fmaf(sum, f, w * lv);
+      top = m;
+    };
+    // the first partial lies in the odd slot of CTA c, the others in the even ones behind
+    const int quarter = (sp.parts + kJoinGroups - 1) / kJoinGroups;
+    const int i0 = shared ? min(grp * quarter, sp.parts) : 0;
+    const int i1 = n >= sp.rows ? i0 : shared ? min(i0 + quarter, sp.parts) : sp.parts;
+#pragma unroll 1
+    for (int i = i0; i < i1; i += 8) {
+      float4 v[8];
+      float lv[8], mv[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int64_t row = (2 * (int64_t)(c + i + k) + (i + k == 0 ? 1 : 0)) * NR + n;
+        v[k] = make_float4(0, 0, 0, 0);
+        lv[k] = 0.0f;
+        mv[k] = -INFINITY;
+        if (i + k < i1) {
+          v[k] = __ldcs(reinterpret_cast<const float4*>(ws.o + row * kRank) + d4);
+          lv[k] = ws.l[row];
+          mv[k] = ws.m[row];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) add(v[k], lv[k], mv[k]);
+    }
+    if (shared) {
+      acc_s[grp][d4] = acc;
+      if (d4 == 0) sum_s[grp] = make_float2(sum, top);
+      __syncthreads();
+      if (grp == 0)
+#pragma unroll 1
+        for (int k = 1; k < kJoinGroups; ++k) add(acc_s[k][d4], sum_s[k].x, sum_s[k].y);
+      __syncthreads();
+      if (grp != 0) continue;
+    }
+    if (n >= sp.rows) continue;
+    const int dt = token_of(a, sp.head0 + n);
+    const int64_t t = sp.tok0 + dt, h = sp.head0 + n - dt * a.num_heads;
+    const float inv = sum == 0.0f ? 0.0f : ks / sum;
+    st8(a.out + t * a.out_ts + h * a.out_hs + d4 * 8,
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv)));
+    if (d4 == 0 && a.lse)
+      a.lse[t * a.lse_ts + h * a.lse_hs] = sum == 0.0f ? -INFINITY : fmaf(top, kLn2, logf(sum));
+  }
 }
 
 // Rows of a query tile: the average rows (tokens x heads) per sequence decide.
@@ -1207,10 +1361,9 @@ inline int tile_rows(int32_t num_tokens, int32_t num_heads, int32_t num_seqs, bo
   return rows <= 16 ? 16 : rows <= 32 || fp8 ? 32 : 64;
 }
 
-// The cache as a tensor of (column, entry, block), read in boxes of one chunk of
-// box_rows entries.  Without a box (entries per block not a multiple of 8, or
-// sizes that a tensor map does not hold) rows are copied one by one.
-int box_map(const LatentAttnArgs& a, bool fp8, CUtensorMap* map) {
+// Without a box (entries per block not a multiple of 8, or sizes that a tensor map
+// does not hold) rows are copied one by one.  Returns the entries of a box.
+int box_maps(const LatentAttnArgs& a, bool fp8, Maps* maps) {
   int rows = kKeys;
   while (a.block_size % rows) rows >>= 1;
   if (rows < 8 || a.num_blocks >= INT32_MAX) return 0;
@@ -1225,19 +1378,26 @@ int box_map(const LatentAttnArgs& a, bool fp8, CUtensorMap* map) {
     return reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(f);
   }();
   if (!encode) return 0;
-  const cuuint64_t dims[3] = {576, (cuuint64_t)a.block_size, (cuuint64_t)a.num_blocks};
-  const cuuint64_t strides[2] = {(cuuint64_t)a.entry_stride, (cuuint64_t)a.block_stride};
-  const cuuint32_t box[3] = {fp8 ? 128u : 64u, (cuuint32_t)rows, 1}, unit[3] = {1, 1, 1};
-  const CUresult r = encode(
-      map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-      const_cast<uint8_t*>(a.cache), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? rows : 0;
+  // a chunk is 128 bytes; columns reach past it so that a box may start inside one
+  const cuuint64_t dims[4] = {576, (cuuint64_t)a.block_size, fp8 ? 4u : 9u, (cuuint64_t)a.num_blocks};
+  const cuuint64_t strides[3] = {(cuuint64_t)a.entry_stride, 128, (cuuint64_t)a.block_stride};
+  const cuuint32_t unit[4] = {1, 1, 1, 1};
+  auto make = [&](CUtensorMap* map, cuuint32_t chunks) {
+    const cuuint32_t box[4] = {fp8 ? 128u : 64u, (cuuint32_t)rows, chunks, 1};
+    return encode(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                  const_cast<uint8_t*>(a.cache), dims, strides, box, unit,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  const bool one = rows == kKeys;  // a tile is one box
+  if (one && !make(&maps->tile, fp8 ? 4 : 9)) return 0;
+  if ((!one || fp8) && !make(&maps->chunk, 1)) return 0;
+  return rows;
 }
 
 template <int FMT, int NR>
-cudaError_t launch_t(const LatentAttnArgs& a, const CUtensorMap& map, int ctas,
+cudaError_t launch_t(const LatentAttnArgs& a, const Maps& maps, int ctas,
                      const LaunchCfg& cfg) {
   using L = Lay<FMT, NR>;
   auto kern = latent_attention_kernel<FMT, NR>;
@@ -1253,24 +1413,24 @@ cudaError_t launch_t(const LatentAttnArgs& a, const CUtensorMap& map, int ctas,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = attr;
   lc.numAttrs = cfg.pdl ? 1 : 0;
-  e = cudaLaunchKernelEx(&lc, kern, a, map);
+  e = cudaLaunchKernelEx(&lc, kern, a, maps);
   if (e != cudaSuccess) return e;
-  lc.gridDim = dim3(NR, ctas);
+  lc.gridDim = dim3(2 * ctas);
   lc.blockDim = dim3(kJoinThreads);
   lc.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&lc, latent_join_kernel<FMT, NR>, a);
+  return cudaLaunchKernelEx(&lc, latent_join_kernel<FMT, NR>, a, ctas);
 }
 
 template <int FMT>
 cudaError_t launch_f(LatentAttnArgs a, int ctas, const LaunchCfg& cfg) {
   constexpr bool kF8 = FMT != kBF16;
-  CUtensorMap map = {};
-  a.box_rows = box_map(a, kF8, &map);
+  Maps maps = {};
+  a.box_rows = box_maps(a, kF8, &maps);
   switch (tile_rows(a.num_tokens, a.num_heads, a.num_seqs, kF8)) {
-    case 16: return launch_t<FMT, 16>(a, map, ctas, cfg);
-    case 32: return launch_t<FMT, 32>(a, map, ctas, cfg);
+    case 16: return launch_t<FMT, 16>(a, maps, ctas, cfg);
+    case 32: return launch_t<FMT, 32>(a, maps, ctas, cfg);
     default:
-      if constexpr (!kF8) return launch_t<FMT, 64>(a, map, ctas, cfg);
+      if constexpr (!kF8) return launch_t<FMT, 64>(a, maps, ctas, cfg);
       else return cudaErrorInvalidValue;
   }
 }
@@ -1280,7 +1440,7 @@ cudaError_t launch_f(LatentAttnArgs a, int ctas, const LaunchCfg& cfg) {
 // The largest call within these sizes may use any tile: enough for 64 rows.
 int64_t latent_attention_workspace(int32_t, int32_t, int32_t, int num_sms) {
   const int64_t ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
-  return ctas * ((int64_t)sizeof(Split) + 2 * 64 * (sizeof(float2) + kRank * sizeof(float)));
+  return ctas * ((int64_t)sizeof(Split) + 2 * 64 * (2 + kRank) * (int64_t)sizeof(float));
 }
 
 cudaError_t launch_latent_attention(const LatentAttnArgs& a, int cache_fmt, int num_sms,
