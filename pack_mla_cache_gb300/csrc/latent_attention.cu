@@ -38,9 +38,9 @@
 // instructions, 1500 cycles at NR = 16 and 2000 at NR = 64; fp8 18 + 8, 780 at
 // NR = 16.  HBM delivers a bf16 tile to each SM in 3140 cycles, an fp8 one in 1570.
 //
-// Roles (9 or 13 warps): 4 or 8 warps do the softmax (running maximum per query
+// Roles (10 or 14 warps): 4 or 8 warps do the softmax (running maximum per query
 // row, rescaling O^T only when a maximum has grown by more than 2^8, or 2^4 for
-// fp8) and the output; one warp issues the matrix instructions; 4 warps load.
+// fp8) and the output; two warps issue the matrix instructions; 4 warps load.
 // Whole tiles come by TMA where a tile is a few boxes of the paged cache (block
 // size a multiple of 8); the others, and the last tile of a sequence, whose rows
 // behind the end are zeros, by 16-byte asynchronous copies.
@@ -53,6 +53,8 @@
 // Waits are bounded (wait_limit_ns): one that runs out marks the CTA as given
 // up, every later wait returns at once, and MLA_ERRBIT_TIMEOUT is set.
 #include <cuda.h>
+
+#include <atomic>
 
 #include "mla_device.cuh"
 #include "mla_internal.h"
@@ -88,8 +90,9 @@ struct Lay {
   static constexpr int kQ = kChunks * kN * 128;
   static constexpr int kSoftWarps = NR == 64 ? 8 : 4;   // 4 warps per 32 query rows
   static constexpr int kCols = NR == 64 ? 32 : NR;      // query rows of a group of 4 warps
-  static constexpr int kMmaWarp = kSoftWarps;
-  static constexpr int kProdWarp = kMmaWarp + 1;
+  static constexpr int kScoreWarp = kSoftWarps;         // issues the scores' products
+  static constexpr int kOutWarp = kScoreWarp + 1;       // and the outputs'
+  static constexpr int kProdWarp = kOutWarp + 1;
   static constexpr int kWarps = kProdWarp + kProdWarps;
   static constexpr int kThreads = kWarps * 32;
   // a maximum may grow this much (log2) before the sums are rescaled; the fp8
@@ -97,15 +100,17 @@ struct Lay {
   static constexpr float kGrow = kF8 ? 4.0f : 8.0f;
   // shared memory
   static constexpr int q = kStages * kTile;
-  static constexpr int p = q + kQBufs * kQ;              // kN rows x 128 bytes
-  static constexpr int red = p + kN * 128;               // float [2][kSoftWarps][kCols]
+  static constexpr int kPBufs = NR == 64 ? 1 : 2;
+  static constexpr int kP = kN * 128;                    // kN rows x 64 keys (fp8: half of each row)
+  static constexpr int p = q + kQBufs * kQ;
+  static constexpr int red = p + kPBufs * kP;               // float [2][kSoftWarps][kCols]
   static constexpr int qs = red + 2 * kSoftWarps * kCols * 4;  // float [kQBufs][NR]
   static constexpr int flags = qs + (kF8 ? kQBufs * NR * 4 : 0);  // uint8 [kStages][64]
   static constexpr int bars = flags + kStages * kKeys;
   // barriers, by index
   static constexpr int kFull = 0, kEmpty = kStages, kQFull = 2 * kStages, kQEmpty = kQFull + 2,
-                       kSFull = kQEmpty + 2, kPFull = kSFull + 2, kPvDone = kPFull + 1,
-                       kOFree = kPvDone + 1, kBars = kOFree + 1;
+                       kSFull = kQEmpty + 2, kPFull = kSFull + 2, kPvDone = kPFull + 2,
+                       kOFree = kPvDone + 2, kBars = kOFree + 1;
   static constexpr int misc = (bars + kBars * 8 + 15) / 16 * 16;
   static constexpr int bytes = misc + 64;
   static_assert(bytes <= 232448, "shared memory of a CTA");
@@ -332,6 +337,11 @@ __device__ __forceinline__ const uint8_t* row_in(const LatentAttnArgs& a, int p,
   return ok ? r : nullptr;
 }
 
+// Whether the tile comes by TMA: whole, and every row of the query tile sees it.
+__device__ __forceinline__ bool by_box(const LatentAttnArgs& a, const Tile& t) {
+  return a.box_rows != 0 && (t.kt + 1) * kKeys <= t.least;
+}
+
 // ------------------------------------------------------------------ producers
 // One query tile into shared memory: bf16 rows by asynchronous copies.
 template <int NR>
@@ -414,14 +424,8 @@ __device__ __forceinline__ void split_q(const LatentAttnArgs& a, const Tile& q, 
   if (lane == 0) mbar_arrive_n(bar, 32);
 }
 
-// The cache as a tensor of (column, entry, chunk, block): boxes of one chunk of
-// box_rows entries, and of all chunks (fp8: the first four) of a whole tile.
-struct Maps {
-  CUtensorMap chunk, tile;
-};
-
 template <int FMT, int NR>
-__device__ __forceinline__ void produce(const LatentAttnArgs& a, const Maps& maps,
+__device__ __forceinline__ void produce(const LatentAttnArgs& a, const CUtensorMap& map,
                                         const Run& run, uint32_t smem, const Waiter& wait, int pw,
                                         int lane, uint32_t& errbits) {
   using L = Lay<FMT, NR>;
@@ -435,8 +439,8 @@ __device__ __forceinline__ void produce(const LatentAttnArgs& a, const Maps& map
   const int row0 = pw * 16 + (lane >> 3), col = lane & 7;
   const int boxes = a.box_rows ? kKeys / a.box_rows : 0;
   const int box = boxes ? lane & (boxes - 1) : 0;
-  // whole tiles, whose rows every row of the query tile sees
-  auto by_box = [&](const Tile& t) { return boxes && (t.kt + 1) * kKeys <= t.least; };
+  const int box_chunk = boxes ? lane / boxes : 0, box_step = boxes ? 32 / boxes : 1;
+  const int box_word = boxes ? (lane & 15) * 4 / a.box_rows : 0;  // the box of flag word `lane`
   // Blocks are looked up two tiles ahead.
   Tile cur{}, nxt{};
   int32_t blk[kRows] = {}, nblk[kRows] = {};
@@ -445,7 +449,7 @@ __device__ __forceinline__ void produce(const LatentAttnArgs& a, const Maps& map
   for (int step = -2;; ++step) {
     const Tile far = walk.next(a);
     int32_t fblk[kRows];
-    if (by_box(far)) {
+    if (by_box(a, far)) {
       fblk[0] = pw == 0 ? find_block(a, far, far.kt * kKeys + box * a.box_rows) : kUnseen;
     } else {
 #pragma unroll
@@ -458,12 +462,12 @@ __device__ __forceinline__ void produce(const LatentAttnArgs& a, const Maps& map
       if (g >= L::kStages) wait(bars + 8 * (L::kEmpty + st), (g / L::kStages - 1) & 1);
       __syncwarp();
       const uint32_t base = smem + st * L::kTile;
-      if (by_box(cur)) {
+      if (by_box(a, cur)) {
         if (pw == 0) {
           const bool ok = blk[0] >= 0 && blk[0] < a.num_blocks;
           if (!ok) errbits |= kErrBlockOOB;
           const uint32_t none = __shfl_sync(0xFFFFFFFFu, ok ? 0u : 0x01010101u * kAbsent,
-                                            (lane & 15) * 4 / a.box_rows);
+                                            box_word);
           if (lane < 16) sts_u32(flags + 4 * lane, none);
           __syncwarp();
           if (lane == 0) {
@@ -475,16 +479,9 @@ __device__ __forceinline__ void produce(const LatentAttnArgs& a, const Maps& map
           const int off = a.bs_shift >= 0 ? p & (a.block_size - 1) : p % a.block_size;
           const int z = ok ? blk[0] : (int)a.num_blocks;  // outside the tensor: zeros
           const uint32_t to = base + box * a.box_rows * 128;
-          if (boxes == 1) {
-            // one box of all chunks (fp8: of four; the last one starts in the middle)
-            if (lane == 0) tc::tma_load4(base, &maps.tile, 0, off, 0, z, full);
-            if (L::kF8 && lane == 1) tc::tma_load4(base + 4 * kChunk, &maps.chunk, 448, off, 0, z, full);
-          } else {
-            for (int i = lane / boxes; i < L::kChunks; i += 32 / boxes) {
-              if (L::kF8 && i == 4) tc::tma_load4(to + i * kChunk, &maps.chunk, 448, off, 0, z, full);
-              else tc::tma_load4(to + i * kChunk, &maps.chunk, 0, off, i, z, full);
-            }
-          }
+          for (int i = box_chunk; i < L::kChunks; i += box_step)
+            tc::tma_load3(to + i * kChunk, &map, L::kF8 ? (i < 4 ? i * 128 : 448) : i * 64, off, z,
+                          full);
         } else if (lane == 0) {
           mbar_arrive_n(full, 33);
         }
@@ -591,7 +588,7 @@ __device__ __forceinline__ void issue_outputs(uint32_t smem, uint32_t tmem, bool
   // The K tile, MN-major.  128 dims are two bf16 chunks or one fp8 chunk; a k step
   // is 16 keys (2 groups of 8 rows) or 32.
   const uint64_t va = tc::smem_desc(smem + ST * L::kTile, L::kF8 ? 0 : kChunk, 1024);
-  const uint64_t pa = tc::smem_desc(smem + L::p, 0, 1024);
+  const uint64_t pa = tc::smem_desc(smem + L::p + (ST & (L::kPBufs - 1)) * L::kP, 0, 1024);
   constexpr int kDims = L::kF8 ? kChunk : 2 * kChunk, kStep = L::kF8 ? 4096 : 2048;
 #pragma unroll 1
   for (int b = 0; b < 4; ++b)
@@ -603,35 +600,40 @@ __device__ __forceinline__ void issue_outputs(uint32_t smem, uint32_t tmem, bool
       else tc::mma_bf16(one, d, ak, bk, kId, k > 0 || !first);
     }
   tc::commit(one, smem + L::bars + 8 * (L::kEmpty + ST));
-  tc::commit(one, smem + L::bars + 8 * L::kPvDone);
+  tc::commit(one, smem + L::bars + 8 * (L::kPvDone + (ST & 1)));
 }
 
+// One warp issues the scores, another the outputs, each as soon as its operands
+// are there: outputs free the stage that the rows behind need, and from one warp
+// they would wait for the scores of the next tile (1000 to 1300 cycles) or for its
+// polls of both.
 template <int FMT, int NR>
-__device__ __forceinline__ void issue_mma(const LatentAttnArgs& a, const Run& run, uint32_t smem,
-                                          uint32_t tmem, const Waiter& wait) {
+__device__ __forceinline__ void score_role(const LatentAttnArgs& a, const Run& run, uint32_t smem,
+                                           uint32_t tmem, const Waiter& waiter) {
   using L = Lay<FMT, NR>;
   const uint32_t bars = smem + L::bars;
+  auto wait = [&](int bar, uint32_t phase) { waiter(bars + 8 * bar, phase & 1); };
   Walk<NR> walk;
   walk.start(run);
   const bool one = tc::elect();
-  uint32_t items = 0;       // query tiles whose scores have begun
-  uint32_t done_items = 0;  // query tiles whose outputs have begun
-  // whether tile g's rows (and its query) are there
-  auto loaded = [&](const Tile& t, uint32_t g) {
-    return mbar_test(bars + 8 * (L::kFull + g % L::kStages), (g / L::kStages) & 1) &&
-           (!t.first ||
-            mbar_test(bars + 8 * (L::kQFull + items % L::kQBufs), (items / L::kQBufs) & 1));
-  };
-  auto scores = [&](const Tile& t, uint32_t g) {
-    items += t.first;
-    // Rows may have been written by ordinary and asynchronous stores of the
-    // producers; the fence towards the tensor core's reads stands here, behind the
-    // barrier (in the producers it would also wait for their loads in flight).
-    tc::fence_smem_async();
+  uint32_t item = 0;
+#pragma unroll 1
+  for (uint32_t g = 0;; ++g) {
+    const Tile t = walk.next(a);
+    if (!t.valid) break;
+    const int qb = item % L::kQBufs, st = g % L::kStages;
+    if (t.first) wait(L::kQFull + qb, item / L::kQBufs);
+    if (g >= 2) wait(L::kPFull + (g & 1), (g - 2) >> 1);  // the score buffer is read
+    wait(L::kFull + st, g / L::kStages);
+    __syncwarp();
+    // Queries, and rows that do not come by TMA, are written by ordinary and
+    // asynchronous stores of the producers; the fence towards the tensor core's reads
+    // stands here, behind the barrier (in the producers it would also wait for their
+    // loads in flight).
+    if (t.first || !by_box(a, t)) tc::fence_smem_async();
     tc::fence_after_sync();
     constexpr int kQ1 = L::kQBufs - 1, kS2 = L::kStages - 2, kS3 = L::kStages - 1;
-    const int st = g % L::kStages;
-    if (L::kQBufs == 1 || (items & 1)) {
+    if (qb == 0) {
       if (st == 0) issue_scores<FMT, NR, 0, 0>(smem, tmem, one, t.last);
       else if (st == 1) issue_scores<FMT, NR, 1, 0>(smem, tmem, one, t.last);
       else if (st == 2) issue_scores<FMT, NR, kS2, 0>(smem, tmem, one, t.last);
@@ -642,13 +644,27 @@ __device__ __forceinline__ void issue_mma(const LatentAttnArgs& a, const Run& ru
       else if (st == 2) issue_scores<FMT, NR, kS2, kQ1>(smem, tmem, one, t.last);
       else issue_scores<FMT, NR, kS3, kQ1>(smem, tmem, one, t.last);
     }
-  };
-  auto weighted = [&](const Tile& t, uint32_t g) {
-    return mbar_test(bars + 8 * L::kPFull, g & 1) &&
-           (!t.first || done_items == 0 || mbar_test(bars + 8 * L::kOFree, (done_items - 1) & 1));
-  };
-  auto outputs = [&](const Tile& t, uint32_t g) {
-    done_items += t.first;
+    item += t.last;
+  }
+}
+
+template <int FMT, int NR>
+__device__ __forceinline__ void output_role(const LatentAttnArgs& a, const Run& run, uint32_t smem,
+                                            uint32_t tmem, const Waiter& waiter) {
+  using L = Lay<FMT, NR>;
+  const uint32_t bars = smem + L::bars;
+  auto wait = [&](int bar, uint32_t phase) { waiter(bars + 8 * bar, phase & 1); };
+  Walk<NR> walk;
+  walk.start(run);
+  const bool one = tc::elect();
+  uint32_t item = 0;
+#pragma unroll 1
+  for (uint32_t g = 0;; ++g) {
+    const Tile t = walk.next(a);
+    if (!t.valid) break;
+    wait(L::kPFull + (g & 1), g >> 1);
+    if (t.first && item > 0) wait(L::kOFree, item - 1);  // the sums of the query tile before are read
+    __syncwarp();
     tc::fence_after_sync();
     constexpr int kS2 = L::kStages - 2, kS3 = L::kStages - 1;
     const int st = g % L::kStages;
@@ -656,35 +672,7 @@ __device__ __forceinline__ void issue_mma(const LatentAttnArgs& a, const Run& ru
     else if (st == 1) issue_outputs<FMT, NR, 1>(smem, tmem, one, t.first);
     else if (st == 2) issue_outputs<FMT, NR, kS2>(smem, tmem, one, t.first);
     else issue_outputs<FMT, NR, kS3>(smem, tmem, one, t.first);
-  };
-  Tile cur{};
-  // The scores of tile g and the outputs of tile g - 1 are issued as each
-  // becomes ready, scores first: waiting for rows never holds back outputs (they
-  // free the stage that the rows behind them need).  With one query buffer the
-  // scores of a new query tile come after the outputs before them: their query
-  // is loaded over the old one.
-#pragma unroll 1
-  for (uint32_t g = 0;; ++g) {
-    const Tile nxt = walk.next(a);
-    if (!cur.valid && !nxt.valid) break;
-    bool s_due = nxt.valid, o_due = cur.valid;
-    const bool s_held = L::kQBufs == 1 && nxt.first;
-    uint64_t since = 0;
-#pragma unroll 1
-    for (uint32_t spin = 1; s_due || o_due; ++spin) {
-      const bool lost = (spin & 127u) == 0 && wait.expired(since);
-      const bool s_go = s_due && !(s_held && o_due) && (loaded(nxt, g) || lost);
-      if (__all_sync(0xFFFFFFFFu, s_go)) {
-        scores(nxt, g);
-        s_due = false;
-      }
-      const bool o_go = o_due && (weighted(cur, g - 1) || lost);
-      if (__all_sync(0xFFFFFFFFu, o_go)) {
-        outputs(cur, g - 1);
-        o_due = false;
-      }
-    }
-    cur = nxt;
+    item += t.last;
   }
 }
 
@@ -803,8 +791,11 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
       for (int e = 0; e < 2; ++e)
         grown |= fmaxf(x[j][e], x[j][e + 2]) > mu[j][e] + L::kGrow;
     grown = soft_any(group, grown);
-    // P's buffer, and O^T for the rescaling, are free when the outputs of the tile before are done
-    if (g > 0) wait(bars + 8 * L::kPvDone, (g - 1) & 1);
+    // P's buffer is free when the outputs of the tile that had it are done
+    if (g >= L::kPBufs) {
+      const uint32_t o = g - L::kPBufs;
+      wait(bars + 8 * (L::kPvDone + (o & 1)), (o >> 1) & 1);
+    }
     if (grown) {
       // maximum over the tile's 64 keys: in the warp, then across the four warps
       float* mine = red + warp * kC;
@@ -843,7 +834,8 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
         if (lane < 4) *reinterpret_cast<float2*>(fac + 8 * j + c2) = make_float2(f[0], f[1]);
       }
       soft_sync(group);  // the maxima are read, the factors written
-      if (!t.first) {
+      if (!t.first) {  // and O^T when those of the tile before are
+        wait(bars + 8 * (L::kPvDone + ((g - 1) & 1)), ((g - 1) >> 1) & 1);
         tc::fence_after_sync();
 #pragma unroll 1
         for (int n = 0; n < 4 * L::kParts * kC; n += 16) {
@@ -886,8 +878,8 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
             const uint32_t lo = pack_fp8x2<kE4M3>((u - uh) * (1.0f / kP2), (v - vh) * (1.0f / kP2));
             const int n = (j + jj) * 8 + c2;  // and n + 1
             const uint32_t in = (lane >> 2) + 8 * h;
-            const uint32_t d0 = smem + L::p + n * 128 + ((w4 ^ (n & 7)) << 4) + in;
-            const uint32_t d1 = smem + L::p + (n + 1) * 128 + ((w4 ^ ((n + 1) & 7)) << 4) + in;
+            const uint32_t d0 = smem + L::p + (g & (L::kPBufs - 1)) * L::kP + n * 128 + ((w4 ^ (n & 7)) << 4) + in;
+            const uint32_t d1 = smem + L::p + (g & (L::kPBufs - 1)) * L::kP + (n + 1) * 128 + ((w4 ^ ((n + 1) & 7)) << 4) + in;
             sts_u8(d0, hi);
             sts_u8(d1, hi >> 8);
             sts_u8(d0 + NR * 128, lo);
@@ -898,17 +890,17 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
       if constexpr (!L::kF8) {
         const int n = col0 + (j + (lane >> 4)) * 8 + (lane & 7);
         const int unit = 2 * w4 + ((lane >> 3) & 1);
-        tc::st_8x8_t(smem + L::p + n * 128 + ((unit ^ (n & 7)) << 4), w[0], w[1], w[2], w[3]);
+        tc::st_8x8_t(smem + L::p + (g & (L::kPBufs - 1)) * L::kP + n * 128 + ((unit ^ (n & 7)) << 4), w[0], w[1], w[2], w[3]);
       }
     }
     tc::fence_smem_async();
     tc::fence_before_sync();
     __syncwarp();
-    if (lane == 0) mbar_arrive(bars + 8 * L::kPFull);
+    if (lane == 0) mbar_arrive(bars + 8 * (L::kPFull + b));
     if (!t.last) continue;
 
     // ---- the end of this CTA's run of the query tile
-    wait(bars + 8 * L::kPvDone, g & 1);
+    wait(bars + 8 * (L::kPvDone + b), (g >> 1) & 1);
     tc::fence_after_sync();
     // the sums of the weights over lanes (and warps, below); row n's sum and maximum
     // then go to lane n
@@ -1174,7 +1166,7 @@ __device__ __noinline__ void schedule_large(const LatentAttnArgs& a, uint8_t* sc
 
 template <int FMT, int NR>
 __global__ void __launch_bounds__(Lay<FMT, NR>::kThreads, 1)
-    latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ Maps maps) {
+    latent_attention_kernel(const LatentAttnArgs a, const __grid_constant__ CUtensorMap map) {
   using L = Lay<FMT, NR>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t smem = smem_addr(smem_raw);
@@ -1182,7 +1174,7 @@ __global__ void __launch_bounds__(Lay<FMT, NR>::kThreads, 1)
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   Misc& m = *reinterpret_cast<Misc*>(smem_raw + L::misc);
   pdl_trigger();
-  if (warp == L::kMmaWarp) tc::alloc(smem_addr(&m.tmem), L::kTmem);
+  if (warp == L::kScoreWarp) tc::alloc(smem_addr(&m.tmem), L::kTmem);
   if (threadIdx.x == 0) {
     m.abort = 0;
     const uint32_t bars = smem + L::bars;
@@ -1196,9 +1188,9 @@ __global__ void __launch_bounds__(Lay<FMT, NR>::kThreads, 1)
       // the last scores of its query tile, and for fp8 the softmax warps' look at the scales
       mbar_init(bars + 8 * (L::kQEmpty + i), 1 + (L::kF8 ? L::kSoftWarps : 0));
       mbar_init(bars + 8 * (L::kSFull + i), 1);
+      mbar_init(bars + 8 * (L::kPFull + i), L::kSoftWarps);
+      mbar_init(bars + 8 * (L::kPvDone + i), 1);
     }
-    mbar_init(bars + 8 * L::kPFull, L::kSoftWarps);
-    mbar_init(bars + 8 * L::kPvDone, 1);
     mbar_init(bars + 8 * L::kOFree, L::kSoftWarps);
     mbar_fence_init();
   }
@@ -1221,9 +1213,11 @@ __global__ void __launch_bounds__(Lay<FMT, NR>::kThreads, 1)
     if (warp < L::kSoftWarps)
       soften<FMT, NR>(a, run, smem, tmem, wait, warp, lane, ws);
     else if (warp >= L::kProdWarp)
-      produce<FMT, NR>(a, maps, run, smem, wait, warp - L::kProdWarp, lane, errbits);
+      produce<FMT, NR>(a, map, run, smem, wait, warp - L::kProdWarp, lane, errbits);
+    else if (warp == L::kScoreWarp)
+      score_role<FMT, NR>(a, run, smem, tmem, wait);
     else
-      issue_mma<FMT, NR>(a, run, smem, tmem, wait);
+      output_role<FMT, NR>(a, run, smem, tmem, wait);
   }
   __syncwarp();
   if (a.err) {
@@ -1236,7 +1230,7 @@ __global__ void __launch_bounds__(Lay<FMT, NR>::kThreads, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  if (warp == L::kMmaWarp) tc::dealloc(tmem, L::kTmem);
+  if (warp == L::kScoreWarp) tc::dealloc(tmem, L::kTmem);
 }
 
 // ---------------------------------------------------- join of the split query tiles
@@ -1361,9 +1355,12 @@ inline int tile_rows(int32_t num_tokens, int32_t num_heads, int32_t num_seqs, bo
   return rows <= 16 ? 16 : rows <= 32 || fp8 ? 32 : 64;
 }
 
-// Without a box (entries per block not a multiple of 8, or sizes that a tensor map
-// does not hold) rows are copied one by one.  Returns the entries of a box.
-int box_maps(const LatentAttnArgs& a, bool fp8, Maps* maps) {
+// The cache as a tensor of (column, entry, block), read in boxes of one chunk of
+// `rows` entries.  Without a box (entries per block not a multiple of 8, or sizes
+// that a tensor map does not hold) rows are copied one by one.  Returns the
+// entries of a box, or 0.  (All chunks of a tile as one box of a 4-dimensional map
+// took the same time.)
+int box_map(const LatentAttnArgs& a, bool fp8, CUtensorMap* map) {
   int rows = kKeys;
   while (a.block_size % rows) rows >>= 1;
   if (rows < 8 || a.num_blocks >= INT32_MAX) return 0;
@@ -1378,31 +1375,32 @@ int box_maps(const LatentAttnArgs& a, bool fp8, Maps* maps) {
     return reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(f);
   }();
   if (!encode) return 0;
-  // a chunk is 128 bytes; columns reach past it so that a box may start inside one
-  const cuuint64_t dims[4] = {576, (cuuint64_t)a.block_size, fp8 ? 4u : 9u, (cuuint64_t)a.num_blocks};
-  const cuuint64_t strides[3] = {(cuuint64_t)a.entry_stride, 128, (cuuint64_t)a.block_stride};
-  const cuuint32_t unit[4] = {1, 1, 1, 1};
-  auto make = [&](CUtensorMap* map, cuuint32_t chunks) {
-    const cuuint32_t box[4] = {fp8 ? 128u : 64u, (cuuint32_t)rows, chunks, 1};
-    return encode(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-                  const_cast<uint8_t*>(a.cache), dims, strides, box, unit,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-  };
-  const bool one = rows == kKeys;  // a tile is one box
-  if (one && !make(&maps->tile, fp8 ? 4 : 9)) return 0;
-  if ((!one || fp8) && !make(&maps->chunk, 1)) return 0;
-  return rows;
+  const cuuint64_t dims[3] = {576, (cuuint64_t)a.block_size, (cuuint64_t)a.num_blocks};
+  const cuuint64_t strides[2] = {(cuuint64_t)a.entry_stride, (cuuint64_t)a.block_stride};
+  const cuuint32_t box[3] = {fp8 ? 128u : 64u, (cuuint32_t)rows, 1}, unit[3] = {1, 1, 1};
+  const CUresult r = encode(
+      map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+      const_cast<uint8_t*>(a.cache), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? rows : 0;
 }
 
 template <int FMT, int NR>
-cudaError_t launch_t(const LatentAttnArgs& a, const Maps& maps, int ctas,
+cudaError_t launch_t(const LatentAttnArgs& a, const CUtensorMap& map, int ctas,
                      const LaunchCfg& cfg) {
   using L = Lay<FMT, NR>;
   auto kern = latent_attention_kernel<FMT, NR>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::bytes);
+  // the attribute stays with the device's context: set on a device's first call
+  static std::atomic<uint64_t> set{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(set.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::bytes);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) set.fetch_or(uint64_t(1) << dev);
+  }
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(ctas);
   lc.blockDim = dim3(L::kThreads);
@@ -1413,7 +1411,7 @@ cudaError_t launch_t(const LatentAttnArgs& a, const Maps& maps, int ctas,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = attr;
   lc.numAttrs = cfg.pdl ? 1 : 0;
-  e = cudaLaunchKernelEx(&lc, kern, a, maps);
+  e = cudaLaunchKernelEx(&lc, kern, a, map);
   if (e != cudaSuccess) return e;
   lc.gridDim = dim3(2 * ctas);
   lc.blockDim = dim3(kJoinThreads);
@@ -1424,13 +1422,13 @@ cudaError_t launch_t(const LatentAttnArgs& a, const Maps& maps, int ctas,
 template <int FMT>
 cudaError_t launch_f(LatentAttnArgs a, int ctas, const LaunchCfg& cfg) {
   constexpr bool kF8 = FMT != kBF16;
-  Maps maps = {};
-  a.box_rows = box_maps(a, kF8, &maps);
+  CUtensorMap map = {};
+  a.box_rows = box_map(a, kF8, &map);
   switch (tile_rows(a.num_tokens, a.num_heads, a.num_seqs, kF8)) {
-    case 16: return launch_t<FMT, 16>(a, maps, ctas, cfg);
-    case 32: return launch_t<FMT, 32>(a, maps, ctas, cfg);
+    case 16: return launch_t<FMT, 16>(a, map, ctas, cfg);
+    case 32: return launch_t<FMT, 32>(a, map, ctas, cfg);
     default:
-      if constexpr (!kF8) return launch_t<FMT, 64>(a, maps, ctas, cfg);
+      if constexpr (!kF8) return launch_t<FMT, 64>(a, map, ctas, cfg);
       else return cudaErrorInvalidValue;
   }
 }

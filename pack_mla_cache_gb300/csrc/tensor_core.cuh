@@ -166,15 +166,15 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool v
                "r"(valid ? 16u : 0u)
                : "memory");
 }
-// One box of a 4-dimensional tensor map to shared memory, completing on `bar`
+// One box of a 3-dimensional tensor map to shared memory, completing on `bar`
 // (parts outside the tensor are filled with zeros; x * element size a multiple of
 // 16 bytes).
-__device__ __forceinline__ void tma_load4(uint32_t dst, const void* map, int x, int y, int z,
-                                          int w, uint32_t bar) {
+__device__ __forceinline__ void tma_load3(uint32_t dst, const void* map, int x, int y, int z,
+                                          uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
-      "[%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
 // Arrive on `bar` when this thread's cp_async16 so far are done.

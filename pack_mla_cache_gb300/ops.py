@@ -133,7 +133,13 @@ def _check(status: int) -> None:
         raise MlaError(status, lib().mla_last_error().decode())
 
 
+_CODES = {v: k for k, v in _TORCH_DTYPE.items()}
+
+
 def dtype_code(d) -> int:
+    code = _CODES.get(d)  # most calls name a torch dtype
+    if code is not None:
+        return code
     if isinstance(d, int):
         return d
     if isinstance(d, torch.dtype):
@@ -152,8 +158,8 @@ def _ptr(t) -> int | None:
 
 
 def _stream(stream) -> int | None:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # the handle alone: a Stream object costs 3 us
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
