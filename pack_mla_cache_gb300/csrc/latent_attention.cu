@@ -213,7 +213,7 @@ struct Walk {
   __device__ __forceinline__ Tile next(const LatentAttnArgs& a) {
     Tile t{};
     if (left <= 0) return t;
-    if (kt >= nkt) {  // another query tile (the first: nkt is 0)
+    if (__builtin_expect(kt >= nkt, 0)) {  // another query tile (the first: nkt is 0)
       if (nkt > 0) {
         kt = 0;
         ++qt;
@@ -242,24 +242,28 @@ struct Walk {
   }
 };
 
-// Bounded waits of one thread.
+// Bounded waits.  The loops of the roles have to stay small (13 warps of different
+// code share the instruction caches; fetching was the largest stall), so all but
+// the first look at a barrier is out of line.
+__device__ __noinline__ void wait_on(uint32_t bar, uint32_t parity, uint32_t abort, uint64_t limit) {
+  uint64_t since = 0;
+  for (uint32_t spin = 1; !mbar_try_wait(bar, parity); ++spin) {
+    if (spin & 31u) continue;
+    if (lds_u32(abort) != 0) return;
+    const uint64_t now = global_ns();
+    if (since == 0) since = now;
+    if (now - since > limit) {
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(abort), "r"(1u) : "memory");
+      return;
+    }
+  }
+}
 struct Waiter {
   uint32_t abort;  // shared address of Misc::abort
   uint64_t limit;
   __device__ __forceinline__ bool given_up() const { return lds_u32(abort) != 0; }
-  // Called now and then while waiting; since: 0 at first.
-  __device__ __forceinline__ bool expired(uint64_t& since) const {
-    if (given_up()) return true;
-    const uint64_t now = global_ns();
-    if (since == 0) since = now;
-    if (now - since <= limit) return false;
-    asm volatile("st.shared.u32 [%0], %1;" ::"r"(abort), "r"(1u) : "memory");
-    return true;
-  }
   __device__ __forceinline__ void operator()(uint32_t bar, uint32_t parity) const {
-    uint64_t since = 0;
-    for (uint32_t spin = 1; !mbar_try_wait(bar, parity); ++spin)
-      if ((spin & 31u) == 0 && expired(since)) return;
+    if (!mbar_try_wait(bar, parity)) wait_on(bar, parity, abort, limit);
   }
 };
 
@@ -449,7 +453,7 @@ __device__ __forceinline__ void produce(const LatentAttnArgs& a, const CUtensorM
   for (int step = -2;; ++step) {
     const Tile far = walk.next(a);
     int32_t fblk[kRows];
-    if (by_box(a, far)) {
+    if (__builtin_expect(by_box(a, far), 1)) {
       fblk[0] = pw == 0 ? find_block(a, far, far.kt * kKeys + box * a.box_rows) : kUnseen;
     } else {
 #pragma unroll
@@ -462,7 +466,7 @@ __device__ __forceinline__ void produce(const LatentAttnArgs& a, const CUtensorM
       if (g >= L::kStages) wait(bars + 8 * (L::kEmpty + st), (g / L::kStages - 1) & 1);
       __syncwarp();
       const uint32_t base = smem + st * L::kTile;
-      if (by_box(a, cur)) {
+      if (__builtin_expect(by_box(a, cur), 1)) {
         if (pw == 0) {
           const bool ok = blk[0] >= 0 && blk[0] < a.num_blocks;
           if (!ok) errbits |= kErrBlockOOB;
@@ -528,7 +532,7 @@ __device__ __forceinline__ void produce(const LatentAttnArgs& a, const CUtensorM
           tc::cp_async_arrive(full);
         }
       }
-      if (cur.first) {
+      if (__builtin_expect(cur.first, 0)) {
         const int b = item % L::kQBufs;
         const uint32_t n = item / L::kQBufs;
         if (n > 0) wait(bars + 8 * (L::kQEmpty + b), (n - 1) & 1);
@@ -766,7 +770,7 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
     for (int j = 0; j < kG; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[j][i] *= cs[j][i & 1];
-    if ((t.kt + 1) * kKeys > t.least || __any_sync(0xFFFFFFFFu, (f0 | f1) != 0)) {
+    if (__builtin_expect((t.kt + 1) * kKeys > t.least || __any_sync(0xFFFFFFFFu, (f0 | f1) != 0), 0)) {
       const int p = t.kt * kKeys + key0;
 #pragma unroll
       for (int j = 0; j < kG; ++j)
@@ -796,7 +800,7 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
       const uint32_t o = g - L::kPBufs;
       wait(bars + 8 * (L::kPvDone + (o & 1)), (o >> 1) & 1);
     }
-    if (grown) {
+    if (__builtin_expect(grown, 0)) {
       // maximum over the tile's 64 keys: in the warp, then across the four warps
       float* mine = red + warp * kC;
       float* fac = red + (L::kSoftWarps + warp) * kC;
@@ -897,7 +901,7 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
     tc::fence_before_sync();
     __syncwarp();
     if (lane == 0) mbar_arrive(bars + 8 * (L::kPFull + b));
-    if (!t.last) continue;
+    if (__builtin_expect(!t.last, 1)) continue;
 
     // ---- the end of this CTA's run of the query tile
     wait(bars + 8 * (L::kPvDone + b), (g >> 1) & 1);
