@@ -383,34 +383,37 @@ __device__ __forceinline__ void split_q(const LatentAttnArgs& a, const Tile& q, 
 #pragma unroll 1
   for (int r = pw * 4 + (lane >> 3); r < NR; r += kProdWarps * 4) {
     const uint32_t row = (uint32_t)q.qt * NR + r;
-    uint4 v[9] = {};
-    if (row < rows) {
-      const int tok = token_of(a, row);
-      const int64_t t = q.t0 + tok, h = (int)row - tok * a.num_heads;
-      const uint8_t* c = a.q_c + t * a.qc_ts + h * a.qc_hs + col * 16;
-#pragma unroll
-      for (int ch = 0; ch < 8; ++ch) v[ch] = ld_stream16(c + ch * 128);
-      v[8] = ld_stream16(a.q_pe + t * a.qp_ts + h * a.qp_hs + col * 16);
-    }
+    const bool ok = row < rows;
+    const int tok = ok ? token_of(a, row) : 0;
+    const int64_t t = ok ? q.t0 + tok : 0, h = ok ? (int)row - tok * a.num_heads : 0;
+    const uint8_t* c = a.q_c + t * a.qc_ts + h * a.qc_hs + col * 16;
+    const uint8_t* pe = a.q_pe + t * a.qp_ts + h * a.qp_hs + col * 16;
+    // once for the largest magnitude, and again (from L1) to split
     uint32_t top = 0;
+    {
+      uint4 v[9];
 #pragma unroll
-    for (int ch = 0; ch < 9; ++ch)
-      top = umax16x2(top, umax16x2(umax16x2(v[ch].x & 0x7FFF7FFFu, v[ch].y & 0x7FFF7FFFu),
-                                   umax16x2(v[ch].z & 0x7FFF7FFFu, v[ch].w & 0x7FFF7FFFu)));
-    top = max(top & 0xFFFFu, top >> 16);
+      for (int ch = 0; ch < 9; ++ch) v[ch] = ld_shared_ro16(ch < 8 ? c + ch * 128 : pe);
+#pragma unroll
+      for (int ch = 0; ch < 9; ++ch)
+        top = umax16x2(top, umax16x2(umax16x2(v[ch].x & 0x7FFF7FFFu, v[ch].y & 0x7FFF7FFFu),
+                                     umax16x2(v[ch].z & 0x7FFF7FFFu, v[ch].w & 0x7FFF7FFFu)));
+    }
+    top = ok ? max(top & 0xFFFFu, top >> 16) : 0;
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
     const uint32_t e = max(top >> 7, 8u);  // exponent field of the largest magnitude
-    const float s = __uint_as_float((261u - e) << 23);  // 2^(134 - e)
+    const float s = ok ? __uint_as_float((261u - e) << 23) : 0.0f;  // 2^(134 - e)
     // columns 64 ch + 8 col ..: 8 bytes at byte 64 (ch % 2) + 8 col of chunk ch / 2
     const uint32_t d = dst + r * 128 + 8 * (col & 1);
-#pragma unroll
+#pragma unroll 3
     for (int ch = 0; ch < 9; ++ch) {
-      const uint32_t w[4] = {v[ch].x, v[ch].y, v[ch].z, v[ch].w};
+      const uint4 v = ld_shared_ro16(ch < 8 ? c + ch * 128 : pe);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
       uint32_t p1[4], p2[4];  // two codes each
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float x0 = bf16lo(w[i]) * s, x1 = bf16hi(w[i]) * s;
+        const float x0 = ok ? bf16lo(w[i]) * s : 0.0f, x1 = ok ? bf16hi(w[i]) * s : 0.0f;
         p1[i] = pack_fp8x2<kE4M3>(x0, x1);
         float y0, y1;
         fp8x2_to_f32x2<kE4M3>(p1[i], y0, y1);
@@ -509,18 +512,18 @@ __device__ __forceinline__ void produce(const LatentAttnArgs& a, const CUtensorM
             for (int c = 0; c < L::kChunks; ++c)
               if (has(c)) tc::cp_async16(d + c * kChunk, src ? src + part(c) : a.cache, src != nullptr);
           } else {
-            uint4 v[L::kChunks];
+            // once to look for NaNs and infinities, and again to store
             bool sp = false;
 #pragma unroll
-            for (int c = 0; c < L::kChunks; ++c) {
-              v[c] = src && has(c) ? ld_stream16(src + part(c)) : make_uint4(0, 0, 0, 0);
-              sp |= any_special<FMT>(v[c]);
-            }
+            for (int c = 0; c < L::kChunks; ++c)
+              sp |= any_special<FMT>(src && has(c) ? ld_shared_ro16(src + part(c)) : make_uint4(0, 0, 0, 0));
             const bool drop = __ballot_sync(0xFFFFFFFFu, sp) & (0xFFu << (lane & 24));
             if (drop) flag = kPoison;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < L::kChunks; ++c)
-              if (has(c)) sts16(d + c * kChunk, drop ? make_uint4(0, 0, 0, 0) : v[c]);
+              if (has(c))
+                sts16(d + c * kChunk,
+                      src && !drop ? ld_shared_ro16(src + part(c)) : make_uint4(0, 0, 0, 0));
           }
           if (col == 0) sts_u8(flags + row, flag);
         }
@@ -555,18 +558,23 @@ __device__ __forceinline__ void produce(const LatentAttnArgs& a, const CUtensorM
 }
 
 // --------------------------------------------------------------- matrix issue
-// The whole warp runs this; one elected lane issues.  Stage and query buffer are
-// template arguments, so every descriptor is the shared base plus a constant
-// (computed per instruction in a branch of one lane they cost ~90 cycles each,
-// three times the instruction).
-template <int FMT, int NR, int ST, int QB>
-__device__ __forceinline__ void issue_scores(uint32_t smem, uint32_t tmem, bool one, bool last) {
+// The whole warp runs these; one elected lane issues.  Descriptors are made the
+// same in all lanes (stage and buffer by a shuffle) and their loops have constant
+// bounds without branches inside, so that they live in uniform registers: 5
+// machine instructions and 25 to 50 cycles per product.  (In a branch of one lane
+// it was 90 cycles; an instance per stage and buffer spread the loop over 16 KB
+// of code, and fetching it cost as much again.)
+template <int FMT, int NR>
+__device__ __forceinline__ void issue_scores(uint32_t smem, uint32_t tmem, bool one, int stage,
+                                             int qbuf, int sbuf, bool last) {
   using L = Lay<FMT, NR>;
   constexpr uint32_t kId =
       tc::instr_desc(kKeys, L::kN, false, FMT == kE4M3 ? 0 : 1, L::kF8 ? 0 : 1);
-  const uint64_t ka = tc::smem_desc(smem + ST * L::kTile, 0, 1024);
-  const uint64_t qa = tc::smem_desc(smem + L::q + QB * L::kQ, 0, 1024);
-  const uint32_t d = tmem + (ST & 1) * L::kN;
+  const uint32_t st = __shfl_sync(0xFFFFFFFFu, stage, 0), qb = __shfl_sync(0xFFFFFFFFu, qbuf, 0);
+  const uint32_t sb = __shfl_sync(0xFFFFFFFFu, sbuf, 0);
+  const uint64_t ka = tc::smem_desc(smem + st * L::kTile, 0, 1024);
+  const uint64_t qa = tc::smem_desc(smem + L::q + qb * L::kQ, 0, 1024);
+  const uint32_t d = tmem + sb * L::kN;
   // a k step is 32 bytes of a row
 #pragma unroll 1
   for (int c = 0; c < (L::kF8 ? 4 : 9); ++c)
@@ -582,17 +590,19 @@ __device__ __forceinline__ void issue_scores(uint32_t smem, uint32_t tmem, bool 
     for (int k = 0; k < 2; ++k)
       tc::mma_fp8(one, d, ka + (4 * kChunk >> 4) + 2 * k + 4, qa + (4 * L::kN * 128 >> 4) + 2 * k, kId,
                   true);
-  tc::commit(one, smem + L::bars + 8 * (L::kSFull + (ST & 1)));
-  if (last) tc::commit(one, smem + L::bars + 8 * (L::kQEmpty + QB));
+  tc::commit(one, smem + L::bars + 8 * (L::kSFull + sb));
+  if (last) tc::commit(one, smem + L::bars + 8 * (L::kQEmpty + qb));
 }
-template <int FMT, int NR, int ST>
-__device__ __forceinline__ void issue_outputs(uint32_t smem, uint32_t tmem, bool one, bool first) {
+template <int FMT, int NR>
+__device__ __forceinline__ void issue_outputs(uint32_t smem, uint32_t tmem, bool one, int stage,
+                                              int pbuf, bool first) {
   using L = Lay<FMT, NR>;
   constexpr uint32_t kId = tc::instr_desc(128, L::kN, true, FMT == kE4M3 ? 0 : 1, L::kF8 ? 0 : 1);
+  const uint32_t st = __shfl_sync(0xFFFFFFFFu, stage, 0), pb = __shfl_sync(0xFFFFFFFFu, pbuf, 0);
   // The K tile, MN-major.  128 dims are two bf16 chunks or one fp8 chunk; a k step
   // is 16 keys (2 groups of 8 rows) or 32.
-  const uint64_t va = tc::smem_desc(smem + ST * L::kTile, L::kF8 ? 0 : kChunk, 1024);
-  const uint64_t pa = tc::smem_desc(smem + L::p + (ST & (L::kPBufs - 1)) * L::kP, 0, 1024);
+  const uint64_t va = tc::smem_desc(smem + st * L::kTile, L::kF8 ? 0 : kChunk, 1024);
+  const uint64_t pa = tc::smem_desc(smem + L::p + (pb & (L::kPBufs - 1)) * L::kP, 0, 1024);
   constexpr int kDims = L::kF8 ? kChunk : 2 * kChunk, kStep = L::kF8 ? 4096 : 2048;
 #pragma unroll 1
   for (int b = 0; b < 4; ++b)
@@ -603,8 +613,8 @@ __device__ __forceinline__ void issue_outputs(uint32_t smem, uint32_t tmem, bool
       if constexpr (L::kF8) tc::mma_fp8(one, d, ak, bk, kId, k > 0 || !first);
       else tc::mma_bf16(one, d, ak, bk, kId, k > 0 || !first);
     }
-  tc::commit(one, smem + L::bars + 8 * (L::kEmpty + ST));
-  tc::commit(one, smem + L::bars + 8 * (L::kPvDone + (ST & 1)));
+  tc::commit(one, smem + L::bars + 8 * (L::kEmpty + st));
+  tc::commit(one, smem + L::bars + 8 * (L::kPvDone + pb));
 }
 
 // One warp issues the scores, another the outputs, each as soon as its operands
@@ -636,18 +646,7 @@ __device__ __forceinline__ void score_role(const LatentAttnArgs& a, const Run& r
     // loads in flight).
     if (t.first || !by_box(a, t)) tc::fence_smem_async();
     tc::fence_after_sync();
-    constexpr int kQ1 = L::kQBufs - 1, kS2 = L::kStages - 2, kS3 = L::kStages - 1;
-    if (qb == 0) {
-      if (st == 0) issue_scores<FMT, NR, 0, 0>(smem, tmem, one, t.last);
-      else if (st == 1) issue_scores<FMT, NR, 1, 0>(smem, tmem, one, t.last);
-      else if (st == 2) issue_scores<FMT, NR, kS2, 0>(smem, tmem, one, t.last);
-      else issue_scores<FMT, NR, kS3, 0>(smem, tmem, one, t.last);
-    } else {
-      if (st == 0) issue_scores<FMT, NR, 0, kQ1>(smem, tmem, one, t.last);
-      else if (st == 1) issue_scores<FMT, NR, 1, kQ1>(smem, tmem, one, t.last);
-      else if (st == 2) issue_scores<FMT, NR, kS2, kQ1>(smem, tmem, one, t.last);
-      else issue_scores<FMT, NR, kS3, kQ1>(smem, tmem, one, t.last);
-    }
+    issue_scores<FMT, NR>(smem, tmem, one, st, qb, g & 1, t.last);
     item += t.last;
   }
 }
@@ -670,12 +669,7 @@ __device__ __forceinline__ void output_role(const LatentAttnArgs& a, const Run& 
     if (t.first && item > 0) wait(L::kOFree, item - 1);  // the sums of the query tile before are read
     __syncwarp();
     tc::fence_after_sync();
-    constexpr int kS2 = L::kStages - 2, kS3 = L::kStages - 1;
-    const int st = g % L::kStages;
-    if (st == 0) issue_outputs<FMT, NR, 0>(smem, tmem, one, t.first);
-    else if (st == 1) issue_outputs<FMT, NR, 1>(smem, tmem, one, t.first);
-    else if (st == 2) issue_outputs<FMT, NR, kS2>(smem, tmem, one, t.first);
-    else issue_outputs<FMT, NR, kS3>(smem, tmem, one, t.first);
+    issue_outputs<FMT, NR>(smem, tmem, one, g % L::kStages, g & 1, t.first);
     item += t.last;
   }
 }
@@ -937,6 +931,9 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
     const int dt0 = token_of(a, first + col0), tok0 = t.t0 + dt0;
     const int head0 = (int)(first + col0) - dt0 * a.num_heads;
     const bool lost = waiter.given_up();
+    // where row `lane` of the group goes in out
+    const int dt = token_of(a, head0 + lane), row_h = head0 + lane - dt * a.num_heads;
+    const int64_t row_at = (int64_t)(tok0 + dt) * a.out_ts + (int64_t)row_h * a.out_hs;
     if (lane < kC) {
       float sum = 0.0f;
 #pragma unroll
@@ -949,8 +946,7 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
           ws.m[slot * NR + col0 + lane] = top;
           ws.l[slot * NR + col0 + lane] = sum;
         } else if (a.lse) {
-          const int dt = token_of(a, head0 + lane);
-          a.lse[(int64_t)(tok0 + dt) * a.lse_ts + (int64_t)(head0 + lane - dt * a.num_heads) * a.lse_hs] =
+          a.lse[(int64_t)(tok0 + dt) * a.lse_ts + (int64_t)row_h * a.lse_hs] =
               sum == 0.0f ? -INFINITY : fmaf(top, kLn2, logf(sum));
         }
       }
@@ -981,23 +977,16 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
         if (lost) continue;
         if (whole) {
           // lanes 2 i and 2 i + 1 exchange, so that each holds two neighbouring columns of out
-          int h = head0 + n0 + (lane & 1), tok = token_of(a, h);
-          h -= tok * a.num_heads;
-          tok += tok0;
-          const int d = blk * 128 + w4 * 32 + (lane & ~1);
+          uint8_t* o = a.out + (blk * 128 + w4 * 32 + (lane & ~1)) * 2;
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
             const float v0 = __uint_as_float(r[i]) * mine[n0 + i];
             const float v1 = __uint_as_float(r[i + 1]) * mine[n0 + i + 1];
             const float x = __shfl_xor_sync(0xFFFFFFFFu, (lane & 1) ? v0 : v1, 1);
             const uint32_t w = (lane & 1) ? pack_bf16x2(x, v1) : pack_bf16x2(v0, x);
-            if (n0 + i + (lane & 1) < nv)
-              *reinterpret_cast<uint32_t*>(a.out + (int64_t)tok * a.out_ts + (int64_t)h * a.out_hs + d * 2) = w;
-            h += 2;
-            while (h >= a.num_heads) {
-              h -= a.num_heads;
-              ++tok;
-            }
+            const int n = n0 + i + (lane & 1);
+            const int64_t at = __shfl_sync(0xFFFFFFFFu, row_at, n);
+            if (n < nv) *reinterpret_cast<uint32_t*>(o + at) = w;
           }
         } else {
           // (16 rows of a dim in a run, 16 bytes per store, took three times as long: a
@@ -1039,60 +1028,61 @@ __device__ __forceinline__ int64_t scan64(int64_t v, int lane) {  // inclusive, 
 }
 
 // This CTA's run.  Up to 128 sequences of at most 8 query tiles: every warp finds
-// it by itself (a lane has four sequences), without a barrier.
-constexpr int kLaneSeqs = 4, kLaneTiles = 8;
+// it by itself, 32 sequences at a time, without a barrier.
+constexpr int kSmallSeqs = 128, kSmallTiles = 8;
 template <int NR>
 __device__ __forceinline__ bool schedule_small(const LatentAttnArgs& a, int lane, Run& r,
                                                uint32_t& errbits) {
-  const int per = (a.num_seqs + 31) >> 5;
-  Seq q[kLaneSeqs];
-  int64_t u[kLaneSeqs], sum = 0;
-  bool big = a.num_seqs > 32 * kLaneSeqs;
-#pragma unroll
-  for (int i = 0; i < kLaneSeqs; ++i) {
-    const int s = lane * per + i;
-    q[i].nqt = 0;
-    if (!big && i < per && s < a.num_seqs) q[i] = load_seq<NR>(a, s);
-  }
-#pragma unroll
-  for (int i = 0; i < kLaneSeqs; ++i) {
-    big |= q[i].nqt > kLaneTiles;
-    u[i] = 0;
+  if (a.num_seqs > kSmallSeqs) return false;
+  int64_t before = 0;  // units of the sequences in front of these 32
+  int s = lane;
+  int64_t off = 0;
+  uint32_t has = 0;
+  Seq q;
+  // first round over the sequences: their units; second: the one with the first unit
 #pragma unroll 1
-    for (int qt = 0; qt < min(q[i].nqt, kLaneTiles); ++qt) u[i] += key_tiles(most_seen<NR>(a, q[i], qt));
-    sum += u[i];
-    if (q[i].nqt > 0 && over_room(a, q[i])) errbits |= kErrBlockOOB;
-  }
-  if (__any_sync(0xFFFFFFFFu, big)) return false;
-  const int64_t inc = scan64(sum, lane);
-  cut(__shfl_sync(0xFFFFFFFFu, inc, 31), r);
-  int64_t off = r.begin - (inc - sum);  // the first unit among this lane's
-  const uint32_t has = __ballot_sync(0xFFFFFFFFu, r.count > 0 && off >= 0 && off < sum);
-  if (has == 0) return true;
-  int s = lane * per, qt = 0, kt = 0;
-  Seq qq = q[0];
-#pragma unroll
-  for (int i = 0; i + 1 < kLaneSeqs; ++i)
-    if (s == lane * per + i && off >= u[i]) {
-      off -= u[i];
-      ++s;
-      qq = q[i + 1];
+  for (int round = 0, base = 0;; ) {
+    s = base + lane;
+    q.nqt = 0;
+    if (s < a.num_seqs) q = load_seq<NR>(a, s);
+    if (__any_sync(0xFFFFFFFFu, q.nqt > kSmallTiles)) return false;
+    int64_t u = 0;
+#pragma unroll 1
+    for (int qt = 0; qt < q.nqt; ++qt) u += key_tiles(most_seen<NR>(a, q, qt));
+    const int64_t inc = scan64(u, lane);
+    if (round == 1) {
+      off = r.begin - before - (inc - u);
+      has = __ballot_sync(0xFFFFFFFFu, off >= 0 && off < u);
+      if (has != 0) break;
+    } else if (q.nqt > 0 && over_room(a, q)) {
+      errbits |= kErrBlockOOB;
     }
+    before += __shfl_sync(0xFFFFFFFFu, inc, 31);
+    base += 32;
+    if (base >= a.num_seqs) {
+      if (round == 1) return true;  // (not reached: some sequence has the unit)
+      cut(before, r);
+      if (r.count == 0) return true;
+      round = 1;
+      base = 0;
+      before = 0;
+    }
+  }
+  int qt = 0;
   if (has >> lane & 1) {
 #pragma unroll 1
     for (;; ++qt) {
-      const int k = key_tiles(most_seen<NR>(a, qq, qt));
+      const int k = key_tiles(most_seen<NR>(a, q, qt));
       if (off < k) break;
       off -= k;
     }
-    kt = (int)off;
   }
   const int from = __ffs(has) - 1;
   auto all = [&](int v) { return __shfl_sync(0xFFFFFFFFu, v, from); };
   r.s = all(s);
   r.qt = all(qt);
-  r.kt = all(kt);
-  r.q = Seq{all(qq.t0), all(qq.ntok), all(qq.c1), all(qq.kv), all(qq.nqt)};
+  r.kt = all((int)off);
+  r.q = Seq{all(q.t0), all(q.ntok), all(q.c1), all(q.kv), all(q.nqt)};
   return true;
 }
 
