@@ -906,6 +906,8 @@ mla_status_t mla_merge_attn_states(
     return fail(MLA_ERR_INVALID_ARG, "dtype must be MLA_BF16, MLA_FP16 or MLA_FP32; got %d",
                 (int)dtype);
   const int es = dtype == MLA_FP32 ? 4 : 2;
+  if ((int64_t)num_heads * ((int64_t)dim * es / 16) > (int64_t(1) << 30))
+    return fail(MLA_ERR_UNSUPPORTED, "num_heads * dim is too large for one call");
   if (!m16((int64_t)dim * es))
     return fail(MLA_ERR_MISALIGNED, "dim must span a multiple of 16 bytes");
   if (!a16(parts) || !m16(part_stride * es) || !m16(token_stride * es) || !m16(head_stride * es))
@@ -934,6 +936,8 @@ mla_status_t mla_merge_attn_states(
   a.num_tokens = num_tokens;
   a.num_heads = num_heads;
   a.row_chunks = (int32_t)((int64_t)dim * es / 16);
+  a.by_chunks = mla::Divider::by((uint32_t)a.row_chunks);
+  a.by_heads = mla::Divider::by((uint32_t)num_heads);
   a.out = static_cast<uint8_t*>(out);
   a.ots = out_token_stride * es;
   a.ohs = out_head_stride * es;
@@ -1024,10 +1028,7 @@ mla_status_t mla_latent_attention(
   a.qp_hs = qpe_head_stride * 2;
   a.num_tokens = num_tokens;
   a.num_heads = num_heads;
-  // division by an invariant integer using multiplication (Granlund and
-  // Montgomery, PLDI 1994): shift = ceil(log2 d), mul = floor(2^32 (2^shift - d) / d) + 1
-  while ((int64_t(1) << a.heads_shift) < num_heads) ++a.heads_shift;
-  a.heads_mul = (uint32_t)((((uint64_t(1) << a.heads_shift) - num_heads) << 32) / num_heads + 1);
+  a.by_heads = mla::Divider::by((uint32_t)num_heads);
   a.cache = static_cast<const uint8_t*>(kv_cache);
   a.block_stride = block_stride * ce;
   a.entry_stride = entry_stride * ce;

@@ -125,10 +125,13 @@ struct Misc {
 };
 static_assert(sizeof(Misc) <= 64, "Misc fits");
 
-// A query tile that CTA c starts and others go on with: rows first_row .. of the
-// sequence, the partials of the CTAs c .. c + parts - 1 (rows 0: none).
+// What the join needs of a split query tile: token and head of its first row, its
+// rows, and the CTAs with partials, first .. first + parts - 1.  Written by each of
+// them but the last (whose run goes on with other query tiles); rows 0: none.
 struct Split {
-  int32_t tok0, head0, rows, parts;
+  int32_t tok0, head0;
+  uint16_t rows, parts;
+  int32_t first;
 };
 
 struct Seq {
@@ -137,9 +140,9 @@ struct Seq {
   int32_t nqt;       // query tiles
 };
 
-// Token of a sequence's query row (row < 2^31), by the reciprocal of num_heads.
+// Token of a sequence's query row (row < 2^31).
 __device__ __forceinline__ int token_of(const LatentAttnArgs& a, uint32_t row) {
-  return (int)((__umulhi(row, a.heads_mul) + row) >> a.heads_shift);
+  return (int)a.by_heads(row);
 }
 
 template <int NR>
@@ -689,9 +692,10 @@ __host__ __device__ inline Workspace workspace_of(uint8_t* p, int ctas) {
   w.o = w.l + (int64_t)ctas * 2 * NR;
   return w;
 }
-// n / d where both mostly fit 32 bits.
-__device__ __forceinline__ int quotient(int64_t n, int64_t d) {
-  return ((n | d) >> 32) == 0 ? (int)((uint32_t)n / (uint32_t)d) : (int)(n / d);
+// The CTA whose run has unit u.
+__device__ __noinline__ int cta_of(int64_t u, int64_t each, int extra) {
+  const int64_t longer = (each + 1) * extra;  // units of the runs of each + 1
+  return (int)(u < longer ? u / (each + 1) : extra + (u - longer) / each);
 }
 
 template <int FMT, int NR>
@@ -940,25 +944,24 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
       for (int w = 0; w < 4; ++w)
         sum += red[(group * 4 + w) * kC + lane];
       const float top = mine[lane];
-      mine[lane] = sum == 0.0f ? 0.0f : ks / sum;
+      mine[lane] = sum == 0.0f ? 0.0f : __fdividef(ks, sum);
       if (w4 == 0 && lane < nv && !lost) {
         if (!whole) {
           ws.m[slot * NR + col0 + lane] = top;
           ws.l[slot * NR + col0 + lane] = sum;
         } else if (a.lse) {
           a.lse[(int64_t)(tok0 + dt) * a.lse_ts + (int64_t)row_h * a.lse_hs] =
-              sum == 0.0f ? -INFINITY : fmaf(top, kLn2, logf(sum));
+              sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * kLn2;
         }
       }
     }
     __syncwarp();
-    if (!whole && kt_begin == 0 && warp == 0 && lane == 0 && !lost) {
-      // the CTA of the query tile's last unit
-      const int64_t u1 = run.begin + run.count - 1 + (t.nkt - 1 - t.kt);
-      const int64_t long_end = (run.each + 1) * run.extra;
-      const int last = u1 < long_end ? quotient(u1, run.each + 1)
-                                     : run.extra + quotient(u1 - long_end, run.each);
-      ws.split[blockIdx.x] = Split{tok0, head0, rows, last - (int)blockIdx.x + 1};
+    if (t.kt + 1 < t.nkt && warp == 0 && lane == 0 && !lost) {
+      // units of the query tile: this run's last one is number t.kt of them
+      const int64_t u0 = run.begin + run.count - 1 - t.kt;
+      const int c0 = cta_of(u0, run.each, run.extra);
+      const int c1 = cta_of(u0 + t.nkt - 1, run.each, run.extra);
+      ws.split[blockIdx.x] = Split{tok0, head0, (uint16_t)rows, (uint16_t)(c1 - c0 + 1), c0};
     }
 #pragma unroll 1
     for (int n0 = 0; n0 < nv; n0 += 16) {
@@ -1008,12 +1011,13 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
 // ------------------------------------------------------------------ the kernel
 // The runs of `total` units: the first `extra` CTAs take one unit more than the
 // others; fewer CTAs than the grid has when each would get less than kMinUnits.
+__device__ __noinline__ int64_t divide(int64_t n, int64_t d) { return n / d; }
 __device__ __forceinline__ void cut(int64_t total, Run& r) {
   const uint32_t ctas = total >= (int64_t)gridDim.x * kMinUnits
                             ? gridDim.x
                             : max(1u, (uint32_t)total / (uint32_t)kMinUnits);
   if ((total >> 32) == 0) r.each = (uint32_t)total / ctas;
-  else r.each = total / ctas;
+  else r.each = divide(total, ctas);
   r.extra = (int)(total - r.each * ctas);
   r.begin = r.each * blockIdx.x + min((int)blockIdx.x, r.extra);
   r.count = blockIdx.x < ctas ? (int)r.each + ((int)blockIdx.x < r.extra ? 1 : 0) : 0;
@@ -1195,7 +1199,7 @@ __global__ void __launch_bounds__(Lay<FMT, NR>::kThreads, 1)
   const Waiter wait{smem_addr(&m.abort), a.wait_limit_ns};
   pdl_wait();
   const Workspace ws = workspace_of<NR>(a.workspace, gridDim.x);
-  if (threadIdx.x == 0) ws.split[blockIdx.x] = Split{0, 0, 0, 0};
+  if (threadIdx.x == 0) ws.split[blockIdx.x] = Split{0, 0, 0, 0, 0};
   uint32_t errbits = 0;
   Run run;
   if (!schedule_small<NR>(a, lane, run, errbits)) {
@@ -1228,118 +1232,83 @@ __global__ void __launch_bounds__(Lay<FMT, NR>::kThreads, 1)
 }
 
 // ---------------------------------------------------- join of the split query tiles
-// A step is one row of a split: 128 threads, four dims each.  With up to kFewParts
-// partials the block's four groups of 128 threads take four rows; with more they
-// share one, a quarter of the partials each, added in order.  The steps of all
-// splits are dealt to the blocks in turn.
+// Block (r, c) looks at what CTA c left.  With up to kFewParts partials the blocks
+// of the first CTA take four rows each, one per group of 128 threads (four dims a
+// thread); with more, the blocks of all its CTAs but the last take a row each, a
+// group a quarter of the partials.  (There are at least as many of them as rows:
+// kFewParts * NR / 4.)  So a block costs two dependent loads, whatever the batch.
 constexpr int kJoinGroups = 4;
 constexpr int kJoinThreads = kJoinGroups * 128;
 constexpr int kFewParts = 8;
 constexpr int kMaxCtas = 1024;
 
 template <int FMT, int NR>
-__global__ void __launch_bounds__(kJoinThreads, 2) latent_join_kernel(const LatentAttnArgs a, int ctas) {
-  __shared__ int ends[kMaxCtas];  // steps of the splits up to c
-  __shared__ int warp_sum_s[kJoinThreads / 32];
+__global__ void __launch_bounds__(kJoinThreads, 2) latent_join_kernel(const LatentAttnArgs a) {
   __shared__ float4 acc_s[kJoinGroups][128];
   __shared__ float2 sum_s[kJoinGroups];
   pdl_trigger();
   pdl_wait();
-  const Workspace ws = workspace_of<NR>(a.workspace, ctas);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int grp = tid >> 7, d4 = tid & 127;
-  // steps of each split, and their running sums
-  int total = 0;
-#pragma unroll 1
-  for (int c0 = 0; c0 < ctas; c0 += kJoinThreads) {
-    const Split sp = c0 + tid < ctas ? ws.split[c0 + tid] : Split{0, 0, 0, 0};
-    int v = sp.parts > kFewParts ? sp.rows : (sp.rows + kJoinGroups - 1) / kJoinGroups;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xFFFFFFFFu, v, o);
-      if (lane >= o) v += u;
-    }
-    if (lane == 31) warp_sum_s[warp] = v;
-    __syncthreads();
-    int sum = 0;
-#pragma unroll 1
-    for (int w = 0; w < kJoinThreads / 32; ++w) {
-      if (w < warp) v += warp_sum_s[w];
-      sum += warp_sum_s[w];
-    }
-    if (c0 + tid < ctas) ends[c0 + tid] = total + v;
-    total += sum;
-    __syncthreads();
-  }
+  const Workspace ws = workspace_of<NR>(a.workspace, gridDim.y);
+  const int grp = threadIdx.x >> 7, d4 = threadIdx.x & 127;
+  const Split sp = ws.split[blockIdx.y];
+  const int c = sp.first;
+  const bool few = sp.parts <= kFewParts;
+  const int n = few ? blockIdx.x * kJoinGroups + grp
+                    : ((int)blockIdx.y - c) * (NR / kJoinGroups) + (int)blockIdx.x;
+  if (few && (int)blockIdx.y != c) return;
+  if (n >= sp.rows) return;  // the whole group, and the whole block when it is shared
   const float ks = FMT == kBF16 ? 1.0f : __ldg(a.k_scale);
+  float4 acc = make_float4(0, 0, 0, 0);
+  float sum = 0.0f, top = -INFINITY;
+  // joins `v` with weight sum lv and maximum mv to what is there
+  auto add = [&](const float4& v, float lv, float mv) {
+    const float m = fmaxf(top, mv), m0 = m == -INFINITY ? 0.0f : m;
+    const float f = ex2(top - m0), w = ex2(mv - m0);
+    acc.x = fmaf(acc.x, f, w * v.x);
+    acc.y = fmaf(acc.y, f, w * v.y);
+    acc.z = fmaf(acc.z, f, w * v.z);
+    acc.w = fmaf(acc.w, f, w * v.w);
+    sum = fmaf(sum, f, w * lv);
+    top = m;
+  };
+  // the first partial lies in the odd slot of CTA c, the others in the even ones behind
+  const int quarter = (sp.parts + kJoinGroups - 1) / kJoinGroups;
+  const int i0 = few ? 0 : min(grp * quarter, (int)sp.parts);
+  const int i1 = few ? sp.parts : min(i0 + quarter, (int)sp.parts);
 #pragma unroll 1
-  for (int step = blockIdx.x; step < total; step += gridDim.x) {
-    int lo = 0, hi = ctas - 1;  // the split: the first with ends[c] > step
-#pragma unroll 1
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (ends[mid] > step) hi = mid;
-      else lo = mid + 1;
-    }
-    const int c = lo, in = step - (c > 0 ? ends[c - 1] : 0);
-    const Split sp = ws.split[c];
-    const bool shared = sp.parts > kFewParts;
-    const int n = shared ? in : in * kJoinGroups + grp;
-    float4 acc = make_float4(0, 0, 0, 0);
-    float sum = 0.0f, top = -INFINITY;
-    // joins `v` with weight sum lv and maximum mv to what is there
-    auto add = [&](const float4& v, float lv, float mv) {
-      const float m = fmaxf(top, mv), m0 = m == -INFINITY ? 0.0f : m;
-      const float f = ex2(top - m0), w = ex2(mv - m0);
-      acc.x = fmaf(acc.x, f, w * v.x);
-      acc.y = fmaf(acc.y, f, w * v.y);
-      acc.z = fmaf(acc.z, f, w * v.z);
-      acc.w = fmaf(acc.w, f, w * v.w);
-      sum = fmaf(sum, f, w * lv);
-      top = m;
-    };
-    // the first partial lies in the odd slot of CTA c, the others in the even ones behind
-    const int quarter = (sp.parts + kJoinGroups - 1) / kJoinGroups;
-    const int i0 = shared ? min(grp * quarter, sp.parts) : 0;
-    const int i1 = n >= sp.rows ? i0 : shared ? min(i0 + quarter, sp.parts) : sp.parts;
-#pragma unroll 1
-    for (int i = i0; i < i1; i += 8) {
-      float4 v[8];
-      float lv[8], mv[8];
+  for (int i = i0; i < i1; i += 4) {
+    float4 v[4];
+    float lv[4], mv[4];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int64_t row = (2 * (int64_t)(c + i + k) + (i + k == 0 ? 1 : 0)) * NR + n;
-        v[k] = make_float4(0, 0, 0, 0);
-        lv[k] = 0.0f;
-        mv[k] = -INFINITY;
-        if (i + k < i1) {
-          v[k] = __ldcs(reinterpret_cast<const float4*>(ws.o + row * kRank) + d4);
-          lv[k] = ws.l[row];
-          mv[k] = ws.m[row];
-        }
+    for (int k = 0; k < 4; ++k) {
+      const int64_t row = (2 * (int64_t)(c + i + k) + (i + k == 0 ? 1 : 0)) * NR + n;
+      v[k] = make_float4(0, 0, 0, 0);
+      lv[k] = 0.0f;
+      mv[k] = -INFINITY;
+      if (i + k < i1) {
+        v[k] = __ldcs(reinterpret_cast<const float4*>(ws.o + row * kRank) + d4);
+        lv[k] = ws.l[row];
+        mv[k] = ws.m[row];
       }
+    }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) add(v[k], lv[k], mv[k]);
-    }
-    if (shared) {
-      acc_s[grp][d4] = acc;
-      if (d4 == 0) sum_s[grp] = make_float2(sum, top);
-      __syncthreads();
-      if (grp == 0)
-#pragma unroll 1
-        for (int k = 1; k < kJoinGroups; ++k) add(acc_s[k][d4], sum_s[k].x, sum_s[k].y);
-      __syncthreads();
-      if (grp != 0) continue;
-    }
-    if (n >= sp.rows) continue;
-    const int dt = token_of(a, sp.head0 + n);
-    const int64_t t = sp.tok0 + dt, h = sp.head0 + n - dt * a.num_heads;
-    const float inv = sum == 0.0f ? 0.0f : ks / sum;
-    st8(a.out + t * a.out_ts + h * a.out_hs + d4 * 8,
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv)));
-    if (d4 == 0 && a.lse)
-      a.lse[t * a.lse_ts + h * a.lse_hs] = sum == 0.0f ? -INFINITY : fmaf(top, kLn2, logf(sum));
+    for (int k = 0; k < 4; ++k) add(v[k], lv[k], mv[k]);
   }
+  if (!few) {
+    acc_s[grp][d4] = acc;
+    if (d4 == 0) sum_s[grp] = make_float2(sum, top);
+    __syncthreads();
+    if (grp != 0) return;
+#pragma unroll 1
+    for (int k = 1; k < kJoinGroups; ++k) add(acc_s[k][d4], sum_s[k].x, sum_s[k].y);
+  }
+  const int dt = token_of(a, sp.head0 + n);
+  const int64_t t = sp.tok0 + dt, h = sp.head0 + n - dt * a.num_heads;
+  const float inv = sum == 0.0f ? 0.0f : __fdividef(ks, sum);
+  st8(a.out + t * a.out_ts + h * a.out_hs + d4 * 8,
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv)));
+  if (d4 == 0 && a.lse)
+    a.lse[t * a.lse_ts + h * a.lse_hs] = sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * kLn2;
 }
 
 // Rows of a query tile: the average rows (tokens x heads) per sequence decide.
@@ -1407,10 +1376,10 @@ cudaError_t launch_t(const LatentAttnArgs& a, const CUtensorMap& map, int ctas,
   lc.numAttrs = cfg.pdl ? 1 : 0;
   e = cudaLaunchKernelEx(&lc, kern, a, map);
   if (e != cudaSuccess) return e;
-  lc.gridDim = dim3(2 * ctas);
+  lc.gridDim = dim3(NR / kJoinGroups, ctas);
   lc.blockDim = dim3(kJoinThreads);
   lc.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&lc, latent_join_kernel<FMT, NR>, a, ctas);
+  return cudaLaunchKernelEx(&lc, latent_join_kernel<FMT, NR>, a);
 }
 
 template <int FMT>

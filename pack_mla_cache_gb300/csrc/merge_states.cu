@@ -11,7 +11,10 @@
 // Design: a thread owns one 16-byte chunk of an output row.  The lse of its
 // row are read twice (for m, then for the weights); the threads of a row read
 // the same words, so the second pass and all but one thread's first hit L1.
-// Parts are taken four at a time, their loads issued before their sums.
+// Parts are taken four at a time, their loads issued before their sums; the first
+// four parts' before the lse are looked at.  Row, token and head of a chunk come
+// from multiplications by reciprocals (with 64-bit divisions 4 parts of 8192 x 16
+// rows of 128 took 39 us).
 #include "mla_device.cuh"
 #include "mla_internal.h"
 
@@ -47,15 +50,16 @@ __global__ void __launch_bounds__(kThreads) merge_states_kernel(const MergeArgs 
   constexpr int kElts = F == kF32 ? 4 : 8;  // elements of a 16-byte chunk
   pdl_trigger();
   pdl_wait();
-  const int64_t chunks = (int64_t)a.num_tokens * a.num_heads * a.row_chunks;
-  for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < chunks;
-       u += (int64_t)gridDim.x * kThreads) {
-    const int64_t row = u / a.row_chunks;
-    const int32_t ch = (int32_t)(u - row * a.row_chunks);
-    const int64_t t = row / a.num_heads;
-    const int32_t h = (int32_t)(row - t * a.num_heads);
-    const float* lse = a.lse + t * a.lts + h * a.lhs;
-    const uint8_t* src = a.parts + t * a.ts + h * a.hs + (int64_t)ch * 16;
+  const uint32_t chunks = (uint32_t)a.num_tokens * a.num_heads * a.row_chunks;  // < 2^31
+  for (uint32_t u = blockIdx.x * kThreads + threadIdx.x; u < chunks; u += gridDim.x * kThreads) {
+    const uint32_t row = a.by_chunks(u), ch = u - row * a.row_chunks;
+    const uint32_t t = a.by_heads(row), h = row - t * a.num_heads;
+    const float* lse = a.lse + (int64_t)t * a.lts + (int64_t)h * a.lhs;
+    const uint8_t* src = a.parts + (int64_t)t * a.ts + (int64_t)h * a.hs + (int64_t)ch * 16;
+    uint4 v[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (k < a.num_parts) v[k] = ld_stream16(src + k * a.ps);
     float m = -INFINITY, bad = 0.0f;
     for (int i = 0; i < a.num_parts; ++i) {
       const float x = __ldg(lse + i * a.lps);
@@ -67,26 +71,22 @@ __global__ void __launch_bounds__(kThreads) merge_states_kernel(const MergeArgs 
 #pragma unroll
     for (int e = 0; e < kElts; ++e) acc[e] = 0.0f;
     float sum = 0.0f;
-    for (int i0 = 0; i0 < a.num_parts; i0 += kBatch) {
-      uint4 v[kBatch];
-      float w[kBatch];
+    for (int i0 = 0;; i0 += kBatch) {
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        w[k] = 0.0f;
-        v[k] = make_uint4(0, 0, 0, 0);
         if (i0 + k < a.num_parts) {
           const float x = __ldg(lse + (i0 + k) * a.lps);
-          if (x != -INFINITY) {
-            v[k] = ld_stream16(src + (i0 + k) * a.ps);
-            w[k] = expf(x - m0);
+          if (x != -INFINITY) {  // a part without weight has no influence, whatever it holds
+            const float w = expf(x - m0);
+            sum += w;
+            add_weighted<F>(v[k], w, acc);
           }
         }
       }
+      if (i0 + kBatch >= a.num_parts) break;
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        sum += w[k];
-        add_weighted<F>(v[k], w[k], acc);
-      }
+      for (int k = 0; k < kBatch; ++k)
+        if (i0 + kBatch + k < a.num_parts) v[k] = ld_stream16(src + (i0 + kBatch + k) * a.ps);
     }
     const float inv = (sum > 0.0f ? __frcp_rn(sum) : 0.0f) + bad;
     uint4 o;
@@ -100,17 +100,15 @@ __global__ void __launch_bounds__(kThreads) merge_states_kernel(const MergeArgs 
       o = make_uint4(pack_f16x2(acc[0] * inv, acc[1] * inv), pack_f16x2(acc[2] * inv, acc[3] * inv),
                      pack_f16x2(acc[4] * inv, acc[5] * inv), pack_f16x2(acc[6] * inv, acc[7] * inv));
     }
-    st16(a.out + t * a.ots + h * a.ohs + (int64_t)ch * 16, o);
-    if (ch == 0 && a.lse_out) a.lse_out[t * a.lots + h * a.lohs] = m0 + logf(sum) + bad;
+    st16(a.out + (int64_t)t * a.ots + (int64_t)h * a.ohs + (int64_t)ch * 16, o);
+    if (ch == 0 && a.lse_out)
+      a.lse_out[(int64_t)t * a.lots + (int64_t)h * a.lohs] = m0 + logf(sum) + bad;
   }
 }
 
 template <int F>
-cudaError_t launch_t(const MergeArgs& a, const LaunchCfg& cfg) {
-  const int64_t chunks = (int64_t)a.num_tokens * a.num_heads * a.row_chunks;
+cudaError_t launch_t(MergeArgs a, const LaunchCfg& cfg) {
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3(capped_grid(reinterpret_cast<const void*>(merge_states_kernel<F>), kThreads,
-                                (chunks + kThreads - 1) / kThreads));
   lc.blockDim = dim3(kThreads);
   lc.stream = cfg.stream;
   cudaLaunchAttribute attr[1];
@@ -118,7 +116,23 @@ cudaError_t launch_t(const MergeArgs& a, const LaunchCfg& cfg) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = attr;
   lc.numAttrs = cfg.pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&lc, merge_states_kernel<F>, a);
+  // chunk numbers stay below 2^31 - 2^24 (the last stride of the grid included): larger
+  // calls, of many GiB, go in several launches
+  const int64_t per_token = (int64_t)a.num_heads * a.row_chunks;
+  const int32_t most = (int32_t)((INT32_MAX - (1 << 24)) / per_token), tokens = a.num_tokens;
+  for (int32_t t0 = 0; t0 < tokens; t0 += most) {
+    a.num_tokens = tokens - t0 < most ? tokens - t0 : most;
+    const int64_t chunks = a.num_tokens * per_token;
+    lc.gridDim = dim3(capped_grid(reinterpret_cast<const void*>(merge_states_kernel<F>), kThreads,
+                                  (chunks + kThreads - 1) / kThreads));
+    const cudaError_t e = cudaLaunchKernelEx(&lc, merge_states_kernel<F>, a);
+    if (e != cudaSuccess) return e;
+    a.parts += most * a.ts;
+    a.lse += most * a.lts;
+    a.out += most * a.ots;
+    if (a.lse_out) a.lse_out += most * a.lots;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace

@@ -125,6 +125,24 @@ struct CopyBlocksArgs {
   uint32_t* err;
 };
 
+// Division by an invariant d >= 1 using multiplication (Granlund and Montgomery,
+// PLDI 1994): shift = ceil(log2 d), mul = floor(2^32 (2^shift - d) / d) + 1; exact
+// for n < 2^31 (the sum below stays in 32 bits).
+struct Divider {
+  uint32_t mul, shift;
+  static Divider by(uint32_t d) {
+    Divider r{0, 0};
+    while ((uint64_t(1) << r.shift) < d) ++r.shift;
+    r.mul = (uint32_t)((((uint64_t(1) << r.shift) - d) << 32) / d + 1);
+    return r;
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
+    return (__umulhi(n, mul) + n) >> shift;
+  }
+#endif
+};
+
 // Join of partial attention results (bytes; lse strides in elements).
 struct MergeArgs {
   const uint8_t* parts;
@@ -133,6 +151,7 @@ struct MergeArgs {
   int64_t lps, lts, lhs;
   int32_t num_parts, num_tokens, num_heads;
   int32_t row_chunks;  // 16-byte chunks of a row
+  Divider by_chunks, by_heads;
   uint8_t* out;
   int64_t ots, ohs;
   float* lse_out;  // may be null
@@ -146,7 +165,7 @@ struct LatentAttnArgs {
   const uint8_t* q_pe;
   int64_t qp_ts, qp_hs;
   int32_t num_tokens, num_heads;
-  uint32_t heads_mul, heads_shift;  // n / num_heads = (mulhi(n, mul) + n) >> shift, n < 2^31
+  Divider by_heads;
   const uint8_t* cache;
   int64_t block_stride, entry_stride, num_blocks;
   int32_t block_size, bs_shift;  // bs_shift = log2(block_size) or -1
