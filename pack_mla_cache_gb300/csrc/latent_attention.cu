@@ -88,8 +88,8 @@ struct Lay {
   static constexpr int kStages = kF8 ? 4 : 2;
   static constexpr int kQBufs = NR <= (kF8 ? 16 : 32) ? 2 : 1;
   static constexpr int kQ = kChunks * kN * 128;
-  static constexpr int kSoftWarps = NR == 64 ? 8 : 4;   // 4 warps per 32 query rows
-  static constexpr int kCols = NR == 64 ? 32 : NR;      // query rows of a group of 4 warps
+  static constexpr int kSoftWarps = NR == 16 ? 4 : 8;   // one or two groups of 4 warps
+  static constexpr int kCols = NR / (kSoftWarps / 4);   // query rows of a group
   static constexpr int kScoreWarp = kSoftWarps;         // issues the scores' products
   static constexpr int kOutWarp = kScoreWarp + 1;       // and the outputs'
   static constexpr int kProdWarp = kOutWarp + 1;
@@ -443,14 +443,16 @@ __device__ __forceinline__ void produce(const LatentAttnArgs& a, const CUtensorM
   Walk<NR> walk;
   walk.start(run);
   // Row copies: 8 lanes x 16 bytes per row and chunk; this thread has the rows
-  // pw * 16 + 4 i + lane / 8.  Boxes: box_rows keys x one chunk; the first warp's
-  // lane l has the boxes of keys (l % boxes) * box_rows.
+  // pw * 16 + 4 i + lane / 8.
   constexpr int kRows = 4;
   const int row0 = pw * 16 + (lane >> 3), col = lane & 7;
-  const int boxes = a.box_rows ? kKeys / a.box_rows : 0;
-  const int box = boxes ? lane & (boxes - 1) : 0;
-  const int box_chunk = boxes ? lane / boxes : 0, box_step = boxes ? 32 / boxes : 1;
-  const int box_word = boxes ? (lane & 15) * 4 / a.box_rows : 0;  // the box of flag word `lane`
+  // Boxes of box_rows keys x one chunk, `boxes` per chunk: number pw + 4 lane is this
+  // thread's (at most 72; issuing one takes ~100 cycles, so the four warps share
+  // them).  Lanes 28 to 31 write the flags of the warp's 16 keys, four each.
+  const int boxes = a.box_rows ? kKeys / a.box_rows : 1;
+  const int box = (pw + 4 * lane) & (boxes - 1), box_chunk = (pw + 4 * lane) / boxes;
+  const uint32_t box_bytes = (uint32_t)((boxes * L::kChunks - pw + 3) >> 2) * a.box_rows * 128;
+  const int box_key = lane < 28 ? box * a.box_rows : pw * 16 + 4 * (lane - 28);
   // Blocks are looked up two tiles ahead.
   Tile cur{}, nxt{};
   int32_t blk[kRows] = {}, nblk[kRows] = {};
@@ -460,7 +462,7 @@ __device__ __forceinline__ void produce(const LatentAttnArgs& a, const CUtensorM
     const Tile far = walk.next(a);
     int32_t fblk[kRows];
     if (__builtin_expect(by_box(a, far), 1)) {
-      fblk[0] = pw == 0 ? find_block(a, far, far.kt * kKeys + box * a.box_rows) : kUnseen;
+      fblk[0] = find_block(a, far, far.kt * kKeys + box_key);
     } else {
 #pragma unroll
       for (int i = 0; i < kRows; ++i) fblk[i] = find_block(a, far, far.kt * kKeys + row0 + 4 * i);
@@ -473,27 +475,22 @@ __device__ __forceinline__ void produce(const LatentAttnArgs& a, const CUtensorM
       __syncwarp();
       const uint32_t base = smem + st * L::kTile;
       if (__builtin_expect(by_box(a, cur), 1)) {
-        if (pw == 0) {
-          const bool ok = blk[0] >= 0 && blk[0] < a.num_blocks;
-          if (!ok) errbits |= kErrBlockOOB;
-          const uint32_t none = __shfl_sync(0xFFFFFFFFu, ok ? 0u : 0x01010101u * kAbsent,
-                                            box_word);
-          if (lane < 16) sts_u32(flags + 4 * lane, none);
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive_expect_tx(full, L::kTile);
-            mbar_arrive_n(full, 32);
-          }
-          __syncwarp();
-          const int p = cur.kt * kKeys + box * a.box_rows;
+        const bool ok = blk[0] >= 0 && blk[0] < a.num_blocks;
+        if (!ok) errbits |= kErrBlockOOB;
+        if (lane >= 28) sts_u32(flags + box_key, ok ? 0u : 0x01010101u * kAbsent);
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_expect_tx(full, box_bytes);
+          mbar_arrive_n(full, 32);
+        }
+        __syncwarp();
+        if (box_chunk < L::kChunks) {
+          const int p = cur.kt * kKeys + box_key;
           const int off = a.bs_shift >= 0 ? p & (a.block_size - 1) : p % a.block_size;
           const int z = ok ? blk[0] : (int)a.num_blocks;  // outside the tensor: zeros
-          const uint32_t to = base + box * a.box_rows * 128;
-          for (int i = box_chunk; i < L::kChunks; i += box_step)
-            tc::tma_load3(to + i * kChunk, &map, L::kF8 ? (i < 4 ? i * 128 : 448) : i * 64, off, z,
-                          full);
-        } else if (lane == 0) {
-          mbar_arrive_n(full, 33);
+          tc::tma_load3(base + box_chunk * kChunk + box_key * 128, &map,
+                        L::kF8 ? (box_chunk < 4 ? box_chunk * 128 : 448) : box_chunk * 64, off, z,
+                        full);
         }
       } else {
         // tokens of the query tile see different rows of this key tile
@@ -878,7 +875,7 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
             float uh, vh;
             fp8x2_to_f32x2<kE4M3>(hi, uh, vh);
             const uint32_t lo = pack_fp8x2<kE4M3>((u - uh) * (1.0f / kP2), (v - vh) * (1.0f / kP2));
-            const int n = (j + jj) * 8 + c2;  // and n + 1
+            const int n = col0 + (j + jj) * 8 + c2;  // and n + 1
             const uint32_t in = (lane >> 2) + 8 * h;
             const uint32_t d0 = smem + L::p + (g & (L::kPBufs - 1)) * L::kP + n * 128 + ((w4 ^ (n & 7)) << 4) + in;
             const uint32_t d1 = smem + L::p + (g & (L::kPBufs - 1)) * L::kP + (n + 1) * 128 + ((w4 ^ ((n + 1) & 7)) << 4) + in;
