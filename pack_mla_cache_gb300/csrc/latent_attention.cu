@@ -535,7 +535,7 @@ __device__ __forceinline__ void produce(const LatentAttnArgs& a, const CUtensorM
           tc::cp_async_arrive(full);
         }
       }
-      if (__builtin_expect(cur.first, 0)) {
+      if (__builtin_expect(cur.first, 0)) {  // the query, behind the first rows
         const int b = item % L::kQBufs;
         const uint32_t n = item / L::kQBufs;
         if (n > 0) wait(bars + 8 * (L::kQEmpty + b), (n - 1) & 1);

@@ -387,15 +387,19 @@ def mla_latent_attention(q_c, q_pe, kv_cache, cache_dtype, num_blocks, block_siz
     int32 [S + 1], kv_lens int32 [S]; workspace: a uint8 tensor of
     ``mla_latent_attention_workspace`` bytes."""
     T, H, R = q_c.shape
-    _check(lib().mla_latent_attention(
-        _ptr(q_c), q_c.stride(0), q_c.stride(1), _ptr(q_pe), q_pe.stride(0), q_pe.stride(1), T, H,
-        R, q_pe.shape[2], _ptr(kv_cache), dtype_code(cache_dtype), num_blocks, block_size,
-        block_stride, entry_stride, _ptr(block_table), _bt_stride(block_table), _ptr(cu_q_lens),
-        _ptr(kv_lens), kv_lens.shape[0], softmax_scale, _ptr(k_scale), 1 if causal else 0,
-        _ptr(out), out.stride(0), out.stride(1), _ptr(lse),
-        0 if lse is None else lse.stride(0), 0 if lse is None else lse.stride(1),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(err_word),
-        _stream(stream)))
+    qc_t, qc_h, _ = q_c.stride()
+    qp_t, qp_h, _ = q_pe.stride()
+    out_t, out_h, _ = out.stride()
+    lse_t, lse_h = (0, 0) if lse is None else lse.stride()
+    status = lib().mla_latent_attention(
+        q_c.data_ptr(), qc_t, qc_h, q_pe.data_ptr(), qp_t, qp_h, T, H, R, q_pe.shape[2],
+        kv_cache.data_ptr(), dtype_code(cache_dtype), num_blocks, block_size, block_stride,
+        entry_stride, block_table.data_ptr(), _bt_stride(block_table), cu_q_lens.data_ptr(),
+        kv_lens.data_ptr(), kv_lens.shape[0], softmax_scale, _ptr(k_scale), 1 if causal else 0,
+        out.data_ptr(), out_t, out_h, _ptr(lse), lse_t, lse_h, workspace.data_ptr(),
+        workspace.nbytes, _ptr(err_word), _stream(stream))
+    if status:
+        _check(status)
 
 
 def mla_merge_attn_states(parts, lse, out, *, lse_out=None, stream=None):

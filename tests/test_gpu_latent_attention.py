@@ -129,6 +129,77 @@ def test_parity(case):
     check(Call(pg, q, cu_of(ql), kv, causal=causal).run(), q)
 
 
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("block", [1, 7, 8, 16, 24, 40, 64, 96, 128, 256])
+def test_page_sizes(fmt, block):
+    """Pages that are parts of a tile, tiles, several tiles, and neither; one page missing."""
+    kv, ql = [391, 64, 200], [1, 2, 1]
+    pg = R.paged(kv, fmt, block, seed=block)
+    if pg.table.shape[1] > 2:
+        pg.table[2, 1] = -5
+    q = R.queries(4, 16)
+    missing = kv[2] > block
+    check(Call(pg, q, cu_of(ql), kv).run(), q, err=ops.MLA_ERRBIT_BLOCK_OOB if missing else 0)
+
+
+@pytest.mark.parametrize("seed", range(30))
+def test_random_batches(seed):
+    """Batches of every mixture: head counts, new tokens, lengths around the tile and
+    split borders, pages, types, both masks."""
+    rng = np.random.default_rng(1000 + seed)
+    n = int(rng.integers(1, 12))
+    heads = int(rng.choice([1, 2, 5, 8, 16, 16, 31, 33, 64, 100, 128]))
+    most = max(1, 1500 // heads // n)
+    ql = [int(rng.choice([0, 1, 1, 1, 2, int(rng.integers(1, most + 1))])) for _ in range(n)]
+    ql[0] = max(ql[0], 1)
+    kv = [int(rng.choice([0, 1, 63, 64, 65, 128, int(rng.integers(1, 300)),
+                          int(rng.integers(1, 4000 // n + 2))])) for _ in range(n)]
+    fmt, block = int(rng.integers(0, 3)), int(rng.choice([8, 16, 32, 48, 64, 128]))
+    pg = R.paged(kv, fmt, block, seed=seed, pad_entry=int(rng.choice([0, 16])))
+    q = R.queries(sum(ql), heads, seed=seed, mul=float(rng.choice([0.3, 1.0, 4.0])))
+    check(Call(pg, q, cu_of(ql), kv, causal=bool(rng.integers(0, 2))).run(), q)
+
+
+@pytest.mark.parametrize("fmt", [0, 1, 2])
+def test_query_magnitudes(fmt):
+    """Rows of very different sizes, and rows whose elements are (an fp8 cache takes
+    the query in two 4-bit parts relative to the row's largest)."""
+    pg = R.paged([300], fmt, 64)
+    q = R.orc.bf16_bits_to_f64(R.queries(1, 16))
+    q[0, 0] *= 1e-30
+    q[0, 1] *= 2.0 ** -100
+    q[0, 2] *= 30
+    q[0, 3, ::7] *= 100
+    q[0, 4] *= np.exp(np.linspace(-12, 1, R.ENTRY))
+    q[0, 5] = 0
+    q[0, 6] = 0
+    q[0, 6, 575] = 8
+    q = R.orc.bf16_from_f32_array(q.astype(np.float32))
+    check(Call(pg, q, [0, 1], [300]).run(), q)
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("bad", [0x7FC0, 0x7F80, 0xFF80])
+def test_a_bad_query_row_stays_alone(fmt, bad):
+    pg = R.paged([300], fmt, 64)
+    q = R.queries(2, 16)
+    good = Call(pg, q, [0, 2], [300]).run().got()
+    q[1, 5, 100] = bad
+    out, lse, _ = Call(pg, q, [0, 2], [300]).run().got()
+    assert np.isnan(out[1, 5]).all() and np.isnan(lse[1, 5])
+    keep = np.ones((2, 16), bool)
+    keep[1, 5] = False
+    assert (out[keep] == good[0][keep]).all() and (lse[keep] == good[1][keep]).all()
+
+
+def test_negative_lengths_are_empty():
+    pg = R.paged([100, 50], 0, 64)
+    q = R.queries(2, 16)
+    call = Call(pg, q, [0, 1, 2], [0, 50])
+    call.kv_t[0] = -3
+    check(call.run(), q)
+
+
 @pytest.mark.parametrize("fmt", [0, 1, 2])
 def test_strides_and_padding(fmt):
     kv, ql = [150, 77], [9, 1]
