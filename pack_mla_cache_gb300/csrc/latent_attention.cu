@@ -95,6 +95,12 @@ struct Lay {
   static constexpr int kProdWarp = kOutWarp + 1;
   static constexpr int kWarps = kProdWarp + kProdWarps;
   static constexpr int kThreads = kWarps * 32;
+  // What beginning another query tile costs a CTA, in key tiles (its queries, the sums
+  // of the one before; measured 2.3 us at fp8 NR = 16, 6.4 at fp8 NR = 32, 3.4 at
+  // bf16 NR = 64): the runs are cut as if each query tile had this many more.  Cut
+  // without it: 64 ragged decodes 66.4 us (62.8 with it), 32 verifications 58.0 (49.9),
+  // 16 decodes of 128 heads 50.3 (49.0).
+  static constexpr int kSwitch = kF8 ? (NR == 16 ? 3 : 6) : (NR == 16 ? 1 : 2);
   // a maximum may grow this much (log2) before the sums are rescaled; the fp8
   // weights stay below 2^4 (p1 rounds by at most 1/2 there, p2 = 512 (p - p1) fits)
   static constexpr float kGrow = kF8 ? 4.0f : 8.0f;
@@ -182,16 +188,19 @@ struct Tile {
   int t0, ntok;             // the sequence's tokens
 };
 
-// A CTA's run of units: where it starts, and what finds the CTA of another unit.
+// A CTA's run of units: where it starts, and what finds the CTA of another unit.  A
+// query tile is kSwitch units that stand for beginning it, then its key tiles: a run
+// starts before the first of these when kt is negative.
 struct Run {
   Seq q;               // of sequence s
   int s, qt, kt, count;
   int64_t begin, each; // the first unit; units of the CTAs c >= extra (each + 1 of the ones before)
   int extra;
+  __device__ __forceinline__ int left() const { return count + min(kt, 0); }
 };
 
 // Walks the run; every role has its own copy.
-template <int NR>
+template <int NR, int kSwitch>
 struct Walk {
   Seq q;
   int s, qt, kt, nkt, most, least;
@@ -207,12 +216,12 @@ struct Walk {
     q = r.q;
     s = r.s;
     qt = r.qt;
-    kt = r.kt;
-    left = r.count;
+    kt = max(r.kt, 0);
+    left = r.left();
     nkt = 0;
   }
-  // The next unit.  Each role calls this at one place only: 13 warps of different
-  // code share the instruction caches.
+  // The next unit.  Each role calls this at one place only: 10 or 14 warps of
+  // different code share the instruction caches.
   __device__ __forceinline__ Tile next(const LatentAttnArgs& a) {
     Tile t{};
     if (left <= 0) return t;
@@ -225,6 +234,8 @@ struct Walk {
           do q = load_seq<NR>(a, ++s);
           while (q.nqt == 0 && s + 1 < a.num_seqs);
         }
+        left -= kSwitch;
+        if (left <= 0) return t;
       }
       item(a);
     }
@@ -245,8 +256,8 @@ struct Walk {
   }
 };
 
-// Bounded waits.  The loops of the roles have to stay small (13 warps of different
-// code share the instruction caches; fetching was the largest stall), so all but
+// Bounded waits.  The loops of the roles have to stay small (10 or 14 warps of
+// different code share the instruction caches; fetching was the largest stall), so all but
 // the first look at a barrier is out of line.
 __device__ __noinline__ void wait_on(uint32_t bar, uint32_t parity, uint32_t abort, uint64_t limit) {
   uint64_t since = 0;
@@ -440,7 +451,7 @@ __device__ __forceinline__ void produce(const LatentAttnArgs& a, const CUtensorM
                                         int lane, uint32_t& errbits) {
   using L = Lay<FMT, NR>;
   const uint32_t bars = smem + L::bars;
-  Walk<NR> walk;
+  Walk<NR, L::kSwitch> walk;
   walk.start(run);
   // Row copies: 8 lanes x 16 bytes per row and chunk; this thread has the rows
   // pw * 16 + 4 i + lane / 8.
@@ -627,7 +638,7 @@ __device__ __forceinline__ void score_role(const LatentAttnArgs& a, const Run& r
   using L = Lay<FMT, NR>;
   const uint32_t bars = smem + L::bars;
   auto wait = [&](int bar, uint32_t phase) { waiter(bars + 8 * bar, phase & 1); };
-  Walk<NR> walk;
+  Walk<NR, L::kSwitch> walk;
   walk.start(run);
   const bool one = tc::elect();
   uint32_t item = 0;
@@ -657,7 +668,7 @@ __device__ __forceinline__ void output_role(const LatentAttnArgs& a, const Run& 
   using L = Lay<FMT, NR>;
   const uint32_t bars = smem + L::bars;
   auto wait = [&](int bar, uint32_t phase) { waiter(bars + 8 * bar, phase & 1); };
-  Walk<NR> walk;
+  Walk<NR, L::kSwitch> walk;
   walk.start(run);
   const bool one = tc::elect();
   uint32_t item = 0;
@@ -716,7 +727,7 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
   float* red = reinterpret_cast<float*>(__cvta_shared_to_generic(smem + L::red));
   float mu[kG][2], l[kG][2];
   float cs[kG][2];  // score of a product: softmax and cache scale, log2 e, the query row's scale
-  Walk<NR> walk;
+  Walk<NR, L::kSwitch> walk;
   walk.start(run);
   int kt_begin = 0;
   uint32_t g = 0, item = 0;
@@ -1031,7 +1042,7 @@ __device__ __forceinline__ int64_t scan64(int64_t v, int lane) {  // inclusive, 
 // This CTA's run.  Up to 128 sequences of at most 8 query tiles: every warp finds
 // it by itself, 32 sequences at a time, without a barrier.
 constexpr int kSmallSeqs = 128, kSmallTiles = 8;
-template <int NR>
+template <int NR, int kSwitch>
 __device__ __forceinline__ bool schedule_small(const LatentAttnArgs& a, int lane, Run& r,
                                                uint32_t& errbits) {
   if (a.num_seqs > kSmallSeqs) return false;
@@ -1049,7 +1060,7 @@ __device__ __forceinline__ bool schedule_small(const LatentAttnArgs& a, int lane
     if (__any_sync(0xFFFFFFFFu, q.nqt > kSmallTiles)) return false;
     int64_t u = 0;
 #pragma unroll 1
-    for (int qt = 0; qt < q.nqt; ++qt) u += key_tiles(most_seen<NR>(a, q, qt));
+    for (int qt = 0; qt < q.nqt; ++qt) u += kSwitch + key_tiles(most_seen<NR>(a, q, qt));
     const int64_t inc = scan64(u, lane);
     if (round == 1) {
       off = r.begin - before - (inc - u);
@@ -1063,6 +1074,7 @@ __device__ __forceinline__ bool schedule_small(const LatentAttnArgs& a, int lane
     if (base >= a.num_seqs) {
       if (round == 1) return true;  // (not reached: some sequence has the unit)
       cut(before, r);
+      r.kt = 0;
       if (r.count == 0) return true;
       round = 1;
       base = 0;
@@ -1073,7 +1085,7 @@ __device__ __forceinline__ bool schedule_small(const LatentAttnArgs& a, int lane
   if (has >> lane & 1) {
 #pragma unroll 1
     for (;; ++qt) {
-      const int k = key_tiles(most_seen<NR>(a, q, qt));
+      const int k = kSwitch + key_tiles(most_seen<NR>(a, q, qt));
       if (off < k) break;
       off -= k;
     }
@@ -1082,14 +1094,14 @@ __device__ __forceinline__ bool schedule_small(const LatentAttnArgs& a, int lane
   auto all = [&](int v) { return __shfl_sync(0xFFFFFFFFu, v, from); };
   r.s = all(s);
   r.qt = all(qt);
-  r.kt = all((int)off);
+  r.kt = all((int)off) - kSwitch;
   r.q = Seq{all(q.t0), all(q.ntok), all(q.c1), all(q.kv), all(q.nqt)};
   return true;
 }
 
 // Any number of sequences and query tiles, by the whole CTA; the scratch is the
 // (still unused) first key stage.
-template <int NR, int kWarps>
+template <int NR, int kSwitch, int kWarps>
 __device__ __noinline__ void schedule_large(const LatentAttnArgs& a, uint8_t* scratch, Run& r) {
   constexpr int kThreads = kWarps * 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1099,7 +1111,8 @@ __device__ __noinline__ void schedule_large(const LatentAttnArgs& a, uint8_t* sc
   for (int s = warp; s < a.num_seqs; s += kWarps) {
     const Seq q = load_seq<NR>(a, s);
     int64_t u = 0;
-    for (int qt = lane; qt < q.nqt; qt += 32) u += key_tiles(most_seen<NR>(a, q, qt));
+    for (int qt = lane; qt < q.nqt; qt += 32)
+      u += kSwitch + key_tiles(most_seen<NR>(a, q, qt));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
     if (lane == 0) pre[s] = u;
@@ -1120,6 +1133,7 @@ __device__ __noinline__ void schedule_large(const LatentAttnArgs& a, uint8_t* sc
     total += part[w];
   }
   cut(total, r);
+  r.kt = 0;
   if (r.count > 0)
     for (int s = s0; s < s1; ++s) {
       const int64_t u = pre[s];
@@ -1138,7 +1152,8 @@ __device__ __noinline__ void schedule_large(const LatentAttnArgs& a, uint8_t* sc
     const int64_t off = at[1];
     int64_t base = 0;
     for (int q0 = 0; q0 < r.q.nqt; q0 += 32) {
-      const int64_t u = q0 + lane < r.q.nqt ? key_tiles(most_seen<NR>(a, r.q, q0 + lane)) : 0;
+      const int64_t u =
+          q0 + lane < r.q.nqt ? kSwitch + key_tiles(most_seen<NR>(a, r.q, q0 + lane)) : 0;
       const int64_t in = scan64(u, lane);
       const uint32_t hit = __ballot_sync(0xFFFFFFFFu, off < base + in);
       if (hit) {
@@ -1154,7 +1169,7 @@ __device__ __noinline__ void schedule_large(const LatentAttnArgs& a, uint8_t* sc
   __syncthreads();
   if (r.count > 0) {
     r.qt = (int)at[2];
-    r.kt = (int)at[3];
+    r.kt = (int)at[3] - kSwitch;
   }
   __syncthreads();  // the scratch is read
 }
@@ -1199,12 +1214,12 @@ __global__ void __launch_bounds__(Lay<FMT, NR>::kThreads, 1)
   if (threadIdx.x == 0) ws.split[blockIdx.x] = Split{0, 0, 0, 0, 0};
   uint32_t errbits = 0;
   Run run;
-  if (!schedule_small<NR>(a, lane, run, errbits)) {
+  if (!schedule_small<NR, L::kSwitch>(a, lane, run, errbits)) {
     Run large;  // apart, so that only this branch has it in memory
-    schedule_large<NR, L::kWarps>(a, smem_raw, large);
+    schedule_large<NR, L::kSwitch, L::kWarps>(a, smem_raw, large);
     run = large;
   }
-  if (run.count > 0) {
+  if (run.left() > 0) {
     if (warp < L::kSoftWarps)
       soften<FMT, NR>(a, run, smem, tmem, wait, warp, lane, ws);
     else if (warp >= L::kProdWarp)
