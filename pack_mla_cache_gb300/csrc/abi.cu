@@ -19,6 +19,7 @@
 #include "mla_cache.h"
 #include "mla_device.cuh"
 #include "mla_internal.h"
+#include "serving.h"
 
 namespace {
 

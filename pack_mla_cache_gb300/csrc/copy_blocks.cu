@@ -12,7 +12,7 @@
 // items).  When entries are contiguous a block's rows are one run; otherwise a
 // chunk's row and column come from one 32-bit division.
 #include "mla_device.cuh"
-#include "mla_internal.h"
+#include "serving.h"
 
 namespace mla {
 namespace {

@@ -57,7 +57,7 @@
 #include <atomic>
 
 #include "mla_device.cuh"
-#include "mla_internal.h"
+#include "serving.h"
 #include "tensor_core.cuh"
 
 namespace mla {

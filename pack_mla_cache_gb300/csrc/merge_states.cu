@@ -16,7 +16,7 @@
 // from multiplications by reciprocals (with 64-bit divisions 4 parts of 8192 x 16
 // rows of 128 took 39 us).
 #include "mla_device.cuh"
-#include "mla_internal.h"
+#include "serving.h"
 
 namespace mla {
 namespace {

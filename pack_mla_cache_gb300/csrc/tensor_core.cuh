@@ -1,8 +1,8 @@
 // tensor_core.cuh -- thin wrappers over the 5th-generation tensor core PTX of
 // sm_103a (tcgen05) that the latent attention uses: tensor memory allocation,
-// shared-memory and instruction descriptors, the bf16 matrix instruction with
-// fp32 accumulators in tensor memory, its completion on an mbarrier, and loads
-// and stores of tensor memory.
+// shared-memory and instruction descriptors, the bf16 and e4m3 / e5m2 matrix
+// instructions with fp32 accumulators in tensor memory, their completion on an
+// mbarrier, loads and stores of tensor memory, and the copies that feed them.
 #pragma once
 
 #include <cstdint>
@@ -10,6 +10,11 @@
 #include "mla_device.cuh"
 
 namespace mla {
+// Arrives n times.
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
+
 namespace tc {
 
 // Tensor memory: `cols` columns (a power of two >= 32) of 128 lanes x 32 bits;
