@@ -609,11 +609,13 @@ mla_status_t mla_cache_copy_blocks(const int64_t* kv_cache_ptrs, int32_t num_lay
  *                       boundaries.
  *   lse                 fp32 [T, H] by strides, or NULL.
  *   workspace           16-byte aligned device memory of workspace_bytes >=
- *                       what mla_latent_attention_workspace gives.  Its contents before and after a call
- *                       mean nothing; calls that may run at the same time (on
+ *                       what mla_latent_attention_workspace gives.  Its
+ *                       contents before and after a call mean nothing; calls that may run at the same time (on
  *                       two streams) need one each.
+ * out, lse and workspace must not overlap each other or the inputs.
  * The kernel's internal waits are bounded (2 s, which means a fault or a stalled
- * GPU); one that runs out leaves rows of out unwritten and sets
+ * GPU); a block whose wait runs out stops issuing work, waits (bounded again) for
+ * what it has in flight, leaves its rows of out unspecified and sets
  * MLA_ERRBIT_TIMEOUT.
  */
 mla_status_t mla_latent_attention(
@@ -626,6 +628,13 @@ mla_status_t mla_latent_attention(
     int32_t causal, void* out, int64_t out_token_stride, int64_t out_head_stride, float* lse,
     int64_t lse_token_stride, int64_t lse_head_stride, void* workspace, int64_t workspace_bytes,
     uint32_t* err_word, mla_stream_t stream);
+
+/* TESTING HOOK for mla_latent_attention, applied to every later call from this
+ * process (not for production use).  wait_limit_ns: how long a wait may last before
+ * the kernel gives up (0 restores the default of 2 s).  stall_stage >= 1: that stage
+ * of the first CTA's pipeline never fills, so its waits run out of time; 0 (the
+ * default) stalls nothing.  Returns 0. */
+int mla_test_attention_timeout(uint64_t wait_limit_ns, int32_t stall_stage);
 
 /* Writes to *bytes (host memory) the workspace that mla_latent_attention needs
  * on the current device for any call of at most num_tokens tokens, num_heads
@@ -643,7 +652,8 @@ mla_status_t mla_latent_attention_workspace(int32_t num_tokens, int32_t num_head
  *   out[t,h,:]      = sum_i exp(lse_i[t,h] - lse_out[t,h]) * part_i[t,h,:]
  * in fp32, rounded once to dtype.  A part whose lse is -infinity has no
  * influence, whatever its row holds; when every part's is, out = 0 and lse_out
- * = -infinity.  A lse of +infinity or NaN gives NaN.
+ * = -infinity.  A lse of +infinity or NaN gives NaN.  out and lse_out must not
+ * overlap the inputs.
  *
  *   parts               element (i, t, h, e) at i * part_stride +
  *                       t * token_stride + h * head_stride + e, of type dtype;

@@ -31,6 +31,8 @@ std::atomic<int> g_gather_early{0};
 std::atomic<int> g_insert_early{0};
 constexpr uint64_t kDefaultWaitNs = 2000000000ull;  // 2 s: a wait that long means a fault
 std::atomic<uint64_t> g_wait_ns{kDefaultWaitNs};
+std::atomic<uint64_t> g_attention_wait_ns{kDefaultWaitNs};
+std::atomic<int32_t> g_attention_stall{0};
 std::atomic<int64_t> g_skip_item{-1};
 
 mla_status_t fail(mla_status_t st, const char* fmt, ...) {
@@ -282,6 +284,12 @@ int mla_test_insert_timeout(uint64_t wait_limit_ns, int64_t skip_item) {
   if (wait_limit_ns == 0) wait_limit_ns = kDefaultWaitNs;
   g_wait_ns.store(wait_limit_ns);
   g_skip_item.store(skip_item < 0 ? -1 : skip_item);
+  return 0;
+}
+
+int mla_test_attention_timeout(uint64_t wait_limit_ns, int32_t stall_stage) {
+  g_attention_wait_ns.store(wait_limit_ns ? wait_limit_ns : kDefaultWaitNs);
+  g_attention_stall.store(stall_stage);
   return 0;
 }
 
@@ -1055,7 +1063,8 @@ mla_status_t mla_latent_attention(
   a.lse_hs = lse_head_stride;
   a.workspace = static_cast<uint8_t*>(workspace);
   a.err = err_word;
-  a.wait_limit_ns = kDefaultWaitNs;
+  a.wait_limit_ns = g_attention_wait_ns.load();
+  a.stall_stage = g_attention_stall.load();
   return launched(mla::launch_latent_attention(a, (int)cache_dtype, sms, cfg_for(stream)),
                   "mla_latent_attention");
 }

@@ -50,8 +50,9 @@
 // NaN or an infinity is stored as zeros and marked, and its score becomes NaN
 // for the tokens that do see it.
 //
-// Waits are bounded (wait_limit_ns): one that runs out marks the CTA as given
-// up, every later wait returns at once, and MLA_ERRBIT_TIMEOUT is set.
+// Waits are bounded (wait_limit_ns): one that runs out marks the CTA as given up.
+// Every role leaves at its next wait then, copies and products in flight are waited
+// for (bounded again), and MLA_ERRBIT_TIMEOUT is set.
 #include <cuda.h>
 
 #include <atomic>
@@ -259,25 +260,27 @@ struct Walk {
 // Bounded waits.  The loops of the roles have to stay small (10 or 14 warps of
 // different code share the instruction caches; fetching was the largest stall), so all but
 // the first look at a barrier is out of line.
-__device__ __noinline__ void wait_on(uint32_t bar, uint32_t parity, uint32_t abort, uint64_t limit) {
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, uint32_t abort, uint64_t limit) {
   uint64_t since = 0;
   for (uint32_t spin = 1; !mbar_try_wait(bar, parity); ++spin) {
     if (spin & 31u) continue;
-    if (lds_u32(abort) != 0) return;
+    if (lds_u32(abort) != 0) return false;
     const uint64_t now = global_ns();
     if (since == 0) since = now;
     if (now - since > limit) {
       asm volatile("st.shared.u32 [%0], %1;" ::"r"(abort), "r"(1u) : "memory");
-      return;
+      return false;
     }
   }
+  return true;
 }
 struct Waiter {
   uint32_t abort;  // shared address of Misc::abort
   uint64_t limit;
   __device__ __forceinline__ bool given_up() const { return lds_u32(abort) != 0; }
-  __device__ __forceinline__ void operator()(uint32_t bar, uint32_t parity) const {
-    if (!mbar_try_wait(bar, parity)) wait_on(bar, parity, abort, limit);
+  // Whether the barrier's phase completed: false once the CTA has given up.
+  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+    return mbar_try_wait(bar, parity) || wait_on(bar, parity, abort, limit);
   }
 };
 
@@ -445,8 +448,9 @@ __device__ __forceinline__ void split_q(const LatentAttnArgs& a, const Tile& q, 
   if (lane == 0) mbar_arrive_n(bar, 32);
 }
 
+// Returns the key tiles whose copies were issued.
 template <int FMT, int NR>
-__device__ __forceinline__ void produce(const LatentAttnArgs& a, const CUtensorMap& map,
+__device__ __forceinline__ uint32_t produce(const LatentAttnArgs& a, const CUtensorMap& map,
                                         const Run& run, uint32_t smem, const Waiter& wait, int pw,
                                         int lane, uint32_t& errbits) {
   using L = Lay<FMT, NR>;
@@ -467,7 +471,7 @@ __device__ __forceinline__ void produce(const LatentAttnArgs& a, const CUtensorM
   // Blocks are looked up two tiles ahead.
   Tile cur{}, nxt{};
   int32_t blk[kRows] = {}, nblk[kRows] = {};
-  uint32_t item = 0;
+  uint32_t item = 0, issued = 0;
 #pragma unroll 1
   for (int step = -2;; ++step) {
     const Tile far = walk.next(a);
@@ -482,8 +486,10 @@ __device__ __forceinline__ void produce(const LatentAttnArgs& a, const CUtensorM
       const uint32_t g = step;
       const int st = g % L::kStages;
       const uint32_t full = bars + 8 * (L::kFull + st), flags = smem + L::flags + st * kKeys;
-      if (g >= L::kStages) wait(bars + 8 * (L::kEmpty + st), (g / L::kStages - 1) & 1);
-      __syncwarp();
+      if (g >= L::kStages && !__all_sync(0xFFFFFFFFu, wait(bars + 8 * (L::kEmpty + st),
+                                                           (g / L::kStages - 1) & 1)))
+        break;
+      ++issued;
       const uint32_t base = smem + st * L::kTile;
       if (__builtin_expect(by_box(a, cur), 1)) {
         const bool ok = blk[0] >= 0 && blk[0] < a.num_blocks;
@@ -549,7 +555,7 @@ __device__ __forceinline__ void produce(const LatentAttnArgs& a, const CUtensorM
       if (__builtin_expect(cur.first, 0)) {  // the query, behind the first rows
         const int b = item % L::kQBufs;
         const uint32_t n = item / L::kQBufs;
-        if (n > 0) wait(bars + 8 * (L::kQEmpty + b), (n - 1) & 1);
+        if (n > 0 && !__all_sync(0xFFFFFFFFu, wait(bars + 8 * (L::kQEmpty + b), (n - 1) & 1))) break;
         const uint32_t dst = smem + L::q + b * L::kQ, bar = bars + 8 * (L::kQFull + b);
         if constexpr (L::kF8) split_q<NR>(a, cur, dst, smem + L::qs + b * NR * 4, bar, pw, lane);
         else load_q<NR>(a, cur, dst, bar, pw, lane);
@@ -566,6 +572,7 @@ __device__ __forceinline__ void produce(const LatentAttnArgs& a, const CUtensorM
     if (step >= -1 && !cur.valid) break;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
+  return issued;
 }
 
 // --------------------------------------------------------------- matrix issue
@@ -637,7 +644,7 @@ __device__ __forceinline__ void score_role(const LatentAttnArgs& a, const Run& r
                                            uint32_t tmem, const Waiter& waiter) {
   using L = Lay<FMT, NR>;
   const uint32_t bars = smem + L::bars;
-  auto wait = [&](int bar, uint32_t phase) { waiter(bars + 8 * bar, phase & 1); };
+  auto wait = [&](int bar, uint32_t phase) { return waiter(bars + 8 * bar, phase & 1); };
   Walk<NR, L::kSwitch> walk;
   walk.start(run);
   const bool one = tc::elect();
@@ -647,10 +654,10 @@ __device__ __forceinline__ void score_role(const LatentAttnArgs& a, const Run& r
     const Tile t = walk.next(a);
     if (!t.valid) break;
     const int qb = item % L::kQBufs, st = g % L::kStages;
-    if (t.first) wait(L::kQFull + qb, item / L::kQBufs);
-    if (g >= 2) wait(L::kPFull + (g & 1), (g - 2) >> 1);  // the score buffer is read
-    wait(L::kFull + st, g / L::kStages);
-    __syncwarp();
+    bool ok = !t.first || wait(L::kQFull + qb, item / L::kQBufs);
+    if (g >= 2) ok &= wait(L::kPFull + (g & 1), (g - 2) >> 1);  // the score buffer is read
+    ok &= wait(L::kFull + st, g / L::kStages);
+    if (!__all_sync(0xFFFFFFFFu, ok)) break;
     // Queries, and rows that do not come by TMA, are written by ordinary and
     // asynchronous stores of the producers; the fence towards the tensor core's reads
     // stands here, behind the barrier (in the producers it would also wait for their
@@ -667,7 +674,7 @@ __device__ __forceinline__ void output_role(const LatentAttnArgs& a, const Run& 
                                             uint32_t tmem, const Waiter& waiter) {
   using L = Lay<FMT, NR>;
   const uint32_t bars = smem + L::bars;
-  auto wait = [&](int bar, uint32_t phase) { waiter(bars + 8 * bar, phase & 1); };
+  auto wait = [&](int bar, uint32_t phase) { return waiter(bars + 8 * bar, phase & 1); };
   Walk<NR, L::kSwitch> walk;
   walk.start(run);
   const bool one = tc::elect();
@@ -676,9 +683,9 @@ __device__ __forceinline__ void output_role(const LatentAttnArgs& a, const Run& 
   for (uint32_t g = 0;; ++g) {
     const Tile t = walk.next(a);
     if (!t.valid) break;
-    wait(L::kPFull + (g & 1), g >> 1);
-    if (t.first && item > 0) wait(L::kOFree, item - 1);  // the sums of the query tile before are read
-    __syncwarp();
+    bool ok = wait(L::kPFull + (g & 1), g >> 1);
+    if (t.first && item > 0) ok &= wait(L::kOFree, item - 1);  // the sums of the query tile before are read
+    if (!__all_sync(0xFFFFFFFFu, ok)) break;
     tc::fence_after_sync();
     issue_outputs<FMT, NR>(smem, tmem, one, g % L::kStages, g & 1, t.first);
     item += t.last;
@@ -715,8 +722,9 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
   constexpr int kG = kC / 8;    // a thread has the rows 8 j + 2 (lane % 4) + {0, 1} of them
   const int group = warp >> 2, w4 = warp & 3, col0 = group * kC;
   const uint32_t bars = smem + L::bars;
+  bool dead = false;  // a wait of this thread was given up
   auto wait = [&](uint32_t bar, uint32_t parity) {
-    waiter(bar, parity);
+    dead |= !waiter(bar, parity);
     __syncwarp();
   };
   const uint32_t sub = tmem + ((uint32_t)(w4 * 32) << 16);  // this warp's lanes
@@ -800,7 +808,7 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
 #pragma unroll
       for (int e = 0; e < 2; ++e)
         grown |= fmaxf(x[j][e], x[j][e + 2]) > mu[j][e] + L::kGrow;
-    grown = soft_any(group, grown);
+    grown = soft_any(group, grown | dead);
     // P's buffer is free when the outputs of the tile that had it are done
     if (g >= L::kPBufs) {
       const uint32_t o = g - L::kPBufs;
@@ -824,7 +832,14 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
 #pragma unroll
         for (int j = 0; j < kG; ++j)
           *reinterpret_cast<float2*>(mine + 8 * j + c2) = make_float2(tm[j][0], tm[j][1]);
+      // All four warps leave when one has given up (or they would wait for each other):
+      // it says so by a negative factor, which it alone could replace by one.
+      const bool leave = __any_sync(0xFFFFFFFFu, dead);
+      if (lane == 0) fac[0] = leave ? -1.0f : 0.0f;
       soft_sync(group);
+      const float* said = red + (L::kSoftWarps + group * 4) * kC;
+      if (__any_sync(0xFFFFFFFFu, *reinterpret_cast<const volatile float*>(said + (lane & 3) * kC) < 0.0f))
+        break;
 #pragma unroll
       for (int j = 0; j < kG; ++j) {
 #pragma unroll
@@ -942,7 +957,7 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
     // token and head of this group's first row
     const int dt0 = token_of(a, first + col0), tok0 = t.t0 + dt0;
     const int head0 = (int)(first + col0) - dt0 * a.num_heads;
-    const bool lost = waiter.given_up();
+    const bool lost = __any_sync(0xFFFFFFFFu, waiter.given_up());
     // where row `lane` of the group goes in out
     const int dt = token_of(a, head0 + lane), row_h = head0 + lane - dt * a.num_heads;
     const int64_t row_at = (int64_t)(tok0 + dt) * a.out_ts + (int64_t)row_h * a.out_hs;
@@ -1171,7 +1186,23 @@ __device__ __noinline__ void schedule_large(const LatentAttnArgs& a, uint8_t* sc
     r.qt = (int)at[2];
     r.kt = (int)at[3] - kSwitch;
   }
-  __syncthreads();  // the scratch is read
+  tc::fence_smem_async();  // the scratch is read; copies may write there now
+  __syncthreads();
+}
+
+// After giving up: waits, bounded again, for the copies into shared memory that this
+// thread's warp issued, and a millisecond for matrix products in flight (they end by
+// themselves within microseconds).
+template <int FMT, int NR>
+__device__ __noinline__ void settle(uint32_t smem, uint32_t issued, uint64_t limit) {
+  using L = Lay<FMT, NR>;
+  const uint64_t since = global_ns();
+  for (uint32_t g = issued > L::kStages ? issued - L::kStages : 0; g < issued; ++g)
+    while (!mbar_try_wait(smem + L::bars + 8 * (L::kFull + g % L::kStages), (g / L::kStages) & 1) &&
+           global_ns() - since <= limit) {
+    }
+  while (global_ns() - since <= 1000000) {
+  }
 }
 
 template <int FMT, int NR>
@@ -1184,13 +1215,13 @@ __global__ void __launch_bounds__(Lay<FMT, NR>::kThreads, 1)
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   Misc& m = *reinterpret_cast<Misc*>(smem_raw + L::misc);
   pdl_trigger();
-  if (warp == L::kScoreWarp) tc::alloc(smem_addr(&m.tmem), L::kTmem);
   if (threadIdx.x == 0) {
     m.abort = 0;
     const uint32_t bars = smem + L::bars;
     for (int i = 0; i < L::kStages; ++i) {
       // each producer warp's key flags, and each thread's row copies
-      mbar_init(bars + 8 * (L::kFull + i), kProdWarps + kProdThreads);
+      const bool stall = blockIdx.x == 0 && a.stall_stage == i + 1;  // one arrival too many
+      mbar_init(bars + 8 * (L::kFull + i), kProdWarps + kProdThreads + (stall ? 1 : 0));
       mbar_init(bars + 8 * (L::kEmpty + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -1204,12 +1235,11 @@ __global__ void __launch_bounds__(Lay<FMT, NR>::kThreads, 1)
     mbar_init(bars + 8 * L::kOFree, L::kSoftWarps);
     mbar_fence_init();
   }
-  tc::fence_before_sync();
-  __syncthreads();
-  tc::fence_after_sync();
-  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, m.tmem, 0);
   const Waiter wait{smem_addr(&m.abort), a.wait_limit_ns};
+  // Tensor memory is taken behind the wait for the kernel before: holding it there could
+  // keep a block of that kernel from its own.
   pdl_wait();
+  if (warp == L::kScoreWarp) tc::alloc(smem_addr(&m.tmem), L::kTmem);
   const Workspace ws = workspace_of<NR>(a.workspace, gridDim.x);
   if (threadIdx.x == 0) ws.split[blockIdx.x] = Split{0, 0, 0, 0, 0};
   uint32_t errbits = 0;
@@ -1219,11 +1249,16 @@ __global__ void __launch_bounds__(Lay<FMT, NR>::kThreads, 1)
     schedule_large<NR, L::kSwitch, L::kWarps>(a, smem_raw, large);
     run = large;
   }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, m.tmem, 0);
+  uint32_t issued = 0;
   if (run.left() > 0) {
     if (warp < L::kSoftWarps)
       soften<FMT, NR>(a, run, smem, tmem, wait, warp, lane, ws);
     else if (warp >= L::kProdWarp)
-      produce<FMT, NR>(a, map, run, smem, wait, warp - L::kProdWarp, lane, errbits);
+      issued = produce<FMT, NR>(a, map, run, smem, wait, warp - L::kProdWarp, lane, errbits);
     else if (warp == L::kScoreWarp)
       score_role<FMT, NR>(a, run, smem, tmem, wait);
     else
@@ -1240,6 +1275,10 @@ __global__ void __launch_bounds__(Lay<FMT, NR>::kThreads, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
+  if (__builtin_expect(wait.given_up(), 0)) {
+    settle<FMT, NR>(smem, issued, a.wait_limit_ns);
+    __syncthreads();
+  }
   if (warp == L::kScoreWarp) tc::dealloc(tmem, L::kTmem);
 }
 

@@ -5,7 +5,7 @@
 //
 // What it computes: with m = max_i lse_i and w_i = exp(lse_i - m),
 //   out = sum_i w_i part_i / sum_i w_i,   lse = m + ln(sum_i w_i),
-// in fp32, rounded once; a part with lse -inf has weight 0 and is not read.
+// in fp32, rounded once; a part with lse -inf has weight 0, whatever its row holds.
 // Bound by HBM: every part is read once, the result written once.
 //
 // Design: a thread owns one 16-byte chunk of an output row.  The lse of its
@@ -119,9 +119,9 @@ cudaError_t launch_t(MergeArgs a, const LaunchCfg& cfg) {
   // chunk numbers stay below 2^31 - 2^24 (the last stride of the grid included): larger
   // calls, of many GiB, go in several launches
   const int64_t per_token = (int64_t)a.num_heads * a.row_chunks;
-  const int32_t most = (int32_t)((INT32_MAX - (1 << 24)) / per_token), tokens = a.num_tokens;
-  for (int32_t t0 = 0; t0 < tokens; t0 += most) {
-    a.num_tokens = tokens - t0 < most ? tokens - t0 : most;
+  const int64_t most = (INT32_MAX - (1 << 24)) / per_token, tokens = a.num_tokens;
+  for (int64_t t0 = 0; t0 < tokens; t0 += most) {
+    a.num_tokens = (int32_t)(tokens - t0 < most ? tokens - t0 : most);
     const int64_t chunks = a.num_tokens * per_token;
     lc.gridDim = dim3(capped_grid(reinterpret_cast<const void*>(merge_states_kernel<F>), kThreads,
                                   (chunks + kThreads - 1) / kThreads));

@@ -84,6 +84,7 @@ struct LatentAttnArgs {
   uint8_t* workspace;
   uint32_t* err;
   uint64_t wait_limit_ns;
+  int32_t stall_stage;  // testing: this pipeline stage (from 1) of CTA 0 never fills
 };
 
 cudaError_t launch_copy_blocks(const CopyBlocksArgs& a, const LaunchCfg& cfg);

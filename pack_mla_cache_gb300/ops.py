@@ -75,6 +75,7 @@ SIGNATURES = {
     "mla_set_gather_early_tables": (ctypes.c_int, [ctypes.c_int]),
     "mla_set_insert_early_tables": (ctypes.c_int, [ctypes.c_int]),
     "mla_test_insert_timeout": (ctypes.c_int, [ctypes.c_uint64, _i64]),
+    "mla_test_attention_timeout": (ctypes.c_int, [ctypes.c_uint64, _i32]),
     "mla_cache_insert_grouped": (ctypes.c_int, [
         _vp, _i64, _i64, _vp, _i64, _i64, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _vp,
         ctypes.c_int, _i64, _i32, _i64, _i64, ctypes.POINTER(NormRope), _vp, _vp]),
@@ -209,6 +210,12 @@ def mla_test_insert_timeout(wait_limit_ns: int = 0, skip_item: int = -1) -> None
     """Testing hook of the insert's bulk-copy pipeline (see the C header);
     ``mla_test_insert_timeout()`` restores the defaults."""
     lib().mla_test_insert_timeout(int(wait_limit_ns), int(skip_item))
+
+
+def mla_test_attention_timeout(wait_limit_ns: int = 0, stall_stage: int = 0) -> None:
+    """Testing hook for the attention's bounded waits (see mla_cache.h);
+    ``mla_test_attention_timeout()`` restores the defaults."""
+    lib().mla_test_attention_timeout(int(wait_limit_ns), int(stall_stage))
 
 
 def mla_cache_insert_grouped(kv_c, k_pe, slot_mapping, kv_cache_ptrs, kv_scales, cache_dtype,

@@ -155,3 +155,8 @@ def test_without_a_gpu(L):
     assert merge(L) == ops.MLA_ERR_CUDA
     n = ctypes.c_int64(0)
     assert L.mla_latent_attention_workspace(1, 16, 1, ctypes.byref(n)) == ops.MLA_ERR_CUDA
+
+
+def test_attention_timeout_hook(L):
+    assert L.mla_test_attention_timeout(1000, 2) == 0
+    assert L.mla_test_attention_timeout(0, 0) == 0  # defaults back

@@ -419,3 +419,31 @@ def test_refusals_on_the_device():
     call.kv_t = call.kv_t.cpu()
     with pytest.raises(ops.MlaError, match="kv_lens must be device memory"):
         call.run()
+
+
+@pytest.mark.parametrize("stage", [1, 2])
+@pytest.mark.parametrize("fmt,heads", [(0, 16), (0, 128), (1, 16), (2, 40)])
+def test_waits_that_run_out_return_and_report(fmt, heads, stage):
+    """With a 1 ms limit and a pipeline stage of the first CTA that never fills (a testing hook),
+    its waits run out: the call returns and says so, the other CTAs' sequences are as ever, and
+    the next call is exact.  No fault is involved: only bounded waits that give up."""
+    kv = [1500] + [64 * (i % 5 + 1) for i in range(320)]
+    pg = R.paged(kv, fmt, 64, seed=19)
+    q = R.queries(len(kv), heads)
+    cu = list(range(len(kv) + 1))
+    good, _, e = Call(pg, q, cu, kv).run().got()
+    assert e == 0
+    c = Call(pg, q, cu, kv)
+    try:
+        ops.mla_test_attention_timeout(1_000_000, stage)
+        out, _, e = c.run().got()
+    finally:
+        ops.mla_test_attention_timeout()
+    assert e == ops.MLA_ERRBIT_TIMEOUT
+    c.canaries()
+    np.testing.assert_array_equal(out[40:], good[40:])  # (the first CTA has a few sequences)
+    assert not np.array_equal(out[:2], good[:2])
+    c.err.zero_()
+    out, _, e = c.run().got()
+    assert e == 0
+    np.testing.assert_array_equal(out, good)

@@ -101,6 +101,21 @@ def test_merge_of_a_bad_lse_is_nan(bad):
     assert (out[1] == 1).all() and lo[1].isfinite().all()
 
 
+def test_merge_of_more_tokens_than_one_launch_takes():
+    """2^31 - 1 tokens that share one row (strides of 0) of 16 bytes: two launches."""
+    parts = torch.tensor([[1.0] * 8, [3.0] * 8], dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros(2, device="cuda")
+    out, lo = torch.zeros(8, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, device="cuda")
+    T = 2 ** 31 - 1
+    ops.mla_merge_attn_states(parts.as_strided((2, T, 1, 8), (8, 0, 0, 1)),
+                              lse.as_strided((2, T, 1), (1, 0, 0)),
+                              out.as_strided((T, 1, 8), (0, 0, 1)),
+                              lse_out=lo.as_strided((T, 1), (0, 0)))
+    torch.cuda.synchronize()
+    assert (out == 2).all()
+    assert abs(float(lo) - np.log(2)) < 4 * R.FP32_HALF
+
+
 def test_merge_refuses_host_memory():
     p = torch.zeros(2, 1, 1, 8, device="cuda")
     with pytest.raises(ops.MlaError, match="lse must be device memory"):
