@@ -722,9 +722,8 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
   constexpr int kG = kC / 8;    // a thread has the rows 8 j + 2 (lane % 4) + {0, 1} of them
   const int group = warp >> 2, w4 = warp & 3, col0 = group * kC;
   const uint32_t bars = smem + L::bars;
-  bool dead = false;  // a wait of this thread was given up
   auto wait = [&](uint32_t bar, uint32_t parity) {
-    dead |= !waiter(bar, parity);
+    waiter(bar, parity);
     __syncwarp();
   };
   const uint32_t sub = tmem + ((uint32_t)(w4 * 32) << 16);  // this warp's lanes
@@ -768,6 +767,7 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
     wait(bars + 8 * (L::kFull + st), (g / L::kStages) & 1);  // the key flags
     wait(bars + 8 * (L::kSFull + b), (g >> 1) & 1);
     tc::fence_after_sync();
+    const bool dead = waiter.given_up();  // (cheaper than each wait's answer)
     float x[kG][4];
     tc::ld_16x256<kG>(sub + b * L::kN + col0, reinterpret_cast<uint32_t*>(&x[0][0]));
     if constexpr (L::kF8) {
