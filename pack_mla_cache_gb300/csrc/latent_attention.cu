@@ -56,6 +56,7 @@
 #include <cuda.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "mla_device.cuh"
 #include "serving.h"
@@ -87,6 +88,11 @@ struct Lay {
   static constexpr int kChunks = kF8 ? 5 : 9;
   static constexpr int kTile = kChunks * kChunk;
   static constexpr int kStages = kF8 ? 4 : 2;
+  // Halves of a stage (chunks 0 to 3 and the rest) that fill and are freed by
+  // themselves.  At 64 query rows the chain load, scores, weights, outputs of the two
+  // stages is what takes the time, and a half's load overlaps the outputs of the other
+  // (2 chunks of 1024 tokens over 8192 rows: 638 us, 682 with whole stages).
+  static constexpr int kHalves = NR == 64 ? 2 : 1;
   static constexpr int kQBufs = NR <= (kF8 ? 16 : 32) ? 2 : 1;
   static constexpr int kQ = kChunks * kN * 128;
   static constexpr int kSoftWarps = NR == 16 ? 4 : 8;   // one or two groups of 4 warps
@@ -115,7 +121,7 @@ struct Lay {
   static constexpr int flags = qs + (kF8 ? kQBufs * NR * 4 : 0);  // uint8 [kStages][64]
   static constexpr int bars = flags + kStages * kKeys;
   // barriers, by index
-  static constexpr int kFull = 0, kEmpty = kStages, kQFull = 2 * kStages, kQEmpty = kQFull + 2,
+  static constexpr int kFull = 0, kEmpty = kStages * kHalves, kQFull = 2 * kEmpty, kQEmpty = kQFull + 2,
                        kSFull = kQEmpty + 2, kPFull = kSFull + 2, kPvDone = kPFull + 2,
                        kOFree = kPvDone + 2, kBars = kOFree + 1;
   static constexpr int misc = (bars + kBars * 8 + 15) / 16 * 16;
@@ -485,31 +491,47 @@ __device__ __forceinline__ uint32_t produce(const LatentAttnArgs& a, const CUten
     if (cur.valid) {
       const uint32_t g = step;
       const int st = g % L::kStages;
-      const uint32_t full = bars + 8 * (L::kFull + st), flags = smem + L::flags + st * kKeys;
-      if (g >= L::kStages && !__all_sync(0xFFFFFFFFu, wait(bars + 8 * (L::kEmpty + st),
-                                                           (g / L::kStages - 1) & 1)))
-        break;
+      const uint32_t full = bars + 8 * (L::kFull + st * L::kHalves), flags = smem + L::flags + st * kKeys;
+      // (the halves of a stage one after the other; rows need both)
+      auto freed = [&](int h) {
+        return g < L::kStages ||
+               __all_sync(0xFFFFFFFFu, wait(bars + 8 * (L::kEmpty + st * L::kHalves + h),
+                                            (g / L::kStages - 1) & 1));
+      };
+      if (!freed(0)) break;
       ++issued;
       const uint32_t base = smem + st * L::kTile;
       if (__builtin_expect(by_box(a, cur), 1)) {
         const bool ok = blk[0] >= 0 && blk[0] < a.num_blocks;
         if (!ok) errbits |= kErrBlockOOB;
         if (lane >= 28) sts_u32(flags + box_key, ok ? 0u : 0x01010101u * kAbsent);
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive_expect_tx(full, box_bytes);
-          mbar_arrive_n(full, 32);
+        bool gone = false;
+#pragma unroll 1
+        for (int h = 0; h < L::kHalves; ++h) {
+          // this warp's boxes of chunks 0 to 3 are those of the lanes below `boxes`
+          const bool both = L::kHalves == 1;
+          if (h > 0 && !freed(h)) {
+            gone = true;
+            break;
+          }
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive_expect_tx(full + 8 * h, both ? box_bytes : h ? box_bytes - kChunk : (uint32_t)kChunk);
+            mbar_arrive_n(full + 8 * h, 32);
+          }
+          __syncwarp();
+          if (box_chunk < L::kChunks && (both || (lane >= boxes) == (h > 0))) {
+            const int p = cur.kt * kKeys + box_key;
+            const int off = a.bs_shift >= 0 ? p & (a.block_size - 1) : p % a.block_size;
+            const int z = ok ? blk[0] : (int)a.num_blocks;  // outside the tensor: zeros
+            tc::tma_load3(base + box_chunk * kChunk + box_key * 128, &map,
+                          L::kF8 ? (box_chunk < 4 ? box_chunk * 128 : 448) : box_chunk * 64, off, z,
+                          full + 8 * h);
+          }
         }
-        __syncwarp();
-        if (box_chunk < L::kChunks) {
-          const int p = cur.kt * kKeys + box_key;
-          const int off = a.bs_shift >= 0 ? p & (a.block_size - 1) : p % a.block_size;
-          const int z = ok ? blk[0] : (int)a.num_blocks;  // outside the tensor: zeros
-          tc::tma_load3(base + box_chunk * kChunk + box_key * 128, &map,
-                        L::kF8 ? (box_chunk < 4 ? box_chunk * 128 : 448) : box_chunk * 64, off, z,
-                        full);
-        }
+        if (gone) break;
       } else {
+        if (L::kHalves > 1 && !freed(1)) break;
         // tokens of the query tile see different rows of this key tile
         const bool mixed = cur.least < cur.most && (cur.kt + 1) * kKeys > cur.least;
 #pragma unroll 1
@@ -545,11 +567,14 @@ __device__ __forceinline__ uint32_t produce(const LatentAttnArgs& a, const CUten
           if (col == 0) sts_u8(flags + row, flag);
         }
         __syncwarp();
-        if (mixed) {
-          if (lane == 0) mbar_arrive_n(full, 33);
-        } else {
-          if (lane == 0) mbar_arrive(full);
-          tc::cp_async_arrive(full);
+#pragma unroll
+        for (int h = 0; h < L::kHalves; ++h) {
+          if (mixed) {
+            if (lane == 0) mbar_arrive_n(full + 8 * h, 33);
+          } else {
+            if (lane == 0) mbar_arrive(full + 8 * h);
+            tc::cp_async_arrive(full + 8 * h);
+          }
         }
       }
       if (__builtin_expect(cur.first, 0)) {  // the query, behind the first rows
@@ -584,7 +609,7 @@ __device__ __forceinline__ uint32_t produce(const LatentAttnArgs& a, const CUten
 // of code, and fetching it cost as much again.)
 template <int FMT, int NR>
 __device__ __forceinline__ void issue_scores(uint32_t smem, uint32_t tmem, bool one, int stage,
-                                             int qbuf, int sbuf, bool last) {
+                                             int qbuf, int sbuf, int half, bool last) {
   using L = Lay<FMT, NR>;
   constexpr uint32_t kId =
       tc::instr_desc(kKeys, L::kN, false, FMT == kE4M3 ? 0 : 1, L::kF8 ? 0 : 1);
@@ -594,14 +619,25 @@ __device__ __forceinline__ void issue_scores(uint32_t smem, uint32_t tmem, bool 
   const uint64_t qa = tc::smem_desc(smem + L::q + qb * L::kQ, 0, 1024);
   const uint32_t d = tmem + sb * L::kN;
   // a k step is 32 bytes of a row
+  auto chunks = [&](auto from, auto to) {
 #pragma unroll 1
-  for (int c = 0; c < (L::kF8 ? 4 : 9); ++c)
+    for (int c = from; c < to; ++c)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint64_t ak = ka + (c * kChunk >> 4) + 2 * k, bk = qa + (c * L::kN * 128 >> 4) + 2 * k;
-      if constexpr (L::kF8) tc::mma_fp8(one, d, ak, bk, kId, c + k > 0);
-      else tc::mma_bf16(one, d, ak, bk, kId, c + k > 0);
-    }
+      for (int k = 0; k < 4; ++k) {
+        const uint64_t ak = ka + (c * kChunk >> 4) + 2 * k, bk = qa + (c * L::kN * 128 >> 4) + 2 * k;
+        if constexpr (L::kF8) tc::mma_fp8(one, d, ak, bk, kId, c + k > 0);
+        else tc::mma_bf16(one, d, ak, bk, kId, c + k > 0);
+      }
+  };
+  using std::integral_constant;
+  if (L::kHalves == 1) {
+    chunks(integral_constant<int, 0>(), integral_constant<int, L::kF8 ? 4 : 9>());
+  } else if (half == 0) {
+    chunks(integral_constant<int, 0>(), integral_constant<int, 4>());
+    return;
+  } else {
+    chunks(integral_constant<int, 4>(), integral_constant<int, 9>());
+  }
   // the fp8 rotary columns are the upper half of their chunk, the lower half of the query's
   if constexpr (L::kF8)
 #pragma unroll
@@ -622,16 +658,19 @@ __device__ __forceinline__ void issue_outputs(uint32_t smem, uint32_t tmem, bool
   const uint64_t va = tc::smem_desc(smem + st * L::kTile, L::kF8 ? 0 : kChunk, 1024);
   const uint64_t pa = tc::smem_desc(smem + L::p + (pb & (L::kPBufs - 1)) * L::kP, 0, 1024);
   constexpr int kDims = L::kF8 ? kChunk : 2 * kChunk, kStep = L::kF8 ? 4096 : 2048;
-#pragma unroll 1
-  for (int b = 0; b < 4; ++b)
 #pragma unroll
-    for (int k = 0; k < (L::kF8 ? 2 : 4); ++k) {
-      const uint32_t d = tmem + L::kO + b * L::kN;
-      const uint64_t ak = va + (b * kDims >> 4) + k * (kStep >> 4), bk = pa + 2 * k;
-      if constexpr (L::kF8) tc::mma_fp8(one, d, ak, bk, kId, k > 0 || !first);
-      else tc::mma_bf16(one, d, ak, bk, kId, k > 0 || !first);
-    }
-  tc::commit(one, smem + L::bars + 8 * (L::kEmpty + st));
+  for (int h = 0; h < L::kHalves; ++h) {
+#pragma unroll 1
+    for (int b = h * 2; b < (h + 1 == L::kHalves ? 4 : 2); ++b)
+#pragma unroll
+      for (int k = 0; k < (L::kF8 ? 2 : 4); ++k) {
+        const uint32_t d = tmem + L::kO + b * L::kN;
+        const uint64_t ak = va + (b * kDims >> 4) + k * (kStep >> 4), bk = pa + 2 * k;
+        if constexpr (L::kF8) tc::mma_fp8(one, d, ak, bk, kId, k > 0 || !first);
+        else tc::mma_bf16(one, d, ak, bk, kId, k > 0 || !first);
+      }
+    tc::commit(one, smem + L::bars + 8 * (L::kEmpty + st * L::kHalves + h));
+  }
   tc::commit(one, smem + L::bars + 8 * (L::kPvDone + pb));
 }
 
@@ -656,7 +695,7 @@ __device__ __forceinline__ void score_role(const LatentAttnArgs& a, const Run& r
     const int qb = item % L::kQBufs, st = g % L::kStages;
     bool ok = !t.first || wait(L::kQFull + qb, item / L::kQBufs);
     if (g >= 2) ok &= wait(L::kPFull + (g & 1), (g - 2) >> 1);  // the score buffer is read
-    ok &= wait(L::kFull + st, g / L::kStages);
+    ok &= wait(L::kFull + st * L::kHalves, g / L::kStages);
     if (!__all_sync(0xFFFFFFFFu, ok)) break;
     // Queries, and rows that do not come by TMA, are written by ordinary and
     // asynchronous stores of the producers; the fence towards the tensor core's reads
@@ -664,7 +703,12 @@ __device__ __forceinline__ void score_role(const LatentAttnArgs& a, const Run& r
     // loads in flight).
     if (t.first || !by_box(a, t)) tc::fence_smem_async();
     tc::fence_after_sync();
-    issue_scores<FMT, NR>(smem, tmem, one, st, qb, g & 1, t.last);
+    issue_scores<FMT, NR>(smem, tmem, one, st, qb, g & 1, 0, t.last);
+    if constexpr (L::kHalves > 1) {
+      if (!__all_sync(0xFFFFFFFFu, wait(L::kFull + st * L::kHalves + 1, g / L::kStages))) break;
+      tc::fence_after_sync();
+      issue_scores<FMT, NR>(smem, tmem, one, st, qb, g & 1, 1, t.last);
+    }
     item += t.last;
   }
 }
@@ -764,7 +808,7 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
     }
     const int b = g & 1;
     const int st = g % L::kStages;
-    wait(bars + 8 * (L::kFull + st), (g / L::kStages) & 1);  // the key flags
+    wait(bars + 8 * (L::kFull + (st + 1) * L::kHalves - 1), (g / L::kStages) & 1);  // the key flags
     wait(bars + 8 * (L::kSFull + b), (g >> 1) & 1);
     tc::fence_after_sync();
     const bool dead = waiter.given_up();  // (cheaper than each wait's answer)
@@ -1198,9 +1242,11 @@ __device__ __noinline__ void settle(uint32_t smem, uint32_t issued, uint64_t lim
   using L = Lay<FMT, NR>;
   const uint64_t since = global_ns();
   for (uint32_t g = issued > L::kStages ? issued - L::kStages : 0; g < issued; ++g)
-    while (!mbar_try_wait(smem + L::bars + 8 * (L::kFull + g % L::kStages), (g / L::kStages) & 1) &&
-           global_ns() - since <= limit) {
-    }
+    for (int h = 0; h < L::kHalves; ++h)
+      while (!mbar_try_wait(smem + L::bars + 8 * (L::kFull + g % L::kStages * L::kHalves + h),
+                            (g / L::kStages) & 1) &&
+             global_ns() - since <= limit) {
+      }
   while (global_ns() - since <= 1000000) {
   }
 }
@@ -1218,9 +1264,9 @@ __global__ void __launch_bounds__(Lay<FMT, NR>::kThreads, 1)
   if (threadIdx.x == 0) {
     m.abort = 0;
     const uint32_t bars = smem + L::bars;
-    for (int i = 0; i < L::kStages; ++i) {
+    for (int i = 0; i < L::kStages * L::kHalves; ++i) {
       // each producer warp's key flags, and each thread's row copies
-      const bool stall = blockIdx.x == 0 && a.stall_stage == i + 1;  // one arrival too many
+      const bool stall = blockIdx.x == 0 && a.stall_stage == i / L::kHalves + 1;  // one arrival too many
       mbar_init(bars + 8 * (L::kFull + i), kProdWarps + kProdThreads + (stall ? 1 : 0));
       mbar_init(bars + 8 * (L::kEmpty + i), 1);
     }
