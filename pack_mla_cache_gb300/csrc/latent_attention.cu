@@ -397,14 +397,16 @@ __device__ __forceinline__ void load_q(const LatentAttnArgs& a, const Tile& q, u
 // q1)).  q1 + q2 / 16 has every bit of a bf16 down to 2^-14 of the largest, and
 // is off by at most 2^-21 of it below.  A row with a NaN or an infinity gets NaN
 // as its inverse scale.  8 lanes take a row, 16 bytes of every chunk each, so a
-// tile of 16 rows costs the four warps one round of loads.
-template <int NR>
+// tile of 16 rows costs four warps one round of loads.  The producers do it, but for a
+// CTA's first query tile: there the kWarps softmax warps have nothing else to do (and the
+// producers did it behind the first rows, 5000 cycles into the kernel).
+template <int NR, int kWarps>
 __device__ __forceinline__ void split_q(const LatentAttnArgs& a, const Tile& q, uint32_t dst,
                                         uint32_t scales, uint32_t bar, int pw, int lane) {
   const uint32_t rows = (uint32_t)q.ntok * (uint32_t)a.num_heads;
   const int col = lane & 7;
 #pragma unroll 1
-  for (int r = pw * 4 + (lane >> 3); r < NR; r += kProdWarps * 4) {
+  for (int r = pw * 4 + (lane >> 3); r < NR; r += kWarps * 4) {
     const uint32_t row = (uint32_t)q.qt * NR + r;
     const bool ok = row < rows;
     const int tok = ok ? token_of(a, row) : 0;
@@ -451,7 +453,7 @@ __device__ __forceinline__ void split_q(const LatentAttnArgs& a, const Tile& q, 
       sts_u32(scales + 4 * r, top >= 0x7F80u ? 0x7FC00000u : (e - 7u) << 23);  // 2^(e - 134)
   }
   __syncwarp();
-  if (lane == 0) mbar_arrive_n(bar, 32);
+  if (lane == 0) mbar_arrive_n(bar, kProdThreads / kWarps);
 }
 
 // Returns the key tiles whose copies were issued.
@@ -582,8 +584,10 @@ __device__ __forceinline__ uint32_t produce(const LatentAttnArgs& a, const CUten
         const uint32_t n = item / L::kQBufs;
         if (n > 0 && !__all_sync(0xFFFFFFFFu, wait(bars + 8 * (L::kQEmpty + b), (n - 1) & 1))) break;
         const uint32_t dst = smem + L::q + b * L::kQ, bar = bars + 8 * (L::kQFull + b);
-        if constexpr (L::kF8) split_q<NR>(a, cur, dst, smem + L::qs + b * NR * 4, bar, pw, lane);
-        else load_q<NR>(a, cur, dst, bar, pw, lane);
+        if constexpr (L::kF8) {
+          if (item > 0)
+            split_q<NR, kProdWarps>(a, cur, dst, smem + L::qs + b * NR * 4, bar, pw, lane);
+        } else load_q<NR>(a, cur, dst, bar, pw, lane);
         ++item;
       }
     }
@@ -789,7 +793,11 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
     if (t.first) {
       kt_begin = t.kt;
       const uint32_t scales = smem + L::qs + (item % L::kQBufs) * NR * 4;
-      if constexpr (L::kF8) wait(bars + 8 * (L::kQFull + item % L::kQBufs), (item / L::kQBufs) & 1);
+      if constexpr (L::kF8) {
+        if (item == 0)
+          split_q<NR, L::kSoftWarps>(a, t, smem + L::q, scales, bars + 8 * L::kQFull, warp, lane);
+        wait(bars + 8 * (L::kQFull + item % L::kQBufs), (item / L::kQBufs) & 1);
+      }
 #pragma unroll
       for (int j = 0; j < kG; ++j)
 #pragma unroll
@@ -808,8 +816,16 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
     }
     const int b = g & 1;
     const int st = g % L::kStages;
-    wait(bars + 8 * (L::kFull + (st + 1) * L::kHalves - 1), (g / L::kStages) & 1);  // the key flags
-    wait(bars + 8 * (L::kSFull + b), (g >> 1) & 1);
+    // The key flags, the scores, and an early look whether P's buffer is free (below): the
+    // three answers are asked for together.
+    const uint32_t full = bars + 8 * (L::kFull + (st + 1) * L::kHalves - 1), full_at = (g / L::kStages) & 1;
+    const uint32_t o = g - L::kPBufs;  // the tile whose outputs free the buffer
+    const bool flagged = mbar_try_wait(full, full_at);
+    const bool scored = mbar_try_wait(bars + 8 * (L::kSFull + b), (g >> 1) & 1);
+    const bool unused = g < L::kPBufs || mbar_test(bars + 8 * (L::kPvDone + (o & 1)), (o >> 1) & 1);
+    if (!flagged) waiter(full, full_at);
+    if (!scored) waiter(bars + 8 * (L::kSFull + b), (g >> 1) & 1);
+    __syncwarp();
     tc::fence_after_sync();
     const bool dead = waiter.given_up();  // (cheaper than each wait's answer)
     float x[kG][4];
@@ -854,10 +870,8 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
         grown |= fmaxf(x[j][e], x[j][e + 2]) > mu[j][e] + L::kGrow;
     grown = soft_any(group, grown | dead);
     // P's buffer is free when the outputs of the tile that had it are done
-    if (g >= L::kPBufs) {
-      const uint32_t o = g - L::kPBufs;
-      wait(bars + 8 * (L::kPvDone + (o & 1)), (o >> 1) & 1);
-    }
+    if (!unused) waiter(bars + 8 * (L::kPvDone + (o & 1)), (o >> 1) & 1);
+    __syncwarp();
     if (__builtin_expect(grown, 0)) {
       // maximum over the tile's 64 keys: in the warp, then across the four warps
       float* mine = red + warp * kC;
@@ -1098,63 +1112,63 @@ __device__ __forceinline__ int64_t scan64(int64_t v, int lane) {  // inclusive, 
   return v;
 }
 
-// This CTA's run.  Up to 128 sequences of at most 8 query tiles: every warp finds
-// it by itself, 32 sequences at a time, without a barrier.
-constexpr int kSmallSeqs = 128, kSmallTiles = 8;
+// This CTA's run.  Up to 128 sequences of at most 8 query tiles: every warp finds it
+// by itself without a barrier, a lane looking at four neighbouring sequences.
+constexpr int kLaneSeqs = 4, kSmallTiles = 8;
 template <int NR, int kSwitch>
 __device__ __forceinline__ bool schedule_small(const LatentAttnArgs& a, int lane, Run& r,
                                                uint32_t& errbits) {
-  if (a.num_seqs > kSmallSeqs) return false;
-  int64_t before = 0;  // units of the sequences in front of these 32
-  int s = lane;
-  int64_t off = 0;
-  uint32_t has = 0;
-  Seq q;
-  // first round over the sequences: their units; second: the one with the first unit
-#pragma unroll 1
-  for (int round = 0, base = 0;; ) {
-    s = base + lane;
-    q.nqt = 0;
-    if (s < a.num_seqs) q = load_seq<NR>(a, s);
-    if (__any_sync(0xFFFFFFFFu, q.nqt > kSmallTiles)) return false;
-    int64_t u = 0;
-#pragma unroll 1
-    for (int qt = 0; qt < q.nqt; ++qt) u += kSwitch + key_tiles(most_seen<NR>(a, q, qt));
-    const int64_t inc = scan64(u, lane);
-    if (round == 1) {
-      off = r.begin - before - (inc - u);
-      has = __ballot_sync(0xFFFFFFFFu, off >= 0 && off < u);
-      if (has != 0) break;
-    } else if (q.nqt > 0 && over_room(a, q)) {
-      errbits |= kErrBlockOOB;
-    }
-    before += __shfl_sync(0xFFFFFFFFu, inc, 31);
-    base += 32;
-    if (base >= a.num_seqs) {
-      if (round == 1) return true;  // (not reached: some sequence has the unit)
-      cut(before, r);
-      r.kt = 0;
-      if (r.count == 0) return true;
-      round = 1;
-      base = 0;
-      before = 0;
-    }
+  if (a.num_seqs > 32 * kLaneSeqs) return false;
+  const int per = (a.num_seqs + 31) >> 5, s0 = lane * per;  // this lane's sequences
+  Seq q[kLaneSeqs];
+#pragma unroll
+  for (int i = 0; i < kLaneSeqs; ++i) {
+    q[i].nqt = 0;
+    if (i < per && s0 + i < a.num_seqs) q[i] = load_seq<NR>(a, s0 + i);
   }
-  int qt = 0;
-  if (has >> lane & 1) {
+  bool large = false;
+  int u[kLaneSeqs], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kLaneSeqs; ++i) {
+    u[i] = 0;
+    if (q[i].nqt == 0) continue;
+    // the last query tile has the most key tiles: the sums stay below 2^31
+    large |= q[i].nqt > kSmallTiles || most_seen<NR>(a, q[i], q[i].nqt - 1) > 1 << 24;
+    if (over_room(a, q[i])) errbits |= kErrBlockOOB;
 #pragma unroll 1
-    for (;; ++qt) {
-      const int k = kSwitch + key_tiles(most_seen<NR>(a, q, qt));
-      if (off < k) break;
-      off -= k;
-    }
+    for (int qt = 0; qt < min(q[i].nqt, kSmallTiles); ++qt)
+      u[i] += kSwitch + key_tiles(most_seen<NR>(a, q[i], qt));
+    sum += u[i];
   }
-  const int from = __ffs(has) - 1;
-  auto all = [&](int v) { return __shfl_sync(0xFFFFFFFFu, v, from); };
-  r.s = all(s);
-  r.qt = all(qt);
-  r.kt = all((int)off) - kSwitch;
-  r.q = Seq{all(q.t0), all(q.ntok), all(q.c1), all(q.kv), all(q.nqt)};
+  if (__any_sync(0xFFFFFFFFu, large)) return false;
+  int inc = sum;  // inclusive sum over the warp
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  cut(__shfl_sync(0xFFFFFFFFu, inc, 31), r);
+  r.kt = 0;
+  if (r.count == 0) return true;
+  // the lane, sequence and query tile with the run's first unit
+  int off = (int)r.begin - (inc - sum), s = s0;
+  const int from = __ffs(__ballot_sync(0xFFFFFFFFu, off >= 0 && off < sum)) - 1;
+#pragma unroll
+  for (int i = 0; i + 1 < kLaneSeqs; ++i)
+    if (s == s0 + i && off >= u[i]) {
+      off -= u[i];
+      ++s;
+    }
+  r.s = __shfl_sync(0xFFFFFFFFu, s, from);
+  off = __shfl_sync(0xFFFFFFFFu, off, from);
+  r.q = load_seq<NR>(a, r.s);
+#pragma unroll 1
+  for (r.qt = 0;; ++r.qt) {
+    const int k = kSwitch + key_tiles(most_seen<NR>(a, r.q, r.qt));
+    if (off < k) break;
+    off -= k;
+  }
+  r.kt = off - kSwitch;
   return true;
 }
 

@@ -315,6 +315,21 @@ def test_many_sequences():
     check(Call(pg, q, cu_of([1] * 700), kv).run(), q)
 
 
+@pytest.mark.parametrize("n", [31, 32, 33, 63, 96, 97, 128, 129])
+def test_batch_sizes_with_empty_sequences(n):
+    """Batches of every shape that the CTAs cut their runs from: some sequences have no tokens,
+    some no rows, one has several query tiles."""
+    rng = np.random.default_rng(n)
+    kv = rng.integers(0, 200, n)
+    ql = rng.integers(0, 3, n)
+    ql[n // 2] = 9
+    ql[0], kv[0] = 0, 50
+    kv[n - 1] = 700
+    pg = R.paged(list(kv), n % 3, 16, seed=n)
+    q = R.queries(int(ql.sum()), 8)
+    check(Call(pg, q, cu_of([int(x) for x in ql]), [int(x) for x in kv]).run(), q)
+
+
 def test_most_sequences():
     kv = [1 + (i % 7) for i in range(4096)]
     pg = R.paged(kv, 0, 16)
