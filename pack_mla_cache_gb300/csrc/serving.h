@@ -68,6 +68,8 @@ struct LatentAttnArgs {
   int64_t block_stride, entry_stride, num_blocks;
   int32_t block_size, bs_shift;  // bs_shift = log2(block_size) or -1
   int32_t box_rows;              // entries of a TMA box (set by the launch), 0 = row copies
+  int32_t box_shift;             // log2 of the boxes that a key tile's column of entries takes
+  bool stream_rows;              // cache rows leave L2 first (set by the launch)
   const int32_t* block_table;
   int64_t bt_stride;  // elements
   int32_t room;       // rows that a table row can hold (below 2^31 - 127)

@@ -182,15 +182,22 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool v
                "r"(valid ? 16u : 0u)
                : "memory");
 }
+// The L2 policy of loads: first to be evicted, or as usual.
+__device__ __forceinline__ uint64_t l2_policy(bool first) {
+  uint64_t p;
+  if (first) asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  else asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
 // One box of a 3-dimensional tensor map to shared memory, completing on `bar`
 // (parts outside the tensor are filled with zeros; x * element size a multiple of
 // 16 bytes).
 __device__ __forceinline__ void tma_load3(uint32_t dst, const void* map, int x, int y, int z,
-                                          uint32_t bar) {
+                                          uint32_t bar, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
-      "[%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
       : "memory");
 }
 // Arrive on `bar` when this thread's cp_async16 so far are done.
