@@ -679,6 +679,26 @@ __device__ __forceinline__ void issue_outputs(uint32_t smem, uint32_t tmem, bool
   tc::commit(one, smem + L::bars + 8 * (L::kPvDone + pb));
 }
 
+struct Workspace {
+  Split* split;   // [ctas]
+  float *m, *l;   // [2 ctas][NR]: running maximum (log2 units) and sum
+  float* o;       // [2 ctas][NR][512]: unnormalised sums
+};
+template <int NR>
+__host__ __device__ inline Workspace workspace_of(uint8_t* p, int ctas) {
+  Workspace w;
+  w.split = reinterpret_cast<Split*>(p);
+  w.m = reinterpret_cast<float*>(p + (int64_t)ctas * sizeof(Split));
+  w.l = w.m + (int64_t)ctas * 2 * NR;
+  w.o = w.l + (int64_t)ctas * 2 * NR;
+  return w;
+}
+// The CTA whose run has unit u.
+__device__ __noinline__ int cta_of(int64_t u, int64_t each, int extra) {
+  const int64_t longer = (each + 1) * extra;  // units of the runs of each + 1
+  return (int)(u < longer ? u / (each + 1) : extra + (u - longer) / each);
+}
+
 // One warp issues the scores, another the outputs, each as soon as its operands
 // are there: outputs free the stage that the rows behind need, and from one warp
 // they would wait for the scores of the next tile (1000 to 1300 cycles) or for its
@@ -720,7 +740,8 @@ __device__ __forceinline__ void score_role(const LatentAttnArgs& a, const Run& r
 
 template <int FMT, int NR>
 __device__ __forceinline__ void output_role(const LatentAttnArgs& a, const Run& run, uint32_t smem,
-                                            uint32_t tmem, const Waiter& waiter) {
+                                            uint32_t tmem, const Waiter& waiter, int lane,
+                                            const Workspace& ws) {
   using L = Lay<FMT, NR>;
   const uint32_t bars = smem + L::bars;
   auto wait = [&](int bar, uint32_t phase) { return waiter(bars + 8 * bar, phase & 1); };
@@ -738,30 +759,23 @@ __device__ __forceinline__ void output_role(const LatentAttnArgs& a, const Run& 
     tc::fence_after_sync();
     issue_outputs<FMT, NR>(smem, tmem, one, g % L::kStages, g & 1, t.first);
     item += t.last;
+    if (__builtin_expect(t.last && t.kt + 1 < t.nkt && lane == 0, 0)) {
+      // The run ends inside the query tile: for the join.  (This warp has nothing else to
+      // do now; the softmax warps spent 900 cycles on the divisions.)  The run's last unit
+      // is number t.kt of the tile's.
+      const int64_t u0 = run.begin + run.count - 1 - t.kt;
+      const int c0 = cta_of(u0, run.each, run.extra);
+      const int c1 = cta_of(u0 + t.nkt - 1, run.each, run.extra);
+      const uint32_t row = (uint32_t)t.qt * NR;
+      const int rows = (int)min((uint32_t)NR, (uint32_t)t.ntok * (uint32_t)a.num_heads - row);
+      const int dt = token_of(a, row);
+      ws.split[blockIdx.x] = Split{t.t0 + dt, (int)row - dt * a.num_heads, (uint16_t)rows,
+                                   (uint16_t)(c1 - c0 + 1), c0};
+    }
   }
 }
 
 // ----------------------------------------------------------- softmax and output
-struct Workspace {
-  Split* split;   // [ctas]
-  float *m, *l;   // [2 ctas][NR]: running maximum (log2 units) and sum
-  float* o;       // [2 ctas][NR][512]: unnormalised sums
-};
-template <int NR>
-__host__ __device__ inline Workspace workspace_of(uint8_t* p, int ctas) {
-  Workspace w;
-  w.split = reinterpret_cast<Split*>(p);
-  w.m = reinterpret_cast<float*>(p + (int64_t)ctas * sizeof(Split));
-  w.l = w.m + (int64_t)ctas * 2 * NR;
-  w.o = w.l + (int64_t)ctas * 2 * NR;
-  return w;
-}
-// The CTA whose run has unit u.
-__device__ __noinline__ int cta_of(int64_t u, int64_t each, int extra) {
-  const int64_t longer = (each + 1) * extra;  // units of the runs of each + 1
-  return (int)(u < longer ? u / (each + 1) : extra + (u - longer) / each);
-}
-
 template <int FMT, int NR>
 __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, uint32_t smem,
                                        uint32_t tmem, const Waiter& waiter, int warp, int lane,
@@ -1010,9 +1024,8 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
     const bool whole = kt_begin == 0 && t.kt + 1 == t.nkt;
     const int64_t slot = 2 * (int64_t)blockIdx.x + (kt_begin == 0 ? 1 : 0);
     const uint32_t first = (uint32_t)t.qt * NR;
-    // rows of the tile that exist, and of them this group's (none or less: not one)
-    const int rows = (int)min((uint32_t)NR, (uint32_t)t.ntok * (uint32_t)a.num_heads - first);
-    const int nv = min(rows - col0, kC);
+    // this group's rows that exist (none or less: not one)
+    const int nv = min((int)min((uint32_t)NR, (uint32_t)t.ntok * (uint32_t)a.num_heads - first) - col0, kC);
     // token and head of this group's first row
     const int dt0 = token_of(a, first + col0), tok0 = t.t0 + dt0;
     const int head0 = (int)(first + col0) - dt0 * a.num_heads;
@@ -1038,13 +1051,6 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
       }
     }
     __syncwarp();
-    if (t.kt + 1 < t.nkt && warp == 0 && lane == 0 && !lost) {
-      // units of the query tile: this run's last one is number t.kt of them
-      const int64_t u0 = run.begin + run.count - 1 - t.kt;
-      const int c0 = cta_of(u0, run.each, run.extra);
-      const int c1 = cta_of(u0 + t.nkt - 1, run.each, run.extra);
-      ws.split[blockIdx.x] = Split{tok0, head0, (uint16_t)rows, (uint16_t)(c1 - c0 + 1), c0};
-    }
 #pragma unroll 1
     for (int n0 = 0; n0 < nv; n0 += 16) {
 #pragma unroll 1
@@ -1323,7 +1329,7 @@ __global__ void __launch_bounds__(Lay<FMT, NR>::kThreads, 1)
     else if (warp == L::kScoreWarp)
       score_role<FMT, NR>(a, run, smem, tmem, wait);
     else
-      output_role<FMT, NR>(a, run, smem, tmem, wait);
+      output_role<FMT, NR>(a, run, smem, tmem, wait, lane, ws);
   }
   __syncwarp();
   if (a.err) {
