@@ -15,6 +15,12 @@
 // partial sums in the workspace, which a second small launch joins in the
 // order of the CTAs (no atomics: equal calls give equal bits).
 //
+// Measured (replayed from a graph, without the profiler; 16 heads, 64-row blocks): one
+// new token of 4 sequences over 131072 bf16 rows 99.9 us (6.05 TB/s), of 64 over 130 to
+// 16384 e4m3 rows 58.0 us (5.4 TB/s), of one over 2047 bf16 rows 10.4 us; 1024 new
+// tokens of 2 over 8192 bf16 rows 645 us (849 TFLOP/s).  About 10 us of a call are fixed
+// (finding the run and the first rows 3, filling and draining the pipeline 4, the join 3).
+//
 // Both products are computed transposed, so that few query rows (a decode
 // batch has 16 per token) are the N dimension of the tensor core's tile and no
 // row of it is wasted:
@@ -72,7 +78,9 @@ constexpr int kProdThreads = kProdWarps * 32;
 constexpr int kRank = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kMinUnits = 2;              // a CTA takes at least this many units
+// A CTA takes at least this many units: one decode over 2047 rows took 11.3, 10.8 and
+// 12.9 us with 1, 2 and 3 (fewer: more partial sums to join; more: fewer SMs).
+constexpr int kMinUnits = 2;
 constexpr float kQ2 = 0.0625f;            // query parts: q = q1 + q2 / 16
 constexpr float kP2 = 1.0f / 512.0f;      // weight parts: p = p1 + p2 / 512
 
@@ -1431,6 +1439,9 @@ __global__ void __launch_bounds__(kJoinThreads, 2) latent_join_kernel(const Late
 
 // Rows of a query tile: the average rows (tokens x heads) per sequence decide.
 // fp8 tiles stop at 32: their split sums take two columns of tensor memory each.
+// Measured: 16 rows per sequence 57.9 us in tiles of 16 (64.7 in tiles of 32; 64 ragged
+// e4m3 decodes), 64 e5m2 rows 46.6 in tiles of 32 (60.7 in 16), 128 bf16 rows 47.3 and
+// 16384 rows 645 in tiles of 64 (61.9 and 1127 in 32).
 inline int tile_rows(int32_t num_tokens, int32_t num_heads, int32_t num_seqs, bool fp8) {
   const int64_t rows = (int64_t)((num_tokens + num_seqs - 1) / num_seqs) * num_heads;
   return rows <= 16 ? 16 : rows <= 32 || fp8 ? 32 : 64;
@@ -1438,9 +1449,10 @@ inline int tile_rows(int32_t num_tokens, int32_t num_heads, int32_t num_seqs, bo
 
 // The cache as a tensor of (column, entry, block), read in boxes of one chunk of
 // `rows` entries.  Without a box (entries per block not a multiple of 8, or sizes
-// that a tensor map does not hold) rows are copied one by one.  Returns the
-// entries of a box, or 0.  (All chunks of a tile as one box of a 4-dimensional map
-// took the same time.)
+// that a tensor map does not hold) rows are copied one by one: 64 ragged e4m3 decodes
+// then take 93.5 us instead of 57.9, 4 x 131072 bf16 rows 107 instead of 99.9.
+// Returns the entries of a box, or 0.  (All chunks of a tile as one box of a
+// 4-dimensional map took the same time.)
 int box_map(const LatentAttnArgs& a, bool fp8, CUtensorMap* map) {
   int rows = kKeys;
   while (a.block_size % rows) rows >>= 1;

