@@ -142,6 +142,17 @@ def test_page_sizes(fmt, block):
     check(Call(pg, q, cu_of(ql), kv).run(), q, err=ops.MLA_ERRBIT_BLOCK_OOB if missing else 0)
 
 
+@pytest.mark.parametrize("block", [7, 8, 16, 24, 32, 64])
+def test_page_sizes_at_64_query_rows(block):
+    """The widest query tiles take a stage in halves: pages of every size, a page missing, mixed
+    tiles of a few new tokens, two query tiles per sequence."""
+    kv, ql = [391, 64, 1000, 130], [1, 2, 3, 1]
+    pg = R.paged(kv, 0, block, seed=block)
+    pg.table[2, 3] = pg.num_blocks
+    q = R.queries(7, 96)
+    check(Call(pg, q, cu_of(ql), kv).run(), q, err=ops.MLA_ERRBIT_BLOCK_OOB)
+
+
 @pytest.mark.parametrize("seed", range(30))
 def test_random_batches(seed):
     """Batches of every mixture: head counts, new tokens, lengths around the tile and
@@ -462,3 +473,37 @@ def test_waits_that_run_out_return_and_report(fmt, heads, stage):
     out, _, e = c.run().got()
     assert e == 0
     np.testing.assert_array_equal(out, good)
+
+
+def test_two_graphs_share_a_workspace():
+    """Replayed in turn on one stream; each gives its own result every time."""
+    calls, want = [], []
+    for seed, kv in ((3, [900, 40, 2000]), (4, [70, 1500, 333])):
+        pg = R.paged(kv, 1, 64, seed=seed)
+        q = R.queries(3, 16, seed=seed)
+        calls.append(Call(pg, q, [0, 1, 2, 3], kv))
+    calls[1].ws = calls[0].ws
+    for c in calls:
+        want.append(c.run().got()[:2])
+    graphs = []
+    for c in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.run()
+        graphs.append(g)
+    for i in (0, 1, 1, 0, 1, 0, 0):
+        calls[i].out.fill_(7.0)
+        graphs[i].replay()
+        out, lse, e = calls[i].got()
+        np.testing.assert_array_equal(out, want[i][0])
+        np.testing.assert_array_equal(lse, want[i][1])
+        assert e == 0
+
+
+def test_runs_that_start_and_end_between_query_tiles():
+    """Equal short sequences, so that many CTAs' runs begin or end where a query tile does."""
+    for n, rows in ((152, 64), (304, 64), (76, 640), (151, 65), (500, 64 * 3)):
+        kv = [rows] * n
+        pg = R.paged(kv, 1, 64, seed=n)
+        q = R.queries(n, 16, seed=n)
+        check(Call(pg, q, cu_of([1] * n), kv).run(), q)
