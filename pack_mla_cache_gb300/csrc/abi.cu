@@ -945,7 +945,6 @@ mla_status_t mla_merge_attn_states(
   a.num_tokens = num_tokens;
   a.num_heads = num_heads;
   a.row_chunks = (int32_t)((int64_t)dim * es / 16);
-  a.by_chunks = mla::Divider::by((uint32_t)a.row_chunks);
   a.by_heads = mla::Divider::by((uint32_t)num_heads);
   a.out = static_cast<uint8_t*>(out);
   a.ots = out_token_stride * es;

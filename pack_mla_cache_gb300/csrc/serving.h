@@ -49,7 +49,8 @@ struct MergeArgs {
   int64_t lps, lts, lhs;
   int32_t num_parts, num_tokens, num_heads;
   int32_t row_chunks;  // 16-byte chunks of a row
-  Divider by_chunks, by_heads;
+  Divider by_units, by_heads;  // by_units (of a row) set by the launch
+  float shift;                 // log2 of the weights' scale, set by the launch
   uint8_t* out;
   int64_t ots, ohs;
   float* lse_out;  // may be null

@@ -284,3 +284,20 @@ def test_insert_fork_attend_merge(fmt):
         part_mag = np.abs(f(parts)).max(0) + mag
         bm = bo + 2 * (R.BF16_HALF + 2 * bl[..., None]) * part_mag * 2
         assert (np.abs(f(out) - ro) <= bm).all() and (np.abs(f(lse) - rl) <= 2 * bl).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("P,Dm", [(2, 64), (7, 24), (1024, 8)])
+def test_merge_of_the_largest_values_stays_finite(kind, P, Dm):
+    """The join of equal rows is the row, also near the type's largest value (half a step of
+    the type, and the weights' own rounding: 1024 additions of half a unit at most)."""
+    dt = TYPES[kind][0]
+    top = torch.finfo(dt).max * 0.99
+    parts = torch.full((P, 3, 2, Dm), top).to(dt).cuda()
+    lse = torch.zeros(P, 3, 2, device="cuda")
+    out, lo = torch.zeros(3, 2, Dm, dtype=dt, device="cuda"), torch.zeros(3, 2, device="cuda")
+    ops.mla_merge_attn_states(parts, lse, out, lse_out=lo)
+    want = float(parts[0, 0, 0, 0])
+    rel = TYPES[kind][1] + 2 * (P + 8) * R.FP32_HALF
+    assert (out.double() - want).abs().max().item() <= rel * want
+    assert (lo.double() - np.log(P)).abs().max().item() <= 8 * R.FP32_HALF * (1 + np.log(P))
