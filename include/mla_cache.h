@@ -613,7 +613,7 @@ mla_status_t mla_cache_copy_blocks(const int64_t* kv_cache_ptrs, int32_t num_lay
  *                       contents before and after a call mean nothing; calls that may run at the same time (on
  *                       two streams) need one each.
  * out, lse and workspace must not overlap each other or the inputs.
- * Scores times log2 e must be finite in fp32, and cache values below 2^90 in magnitude
+ * Scores times log2 e must be finite in fp32, and cache values below 2^80 in magnitude
  * (unnormalised sums are held in fp32).
  * The kernel's internal waits are bounded (2 s, which means a fault or a stalled
  * GPU); a block whose wait runs out stops issuing work, waits (bounded again) for
