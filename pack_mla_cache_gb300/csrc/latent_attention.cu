@@ -17,7 +17,7 @@
 //
 // Measured (replayed from a graph, without the profiler; 16 heads, 64-row blocks): one
 // new token of 4 sequences over 131072 bf16 rows 99.9 us (6.05 TB/s), of 64 over 130 to
-// 16384 e4m3 rows 58.0 us (5.4 TB/s), of one over 2047 bf16 rows 10.4 us; 1024 new
+// 16384 e4m3 rows 58.0 us (5.4 TB/s), of one over 2047 bf16 rows 10.1 us; 1024 new
 // tokens of 2 over 8192 bf16 rows 645 us (849 TFLOP/s).  About 10 us of a call are fixed
 // (finding the run and the first rows 3, filling and draining the pipeline 4, the join 3).
 //
@@ -1358,11 +1358,15 @@ __global__ void __launch_bounds__(Lay<FMT, NR>::kThreads, 1)
 }
 
 // ---------------------------------------------------- join of the split query tiles
-// Block (r, c) looks at what CTA c left.  With up to kFewParts partials the blocks
-// of the first CTA take four rows each, one per group of 128 threads (four dims a
-// thread); with more, the blocks of all its CTAs but the last take a row each, a
-// group a quarter of the partials.  (There are at least as many of them as rows:
-// kFewParts * NR / 4.)  So a block costs two dependent loads, whatever the batch.
+// Block (r, c) looks at what CTA c left.  The blocks of all CTAs of a split query tile
+// but the last (which noted another tile, or none) deal its rows out: one per group of
+// 128 threads (four dims a thread) with up to kFewParts partials, else one per block, a
+// group a quarter of the partials (there are at least kFewParts * NR / 8 of those, one
+// for every row).  So a block mostly costs two dependent loads, whatever the batch, and
+// the grid, NR / 8 blocks per CTA, is one to four rounds of resident blocks.  With NR / 4
+// and the rows of few partials left to the first CTA's, most blocks found nothing to do:
+// 32 verifications took 46.6 us (45.9 now), 16 decodes of 128 heads 47.2 (45.8), one
+// decode 10.5 (10.1).
 constexpr int kJoinGroups = 4;
 constexpr int kJoinThreads = kJoinGroups * 128;
 constexpr int kFewParts = 8;
@@ -1379,62 +1383,65 @@ __global__ void __launch_bounds__(kJoinThreads, 2) latent_join_kernel(const Late
   const Split sp = ws.split[blockIdx.y];
   const int c = sp.first;
   const bool few = sp.parts <= kFewParts;
-  const int n = few ? blockIdx.x * kJoinGroups + grp
-                    : ((int)blockIdx.y - c) * (NR / kJoinGroups) + (int)blockIdx.x;
-  if (few && (int)blockIdx.y != c) return;
+  const int blocks = (sp.parts - 1) * (int)gridDim.x;
+  int n = ((int)blockIdx.y - c) * (int)gridDim.x + (int)blockIdx.x;
+  if (few) n = n * kJoinGroups + grp;
   if (n >= sp.rows) return;  // the whole group, and the whole block when it is shared
   const float ks = FMT == kBF16 ? 1.0f : __ldg(a.k_scale);
-  float4 acc = make_float4(0, 0, 0, 0);
-  float sum = 0.0f, top = -INFINITY;
-  // joins `v` with weight sum lv and maximum mv to what is there
-  auto add = [&](const float4& v, float lv, float mv) {
-    const float m = fmaxf(top, mv), m0 = m == -INFINITY ? 0.0f : m;
-    const float f = ex2(top - m0), w = ex2(mv - m0);
-    acc.x = fmaf(acc.x, f, w * v.x);
-    acc.y = fmaf(acc.y, f, w * v.y);
-    acc.z = fmaf(acc.z, f, w * v.z);
-    acc.w = fmaf(acc.w, f, w * v.w);
-    sum = fmaf(sum, f, w * lv);
-    top = m;
-  };
-  // the first partial lies in the odd slot of CTA c, the others in the even ones behind
-  const int quarter = (sp.parts + kJoinGroups - 1) / kJoinGroups;
-  const int i0 = few ? 0 : min(grp * quarter, (int)sp.parts);
-  const int i1 = few ? sp.parts : min(i0 + quarter, (int)sp.parts);
+  do {
+    float4 acc = make_float4(0, 0, 0, 0);
+    float sum = 0.0f, top = -INFINITY;
+    // joins `v` with weight sum lv and maximum mv to what is there
+    auto add = [&](const float4& v, float lv, float mv) {
+      const float m = fmaxf(top, mv), m0 = m == -INFINITY ? 0.0f : m;
+      const float f = ex2(top - m0), w = ex2(mv - m0);
+      acc.x = fmaf(acc.x, f, w * v.x);
+      acc.y = fmaf(acc.y, f, w * v.y);
+      acc.z = fmaf(acc.z, f, w * v.z);
+      acc.w = fmaf(acc.w, f, w * v.w);
+      sum = fmaf(sum, f, w * lv);
+      top = m;
+    };
+    // the first partial lies in the odd slot of CTA c, the others in the even ones behind
+    const int quarter = (sp.parts + kJoinGroups - 1) / kJoinGroups;
+    const int i0 = few ? 0 : min(grp * quarter, (int)sp.parts);
+    const int i1 = few ? sp.parts : min(i0 + quarter, (int)sp.parts);
 #pragma unroll 1
-  for (int i = i0; i < i1; i += 4) {
-    float4 v[4];
-    float lv[4], mv[4];
+    for (int i = i0; i < i1; i += 4) {
+      float4 v[4];
+      float lv[4], mv[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int64_t row = (2 * (int64_t)(c + i + k) + (i + k == 0 ? 1 : 0)) * NR + n;
-      v[k] = make_float4(0, 0, 0, 0);
-      lv[k] = 0.0f;
-      mv[k] = -INFINITY;
-      if (i + k < i1) {
-        v[k] = __ldcs(reinterpret_cast<const float4*>(ws.o + row * kRank) + d4);
-        lv[k] = ws.l[row];
-        mv[k] = ws.m[row];
+      for (int k = 0; k < 4; ++k) {
+        const int64_t row = (2 * (int64_t)(c + i + k) + (i + k == 0 ? 1 : 0)) * NR + n;
+        v[k] = make_float4(0, 0, 0, 0);
+        lv[k] = 0.0f;
+        mv[k] = -INFINITY;
+        if (i + k < i1) {
+          v[k] = __ldcs(reinterpret_cast<const float4*>(ws.o + row * kRank) + d4);
+          lv[k] = ws.l[row];
+          mv[k] = ws.m[row];
+        }
       }
-    }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) add(v[k], lv[k], mv[k]);
-  }
-  if (!few) {
-    acc_s[grp][d4] = acc;
-    if (d4 == 0) sum_s[grp] = make_float2(sum, top);
-    __syncthreads();
-    if (grp != 0) return;
+      for (int k = 0; k < 4; ++k) add(v[k], lv[k], mv[k]);
+    }
+    if (!few) {
+      acc_s[grp][d4] = acc;
+      if (d4 == 0) sum_s[grp] = make_float2(sum, top);
+      __syncthreads();
+      if (grp != 0) return;
 #pragma unroll 1
-    for (int k = 1; k < kJoinGroups; ++k) add(acc_s[k][d4], sum_s[k].x, sum_s[k].y);
-  }
-  const int dt = token_of(a, sp.head0 + n);
-  const int64_t t = sp.tok0 + dt, h = sp.head0 + n - dt * a.num_heads;
-  const float inv = sum == 0.0f ? 0.0f : __fdividef(ks, sum);
-  st8(a.out + t * a.out_ts + h * a.out_hs + d4 * 8,
-      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv)));
-  if (d4 == 0 && a.lse)
-    a.lse[t * a.lse_ts + h * a.lse_hs] = sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * kLn2;
+      for (int k = 1; k < kJoinGroups; ++k) add(acc_s[k][d4], sum_s[k].x, sum_s[k].y);
+    }
+    const int dt = token_of(a, sp.head0 + n);
+    const int64_t t = sp.tok0 + dt, h = sp.head0 + n - dt * a.num_heads;
+    const float inv = sum == 0.0f ? 0.0f : __fdividef(ks, sum);
+    st8(a.out + t * a.out_ts + h * a.out_hs + d4 * 8,
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv)));
+    if (d4 == 0 && a.lse)
+      a.lse[t * a.lse_ts + h * a.lse_hs] = sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * kLn2;
+    n += blocks * kJoinGroups;
+  } while (few && n < sp.rows);
 }
 
 // Rows of a query tile: the average rows (tokens x heads) per sequence decide.
@@ -1506,7 +1513,7 @@ cudaError_t launch_t(const LatentAttnArgs& a, const CUtensorMap& map, int ctas,
   lc.numAttrs = cfg.pdl ? 1 : 0;
   e = cudaLaunchKernelEx(&lc, kern, a, map);
   if (e != cudaSuccess) return e;
-  lc.gridDim = dim3(NR / kJoinGroups, ctas);
+  lc.gridDim = dim3(NR / 8, ctas);
   lc.blockDim = dim3(kJoinThreads);
   lc.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&lc, latent_join_kernel<FMT, NR>, a);
