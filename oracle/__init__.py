@@ -21,6 +21,9 @@ Passages followed (page title, section):
     Implementation items 1, 2, 5 and Source snippets (fused_mla_kv_concat,
     fused_mla_kv_concat_quant_fp8): ``context_gather``, ``cast_rows``,
     ``concat_key``, ``context_kv_pack``.
+  * the same page, Implementation items 1-2 (the chunk loop whose partial results are
+    joined), and the formulas of include/mla_cache.h: ``latent_attention``,
+    ``merge_attn_states``, ``copy_blocks``.
   * OCP 8-bit Floating Point Specification (OFP8) rev. 1.0: the e4m3fn and
     e5m2 encodings behind ``fp8_from_f32`` / ``fp8_to_f64``; IEEE 754 binary16
     behind ``f16_from_f64`` / ``f16_to_f64`` (the pack's fp16 inputs).
