@@ -579,12 +579,18 @@ mla_status_t mla_cache_copy_blocks(const int64_t* kv_cache_ptrs, int32_t num_lay
  * does not see has no influence on its result, whatever the row holds; the
  * result of a token that sees a row with a NaN or an infinity is not specified.
  *
- * Arithmetic: products of bf16 values (fp8 ones are exact in bf16) summed in
- * fp32, softmax in fp32; the weights exp(x_p - max) are rounded to bf16 before
- * they multiply the rows, the sums stay in fp32, and the result is rounded once
- * to bf16.  Results do not depend on other work on the device; on the call's
- * shape (num_tokens, num_seqs, num_heads) and lengths they depend through the
- * order of fp32 sums only.
+ * Arithmetic: exact products summed in fp32, softmax in fp32, one rounding of the
+ * result to bf16.  Two operands are rounded before their products:
+ *   - a weight exp(x_p - r), r a reference near the largest score seen so far, to
+ *     bf16 (2^-8 of itself) with a bf16 cache, and to 2^-11 of itself or 2^-34 of
+ *     the row's largest weight with an fp8 cache; the sum that they are divided by
+ *     counts them unrounded;
+ *   - with an fp8 cache, elements of q below 2^-14 of their row's largest
+ *     magnitude, by at most 2^-21 of that magnitude.
+ * Results do not depend on other work on the device.  The call's shape (num_tokens,
+ * num_seqs, num_heads), its lengths and the device's number of SMs decide how the
+ * rows are cut; results depend on them through the order of fp32 sums and through
+ * the references r, relative to which the weights are rounded.
  *
  *   q_c, q_pe           bf16; element (t, h, e) at t * token_stride +
  *                       h * head_stride + e; rows start on 16-byte boundaries.

@@ -17,7 +17,7 @@
 //
 // Measured (replayed from a graph, without the profiler; 16 heads, 64-row blocks): one
 // new token of 4 sequences over 131072 bf16 rows 99.9 us (6.05 TB/s), of 64 over 130 to
-// 16384 e4m3 rows 58.0 us (5.4 TB/s), of one over 2047 bf16 rows 10.1 us; 1024 new
+// 16384 e4m3 rows 60.3 us (5.2 TB/s), of one over 2047 bf16 rows 10.1 us; 1024 new
 // tokens of 2 over 8192 bf16 rows 645 us (849 TFLOP/s).  About 10 us of a call are fixed
 // (finding the run and the first rows 3, filling and draining the pipeline 4, the join 3).
 //
@@ -33,11 +33,18 @@
 // bf16 cache: 9 chunks of 64 columns, two tiles in flight (2 x 72 KB).
 // fp8 cache: the codes themselves are the A operand (5 chunks, the last one
 // columns 448 to 575, four tiles in flight), and the 16-bit operands are split
-// into two e4m3 parts that together hold a bf16's 8 bits: a query row, scaled by
-// a power of two, is q1 + q2 / 16; a weight is p1 + p2 / 512.  The parts are 2 NR
-// columns of one product, added when the sums are read.  (Widening the codes to
-// bf16 in shared memory instead took 4000 cycles per tile of producers' time,
-// against 1570 for its bytes from HBM.)
+// into 8-bit parts: a query row, scaled by a power of two, is two e4m3 parts, q1 +
+// q2 / 16; a weight is three e5m2 parts, p1 + p2 / 16 + p3 / 256.  The parts are 2 NR
+// or 3 NR columns of one product, added when the sums are read.
+//
+// Why three e5m2 parts for a weight.  A long tail of small weights can hold most of a
+// row's mass, so small weights need their 8 bits as much as large ones.  Weights reach
+// 2^14 (a reference 2^10 below the maximum, which may grow by 2^4 more).  A part of a
+// value in [2^k, 2^(k+1)) is off by at most 2^(k-3), which times 16 is at most 2^(k+1)
+// again: three parts hold a weight to 2^-11 of itself, or to half the last part's
+// smallest step, 2^-16 / 256 / 2 = 2^-25, which is 2^-34 of the row's largest weight or
+// less.  (Two e4m3 parts held 8 bits down to 2^-7 of the largest weight and nothing
+// below 2^-19: a tail of 131072 equal weights with 20% of the mass was lost.)
 //
 // Cost of a tile (measured, cycles per instruction: M = 64, N = 16 / 64 24 / 33;
 // M = 128 40 / 49; the A operand's shared memory reads bound both): bf16 36 + 16
@@ -82,7 +89,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 // 12.9 us with 1, 2 and 3 (fewer: more partial sums to join; more: fewer SMs).
 constexpr int kMinUnits = 2;
 constexpr float kQ2 = 0.0625f;            // query parts: q = q1 + q2 / 16
-constexpr float kP2 = 1.0f / 512.0f;      // weight parts: p = p1 + p2 / 512
+constexpr float kPStep = 16.0f;           // weight parts: p = p1 + p2 / 16 + p3 / 256
 
 // Key flags of a tile (one byte per key).
 constexpr uint32_t kAbsent = 1;  // its block was not found: left out
@@ -91,8 +98,9 @@ constexpr uint32_t kPoison = 2;  // holds a NaN or an infinity
 template <int FMT, int NR>
 struct Lay {
   static constexpr bool kF8 = FMT != kBF16;
-  static constexpr int kParts = kF8 ? 2 : 1;            // columns per query row
-  static constexpr int kN = kParts * NR;
+  static constexpr int kN = (kF8 ? 2 : 1) * NR;         // columns of the scores: parts of the queries
+  static constexpr int kParts = kF8 ? 3 : 1;            // parts of a weight
+  static constexpr int kPN = kParts * NR;               // columns of the outputs
   static constexpr int kChunks = kF8 ? 5 : 9;
   static constexpr int kTile = kChunks * kChunk;
   static constexpr int kStages = kF8 ? 4 : 2;
@@ -116,13 +124,14 @@ struct Lay {
   // without it: 64 ragged decodes 66.4 us (62.8 with it), 32 verifications 58.0 (49.9),
   // 16 decodes of 128 heads 50.3 (49.0).
   static constexpr int kSwitch = kF8 ? (NR == 16 ? 3 : 6) : (NR == 16 ? 1 : 2);
-  // a maximum may grow this much (log2) before the sums are rescaled; the fp8
-  // weights stay below 2^4 (p1 rounds by at most 1/2 there, p2 = 512 (p - p1) fits)
-  static constexpr float kGrow = kF8 ? 4.0f : 8.0f;
+  // The reference of a row's weights is its maximum (log2) less kTop; a score may pass
+  // the reference by kGrow before the sums are rescaled.
+  static constexpr float kTop = kF8 ? 10.0f : 0.0f;
+  static constexpr float kGrow = kF8 ? 14.0f : 8.0f;
   // shared memory
   static constexpr int q = kStages * kTile;
   static constexpr int kPBufs = NR == 64 ? 1 : 2;
-  static constexpr int kP = kN * 128;                    // kN rows x 64 keys (fp8: half of each row)
+  static constexpr int kP = kPN * 128;                   // kPN rows x 64 keys (fp8: half of each row)
   static constexpr int p = q + kQBufs * kQ;
   static constexpr int red = p + kPBufs * kP;               // float [2][kSoftWarps][kCols]
   static constexpr int qs = red + 2 * kSoftWarps * kCols * 4;  // float [kQBufs][NR]
@@ -137,7 +146,9 @@ struct Lay {
   static_assert(bytes <= 232448, "shared memory of a CTA");
   // tensor memory columns: two score buffers, then the sums of 4 x 128 dims
   static constexpr int kO = 2 * kN;
-  static constexpr int kTmem = kN <= 16 ? 128 : kN <= 32 ? 256 : 512;
+  static constexpr int kCols32 = 2 * kN + 4 * kPN;
+  static constexpr int kTmem = kCols32 <= 128 ? 128 : kCols32 <= 256 ? 256 : 512;
+  static_assert(kCols32 <= 512, "tensor memory of an SM");
 };
 
 struct Misc {
@@ -664,7 +675,7 @@ template <int FMT, int NR>
 __device__ __forceinline__ void issue_outputs(uint32_t smem, uint32_t tmem, bool one, int stage,
                                               int pbuf, bool first) {
   using L = Lay<FMT, NR>;
-  constexpr uint32_t kId = tc::instr_desc(128, L::kN, true, FMT == kE4M3 ? 0 : 1, L::kF8 ? 0 : 1);
+  constexpr uint32_t kId = tc::instr_desc(128, L::kPN, true, FMT == kE4M3 ? 0 : 1, 1);
   const uint32_t st = __shfl_sync(0xFFFFFFFFu, stage, 0), pb = __shfl_sync(0xFFFFFFFFu, pbuf, 0);
   // The K tile, MN-major.  128 dims are two bf16 chunks or one fp8 chunk; a k step
   // is 16 keys (2 groups of 8 rows) or 32.
@@ -677,7 +688,7 @@ __device__ __forceinline__ void issue_outputs(uint32_t smem, uint32_t tmem, bool
     for (int b = h * 2; b < (h + 1 == L::kHalves ? 4 : 2); ++b)
 #pragma unroll
       for (int k = 0; k < (L::kF8 ? 2 : 4); ++k) {
-        const uint32_t d = tmem + L::kO + b * L::kN;
+        const uint32_t d = tmem + L::kO + b * L::kPN;
         const uint64_t ak = va + (b * kDims >> 4) + k * (kStep >> 4), bk = pa + 2 * k;
         if constexpr (L::kF8) tc::mma_fp8(one, d, ak, bk, kId, k > 0 || !first);
         else tc::mma_bf16(one, d, ak, bk, kId, k > 0 || !first);
@@ -932,7 +943,7 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
         float f[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float mn = fmaxf(mu[j][e], tm[j][e]);
+          const float mn = fmaxf(mu[j][e], tm[j][e] - L::kTop);
           f[e] = mu[j][e] == -INFINITY ? 0.0f : ex2(mu[j][e] - mn);
           l[j][e] *= f[e];
           mu[j][e] = mn;
@@ -973,23 +984,24 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
           w[2 * jj] = pack_bf16x2(p0, p1);
           w[2 * jj + 1] = pack_bf16x2(p2, p3);
         } else {
-          // each weight as two e4m3 parts, p1 in row n and p2 in row NR + n: 2^-8 of the
-          // weight, or 2^-19 (half of p2's smallest step / 512), as a bf16 would round it
+          // each weight as three e5m2 parts, in the rows n, NR + n and 2 NR + n
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float u = h ? p2 : p0, v = h ? p3 : p1;
-            const uint32_t hi = pack_fp8x2<kE4M3>(u, v);
-            float uh, vh;
-            fp8x2_to_f32x2<kE4M3>(hi, uh, vh);
-            const uint32_t lo = pack_fp8x2<kE4M3>((u - uh) * (1.0f / kP2), (v - vh) * (1.0f / kP2));
+            float u = h ? p2 : p0, v = h ? p3 : p1;
             const int n = col0 + (j + jj) * 8 + c2;  // and n + 1
             const uint32_t in = (lane >> 2) + 8 * h;
             const uint32_t d0 = smem + L::p + (g & (L::kPBufs - 1)) * L::kP + n * 128 + ((w4 ^ (n & 7)) << 4) + in;
             const uint32_t d1 = smem + L::p + (g & (L::kPBufs - 1)) * L::kP + (n + 1) * 128 + ((w4 ^ ((n + 1) & 7)) << 4) + in;
-            sts_u8(d0, hi);
-            sts_u8(d1, hi >> 8);
-            sts_u8(d0 + NR * 128, lo);
-            sts_u8(d1 + NR * 128, lo >> 8);
+#pragma unroll
+            for (int i = 0; i < L::kParts; ++i) {
+              const uint32_t part = pack_fp8x2<kE5M2>(u, v);
+              sts_u8(d0 + i * NR * 128, part);
+              sts_u8(d1 + i * NR * 128, part >> 8);
+              float uh, vh;
+              fp8x2_to_f32x2<kE5M2>(part, uh, vh);
+              u = (u - uh) * kPStep;
+              v = (v - vh) * kPStep;
+            }
           }
         }
       }
@@ -1064,14 +1076,18 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
 #pragma unroll 1
       for (int blk = 0; blk < 4; ++blk) {
         uint32_t r[16];
-        const uint32_t o = sub + L::kO + blk * L::kN + col0 + n0;
+        const uint32_t o = sub + L::kO + blk * L::kPN + col0 + n0;
         tc::ld_32x16(o, r);
         if constexpr (L::kF8) {
-          uint32_t r2[16];
-          tc::ld_32x16(o + NR, r2);
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            r[i] = __float_as_uint(fmaf(__uint_as_float(r2[i]), kP2, __uint_as_float(r[i])));
+          for (int k = 1; k < L::kParts; ++k) {
+            uint32_t rk[16];
+            tc::ld_32x16(o + k * NR, rk);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              r[i] = __float_as_uint(fmaf(__uint_as_float(rk[i]), k == 1 ? 1 / kPStep : 1 / (kPStep * kPStep),
+                                          __uint_as_float(r[i])));
+          }
         }
         if (lost) continue;
         if (whole) {
