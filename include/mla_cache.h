@@ -581,7 +581,7 @@ mla_status_t mla_cache_copy_blocks(const int64_t* kv_cache_ptrs, int32_t num_lay
  *
  * Arithmetic: exact products summed in fp32, softmax in fp32, one rounding of the
  * result to bf16.  Two operands are rounded before their products:
- *   - a weight exp(x_p - r), r a reference near the largest score seen so far, to
+ *   - a weight exp(x_p) relative to a power of two near the largest seen so far, to
  *     bf16 (2^-8 of itself) with a bf16 cache, and to 2^-11 of itself or 2^-34 of
  *     the row's largest weight with an fp8 cache; the sum that they are divided by
  *     counts them unrounded;
@@ -589,8 +589,8 @@ mla_status_t mla_cache_copy_blocks(const int64_t* kv_cache_ptrs, int32_t num_lay
  *     magnitude, by at most 2^-21 of that magnitude.
  * Results do not depend on other work on the device.  The call's shape (num_tokens,
  * num_seqs, num_heads), its lengths and the device's number of SMs decide how the
- * rows are cut; results depend on them through the order of fp32 sums and through
- * the references r, relative to which the weights are rounded.
+ * rows are cut; results depend on them through fp32 roundings only (the order of
+ * sums, and a score's distance to the power of two of the rows around it).
  *
  *   q_c, q_pe           bf16; element (t, h, e) at t * token_stride +
  *                       h * head_stride + e; rows start on 16-byte boundaries.

@@ -124,8 +124,9 @@ struct Lay {
   // without it: 64 ragged decodes 66.4 us (62.8 with it), 32 verifications 58.0 (49.9),
   // 16 decodes of 128 heads 50.3 (49.0).
   static constexpr int kSwitch = kF8 ? (NR == 16 ? 3 : 6) : (NR == 16 ? 1 : 2);
-  // The reference of a row's weights is its maximum (log2) less kTop; a score may pass
-  // the reference by kGrow before the sums are rescaled.
+  // The reference of a row's weights is the next whole number (log2) above its maximum
+  // less kTop; a score may pass the reference by kGrow before the sums are rescaled.
+  // Whole numbers, so that the weights round alike whichever rows a CTA's run begins with.
   static constexpr float kTop = kF8 ? 10.0f : 0.0f;
   static constexpr float kGrow = kF8 ? 14.0f : 8.0f;
   // shared memory
@@ -943,7 +944,7 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
         float f[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float mn = fmaxf(mu[j][e], tm[j][e] - L::kTop);
+          const float mn = fmaxf(mu[j][e], ceilf(tm[j][e]) - L::kTop);
           f[e] = mu[j][e] == -INFINITY ? 0.0f : ex2(mu[j][e] - mn);
           l[j][e] *= f[e];
           mu[j][e] = mn;

@@ -1,5 +1,5 @@
 """The softmax weights of mla_latent_attention: 8 bits of every weight, whatever
-its size, whether a row lies in one CTA's run or is cut over many.
+its size, and results that do not depend on how a call is cut over the SMs.
 
 Each case is one early row that takes much of the weight (5 to 14 nats above the
 others, one gap per head) and a long tail of equal scores whose values are all
@@ -109,3 +109,19 @@ def test_a_long_tail_behind_a_sink(fmt, heads, rows):
         worst = (np.abs(o - ro) / bo).max(-1)
         assert worst.max() <= 1, (seqs, worst)
         assert (np.abs(le - rl) <= bl).all()
+
+
+@pytest.mark.parametrize("heads", [16, 64])
+@pytest.mark.parametrize("fmt", [0, 1, 2])
+def test_the_cut_over_the_sms_does_not_change_the_weights(fmt, heads):
+    """In one run and cut into sixteen, the weights round alike: what differs are fp32
+    sums.  2048 rows are 32 tiles, 128 additions of a matrix unit at most, each off by one
+    fp32 step: a relative 2^-16, against steps of the bf16 result of 2^-8 and more.  A
+    result then rounds differently in one element of 2^8, and by one step; twice that is
+    allowed here for the sum of the weights, which differs in the same way."""
+    s = Sink(fmt, heads, 2048, 3)  # (no cancellation in the results)
+    (a, la), (b, lb) = s.run(sms()), s.run(1)
+    a, b = D.host_u16(a[0]).astype(np.int64), D.host_u16(b[0]).astype(np.int64)
+    assert np.abs(a - b).max() <= 1
+    assert (a != b).mean() <= 2 * 2.0 ** -8
+    assert (la[0] - lb[0]).abs().max().item() <= 2.0 ** -16 * (1 + lb.abs().max().item())
