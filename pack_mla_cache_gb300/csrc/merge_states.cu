@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kThreads) merge_states_kernel(const MergeArgs 
   pdl_trigger();
   pdl_wait();
   const uint32_t units = (uint32_t)a.num_tokens * a.num_heads * (a.row_chunks / C);  // < 2^31
-  const int step = a.row_chunks / C * 16;  // bytes between a thread's chunks
+  const int64_t step = (int64_t)(a.row_chunks / C) * 16;  // bytes between a thread's chunks
   for (uint32_t u = blockIdx.x * kThreads + threadIdx.x; u < units; u += gridDim.x * kThreads) {
     const uint32_t row = a.by_units(u), ch = u - row * (a.row_chunks / C);
     const uint32_t t = a.by_heads(row), h = row - t * a.num_heads;
