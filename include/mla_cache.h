@@ -531,8 +531,8 @@ mla_status_t mla_rope_cos_sin_cache(float* out, int64_t max_position, int32_t ro
  *   - forking: a block may be the source of any number of copies; the last,
  *     part-filled block of a sequence is copied with its row count;
  *   - freeing: src -1 clears a block before it is handed out again.
- * A copy with dst_blocks[i] == -1 or n == 0 is padding and is skipped, and so
- * is one with dst == src.  A block that is the destination of one copy must
+ * A copy with dst_blocks[i] == -1 or n == 0 is padding and is skipped, whatever
+ * its other numbers are; one with dst == src, both in range, is skipped too.  A block that is the destination of one copy must
  * be neither destination nor source of another (its contents are unspecified
  * otherwise); caches of different layers must not overlap.
  *
@@ -543,7 +543,8 @@ mla_status_t mla_rope_cos_sin_cache(float* out, int64_t max_position, int32_t ro
  *   entry_dim           elements of an entry that are copied, a multiple of 16
  *                       bytes.
  *   src_blocks, dst_blocks  int32 device [num_copies]; an id below -1 or not
- *                       below num_blocks skips the copy (MLA_ERRBIT_BLOCK_OOB).
+ *                       below num_blocks skips the copy (MLA_ERRBIT_BLOCK_OOB),
+ *                       also where dst == src.
  *   row_counts          int32 device [num_copies] or NULL; a count outside
  *                       [0, block_size] skips the copy (MLA_ERRBIT_BLOCK_OOB).
  */

@@ -836,7 +836,7 @@ uint32_t orc_copy_blocks(void* const* caches, int32_t num_layers, int32_t elt_si
     for (int32_t i = 0; i < num_copies; ++i) {
       int64_t src = src_blocks[i], dst = dst_blocks[i];
       int32_t n = row_counts ? row_counts[i] : block_size;
-      if (dst == -1) continue;
+      if (dst == -1 || n == 0) continue;
       if (src < -1 || dst < -1 || src >= num_blocks || dst >= num_blocks || n < 0 ||
           n > block_size) {
         err |= ORC_ERR_BLOCK_OOB;

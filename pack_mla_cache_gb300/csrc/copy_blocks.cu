@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(kThreads) copy_blocks_kernel(const CopyBlocksA
     const int32_t src = a.src[c], dst = a.dst[c];
     const int32_t n = a.rows ? a.rows[c] : a.block_size;
     const int64_t base = a.cache_ptrs[l];
-    if (dst == -1) continue;  // padding
+    if (dst == -1 || n == 0) continue;  // padding
     if (src < -1 || dst < -1 || src >= a.num_blocks || dst >= a.num_blocks || n < 0 ||
         n > a.block_size) {
       errbits |= kErrBlockOOB;

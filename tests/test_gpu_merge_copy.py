@@ -301,3 +301,15 @@ def test_merge_of_the_largest_values_stays_finite(kind, P, Dm):
     rel = TYPES[kind][1] + 2 * (P + 8) * R.FP32_HALF
     assert (out.double() - want).abs().max().item() <= rel * want
     assert (lo.double() - np.log(P)).abs().max().item() <= 8 * R.FP32_HALF * (1 + np.log(P))
+
+
+def test_copies_of_no_rows_are_padding(orc):
+    """A count of 0 is padding whatever the ids are, next to copies that are not."""
+    copy_both(orc, 2, 8, 16, 16 * 576, 576, 576, 1, [99, 0, -9, 0, 1], [1, 99, -9, 5, 6],
+              [0, 0, 0, 16, 3])
+
+
+def test_copies_onto_themselves_are_checked_first(orc):
+    copy_both(orc, 2, 8, 16, 16 * 576, 576, 576, 1, [3, 4], [3, 4], [16, 2])
+    copy_both(orc, 2, 8, 16, 16 * 576, 576, 576, 1, [8, 0], [8, 5], [16, 2],
+              want_err=ops.MLA_ERRBIT_BLOCK_OOB)

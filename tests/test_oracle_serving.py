@@ -96,3 +96,15 @@ def test_copy_blocks_against_numpy(orc, esz):
         e[7, :3, :ed] = 0
     for c, r in zip(caches, ref):
         np.testing.assert_array_equal(c.reshape(nb, bst), r)
+
+
+def test_copy_blocks_of_no_rows_are_padding(orc):
+    """A count of 0 is padding whatever the ids are; equal ids out of range are reported."""
+    i = lambda *v: np.array(v, np.int32)
+    cache = np.arange(4 * 2 * 32, dtype=np.uint8)
+    ref = cache.copy()
+    args = (1, 4, 2, 64, 32, 32)
+    assert orc.copy_blocks([cache], *args, i(99, 0, -9), i(1, 99, -9), i(0, 0, 0)) == 0
+    assert orc.copy_blocks([cache], *args, i(99), i(99), i(1)) == 2
+    assert orc.copy_blocks([cache], *args, i(1), i(1), i(2)) == 0
+    np.testing.assert_array_equal(cache, ref)
