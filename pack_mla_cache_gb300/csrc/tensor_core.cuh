@@ -122,7 +122,7 @@ __device__ __forceinline__ void wait_st() {
 // t / 4 + 8 in r[4 j + 2], r[4 j + 3].  G groups.
 template <int G>
 __device__ __forceinline__ void ld_16x256(uint32_t addr, uint32_t* r) {
-  static_assert(G == 2 || G == 4 || G == 8, "groups built");
+  static_assert(G == 2 || G == 4, "groups built");
   if constexpr (G == 2) {
     asm volatile(
         "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
@@ -141,7 +141,6 @@ __device__ __forceinline__ void ld_16x256(uint32_t addr, uint32_t* r) {
           "=r"(r[14]), "=r"(r[15])
         : "r"(addr)
         : "memory");
-    if constexpr (G == 8) ld_16x256<4>(addr + 32, r + 16);
   }
 }
 
