@@ -1461,16 +1461,6 @@ __global__ void __launch_bounds__(kJoinThreads, 2) latent_join_kernel(const Late
   } while (few && n < sp.rows);
 }
 
-// Rows of a query tile: the average rows (tokens x heads) per sequence decide.
-// fp8 tiles stop at 32: their split sums take two columns of tensor memory each.
-// Measured: 16 rows per sequence 57.9 us in tiles of 16 (64.7 in tiles of 32; 64 ragged
-// e4m3 decodes), 64 e5m2 rows 46.6 in tiles of 32 (60.7 in 16), 128 bf16 rows 47.3 and
-// 16384 rows 645 in tiles of 64 (61.9 and 1127 in 32).
-inline int tile_rows(int32_t num_tokens, int32_t num_heads, int32_t num_seqs, bool fp8) {
-  const int64_t rows = (int64_t)((num_tokens + num_seqs - 1) / num_seqs) * num_heads;
-  return rows <= 16 ? 16 : rows <= 32 || fp8 ? 32 : 64;
-}
-
 // The cache as a tensor of (column, entry, block), read in boxes of one chunk of
 // `rows` entries.  Without a box (entries per block not a multiple of 8, or sizes
 // that a tensor map does not hold) rows are copied one by one: 64 ragged e4m3 decodes
@@ -1542,7 +1532,7 @@ cudaError_t launch_f(LatentAttnArgs a, int ctas, const LaunchCfg& cfg) {
   CUtensorMap map = {};
   a.box_rows = box_map(a, kF8, &map);
   for (int rows = a.box_rows; rows != 0 && rows < kKeys; rows *= 2) ++a.box_shift;
-  const int nr = tile_rows(a.num_tokens, a.num_heads, a.num_seqs, kF8);
+  const int nr = attention_tile_rows(a.num_tokens, a.num_heads, a.num_seqs, kF8);
   // Cache rows that up to four query tiles of a sequence read (at about the same time) are
   // the first to leave L2: 64 ragged decodes 58.4 us (61.9 without the hint), 32
   // verifications 46.3 (48.5), 16 decodes of 128 heads 47.1 (47.8).  The many query tiles

@@ -90,6 +90,16 @@ struct LatentAttnArgs {
   int32_t stall_stage;  // testing: this pipeline stage (from 1) of CTA 0 never fills
 };
 
+// Rows of a query tile of the attention: the average rows (tokens x heads) per sequence
+// decide.  fp8 tiles stop at 32: their split sums take three columns of tensor memory each.
+// Measured: 16 rows per sequence 57.9 us in tiles of 16 (64.7 in tiles of 32; 64 ragged
+// e4m3 decodes), 64 e5m2 rows 46.6 in tiles of 32 (60.7 in 16), 128 bf16 rows 47.3 and
+// 16384 rows 645 in tiles of 64 (61.9 and 1127 in 32).
+inline int attention_tile_rows(int32_t num_tokens, int32_t num_heads, int32_t num_seqs, bool fp8) {
+  const int64_t rows = ((int64_t)num_tokens + num_seqs - 1) / num_seqs * num_heads;
+  return rows <= 16 ? 16 : rows <= 32 || fp8 ? 32 : 64;
+}
+
 cudaError_t launch_copy_blocks(const CopyBlocksArgs& a, const LaunchCfg& cfg);
 // fmt: kBF16, kF16 or kF32.
 cudaError_t launch_merge(const MergeArgs& a, int fmt, const LaunchCfg& cfg);
