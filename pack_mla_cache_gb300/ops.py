@@ -365,16 +365,35 @@ def mla_context_kv_pack_gather(pack: KvPack, next_gather: ContextGather, *, err_
                                             _ptr(err_word), _stream(stream)))
 
 
+def _check_list(name, t, dtype, n):
+    # at least n elements of the type, one behind the other
+    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] < n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be contiguous {dtype} [{n}] (got {t.dtype} {list(t.shape)}, "
+                         f"strides {t.stride()})")
+
+
+def _check_lse(name, t, shape):
+    if t.dtype is not torch.float32 or t.shape != shape:
+        raise ValueError(f"{name} must be fp32 {list(shape)} (got {t.dtype} {list(t.shape)})")
+    return t.stride()
+
+
 def mla_cache_copy_blocks(kv_cache_ptrs, cache_dtype, num_blocks, block_size, block_stride,
                           entry_stride, entry_dim, src_blocks, dst_blocks, *, row_counts=None,
                           err_word=None, stream=None):
     """Copy (fork, compact) or clear (src -1) blocks in every layer's cache:
     kv_cache_ptrs int64 [L]; src_blocks / dst_blocks / row_counts int32 [N],
     row_counts None for whole blocks."""
+    N = dst_blocks.shape[0]
+    _check_list("kv_cache_ptrs", kv_cache_ptrs, torch.int64, kv_cache_ptrs.shape[0])
+    _check_list("dst_blocks", dst_blocks, torch.int32, N)
+    _check_list("src_blocks", src_blocks, torch.int32, N)
+    if row_counts is not None:
+        _check_list("row_counts", row_counts, torch.int32, N)
     _check(lib().mla_cache_copy_blocks(
         _ptr(kv_cache_ptrs), kv_cache_ptrs.shape[0], dtype_code(cache_dtype), num_blocks,
         block_size, block_stride, entry_stride, entry_dim, _ptr(src_blocks), _ptr(dst_blocks),
-        _ptr(row_counts), dst_blocks.shape[0], _ptr(err_word), _stream(stream)))
+        _ptr(row_counts), N, _ptr(err_word), _stream(stream)))
 
 
 def mla_latent_attention_workspace(num_tokens: int, num_heads: int, num_seqs: int) -> int:
@@ -389,20 +408,41 @@ def mla_latent_attention(q_c, q_pe, kv_cache, cache_dtype, num_blocks, block_siz
                          softmax_scale, k_scale=None, causal=True, lse=None, err_word=None,
                          stream=None):
     """Attention of new tokens over the paged latent cache (absorbed form):
-    q_c [T, H, 512] and q_pe [T, H, 64] bf16 views (strided), out bf16
-    [T, H, 512], lse fp32 [T, H] or None; block_table int32 [S, W], cu_q_lens
-    int32 [S + 1], kv_lens int32 [S]; workspace: a uint8 tensor of
-    ``mla_latent_attention_workspace`` bytes."""
+    q_c [T, H, 512] and q_pe [T, H, 64] bf16 views (any strides, unit last
+    stride), out bf16 [T, H, 512] likewise, lse fp32 [T, H] or None; block_table
+    int32 [S, W], cu_q_lens int32 [S + 1], kv_lens int32 [S]; k_scale fp32;
+    workspace: a uint8 tensor of ``mla_latent_attention_workspace`` bytes."""
     T, H, R = q_c.shape
-    qc_t, qc_h, _ = q_c.stride()
-    qp_t, qp_h, _ = q_pe.stride()
-    out_t, out_h, _ = out.stride()
-    lse_t, lse_h = (0, 0) if lse is None else lse.stride()
+    qc_t, qc_h, qc_e = q_c.stride()
+    qp_t, qp_h, qp_e = q_pe.stride()
+    out_t, out_h, out_e = out.stride()
+    S = kv_lens.shape[0]
+    bf16 = torch.bfloat16
+    if q_c.dtype is not bf16 or q_pe.dtype is not bf16 or out.dtype is not bf16:
+        raise ValueError(f"q_c, q_pe and out must be bf16 (got {q_c.dtype}, {q_pe.dtype}, {out.dtype})")
+    if qc_e != 1 or qp_e != 1 or out_e != 1:
+        raise ValueError("q_c, q_pe and out must have a unit last stride")
+    if q_pe.shape[:2] != (T, H) or out.shape != (T, H, R):
+        raise ValueError(f"q_pe must be [{T}, {H}, 64] and out [{T}, {H}, {R}] "
+                         f"(got {list(q_pe.shape)}, {list(out.shape)})")
+    lse_t = lse_h = 0
+    if lse is not None:
+        lse_t, lse_h = _check_lse("lse", lse, (T, H))
+    _check_list("kv_lens", kv_lens, torch.int32, S)
+    _check_list("cu_q_lens", cu_q_lens, torch.int32, S + 1)
+    if (block_table.dtype is not torch.int32 or block_table.dim() != 2 or block_table.stride(1) != 1
+            or block_table.shape[0] < S):
+        raise ValueError(f"block_table must be int32 [{S}, W] with a unit last stride "
+                         f"(got {block_table.dtype} {list(block_table.shape)})")
+    if k_scale is not None and (k_scale.dtype is not torch.float32 or k_scale.numel() < 1):
+        raise ValueError(f"k_scale must be an fp32 scalar (got {k_scale.dtype} {list(k_scale.shape)})")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     status = lib().mla_latent_attention(
         q_c.data_ptr(), qc_t, qc_h, q_pe.data_ptr(), qp_t, qp_h, T, H, R, q_pe.shape[2],
         kv_cache.data_ptr(), dtype_code(cache_dtype), num_blocks, block_size, block_stride,
         entry_stride, block_table.data_ptr(), _bt_stride(block_table), cu_q_lens.data_ptr(),
-        kv_lens.data_ptr(), kv_lens.shape[0], softmax_scale, _ptr(k_scale), 1 if causal else 0,
+        kv_lens.data_ptr(), S, softmax_scale, _ptr(k_scale), 1 if causal else 0,
         out.data_ptr(), out_t, out_h, _ptr(lse), lse_t, lse_h, workspace.data_ptr(),
         workspace.nbytes, _ptr(err_word), _stream(stream))
     if status:
@@ -411,11 +451,18 @@ def mla_latent_attention(q_c, q_pe, kv_cache, cache_dtype, num_blocks, block_siz
 
 def mla_merge_attn_states(parts, lse, out, *, lse_out=None, stream=None):
     """Join attention results over disjoint parts of the context: parts
-    [P, T, H, D] (bf16, fp16 or fp32; strided, unit last stride) with lse fp32
+    [P, T, H, D] (bf16, fp16 or fp32; any strides, unit last stride) with lse fp32
     [P, T, H] into out [T, H, D] of the same type and lse_out fp32 [T, H]."""
     P, T, H, Dm = parts.shape
     if parts.dtype != out.dtype:
         raise ValueError(f"out must have the parts' dtype ({parts.dtype}, got {out.dtype})")
+    if out.shape != (T, H, Dm):
+        raise ValueError(f"out must be [{T}, {H}, {Dm}] (got {list(out.shape)})")
+    if parts.stride(3) != 1 or out.stride(2) != 1:
+        raise ValueError("parts and out must have a unit last stride")
+    _check_lse("lse", lse, (P, T, H))
+    if lse_out is not None:
+        _check_lse("lse_out", lse_out, (T, H))
     code = MLA_FP32 if parts.dtype == torch.float32 else dtype_code(parts.dtype)
     _check(lib().mla_merge_attn_states(
         _ptr(parts), parts.stride(0), parts.stride(1), parts.stride(2), _ptr(lse), lse.stride(0),
