@@ -158,9 +158,16 @@ def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
+# The current stream's handle alone (a Stream object costs 3 us).  Not part of torch's
+# public interface: a torch without it goes the public way.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int | None:
-    if stream is None:  # the handle alone: a Stream object costs 3 us
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:
+        if _raw_stream is None:
+            return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
