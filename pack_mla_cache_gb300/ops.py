@@ -372,17 +372,14 @@ def mla_context_kv_pack_gather(pack: KvPack, next_gather: ContextGather, *, err_
                                             _ptr(err_word), _stream(stream)))
 
 
-def _check_list(name, t, dtype, n):
+# (The checks' usual path is a few attribute reads: a small call's time is its host work.)
+def _is_list(t, dtype, n):
     # at least n elements of the type, one behind the other
-    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] < n or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be contiguous {dtype} [{n}] (got {t.dtype} {list(t.shape)}, "
-                         f"strides {t.stride()})")
+    return t.dtype is dtype and t.numel() >= n and t.is_contiguous()
 
 
-def _check_lse(name, t, shape):
-    if t.dtype is not torch.float32 or t.shape != shape:
-        raise ValueError(f"{name} must be fp32 {list(shape)} (got {t.dtype} {list(t.shape)})")
-    return t.stride()
+def _refuse(name, t, want):
+    raise ValueError(f"{name} must be {want} (got {t.dtype} {list(t.shape)}, strides {t.stride()})")
 
 
 def mla_cache_copy_blocks(kv_cache_ptrs, cache_dtype, num_blocks, block_size, block_stride,
@@ -392,11 +389,14 @@ def mla_cache_copy_blocks(kv_cache_ptrs, cache_dtype, num_blocks, block_size, bl
     kv_cache_ptrs int64 [L]; src_blocks / dst_blocks / row_counts int32 [N],
     row_counts None for whole blocks."""
     N = dst_blocks.shape[0]
-    _check_list("kv_cache_ptrs", kv_cache_ptrs, torch.int64, kv_cache_ptrs.shape[0])
-    _check_list("dst_blocks", dst_blocks, torch.int32, N)
-    _check_list("src_blocks", src_blocks, torch.int32, N)
-    if row_counts is not None:
-        _check_list("row_counts", row_counts, torch.int32, N)
+    if not _is_list(kv_cache_ptrs, torch.int64, 0):
+        _refuse("kv_cache_ptrs", kv_cache_ptrs, "contiguous int64")
+    if not _is_list(dst_blocks, torch.int32, N):
+        _refuse("dst_blocks", dst_blocks, "contiguous int32")
+    if not _is_list(src_blocks, torch.int32, N):
+        _refuse("src_blocks", src_blocks, f"contiguous int32 [{N}]")
+    if row_counts is not None and not _is_list(row_counts, torch.int32, N):
+        _refuse("row_counts", row_counts, f"contiguous int32 [{N}]")
     _check(lib().mla_cache_copy_blocks(
         _ptr(kv_cache_ptrs), kv_cache_ptrs.shape[0], dtype_code(cache_dtype), num_blocks,
         block_size, block_stride, entry_stride, entry_dim, _ptr(src_blocks), _ptr(dst_blocks),
@@ -425,30 +425,38 @@ def mla_latent_attention(q_c, q_pe, kv_cache, cache_dtype, num_blocks, block_siz
     out_t, out_h, out_e = out.stride()
     S = kv_lens.shape[0]
     bf16 = torch.bfloat16
+    qp_T, qp_H, P = q_pe.shape
     if q_c.dtype is not bf16 or q_pe.dtype is not bf16 or out.dtype is not bf16:
         raise ValueError(f"q_c, q_pe and out must be bf16 (got {q_c.dtype}, {q_pe.dtype}, {out.dtype})")
     if qc_e != 1 or qp_e != 1 or out_e != 1:
         raise ValueError("q_c, q_pe and out must have a unit last stride")
-    if q_pe.shape[:2] != (T, H) or out.shape != (T, H, R):
-        raise ValueError(f"q_pe must be [{T}, {H}, 64] and out [{T}, {H}, {R}] "
-                         f"(got {list(q_pe.shape)}, {list(out.shape)})")
+    if qp_T != T or qp_H != H:
+        _refuse("q_pe", q_pe, f"[{T}, {H}, 64]")
+    if out.shape != (T, H, R):
+        _refuse("out", out, f"[{T}, {H}, {R}]")
     lse_t = lse_h = 0
     if lse is not None:
-        lse_t, lse_h = _check_lse("lse", lse, (T, H))
-    _check_list("kv_lens", kv_lens, torch.int32, S)
-    _check_list("cu_q_lens", cu_q_lens, torch.int32, S + 1)
-    if (block_table.dtype is not torch.int32 or block_table.dim() != 2 or block_table.stride(1) != 1
-            or block_table.shape[0] < S):
-        raise ValueError(f"block_table must be int32 [{S}, W] with a unit last stride "
-                         f"(got {block_table.dtype} {list(block_table.shape)})")
-    if k_scale is not None and (k_scale.dtype is not torch.float32 or k_scale.numel() < 1):
-        raise ValueError(f"k_scale must be an fp32 scalar (got {k_scale.dtype} {list(k_scale.shape)})")
+        if lse.dtype is not torch.float32 or lse.shape != (T, H):
+            _refuse("lse", lse, f"fp32 [{T}, {H}]")
+        lse_t, lse_h = lse.stride()
+    if not _is_list(kv_lens, torch.int32, S):
+        _refuse("kv_lens", kv_lens, "contiguous int32")
+    if not _is_list(cu_q_lens, torch.int32, S + 1):
+        _refuse("cu_q_lens", cu_q_lens, f"contiguous int32 [{S + 1}]")
+    if block_table.dtype is not torch.int32 or block_table.ndim != 2:
+        _refuse("block_table", block_table, f"int32 [{S}, W]")
+    tab_S, tab_W = block_table.shape
+    tab_s, tab_e = block_table.stride()
+    if tab_e != 1 or tab_S < S:
+        _refuse("block_table", block_table, f"int32 [{S}, W] with a unit last stride")
+    if k_scale is not None and not _is_list(k_scale, torch.float32, 1):
+        _refuse("k_scale", k_scale, "an fp32 scalar")
     if not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
+        _refuse("workspace", workspace, "contiguous")
     status = lib().mla_latent_attention(
-        q_c.data_ptr(), qc_t, qc_h, q_pe.data_ptr(), qp_t, qp_h, T, H, R, q_pe.shape[2],
+        q_c.data_ptr(), qc_t, qc_h, q_pe.data_ptr(), qp_t, qp_h, T, H, R, P,
         kv_cache.data_ptr(), dtype_code(cache_dtype), num_blocks, block_size, block_stride,
-        entry_stride, block_table.data_ptr(), _bt_stride(block_table), cu_q_lens.data_ptr(),
+        entry_stride, block_table.data_ptr(), tab_s if tab_S > 1 else tab_W, cu_q_lens.data_ptr(),
         kv_lens.data_ptr(), S, softmax_scale, _ptr(k_scale), 1 if causal else 0,
         out.data_ptr(), out_t, out_h, _ptr(lse), lse_t, lse_h, workspace.data_ptr(),
         workspace.nbytes, _ptr(err_word), _stream(stream))
@@ -461,18 +469,23 @@ def mla_merge_attn_states(parts, lse, out, *, lse_out=None, stream=None):
     [P, T, H, D] (bf16, fp16 or fp32; any strides, unit last stride) with lse fp32
     [P, T, H] into out [T, H, D] of the same type and lse_out fp32 [T, H]."""
     P, T, H, Dm = parts.shape
+    p_p, p_t, p_h, p_e = parts.stride()
+    out_t, out_h, out_e = out.stride()
+    lo_t = lo_h = 0
     if parts.dtype != out.dtype:
         raise ValueError(f"out must have the parts' dtype ({parts.dtype}, got {out.dtype})")
     if out.shape != (T, H, Dm):
-        raise ValueError(f"out must be [{T}, {H}, {Dm}] (got {list(out.shape)})")
-    if parts.stride(3) != 1 or out.stride(2) != 1:
+        _refuse("out", out, f"[{T}, {H}, {Dm}]")
+    if p_e != 1 or out_e != 1:
         raise ValueError("parts and out must have a unit last stride")
-    _check_lse("lse", lse, (P, T, H))
+    if lse.dtype is not torch.float32 or lse.shape != (P, T, H):
+        _refuse("lse", lse, f"fp32 [{P}, {T}, {H}]")
     if lse_out is not None:
-        _check_lse("lse_out", lse_out, (T, H))
+        if lse_out.dtype is not torch.float32 or lse_out.shape != (T, H):
+            _refuse("lse_out", lse_out, f"fp32 [{T}, {H}]")
+        lo_t, lo_h = lse_out.stride()
+    lse_p, lse_t, lse_h = lse.stride()
     code = MLA_FP32 if parts.dtype == torch.float32 else dtype_code(parts.dtype)
     _check(lib().mla_merge_attn_states(
-        _ptr(parts), parts.stride(0), parts.stride(1), parts.stride(2), _ptr(lse), lse.stride(0),
-        lse.stride(1), lse.stride(2), code, P, T, H, Dm, _ptr(out), out.stride(0), out.stride(1),
-        _ptr(lse_out), 0 if lse_out is None else lse_out.stride(0),
-        0 if lse_out is None else lse_out.stride(1), _stream(stream)))
+        parts.data_ptr(), p_p, p_t, p_h, lse.data_ptr(), lse_p, lse_t, lse_h, code, P, T, H, Dm,
+        out.data_ptr(), out_t, out_h, _ptr(lse_out), lo_t, lo_h, _stream(stream)))
