@@ -1549,10 +1549,12 @@ cudaError_t launch_f(LatentAttnArgs a, int ctas, const LaunchCfg& cfg) {
 
 }  // namespace
 
-// The largest call within these sizes may use any tile: enough for 64 rows.
-int64_t latent_attention_workspace(int32_t, int32_t, int32_t, int num_sms) {
+// Calls of fewer sequences within these sizes have more rows per sequence, at most all of
+// them in one: its (bf16) tile is the largest that any of them takes.
+int64_t latent_attention_workspace(int32_t num_tokens, int32_t num_heads, int32_t, int num_sms) {
   const int64_t ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
-  return ctas * ((int64_t)sizeof(Split) + 2 * 64 * (2 + kRank) * (int64_t)sizeof(float));
+  const int64_t nr = attention_tile_rows(num_tokens, num_heads, 1, false);
+  return ctas * ((int64_t)sizeof(Split) + 2 * nr * (2 + kRank) * (int64_t)sizeof(float));
 }
 
 cudaError_t launch_latent_attention(const LatentAttnArgs& a, int cache_fmt, int num_sms,
