@@ -16,9 +16,9 @@
 // order of the CTAs (no atomics: equal calls give equal bits).
 //
 // Measured (replayed from a graph, without the profiler; 16 heads, 64-row blocks): one
-// new token of 4 sequences over 131072 bf16 rows 99.9 us (6.05 TB/s), of 64 over 130 to
-// 16384 e4m3 rows 60.3 us (5.2 TB/s), of one over 2047 bf16 rows 10.1 us; 1024 new
-// tokens of 2 over 8192 bf16 rows 645 us (849 TFLOP/s).  About 10 us of a call are fixed
+// new token of 4 sequences over 131072 bf16 rows 101 us (5.97 TB/s), of 64 over 130 to
+// 16384 e4m3 rows 60.3 us (5.2 TB/s), of one over 2047 bf16 rows 10.2 us; 1024 new
+// tokens of 2 over 8192 bf16 rows 643 us (852 TFLOP/s).  About 10 us of a call are fixed
 // (finding the run and the first rows 3, filling and draining the pipeline 4, the join 3).
 //
 // Both products are computed transposed, so that few query rows (a decode
@@ -46,10 +46,12 @@
 // less.  (Two e4m3 parts held 8 bits down to 2^-7 of the largest weight and nothing
 // below 2^-19: a tail of 131072 equal weights with 20% of the mass was lost.)
 //
-// Cost of a tile (measured, cycles per instruction: M = 64, N = 16 / 64 24 / 33;
-// M = 128 40 / 49; the A operand's shared memory reads bound both): bf16 36 + 16
-// instructions, 1500 cycles at NR = 16 and 2000 at NR = 64; fp8 18 + 8, 780 at
-// NR = 16.  HBM delivers a bf16 tile to each SM in 3140 cycles, an fp8 one in 1570.
+// Cost of a tile.  64 products in a row on resident operands take, per product, 24 / 25 /
+// 33 cycles at M = 64 and N = 16 / 32 / 64, and 40 / 45 / 49 / 57 at M = 128 and N = 16 /
+// 48 / 64 / 96 (the A operand's shared-memory reads bound them).  So the 36 + 16 products
+// of a bf16 tile take 1500 cycles at NR = 16 and 2000 at NR = 64, the 18 + 8 of an fp8
+// tile 820 and 1060: 0.4 to 1 us at 2070 MHz.  HBM's rate delivers a bf16 tile to each SM
+// in 1.65 us, an fp8 one in 0.82.
 //
 // Roles (10 or 14 warps): 4 or 8 warps do the softmax (running maximum per query
 // row, rescaling O^T only when a maximum has grown by more than 2^8, or 2^4 for
@@ -85,8 +87,10 @@ constexpr int kProdThreads = kProdWarps * 32;
 constexpr int kRank = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// A CTA takes at least this many units: one decode over 2047 rows took 11.3, 10.8 and
-// 12.9 us with 1, 2 and 3 (fewer: more partial sums to join; more: fewer SMs).
+// A CTA takes at least this many units (fewer: more partial sums to join; more: fewer SMs).
+// us with 1, 2 and 3, 16 heads, bf16: one decode over 512 rows 9.2, 9.5, 10.7, over 2047
+// 10.7, 10.3, 11.6, over 8192 16.7, 13.7, 13.6; four over 2047 11.7, 11.4, 12.2; one of
+// 128 heads over 2047 15.5, 14.8, 17.3.
 constexpr int kMinUnits = 2;
 constexpr float kQ2 = 0.0625f;            // query parts: q = q1 + q2 / 16
 constexpr float kPStep = 16.0f;           // weight parts: p = p1 + p2 / 16 + p3 / 256
@@ -107,7 +111,8 @@ struct Lay {
   // Halves of a stage (chunks 0 to 3 and the rest) that fill and are freed by
   // themselves.  At 64 query rows the chain load, scores, weights, outputs of the two
   // stages is what takes the time, and a half's load overlaps the outputs of the other
-  // (2 chunks of 1024 tokens over 8192 rows: 638 us, 682 with whole stages).
+  // (2 chunks of 1024 tokens over 8192 rows: 645 us, 689 with whole stages; 16 decodes of
+  // 128 heads 46.1, 47.7).
   static constexpr int kHalves = NR == 64 ? 2 : 1;
   static constexpr int kQBufs = NR <= (kF8 ? 16 : 32) ? 2 : 1;
   static constexpr int kQ = kChunks * kN * 128;
@@ -119,10 +124,15 @@ struct Lay {
   static constexpr int kWarps = kProdWarp + kProdWarps;
   static constexpr int kThreads = kWarps * 32;
   // What beginning another query tile costs a CTA, in key tiles (its queries, the sums
-  // of the one before; measured 2.3 us at fp8 NR = 16, 6.4 at fp8 NR = 32, 3.4 at
-  // bf16 NR = 64): the runs are cut as if each query tile had this many more.  Cut
-  // without it: 64 ragged decodes 66.4 us (62.8 with it), 32 verifications 58.0 (49.9),
-  // 16 decodes of 128 heads 50.3 (49.0).
+  // of the one before): the runs are cut as if each query tile had this many more.
+  // us with 0, 1, 2, 3, 4 and 6 of them (r. = ragged, 16 heads):
+  //   fp8  16  64 r. e4m3 decodes           62.1 61.2 60.8 60.2 60.0 61.0
+  //   fp8  32  32 r. verifications of 4     56.6 55.2 53.3 52.4 50.6 48.2
+  //            32 r. verifications of 2     37.0 36.8 35.5 34.4 33.9 31.9
+  //   bf16 16  64 r. decodes               103.7 103.5 103.7 104.1 104.4 105.3
+  //   bf16 32  32 r. verifications of 2     45.5 45.4 43.1 42.2 41.8 42.6
+  //   bf16 64  16 r. decodes, 128 heads     48.1 47.4 46.1 47.1 47.0 46.3
+  //            32 r. verifications of 4     55.7 55.7 53.1 52.0 50.9 51.2
   static constexpr int kSwitch = kF8 ? (NR == 16 ? 3 : 6) : (NR == 16 ? 1 : 2);
   // The reference of a row's weights is the next whole number (log2) above its maximum
   // less kTop; a score may pass the reference by kGrow before the sums are rescaled.
@@ -418,8 +428,8 @@ __device__ __forceinline__ void load_q(const LatentAttnArgs& a, const Tile& q, u
 // is off by at most 2^-21 of it below.  A row with a NaN or an infinity gets NaN
 // as its inverse scale.  8 lanes take a row, 16 bytes of every chunk each, so a
 // tile of 16 rows costs four warps one round of loads.  The producers do it, but for a
-// CTA's first query tile: there the kWarps softmax warps have nothing else to do (and the
-// producers did it behind the first rows, 5000 cycles into the kernel).
+// CTA's first query tile: there the kWarps softmax warps have nothing else to do (the
+// producers would do it behind the first rows).
 template <int NR, int kWarps>
 __device__ __forceinline__ void split_q(const LatentAttnArgs& a, const Tile& q, uint32_t dst,
                                         uint32_t scales, uint32_t bar, int pw, int lane) {
@@ -490,7 +500,7 @@ __device__ __forceinline__ uint32_t produce(const LatentAttnArgs& a, const CUten
   constexpr int kRows = 4;
   const int row0 = pw * 16 + (lane >> 3), col = lane & 7;
   // Boxes of box_rows keys x one chunk, `boxes` per chunk: number pw + 4 lane is this
-  // thread's (at most 72; issuing one takes ~100 cycles, so the four warps share
+  // thread's (at most 72; issuing them takes time, so the four warps share
   // them).  Lanes 28 to 31 write the flags of the warp's 16 keys, four each.
   const int boxes = 1 << a.box_shift;
   const int box = (pw + 4 * lane) & (boxes - 1), box_chunk = (pw + 4 * lane) >> a.box_shift;
@@ -628,10 +638,10 @@ __device__ __forceinline__ uint32_t produce(const LatentAttnArgs& a, const CUten
 // --------------------------------------------------------------- matrix issue
 // The whole warp runs these; one elected lane issues.  Descriptors are made the
 // same in all lanes (stage and buffer by a shuffle) and their loops have constant
-// bounds without branches inside, so that they live in uniform registers: 5
-// machine instructions and 25 to 50 cycles per product.  (In a branch of one lane
-// it was 90 cycles; an instance per stage and buffer spread the loop over 16 KB
-// of code, and fetching it cost as much again.)
+// bounds without branches inside, so that they live in uniform registers.  One instance
+// of each loop for all stages and buffers: the roles share the instruction caches, and
+// with an instance each, fetching was the largest stall (64 ragged decodes 81 us, 71
+// with one, both before later steps).
 template <int FMT, int NR>
 __device__ __forceinline__ void issue_scores(uint32_t smem, uint32_t tmem, bool one, int stage,
                                              int qbuf, int sbuf, int half, bool last) {
@@ -721,8 +731,8 @@ __device__ __noinline__ int cta_of(int64_t u, int64_t each, int extra) {
 
 // One warp issues the scores, another the outputs, each as soon as its operands
 // are there: outputs free the stage that the rows behind need, and from one warp
-// they would wait for the scores of the next tile (1000 to 1300 cycles) or for its
-// polls of both.
+// they would wait for the scores of the next tile or for its polls of both (2 chunks of
+// 1024 tokens 726 us from one warp, 695 from two, both before later steps).
 template <int FMT, int NR>
 __device__ __forceinline__ void score_role(const LatentAttnArgs& a, const Run& run, uint32_t smem,
                                            uint32_t tmem, const Waiter& waiter) {
@@ -781,7 +791,8 @@ __device__ __forceinline__ void output_role(const LatentAttnArgs& a, const Run& 
     item += t.last;
     if (__builtin_expect(t.last && t.kt + 1 < t.nkt && lane == 0, 0)) {
       // The run ends inside the query tile: for the join.  (This warp has nothing else to
-      // do now; the softmax warps spent 900 cycles on the divisions.)  The run's last unit
+      // do now; from the softmax warps one decode took 10.6 us, 10.3 from here, both before
+      // later steps.)  The run's last unit
       // is number t.kt of the tile's.
       const int64_t u0 = run.begin + run.count - 1 - t.kt;
       const int c0 = cta_of(u0, run.each, run.extra);
@@ -1382,8 +1393,8 @@ __global__ void __launch_bounds__(Lay<FMT, NR>::kThreads, 1)
 // for every row).  So a block mostly costs two dependent loads, whatever the batch, and
 // the grid, NR / 8 blocks per CTA, is one to four rounds of resident blocks.  With NR / 4
 // and the rows of few partials left to the first CTA's, most blocks found nothing to do:
-// 32 verifications took 46.6 us (45.9 now), 16 decodes of 128 heads 47.2 (45.8), one
-// decode 10.5 (10.1).
+// 32 verifications took 48.5 us (48.2 now), 16 decodes of 128 heads 47.3 (46.1), one
+// decode 10.7 (10.3).
 constexpr int kJoinGroups = 4;
 constexpr int kJoinThreads = kJoinGroups * 128;
 constexpr int kFewParts = 8;
@@ -1464,7 +1475,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) latent_join_kernel(const Late
 // The cache as a tensor of (column, entry, block), read in boxes of one chunk of
 // `rows` entries.  Without a box (entries per block not a multiple of 8, or sizes
 // that a tensor map does not hold) rows are copied one by one: 64 ragged e4m3 decodes
-// then take 93.5 us instead of 57.9, 4 x 131072 bf16 rows 107 instead of 99.9.
+// then take 94.0 us instead of 60.5, 4 x 131072 bf16 rows 107.5 instead of 99.4.
 // Returns the entries of a box, or 0.  (All chunks of a tile as one box of a
 // 4-dimensional map took the same time.)
 int box_map(const LatentAttnArgs& a, bool fp8, CUtensorMap* map) {
@@ -1534,9 +1545,11 @@ cudaError_t launch_f(LatentAttnArgs a, int ctas, const LaunchCfg& cfg) {
   for (int rows = a.box_rows; rows != 0 && rows < kKeys; rows *= 2) ++a.box_shift;
   const int nr = attention_tile_rows(a.num_tokens, a.num_heads, a.num_seqs, kF8);
   // Cache rows that up to four query tiles of a sequence read (at about the same time) are
-  // the first to leave L2: 64 ragged decodes 58.4 us (61.9 without the hint), 32
-  // verifications 46.3 (48.5), 16 decodes of 128 heads 47.1 (47.8).  The many query tiles
-  // of a prefill want them kept: 2 chunks of 1024 tokens 650 us (697 with the hint).
+  // the first to leave L2: 64 ragged decodes 60.5 us (62.9 without the hint), in bf16 103.5
+  // (107.3), 32 verifications 48.2 (50.5), 16 decodes of 128 heads 46.1 (46.9).  The many
+  // query tiles of a prefill want them kept: 2 chunks of 1024 tokens 645 us (699 with the
+  // hint).  16 bf16 sequences over 8192 rows at 2, 4, 8 and 16 query tiles each: 73.7, 121.8,
+  // 219.7 and 415 us with it, 74.0, 121.4, 213.6 and 391 without.
   a.stream_rows = (int64_t)a.num_tokens * a.num_heads <= (int64_t)4 * nr * a.num_seqs;
   switch (nr) {
     case 16: return launch_t<FMT, 16>(a, map, ctas, cfg);

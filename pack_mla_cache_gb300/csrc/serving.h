@@ -92,9 +92,13 @@ struct LatentAttnArgs {
 
 // Rows of a query tile of the attention: the average rows (tokens x heads) per sequence
 // decide.  fp8 tiles stop at 32: their split sums take three columns of tensor memory each.
-// Measured: 16 rows per sequence 57.9 us in tiles of 16 (64.7 in tiles of 32; 64 ragged
-// e4m3 decodes), 64 e5m2 rows 46.6 in tiles of 32 (60.7 in 16), 128 bf16 rows 47.3 and
-// 16384 rows 645 in tiles of 64 (61.9 and 1127 in 32).
+// Measured: 16 rows per sequence 60.5 us in tiles of 16 (67.7 in tiles of 32; 64 ragged
+// e4m3 decodes; in bf16 103.5 and 105.7), 32 bf16 rows 43.7 in tiles of 32 (57.5 in 16), 64
+// e5m2 rows 48.2 in tiles of 32 (65.5 in 16), 128 bf16 rows 46.1 and 16384 rows 645 in tiles
+// of 64 (61.9 and 1120 in 32).  One size for the whole call: a chunk of 1024 tokens beside 63
+// ragged decodes of 16 heads takes 444 us in bf16 and 478 in e4m3 (334 + 101 and 420 + 59
+// apart), one of 2048 beside 255 decodes of one head, in tiles of 16, 494 and 291 (62 + 371
+// and 64 + 203 apart).
 inline int attention_tile_rows(int32_t num_tokens, int32_t num_heads, int32_t num_seqs, bool fp8) {
   const int64_t rows = ((int64_t)num_tokens + num_seqs - 1) / num_seqs * num_heads;
   return rows <= 16 ? 16 : rows <= 32 || fp8 ? 32 : 64;
