@@ -617,8 +617,9 @@ mla_status_t mla_cache_copy_blocks(const int64_t* kv_cache_ptrs, int32_t num_lay
  *   lse                 fp32 [T, H] by strides, or NULL.
  *   workspace           16-byte aligned device memory of workspace_bytes >=
  *                       what mla_latent_attention_workspace gives.  Its
- *                       contents before and after a call mean nothing; calls that may run at the same time (on
- *                       two streams) need one each.
+ *                       contents before and after a call mean nothing; calls
+ *                       that may run at the same time (on two streams) need
+ *                       one each.
  * out, lse and workspace must not overlap each other or the inputs.
  * Scores times log2 e must be finite in fp32, and cache values below 2^80 in magnitude
  * (unnormalised sums are held in fp32).

@@ -417,7 +417,8 @@ def mla_latent_attention(q_c, q_pe, kv_cache, cache_dtype, num_blocks, block_siz
     """Attention of new tokens over the paged latent cache (absorbed form):
     q_c [T, H, 512] and q_pe [T, H, 64] bf16 views (any strides, unit last
     stride), out bf16 [T, H, 512] likewise, lse fp32 [T, H] or None; block_table
-    int32 [S, W], cu_q_lens int32 [S + 1], kv_lens int32 [S]; k_scale fp32;
+    int32 [S, W] (a slice of a wider table is as wide as its row stride),
+    cu_q_lens int32 [S + 1], kv_lens int32 [S]; k_scale fp32;
     workspace: a uint8 tensor of ``mla_latent_attention_workspace`` bytes."""
     T, H, R = q_c.shape
     qc_t, qc_h, qc_e = q_c.stride()
