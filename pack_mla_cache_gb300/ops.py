@@ -388,8 +388,8 @@ def mla_cache_copy_blocks(kv_cache_ptrs, cache_dtype, num_blocks, block_size, bl
     """Copy (fork, compact) or clear (src -1) blocks in every layer's cache:
     kv_cache_ptrs int64 [L]; src_blocks / dst_blocks / row_counts int32 [N],
     row_counts None for whole blocks."""
-    N = dst_blocks.shape[0]
-    if not _is_list(kv_cache_ptrs, torch.int64, 0):
+    N, L = dst_blocks.numel(), kv_cache_ptrs.numel()
+    if not _is_list(kv_cache_ptrs, torch.int64, L):
         _refuse("kv_cache_ptrs", kv_cache_ptrs, "contiguous int64")
     if not _is_list(dst_blocks, torch.int32, N):
         _refuse("dst_blocks", dst_blocks, "contiguous int32")
@@ -398,7 +398,7 @@ def mla_cache_copy_blocks(kv_cache_ptrs, cache_dtype, num_blocks, block_size, bl
     if row_counts is not None and not _is_list(row_counts, torch.int32, N):
         _refuse("row_counts", row_counts, f"contiguous int32 [{N}]")
     _check(lib().mla_cache_copy_blocks(
-        _ptr(kv_cache_ptrs), kv_cache_ptrs.shape[0], dtype_code(cache_dtype), num_blocks,
+        _ptr(kv_cache_ptrs), L, dtype_code(cache_dtype), num_blocks,
         block_size, block_stride, entry_stride, entry_dim, _ptr(src_blocks), _ptr(dst_blocks),
         _ptr(row_counts), N, _ptr(err_word), _stream(stream)))
 
@@ -424,7 +424,7 @@ def mla_latent_attention(q_c, q_pe, kv_cache, cache_dtype, num_blocks, block_siz
     qc_t, qc_h, qc_e = q_c.stride()
     qp_t, qp_h, qp_e = q_pe.stride()
     out_t, out_h, out_e = out.stride()
-    S = kv_lens.shape[0]
+    S = kv_lens.numel()
     bf16 = torch.bfloat16
     qp_T, qp_H, P = q_pe.shape
     if q_c.dtype is not bf16 or q_pe.dtype is not bf16 or out.dtype is not bf16:

@@ -135,3 +135,23 @@ def test_the_current_stream_is_the_one_torch_names():
     assert ops._stream(None) == torch.cuda.current_stream().cuda_stream
     with torch.cuda.stream(s):
         assert ops._stream(None) == s.cuda_stream == torch.cuda.current_stream().cuda_stream
+
+
+def test_lists_count_their_elements(monkeypatch):
+    """A list as a row [1, n] is n elements (its first extent alone dropped the others)."""
+    seen = {}
+
+    class Lib:
+        @staticmethod
+        def mla_cache_copy_blocks(*a):
+            seen["copy"] = (a[1], a[11])
+            return 0
+
+        @staticmethod
+        def mla_latent_attention(*a):
+            seen["seqs"] = a[20]
+            return 0
+    monkeypatch.setattr(ops, "lib", lambda: Lib)
+    copy(kv_cache_ptrs=torch.zeros(1, 2, dtype=torch.int64), dst_blocks=torch.zeros(1, 3, dtype=I32))
+    attend(kv_lens=torch.zeros(1, 3, dtype=I32))
+    assert seen == {"copy": (2, 3), "seqs": 3}
