@@ -448,9 +448,9 @@ def mla_latent_attention(q_c, q_pe, kv_cache, cache_dtype, num_blocks, block_siz
         _refuse("block_table", block_table, f"int32 [{S}, W]")
     tab_S, tab_W = block_table.shape
     tab_s, tab_e = block_table.stride()
-    if tab_e != 1 or tab_S < S:
+    if (tab_e != 1 and tab_W > 1) or tab_S < S:
         _refuse("block_table", block_table, f"int32 [{S}, W] with a unit last stride")
-    if k_scale is not None and not _is_list(k_scale, torch.float32, 1):
+    if k_scale is not None and (k_scale.dtype is not torch.float32 or k_scale.numel() < 1):
         _refuse("k_scale", k_scale, "an fp32 scalar")
     if not workspace.is_contiguous():
         _refuse("workspace", workspace, "contiguous")

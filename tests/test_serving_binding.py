@@ -55,6 +55,8 @@ def test_attention_refuses(kw, msg):
     dict(), dict(lse=None), dict(block_table=torch.zeros(4, 5, dtype=I32)),
     dict(lse=torch.zeros(2, 4).t()), dict(q_c=torch.zeros(1, 1, 512, dtype=BF16).expand(4, 2, 512)),
     dict(block_table=torch.zeros(3, 9, dtype=I32)[:, :5]), dict(cu_q_lens=torch.zeros(9, dtype=I32)),
+    dict(block_table=torch.zeros(1, 3, dtype=I32).t()), dict(k_scale=torch.ones(1).expand(4)),
+    dict(k_scale=torch.tensor(1.0)),
 ])
 def test_attention_forwards_what_the_interface_takes(kw):
     """Host tensors of the right form pass the binding and are refused by the library."""
