@@ -14,9 +14,11 @@
  *      packing", Implementation items 1-2 and Source snippets:
  *      fused_mla_kv_concat / fused_mla_kv_concat_quant_fp8);
  *   3. what a serving loop runs on these caches next: the attention of new
- *      tokens over the paged latent rows, the join of attention results over
- *      parts of the context, and the copying, forking, compacting and clearing
- *      of cache blocks.
+ *      tokens (a run of them, or a tree of drafted ones) over the paged latent
+ *      rows, the attention of prompts and chunks over the packed keys and values,
+ *      the join of attention results over parts of the context, the copying,
+ *      forking, compacting and clearing of cache blocks, and the moving of
+ *      accepted rows.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -101,7 +103,7 @@ enum {
   MLA_ERRBIT_POS_OOB = 4u,    /* position outside [0, max_position) */
   MLA_ERRBIT_MISALIGNED = 8u, /* a per-layer cache base null or not 16-byte aligned */
   MLA_ERRBIT_TIMEOUT = 16u     /* a pipeline wait gave up (see mla_cache_insert_grouped
-                                  and mla_latent_attention) */
+                                  and the attentions) */
 };
 
 /* Map a vLLM kv-cache-dtype string to mla_dtype_t; -1 if it is not one of
@@ -639,8 +641,147 @@ mla_status_t mla_latent_attention(
     int64_t lse_token_stride, int64_t lse_head_stride, void* workspace, int64_t workspace_bytes,
     uint32_t* err_word, mla_stream_t stream);
 
-/* TESTING HOOK for mla_latent_attention, applied to every later call from this
- * process (not for production use).  wait_limit_ns: how long a wait may last before
+/*
+ * The attention of mla_latent_attention for trees of drafted tokens: a token sees
+ * all rows before its sequence's new tokens, and of the new ones' rows those that its
+ * mask names (its ancestors and itself).  Sequence s has n = cu_q_lens[s+1] -
+ * cu_q_lens[s] new tokens, whose rows are the last n of its kv_lens[s]; its token
+ * number j (t = cu_q_lens[s] + j) sees the rows
+ *   p < kv_lens[s] - n, and
+ *   p = kv_lens[s] - n + i  (0 <= i < n, p >= 0)  where bit i % 32 of
+ *   tree_mask[t * mask_stride + i / 32] is set.
+ * A new row whose word lies behind mask_words is not seen.  A mask may name any rows,
+ * also none, and any token's row.
+ *
+ *   tree_mask           int32 device [num_tokens, mask_words], rows mask_stride
+ *                       words apart.
+ *   mask_words          1 to 1024.
+ * Every other argument and rule is that of mla_latent_attention, its workspace
+ * (mla_latent_attention_workspace) too.
+ */
+mla_status_t mla_latent_tree_attention(
+    const void* q_c, int64_t qc_token_stride, int64_t qc_head_stride, const void* q_pe,
+    int64_t qpe_token_stride, int64_t qpe_head_stride, int32_t num_tokens, int32_t num_heads,
+    int32_t kv_lora_rank, int32_t pe_dim, const void* kv_cache, mla_dtype_t cache_dtype,
+    int64_t num_blocks, int32_t block_size, int64_t block_stride, int64_t entry_stride,
+    const int32_t* block_table, int64_t block_table_stride, const int32_t* cu_q_lens,
+    const int32_t* kv_lens, int32_t num_seqs, float softmax_scale, const float* k_scale,
+    const int32_t* tree_mask, int64_t mask_stride, int32_t mask_words, void* out,
+    int64_t out_token_stride, int64_t out_head_stride, float* lse, int64_t lse_token_stride,
+    int64_t lse_head_stride, void* workspace, int64_t workspace_bytes, uint32_t* err_word,
+    mla_stream_t stream);
+
+/*
+ * Move the rows of accepted drafted tokens to the front of the drafted ones, in the
+ * paged caches of every layer in ONE launch: what follows the verification of a tree
+ * (mla_latent_tree_attention), whose accepted branch is rarely contiguous.  For every
+ * layer l < num_layers, sequence s < num_seqs and i < counts[s], with start = starts[s]:
+ *   row start + i of the sequence becomes what its row
+ *   start + rows[s * rows_stride + i] was before the call,
+ * where row p is the first entry_dim elements of entry p % block_size of block
+ * block_table[s * block_table_stride + p / block_size].  Everything else is left as it
+ * was (rows behind the last accepted one too).
+ *
+ *   kv_cache_ptrs ... entry_dim  as in mla_cache_copy_blocks.
+ *   block_table         int32 device [num_seqs, block_table_stride].  Blocks that
+ *                       receive rows must belong to one sequence only.
+ *   starts              int32 device [num_seqs]: the row of the first drafted token.
+ *   rows                int32 device [num_seqs, max_rows], lists rows_stride elements
+ *                       apart, each strictly increasing over its first counts[s]
+ *                       elements and not below 0.  max_rows at most 1024.
+ *   counts              int32 device [num_seqs]; 0 moves nothing.
+ * A sequence whose list is not of that form, or whose start or count is negative or
+ * count above max_rows, is left as it is (MLA_ERRBIT_POS_OOB); so is one with a row
+ * behind its table's or in a block whose id is out of range (MLA_ERRBIT_BLOCK_OOB).
+ */
+mla_status_t mla_cache_compact_rows(const int64_t* kv_cache_ptrs, int32_t num_layers,
+                                    mla_dtype_t cache_dtype, int64_t num_blocks,
+                                    int32_t block_size, int64_t block_stride,
+                                    int64_t entry_stride, int32_t entry_dim,
+                                    const int32_t* block_table, int64_t block_table_stride,
+                                    const int32_t* starts, const int32_t* rows,
+                                    int64_t rows_stride, int32_t max_rows, const int32_t* counts,
+                                    int32_t num_seqs, uint32_t* err_word, mla_stream_t stream);
+
+/*
+ * Attention of packed sequences over keys and values per head: whole prompts, chunks
+ * of new tokens and single tokens, over what the chunked-context pack writes ("PR
+ * #51772", Implementation items 1-2: each chunk's packed K/V gives a partial result;
+ * mla_merge_attn_states joins them), or over the kv_b_proj output and the k_pe
+ * workspace in place.
+ *
+ * Sequence s < num_seqs owns the tokens [cu_q_lens[s], cu_q_lens[s+1]), n of them, and
+ * the key rows [cu_kv_lens[s], cu_kv_lens[s+1]), m of them.  Its token number j sees
+ *   p < m                  causal == 0
+ *   p < m - n + 1 + j      causal != 0   (its own row is the last one it sees)
+ * of them, and for each head h, with g = h / (num_heads / num_kv_heads),
+ *   x_p       = softmax_scale * (<q_nope[t,h], k_nope[p,g]> + <q_pe[t,h], k_pe[p,g]>)
+ *   lse[t,h]  = ln(sum_p exp(x_p))
+ *   out[t,h]  = sum_p exp(x_p - lse[t,h]) * v[p,g]
+ * where fp8 keys and values are the codes' values times *kv_scale.  A token that sees
+ * no row has out = 0 and lse = -infinity.  A row that a token does not see has no
+ * influence on its result, whatever the row holds; the result of a token that sees a
+ * row with a NaN or an infinity is not specified.
+ *
+ * Arithmetic: products of the stored 16-bit values summed in fp32, softmax in fp32,
+ * one rounding of the result to dtype.  Weights exp(x_p), relative to a power of two
+ * near the largest seen so far, are rounded before their products: to bf16 (2^-8 of
+ * themselves) with bf16 keys and values, and to fp16 (2^-11 of themselves, or 2^-34 of
+ * the row's largest) with fp16 and fp8 ones; the sum that they are divided by counts
+ * them unrounded.  With fp8 keys and bf16 queries, elements of q below 2^-28 of their
+ * row's largest magnitude are off by at most 2^-39 of that magnitude.  Results do not
+ * depend on other work on the device; the call's sizes, its lengths and the device's
+ * number of SMs decide how rows are cut, and results depend on them through fp32
+ * roundings only.
+ *
+ *   q_nope, q_pe        dtype (MLA_BF16 or MLA_FP16); element (t, h, e) at
+ *                       t * token_stride + h * head_stride + e (a [T, H, 192] query:
+ *                       q_nope = base, q_pe = base + 128).
+ *   num_tokens          rows of q and out; tokens owned by no sequence, and those
+ *                       numbered num_tokens and above, are not touched.
+ *   num_heads           1 to 1024, a multiple of num_kv_heads.
+ *   k_nope, k_pe, v     kv_dtype (dtype, MLA_FP8_E4M3 or MLA_FP8_E5M2); element
+ *                       (p, g, e) by their strides (positive between tokens; 0
+ *                       between heads where all heads share the rows, as k_pe does).
+ *   num_kv_tokens       rows of k and v; key rows of a sequence behind them (or
+ *                       before 0) are left out of the sums (MLA_ERRBIT_POS_OOB).
+ *   nope_dim, rope_dim, v_dim  must be 128, 64, 128 (else UNSUPPORTED).
+ *   cu_q_lens, cu_kv_lens  int32 device [num_seqs + 1], non-decreasing.
+ *   num_seqs            1 to 4096.
+ *   softmax_scale       finite.
+ *   kv_scale            device fp32 scalar: required for fp8 keys and values, must be
+ *                       NULL for others.
+ *   out                 dtype [T, H, v_dim] by strides.
+ *   lse                 fp32 [T, H] by strides, or NULL.
+ *   workspace           16-byte aligned device memory of workspace_bytes >= what
+ *                       mla_prefill_attention_workspace gives, as in
+ *                       mla_latent_attention.
+ * All rows start on 16-byte boundaries.  out, lse and workspace must not overlap each
+ * other or the inputs.  Scores times log2 e must be finite in fp32.
+ * The kernel's internal waits are bounded as mla_latent_attention's are
+ * (MLA_ERRBIT_TIMEOUT).
+ */
+mla_status_t mla_prefill_attention(
+    const void* q_nope, int64_t qn_token_stride, int64_t qn_head_stride, const void* q_pe,
+    int64_t qpe_token_stride, int64_t qpe_head_stride, mla_dtype_t dtype, int32_t num_tokens,
+    int32_t num_heads, const void* k_nope, int64_t kn_token_stride, int64_t kn_head_stride,
+    const void* k_pe, int64_t kpe_token_stride, int64_t kpe_head_stride, const void* v,
+    int64_t v_token_stride, int64_t v_head_stride, mla_dtype_t kv_dtype, int32_t num_kv_tokens,
+    int32_t num_kv_heads, int32_t nope_dim, int32_t rope_dim, int32_t v_dim,
+    const int32_t* cu_q_lens, const int32_t* cu_kv_lens, int32_t num_seqs, float softmax_scale,
+    const float* kv_scale, int32_t causal, void* out, int64_t out_token_stride,
+    int64_t out_head_stride, float* lse, int64_t lse_token_stride, int64_t lse_head_stride,
+    void* workspace, int64_t workspace_bytes, uint32_t* err_word, mla_stream_t stream);
+
+/* Writes to *bytes (host memory) the workspace that mla_prefill_attention needs on the
+ * current device for any call of at most num_tokens tokens and num_seqs sequences with
+ * num_heads and num_kv_heads heads.  Host only. */
+mla_status_t mla_prefill_attention_workspace(int32_t num_tokens, int32_t num_heads,
+                                             int32_t num_kv_heads, int32_t num_seqs,
+                                             int64_t* bytes);
+
+/* TESTING HOOK for the attentions (mla_latent_attention, mla_latent_tree_attention,
+ * mla_prefill_attention), applied to every later call from this process (not for production use).  wait_limit_ns: how long a wait may last before
  * the kernel gives up (0 restores the default of 2 s).  stall_stage >= 1: that stage
  * of the first CTA's pipeline never fills, so its waits run out of time; 0 (the
  * default) stalls nothing.  Returns 0. */

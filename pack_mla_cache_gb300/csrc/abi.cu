@@ -966,7 +966,9 @@ mla_status_t mla_latent_attention_workspace(int32_t num_tokens, int32_t num_head
   return MLA_OK;
 }
 
-mla_status_t mla_latent_attention(
+// Both attentions over the latent cache; tree: a mask over the new tokens instead of causal.
+static mla_status_t latent_attention(
+    bool tree, const int32_t* tree_mask, int64_t mask_stride, int32_t mask_words,
     const void* q_c, int64_t qc_token_stride, int64_t qc_head_stride, const void* q_pe,
     int64_t qpe_token_stride, int64_t qpe_head_stride, int32_t num_tokens, int32_t num_heads,
     int32_t kv_lora_rank, int32_t pe_dim, const void* kv_cache, mla_dtype_t cache_dtype,
@@ -990,6 +992,13 @@ mla_status_t mla_latent_attention(
   if (!fp8 && k_scale) return fail(MLA_ERR_INVALID_ARG, "a bf16 cache does not use k_scale");
   if (!(softmax_scale > -3.0e38f) || !(softmax_scale < 3.0e38f))
     return fail(MLA_ERR_INVALID_ARG, "softmax_scale must be finite");
+  if (tree) {
+    if (mask_words < 1) return fail(MLA_ERR_INVALID_ARG, "mask_words must be >= 1");
+    if (mask_words > mla::kMaxTree / 32)
+      return fail(MLA_ERR_UNSUPPORTED, "masks of more than %d drafted tokens are not built", mla::kMaxTree);
+    if (reinterpret_cast<uintptr_t>(tree_mask) & 3)
+      return fail(MLA_ERR_MISALIGNED, "tree_mask must be 4-byte aligned");
+  }
   const int ce = elt_size(cache_dtype);
   MLA_TRY(check_paged(kv_cache, num_blocks, block_size, block_stride, entry_stride, 0,
                       kv_lora_rank + pe_dim, ce, block_table, block_table_stride, cu_q_lens,
@@ -1009,6 +1018,7 @@ mla_status_t mla_latent_attention(
     return fail(MLA_ERR_INVALID_ARG,
                 "q_c, q_pe, kv_cache, block_table, cu_q_lens, kv_lens, out and workspace must be "
                 "non-null");
+  if (tree && !tree_mask) return fail(MLA_ERR_INVALID_ARG, "tree_mask must be non-null");
   int sms = 0;
   MLA_TRY(current_sms(&sms));
   const int64_t need = mla::latent_attention_workspace(num_tokens, num_heads, num_seqs, sms);
@@ -1025,6 +1035,7 @@ mla_status_t mla_latent_attention(
   MLA_TRY(check_device_ptr(out, "out"));
   if (lse) MLA_TRY(check_device_ptr(lse, "lse"));
   MLA_TRY(check_device_ptr(workspace, "workspace"));
+  if (tree) MLA_TRY(check_device_ptr(tree_mask, "tree_mask"));
   if (err_word) MLA_TRY(check_device_ptr(err_word, "err_word"));
 
   mla::LatentAttnArgs a{};
@@ -1054,6 +1065,9 @@ mla_status_t mla_latent_attention(
   a.softmax_scale = softmax_scale;
   a.k_scale = k_scale;
   a.causal = causal != 0;
+  a.tree = reinterpret_cast<const uint32_t*>(tree_mask);
+  a.tree_ts = mask_stride;
+  a.tree_words = (uint32_t)mask_words;
   a.out = static_cast<uint8_t*>(out);
   a.out_ts = out_token_stride * 2;
   a.out_hs = out_head_stride * 2;
@@ -1064,8 +1078,266 @@ mla_status_t mla_latent_attention(
   a.err = err_word;
   a.wait_limit_ns = g_attention_wait_ns.load();
   a.stall_stage = g_attention_stall.load();
+  if (tree)
+    return launched(mla::launch_latent_tree_attention(a, (int)cache_dtype, sms, cfg_for(stream)),
+                    "mla_latent_tree_attention");
   return launched(mla::launch_latent_attention(a, (int)cache_dtype, sms, cfg_for(stream)),
                   "mla_latent_attention");
+}
+
+mla_status_t mla_latent_attention(
+    const void* q_c, int64_t qc_token_stride, int64_t qc_head_stride, const void* q_pe,
+    int64_t qpe_token_stride, int64_t qpe_head_stride, int32_t num_tokens, int32_t num_heads,
+    int32_t kv_lora_rank, int32_t pe_dim, const void* kv_cache, mla_dtype_t cache_dtype,
+    int64_t num_blocks, int32_t block_size, int64_t block_stride, int64_t entry_stride,
+    const int32_t* block_table, int64_t block_table_stride, const int32_t* cu_q_lens,
+    const int32_t* kv_lens, int32_t num_seqs, float softmax_scale, const float* k_scale,
+    int32_t causal, void* out, int64_t out_token_stride, int64_t out_head_stride, float* lse,
+    int64_t lse_token_stride, int64_t lse_head_stride, void* workspace, int64_t workspace_bytes,
+    uint32_t* err_word, mla_stream_t stream) {
+  return latent_attention(false, nullptr, 0, 0, q_c, qc_token_stride, qc_head_stride, q_pe,
+                          qpe_token_stride, qpe_head_stride, num_tokens, num_heads, kv_lora_rank, pe_dim, kv_cache, cache_dtype,
+                          num_blocks, block_size, block_stride, entry_stride, block_table,
+                          block_table_stride, cu_q_lens, kv_lens, num_seqs, softmax_scale, k_scale,
+                          causal, out, out_token_stride, out_head_stride, lse, lse_token_stride,
+                          lse_head_stride, workspace, workspace_bytes, err_word, stream);
+}
+
+mla_status_t mla_latent_tree_attention(
+    const void* q_c, int64_t qc_token_stride, int64_t qc_head_stride, const void* q_pe,
+    int64_t qpe_token_stride, int64_t qpe_head_stride, int32_t num_tokens, int32_t num_heads,
+    int32_t kv_lora_rank, int32_t pe_dim, const void* kv_cache, mla_dtype_t cache_dtype,
+    int64_t num_blocks, int32_t block_size, int64_t block_stride, int64_t entry_stride,
+    const int32_t* block_table, int64_t block_table_stride, const int32_t* cu_q_lens,
+    const int32_t* kv_lens, int32_t num_seqs, float softmax_scale, const float* k_scale,
+    const int32_t* tree_mask, int64_t mask_stride, int32_t mask_words, void* out,
+    int64_t out_token_stride, int64_t out_head_stride, float* lse, int64_t lse_token_stride,
+    int64_t lse_head_stride, void* workspace, int64_t workspace_bytes, uint32_t* err_word,
+    mla_stream_t stream) {
+  return latent_attention(true, tree_mask, mask_stride, mask_words, q_c, qc_token_stride,
+                          qc_head_stride, q_pe, qpe_token_stride, qpe_head_stride, num_tokens, num_heads, kv_lora_rank, pe_dim, kv_cache, cache_dtype,
+                          num_blocks, block_size, block_stride, entry_stride, block_table,
+                          block_table_stride, cu_q_lens, kv_lens, num_seqs, softmax_scale, k_scale,
+                          0, out, out_token_stride, out_head_stride, lse, lse_token_stride,
+                          lse_head_stride, workspace, workspace_bytes, err_word, stream);
+}
+
+mla_status_t mla_cache_compact_rows(const int64_t* kv_cache_ptrs, int32_t num_layers,
+                                    mla_dtype_t cache_dtype, int64_t num_blocks,
+                                    int32_t block_size, int64_t block_stride,
+                                    int64_t entry_stride, int32_t entry_dim,
+                                    const int32_t* block_table, int64_t block_table_stride,
+                                    const int32_t* starts, const int32_t* rows,
+                                    int64_t rows_stride, int32_t max_rows, const int32_t* counts,
+                                    int32_t num_seqs, uint32_t* err_word, mla_stream_t stream) {
+  if (num_seqs < 0) return fail(MLA_ERR_INVALID_ARG, "num_seqs must be >= 0");
+  if (num_layers <= 0) return fail(MLA_ERR_INVALID_ARG, "num_layers must be >= 1");
+  if (num_layers > 128) return fail(MLA_ERR_UNSUPPORTED, "at most 128 layers per call are built");
+  if (!cache_dtype_ok(cache_dtype))
+    return fail(MLA_ERR_INVALID_ARG,
+                "cache_dtype must be MLA_BF16, MLA_FP8_E4M3 or MLA_FP8_E5M2; got %d",
+                (int)cache_dtype);
+  if (block_size <= 0 || num_blocks <= 0 || block_table_stride <= 0)
+    return fail(MLA_ERR_INVALID_ARG, "block_size, num_blocks and block_table_stride must be >= 1");
+  if (entry_dim <= 0 || entry_dim > entry_stride)
+    return fail(MLA_ERR_INVALID_ARG, "entry_dim must lie in [1, entry_stride]");
+  if (!block_holds(block_size, block_stride, entry_stride, entry_dim))
+    return fail(MLA_ERR_INVALID_ARG, "block_stride is too small for block_size entries");
+  if (max_rows < 0) return fail(MLA_ERR_INVALID_ARG, "max_rows must be >= 0");
+  if (max_rows > mla::kMaxAccepted)
+    return fail(MLA_ERR_UNSUPPORTED, "at most %d rows per sequence are built", mla::kMaxAccepted);
+  const int ce = elt_size(cache_dtype);
+  if (!m16(block_stride * ce) || !m16(entry_stride * ce))
+    return fail(MLA_ERR_MISALIGNED, "cache block_stride / entry_stride must be multiples of 16 bytes");
+  if (!m16((int64_t)entry_dim * ce))
+    return fail(MLA_ERR_MISALIGNED, "entry_dim must span a multiple of 16 bytes");
+  const int64_t row_chunks = (int64_t)entry_dim * ce / 16;
+  if ((row_chunks * num_layers / 128 + 1) * num_seqs >= (int64_t(1) << 31))
+    return fail(MLA_ERR_UNSUPPORTED, "num_seqs * num_layers * entry_dim is too large for one call");
+  if (reinterpret_cast<uintptr_t>(kv_cache_ptrs) & 7)
+    return fail(MLA_ERR_MISALIGNED, "kv_cache_ptrs must be 8-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(starts) |
+       reinterpret_cast<uintptr_t>(rows) | reinterpret_cast<uintptr_t>(counts)) & 3)
+    return fail(MLA_ERR_MISALIGNED, "int32 index arrays must be 4-byte aligned");
+  if (err_word && (reinterpret_cast<uintptr_t>(err_word) & 3))
+    return fail(MLA_ERR_MISALIGNED, "err_word must be 4-byte aligned");
+  if (num_seqs == 0 || max_rows == 0) return MLA_OK;  // empty inputs may have null data pointers
+  if (!kv_cache_ptrs || !block_table || !starts || !rows || !counts)
+    return fail(MLA_ERR_INVALID_ARG,
+                "kv_cache_ptrs, block_table, starts, rows and counts must be non-null");
+  MLA_TRY(check_device_ptr(kv_cache_ptrs, "kv_cache_ptrs"));
+  MLA_TRY(check_device_ptr(block_table, "block_table"));
+  MLA_TRY(check_device_ptr(starts, "starts"));
+  MLA_TRY(check_device_ptr(rows, "rows"));
+  MLA_TRY(check_device_ptr(counts, "counts"));
+  if (err_word) MLA_TRY(check_device_ptr(err_word, "err_word"));
+
+  mla::CompactArgs a{};
+  a.cache_ptrs = kv_cache_ptrs;
+  a.num_layers = num_layers;
+  a.num_blocks = num_blocks;
+  a.block_stride = block_stride * ce;
+  a.entry_stride = entry_stride * ce;
+  a.block_size = block_size;
+  a.by_block = mla::Divider::by((uint32_t)block_size);
+  a.row_chunks = (int32_t)row_chunks;
+  a.block_table = block_table;
+  a.bt_stride = block_table_stride;
+  a.room = (int32_t)(block_table_stride > INT32_MAX / block_size ? INT32_MAX
+                                                                 : block_table_stride * block_size);
+  a.starts = starts;
+  a.rows = rows;
+  a.rows_stride = rows_stride;
+  a.width = max_rows;
+  a.counts = counts;
+  a.num_seqs = num_seqs;
+  a.err = err_word;
+  return launched(mla::launch_compact_rows(a, cfg_for(stream)), "mla_cache_compact_rows");
+}
+
+// Sizes of a prefill attention; no CUDA call.
+static mla_status_t check_prefill_sizes(int32_t num_tokens, int32_t num_heads,
+                                        int32_t num_kv_heads, int32_t num_seqs) {
+  MLA_TRY(check_attention_sizes(num_tokens, num_heads, num_seqs));
+  if (num_kv_heads <= 0 || num_heads % num_kv_heads)
+    return fail(MLA_ERR_INVALID_ARG, "num_kv_heads must be >= 1 and divide num_heads (got %d, %d)",
+                num_kv_heads, num_heads);
+  return MLA_OK;
+}
+
+mla_status_t mla_prefill_attention_workspace(int32_t num_tokens, int32_t num_heads,
+                                             int32_t num_kv_heads, int32_t num_seqs,
+                                             int64_t* bytes) {
+  MLA_TRY(check_prefill_sizes(num_tokens, num_heads, num_kv_heads, num_seqs));
+  if (!bytes) return fail(MLA_ERR_INVALID_ARG, "bytes must be non-null");
+  int sms = 0;
+  MLA_TRY(current_sms(&sms));
+  *bytes = mla::prefill_attention_workspace(num_tokens, num_heads, num_kv_heads, num_seqs, sms);
+  return MLA_OK;
+}
+
+mla_status_t mla_prefill_attention(
+    const void* q_nope, int64_t qn_token_stride, int64_t qn_head_stride, const void* q_pe,
+    int64_t qpe_token_stride, int64_t qpe_head_stride, mla_dtype_t dtype, int32_t num_tokens,
+    int32_t num_heads, const void* k_nope, int64_t kn_token_stride, int64_t kn_head_stride,
+    const void* k_pe, int64_t kpe_token_stride, int64_t kpe_head_stride, const void* v,
+    int64_t v_token_stride, int64_t v_head_stride, mla_dtype_t kv_dtype, int32_t num_kv_tokens,
+    int32_t num_kv_heads, int32_t nope_dim, int32_t rope_dim, int32_t v_dim,
+    const int32_t* cu_q_lens, const int32_t* cu_kv_lens, int32_t num_seqs, float softmax_scale,
+    const float* kv_scale, int32_t causal, void* out, int64_t out_token_stride,
+    int64_t out_head_stride, float* lse, int64_t lse_token_stride, int64_t lse_head_stride,
+    void* workspace, int64_t workspace_bytes, uint32_t* err_word, mla_stream_t stream) {
+  MLA_TRY(check_prefill_sizes(num_tokens, num_heads, num_kv_heads, num_seqs));
+  if (num_kv_tokens < 0) return fail(MLA_ERR_INVALID_ARG, "num_kv_tokens must be >= 0");
+  if (nope_dim != 128 || rope_dim != 64 || v_dim != 128)
+    return fail(MLA_ERR_UNSUPPORTED, "only nope_dim 128, rope_dim 64, v_dim 128 are built");
+  if (dtype != MLA_BF16 && dtype != MLA_FP16)
+    return fail(MLA_ERR_INVALID_ARG, "dtype must be MLA_BF16 or MLA_FP16; got %d", (int)dtype);
+  const bool fp8 = kv_dtype == MLA_FP8_E4M3 || kv_dtype == MLA_FP8_E5M2;
+  if (!fp8 && kv_dtype != dtype)
+    return fail(MLA_ERR_INVALID_ARG, "kv_dtype must be dtype, MLA_FP8_E4M3 or MLA_FP8_E5M2; got %d",
+                (int)kv_dtype);
+  if (fp8 && !kv_scale) return fail(MLA_ERR_INVALID_ARG, "fp8 keys and values require kv_scale");
+  if (!fp8 && kv_scale)
+    return fail(MLA_ERR_INVALID_ARG, "16-bit keys and values do not use kv_scale");
+  if (!(softmax_scale > -3.0e38f) || !(softmax_scale < 3.0e38f))
+    return fail(MLA_ERR_INVALID_ARG, "softmax_scale must be finite");
+  const int ce = elt_size(kv_dtype);
+  if (!a16(q_nope) || !m16(qn_token_stride * 2) || !m16(qn_head_stride * 2))
+    return fail(MLA_ERR_MISALIGNED, "q_nope rows must start on 16-byte boundaries");
+  if (!a16(q_pe) || !m16(qpe_token_stride * 2) || !m16(qpe_head_stride * 2))
+    return fail(MLA_ERR_MISALIGNED, "q_pe rows must start on 16-byte boundaries");
+  if (!a16(k_nope) || !m16(kn_token_stride * ce) || !m16(kn_head_stride * ce))
+    return fail(MLA_ERR_MISALIGNED, "k_nope rows must start on 16-byte boundaries");
+  if (!a16(k_pe) || !m16(kpe_token_stride * ce) || !m16(kpe_head_stride * ce))
+    return fail(MLA_ERR_MISALIGNED, "k_pe rows must start on 16-byte boundaries");
+  if (!a16(v) || !m16(v_token_stride * ce) || !m16(v_head_stride * ce))
+    return fail(MLA_ERR_MISALIGNED, "v rows must start on 16-byte boundaries");
+  if (!a16(out) || !m16(out_token_stride * 2) || !m16(out_head_stride * 2))
+    return fail(MLA_ERR_MISALIGNED, "out rows must start on 16-byte boundaries");
+  // rows of keys and values are read in boxes of a tensor map
+  const int64_t most = int64_t(1) << 39;
+  const int64_t kv_strides[] = {kn_token_stride, kpe_token_stride, v_token_stride};
+  const int64_t kv_heads[] = {kn_head_stride, kpe_head_stride, v_head_stride};
+  for (int i = 0; i < 3; ++i) {
+    if (num_kv_tokens > 1 && (kv_strides[i] <= 0 || kv_strides[i] > most))
+      return fail(MLA_ERR_UNSUPPORTED, "token strides of k_nope, k_pe and v must be positive, below 2^39");
+    if (num_kv_heads > 1 && (kv_heads[i] < 0 || kv_heads[i] > most))
+      return fail(MLA_ERR_UNSUPPORTED, "head strides of k_nope, k_pe and v must lie in [0, 2^39]");
+  }
+  if (!a16(workspace)) return fail(MLA_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(kv_scale) |
+       reinterpret_cast<uintptr_t>(err_word) | reinterpret_cast<uintptr_t>(cu_q_lens) |
+       reinterpret_cast<uintptr_t>(cu_kv_lens)) & 3)
+    return fail(MLA_ERR_MISALIGNED,
+                "cu_q_lens, cu_kv_lens, lse, kv_scale and err_word must be 4-byte aligned");
+  if (num_tokens == 0) return MLA_OK;  // empty inputs may have null data pointers
+  if (!q_nope || !q_pe || !cu_q_lens || !cu_kv_lens || !out || !workspace)
+    return fail(MLA_ERR_INVALID_ARG,
+                "q_nope, q_pe, cu_q_lens, cu_kv_lens, out and workspace must be non-null");
+  if (num_kv_tokens > 0 && (!k_nope || !k_pe || !v))
+    return fail(MLA_ERR_INVALID_ARG, "k_nope, k_pe and v must be non-null");
+  int sms = 0;
+  MLA_TRY(current_sms(&sms));
+  const int64_t need =
+      mla::prefill_attention_workspace(num_tokens, num_heads, num_kv_heads, num_seqs, sms);
+  if (workspace_bytes < need)
+    return fail(MLA_ERR_INVALID_ARG, "workspace_bytes must be >= %lld (got %lld)", (long long)need,
+                (long long)workspace_bytes);
+  MLA_TRY(check_device_ptr(q_nope, "q_nope"));
+  MLA_TRY(check_device_ptr(q_pe, "q_pe"));
+  if (num_kv_tokens > 0) {
+    MLA_TRY(check_device_ptr(k_nope, "k_nope"));
+    MLA_TRY(check_device_ptr(k_pe, "k_pe"));
+    MLA_TRY(check_device_ptr(v, "v"));
+  }
+  MLA_TRY(check_device_ptr(cu_q_lens, "cu_q_lens"));
+  MLA_TRY(check_device_ptr(cu_kv_lens, "cu_kv_lens"));
+  if (fp8) MLA_TRY(check_device_ptr(kv_scale, "kv_scale"));
+  MLA_TRY(check_device_ptr(out, "out"));
+  if (lse) MLA_TRY(check_device_ptr(lse, "lse"));
+  MLA_TRY(check_device_ptr(workspace, "workspace"));
+  if (err_word) MLA_TRY(check_device_ptr(err_word, "err_word"));
+
+  mla::PrefillArgs a{};
+  a.q_nope = static_cast<const uint8_t*>(q_nope);
+  a.qn_ts = qn_token_stride * 2;
+  a.qn_hs = qn_head_stride * 2;
+  a.q_pe = static_cast<const uint8_t*>(q_pe);
+  a.qp_ts = qpe_token_stride * 2;
+  a.qp_hs = qpe_head_stride * 2;
+  a.num_tokens = num_tokens;
+  a.num_heads = num_heads;
+  a.k_nope = static_cast<const uint8_t*>(k_nope);
+  a.kn_ts = kn_token_stride * ce;
+  a.kn_hs = kn_head_stride * ce;
+  a.k_pe = static_cast<const uint8_t*>(k_pe);
+  a.kp_ts = kpe_token_stride * ce;
+  a.kp_hs = kpe_head_stride * ce;
+  a.v = static_cast<const uint8_t*>(v);
+  a.v_ts = v_token_stride * ce;
+  a.v_hs = v_head_stride * ce;
+  a.num_kv = num_kv_tokens;
+  a.kv_heads = num_kv_heads;
+  a.group = num_heads / num_kv_heads;
+  a.cu_q = cu_q_lens;
+  a.cu_kv = cu_kv_lens;
+  a.num_seqs = num_seqs;
+  a.softmax_scale = softmax_scale;
+  a.kv_scale = kv_scale;
+  a.causal = causal != 0;
+  a.out = static_cast<uint8_t*>(out);
+  a.out_ts = out_token_stride * 2;
+  a.out_hs = out_head_stride * 2;
+  a.lse = lse;
+  a.lse_ts = lse_token_stride;
+  a.lse_hs = lse_head_stride;
+  a.workspace = static_cast<uint8_t*>(workspace);
+  a.err = err_word;
+  a.wait_limit_ns = g_attention_wait_ns.load();
+  a.stall_stage = g_attention_stall.load();
+  return launched(mla::launch_prefill_attention(a, (int)dtype, (int)kv_dtype, sms, cfg_for(stream)),
+                  "mla_prefill_attention");
 }
 
 }  // extern "C"

@@ -80,6 +80,67 @@ struct LatentAttnArgs {
   float softmax_scale;
   const float* k_scale;  // fp8 caches only
   bool causal;
+  const uint32_t* tree;  // trees only: ancestor bits, tree_words words a token
+  int64_t tree_ts;       // words
+  uint32_t tree_words;   // at most kMaxTree / 32
+  uint8_t* out;
+  int64_t out_ts, out_hs;
+  float* lse;  // may be null
+  int64_t lse_ts, lse_hs;
+  uint8_t* workspace;
+  uint32_t* err;
+  uint64_t wait_limit_ns;
+  int32_t stall_stage;  // testing: this pipeline stage (from 1) of CTA 0 never fills
+};
+
+// Drafted tokens that a tree's masks can name.
+constexpr int kMaxTree = 32768;
+
+// Accepted rows moved to the front of the drafted ones (bytes; a row = the moved part of an
+// entry).
+struct CompactArgs {
+  const int64_t* cache_ptrs;
+  int32_t num_layers;
+  int64_t num_blocks, block_stride, entry_stride;
+  int32_t block_size;
+  Divider by_block;
+  int32_t row_chunks;  // 16-byte chunks of a row
+  const int32_t* block_table;
+  int64_t bt_stride;  // elements
+  int32_t room;       // rows that a table row can hold (below 2^31)
+  const int32_t* starts;
+  const int32_t* rows;
+  int64_t rows_stride;  // elements
+  int32_t width;        // of a list in rows
+  const int32_t* counts;
+  int32_t num_seqs;
+  uint32_t* err;
+};
+// The longest list of accepted rows.
+constexpr int kMaxAccepted = 1024;
+
+// Attention of packed sequences over keys and values per head (bytes; lse strides in
+// elements).
+struct PrefillArgs {
+  const uint8_t* q_nope;
+  int64_t qn_ts, qn_hs;
+  const uint8_t* q_pe;
+  int64_t qp_ts, qp_hs;
+  int32_t num_tokens, num_heads;
+  const uint8_t* k_nope;
+  int64_t kn_ts, kn_hs;
+  const uint8_t* k_pe;
+  int64_t kp_ts, kp_hs;  // kp_hs 0: one rotary row for all heads
+  const uint8_t* v;
+  int64_t v_ts, v_hs;
+  int32_t num_kv, kv_heads;
+  int32_t group;  // query heads of a key head
+  const int32_t* cu_q;
+  const int32_t* cu_kv;
+  int32_t num_seqs;
+  float softmax_scale;
+  const float* kv_scale;  // fp8 keys and values only
+  bool causal;
   uint8_t* out;
   int64_t out_ts, out_hs;
   float* lse;  // may be null
@@ -109,6 +170,14 @@ cudaError_t launch_copy_blocks(const CopyBlocksArgs& a, const LaunchCfg& cfg);
 cudaError_t launch_merge(const MergeArgs& a, int fmt, const LaunchCfg& cfg);
 cudaError_t launch_latent_attention(const LatentAttnArgs& a, int cache_fmt, int num_sms,
                                     const LaunchCfg& cfg);
+cudaError_t launch_latent_tree_attention(const LatentAttnArgs& a, int cache_fmt, int num_sms,
+                                         const LaunchCfg& cfg);
+cudaError_t launch_compact_rows(const CompactArgs& a, const LaunchCfg& cfg);
+// fmt: of the queries and the output (kBF16 or kF16); kv_fmt: of keys and values.
+cudaError_t launch_prefill_attention(const PrefillArgs& a, int fmt, int kv_fmt, int num_sms,
+                                     const LaunchCfg& cfg);
+int64_t prefill_attention_workspace(int32_t num_tokens, int32_t num_heads, int32_t kv_heads,
+                                    int32_t num_seqs, int num_sms);
 // Bytes of workspace of such a call on a device of num_sms SMs.
 int64_t latent_attention_workspace(int32_t num_tokens, int32_t num_heads, int32_t num_seqs,
                                    int num_sms);

@@ -105,6 +105,19 @@ SIGNATURES = {
         _vp, _i64, _i64, _vp, _i64, _i64, _i32, _i32, _i32, _i32, _vp, ctypes.c_int, _i64, _i32,
         _i64, _i64, _vp, _i64, _vp, _vp, _i32, ctypes.c_float, _vp, _i32, _vp, _i64, _i64, _vp,
         _i64, _i64, _vp, _i64, _vp, _vp]),
+    "mla_latent_tree_attention": (ctypes.c_int, [
+        _vp, _i64, _i64, _vp, _i64, _i64, _i32, _i32, _i32, _i32, _vp, ctypes.c_int, _i64, _i32,
+        _i64, _i64, _vp, _i64, _vp, _vp, _i32, ctypes.c_float, _vp, _vp, _i64, _i32, _vp, _i64,
+        _i64, _vp, _i64, _i64, _vp, _i64, _vp, _vp]),
+    "mla_cache_compact_rows": (ctypes.c_int, [
+        _vp, _i32, ctypes.c_int, _i64, _i32, _i64, _i64, _i32, _vp, _i64, _vp, _vp, _i64, _i32, _vp,
+        _i32, _vp, _vp]),
+    "mla_prefill_attention": (ctypes.c_int, [
+        _vp, _i64, _i64, _vp, _i64, _i64, ctypes.c_int, _i32, _i32, _vp, _i64, _i64, _vp, _i64, _i64,
+        _vp, _i64, _i64, ctypes.c_int, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _i32, ctypes.c_float,
+        _vp, _i32, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _vp]),
+    "mla_prefill_attention_workspace": (ctypes.c_int, [_i32, _i32, _i32, _i32,
+                                                       ctypes.POINTER(_i64)]),
     "mla_latent_attention_workspace": (ctypes.c_int, [_i32, _i32, _i32, ctypes.POINTER(_i64)]),
     "mla_merge_attn_states": (ctypes.c_int, [
         _vp, _i64, _i64, _i64, _vp, _i64, _i64, _i64, ctypes.c_int, _i32, _i32, _i32, _i32, _vp,
@@ -410,16 +423,8 @@ def mla_latent_attention_workspace(num_tokens: int, num_heads: int, num_seqs: in
     return n.value
 
 
-def mla_latent_attention(q_c, q_pe, kv_cache, cache_dtype, num_blocks, block_size, block_stride,
-                         entry_stride, block_table, cu_q_lens, kv_lens, out, workspace, *,
-                         softmax_scale, k_scale=None, causal=True, lse=None, err_word=None,
-                         stream=None):
-    """Attention of new tokens over the paged latent cache (absorbed form):
-    q_c [T, H, 512] and q_pe [T, H, 64] bf16 views (any strides, unit last
-    stride), out bf16 [T, H, 512] likewise, lse fp32 [T, H] or None; block_table
-    int32 [S, W] (a slice of a wider table is as wide as its row stride),
-    cu_q_lens int32 [S + 1], kv_lens int32 [S]; k_scale fp32;
-    workspace: a uint8 tensor of ``mla_latent_attention_workspace`` bytes."""
+def _latent_args(q_c, q_pe, kv_lens, cu_q_lens, block_table, k_scale, out, lse, workspace):
+    """Checks what both attentions over the latent cache take; strides and sizes of it."""
     T, H, R = q_c.shape
     qc_t, qc_h, qc_e = q_c.stride()
     qp_t, qp_h, qp_e = q_pe.stride()
@@ -454,13 +459,143 @@ def mla_latent_attention(q_c, q_pe, kv_cache, cache_dtype, num_blocks, block_siz
         _refuse("k_scale", k_scale, "an fp32 scalar")
     if not workspace.is_contiguous():
         _refuse("workspace", workspace, "contiguous")
+    return (T, H, R, P, S, qc_t, qc_h, qp_t, qp_h, out_t, out_h, lse_t, lse_h,
+            tab_s if tab_S > 1 else tab_W)
+
+
+def mla_latent_attention(q_c, q_pe, kv_cache, cache_dtype, num_blocks, block_size, block_stride,
+                         entry_stride, block_table, cu_q_lens, kv_lens, out, workspace, *,
+                         softmax_scale, k_scale=None, causal=True, lse=None, err_word=None,
+                         stream=None):
+    """Attention of new tokens over the paged latent cache (absorbed form):
+    q_c [T, H, 512] and q_pe [T, H, 64] bf16 views (any strides, unit last
+    stride), out bf16 [T, H, 512] likewise, lse fp32 [T, H] or None; block_table
+    int32 [S, W] (a slice of a wider table is as wide as its row stride),
+    cu_q_lens int32 [S + 1], kv_lens int32 [S]; k_scale fp32;
+    workspace: a uint8 tensor of ``mla_latent_attention_workspace`` bytes."""
+    T, H, R, P, S, qc_t, qc_h, qp_t, qp_h, out_t, out_h, lse_t, lse_h, width = _latent_args(
+        q_c, q_pe, kv_lens, cu_q_lens, block_table, k_scale, out, lse, workspace)
     status = lib().mla_latent_attention(
         q_c.data_ptr(), qc_t, qc_h, q_pe.data_ptr(), qp_t, qp_h, T, H, R, P,
         kv_cache.data_ptr(), dtype_code(cache_dtype), num_blocks, block_size, block_stride,
-        entry_stride, block_table.data_ptr(), tab_s if tab_S > 1 else tab_W, cu_q_lens.data_ptr(),
+        entry_stride, block_table.data_ptr(), width, cu_q_lens.data_ptr(),
         kv_lens.data_ptr(), S, softmax_scale, _ptr(k_scale), 1 if causal else 0,
         out.data_ptr(), out_t, out_h, _ptr(lse), lse_t, lse_h, workspace.data_ptr(),
         workspace.nbytes, _ptr(err_word), _stream(stream))
+    if status:
+        _check(status)
+
+
+def mla_latent_tree_attention(q_c, q_pe, kv_cache, cache_dtype, num_blocks, block_size,
+                              block_stride, entry_stride, block_table, cu_q_lens, kv_lens,
+                              tree_mask, out, workspace, *, softmax_scale, k_scale=None, lse=None,
+                              err_word=None, stream=None):
+    """``mla_latent_attention`` for trees of drafted tokens: tree_mask int32 [T, W] (any row
+    stride, unit last stride); bit i % 32 of word i // 32 says that the token sees the row of
+    its sequence's new token i.  The context before the new tokens is seen by all."""
+    T, H, R, P, S, qc_t, qc_h, qp_t, qp_h, out_t, out_h, lse_t, lse_h, width = _latent_args(
+        q_c, q_pe, kv_lens, cu_q_lens, block_table, k_scale, out, lse, workspace)
+    if tree_mask.dtype is not torch.int32 or tree_mask.ndim != 2 or tree_mask.shape[0] != T or \
+            (tree_mask.shape[1] > 1 and tree_mask.stride(1) != 1):
+        _refuse("tree_mask", tree_mask, f"int32 [{T}, W] with a unit last stride")
+    status = lib().mla_latent_tree_attention(
+        q_c.data_ptr(), qc_t, qc_h, q_pe.data_ptr(), qp_t, qp_h, T, H, R, P,
+        kv_cache.data_ptr(), dtype_code(cache_dtype), num_blocks, block_size, block_stride,
+        entry_stride, block_table.data_ptr(), width, cu_q_lens.data_ptr(),
+        kv_lens.data_ptr(), S, softmax_scale, _ptr(k_scale), tree_mask.data_ptr(),
+        tree_mask.stride(0), tree_mask.shape[1], out.data_ptr(), out_t, out_h, _ptr(lse), lse_t,
+        lse_h, workspace.data_ptr(), workspace.nbytes, _ptr(err_word), _stream(stream))
+    if status:
+        _check(status)
+
+
+def mla_cache_compact_rows(kv_cache_ptrs, cache_dtype, num_blocks, block_size, block_stride,
+                           entry_stride, entry_dim, block_table, starts, rows, counts, *,
+                           err_word=None, stream=None):
+    """Move accepted rows to the front of the drafted ones in every layer's cache: row
+    ``starts[s] + i`` becomes row ``starts[s] + rows[s, i]`` for i < counts[s]; kv_cache_ptrs
+    int64 [L], block_table int32 [S, W], starts / counts int32 [S], rows int32 [S, N] (each
+    list strictly increasing)."""
+    L, S = kv_cache_ptrs.numel(), starts.numel()
+    if not _is_list(kv_cache_ptrs, torch.int64, L):
+        _refuse("kv_cache_ptrs", kv_cache_ptrs, "contiguous int64")
+    if not _is_list(starts, torch.int32, S):
+        _refuse("starts", starts, "contiguous int32")
+    if not _is_list(counts, torch.int32, S):
+        _refuse("counts", counts, f"contiguous int32 [{S}]")
+    for name, t in (("block_table", block_table), ("rows", rows)):
+        if t.dtype is not torch.int32 or t.ndim != 2 or t.shape[0] < S or \
+                (t.shape[1] > 1 and t.stride(1) != 1):
+            _refuse(name, t, f"int32 [{S}, .] with a unit last stride")
+    _check(lib().mla_cache_compact_rows(
+        kv_cache_ptrs.data_ptr(), L, dtype_code(cache_dtype), num_blocks, block_size, block_stride,
+        entry_stride, entry_dim, block_table.data_ptr(), _bt_stride(block_table),
+        starts.data_ptr(), rows.data_ptr(), rows.stride(0), rows.shape[1], counts.data_ptr(), S,
+        _ptr(err_word), _stream(stream)))
+
+
+def mla_prefill_attention_workspace(num_tokens: int, num_heads: int, num_kv_heads: int,
+                                    num_seqs: int) -> int:
+    """Bytes of workspace of ``mla_prefill_attention`` on the current device."""
+    n = _i64(0)
+    _check(lib().mla_prefill_attention_workspace(num_tokens, num_heads, num_kv_heads, num_seqs,
+                                                 ctypes.byref(n)))
+    return n.value
+
+
+def mla_prefill_attention(q_nope, q_pe, k_nope, k_pe, v, cu_q_lens, cu_kv_lens, out, workspace, *,
+                          softmax_scale, causal=True, kv_scale=None, lse=None, err_word=None,
+                          stream=None):
+    """Attention of packed sequences over keys and values per head: q_nope [T, H, 128] and
+    q_pe [T, H, 64] (bf16 or fp16), k_nope [K, G, 128], k_pe [K, G, 64] or [K, 64] (shared by
+    all heads) and v [K, G, 128] (q's type, or fp8 with ``kv_scale`` an fp32 scalar), out
+    [T, H, 128] of q's type, lse fp32 [T, H] or None; any strides with a unit last one;
+    cu_q_lens and cu_kv_lens int32 [S + 1]; workspace: a uint8 tensor of
+    ``mla_prefill_attention_workspace`` bytes."""
+    T, H, N = q_nope.shape
+    K, G, _ = k_nope.shape
+    qd, kd = q_nope.dtype, k_nope.dtype
+    P = q_pe.shape[-1]
+    if q_pe.dtype is not qd or out.dtype is not qd:
+        raise ValueError(f"q_pe and out must have q_nope's dtype ({qd}, got {q_pe.dtype}, {out.dtype})")
+    if k_pe.dtype is not kd or v.dtype is not kd:
+        raise ValueError(f"k_pe and v must have k_nope's dtype ({kd}, got {k_pe.dtype}, {v.dtype})")
+    if q_pe.ndim != 3 or q_pe.shape[0] != T or q_pe.shape[1] != H:
+        _refuse("q_pe", q_pe, f"[{T}, {H}, 64]")
+    if k_pe.shape != ((K, P) if k_pe.ndim == 2 else (K, G, P)):
+        _refuse("k_pe", k_pe, f"[{K}, {P}] or [{K}, {G}, {P}]")
+    if k_nope.shape[2] != N:
+        _refuse("k_nope", k_nope, f"[{K}, {G}, {N}]")
+    if v.ndim != 3 or v.shape[0] != K or v.shape[1] != G:
+        _refuse("v", v, f"[{K}, {G}, 128]")
+    V = v.shape[2]
+    if out.shape != (T, H, V):
+        _refuse("out", out, f"[{T}, {H}, {V}]")
+    for t in (q_nope, q_pe, k_nope, k_pe, v, out):
+        if t.stride(-1) != 1:
+            raise ValueError("q_nope, q_pe, k_nope, k_pe, v and out must have a unit last stride")
+    lse_t = lse_h = 0
+    if lse is not None:
+        if lse.dtype is not torch.float32 or lse.shape != (T, H):
+            _refuse("lse", lse, f"fp32 [{T}, {H}]")
+        lse_t, lse_h = lse.stride()
+    S = cu_q_lens.numel() - 1
+    if not _is_list(cu_q_lens, torch.int32, 2):
+        _refuse("cu_q_lens", cu_q_lens, "contiguous int32 [S + 1]")
+    if not _is_list(cu_kv_lens, torch.int32, S + 1):
+        _refuse("cu_kv_lens", cu_kv_lens, f"contiguous int32 [{S + 1}]")
+    if kv_scale is not None and (kv_scale.dtype is not torch.float32 or kv_scale.numel() < 1):
+        _refuse("kv_scale", kv_scale, "an fp32 scalar")
+    if not workspace.is_contiguous():
+        _refuse("workspace", workspace, "contiguous")
+    status = lib().mla_prefill_attention(
+        q_nope.data_ptr(), q_nope.stride(0), q_nope.stride(1), q_pe.data_ptr(), q_pe.stride(0),
+        q_pe.stride(1), dtype_code(qd), T, H, k_nope.data_ptr(), k_nope.stride(0),
+        k_nope.stride(1), k_pe.data_ptr(), k_pe.stride(0), k_pe.stride(1) if k_pe.ndim == 3 else 0,
+        v.data_ptr(), v.stride(0), v.stride(1), dtype_code(kd), K, G, N, P, V,
+        cu_q_lens.data_ptr(), cu_kv_lens.data_ptr(), S, softmax_scale, _ptr(kv_scale),
+        1 if causal else 0, out.data_ptr(), out.stride(0), out.stride(1), _ptr(lse), lse_t, lse_h,
+        workspace.data_ptr(), workspace.nbytes, _ptr(err_word), _stream(stream))
     if status:
         _check(status)
 

@@ -1,0 +1,360 @@
+"""GPU parity of mla_prefill_attention with its definition in 64 bits, within the bounds derived
+in refprefill.bounds: types, head layouts, lengths from no row to several tiles and cuts, masks,
+strides, and what surrounds the data (NaN rows behind a sequence and in rows that a token does
+not see, unowned tokens, rows that do not exist); streams, graphs and repeated calls give the
+same bits."""
+import numpy as np
+import pytest
+import torch
+
+import refprefill as R
+from pack_mla_cache_gb300 import ops
+
+pytestmark = pytest.mark.gpu
+BF, HF, E4, E5 = torch.bfloat16, torch.float16, torch.float8_e4m3fn, torch.float8_e5m2
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from pack_mla_cache_gb300 import build
+    build.build()
+    ops.lib()
+
+
+def cu_of(lens):
+    return [0] + [int(x) for x in np.cumsum(lens)]
+
+
+class Call:
+    """One call's inputs (on the CPU, changeable before `put`) and device buffers; out and lse
+    start as canaries, the workspace as NaN words."""
+
+    def __init__(self, q_lens, kv_lens, heads=2, kv_heads=None, dtype=BF, kv=None, *, causal=True,
+                 scale=R.SCALE, seed=0, q_mul=1.5, spare_q=0, spare_kv=0, layout="packed"):
+        kv_heads = kv_heads or heads
+        self.dtype, self.kv, self.causal, self.scale, self.layout = dtype, kv or dtype, causal, scale, layout
+        self.cu_q, self.cu_kv = cu_of(q_lens), cu_of(kv_lens)
+        T, K = self.cu_q[-1] + spare_q, self.cu_kv[-1] + spare_kv
+        self.q = R.values((T, heads, 192), dtype, seed, q_mul)
+        self.key = R.values((K, kv_heads, 192), self.kv, seed + 1, 1.0 if self.kv not in R.FP8 else 30.0)
+        if layout == "shared":
+            self.key.view(torch.uint8)[:, :, -64 * self.key.element_size():] = \
+                self.key.view(torch.uint8)[:, :1, -64 * self.key.element_size():].clone()
+        self.v = R.values((K, kv_heads, 128), self.kv, seed + 2, 1.0 if self.kv not in R.FP8 else 30.0)
+        self.kv_scale = 0.03 if self.kv in R.FP8 else None
+
+    def put(self):
+        T, H, _ = self.q.shape
+        K, G, _ = self.key.shape
+        raw = lambda t: t.view(torch.uint8)
+        es = self.key.element_size()
+        self.dq = self.q.cuda()
+        if self.layout == "packed":
+            key = self.key.cuda()
+            self.dk, self.dp, self.dv = key[:, :, :128], key[:, :, 128:], self.v.cuda()
+        else:  # kv_b_proj's output with padding behind a row, rotary rows apart
+            both = torch.full((K, G, 272 * es), 0xFF, dtype=torch.uint8)
+            both[:, :, :128 * es] = raw(self.key[:, :, :128].contiguous())
+            both[:, :, 128 * es:256 * es] = raw(self.v)
+            both = both.cuda().view(self.kv)
+            self.dk, self.dv = both[:, :, :128], both[:, :, 128:256]
+            pe = self.key[:, :, 128:].contiguous()
+            self.dp = pe[:, 0].contiguous().cuda() if self.layout == "shared" else pe.cuda()
+        self.out_full = torch.full((T + 1, H, 136), 7.0, dtype=self.dtype, device="cuda")
+        self.out = self.out_full[:T, :, :128]
+        self.lse_full = torch.full((H, T + 1), 7.0, device="cuda")
+        self.lse = self.lse_full.t()[:T]
+        self.err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+        self.dcq, self.dck = i32(self.cu_q), i32(self.cu_kv)
+        self.ds = None if self.kv_scale is None else torch.tensor([self.kv_scale], device="cuda")
+        n = ops.mla_prefill_attention_workspace(max(T, 1), H, G, len(self.cu_q) - 1)
+        self.ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+        return self
+
+    def run(self, **kw):
+        a = dict(softmax_scale=self.scale, causal=self.causal, kv_scale=self.ds, lse=self.lse,
+                 err_word=self.err)
+        ops.mla_prefill_attention(self.dq[:, :, :128], self.dq[:, :, 128:], self.dk, self.dp, self.dv,
+                                  self.dcq, self.dck, self.out, self.ws, **{**a, **kw})
+        return self
+
+    def got(self):
+        torch.cuda.synchronize()
+        return R.f64(self.out.cpu()), R.f64(self.lse.cpu()), int(self.err.item())
+
+    def expected(self, limit=None):
+        ks = 1.0 if self.kv_scale is None else float(np.float32(self.kv_scale))
+        key, v = R.f64(self.key) * ks, R.f64(self.v) * ks
+        return R.attend(R.f64(self.q), key, v, self.cu_q, self.cu_kv, self.scale, self.causal, limit)
+
+    def check(self, err=0, limit=None):
+        out, lse, e = self.got()
+        r = self.expected(limit)
+        own = ~np.isnan(r.lse)
+        assert (out[~own] == 7).all() and (lse[~own] == 7).all()
+        none = np.isneginf(r.lse)
+        assert (out[none] == 0).all() and np.isneginf(lse[none]).all()
+        live = own & ~none
+        assert np.isfinite(out[live]).all() and np.isfinite(lse[live]).all()
+        bo, bl = R.bounds(r, self.dtype, self.kv)
+        if live.any():
+            worst = (np.abs(out - r.out)[live] / bo[live]).max()
+            worst_l = (np.abs(lse - r.lse)[live] / bl[live]).max()
+            assert worst <= 1 and worst_l <= 1, (worst, worst_l)
+        full = R.f64(self.out_full.cpu())
+        assert (full[-1] == 7).all() and (full[:, :, 128:] == 7).all()
+        assert (R.f64(self.lse_full.cpu())[:, -1] == 7).all()
+        assert e == err
+
+
+KINDS = [(BF, BF), (HF, HF), (BF, E4), (BF, E5), (HF, E4), (HF, E5)]
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=["bf16", "fp16", "bf16-e4m3", "bf16-e5m2", "fp16-e4m3", "fp16-e5m2"])
+@pytest.mark.parametrize("lens", [
+    ([1], [1]), ([1], [129]), ([5], [0]), ([0, 3, 0], [4, 3, 0]), ([128], [128]), ([127, 129], [127, 129]),
+    ([300], [300]), ([1, 2, 1, 1], [77, 256, 1, 900]), ([40, 257], [168, 700]), ([20, 130], [7, 60]),
+], ids=str)
+def test_types_and_lengths(kind, lens):
+    """Causal, among them more tokens than rows (the first ones see nothing)."""
+    Call(*lens, heads=2, dtype=kind[0], kv=kind[1]).put().run().check()
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=str)
+@pytest.mark.parametrize("lens", [([1], [1]), ([70], [0]), ([3, 200], [260, 513]), ([129, 1], [127, 1025])], ids=str)
+def test_context_without_mask(kind, lens):
+    Call(*lens, heads=2, dtype=kind[0], kv=kind[1], causal=False).put().run().check()
+
+
+@pytest.mark.parametrize("heads,kv_heads", [(1, 1), (3, 1), (6, 2), (8, 8), (16, 2), (5, 1), (40, 1), (130, 1), (200, 2)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_head_layouts(heads, kv_heads, causal):
+    Call([33, 1, 60], [33, 200, 170], heads, kv_heads, causal=causal).put().run().check()
+
+
+@pytest.mark.parametrize("kind", [(BF, BF), (HF, HF), (BF, E4)], ids=str)
+@pytest.mark.parametrize("layout", ["packed", "apart", "shared"])
+def test_layouts(kind, layout):
+    """The pack's key, and the kv_b_proj output with NaN behind its rows and k_pe apart."""
+    Call([150, 9], [280, 9], 4, 2, kind[0], kind[1], layout=layout).put().run().check()
+
+
+@pytest.mark.parametrize("kind", [(BF, BF), (HF, HF), (BF, E5)], ids=str)
+def test_many_cuts(kind):
+    """One sequence and head cut over many blocks, and a batch of very different lengths."""
+    Call([1], [9000], 1, dtype=kind[0], kv=kind[1]).put().run().check()
+    Call([130], [4000], 1, dtype=kind[0], kv=kind[1]).put().run().check()
+    Call([1, 200, 3, 1, 64], [5000, 300, 3, 1, 1000], 2, dtype=kind[0], kv=kind[1]).put().run().check()
+
+
+@pytest.mark.parametrize("seed", range(30))
+def test_random_batches(seed):
+    rng = np.random.default_rng(seed)
+    n = int(rng.integers(1, 9))
+    kv_heads = int(rng.choice([1, 1, 2, 3]))
+    heads = kv_heads * int(rng.choice([1, 1, 2, 3, 7]))
+    most = max(2, 2000 // heads // n)
+    ql = [int(rng.choice([0, 1, 1, 2, 63, 64, 65, int(rng.integers(1, most + 1))])) for _ in range(n)]
+    ql[0] = max(1, ql[0])
+    ctx = [int(rng.choice([0, 1, 63, 64, 127, 128, int(rng.integers(0, 1200))])) for _ in range(n)]
+    causal = bool(rng.integers(0, 2))
+    kind = KINDS[int(rng.integers(0, len(KINDS)))]
+    c = Call(ql, [x + (q if causal else 0) for q, x in zip(ql, ctx)], heads, kv_heads, *kind, causal=causal,
+             seed=seed, q_mul=float(rng.choice([0.3, 1.5, 8.0])), spare_q=int(rng.integers(0, 3)),
+             spare_kv=int(rng.integers(0, 3)), layout=str(rng.choice(["packed", "apart", "shared"])),
+             scale=float(rng.choice([R.SCALE, -0.05, 0.2])))
+    c.put().run().check()
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=str)
+def test_query_magnitudes(kind):
+    """Rows of very different sizes, and rows whose elements are."""
+    c = Call([8], [200], 1, dtype=kind[0], kv=kind[1], causal=False)
+    q = c.q.float()
+    if kind[0] is BF:
+        q[0] *= 1e-30
+        q[1] *= 2.0 ** -100
+    q[2] *= 30
+    q[3, :, ::7] *= 100
+    q[4] *= torch.exp(torch.linspace(-12, 1, 192))
+    q[5] = 0
+    q[6] = 0
+    q[6, 0, 191] = 8
+    c.q = q.to(kind[0])
+    c.put().run().check()
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=str)
+def test_growing_scores_and_long_tails(kind):
+    """Scores that grow along the row (references move often), fall, and one large weight with a
+    long tail of equal small ones that hold a fifth of the mass."""
+    c = Call([2], [2000], 1, dtype=kind[0], kv=kind[1], causal=False, scale=1.0)
+    ks = c.kv_scale or 1.0
+    q, key = torch.zeros(2, 1, 192), torch.zeros(2000, 1, 192)
+    q[0, 0, 0] = 1.0
+    q[1, 0, 1] = 1.0
+    key[:, 0, 0] = torch.linspace(-60, 60, 2000) / ks   # rises
+    key[:, 0, 1] = torch.linspace(40, -40, 2000) / ks   # falls
+    lim = 400.0 if kind[1] is E4 else 5e4
+    c.q, c.key = q.to(kind[0]), key.clamp(-lim, lim).to(kind[1])
+    c.put().run().check()
+    key[:, 0, 0] = 0
+    key[77, 0, 0] = float(np.log(4 * 1999)) / ks
+    c.key = key.clamp(-lim, lim).to(kind[1])
+    c.put().run().check()
+
+
+NAN_ROW = {BF: 0x7FC0, HF: 0x7E00}
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=str)
+@pytest.mark.parametrize("bad", ["nan", "inf"])
+def test_bad_rows_stay_unseen(kind, bad):
+    """Rows behind a sequence, and rows that come after a token, hold NaN or infinities: tokens
+    that do not see them keep their bits."""
+    lens = ([100, 200], [230, 200])
+    clean = Call(*lens, 2, dtype=kind[0], kv=kind[1], spare_kv=140).put().run().got()
+    c = Call(*lens, 2, dtype=kind[0], kv=kind[1], spare_kv=140)
+    if c.kv is E4 and bad == "inf":
+        pytest.skip("e4m3 has no infinity")
+    val = float("nan") if bad == "nan" else float("inf")
+    key, v = c.key.float(), c.v.float()
+    for x in (key, v):
+        x[430:] = val             # behind the last sequence
+        x[230 + 90] = val         # seen from the second sequence's token 90 on
+        x[230 + 199, :, 5] = val  # by its last token
+        x[229] = val              # by the first sequence's last token
+    c.key, c.v = (x.to(c.kv) if bad == "nan" else _with_inf(x, c.kv) for x in (key, v))
+    out, lse, e = c.put().run().got()
+    sees = np.zeros(300, bool)
+    sees[99] = True
+    sees[100 + 90:] = True
+    assert np.array_equal(out[~sees], clean[0][~sees]) and np.array_equal(lse[~sees], clean[1][~sees])
+    if bad == "nan":
+        assert np.isnan(out[99]).all()
+    assert e == 0
+
+
+def _with_inf(x, dtype):
+    y = x.clamp(-5e4, 5e4).to(dtype)
+    if dtype is E5:
+        y.view(torch.uint8)[torch.isinf(x)] = 0x7C
+    else:
+        y[torch.isinf(x)] = float("inf")
+    return y
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("kv", [BF, E4])
+def test_a_bad_query_row_stays_alone(bad, kv):
+    good = Call([200], [200], 2, kv=kv).put().run().got()
+    c = Call([200], [200], 2, kv=kv)
+    c.q[130, 1, 100] = bad
+    out, lse, _ = c.put().run().got()
+    rest = np.ones((200, 2), bool)
+    rest[130, 1] = False
+    assert np.isnan(out[130, 1]).all()
+    assert np.array_equal(out[rest], good[0][rest]) and np.array_equal(lse[rest], good[1][rest])
+
+
+def test_rows_that_do_not_exist():
+    """Key rows behind the arrays are left out and reported; tokens behind theirs are not touched."""
+    c = Call([10, 20], [100, 60], 2)
+    c.put()
+    K = 130
+    c.dk, c.dp, c.dv = c.dk[:K], c.dp[:K], c.dv[:K]
+    c.run().check(err=8 // 2, limit=K)
+    c = Call([10, 20], [100, 60], 2, spare_q=0)
+    c.put()
+    c.dq, c.out, c.lse = c.dq[:25], c.out[:25], c.lse[:25]
+    c.q = c.q[:25]
+    c.run()
+    torch.cuda.synchronize()
+    assert (c.out_full[25:, :, :128] == 7).all()
+    r = c.expected()
+    bo, bl = R.bounds(r, c.dtype, c.kv)
+    assert (np.abs(R.f64(c.out.cpu()) - r.out) <= bo).all()
+
+
+def test_unowned_tokens_and_empty_calls():
+    c = Call([3, 4], [5, 6], 2, spare_q=5, spare_kv=5)
+    c.cu_q = [2, 5, 9]
+    c.put().run().check()
+    c = Call([3, 4], [5, 6], 2)
+    c.put()
+    c.dq, c.out, c.lse = c.dq[:0], c.out[:0], c.lse[:0]
+    c.run()
+    torch.cuda.synchronize()
+    assert (c.out_full[:, :, :128] == 7).all()
+    c = Call([3, 4], [0, 0], 2)  # no key rows at all
+    c.put().run().check()
+
+
+def test_no_lse():
+    c = Call([30], [30], 2).put()
+    c.run(lse=None)
+    torch.cuda.synchronize()
+    assert (c.lse_full == 7).all()
+    out = R.f64(c.out.cpu())
+    assert np.array_equal(out, Call([30], [30], 2).put().run().got()[0])
+
+
+def test_many_sequences():
+    """More sequences than one block looks at in a round, most of them of a few tokens, some empty."""
+    rng = np.random.default_rng(3)
+    ql = [int(x) for x in rng.integers(0, 4, 700)]
+    kl = [q + int(x) for q, x in zip(ql, rng.integers(0, 40, 700))]
+    Call(ql, kl, 1).put().run().check()
+
+
+def test_broadcast_heads():
+    """All heads share one key and value row (head strides of 0)."""
+    c = Call([50], [90], 4, 4)
+    c.key = c.key[:, :1].expand(-1, 4, -1).contiguous()
+    c.v = c.v[:, :1].expand(-1, 4, -1).contiguous()
+    c.put()
+    c.dk, c.dp, c.dv = (t[:, :1].expand(-1, 4, -1) for t in (c.dk, c.dp, c.dv))
+    c.run().check()
+
+
+def test_calls_repeat_to_the_bit_on_streams_and_in_graphs():
+    c = Call([1, 140, 2], [3000, 300, 200], 4).put().run()
+    first = c.got()
+    for x in (c.out_full, c.lse_full):
+        x.fill_(3.0)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    c.run(stream=s)
+    s.synchronize()
+    again = c.got()
+    assert np.array_equal(first[0], again[0]) and np.array_equal(first[1], again[1])
+    c.out_full.fill_(3.0)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.run()
+        c.run()
+    for _ in range(3):
+        g.replay()
+    again = c.got()
+    assert np.array_equal(first[0], again[0]) and np.array_equal(first[1], again[1])
+
+
+def test_two_graphs_with_one_workspace():
+    """Calls of different shapes captured apart on one workspace, replayed in turn."""
+    a, b = Call([1], [4000], 2).put().run(), Call([90, 90], [700, 90], 2, seed=5).put().run()
+    wa, wb = a.got(), b.got()
+    ws = a.ws if a.ws.numel() >= b.ws.numel() else b.ws
+    a.ws = b.ws = ws
+    graphs = []
+    for c in (a, b):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.run()
+        graphs.append(g)
+    for g in graphs * 3:
+        g.replay()
+    for c, w in ((a, wa), (b, wb)):
+        o = c.got()
+        assert np.array_equal(o[0], w[0]) and np.array_equal(o[1], w[1])
