@@ -1320,6 +1320,7 @@ mla_status_t mla_prefill_attention(
   a.num_kv = num_kv_tokens;
   a.kv_heads = num_kv_heads;
   a.group = num_heads / num_kv_heads;
+  a.by_group = mla::Divider::by((uint32_t)a.group);
   a.cu_q = cu_q_lens;
   a.cu_kv = cu_kv_lens;
   a.num_seqs = num_seqs;

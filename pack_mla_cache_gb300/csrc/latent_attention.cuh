@@ -84,6 +84,7 @@
 #include "mla_device.cuh"
 #include "serving.h"
 #include "tensor_core.cuh"
+#include "tensor_map.h"
 
 namespace mla {
 namespace {
@@ -313,52 +314,6 @@ struct Walk {
   }
 };
 
-// Bounded waits.  The loops of the roles have to stay small (10 or 14 warps of
-// different code share the instruction caches; fetching was the largest stall), so all but
-// the first look at a barrier is out of line.
-__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, uint32_t abort, uint64_t limit) {
-  uint64_t since = 0;
-  for (uint32_t spin = 1; !mbar_try_wait(bar, parity); ++spin) {
-    if (spin & 31u) continue;
-    if (lds_u32(abort) != 0) return false;
-    const uint64_t now = global_ns();
-    if (since == 0) since = now;
-    if (now - since > limit) {
-      asm volatile("st.shared.u32 [%0], %1;" ::"r"(abort), "r"(1u) : "memory");
-      return false;
-    }
-  }
-  return true;
-}
-struct Waiter {
-  uint32_t abort;  // shared address of Misc::abort
-  uint64_t limit;
-  __device__ __forceinline__ bool given_up() const { return lds_u32(abort) != 0; }
-  // Whether the barrier's phase completed: false once the CTA has given up.
-  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
-    return mbar_try_wait(bar, parity) || wait_on(bar, parity, abort, limit);
-  }
-};
-
-__device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
-               "r"(v.z), "r"(v.w)
-               : "memory");
-}
-__device__ __forceinline__ void sts8(uint32_t addr, uint32_t x, uint32_t y) {
-  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
-}
-__device__ __forceinline__ void sts_u8(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-__device__ __forceinline__ void sts_u32(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
-  return v;
-}
 // A barrier of the four warps of one softmax group.
 __device__ __forceinline__ void soft_sync(int group) {
   asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
@@ -374,26 +329,6 @@ __device__ __forceinline__ bool soft_any(int group, bool x) {
       : "memory");
   return any != 0;
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Whether any of the 8 bf16 (16 fp8) values of v is a NaN or an infinity.
-template <int FMT>
-__device__ __forceinline__ bool any_special(uint4 v) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (FMT == kBF16) m |= (w[i] & 0x7FFF7FFFu) + 0x00800080u;  // exponent 255 carries
-    else if constexpr (FMT == kE4M3) m |= (w[i] & 0x7F7F7F7Fu) + 0x01010101u;
-    else m |= (w[i] & 0x7F7F7F7Fu) + 0x04040404u;
-  }
-  return (m & (FMT == kBF16 ? 0x80008000u : 0x80808080u)) != 0;
-}
-
 // The block of row p of sequence s: an id to be checked, or kUnseen when no row of
 // the query tile sees it.  The table's answer is not looked at here, so its load
 // runs on while the tile before is produced.
@@ -681,7 +616,7 @@ __device__ __forceinline__ void issue_scores(uint32_t smem, uint32_t tmem, bool 
       for (int k = 0; k < 4; ++k) {
         const uint64_t ak = ka + (c * kChunk >> 4) + 2 * k, bk = qa + (c * L::kN * 128 >> 4) + 2 * k;
         if constexpr (L::kF8) tc::mma_fp8(one, d, ak, bk, kId, c + k > 0);
-        else tc::mma_bf16(one, d, ak, bk, kId, c + k > 0);
+        else tc::mma_16bit(one, d, ak, bk, kId, c + k > 0);
       }
   };
   using std::integral_constant;
@@ -722,7 +657,7 @@ __device__ __forceinline__ void issue_outputs(uint32_t smem, uint32_t tmem, bool
         const uint32_t d = tmem + L::kO + b * L::kPN;
         const uint64_t ak = va + (b * kDims >> 4) + k * (kStep >> 4), bk = pa + 2 * k;
         if constexpr (L::kF8) tc::mma_fp8(one, d, ak, bk, kId, k > 0 || !first);
-        else tc::mma_bf16(one, d, ak, bk, kId, k > 0 || !first);
+        else tc::mma_16bit(one, d, ak, bk, kId, k > 0 || !first);
       }
     tc::commit(one, smem + L::bars + 8 * (L::kEmpty + st * L::kHalves + h));
   }
@@ -1507,16 +1442,7 @@ int box_map(const LatentAttnArgs& a, bool fp8, CUtensorMap* map) {
   int rows = kKeys;
   while (a.block_size % rows) rows >>= 1;
   if (rows < 8 || a.num_blocks >= INT32_MAX) return 0;
-  static const auto encode = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &found) != cudaSuccess ||
-        found != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    (void)cudaGetLastError();
-    return reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(f);
-  }();
+  const TensorMapEncode encode = tensor_map_encode();
   if (!encode) return 0;
   const cuuint64_t dims[3] = {576, (cuuint64_t)a.block_size, (cuuint64_t)a.num_blocks};
   const cuuint64_t strides[2] = {(cuuint64_t)a.entry_stride, (cuuint64_t)a.block_stride};

@@ -1,21 +1,989 @@
 // prefill_attention.cu -- attention of packed sequences over keys and values per head
-// (include/mla_cache.h: mla_prefill_attention).
+// (include/mla_cache.h: mla_prefill_attention), on the 5th generation tensor cores.
 //
 // What it computes, per (token, head) row q of 128 + 64 elements and the rows of its
 // sequence that the token sees: x_p = scale <q, k_p>, lse = ln sum exp(x_p), out = sum
 // exp(x_p - lse) v_p.
 //
-// A warp takes one (token, head): lanes hold 4 + 2 elements of q and 4 of the output, one
-// key after the other with a running maximum and sum.
+// Shape of the work.  The query rows of a sequence and key head (token-major, the key
+// head's query heads inside) are cut into items of 256 rows, two tiles of 128, its keys
+// into tiles of 128; one unit = (item, key tile).  The units of the whole call, in
+// (sequence, key head, item, key tile) order, are cut into equal contiguous runs, one per
+// CTA (one CTA per SM), so ragged and causal batches load every SM alike.  An item whose
+// units fall into several CTAs leaves unnormalised fp32 partial sums in the workspace, which
+// a second launch joins in the order of the CTAs (no atomics: equal calls give equal bits).
+//
+// A unit: S_i = Q_i K^T (two tiles of 128 x 128, k = 192), weights P_i = exp2(S_i - reference)
+// written over S_i in tensor memory as 16-bit values, O_i += P_i V (128 x 128).  Tensor memory
+// is full: two S and two O of 128 columns.  The two tiles alternate on the tensor core: while
+// one tile's weights are computed, the other tile's products run (1280 of 2560 cycles a unit
+// at 8192 multiply-adds... per tile).
+//
+// Shared memory: the two query tiles (96 KB), and a ring of 8 slots of 128 keys x 64 columns
+// (128 bytes a row, 128-byte swizzle) through which K (three slots a unit) and V (two) flow by
+// TMA, a whole unit ahead of their use.
+//
+// Roles (12 warps): 4 warps per query tile compute weights, a thread a row (running maximum,
+// rescaling O only when a maximum has grown by more than 2^kGrow) and write the output; one
+// issues the products; one loads K and V; two load the queries and look after V rows that not
+// every row of an item sees: those behind the sequence are zeroed (they may hold anything),
+// those with a NaN or an infinity too, and noted, so that the sums of the rows that see them
+// become NaN.
+//
+// Waits are bounded (wait_limit_ns): one that runs out marks the CTA as given up.  Every role
+// leaves at its next wait then, copies and products in flight are waited for (bounded again),
+// and MLA_ERRBIT_TIMEOUT is set.
+#include <atomic>
+
 #include "mla_device.cuh"
 #include "serving.h"
+#include "tensor_core.cuh"
+#include "tensor_map.h"
 
 namespace mla {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kSimpleThreads = 256;
+constexpr int kM = 128;              // query rows of a tile
+constexpr int kItemRows = 2 * kM;
+constexpr int kKeys = 128;           // keys of a tile
+constexpr int kV = 128;
+constexpr int kSlot = kKeys * 128;   // bytes of a ring slot
+constexpr int kSlots = 8;
+constexpr int kUnitSlots = 5;        // 3 of K, 2 of V
+constexpr int kQTile = 3 * kM * 128;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kAuxWarp = 10, kAuxWarps = 2;
+constexpr int kWarps = kAuxWarp + kAuxWarps, kThreads = kWarps * 32;
+constexpr int kMaxCtas = 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// What beginning another item costs a CTA, in units: the runs are cut as if each item had
+// this many more.
+constexpr int kSwitch = 1;
+constexpr int kMinUnits = 2;  // a CTA takes at least this many
+
+// The reference of a row's weights is the next whole number (log2) above its maximum less
+// kTop; a score may pass the reference by kGrow before the sums are rescaled.  fp16 weights:
+// up to 2^14, and 2^-25, half their smallest step, is 2^-34 of the row's largest or less.
+template <int F>
+struct Ref {
+  static constexpr float kTop = F == kF16 ? 10.0f : 0.0f;
+  static constexpr float kGrow = F == kF16 ? 14.0f : 8.0f;
+};
+
+// shared memory
+struct Lay {
+  static constexpr int q = 0;
+  static constexpr int ring = 2 * kQTile;
+  static constexpr int flags = ring + kSlots * kSlot;  // uint32 [4 units][4]: keys with bad V rows
+  static constexpr int bars = flags + 64;
+  static constexpr int kFull = 0, kEmpty = kSlots, kQFull = 2 * kSlots, kQEmpty = kQFull + 2,
+                       kSFull = kQEmpty + 2, kPFull = kSFull + 2, kPvDone = kPFull + 2,
+                       kOFree = kPvDone + 2, kClean = kOFree + 2, kBars = kClean + 2;
+  static constexpr int misc = (bars + kBars * 8 + 15) / 16 * 16;
+  static constexpr int bytes = misc + 64;
+  static_assert(bytes <= 232448, "shared memory of a CTA");
+  // tensor memory columns: S of both tiles (P in their first half), O of both tiles
+  static constexpr int kO = 2 * kKeys, kTmem = 512;
+};
+struct Misc {
+  uint32_t tmem;
+  uint32_t abort;
+};
+
+// How a tensor map reads row p, columns c.. of key head g: box (x_head * g + c, p, z_head * g).
+struct Maps {
+  CUtensorMap kn, kp, v;
+  int32_t kn_x, kn_z, kp_x, kp_z, v_x, v_z;
+};
+
+// What the join needs of a split item; written by each CTA whose run ends inside it.  rows 0:
+// none.
+struct Split {
+  int32_t tok0;        // the sequence's first computed token
+  uint32_t row0;       // of the item, among the sequence's rows of a key head
+  int32_t head;        // key head
+  int16_t rows, parts;
+  int32_t first, pad[3];
+};
+struct Workspace {
+  Split* split;  // [ctas]
+  float *m, *l;  // [2 ctas][slot_rows]: reference (log2) and sum of the weights
+  float* o;      // [2 ctas][slot_rows][128]
+};
+__host__ __device__ inline int slot_rows(int64_t num_tokens, int group) {
+  const int64_t rows = num_tokens * group;
+  return rows < kItemRows ? (int)((rows + 3) / 4 * 4) : kItemRows;
+}
+__host__ __device__ inline Workspace workspace_of(uint8_t* p, int ctas, int rows) {
+  Workspace w;
+  w.split = reinterpret_cast<Split*>(p);
+  w.m = reinterpret_cast<float*>(p + (int64_t)ctas * sizeof(Split));
+  w.l = w.m + (int64_t)ctas * 2 * rows;
+  w.o = w.l + (int64_t)ctas * 2 * rows;
+  return w;
+}
+
+struct Seq {
+  int32_t t0;      // first computed token
+  uint32_t rows;   // query rows of a key head
+  int32_t nb;      // items of a key head
+  int32_t k0, m;   // its key rows that exist
+  int64_t base;    // rows that token t0 sees (before clamping)
+};
+__device__ __forceinline__ Seq load_seq(const PrefillArgs& a, int s, uint32_t& errbits) {
+  Seq q;
+  const int32_t c0 = __ldg(a.cu_q + s), c1 = __ldg(a.cu_q + s + 1);
+  const int32_t k0 = __ldg(a.cu_kv + s), k1 = __ldg(a.cu_kv + s + 1);
+  q.t0 = max(c0, 0);
+  const int32_t ntok = max(min(c1, a.num_tokens) - q.t0, 0);
+  q.rows = (uint32_t)ntok * (uint32_t)a.group;
+  q.nb = (int)((q.rows + kItemRows - 1) / kItemRows);
+  q.k0 = k0;
+  const int64_t n = (int64_t)k1 - k0;
+  q.m = k0 < 0 ? 0 : (int)max((int64_t)0, min(n, (int64_t)a.num_kv - k0));
+  q.base = n + (a.causal ? (int64_t)q.t0 + 1 - c1 : 0);
+  if (ntok > 0 && n > q.m) errbits |= kErrPosOOB;
+  return q;
+}
+// Key rows that the token of a query row sees.
+__device__ __forceinline__ int seen_of(const PrefillArgs& a, const Seq& q, uint32_t row) {
+  const int64_t n = q.base + (a.causal ? (int64_t)a.by_group(row) : 0);
+  return (int)max((int64_t)0, min(n, (int64_t)q.m));
+}
+// Key tiles of rows of which the last sees `most` (one even when it sees none: they are still
+// written).
+__device__ __forceinline__ int key_tiles(int most) { return max(1, (most + kKeys - 1) / kKeys); }
+__device__ __forceinline__ int item_tiles(const PrefillArgs& a, const Seq& q, int b) {
+  return key_tiles(seen_of(a, q, min((uint32_t)(b + 1) * kItemRows, q.rows) - 1));
+}
+
+// A CTA's run of units: where it starts, and what finds the CTA of another unit.  An item is
+// kSwitch units that stand for beginning it, then its key tiles: a run starts before the
+// first of these when kt is negative.
+struct Run {
+  Seq q;
+  int s, head, b, kt, count;
+  int64_t begin, each;
+  int extra;
+};
+
+// Walks the run item by item; every role has its own copy.
+struct Walk {
+  Seq q;
+  int s, head, b, left;
+  bool more;
+  // the present item
+  int kb, ke;              // this CTA's key tiles of it
+  int nkt[2], tiles;       // key tiles of the query tiles (0: the tile has no rows), and of both
+  int least, most;         // rows seen by its first and last row
+  uint32_t row0;
+  int rows;
+  __device__ __forceinline__ void start(const Run& r) {
+    q = r.q;
+    s = r.s;
+    head = r.head;
+    b = r.b;
+    left = r.count + min(r.kt, 0);
+    kb = max(r.kt, 0);
+    more = false;
+  }
+  __device__ __forceinline__ bool next(const PrefillArgs& a) {
+    if (left <= 0) return false;
+    if (more) {
+      kb = 0;
+      if (++b >= q.nb) {
+        b = 0;
+        if (++head >= a.kv_heads) {
+          head = 0;
+          uint32_t ignored = 0;
+          do q = load_seq(a, ++s, ignored);
+          while (q.nb == 0 && s + 1 < a.num_seqs);
+        }
+      }
+      left -= kSwitch;
+      if (left <= 0) return false;
+    }
+    more = true;
+    row0 = (uint32_t)b * kItemRows;
+    rows = (int)min((uint32_t)kItemRows, q.rows - row0);
+    least = seen_of(a, q, row0);
+    most = seen_of(a, q, row0 + rows - 1);
+    tiles = key_tiles(most);
+    nkt[0] = rows > kM ? key_tiles(seen_of(a, q, row0 + kM - 1)) : tiles;
+    nkt[1] = rows > kM ? tiles : 0;
+    ke = min(tiles, kb + left);
+    left -= ke - kb;
+    return true;
+  }
+  // Key tiles of query tile i in this run end here (at kb or before: none).
+  __device__ __forceinline__ int end(int i) const { return min(ke, nkt[i]); }
+  // The first key tile that not every row sees whole.
+  __device__ __forceinline__ int ragged() const { return least / kKeys; }
+  // Units of the item in this run with V rows to be looked after.
+  __device__ __forceinline__ int cleaned() const { return max(0, ke - max(kb, ragged())); }
+};
+
+__device__ __forceinline__ uint32_t slot_of(uint32_t unit, int chunk) {
+  return (unit * kUnitSlots + chunk) & (kSlots - 1);
+}
+__device__ __forceinline__ uint32_t round_of(uint32_t unit, int chunk) {
+  return (unit * kUnitSlots + chunk) / kSlots;
+}
+
+__device__ __noinline__ int cta_of(int64_t u, int64_t each, int extra) {
+  const int64_t longer = (each + 1) * extra;
+  return (int)(u < longer ? u / (each + 1) : extra + (u - longer) / each);
+}
+
+// ------------------------------------------------------------------ the roles
+// K and V by TMA, and where the run ends inside an item, what the join needs; returns the
+// slots filled.
+__device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& maps, const Run& run,
+                                              uint32_t smem, const Waiter& wait, int lane,
+                                              const Workspace& ws) {
+  const uint32_t bars = smem + Lay::bars;
+  // rows that one item reads leave L2 first
+  const uint64_t policy =
+      tc::l2_policy((int64_t)a.num_tokens * a.group <= (int64_t)kItemRows * a.num_seqs);
+  Walk w;
+  w.start(run);
+  uint32_t g = 0;
+  while (w.next(a)) {
+    const int h = w.head;
+#pragma unroll 1
+    for (int kt = w.kb; kt < w.ke; ++kt, ++g) {
+      const int row = w.q.k0 + kt * kKeys;
+#pragma unroll
+      for (int c = 0; c < kUnitSlots; ++c) {
+        const uint32_t slot = slot_of(g, c), round = round_of(g, c);
+        if (round > 0 &&
+            !__all_sync(0xFFFFFFFFu, wait(bars + 8 * (Lay::kEmpty + slot), (round - 1) & 1)))
+          return g * kUnitSlots + c;
+        if (lane == 0) {
+          const uint32_t full = bars + 8 * (Lay::kFull + slot), dst = smem + Lay::ring + slot * kSlot;
+          mbar_arrive_expect_tx(full, kSlot);
+          if (c < 2) tc::tma_load3(dst, &maps.kn, h * maps.kn_x + 64 * c, row, h * maps.kn_z, full, policy);
+          else if (c == 2) tc::tma_load3(dst, &maps.kp, h * maps.kp_x, row, h * maps.kp_z, full, policy);
+          else tc::tma_load3(dst, &maps.v, h * maps.v_x + 64 * (c - 3), row, h * maps.v_z, full, policy);
+        }
+        __syncwarp();
+      }
+    }
+    if (w.ke < w.tiles && lane == 0) {  // the run's last item
+      const int64_t u0 = run.begin + run.count - w.ke;  // the unit of its key tile 0
+      const int c0 = cta_of(u0, run.each, run.extra);
+      const int c1 = cta_of(u0 + w.tiles - 1, run.each, run.extra);
+      ws.split[blockIdx.x] = Split{w.q.t0, w.row0, w.head, (int16_t)w.rows, (int16_t)(c1 - c0 + 1), c0, {}};
+    }
+  }
+  return g * kUnitSlots;
+}
+
+// The queries by asynchronous copies, and the V rows that not every row sees.  (Units looked
+// after use two barriers in turn: this role may be one unit ahead of the last look at its
+// barrier, but not two, as V of the next but one waits for the scores of the next.)
+template <int F>
+__device__ __forceinline__ void aux_role(const PrefillArgs& a, const Run& run, uint32_t smem,
+                                         const Waiter& wait, int aw, int lane) {
+  const uint32_t bars = smem + Lay::bars;
+  auto waited = [&](int bar, uint32_t phase) {
+    return __all_sync(0xFFFFFFFFu, wait(bars + 8 * bar, phase & 1));
+  };
+  Walk w;
+  w.start(run);
+  uint32_t g = 0, used[2] = {0, 0}, cleaned = 0;
+  const int col = lane & 7;
+  while (w.next(a)) {
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      if (w.end(i) <= w.kb) continue;
+      const uint32_t n = i ? used[1]++ : used[0]++;
+      if (n > 0 && !waited(Lay::kQEmpty + i, n - 1)) return;
+#pragma unroll 1
+      for (int r = aw * 4 + (lane >> 3); r < kM; r += kAuxWarps * 4) {
+        const uint32_t row = w.row0 + i * kM + r;
+        const bool ok = row < w.q.rows;
+        const uint32_t dt = ok ? a.by_group(row) : 0;
+        const int64_t t = ok ? w.q.t0 + (int)dt : 0;
+        const int64_t h = ok ? (int64_t)w.head * a.group + (int)(row - dt * a.group) : 0;
+        const uint8_t* nope = a.q_nope + t * a.qn_ts + h * a.qn_hs + col * 16;
+        const uint8_t* pe = a.q_pe + t * a.qp_ts + h * a.qp_hs + col * 16;
+        const uint32_t d = smem + Lay::q + i * kQTile + r * 128 + ((col ^ (r & 7)) << 4);
+        tc::cp_async16(d, nope, ok);
+        tc::cp_async16(d + kM * 128, nope + 128, ok);
+        tc::cp_async16(d + 2 * kM * 128, pe, ok);
+      }
+      tc::cp_async_arrive(bars + 8 * (Lay::kQFull + i));
+    }
+    const int from = max(w.kb, w.ragged());
+#pragma unroll 1
+    for (int kt = from; kt < w.ke; ++kt) {
+      const uint32_t u = g + kt - w.kb;
+      const uint32_t s0 = slot_of(u, 3), s1 = slot_of(u, 4);
+      if (!waited(Lay::kFull + s0, round_of(u, 3)) || !waited(Lay::kFull + s1, round_of(u, 4))) return;
+      const uint32_t v0 = smem + Lay::ring + s0 * kSlot, v1 = smem + Lay::ring + s1 * kSlot;
+      uint32_t bad[2] = {0, 0};  // keys aw * 64 + 0..31, 32..63
+#pragma unroll
+      for (int n = 0; n < 16; ++n) {
+        const int key = aw * 64 + 4 * n + (lane >> 3), p = kt * kKeys + key;
+        const uint32_t off = key * 128 + col * 16;  // every column of the row, in any order
+        bool drop = p >= w.most;
+        const bool sp = any_special<F>(lds16(v0 + off)) | any_special<F>(lds16(v1 + off));
+        const uint32_t votes = __ballot_sync(0xFFFFFFFFu, sp && !drop);
+        if (votes & (0xFFu << (lane & 24)) && p >= w.least) drop = true;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (votes & (0xFFu << (8 * k)) && kt * kKeys + aw * 64 + 4 * n + k >= w.least)
+            bad[n >> 3] |= 1u << (4 * (n & 7) + k);
+        if (drop) {
+          sts16(v0 + off, make_uint4(0, 0, 0, 0));
+          sts16(v1 + off, make_uint4(0, 0, 0, 0));
+        }
+      }
+      if (lane == 0) {
+        sts_u32(smem + Lay::flags + (u & 3) * 16 + aw * 8, bad[0]);
+        sts_u32(smem + Lay::flags + (u & 3) * 16 + aw * 8 + 4, bad[1]);
+      }
+      tc::fence_smem_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * (Lay::kClean + (cleaned & 1)));
+      ++cleaned;
+    }
+    g += w.ke - w.kb;
+  }
+}
+
+template <int F>
+__device__ __forceinline__ void issue_scores(uint32_t smem, uint32_t tmem, bool one, int tile,
+                                             uint32_t unit) {
+  constexpr uint32_t kId = tc::instr_desc(kM, kKeys, false, F == kBF16, F == kBF16);
+  const uint32_t i = __shfl_sync(0xFFFFFFFFu, tile, 0), g = __shfl_sync(0xFFFFFFFFu, unit, 0);
+  const uint64_t qa = tc::smem_desc(smem + Lay::q + i * kQTile, 0, 1024);
+  const uint32_t d = tmem + i * kKeys;
+#pragma unroll
+  for (int c = 0; c < 3; ++c) {
+    const uint64_t kb = tc::smem_desc(smem + Lay::ring + slot_of(g, c) * kSlot, 0, 1024);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      tc::mma_16bit(one, d, qa + (c * kM * 128 >> 4) + 2 * k, kb + 2 * k, kId, c + k > 0);
+  }
+}
+// Each half of V is a slot of its own (they may be the last and the first of the ring).
+template <int F>
+__device__ __forceinline__ void issue_outputs(uint32_t smem, uint32_t tmem, bool one, int tile,
+                                              uint32_t unit, bool first) {
+  constexpr uint32_t kId = tc::instr_desc(kM, 64, false, F == kBF16, F == kBF16, true);
+  const uint32_t i = __shfl_sync(0xFFFFFFFFu, tile, 0), g = __shfl_sync(0xFFFFFFFFu, unit, 0);
+  const uint32_t p = tmem + i * kKeys;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint64_t vb = tc::smem_desc(smem + Lay::ring + slot_of(g, 3 + h) * kSlot, 0, 1024);
+    const uint32_t d = tmem + Lay::kO + i * kV + h * 64;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      tc::mma_16bit_ta(one, d, p + 8 * k, vb + k * (2048 >> 4), kId, k > 0 || !first);
+  }
+}
+
+// The units as the matrix products see them, one after the other over all items.
+struct Unit {
+  bool valid, clean;
+  bool act[2], first[2], last[2];
+};
+struct Units {
+  Walk w;
+  int kt;
+  __device__ __forceinline__ void start(const Run& r) {
+    w.start(r);
+    kt = w.ke = 0;
+  }
+  __device__ __forceinline__ Unit next(const PrefillArgs& a) {
+    Unit u{};
+    if (kt >= w.ke) {
+      if (!w.next(a)) return u;
+      kt = w.kb;
+    }
+    u.valid = true;
+    u.clean = kt >= w.ragged();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      u.act[i] = kt < w.end(i);
+      u.first[i] = kt == w.kb;
+      u.last[i] = kt + 1 == w.end(i);
+    }
+    ++kt;
+    return u;
+  }
+};
+
+template <int F>
+__device__ __forceinline__ void mma_role(const PrefillArgs& a, const Run& run, uint32_t smem,
+                                         uint32_t tmem, const Waiter& waiter, int lane) {
+  const uint32_t bars = smem + Lay::bars;
+  auto wait = [&](int bar, uint32_t phase) {
+    return __all_sync(0xFFFFFFFFu, waiter(bars + 8 * bar, phase & 1));
+  };
+  const bool one = tc::elect();
+  Units units;
+  units.start(run);
+  uint32_t done[2] = {0, 0};    // units whose outputs were issued
+  uint32_t items[2] = {0, 0};   // items whose scores / outputs were begun
+  uint32_t opened[2] = {0, 0};
+  uint32_t cleaned = 0;
+  // Scores of tile i of unit g.
+  auto scores = [&](int i, const Unit& u, uint32_t g, bool keys) {
+    if (u.first[i]) {
+      if (!wait(Lay::kQFull + i, items[i])) return false;
+      ++items[i];
+      tc::fence_smem_async();  // the queries came by ordinary copies
+    }
+    if (keys)
+      for (int c = 0; c < 3; ++c)
+        if (!wait(Lay::kFull + slot_of(g, c), round_of(g, c))) return false;
+    tc::fence_after_sync();
+    issue_scores<F>(smem, tmem, one, i, g);
+    tc::commit(one, bars + 8 * (Lay::kSFull + i));
+    if (i == 1 || !u.act[1])
+      for (int c = 0; c < 3; ++c) tc::commit(one, bars + 8 * (Lay::kEmpty + slot_of(g, c)));
+    if (u.last[i]) tc::commit(one, bars + 8 * (Lay::kQEmpty + i));
+    return true;
+  };
+  uint32_t g = 0;
+  Unit nxt = units.next(a);
+  if (nxt.valid)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (nxt.act[i] && !scores(i, nxt, 0, i == 0 || !nxt.act[0])) return;
+#pragma unroll 1
+  for (;; ++g) {
+    const Unit cur = nxt;
+    if (!cur.valid) break;
+    nxt = units.next(a);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (cur.act[i]) {
+        if (!wait(Lay::kPFull + i, done[i])) return;
+        if (cur.first[i]) {
+          // the sums of the item before are read
+          if (opened[i] > 0 && !wait(Lay::kOFree + i, opened[i] - 1)) return;
+          ++opened[i];
+        }
+        if (i == 0 || !cur.act[0]) {
+          if (!wait(Lay::kFull + slot_of(g, 3), round_of(g, 3)) ||
+              !wait(Lay::kFull + slot_of(g, 4), round_of(g, 4)))
+            return;
+          if (cur.clean) {
+            if (!wait(Lay::kClean + (cleaned & 1), cleaned >> 1)) return;
+            ++cleaned;
+          }
+        }
+        tc::fence_after_sync();
+        issue_outputs<F>(smem, tmem, one, i, g, cur.first[i]);
+        tc::commit(one, bars + 8 * (Lay::kPvDone + i));
+        ++done[i];
+        if (i == 1 || !cur.act[1]) {
+          tc::commit(one, bars + 8 * (Lay::kEmpty + slot_of(g, 3)));
+          tc::commit(one, bars + 8 * (Lay::kEmpty + slot_of(g, 4)));
+        }
+      }
+      if (nxt.valid && !nxt.first[0] && nxt.act[i] && !scores(i, nxt, g + 1, i == 0 || !nxt.act[0]))
+        return;
+    }
+    // another item: its queries may have to wait for, the outputs above not
+    if (nxt.valid && nxt.first[0])
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (nxt.act[i] && !scores(i, nxt, g + 1, i == 0 || !nxt.act[0])) return;
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <int F>
+__device__ __forceinline__ uint32_t pack16x2(float lo, float hi) {
+  if constexpr (F == kF16) return pack_f16x2(lo, hi);
+  else return pack_bf16x2(lo, hi);
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Weights and output of one query tile; a thread has a row.
+template <int F>
+__device__ __forceinline__ void softmax_role(const PrefillArgs& a, const Run& run, uint32_t smem,
+                                             uint32_t tmem, const Waiter& waiter, int tile, int w4,
+                                             int lane, const Workspace& ws, int srows) {
+  using R = Ref<F>;
+  const uint32_t bars = smem + Lay::bars;
+  auto wait = [&](int bar, uint32_t phase) {
+    return __all_sync(0xFFFFFFFFu, waiter(bars + 8 * bar, phase & 1));
+  };
+  const uint32_t s_at = tmem + tile * kKeys + ((uint32_t)(w4 * 32) << 16);
+  const uint32_t o_at = tmem + Lay::kO + tile * kV + ((uint32_t)(w4 * 32) << 16);
+  const float c = a.softmax_scale * kLog2e;
+  const int r = w4 * 32 + lane;
+  Walk w;
+  w.start(run);
+  uint32_t n = 0, g = 0, cleaned = 0;
+#pragma unroll 1
+  while (w.next(a)) {
+    const int e = w.end(tile), mine = w.rows - tile * kM;  // rows of this tile (or less than 0)
+    const bool live = w4 * 32 < mine;  // this warp has rows
+    const uint32_t row = w.row0 + tile * kM + r;
+    const bool ok = r < mine;
+    const int seen = ok ? seen_of(a, w.q, row) : 0;
+    const int from = max(w.kb, w.ragged());
+    float mu = -INFINITY, l = 0.0f;
+#pragma unroll 1
+    for (int kt = w.kb; kt < e; ++kt, ++n) {
+      if (!wait(Lay::kSFull + tile, n)) return;
+      tc::fence_after_sync();
+      if (live) {
+        float x[kKeys];
+        tc::ld_32x128(s_at, reinterpret_cast<uint32_t*>(x));
+        float cs = c;
+        if (__builtin_expect(kt >= from, 0)) {
+          const uint32_t n = cleaned + kt - from;
+          if (!wait(Lay::kClean + (n & 1), n >> 1)) return;
+          const int lim = seen - kt * kKeys;
+          const uint32_t at = smem + Lay::flags + ((g + kt - w.kb) & 3) * 16;
+          bool bad = false;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int below = min(max(lim - 32 * k, 0), 32);
+            bad |= (lds_u32(at + 4 * k) & (below == 32 ? 0xFFFFFFFFu : (1u << below) - 1)) != 0;
+          }
+          if (bad) l = NAN;
+#pragma unroll
+          for (int j = 0; j < kKeys; ++j) x[j] = j < lim ? x[j] * c : -INFINITY;
+          cs = 1.0f;
+        }
+        float top;
+        {
+          float t[8];
+          if (cs >= 0.0f) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) t[j] = fmaxf(x[j], x[j + 8]);
+#pragma unroll
+            for (int j = 16; j < kKeys; j += 16)
+#pragma unroll
+              for (int k = 0; k < 8; ++k) t[k] = fmaxf(t[k], fmaxf(x[j + k], x[j + k + 8]));
+            top = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])),
+                        fmaxf(fmaxf(t[4], t[5]), fmaxf(t[6], t[7])));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) t[j] = fminf(x[j], x[j + 8]);
+#pragma unroll
+            for (int j = 16; j < kKeys; j += 16)
+#pragma unroll
+              for (int k = 0; k < 8; ++k) t[k] = fminf(t[k], fminf(x[j + k], x[j + k + 8]));
+            top = fminf(fminf(fminf(t[0], t[1]), fminf(t[2], t[3])),
+                        fminf(fminf(t[4], t[5]), fminf(t[6], t[7])));
+          }
+          top *= cs;
+        }
+        const bool grown = top > mu + R::kGrow;
+        if (__builtin_expect(__any_sync(0xFFFFFFFFu, grown), 0)) {
+          const float mn = grown ? fmaxf(mu, ceilf(top) - R::kTop) : mu;
+          const float f = mu == -INFINITY ? 0.0f : ex2(mu - mn);
+          l = l == 0.0f ? 0.0f : l * f;  // (a NaN stays)
+          mu = mn;
+          if (kt > w.kb) {
+            if (!wait(Lay::kPvDone + tile, n - 1)) return;
+            tc::fence_after_sync();
+#pragma unroll 1
+            for (int k = 0; k < kV; k += 16) {
+              uint32_t y[16];
+              tc::ld_32x16(o_at + k, y);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
+              tc::st_32x16(o_at + k, y);
+            }
+            tc::wait_st();
+          }
+        }
+        const float m0 = mu == -INFINITY ? 0.0f : -mu;
+        const uint64_t c2 = f2(cs, cs), m2 = f2(m0, m0);
+        uint64_t sum[4] = {0, 0, 0, 0};
+        uint32_t* pk = reinterpret_cast<uint32_t*>(x);
+#pragma unroll
+        for (int j = 0; j < kKeys / 2; ++j) {
+          const float2 y = unf2(fma2(f2(x[2 * j], x[2 * j + 1]), c2, m2));
+          const float p0 = ex2(y.x), p1 = ex2(y.y);
+          sum[j & 3] = add2(sum[j & 3], f2(p0, p1));
+          pk[j] = pack16x2<F>(p0, p1);
+        }
+        tc::st_32x32(s_at, pk);
+        tc::st_32x32(s_at + 32, pk + 32);
+        const float2 t = unf2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+        l += t.x + t.y;
+        tc::wait_st();
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * (Lay::kPFull + tile));
+    }
+    // ---- the end of this CTA's part of the item
+    const bool any = e > w.kb;
+    if (any) {
+      if (!wait(Lay::kPvDone + tile, n - 1)) return;
+      tc::fence_after_sync();
+    }
+    if (live) {
+      const bool whole = w.kb == 0 && w.ke == w.tiles;
+      const int64_t slot = 2 * (int64_t)blockIdx.x + (w.kb == 0 ? 1 : 0);
+      const int64_t at = slot * srows + tile * kM + r;
+      const uint32_t dt = a.by_group(row);
+      const int64_t t = w.q.t0 + (int)dt, h = (int64_t)w.head * a.group + (int)(row - dt * a.group);
+      if (ok && !whole) {
+        ws.m[at] = mu;
+        ws.l[at] = l;
+      } else if (ok && a.lse) {
+        a.lse[t * a.lse_ts + h * a.lse_hs] = l == 0.0f ? -INFINITY : (mu + __log2f(l)) * kLn2;
+      }
+      const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
+      uint8_t* out = a.out + t * a.out_ts + h * a.out_hs;
+      if (any) {
+#pragma unroll 1
+        for (int k = 0; k < kV; k += 32) {
+          uint32_t y[32];
+          tc::ld_32x32(o_at + k, y);
+          if (!ok) continue;
+          if (whole) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+              uint32_t z[4];
+#pragma unroll
+              for (int m = 0; m < 4; ++m)
+                z[m] = pack16x2<F>(__uint_as_float(y[j + 2 * m]) * inv,
+                                   __uint_as_float(y[j + 2 * m + 1]) * inv);
+              st16(out + (k + j) * 2, make_uint4(z[0], z[1], z[2], z[3]));
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              st16(ws.o + at * kV + k + j, make_uint4(y[j], y[j + 1], y[j + 2], y[j + 3]));
+          }
+        }
+      }
+    }
+    if (any) {
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * (Lay::kOFree + tile));
+    }
+    g += w.ke - w.kb;
+    cleaned += w.cleaned();
+  }
+}
+
+// ------------------------------------------------------------------ scheduling
+__device__ __forceinline__ int64_t scan64(int64_t v, int lane) {  // inclusive, over the warp
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+// This CTA's run, by the whole CTA; the scratch is the (still unused) ring.
+__device__ __noinline__ void schedule(const PrefillArgs& a, uint8_t* scratch, Run& r,
+                                      uint32_t& errbits) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int64_t* pre = reinterpret_cast<int64_t*>(scratch);  // [num_seqs]
+  int64_t* part = pre + a.num_seqs;                    // [kWarps]
+  int64_t* at = part + kWarps;                         // sequence, unit in it, item, key tile
+  for (int s = warp; s < a.num_seqs; s += kWarps) {
+    const Seq q = load_seq(a, s, errbits);
+    int64_t u = 0;
+    for (int b = lane; b < q.nb; b += 32) u += kSwitch + item_tiles(a, q, b);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
+    if (lane == 0) pre[s] = u * a.kv_heads;
+  }
+  __syncthreads();
+  const int run = (a.num_seqs + kThreads - 1) / kThreads;
+  const int s0 = min((int)threadIdx.x * run, a.num_seqs), s1 = min(s0 + run, a.num_seqs);
+  int64_t sum = 0;
+  for (int s = s0; s < s1; ++s) sum += pre[s];
+  const int64_t inc = scan64(sum, lane);
+  if (lane == 31) part[warp] = inc;
+  __syncthreads();
+  int64_t before = inc - sum, total = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += part[w];
+    total += part[w];
+  }
+  const int64_t ctas = max((int64_t)1, min((int64_t)gridDim.x, total / kMinUnits));
+  r.each = total / ctas;
+  r.extra = (int)(total - r.each * ctas);
+  r.begin = r.each * blockIdx.x + min((int)blockIdx.x, r.extra);
+  r.count = blockIdx.x < ctas ? (int)r.each + ((int)blockIdx.x < r.extra ? 1 : 0) : 0;
+  r.kt = 0;
+  if (r.count > 0)
+    for (int s = s0; s < s1; ++s) {
+      const int64_t u = pre[s];
+      if (before <= r.begin && r.begin < before + u) {
+        at[0] = s;
+        at[1] = r.begin - before;
+        at[2] = u;
+      }
+      before += u;
+    }
+  __syncthreads();
+  if (r.count > 0) {
+    uint32_t ignored = 0;
+    r.s = (int)at[0];
+    r.q = load_seq(a, r.s, ignored);
+    const int64_t per = at[2] / a.kv_heads;
+    r.head = (int)(at[1] / per);
+    if (warp == 0) {
+      const int64_t off = at[1] - r.head * per;
+      int64_t base = 0;
+      for (int b0 = 0; b0 < r.q.nb; b0 += 32) {
+        const int64_t u = b0 + lane < r.q.nb ? kSwitch + item_tiles(a, r.q, b0 + lane) : 0;
+        const int64_t in = scan64(u, lane);
+        const uint32_t hit = __ballot_sync(0xFFFFFFFFu, off < base + in);
+        if (hit) {
+          if (lane == __ffs(hit) - 1) {
+            at[3] = b0 + lane;
+            at[4] = off - (base + in - u);
+          }
+          break;
+        }
+        base += __shfl_sync(0xFFFFFFFFu, in, 31);
+      }
+    }
+  }
+  __syncthreads();
+  if (r.count > 0) {
+    r.b = (int)at[3];
+    r.kt = (int)at[4] - kSwitch;
+  }
+  tc::fence_smem_async();  // the scratch is read; copies may write there now
+  __syncthreads();
+}
+
+// After giving up: waits, bounded again, for the copies into shared memory, and a
+// millisecond for matrix products in flight (they end by themselves within microseconds).
+__device__ __noinline__ void settle(uint32_t smem, uint32_t issued, uint64_t limit) {
+  const uint64_t since = global_ns();
+  for (uint32_t i = issued > kSlots ? issued - kSlots : 0; i < issued; ++i)
+    while (!mbar_try_wait(smem + Lay::bars + 8 * (Lay::kFull + (i & (kSlots - 1))), (i / kSlots) & 1) &&
+           global_ns() - since <= limit) {
+    }
+  while (global_ns() - since <= 1000000) {
+  }
+}
+
+template <int F>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_attention_kernel(const PrefillArgs a, const __grid_constant__ Maps maps) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t smem = smem_addr(smem_raw);
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  Misc& m = *reinterpret_cast<Misc*>(smem_raw + Lay::misc);
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    m.abort = 0;
+    const uint32_t bars = smem + Lay::bars;
+    for (int i = 0; i < kSlots; ++i) {
+      const bool stall = blockIdx.x == 0 && a.stall_stage == i + 1;  // one arrival too many
+      mbar_init(bars + 8 * (Lay::kFull + i), stall ? 2 : 1);
+      mbar_init(bars + 8 * (Lay::kEmpty + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bars + 8 * (Lay::kQFull + i), kAuxWarps * 32);
+      mbar_init(bars + 8 * (Lay::kQEmpty + i), 1);
+      mbar_init(bars + 8 * (Lay::kSFull + i), 1);
+      mbar_init(bars + 8 * (Lay::kPFull + i), 4);
+      mbar_init(bars + 8 * (Lay::kPvDone + i), 1);
+      mbar_init(bars + 8 * (Lay::kOFree + i), 4);
+      mbar_init(bars + 8 * (Lay::kClean + i), kAuxWarps);
+    }
+    mbar_fence_init();
+  }
+  const Waiter wait{smem_addr(&m.abort), a.wait_limit_ns};
+  pdl_wait();
+  if (warp == kMmaWarp) tc::alloc(smem_addr(&m.tmem), Lay::kTmem);
+  const int srows = slot_rows(a.num_tokens, a.group);
+  const Workspace ws = workspace_of(a.workspace, gridDim.x, srows);
+  if (threadIdx.x == 0) ws.split[blockIdx.x] = Split{};
+  uint32_t errbits = 0;
+  Run run;
+  schedule(a, smem_raw + Lay::ring, run, errbits);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, m.tmem, 0);
+  uint32_t issued = 0;
+  if (run.count > 0) {
+    if (warp < 8) {
+      softmax_role<F>(a, run, smem, tmem, wait, warp >> 2, warp & 3, lane, ws, srows);
+    } else if (warp == kMmaWarp) {
+      mma_role<F>(a, run, smem, tmem, wait, lane);
+    } else if (warp == kLoadWarp) {
+      issued = load_role(a, maps, run, smem, wait, lane, ws);
+    } else {
+      aux_role<F>(a, run, smem, wait, warp - kAuxWarp, lane);
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+  }
+  __syncwarp();
+  if (a.err) {
+    errbits = __reduce_or_sync(0xFFFFFFFFu, errbits);
+    if (lane == 0) {
+      if (wait.given_up()) errbits |= kErrTimeout;
+      if (errbits) atomicOr(a.err, errbits);
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (__builtin_expect(wait.given_up(), 0)) {
+    if (warp == kLoadWarp) settle(smem, issued, a.wait_limit_ns);
+    __syncthreads();
+  }
+  if (warp == kMmaWarp) tc::dealloc(tmem, Lay::kTmem);
+}
+
+// -------------------------------------------------------- join of the split items
+// Block (x, c) looks at what CTA c left.  The rows of an item of `parts` CTAs are dealt to
+// the warps of the blocks of all of them but the last; a lane has four dims.
+constexpr int kJoinWarps = 8, kJoinBlocks = 8;
+
+template <int F>
+__global__ void __launch_bounds__(kJoinWarps * 32) prefill_join_kernel(const PrefillArgs a) {
+  pdl_trigger();
+  pdl_wait();
+  const int srows = slot_rows(a.num_tokens, a.group);
+  const Workspace ws = workspace_of(a.workspace, gridDim.y, srows);
+  const Split sp = ws.split[blockIdx.y];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int stride = (sp.parts - 1) * kJoinBlocks * kJoinWarps;
+  for (int n = (((int)blockIdx.y - sp.first) * kJoinBlocks + (int)blockIdx.x) * kJoinWarps + warp;
+       n < sp.rows; n += stride) {
+    float4 acc = make_float4(0, 0, 0, 0);
+    float sum = 0.0f, top = -INFINITY;
+    // the first partial lies in the odd slot of the first CTA, the others in the even ones behind
+#pragma unroll 1
+    for (int i = 0; i < sp.parts; i += 4) {
+      float4 v[4];
+      float lv[4], mv[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t at = (2 * (int64_t)(sp.first + i + k) + (i + k == 0 ? 1 : 0)) * srows + n;
+        lv[k] = 0.0f;
+        mv[k] = -INFINITY;
+        v[k] = make_float4(0, 0, 0, 0);
+        if (i + k < sp.parts) {
+          lv[k] = ws.l[at];
+          mv[k] = ws.m[at];
+          v[k] = __ldcs(reinterpret_cast<const float4*>(ws.o + at * kV) + lane);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (lv[k] == 0.0f) continue;  // nothing seen there (and perhaps nothing written)
+        const float m = fmaxf(top, mv[k]), m0 = m == -INFINITY ? 0.0f : m;
+        const float f = ex2(top - m0), w = ex2(mv[k] - m0);
+        acc.x = fmaf(acc.x, f, w * v[k].x);
+        acc.y = fmaf(acc.y, f, w * v[k].y);
+        acc.z = fmaf(acc.z, f, w * v[k].z);
+        acc.w = fmaf(acc.w, f, w * v[k].w);
+        sum = fmaf(sum, f, w * lv[k]);
+        top = m;
+      }
+    }
+    const uint32_t row = sp.row0 + n, dt = a.by_group(row);
+    const int64_t t = sp.tok0 + (int)dt, h = (int64_t)sp.head * a.group + (int)(row - dt * a.group);
+    const float inv = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
+    st8(a.out + t * a.out_ts + h * a.out_hs + lane * 8,
+        make_uint2(pack16x2<F>(acc.x * inv, acc.y * inv), pack16x2<F>(acc.z * inv, acc.w * inv)));
+    if (lane == 0 && a.lse)
+      a.lse[t * a.lse_ts + h * a.lse_hs] = sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * kLn2;
+  }
+}
+
+// ------------------------------------------------------------------ launches
+// Rows of keys (or values) of all heads as a tensor map with boxes of `cols` columns and 128
+// rows.  Heads inside a row are columns of it, so that any head stride does; otherwise (heads
+// apart) the third dimension.  `base` stands in for arrays without rows.
+bool make_map(CUtensorMap* map, const void* base, int fmt, int width, int64_t hs, int heads, int64_t ts,
+              int64_t rows, int32_t* x_head, int32_t* z_head) {
+  const TensorMapEncode encode = tensor_map_encode();
+  if (!encode) return false;
+  const int es = is16(fmt) ? 2 : 1;
+  *x_head = *z_head = 0;
+  const int64_t flat = (heads - 1) * hs + (int64_t)width * es;
+  cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)rows, 1};
+  cuuint64_t strides[2] = {(cuuint64_t)ts, (cuuint64_t)ts};
+  if (rows <= 1) strides[0] = strides[1] = (cuuint64_t)((flat + 15) / 16 * 16);
+  if (heads > 1 && hs > 0) {
+    if (rows <= 1 || flat <= ts) {
+      dims[0] = (cuuint64_t)(flat / es);
+      *x_head = (int32_t)(hs / es);
+    } else {
+      dims[2] = (cuuint64_t)heads;
+      strides[1] = (cuuint64_t)hs;
+      *z_head = 1;
+    }
+  }
+  if (dims[0] > INT32_MAX) return false;
+  const cuuint32_t box[3] = {64, (cuuint32_t)kKeys, 1}, unit[3] = {1, 1, 1};
+  const CUtensorMapDataType type =
+      fmt == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return encode(map, type, 3, const_cast<void*>(base), dims, strides, box, unit,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int F>
+cudaError_t launch_tc(const PrefillArgs& a, int ctas, const LaunchCfg& cfg) {
+  Maps maps = {};
+  const bool none = a.num_kv == 0;
+  const int64_t rows = none ? 1 : a.num_kv;
+  const int heads = none ? 1 : a.kv_heads;
+  if (!make_map(&maps.kn, none ? a.q_nope : a.k_nope, F, 128, a.kn_hs, heads, a.kn_ts, rows, &maps.kn_x,
+                &maps.kn_z) ||
+      !make_map(&maps.kp, none ? a.q_nope : a.k_pe, F, 64, a.kp_hs, heads, a.kp_ts, rows, &maps.kp_x,
+                &maps.kp_z) ||
+      !make_map(&maps.v, none ? a.q_nope : a.v, F, 128, a.v_hs, heads, a.v_ts, rows, &maps.v_x, &maps.v_z))
+    return cudaErrorInvalidValue;
+  auto kern = prefill_attention_kernel<F>;
+  // the attribute stays with the device's context: set on a device's first call
+  static std::atomic<uint64_t> set{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(set.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::bytes);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) set.fetch_or(uint64_t(1) << dev);
+  }
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(ctas);
+  lc.blockDim = dim3(kThreads);
+  lc.dynamicSmemBytes = Lay::bytes;
+  lc.stream = cfg.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = cfg.pdl ? 1 : 0;
+  e = cudaLaunchKernelEx(&lc, kern, a, maps);
+  if (e != cudaSuccess) return e;
+  lc.gridDim = dim3(kJoinBlocks, ctas);
+  lc.blockDim = dim3(kJoinWarps * 32);
+  lc.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&lc, prefill_join_kernel<F>, a);
+}
 
 template <int F>
 __device__ __forceinline__ float value_at(const uint8_t* row, int i) {
@@ -29,15 +997,15 @@ __device__ __forceinline__ float value_at(const uint8_t* row, int i) {
 }
 
 template <int F, int KF>
-__global__ void __launch_bounds__(kThreads) prefill_attention_kernel(const PrefillArgs a) {
+__global__ void __launch_bounds__(kSimpleThreads) prefill_simple_kernel(const PrefillArgs a) {
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int64_t rows = (int64_t)a.num_tokens * a.num_heads;
-  const int64_t warps = ((int64_t)gridDim.x * kThreads) >> 5;
+  const int64_t warps = ((int64_t)gridDim.x * kSimpleThreads) >> 5;
   const float ks = KF == kE4M3 || KF == kE5M2 ? *a.kv_scale : 1.0f;
   uint32_t errbits = 0;
-  for (int64_t row = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; row < rows; row += warps) {
+  for (int64_t row = ((int64_t)blockIdx.x * kSimpleThreads + threadIdx.x) >> 5; row < rows; row += warps) {
     const int t = (int)(row / a.num_heads), h = (int)(row - (int64_t)t * a.num_heads);
     int s = -1;
     for (int i = 0; i < a.num_seqs; ++i)
@@ -84,12 +1052,12 @@ __global__ void __launch_bounds__(kThreads) prefill_attention_kernel(const Prefi
 }
 
 template <int F, int KF>
-cudaError_t launch_t(const PrefillArgs& a, const LaunchCfg& cfg) {
-  const auto kern = prefill_attention_kernel<F, KF>;
+cudaError_t launch_simple(const PrefillArgs& a, const LaunchCfg& cfg) {
+  const auto kern = prefill_simple_kernel<F, KF>;
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3(capped_grid(reinterpret_cast<const void*>(kern), kThreads,
-                                ((int64_t)a.num_tokens * a.num_heads + kThreads / 32 - 1) / (kThreads / 32)));
-  lc.blockDim = dim3(kThreads);
+  lc.gridDim = dim3(capped_grid(reinterpret_cast<const void*>(kern), kSimpleThreads,
+                                ((int64_t)a.num_tokens * a.num_heads + kSimpleThreads / 32 - 1) / (kSimpleThreads / 32)));
+  lc.blockDim = dim3(kSimpleThreads);
   lc.stream = cfg.stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -99,18 +1067,25 @@ cudaError_t launch_t(const PrefillArgs& a, const LaunchCfg& cfg) {
   return cudaLaunchKernelEx(&lc, kern, a);
 }
 
+
 }  // namespace
 
-int64_t prefill_attention_workspace(int32_t, int32_t, int32_t, int32_t, int) { return 16; }
+int64_t prefill_attention_workspace(int32_t num_tokens, int32_t num_heads, int32_t kv_heads, int32_t,
+                                    int num_sms) {
+  const int64_t ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
+  return ctas * ((int64_t)sizeof(Split) +
+                 2 * slot_rows(num_tokens, num_heads / kv_heads) * (2 + kV) * (int64_t)sizeof(float));
+}
 
-cudaError_t launch_prefill_attention(const PrefillArgs& a, int fmt, int kv_fmt, int,
+cudaError_t launch_prefill_attention(const PrefillArgs& a, int fmt, int kv_fmt, int num_sms,
                                      const LaunchCfg& cfg) {
+  const int ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
   if (fmt == kBF16) {
-    if (kv_fmt == kBF16) return launch_t<kBF16, kBF16>(a, cfg);
-    return kv_fmt == kE4M3 ? launch_t<kBF16, kE4M3>(a, cfg) : launch_t<kBF16, kE5M2>(a, cfg);
+    if (kv_fmt == kBF16) return launch_tc<kBF16>(a, ctas, cfg);
+    return kv_fmt == kE4M3 ? launch_simple<kBF16, kE4M3>(a, cfg) : launch_simple<kBF16, kE5M2>(a, cfg);
   }
-  if (kv_fmt == kF16) return launch_t<kF16, kF16>(a, cfg);
-  return kv_fmt == kE4M3 ? launch_t<kF16, kE4M3>(a, cfg) : launch_t<kF16, kE5M2>(a, cfg);
+  if (kv_fmt == kF16) return launch_tc<kF16>(a, ctas, cfg);
+  return kv_fmt == kE4M3 ? launch_simple<kF16, kE4M3>(a, cfg) : launch_simple<kF16, kE5M2>(a, cfg);
 }
 
 }  // namespace mla

@@ -135,6 +135,7 @@ struct PrefillArgs {
   int64_t v_ts, v_hs;
   int32_t num_kv, kv_heads;
   int32_t group;  // query heads of a key head
+  Divider by_group;
   const int32_t* cu_q;
   const int32_t* cu_kv;
   int32_t num_seqs;

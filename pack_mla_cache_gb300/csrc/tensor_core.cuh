@@ -1,8 +1,9 @@
 // tensor_core.cuh -- thin wrappers over the 5th-generation tensor core PTX of
-// sm_103a (tcgen05) that the latent attention uses: tensor memory allocation,
-// shared-memory and instruction descriptors, the bf16 and e4m3 / e5m2 matrix
-// instructions with fp32 accumulators in tensor memory, their completion on an
-// mbarrier, loads and stores of tensor memory, and the copies that feed them.
+// sm_103a (tcgen05) that the attentions use: tensor memory allocation, shared-memory
+// and instruction descriptors, the 16-bit and e4m3 / e5m2 matrix instructions with
+// fp32 accumulators in tensor memory, their completion on an mbarrier, loads and
+// stores of tensor memory, and the copies that feed them; and the bounded waits of
+// their pipelines.
 #pragma once
 
 #include <cstdint>
@@ -24,6 +25,74 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
       : "r"(bar), "r"(parity)
       : "memory");
   return done != 0;
+}
+
+// A thread's view of other shared memory, by its shared address.
+__device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
+               "r"(v.z), "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ void sts8(uint32_t addr, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void sts_u8(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void sts_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Bounded waits.  The loops of the roles have to stay small (10 or 14 warps of
+// different code share the instruction caches; fetching was the largest stall), so all but
+// the first look at a barrier is out of line.
+static __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, uint32_t abort, uint64_t limit) {
+  uint64_t since = 0;
+  for (uint32_t spin = 1; !mbar_try_wait(bar, parity); ++spin) {
+    if (spin & 31u) continue;
+    if (lds_u32(abort) != 0) return false;
+    const uint64_t now = global_ns();
+    if (since == 0) since = now;
+    if (now - since > limit) {
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(abort), "r"(1u) : "memory");
+      return false;
+    }
+  }
+  return true;
+}
+struct Waiter {
+  uint32_t abort;  // shared address of Misc::abort
+  uint64_t limit;
+  __device__ __forceinline__ bool given_up() const { return lds_u32(abort) != 0; }
+  // Whether the barrier's phase completed: false once the CTA has given up.
+  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+    return mbar_try_wait(bar, parity) || wait_on(bar, parity, abort, limit);
+  }
+};
+
+// Whether any of the 8 16-bit (16 fp8) values of v is a NaN or an infinity.
+template <int FMT>
+__device__ __forceinline__ bool any_special(uint4 v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (FMT == kBF16) m |= (w[i] & 0x7FFF7FFFu) + 0x00800080u;  // exponent 255 carries
+    else if constexpr (FMT == kF16) m |= (w[i] & 0x7FFF7FFFu) + 0x04000400u;
+    else if constexpr (FMT == kE4M3) m |= (w[i] & 0x7F7F7F7Fu) + 0x01010101u;
+    else m |= (w[i] & 0x7F7F7F7Fu) + 0x04040404u;
+  }
+  return (m & (is16(FMT) ? 0x80008000u : 0x80808080u)) != 0;
 }
 
 namespace tc {
@@ -66,11 +135,13 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
          ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-// Instruction descriptor: fp32 accumulator, M x N tile, A MN-major or K-major, B
-// K-major.  fa / fb: 1 for bf16 (mma_bf16); 0 for e4m3, 1 for e5m2 (mma_fp8).
-__host__ __device__ constexpr uint32_t instr_desc(int m, int n, bool a_mn, int fa, int fb) {
+// Instruction descriptor: fp32 accumulator, M x N tile, A and B MN-major or K-major.
+// fa / fb: 1 for bf16, 0 for fp16 (mma_16bit, both the same); 0 for e4m3, 1 for e5m2
+// (mma_fp8).
+__host__ __device__ constexpr uint32_t instr_desc(int m, int n, bool a_mn, int fa, int fb,
+                                                  bool b_mn = false) {
   return (1u << 4) | ((uint32_t)fa << 7) | ((uint32_t)fb << 10) | (a_mn ? 1u << 15 : 0u) |
-         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+         (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
 // True in one lane of the (converged) warp.
@@ -84,7 +155,7 @@ __device__ __forceinline__ bool elect() {
 // two statements and `lane` holds in the one lane that issues: without a branch
 // around them, descriptors that are the same in all lanes are computed in uniform
 // registers, where the instruction wants them.
-__device__ __forceinline__ void mma_bf16(bool lane, uint32_t d, uint64_t a, uint64_t b,
+__device__ __forceinline__ void mma_16bit(bool lane, uint32_t d, uint64_t a, uint64_t b,
                                          uint32_t idesc, bool accumulate) {
   asm volatile(
       "{ .reg .pred p, q; setp.ne.u32 p, %4, 0; setp.ne.u32 q, %5, 0;\n"
@@ -92,7 +163,16 @@ __device__ __forceinline__ void mma_bf16(bool lane, uint32_t d, uint64_t a, uint
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(lane ? 1u : 0u)
       : "memory");
 }
-// The same for fp8 operands (of either format each): one k step of 32.
+// The same with A in tensor memory: two 16-bit values of a row per column, the lower k low.
+__device__ __forceinline__ void mma_16bit_ta(bool lane, uint32_t d, uint32_t a, uint64_t b,
+                                             uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.u32 p, %4, 0; setp.ne.u32 q, %5, 0;\n"
+      "  @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(lane ? 1u : 0u)
+      : "memory");
+}
+// The same as mma_16bit for fp8 operands (of either format each): one k step of 32.
 __device__ __forceinline__ void mma_fp8(bool lane, uint32_t d, uint64_t a, uint64_t b,
                                         uint32_t idesc, bool accumulate) {
   asm volatile(
@@ -162,6 +242,69 @@ __device__ __forceinline__ void st_32x16(uint32_t addr, const uint32_t* r) {
       "%11, %12, %13, %14, %15, %16};" ::"r"(addr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// 32 lanes x 32 columns: thread t gets lane t's 32 columns.
+__device__ __forceinline__ void ld_32x32(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
+      "%10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, "
+      "%26, %27, %28, %29, %30, %31}, [%32];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr)
+      : "memory");
+}
+// 32 lanes x 128 columns: thread t gets lane t's 128 columns.
+__device__ __forceinline__ void ld_32x128(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x128.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
+      "%10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, "
+      "%26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, "
+      "%42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, "
+      "%58, %59, %60, %61, %62, %63, %64, %65, %66, %67, %68, %69, %70, %71, %72, %73, "
+      "%74, %75, %76, %77, %78, %79, %80, %81, %82, %83, %84, %85, %86, %87, %88, %89, "
+      "%90, %91, %92, %93, %94, %95, %96, %97, %98, %99, %100, %101, %102, %103, %104, "
+      "%105, %106, %107, %108, %109, %110, %111, %112, %113, %114, %115, %116, %117, "
+      "%118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%128];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]),
+        "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]),
+        "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
+        "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]),
+        "=r"(r[63]), "=r"(r[64]), "=r"(r[65]), "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]),
+        "=r"(r[70]), "=r"(r[71]), "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]),
+        "=r"(r[77]), "=r"(r[78]), "=r"(r[79]), "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]),
+        "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]), "=r"(r[88]), "=r"(r[89]), "=r"(r[90]),
+        "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]), "=r"(r[96]), "=r"(r[97]),
+        "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]), "=r"(r[103]),
+        "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]),
+        "=r"(r[110]), "=r"(r[111]), "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]),
+        "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]), "=r"(r[120]), "=r"(r[121]),
+        "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]), "=r"(r[126]), "=r"(r[127])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void st_32x32(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, "
+      "%10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, "
+      "%26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
 
