@@ -79,7 +79,7 @@ struct Lay {
   static constexpr int bars = flags + 64;
   static constexpr int kFull = 0, kEmpty = kSlots, kQFull = 2 * kSlots, kQEmpty = kQFull + 2,
                        kSFull = kQEmpty + 2, kPFull = kSFull + 2, kPvDone = kPFull + 2,
-                       kOFree = kPvDone + 2, kClean = kOFree + 2, kBars = kClean + 2;
+                       kOFree = kPvDone + 2, kClean = kOFree + 2, kRaw = kClean + 2, kBars = kRaw + 2;
   static constexpr int misc = (bars + kBars * 8 + 15) / 16 * 16;
   static constexpr int bytes = misc + 64;
   static_assert(bytes <= 232448, "shared memory of a CTA");
@@ -238,10 +238,12 @@ __device__ __noinline__ int cta_of(int64_t u, int64_t each, int extra) {
 
 // ------------------------------------------------------------------ the roles
 // K and V by TMA, and where the run ends inside an item, what the join needs; returns the
-// slots filled.
+// slots filled and the units whose V is looked after.  V of such a unit completes on a barrier
+// of its own (two in turn), which the aux warps wait for: they do not follow the ring's slots
+// through the units between, and a barrier's parity tells one phase from the next only.
 __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& maps, const Run& run,
                                               uint32_t smem, const Waiter& wait, int lane,
-                                              const Workspace& ws) {
+                                              const Workspace& ws, uint32_t& cleaned) {
   const uint32_t bars = smem + Lay::bars;
   // rows that one item reads leave L2 first
   const uint64_t policy =
@@ -249,6 +251,7 @@ __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& 
   Walk w;
   w.start(run);
   uint32_t g = 0;
+  cleaned = 0;
   while (w.next(a)) {
     const int h = w.head;
 #pragma unroll 1
@@ -261,7 +264,12 @@ __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& 
             !__all_sync(0xFFFFFFFFu, wait(bars + 8 * (Lay::kEmpty + slot), (round - 1) & 1)))
           return g * kUnitSlots + c;
         if (lane == 0) {
-          const uint32_t full = bars + 8 * (Lay::kFull + slot), dst = smem + Lay::ring + slot * kSlot;
+          uint32_t full = bars + 8 * (Lay::kFull + slot);
+          const uint32_t dst = smem + Lay::ring + slot * kSlot;
+          if (c >= 3 && kt >= w.ragged()) {
+            mbar_arrive(full);
+            full = bars + 8 * (Lay::kRaw + (cleaned & 1));
+          }
           mbar_arrive_expect_tx(full, kSlot);
           if (c < 2) tc::tma_load3(dst, &maps.kn, h * maps.kn_x + 64 * c, row, h * maps.kn_z, full, policy);
           else if (c == 2) tc::tma_load3(dst, &maps.kp, h * maps.kp_x, row, h * maps.kp_z, full, policy);
@@ -269,6 +277,7 @@ __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& 
         }
         __syncwarp();
       }
+      cleaned += kt >= w.ragged();
     }
     if (w.ke < w.tiles && lane == 0) {  // the run's last item
       const int64_t u0 = run.begin + run.count - w.ke;  // the unit of its key tile 0
@@ -321,7 +330,7 @@ __device__ __forceinline__ void aux_role(const PrefillArgs& a, const Run& run, u
     for (int kt = from; kt < w.ke; ++kt) {
       const uint32_t u = g + kt - w.kb;
       const uint32_t s0 = slot_of(u, 3), s1 = slot_of(u, 4);
-      if (!waited(Lay::kFull + s0, round_of(u, 3)) || !waited(Lay::kFull + s1, round_of(u, 4))) return;
+      if (!waited(Lay::kRaw + (cleaned & 1), cleaned >> 1)) return;
       const uint32_t v0 = smem + Lay::ring + s0 * kSlot, v1 = smem + Lay::ring + s1 * kSlot;
       uint32_t bad[2] = {0, 0};  // keys aw * 64 + 0..31, 32..63
 #pragma unroll
@@ -772,8 +781,12 @@ __device__ __noinline__ void schedule(const PrefillArgs& a, uint8_t* scratch, Ru
 
 // After giving up: waits, bounded again, for the copies into shared memory, and a
 // millisecond for matrix products in flight (they end by themselves within microseconds).
-__device__ __noinline__ void settle(uint32_t smem, uint32_t issued, uint64_t limit) {
+__device__ __noinline__ void settle(uint32_t smem, uint32_t issued, uint32_t cleaned, uint64_t limit) {
   const uint64_t since = global_ns();
+  for (uint32_t i = cleaned > 2 ? cleaned - 2 : 0; i < cleaned; ++i)
+    while (!mbar_try_wait(smem + Lay::bars + 8 * (Lay::kRaw + (i & 1)), (i >> 1) & 1) &&
+           global_ns() - since <= limit) {
+    }
   for (uint32_t i = issued > kSlots ? issued - kSlots : 0; i < issued; ++i)
     while (!mbar_try_wait(smem + Lay::bars + 8 * (Lay::kFull + (i & (kSlots - 1))), (i / kSlots) & 1) &&
            global_ns() - since <= limit) {
@@ -806,6 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bars + 8 * (Lay::kPvDone + i), 1);
       mbar_init(bars + 8 * (Lay::kOFree + i), 4);
       mbar_init(bars + 8 * (Lay::kClean + i), kAuxWarps);
+      mbar_init(bars + 8 * (Lay::kRaw + i), 2);
     }
     mbar_fence_init();
   }
@@ -822,14 +836,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, m.tmem, 0);
-  uint32_t issued = 0;
+  uint32_t issued = 0, cleaned = 0;
   if (run.count > 0) {
     if (warp < 8) {
       softmax_role<F>(a, run, smem, tmem, wait, warp >> 2, warp & 3, lane, ws, srows);
     } else if (warp == kMmaWarp) {
       mma_role<F>(a, run, smem, tmem, wait, lane);
     } else if (warp == kLoadWarp) {
-      issued = load_role(a, maps, run, smem, wait, lane, ws);
+      issued = load_role(a, maps, run, smem, wait, lane, ws, cleaned);
     } else {
       aux_role<F>(a, run, smem, wait, warp - kAuxWarp, lane);
       asm volatile("cp.async.wait_all;" ::: "memory");
@@ -847,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   if (__builtin_expect(wait.given_up(), 0)) {
-    if (warp == kLoadWarp) settle(smem, issued, a.wait_limit_ns);
+    if (warp == kLoadWarp) settle(smem, issued, cleaned, a.wait_limit_ns);
     __syncthreads();
   }
   if (warp == kMmaWarp) tc::dealloc(tmem, Lay::kTmem);

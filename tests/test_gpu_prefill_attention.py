@@ -358,3 +358,29 @@ def test_two_graphs_with_one_workspace():
     for c, w in ((a, wa), (b, wb)):
         o = c.got()
         assert np.array_equal(o[0], w[0]) and np.array_equal(o[1], w[1])
+
+
+def test_long_items_between_others():
+    """Items of many key tiles beside short ones, several in a block's run: results by 64-bit
+    arithmetic on the device, the same bits every time, and no wait that runs out."""
+    lens = [1400, 30, 2048, 700, 257, 1111]
+    c = Call(lens, lens, 8, 8).put()
+    ref = []
+    for s, n in enumerate(lens):
+        rows = slice(c.cu_q[s], c.cu_q[s + 1])
+        q, key, v = c.dq[rows].double(), torch.cat([c.dk[rows], c.dp[rows]], -1).double(), c.dv[rows].double()
+        x = torch.einsum("the,khe->htk", q, key) * c.scale
+        x.masked_fill_(torch.ones(n, n, dtype=torch.bool, device="cuda").triu(1), -np.inf)
+        ref.append(torch.einsum("htk,khe->the", torch.softmax(x, -1), v))
+    ref = torch.cat(ref)
+    first = None
+    for _ in range(60):
+        c.run()
+        out = c.out.clone()
+        assert first is None or torch.equal(out, first)
+        first = out
+    assert int(c.err.item()) == 0
+    # weights and the result round to bf16: 2^-8 of the row's magnitude each, and of the value
+    mag = 2.0 ** -8 * (2 + 2.0 ** -6) * 4.5  # |v| stays below 4.5 in all but a few of 10^6 values
+    assert c.dv.abs().max() < 6 and (first.double() - ref).abs().max() < mag * 6 / 4.5
+    assert (first.double() - ref).norm() < 2.0 ** -8 * ref.norm()
