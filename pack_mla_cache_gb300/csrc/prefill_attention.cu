@@ -23,10 +23,10 @@
 // (128 bytes a row, 128-byte swizzle) through which K (three slots a unit) and V (two) flow by
 // TMA, a whole unit ahead of their use.
 //
-// Roles (12 warps): 4 warps per query tile compute weights, a thread a row (running maximum,
-// rescaling O only when a maximum has grown by more than 2^kGrow) and write the output; one
-// issues the products; one loads K and V; two load the queries and look after V rows that not
-// every row of an item sees: those behind the sequence are zeroed (they may hold anything),
+// Roles (12 warps): 4 warps per query tile load the queries, compute weights, a thread a row
+// (running maximum, rescaling O only when a maximum has grown by more than 2^kGrow) and write
+// the output; one per tile issues the products; one loads K and V; one looks after V rows that
+// not every row of an item sees: those behind the sequence are zeroed (they may hold anything),
 // those with a NaN or an infinity too, and noted, so that the sums of the rows that see them
 // become NaN.
 //
@@ -52,8 +52,8 @@ constexpr int kSlot = kKeys * 128;   // bytes of a ring slot
 constexpr int kSlots = 8;
 constexpr int kUnitSlots = 5;        // 3 of K, 2 of V
 constexpr int kQTile = 3 * kM * 128;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kAuxWarp = 10, kAuxWarps = 2;
-constexpr int kWarps = kAuxWarp + kAuxWarps, kThreads = kWarps * 32;
+constexpr int kMmaWarp = 8, kLoadWarp = 10;  // and one more, that looks after V
+constexpr int kWarps = 12, kThreads = kWarps * 32;
 constexpr int kMaxCtas = 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -77,9 +77,9 @@ struct Lay {
   static constexpr int ring = 2 * kQTile;
   static constexpr int flags = ring + kSlots * kSlot;  // uint32 [4 units][4]: keys with bad V rows
   static constexpr int bars = flags + 64;
-  static constexpr int kFull = 0, kEmpty = kSlots, kQFull = 2 * kSlots, kQEmpty = kQFull + 2,
-                       kSFull = kQEmpty + 2, kPFull = kSFull + 2, kPvDone = kPFull + 2,
-                       kOFree = kPvDone + 2, kClean = kOFree + 2, kRaw = kClean + 2, kBars = kRaw + 2;
+  // Two of each: of units in turn (K and V), of the query tiles; the weights' by tile and half.
+  static constexpr int kKFull = 0, kVFull = 2, kKEmpty = 4, kVEmpty = 6, kRaw = 8, kClean = 10,
+                       kQFull = 12, kSFull = 14, kPFull = 16, kPvDone = 20, kOFree = 22, kBars = 24;
   static constexpr int misc = (bars + kBars * 8 + 15) / 16 * 16;
   static constexpr int bytes = misc + 64;
   static_assert(bytes <= 232448, "shared memory of a CTA");
@@ -109,7 +109,8 @@ struct Split {
 struct Workspace {
   Split* split;  // [ctas]
   float *m, *l;  // [2 ctas][slot_rows]: reference (log2) and sum of the weights
-  float* o;      // [2 ctas][slot_rows][128]
+  float* o;      // [2 ctas][32][slot_rows][4]: 4 dims of a row lie together, so that a thread a
+                 // row writes whole lines
 };
 __host__ __device__ inline int slot_rows(int64_t num_tokens, int group) {
   const int64_t rows = num_tokens * group;
@@ -227,9 +228,6 @@ struct Walk {
 __device__ __forceinline__ uint32_t slot_of(uint32_t unit, int chunk) {
   return (unit * kUnitSlots + chunk) & (kSlots - 1);
 }
-__device__ __forceinline__ uint32_t round_of(uint32_t unit, int chunk) {
-  return (unit * kUnitSlots + chunk) / kSlots;
-}
 
 __device__ __noinline__ int cta_of(int64_t u, int64_t each, int extra) {
   const int64_t longer = (each + 1) * extra;
@@ -237,10 +235,14 @@ __device__ __noinline__ int cta_of(int64_t u, int64_t each, int extra) {
 }
 
 // ------------------------------------------------------------------ the roles
-// K and V by TMA, and where the run ends inside an item, what the join needs; returns the
-// slots filled and the units whose V is looked after.  V of such a unit completes on a barrier
-// of its own (two in turn), which the aux warps wait for: they do not follow the ring's slots
-// through the units between, and a barrier's parity tells one phase from the next only.
+// K and V by TMA, and where the run ends inside an item, what the join needs.  Returns the
+// copies begun, in K and V of a unit, and the units whose V is looked after.  V of such a unit
+// completes on a barrier of its own (two in turn), which that warp waits for: it does not follow
+// the ring through the units between, and a barrier's parity tells one phase from the next
+// only.
+//
+// The ring holds 8/5 units, so a unit's slots are those of K's last third and V of the unit two
+// before, and of the first two thirds of K of the unit before.
 __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& maps, const Run& run,
                                               uint32_t smem, const Waiter& wait, int lane,
                                               const Workspace& ws, uint32_t& cleaned) {
@@ -257,27 +259,38 @@ __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& 
 #pragma unroll 1
     for (int kt = w.kb; kt < w.ke; ++kt, ++g) {
       const int row = w.q.k0 + kt * kKeys;
-#pragma unroll
-      for (int c = 0; c < kUnitSlots; ++c) {
-        const uint32_t slot = slot_of(g, c), round = round_of(g, c);
-        if (round > 0 &&
-            !__all_sync(0xFFFFFFFFu, wait(bars + 8 * (Lay::kEmpty + slot), (round - 1) & 1)))
-          return g * kUnitSlots + c;
-        if (lane == 0) {
-          uint32_t full = bars + 8 * (Lay::kFull + slot);
-          const uint32_t dst = smem + Lay::ring + slot * kSlot;
-          if (c >= 3 && kt >= w.ragged()) {
-            mbar_arrive(full);
-            full = bars + 8 * (Lay::kRaw + (cleaned & 1));
-          }
-          mbar_arrive_expect_tx(full, kSlot);
-          if (c < 2) tc::tma_load3(dst, &maps.kn, h * maps.kn_x + 64 * c, row, h * maps.kn_z, full, policy);
-          else if (c == 2) tc::tma_load3(dst, &maps.kp, h * maps.kp_x, row, h * maps.kp_z, full, policy);
-          else tc::tma_load3(dst, &maps.v, h * maps.v_x + 64 * (c - 3), row, h * maps.v_z, full, policy);
-        }
-        __syncwarp();
+      auto dst = [&](int c) { return smem + Lay::ring + slot_of(g, c) * kSlot; };
+      auto freed = [&](int bar, uint32_t unit) {  // K (V) of that unit is read
+        return __all_sync(0xFFFFFFFFu, wait(bars + 8 * (bar + (unit & 1)), (unit >> 1) & 1));
+      };
+      const uint32_t kf = bars + 8 * (Lay::kKFull + (g & 1));
+      if (lane == 0) {
+        mbar_arrive_expect_tx(kf, 3 * kSlot);
+        tc::tma_load3(dst(0), &maps.kn, h * maps.kn_x, row, h * maps.kn_z, kf, policy);
       }
-      cleaned += kt >= w.ragged();
+      __syncwarp();
+      if (g >= 2 && !freed(Lay::kVEmpty, g - 2)) return 2 * g;
+      if (lane == 0) {
+        tc::tma_load3(dst(1), &maps.kn, h * maps.kn_x + 64, row, h * maps.kn_z, kf, policy);
+        tc::tma_load3(dst(2), &maps.kp, h * maps.kp_x, row, h * maps.kp_z, kf, policy);
+      }
+      __syncwarp();
+      if (g >= 1 && !freed(Lay::kKEmpty, g - 1)) return 2 * g + 1;
+      const bool clean = kt >= w.ragged();
+      if (lane == 0) {
+        uint32_t vf = bars + 8 * (Lay::kVFull + (g & 1));
+        if (clean) {
+          mbar_arrive(vf);
+          vf = bars + 8 * (Lay::kRaw + (cleaned & 1));
+        }
+        mbar_arrive_expect_tx(vf, 2 * kSlot);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)  // 64 keys x 64 columns each
+          tc::tma_load3(dst(3 + (k >> 1)) + (k & 1) * (kSlot / 2), &maps.v, h * maps.v_x + 64 * (k & 1),
+                        row + 64 * (k >> 1), h * maps.v_z, vf, policy);
+      }
+      __syncwarp();
+      cleaned += clean;
     }
     if (w.ke < w.tiles && lane == 0) {  // the run's last item
       const int64_t u0 = run.begin + run.count - w.ke;  // the unit of its key tile 0
@@ -286,73 +299,49 @@ __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& 
       ws.split[blockIdx.x] = Split{w.q.t0, w.row0, w.head, (int16_t)w.rows, (int16_t)(c1 - c0 + 1), c0, {}};
     }
   }
-  return g * kUnitSlots;
+  return 2 * g;
 }
 
-// The queries by asynchronous copies, and the V rows that not every row sees.  (Units looked
-// after use two barriers in turn: this role may be one unit ahead of the last look at its
-// barrier, but not two, as V of the next but one waits for the scores of the next.)
+// The V rows that not every row of an item sees.  (Units looked after use two barriers in
+// turn: this role may be one unit ahead of the last look at its barrier, but not two, as V of
+// the next but one waits for the scores of the next.)
 template <int F>
-__device__ __forceinline__ void aux_role(const PrefillArgs& a, const Run& run, uint32_t smem,
-                                         const Waiter& wait, int aw, int lane) {
+__device__ __forceinline__ void clean_role(const PrefillArgs& a, const Run& run, uint32_t smem,
+                                           const Waiter& wait, int lane) {
   const uint32_t bars = smem + Lay::bars;
-  auto waited = [&](int bar, uint32_t phase) {
-    return __all_sync(0xFFFFFFFFu, wait(bars + 8 * bar, phase & 1));
-  };
   Walk w;
   w.start(run);
-  uint32_t g = 0, used[2] = {0, 0}, cleaned = 0;
+  uint32_t g = 0, cleaned = 0;
   const int col = lane & 7;
   while (w.next(a)) {
 #pragma unroll 1
-    for (int i = 0; i < 2; ++i) {
-      if (w.end(i) <= w.kb) continue;
-      const uint32_t n = i ? used[1]++ : used[0]++;
-      if (n > 0 && !waited(Lay::kQEmpty + i, n - 1)) return;
-#pragma unroll 1
-      for (int r = aw * 4 + (lane >> 3); r < kM; r += kAuxWarps * 4) {
-        const uint32_t row = w.row0 + i * kM + r;
-        const bool ok = row < w.q.rows;
-        const uint32_t dt = ok ? a.by_group(row) : 0;
-        const int64_t t = ok ? w.q.t0 + (int)dt : 0;
-        const int64_t h = ok ? (int64_t)w.head * a.group + (int)(row - dt * a.group) : 0;
-        const uint8_t* nope = a.q_nope + t * a.qn_ts + h * a.qn_hs + col * 16;
-        const uint8_t* pe = a.q_pe + t * a.qp_ts + h * a.qp_hs + col * 16;
-        const uint32_t d = smem + Lay::q + i * kQTile + r * 128 + ((col ^ (r & 7)) << 4);
-        tc::cp_async16(d, nope, ok);
-        tc::cp_async16(d + kM * 128, nope + 128, ok);
-        tc::cp_async16(d + 2 * kM * 128, pe, ok);
-      }
-      tc::cp_async_arrive(bars + 8 * (Lay::kQFull + i));
-    }
-    const int from = max(w.kb, w.ragged());
-#pragma unroll 1
-    for (int kt = from; kt < w.ke; ++kt) {
+    for (int kt = max(w.kb, w.ragged()); kt < w.ke; ++kt) {
       const uint32_t u = g + kt - w.kb;
-      const uint32_t s0 = slot_of(u, 3), s1 = slot_of(u, 4);
-      if (!waited(Lay::kRaw + (cleaned & 1), cleaned >> 1)) return;
-      const uint32_t v0 = smem + Lay::ring + s0 * kSlot, v1 = smem + Lay::ring + s1 * kSlot;
-      uint32_t bad[2] = {0, 0};  // keys aw * 64 + 0..31, 32..63
+      if (!__all_sync(0xFFFFFFFFu, wait(bars + 8 * (Lay::kRaw + (cleaned & 1)), (cleaned >> 1) & 1)))
+        return;
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {  // 32 keys
+        const int p0 = kt * kKeys + q * 32;
+        uint32_t bad = 0;
+        if (p0 + 32 > w.least) {
+          // 64 keys to a slot: two runs of 64 columns
+          const uint32_t v0 = smem + Lay::ring + slot_of(u, 3 + (q >> 1)) * kSlot + (q & 1) * 4096;
 #pragma unroll
-      for (int n = 0; n < 16; ++n) {
-        const int key = aw * 64 + 4 * n + (lane >> 3), p = kt * kKeys + key;
-        const uint32_t off = key * 128 + col * 16;  // every column of the row, in any order
-        bool drop = p >= w.most;
-        const bool sp = any_special<F>(lds16(v0 + off)) | any_special<F>(lds16(v1 + off));
-        const uint32_t votes = __ballot_sync(0xFFFFFFFFu, sp && !drop);
-        if (votes & (0xFFu << (lane & 24)) && p >= w.least) drop = true;
+          for (int n = 0; n < 8; ++n) {
+            const int key = 4 * n + (lane >> 3), p = p0 + key;
+            const uint32_t at = v0 + key * 128 + col * 16;  // every column of the row, in any order
+            const bool sp = any_special<F>(lds16(at)) | any_special<F>(lds16(at + kSlot / 2));
+            const uint32_t votes = __ballot_sync(0xFFFFFFFFu, sp && p >= w.least && p < w.most);
+            if (p >= w.most || votes & (0xFFu << (lane & 24))) {
+              sts16(at, make_uint4(0, 0, 0, 0));
+              sts16(at + kSlot / 2, make_uint4(0, 0, 0, 0));
+            }
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (votes & (0xFFu << (8 * k)) && kt * kKeys + aw * 64 + 4 * n + k >= w.least)
-            bad[n >> 3] |= 1u << (4 * (n & 7) + k);
-        if (drop) {
-          sts16(v0 + off, make_uint4(0, 0, 0, 0));
-          sts16(v1 + off, make_uint4(0, 0, 0, 0));
+            for (int k = 0; k < 4; ++k)
+              if (votes & (0xFFu << (8 * k))) bad |= 1u << (4 * n + k);
+          }
         }
-      }
-      if (lane == 0) {
-        sts_u32(smem + Lay::flags + (u & 3) * 16 + aw * 8, bad[0]);
-        sts_u32(smem + Lay::flags + (u & 3) * 16 + aw * 8 + 4, bad[1]);
+        if (lane == 0) sts_u32(smem + Lay::flags + (u & 3) * 16 + q * 4, bad);
       }
       tc::fence_smem_async();
       __syncwarp();
@@ -378,132 +367,81 @@ __device__ __forceinline__ void issue_scores(uint32_t smem, uint32_t tmem, bool 
       tc::mma_16bit(one, d, qa + (c * kM * 128 >> 4) + 2 * k, kb + 2 * k, kId, c + k > 0);
   }
 }
-// Each half of V is a slot of its own (they may be the last and the first of the ring).
+// Half of the keys: a slot of V, MN-major (two runs of 64 columns).
 template <int F>
 __device__ __forceinline__ void issue_outputs(uint32_t smem, uint32_t tmem, bool one, int tile,
-                                              uint32_t unit, bool first) {
-  constexpr uint32_t kId = tc::instr_desc(kM, 64, false, F == kBF16, F == kBF16, true);
+                                              uint32_t unit, int half_, bool first) {
+  constexpr uint32_t kId = tc::instr_desc(kM, kV, false, F == kBF16, F == kBF16, true);
   const uint32_t i = __shfl_sync(0xFFFFFFFFu, tile, 0), g = __shfl_sync(0xFFFFFFFFu, unit, 0);
-  const uint32_t p = tmem + i * kKeys;
+  const uint32_t half = __shfl_sync(0xFFFFFFFFu, half_, 0);
+  const uint32_t p = tmem + i * kKeys + half * 32, d = tmem + Lay::kO + i * kV;
+  const uint64_t vb = tc::smem_desc(smem + Lay::ring + slot_of(g, 3 + half) * kSlot, kSlot / 2, 1024);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint64_t vb = tc::smem_desc(smem + Lay::ring + slot_of(g, 3 + h) * kSlot, 0, 1024);
-    const uint32_t d = tmem + Lay::kO + i * kV + h * 64;
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      tc::mma_16bit_ta(one, d, p + 8 * k, vb + k * (2048 >> 4), kId, k > 0 || !first);
-  }
+  for (int k = 0; k < 4; ++k)
+    tc::mma_16bit_ta(one, d, p + 8 * k, vb + k * (2048 >> 4), kId, half + k > 0 || !first);
 }
 
-// The units as the matrix products see them, one after the other over all items.
-struct Unit {
-  bool valid, clean;
-  bool act[2], first[2], last[2];
-};
-struct Units {
-  Walk w;
-  int kt;
-  __device__ __forceinline__ void start(const Run& r) {
-    w.start(r);
-    kt = w.ke = 0;
-  }
-  __device__ __forceinline__ Unit next(const PrefillArgs& a) {
-    Unit u{};
-    if (kt >= w.ke) {
-      if (!w.next(a)) return u;
-      kt = w.kb;
-    }
-    u.valid = true;
-    u.clean = kt >= w.ragged();
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      u.act[i] = kt < w.end(i);
-      u.first[i] = kt == w.kb;
-      u.last[i] = kt + 1 == w.end(i);
-    }
-    ++kt;
-    return u;
-  }
-};
-
+// A warp issues the products of one query tile, whose chain is serial: scores of a unit behind
+// the outputs of the one before, over whose weights they go.  The other tile's products fill
+// the gaps.  (One warp for both took 4900 cycles a unit, most of them its own instructions
+// between the products.)  K and V of a unit are free when both warps have said so; a warp whose
+// tile has no part in a unit says it when they have come, so that it does not run ahead.
 template <int F>
 __device__ __forceinline__ void mma_role(const PrefillArgs& a, const Run& run, uint32_t smem,
-                                         uint32_t tmem, const Waiter& waiter, int lane) {
+                                         uint32_t tmem, const Waiter& waiter, int tile, int lane) {
   const uint32_t bars = smem + Lay::bars;
+  // Looks at barriers without letting itself be suspended: waking takes long.
   auto wait = [&](int bar, uint32_t phase) {
-    return __all_sync(0xFFFFFFFFu, waiter(bars + 8 * bar, phase & 1));
+    for (int spin = 0; spin < 64; ++spin)
+      if (__any_sync(0xFFFFFFFFu, mbar_test(bars + 8 * bar, phase & 1))) return true;
+    return (bool)__all_sync(0xFFFFFFFFu, waiter(bars + 8 * bar, phase & 1));
   };
   const bool one = tc::elect();
-  Units units;
-  units.start(run);
-  uint32_t done[2] = {0, 0};    // units whose outputs were issued
-  uint32_t items[2] = {0, 0};   // items whose scores / outputs were begun
-  uint32_t opened[2] = {0, 0};
-  uint32_t cleaned = 0;
-  // Scores of tile i of unit g.
-  auto scores = [&](int i, const Unit& u, uint32_t g, bool keys) {
-    if (u.first[i]) {
-      if (!wait(Lay::kQFull + i, items[i])) return false;
-      ++items[i];
-      tc::fence_smem_async();  // the queries came by ordinary copies
-    }
-    if (keys)
-      for (int c = 0; c < 3; ++c)
-        if (!wait(Lay::kFull + slot_of(g, c), round_of(g, c))) return false;
-    tc::fence_after_sync();
-    issue_scores<F>(smem, tmem, one, i, g);
-    tc::commit(one, bars + 8 * (Lay::kSFull + i));
-    if (i == 1 || !u.act[1])
-      for (int c = 0; c < 3; ++c) tc::commit(one, bars + 8 * (Lay::kEmpty + slot_of(g, c)));
-    if (u.last[i]) tc::commit(one, bars + 8 * (Lay::kQEmpty + i));
-    return true;
-  };
-  uint32_t g = 0;
-  Unit nxt = units.next(a);
-  if (nxt.valid)
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (nxt.act[i] && !scores(i, nxt, 0, i == 0 || !nxt.act[0])) return;
+  Walk w;
+  w.start(run);
+  uint32_t g = 0, done = 0, opened = 0, cleaned = 0;
 #pragma unroll 1
-  for (;; ++g) {
-    const Unit cur = nxt;
-    if (!cur.valid) break;
-    nxt = units.next(a);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (cur.act[i]) {
-        if (!wait(Lay::kPFull + i, done[i])) return;
-        if (cur.first[i]) {
-          // the sums of the item before are read
-          if (opened[i] > 0 && !wait(Lay::kOFree + i, opened[i] - 1)) return;
-          ++opened[i];
-        }
-        if (i == 0 || !cur.act[0]) {
-          if (!wait(Lay::kFull + slot_of(g, 3), round_of(g, 3)) ||
-              !wait(Lay::kFull + slot_of(g, 4), round_of(g, 4)))
-            return;
-          if (cur.clean) {
-            if (!wait(Lay::kClean + (cleaned & 1), cleaned >> 1)) return;
-            ++cleaned;
-          }
-        }
-        tc::fence_after_sync();
-        issue_outputs<F>(smem, tmem, one, i, g, cur.first[i]);
-        tc::commit(one, bars + 8 * (Lay::kPvDone + i));
-        ++done[i];
-        if (i == 1 || !cur.act[1]) {
-          tc::commit(one, bars + 8 * (Lay::kEmpty + slot_of(g, 3)));
-          tc::commit(one, bars + 8 * (Lay::kEmpty + slot_of(g, 4)));
-        }
+  while (w.next(a)) {
+    const int e = w.end(tile);
+#pragma unroll 1
+    for (int kt = w.kb; kt < w.ke; ++kt, ++g) {
+      const bool act = kt < e;
+      if (act && kt == w.kb) {
+        if (!wait(Lay::kQFull + tile, opened)) return;
+        tc::fence_smem_async();  // the queries came by ordinary copies
       }
-      if (nxt.valid && !nxt.first[0] && nxt.act[i] && !scores(i, nxt, g + 1, i == 0 || !nxt.act[0]))
-        return;
+      if (!wait(Lay::kKFull + (g & 1), g >> 1)) return;
+      if (act) {
+        tc::fence_after_sync();
+        issue_scores<F>(smem, tmem, one, tile, g);
+        tc::commit(one, bars + 8 * (Lay::kSFull + tile));
+        tc::commit(one, bars + 8 * (Lay::kKEmpty + (g & 1)));
+      } else if (lane == 0) {
+        mbar_arrive(bars + 8 * (Lay::kKEmpty + (g & 1)));
+      }
+      if (!wait(Lay::kVFull + (g & 1), g >> 1)) return;
+      if (act) {
+        if (kt >= w.ragged()) {
+          const uint32_t n = cleaned + kt - max(w.kb, w.ragged());
+          if (!wait(Lay::kClean + (n & 1), n >> 1)) return;
+        }
+        // the sums of the item before are read
+        if (kt == w.kb && opened++ > 0 && !wait(Lay::kOFree + tile, opened)) return;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          if (!wait(Lay::kPFull + 2 * tile + h, done)) return;
+          tc::fence_after_sync();
+          issue_outputs<F>(smem, tmem, one, tile, g, h, kt == w.kb);
+        }
+        tc::commit(one, bars + 8 * (Lay::kPvDone + tile));
+        tc::commit(one, bars + 8 * (Lay::kVEmpty + (g & 1)));
+        ++done;
+      } else if (lane == 0) {
+        mbar_arrive(bars + 8 * (Lay::kVEmpty + (g & 1)));
+      }
+      __syncwarp();
     }
-    // another item: its queries may have to wait for, the outputs above not
-    if (nxt.valid && nxt.first[0])
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (nxt.act[i] && !scores(i, nxt, g + 1, i == 0 || !nxt.act[0])) return;
+    cleaned += w.cleaned();
   }
 }
 
@@ -523,7 +461,30 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// Weights and output of one query tile; a thread has a row.
+// The queries of a tile by asynchronous copies, by the tile's four warps.
+__device__ __forceinline__ void load_queries(const PrefillArgs& a, const Walk& w, uint32_t smem,
+                                             int tile, int w4, int lane) {
+  const int col = lane & 7;
+#pragma unroll 1
+  for (int r = w4 * 32 + (lane >> 3); r < w4 * 32 + 32; r += 4) {
+    const uint32_t row = w.row0 + tile * kM + r;
+    const bool ok = row < w.q.rows;
+    const uint32_t dt = ok ? a.by_group(row) : 0;
+    const int64_t t = ok ? w.q.t0 + (int)dt : 0;
+    const int64_t h = ok ? (int64_t)w.head * a.group + (int)(row - dt * a.group) : 0;
+    const uint8_t* nope = a.q_nope + t * a.qn_ts + h * a.qn_hs + col * 16;
+    const uint8_t* pe = a.q_pe + t * a.qp_ts + h * a.qp_hs + col * 16;
+    const uint32_t d = smem + Lay::q + tile * kQTile + r * 128 + ((col ^ (r & 7)) << 4);
+    tc::cp_async16(d, nope, ok);
+    tc::cp_async16(d + kM * 128, nope + 128, ok);
+    tc::cp_async16(d + 2 * kM * 128, pe, ok);
+  }
+  tc::cp_async_arrive(smem + Lay::bars + 8 * (Lay::kQFull + tile));
+}
+
+// Weights and output of one query tile; a thread has a row.  Its queries' place is free when
+// the item's last scores have come: those of the next item are asked for before the output of
+// this one is written.
 template <int F>
 __device__ __forceinline__ void softmax_role(const PrefillArgs& a, const Run& run, uint32_t smem,
                                              uint32_t tmem, const Waiter& waiter, int tile, int w4,
@@ -540,8 +501,10 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, const Run& ru
   Walk w;
   w.start(run);
   uint32_t n = 0, g = 0, cleaned = 0;
+  bool more = w.next(a);
+  if (more && w.end(tile) > w.kb) load_queries(a, w, smem, tile, w4, lane);
 #pragma unroll 1
-  while (w.next(a)) {
+  while (more) {
     const int e = w.end(tile), mine = w.rows - tile * kM;  // rows of this tile (or less than 0)
     const bool live = w4 * 32 < mine;  // this warp has rows
     const uint32_t row = w.row0 + tile * kM + r;
@@ -619,37 +582,49 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, const Run& ru
         }
         const float m0 = mu == -INFINITY ? 0.0f : -mu;
         const uint64_t c2 = f2(cs, cs), m2 = f2(m0, m0);
-        uint64_t sum[4] = {0, 0, 0, 0};
+        uint64_t sum[2] = {0, 0};
         uint32_t* pk = reinterpret_cast<uint32_t*>(x);
 #pragma unroll
-        for (int j = 0; j < kKeys / 2; ++j) {
-          const float2 y = unf2(fma2(f2(x[2 * j], x[2 * j + 1]), c2, m2));
-          const float p0 = ex2(y.x), p1 = ex2(y.y);
-          sum[j & 3] = add2(sum[j & 3], f2(p0, p1));
-          pk[j] = pack16x2<F>(p0, p1);
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int j = 32 * h; j < 32 * h + 32; ++j) {
+            const float2 y = unf2(fma2(f2(x[2 * j], x[2 * j + 1]), c2, m2));
+            const float p0 = ex2(y.x), p1 = ex2(y.y);
+            sum[j & 1] = add2(sum[j & 1], f2(p0, p1));
+            pk[j] = pack16x2<F>(p0, p1);
+          }
+          tc::st_32x32(s_at + 32 * h, pk + 32 * h);
+          tc::wait_st();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars + 8 * (Lay::kPFull + 2 * tile + h));
         }
-        tc::st_32x32(s_at, pk);
-        tc::st_32x32(s_at + 32, pk + 32);
-        const float2 t = unf2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+        const float2 t = unf2(add2(sum[0], sum[1]));
         l += t.x + t.y;
-        tc::wait_st();
+      } else {
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane < 2) mbar_arrive(bars + 8 * (Lay::kPFull + 2 * tile + lane));
       }
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + 8 * (Lay::kPFull + tile));
     }
     // ---- the end of this CTA's part of the item
-    const bool any = e > w.kb;
+    const Walk past = w;
+    g += w.ke - w.kb;
+    cleaned += w.cleaned();
+    more = w.next(a);
+    if (more && w.end(tile) > w.kb) load_queries(a, w, smem, tile, w4, lane);
+    const bool any = e > past.kb;
     if (any) {
       if (!wait(Lay::kPvDone + tile, n - 1)) return;
       tc::fence_after_sync();
     }
     if (live) {
-      const bool whole = w.kb == 0 && w.ke == w.tiles;
-      const int64_t slot = 2 * (int64_t)blockIdx.x + (w.kb == 0 ? 1 : 0);
+      const bool whole = past.kb == 0 && past.ke == past.tiles;
+      const int64_t slot = 2 * (int64_t)blockIdx.x + (past.kb == 0 ? 1 : 0);
       const int64_t at = slot * srows + tile * kM + r;
+      float* part = ws.o + slot * srows * kV + (tile * kM + r) * 4;  // [dims / 4][rows][4]
       const uint32_t dt = a.by_group(row);
-      const int64_t t = w.q.t0 + (int)dt, h = (int64_t)w.head * a.group + (int)(row - dt * a.group);
+      const int64_t t = past.q.t0 + (int)dt, h = (int64_t)past.head * a.group + (int)(row - dt * a.group);
       if (ok && !whole) {
         ws.m[at] = mu;
         ws.l[at] = l;
@@ -677,7 +652,7 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, const Run& ru
           } else {
 #pragma unroll
             for (int j = 0; j < 32; j += 4)
-              st16(ws.o + at * kV + k + j, make_uint4(y[j], y[j + 1], y[j + 2], y[j + 3]));
+              st16(part + (int64_t)(k + j) * srows, make_uint4(y[j], y[j + 1], y[j + 2], y[j + 3]));
           }
         }
       }
@@ -687,8 +662,6 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, const Run& ru
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + 8 * (Lay::kOFree + tile));
     }
-    g += w.ke - w.kb;
-    cleaned += w.cleaned();
   }
 }
 
@@ -787,8 +760,9 @@ __device__ __noinline__ void settle(uint32_t smem, uint32_t issued, uint32_t cle
     while (!mbar_try_wait(smem + Lay::bars + 8 * (Lay::kRaw + (i & 1)), (i >> 1) & 1) &&
            global_ns() - since <= limit) {
     }
-  for (uint32_t i = issued > kSlots ? issued - kSlots : 0; i < issued; ++i)
-    while (!mbar_try_wait(smem + Lay::bars + 8 * (Lay::kFull + (i & (kSlots - 1))), (i / kSlots) & 1) &&
+  for (uint32_t i = issued > 4 ? issued - 4 : 0; i < issued; ++i)
+    while (!mbar_try_wait(smem + Lay::bars + 8 * ((i & 1 ? Lay::kVFull : Lay::kKFull) + ((i >> 1) & 1)),
+                          (i >> 2) & 1) &&
            global_ns() - since <= limit) {
     }
   while (global_ns() - since <= 1000000) {
@@ -806,20 +780,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     m.abort = 0;
     const uint32_t bars = smem + Lay::bars;
-    for (int i = 0; i < kSlots; ++i) {
-      const bool stall = blockIdx.x == 0 && a.stall_stage == i + 1;  // one arrival too many
-      mbar_init(bars + 8 * (Lay::kFull + i), stall ? 2 : 1);
-      mbar_init(bars + 8 * (Lay::kEmpty + i), 1);
-    }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bars + 8 * (Lay::kQFull + i), kAuxWarps * 32);
-      mbar_init(bars + 8 * (Lay::kQEmpty + i), 1);
+      auto stall = [&](int n) { return blockIdx.x == 0 && a.stall_stage == n ? 1 : 0; };
+      mbar_init(bars + 8 * (Lay::kKFull + i), 1 + stall(i + 1));  // (one arrival too many)
+      mbar_init(bars + 8 * (Lay::kVFull + i), 1 + stall(i + 3));
+      mbar_init(bars + 8 * (Lay::kKEmpty + i), 2);
+      mbar_init(bars + 8 * (Lay::kVEmpty + i), 2);
+      mbar_init(bars + 8 * (Lay::kRaw + i), 1);
+      mbar_init(bars + 8 * (Lay::kClean + i), 1);
+      mbar_init(bars + 8 * (Lay::kQFull + i), kM);
       mbar_init(bars + 8 * (Lay::kSFull + i), 1);
-      mbar_init(bars + 8 * (Lay::kPFull + i), 4);
+      mbar_init(bars + 8 * (Lay::kPFull + 2 * i), 4);
+      mbar_init(bars + 8 * (Lay::kPFull + 2 * i + 1), 4);
       mbar_init(bars + 8 * (Lay::kPvDone + i), 1);
       mbar_init(bars + 8 * (Lay::kOFree + i), 4);
-      mbar_init(bars + 8 * (Lay::kClean + i), kAuxWarps);
-      mbar_init(bars + 8 * (Lay::kRaw + i), 2);
     }
     mbar_fence_init();
   }
@@ -840,13 +814,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (run.count > 0) {
     if (warp < 8) {
       softmax_role<F>(a, run, smem, tmem, wait, warp >> 2, warp & 3, lane, ws, srows);
-    } else if (warp == kMmaWarp) {
-      mma_role<F>(a, run, smem, tmem, wait, lane);
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp < kLoadWarp) {
+      mma_role<F>(a, run, smem, tmem, wait, warp - kMmaWarp, lane);
     } else if (warp == kLoadWarp) {
       issued = load_role(a, maps, run, smem, wait, lane, ws, cleaned);
     } else {
-      aux_role<F>(a, run, smem, wait, warp - kAuxWarp, lane);
-      asm volatile("cp.async.wait_all;" ::: "memory");
+      clean_role<F>(a, run, smem, wait, lane);
     }
   }
   __syncwarp();
@@ -868,8 +842,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // -------------------------------------------------------- join of the split items
-// Block (x, c) looks at what CTA c left.  The rows of an item of `parts` CTAs are dealt to
-// the warps of the blocks of all of them but the last; a lane has four dims.
+// Block (x, c) looks at what CTA c left.  An item of `parts` CTAs is dealt to the warps of the
+// blocks of all of them but the last: 8 rows x 16 dims a warp, a lane four dims of a row.
 constexpr int kJoinWarps = 8, kJoinBlocks = 8;
 
 template <int F>
@@ -882,7 +856,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefill_join_kernel(const Pre
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int stride = (sp.parts - 1) * kJoinBlocks * kJoinWarps;
   for (int n = (((int)blockIdx.y - sp.first) * kJoinBlocks + (int)blockIdx.x) * kJoinWarps + warp;
-       n < sp.rows; n += stride) {
+       n < (sp.rows + 7) / 8 * 8; n += stride) {
+    const int r = (n >> 3) * 8 + (lane & 7), quad = (n & 7) * 4 + (lane >> 3);
+    if (r >= sp.rows) continue;
     float4 acc = make_float4(0, 0, 0, 0);
     float sum = 0.0f, top = -INFINITY;
     // the first partial lies in the odd slot of the first CTA, the others in the even ones behind
@@ -892,14 +868,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefill_join_kernel(const Pre
       float lv[4], mv[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int64_t at = (2 * (int64_t)(sp.first + i + k) + (i + k == 0 ? 1 : 0)) * srows + n;
+        const int64_t slot = 2 * (int64_t)(sp.first + i + k) + (i + k == 0 ? 1 : 0);
         lv[k] = 0.0f;
         mv[k] = -INFINITY;
         v[k] = make_float4(0, 0, 0, 0);
         if (i + k < sp.parts) {
-          lv[k] = ws.l[at];
-          mv[k] = ws.m[at];
-          v[k] = __ldcs(reinterpret_cast<const float4*>(ws.o + at * kV) + lane);
+          lv[k] = ws.l[slot * srows + r];
+          mv[k] = ws.m[slot * srows + r];
+          v[k] = __ldcs(reinterpret_cast<const float4*>(ws.o + slot * srows * kV) + quad * srows + r);
         }
       }
 #pragma unroll
@@ -915,22 +891,22 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefill_join_kernel(const Pre
         top = m;
       }
     }
-    const uint32_t row = sp.row0 + n, dt = a.by_group(row);
+    const uint32_t row = sp.row0 + r, dt = a.by_group(row);
     const int64_t t = sp.tok0 + (int)dt, h = (int64_t)sp.head * a.group + (int)(row - dt * a.group);
     const float inv = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
-    st8(a.out + t * a.out_ts + h * a.out_hs + lane * 8,
+    st8(a.out + t * a.out_ts + h * a.out_hs + quad * 8,
         make_uint2(pack16x2<F>(acc.x * inv, acc.y * inv), pack16x2<F>(acc.z * inv, acc.w * inv)));
-    if (lane == 0 && a.lse)
+    if (quad == 0 && a.lse)
       a.lse[t * a.lse_ts + h * a.lse_hs] = sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * kLn2;
   }
 }
 
 // ------------------------------------------------------------------ launches
-// Rows of keys (or values) of all heads as a tensor map with boxes of `cols` columns and 128
-// rows.  Heads inside a row are columns of it, so that any head stride does; otherwise (heads
+// Rows of keys (or values) of all heads as a tensor map with boxes of 64 columns and
+// `box_rows` rows.  Heads inside a row are columns of it, so that any head stride does; otherwise (heads
 // apart) the third dimension.  `base` stands in for arrays without rows.
 bool make_map(CUtensorMap* map, const void* base, int fmt, int width, int64_t hs, int heads, int64_t ts,
-              int64_t rows, int32_t* x_head, int32_t* z_head) {
+              int64_t rows, int box_rows, int32_t* x_head, int32_t* z_head) {
   const TensorMapEncode encode = tensor_map_encode();
   if (!encode) return false;
   const int es = is16(fmt) ? 2 : 1;
@@ -950,7 +926,7 @@ bool make_map(CUtensorMap* map, const void* base, int fmt, int width, int64_t hs
     }
   }
   if (dims[0] > INT32_MAX) return false;
-  const cuuint32_t box[3] = {64, (cuuint32_t)kKeys, 1}, unit[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, unit[3] = {1, 1, 1};
   const CUtensorMapDataType type =
       fmt == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   return encode(map, type, 3, const_cast<void*>(base), dims, strides, box, unit,
@@ -964,11 +940,12 @@ cudaError_t launch_tc(const PrefillArgs& a, int ctas, const LaunchCfg& cfg) {
   const bool none = a.num_kv == 0;
   const int64_t rows = none ? 1 : a.num_kv;
   const int heads = none ? 1 : a.kv_heads;
-  if (!make_map(&maps.kn, none ? a.q_nope : a.k_nope, F, 128, a.kn_hs, heads, a.kn_ts, rows, &maps.kn_x,
-                &maps.kn_z) ||
-      !make_map(&maps.kp, none ? a.q_nope : a.k_pe, F, 64, a.kp_hs, heads, a.kp_ts, rows, &maps.kp_x,
-                &maps.kp_z) ||
-      !make_map(&maps.v, none ? a.q_nope : a.v, F, 128, a.v_hs, heads, a.v_ts, rows, &maps.v_x, &maps.v_z))
+  if (!make_map(&maps.kn, none ? a.q_nope : a.k_nope, F, 128, a.kn_hs, heads, a.kn_ts, rows, kKeys,
+                &maps.kn_x, &maps.kn_z) ||
+      !make_map(&maps.kp, none ? a.q_nope : a.k_pe, F, 64, a.kp_hs, heads, a.kp_ts, rows, kKeys,
+                &maps.kp_x, &maps.kp_z) ||
+      !make_map(&maps.v, none ? a.q_nope : a.v, F, 128, a.v_hs, heads, a.v_ts, rows, kKeys / 2,
+                &maps.v_x, &maps.v_z))
     return cudaErrorInvalidValue;
   auto kern = prefill_attention_kernel<F>;
   // the attribute stays with the device's context: set on a device's first call
