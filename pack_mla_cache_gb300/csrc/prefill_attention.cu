@@ -23,9 +23,9 @@
 // (128 bytes a row, 128-byte swizzle) through which K (three slots a unit) and V (two) flow by
 // TMA, a whole unit ahead of their use.
 //
-// Roles (12 warps): 4 warps per query tile load the queries, compute weights, a thread a row
-// (running maximum, rescaling O only when a maximum has grown by more than 2^kGrow) and write
-// the output; one per tile issues the products; one loads K and V; one looks after V rows that
+// Roles (20 warps): 8 warps per query tile load the queries, compute weights, two threads a row
+// (64 columns each; running maximum, rescaling O only when a maximum has grown by more than
+// 2^kGrow) and write the output; one per tile issues the products; one loads K and V; one looks after V rows that
 // not every row of an item sees: those behind the sequence are zeroed (they may hold anything),
 // those with a NaN or an infinity too, and noted, so that the sums of the rows that see them
 // become NaN.
@@ -52,8 +52,8 @@ constexpr int kSlot = kKeys * 128;   // bytes of a ring slot
 constexpr int kSlots = 8;
 constexpr int kUnitSlots = 5;        // 3 of K, 2 of V
 constexpr int kQTile = 3 * kM * 128;
-constexpr int kMmaWarp = 8, kLoadWarp = 10;  // and one more, that looks after V
-constexpr int kWarps = 12, kThreads = kWarps * 32;
+constexpr int kMmaWarp = 16, kLoadWarp = 18;  // and one more, that looks after V
+constexpr int kWarps = 20, kThreads = kWarps * 32;
 constexpr int kMaxCtas = 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -75,11 +75,13 @@ struct Ref {
 struct Lay {
   static constexpr int q = 0;
   static constexpr int ring = 2 * kQTile;
-  static constexpr int flags = ring + kSlots * kSlot;  // uint32 [4 units][4]: keys with bad V rows
+  static constexpr int red = ring + kSlots * kSlot;  // float [8 pairs of warps][2][32]
+  static constexpr int flags = red + 2048;           // uint32 [4 units][4]: keys with bad V rows
   static constexpr int bars = flags + 64;
   // Two of each: of units in turn (K and V), of the query tiles; the weights' by tile and half.
   static constexpr int kKFull = 0, kVFull = 2, kKEmpty = 4, kVEmpty = 6, kRaw = 8, kClean = 10,
-                       kQFull = 12, kSFull = 14, kPFull = 16, kPvDone = 20, kOFree = 22, kBars = 24;
+                       kQFull = 12, kSFull = 14, kPFull = 16, kOFull = 18, kOFree = 20, kTurn = 22,
+                       kBars = 24;
   static constexpr int misc = (bars + kBars * 8 + 15) / 16 * 16;
   static constexpr int bytes = misc + 64;
   static_assert(bytes <= 232448, "shared memory of a CTA");
@@ -89,7 +91,9 @@ struct Lay {
 struct Misc {
   uint32_t tmem;
   uint32_t abort;
+  uint8_t left[16];  // a weights' warp that has given up, for its partner
 };
+static_assert(sizeof(Misc) <= 64, "Misc fits");
 
 // How a tensor map reads row p, columns c.. of key head g: box (x_head * g + c, p, z_head * g).
 struct Maps {
@@ -259,6 +263,7 @@ __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& 
 #pragma unroll 1
     for (int kt = w.kb; kt < w.ke; ++kt, ++g) {
       const int row = w.q.k0 + kt * kKeys;
+      const bool clean = kt >= w.ragged();
       auto dst = [&](int c) { return smem + Lay::ring + slot_of(g, c) * kSlot; };
       auto freed = [&](int bar, uint32_t unit) {  // K (V) of that unit is read
         return __all_sync(0xFFFFFFFFu, wait(bars + 8 * (bar + (unit & 1)), (unit >> 1) & 1));
@@ -276,7 +281,6 @@ __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& 
       }
       __syncwarp();
       if (g >= 1 && !freed(Lay::kKEmpty, g - 1)) return 2 * g + 1;
-      const bool clean = kt >= w.ragged();
       if (lane == 0) {
         uint32_t vf = bars + 8 * (Lay::kVFull + (g & 1));
         if (clean) {
@@ -354,8 +358,8 @@ __device__ __forceinline__ void clean_role(const PrefillArgs& a, const Run& run,
 
 template <int F>
 __device__ __forceinline__ void issue_scores(uint32_t smem, uint32_t tmem, bool one, int tile,
-                                             uint32_t unit) {
-  constexpr uint32_t kId = tc::instr_desc(kM, kKeys, false, F == kBF16, F == kBF16);
+                                             uint32_t unit, uint32_t negate) {
+  const uint32_t id = negate | tc::instr_desc(kM, kKeys, false, F == kBF16, F == kBF16);
   const uint32_t i = __shfl_sync(0xFFFFFFFFu, tile, 0), g = __shfl_sync(0xFFFFFFFFu, unit, 0);
   const uint64_t qa = tc::smem_desc(smem + Lay::q + i * kQTile, 0, 1024);
   const uint32_t d = tmem + i * kKeys;
@@ -364,28 +368,32 @@ __device__ __forceinline__ void issue_scores(uint32_t smem, uint32_t tmem, bool 
     const uint64_t kb = tc::smem_desc(smem + Lay::ring + slot_of(g, c) * kSlot, 0, 1024);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      tc::mma_16bit(one, d, qa + (c * kM * 128 >> 4) + 2 * k, kb + 2 * k, kId, c + k > 0);
+      tc::mma_16bit(one, d, qa + (c * kM * 128 >> 4) + 2 * k, kb + 2 * k, id, c + k > 0);
   }
 }
-// Half of the keys: a slot of V, MN-major (two runs of 64 columns).
+// V MN-major (two runs of 64 columns), half of the keys a slot.
 template <int F>
 __device__ __forceinline__ void issue_outputs(uint32_t smem, uint32_t tmem, bool one, int tile,
-                                              uint32_t unit, int half_, bool first) {
+                                              uint32_t unit, bool first) {
   constexpr uint32_t kId = tc::instr_desc(kM, kV, false, F == kBF16, F == kBF16, true);
   const uint32_t i = __shfl_sync(0xFFFFFFFFu, tile, 0), g = __shfl_sync(0xFFFFFFFFu, unit, 0);
-  const uint32_t half = __shfl_sync(0xFFFFFFFFu, half_, 0);
-  const uint32_t p = tmem + i * kKeys + half * 32, d = tmem + Lay::kO + i * kV;
-  const uint64_t vb = tc::smem_desc(smem + Lay::ring + slot_of(g, 3 + half) * kSlot, kSlot / 2, 1024);
+  const uint32_t p = tmem + i * kKeys, d = tmem + Lay::kO + i * kV;
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    tc::mma_16bit_ta(one, d, p + 8 * k, vb + k * (2048 >> 4), kId, half + k > 0 || !first);
+  for (int h = 0; h < 2; ++h) {
+    const uint64_t vb = tc::smem_desc(smem + Lay::ring + slot_of(g, 3 + h) * kSlot, kSlot / 2, 1024);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      tc::mma_16bit_ta(one, d, p + h * 32 + 8 * k, vb + k * (2048 >> 4), kId, h + k > 0 || !first);
+  }
 }
 
 // A warp issues the products of one query tile, whose chain is serial: scores of a unit behind
-// the outputs of the one before, over whose weights they go.  The other tile's products fill
-// the gaps.  (One warp for both took 4900 cycles a unit, most of them its own instructions
-// between the products.)  K and V of a unit are free when both warps have said so; a warp whose
-// tile has no part in a unit says it when they have come, so that it does not run ahead.
+// the outputs of the one before, over whose weights they go.  The two warps take turns, so that
+// a tile's weights are computed while the other's products run.  (One warp for both took 4900
+// cycles a unit, most of them its own instructions between the products; two without turns 4600,
+// both tiles waiting for the tensor core and for their weights at the same times.)  K and V of a
+// unit are free when both warps have said so; a warp whose tile has no part in a unit says it
+// when they have come, so that it does not run ahead.
 template <int F>
 __device__ __forceinline__ void mma_role(const PrefillArgs& a, const Run& run, uint32_t smem,
                                          uint32_t tmem, const Waiter& waiter, int tile, int lane) {
@@ -397,48 +405,54 @@ __device__ __forceinline__ void mma_role(const PrefillArgs& a, const Run& run, u
     return (bool)__all_sync(0xFFFFFFFFu, waiter(bars + 8 * bar, phase & 1));
   };
   const bool one = tc::elect();
+  const uint32_t negate = a.softmax_scale < 0.0f ? 1u << 13 : 0u;  // of the scores, by the tensor core
   Walk w;
   w.start(run);
   uint32_t g = 0, done = 0, opened = 0, cleaned = 0;
 #pragma unroll 1
   while (w.next(a)) {
-    const int e = w.end(tile);
+    const int e = w.end(tile), from = max(w.kb, w.ragged());
+    if (e > w.kb) {
+      if (!wait(Lay::kQFull + tile, opened)) return;
+      tc::fence_smem_async();  // the queries came by ordinary copies
+    }
 #pragma unroll 1
     for (int kt = w.kb; kt < w.ke; ++kt, ++g) {
       const bool act = kt < e;
-      if (act && kt == w.kb) {
-        if (!wait(Lay::kQFull + tile, opened)) return;
-        tc::fence_smem_async();  // the queries came by ordinary copies
-      }
-      if (!wait(Lay::kKFull + (g & 1), g >> 1)) return;
-      if (act) {
-        tc::fence_after_sync();
-        issue_scores<F>(smem, tmem, one, tile, g);
-        tc::commit(one, bars + 8 * (Lay::kSFull + tile));
+      // the scores of the item's first unit; the others' follow the outputs before, below
+      if (kt == w.kb) {
+        if (!wait(Lay::kKFull + (g & 1), g >> 1)) return;
+        if (act) {
+          tc::fence_after_sync();
+          issue_scores<F>(smem, tmem, one, tile, g, negate);
+          tc::commit(one, bars + 8 * (Lay::kSFull + tile));
+        }
         tc::commit(one, bars + 8 * (Lay::kKEmpty + (g & 1)));
-      } else if (lane == 0) {
-        mbar_arrive(bars + 8 * (Lay::kKEmpty + (g & 1)));
       }
+      // All that is usually there is asked for before the weights, which are not.
+      const uint32_t n = cleaned + kt - from;
       if (!wait(Lay::kVFull + (g & 1), g >> 1)) return;
       if (act) {
-        if (kt >= w.ragged()) {
-          const uint32_t n = cleaned + kt - max(w.kb, w.ragged());
-          if (!wait(Lay::kClean + (n & 1), n >> 1)) return;
-        }
+        if (kt >= from && !wait(Lay::kClean + (n & 1), n >> 1)) return;
         // the sums of the item before are read
         if (kt == w.kb && opened++ > 0 && !wait(Lay::kOFree + tile, opened)) return;
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          if (!wait(Lay::kPFull + 2 * tile + h, done)) return;
-          tc::fence_after_sync();
-          issue_outputs<F>(smem, tmem, one, tile, g, h, kt == w.kb);
-        }
-        tc::commit(one, bars + 8 * (Lay::kPvDone + tile));
-        tc::commit(one, bars + 8 * (Lay::kVEmpty + (g & 1)));
-        ++done;
-      } else if (lane == 0) {
-        mbar_arrive(bars + 8 * (Lay::kVEmpty + (g & 1)));
       }
+      if (tile + g > 0 && !wait(Lay::kTurn + tile, tile ? g : g - 1)) return;
+      if (act) {
+        if (!wait(Lay::kPFull + tile, done++)) return;
+        tc::fence_after_sync();
+        issue_outputs<F>(smem, tmem, one, tile, g, kt == w.kb);
+        if (kt + 1 == e) tc::commit(one, bars + 8 * (Lay::kOFull + tile));
+      }
+      tc::commit(one, bars + 8 * (Lay::kVEmpty + (g & 1)));
+      if (kt + 1 < w.ke && !wait(Lay::kKFull + ((g + 1) & 1), (g + 1) >> 1)) return;
+      if (kt + 1 < e) {
+        tc::fence_after_sync();
+        issue_scores<F>(smem, tmem, one, tile, g + 1, negate);
+        tc::commit(one, bars + 8 * (Lay::kSFull + tile));
+      }
+      if (kt + 1 < w.ke) tc::commit(one, bars + 8 * (Lay::kKEmpty + ((g + 1) & 1)));
+      if (lane == 0) mbar_arrive(bars + 8 * (Lay::kTurn + (tile ^ 1)));
       __syncwarp();
     }
     cleaned += w.cleaned();
@@ -455,18 +469,28 @@ __device__ __forceinline__ uint32_t pack16x2(float lo, float hi) {
   if constexpr (F == kF16) return pack_f16x2(lo, hi);
   else return pack_bf16x2(lo, hi);
 }
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
+// A barrier of the two warps that share 32 rows of a tile, and whether x holds in any of their
+// threads.
+__device__ __forceinline__ void pair_sync(int pair) {
+  asm volatile("bar.sync %0, 64;" ::"r"(1 + pair) : "memory");
+}
+__device__ __forceinline__ bool pair_any(int pair, bool x) {
+  uint32_t any;
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.u32 q, %2, 0;\n"
+      "  barrier.cta.red.or.pred p, %1, 64, q; selp.u32 %0, 1, 0, p; }"
+      : "=r"(any)
+      : "r"(1 + pair), "r"(x ? 1u : 0u)
+      : "memory");
+  return any != 0;
 }
 
-// The queries of a tile by asynchronous copies, by the tile's four warps.
+// The queries of a tile by asynchronous copies, 16 rows by each of its eight warps.
 __device__ __forceinline__ void load_queries(const PrefillArgs& a, const Walk& w, uint32_t smem,
-                                             int tile, int w4, int lane) {
+                                             int tile, int warp8, int lane) {
   const int col = lane & 7;
 #pragma unroll 1
-  for (int r = w4 * 32 + (lane >> 3); r < w4 * 32 + 32; r += 4) {
+  for (int r = warp8 * 16 + (lane >> 3); r < warp8 * 16 + 16; r += 4) {
     const uint32_t row = w.row0 + tile * kM + r;
     const bool ok = row < w.q.rows;
     const uint32_t dt = ok ? a.by_group(row) : 0;
@@ -482,95 +506,87 @@ __device__ __forceinline__ void load_queries(const PrefillArgs& a, const Walk& w
   tc::cp_async_arrive(smem + Lay::bars + 8 * (Lay::kQFull + tile));
 }
 
-// Weights and output of one query tile; a thread has a row.  Its queries' place is free when
-// the item's last scores have come: those of the next item are asked for before the output of
-// this one is written.
+// Weights and output of one query tile: a thread has a row's keys 64 half .. of a key tile (and
+// dims 64 half .. of the output), its partner in another warp the others.  One warp for 32 whole
+// rows took 2300 cycles a tile, mostly waiting for its own instructions.  The queries' place is
+// free when the item's last scores have come: those of the next item are asked for before the
+// output of this one is written.
 template <int F>
 __device__ __forceinline__ void softmax_role(const PrefillArgs& a, const Run& run, uint32_t smem,
-                                             uint32_t tmem, const Waiter& waiter, int tile, int w4,
-                                             int lane, const Workspace& ws, int srows) {
+                                             uint32_t tmem, const Waiter& waiter, int warp, int lane,
+                                             const Workspace& ws, int srows, Misc& misc) {
   using R = Ref<F>;
+  constexpr int kC = kKeys / 2;
+  const int tile = warp >> 3, half = (warp >> 2) & 1, w4 = warp & 3, pair = tile * 4 + w4;
   const uint32_t bars = smem + Lay::bars;
   auto wait = [&](int bar, uint32_t phase) {
     return __all_sync(0xFFFFFFFFu, waiter(bars + 8 * bar, phase & 1));
   };
   const uint32_t s_at = tmem + tile * kKeys + ((uint32_t)(w4 * 32) << 16);
-  const uint32_t o_at = tmem + Lay::kO + tile * kV + ((uint32_t)(w4 * 32) << 16);
-  const float c = a.softmax_scale * kLog2e;
+  const uint32_t o_at = tmem + Lay::kO + tile * kV + half * 64 + ((uint32_t)(w4 * 32) << 16);
+  const float c = fabsf(a.softmax_scale) * kLog2e;  // (the scores have its sign)
   const int r = w4 * 32 + lane;
+  const uint32_t red = smem + Lay::red + (pair * 2 + half) * 128 + lane * 4;  // partner: ^ 128
+  volatile uint8_t* left = misc.left + pair * 2;
   Walk w;
   w.start(run);
-  uint32_t n = 0, g = 0, cleaned = 0;
+  uint32_t n = 0, g = 0, cleaned = 0, items = 0;
   bool more = w.next(a);
-  if (more && w.end(tile) > w.kb) load_queries(a, w, smem, tile, w4, lane);
+  if (more && w.end(tile) > w.kb) load_queries(a, w, smem, tile, warp & 7, lane);
 #pragma unroll 1
   while (more) {
     const int e = w.end(tile), mine = w.rows - tile * kM;  // rows of this tile (or less than 0)
     const bool live = w4 * 32 < mine;  // this warp has rows
     const uint32_t row = w.row0 + tile * kM + r;
     const bool ok = r < mine;
-    const int seen = ok ? seen_of(a, w.q, row) : 0;
+    const int seen = ok ? seen_of(a, w.q, row) - half * kC : 0;
     const int from = max(w.kb, w.ragged());
     float mu = -INFINITY, l = 0.0f;
 #pragma unroll 1
     for (int kt = w.kb; kt < e; ++kt, ++n) {
-      if (!wait(Lay::kSFull + tile, n)) return;
+      bool fine = wait(Lay::kSFull + tile, n);
       tc::fence_after_sync();
       if (live) {
-        float x[kKeys];
-        tc::ld_32x128(s_at, reinterpret_cast<uint32_t*>(x));
+        float x[kC];
+        tc::ld_32x64(s_at + half * kC, reinterpret_cast<uint32_t*>(x));
         float cs = c;
         if (__builtin_expect(kt >= from, 0)) {
-          const uint32_t n = cleaned + kt - from;
-          if (!wait(Lay::kClean + (n & 1), n >> 1)) return;
+          const uint32_t nc = cleaned + kt - from;
+          fine &= wait(Lay::kClean + (nc & 1), nc >> 1);
           const int lim = seen - kt * kKeys;
-          const uint32_t at = smem + Lay::flags + ((g + kt - w.kb) & 3) * 16;
+          const uint32_t at = smem + Lay::flags + ((g + kt - w.kb) & 3) * 16 + half * 8;
           bool bad = false;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < 2; ++k) {
             const int below = min(max(lim - 32 * k, 0), 32);
             bad |= (lds_u32(at + 4 * k) & (below == 32 ? 0xFFFFFFFFu : (1u << below) - 1)) != 0;
           }
           if (bad) l = NAN;
 #pragma unroll
-          for (int j = 0; j < kKeys; ++j) x[j] = j < lim ? x[j] * c : -INFINITY;
+          for (int j = 0; j < kC; ++j) x[j] = j < lim ? x[j] * c : -INFINITY;
           cs = 1.0f;
         }
-        float top;
-        {
-          float t[8];
-          if (cs >= 0.0f) {
+        float t[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) t[j] = fmaxf(x[j], x[j + 8]);
+        for (int j = 4; j < kC; j += 8)
 #pragma unroll
-            for (int j = 16; j < kKeys; j += 16)
-#pragma unroll
-              for (int k = 0; k < 8; ++k) t[k] = fmaxf(t[k], fmaxf(x[j + k], x[j + k + 8]));
-            top = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])),
-                        fmaxf(fmaxf(t[4], t[5]), fmaxf(t[6], t[7])));
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) t[j] = fminf(x[j], x[j + 8]);
-#pragma unroll
-            for (int j = 16; j < kKeys; j += 16)
-#pragma unroll
-              for (int k = 0; k < 8; ++k) t[k] = fminf(t[k], fminf(x[j + k], x[j + k + 8]));
-            top = fminf(fminf(fminf(t[0], t[1]), fminf(t[2], t[3])),
-                        fminf(fminf(t[4], t[5]), fminf(t[6], t[7])));
-          }
-          top *= cs;
-        }
-        const bool grown = top > mu + R::kGrow;
-        if (__builtin_expect(__any_sync(0xFFFFFFFFu, grown), 0)) {
-          const float mn = grown ? fmaxf(mu, ceilf(top) - R::kTop) : mu;
+          for (int k = 0; k < 4; ++k)
+            t[k] = j + 4 + k < kC ? fmaxf(t[k], fmaxf(x[j + k], x[j + 4 + k])) : fmaxf(t[k], x[j + k]);
+        float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * cs;
+        // (behind this barrier both warps have their scores: P goes over them)
+        if (__builtin_expect(pair_any(pair, !fine || top > mu + R::kGrow), 0)) {
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(red), "f"(top) : "memory");
+          if (lane == 0) left[half] = !fine;
+          pair_sync(pair);
+          if (left[0] | left[1]) return;  // both
+          top = fmaxf(top, __uint_as_float(lds_u32(red ^ 128)));
+          const float mn = fmaxf(mu, ceilf(top) - R::kTop);
           const float f = mu == -INFINITY ? 0.0f : ex2(mu - mn);
           l = l == 0.0f ? 0.0f : l * f;  // (a NaN stays)
           mu = mn;
-          if (kt > w.kb) {
-            if (!wait(Lay::kPvDone + tile, n - 1)) return;
-            tc::fence_after_sync();
+          if (kt > w.kb) {  // the outputs before are done (these scores came behind them)
 #pragma unroll 1
-            for (int k = 0; k < kV; k += 16) {
+            for (int k = 0; k < 64; k += 16) {
               uint32_t y[16];
               tc::ld_32x16(o_at + k, y);
 #pragma unroll
@@ -579,63 +595,71 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, const Run& ru
             }
             tc::wait_st();
           }
+          pair_sync(pair);  // the maxima are read
         }
         const float m0 = mu == -INFINITY ? 0.0f : -mu;
         const uint64_t c2 = f2(cs, cs), m2 = f2(m0, m0);
         uint64_t sum[2] = {0, 0};
-        uint32_t* pk = reinterpret_cast<uint32_t*>(x);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int q = 0; q < 2; ++q) {  // (16 words at a time: more do not fit the registers)
+          uint32_t pk[16];
 #pragma unroll
-          for (int j = 32 * h; j < 32 * h + 32; ++j) {
-            const float2 y = unf2(fma2(f2(x[2 * j], x[2 * j + 1]), c2, m2));
+          for (int j = 0; j < 16; ++j) {
+            const float2 y = unf2(fma2(f2(x[32 * q + 2 * j], x[32 * q + 2 * j + 1]), c2, m2));
             const float p0 = ex2(y.x), p1 = ex2(y.y);
             sum[j & 1] = add2(sum[j & 1], f2(p0, p1));
             pk[j] = pack16x2<F>(p0, p1);
           }
-          tc::st_32x32(s_at + 32 * h, pk + 32 * h);
-          tc::wait_st();
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bars + 8 * (Lay::kPFull + 2 * tile + h));
+          tc::st_32x16(s_at + half * 32 + q * 16, pk);
         }
-        const float2 t = unf2(add2(sum[0], sum[1]));
-        l += t.x + t.y;
-      } else {
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane < 2) mbar_arrive(bars + 8 * (Lay::kPFull + 2 * tile + lane));
+        const float2 s2 = unf2(add2(sum[0], sum[1]));
+        l += s2.x + s2.y;
+        tc::wait_st();
+      } else if (!fine) {
+        return;
       }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * (Lay::kPFull + tile));
     }
     // ---- the end of this CTA's part of the item
     const Walk past = w;
     g += w.ke - w.kb;
     cleaned += w.cleaned();
     more = w.next(a);
-    if (more && w.end(tile) > w.kb) load_queries(a, w, smem, tile, w4, lane);
+    if (more && w.end(tile) > w.kb) load_queries(a, w, smem, tile, warp & 7, lane);
     const bool any = e > past.kb;
+    bool fine = true;
     if (any) {
-      if (!wait(Lay::kPvDone + tile, n - 1)) return;
+      fine = wait(Lay::kOFull + tile, items++);
       tc::fence_after_sync();
     }
     if (live) {
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(red), "f"(l) : "memory");
+      if (lane == 0) left[half] = !fine;
+      pair_sync(pair);
+      if (left[0] | left[1]) return;  // both
+      l += __uint_as_float(lds_u32(red ^ 128));
       const bool whole = past.kb == 0 && past.ke == past.tiles;
       const int64_t slot = 2 * (int64_t)blockIdx.x + (past.kb == 0 ? 1 : 0);
       const int64_t at = slot * srows + tile * kM + r;
-      float* part = ws.o + slot * srows * kV + (tile * kM + r) * 4;  // [dims / 4][rows][4]
+      float* part = ws.o + slot * srows * kV + (int64_t)half * 64 * srows + (tile * kM + r) * 4;
       const uint32_t dt = a.by_group(row);
-      const int64_t t = past.q.t0 + (int)dt, h = (int64_t)past.head * a.group + (int)(row - dt * a.group);
-      if (ok && !whole) {
-        ws.m[at] = mu;
-        ws.l[at] = l;
-      } else if (ok && a.lse) {
-        a.lse[t * a.lse_ts + h * a.lse_hs] = l == 0.0f ? -INFINITY : (mu + __log2f(l)) * kLn2;
+      const int64_t t = past.q.t0 + (int)dt;
+      const int64_t h = (int64_t)past.head * a.group + (int)(row - dt * a.group);
+      if (ok && half == 0) {
+        if (!whole) {
+          ws.m[at] = mu;
+          ws.l[at] = l;
+        } else if (a.lse) {
+          a.lse[t * a.lse_ts + h * a.lse_hs] = l == 0.0f ? -INFINITY : (mu + __log2f(l)) * kLn2;
+        }
       }
       const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
-      uint8_t* out = a.out + t * a.out_ts + h * a.out_hs;
+      uint8_t* out = a.out + t * a.out_ts + h * a.out_hs + half * 128;
       if (any) {
 #pragma unroll 1
-        for (int k = 0; k < kV; k += 32) {
+        for (int k = 0; k < 64; k += 32) {
           uint32_t y[32];
           tc::ld_32x32(o_at + k, y);
           if (!ok) continue;
@@ -656,6 +680,8 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, const Run& ru
           }
         }
       }
+    } else if (!fine) {
+      return;
     }
     if (any) {
       tc::fence_before_sync();
@@ -786,14 +812,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bars + 8 * (Lay::kVFull + i), 1 + stall(i + 3));
       mbar_init(bars + 8 * (Lay::kKEmpty + i), 2);
       mbar_init(bars + 8 * (Lay::kVEmpty + i), 2);
+      mbar_init(bars + 8 * (Lay::kTurn + i), 1);
       mbar_init(bars + 8 * (Lay::kRaw + i), 1);
       mbar_init(bars + 8 * (Lay::kClean + i), 1);
-      mbar_init(bars + 8 * (Lay::kQFull + i), kM);
+      mbar_init(bars + 8 * (Lay::kQFull + i), 8 * 32);
       mbar_init(bars + 8 * (Lay::kSFull + i), 1);
-      mbar_init(bars + 8 * (Lay::kPFull + 2 * i), 4);
-      mbar_init(bars + 8 * (Lay::kPFull + 2 * i + 1), 4);
-      mbar_init(bars + 8 * (Lay::kPvDone + i), 1);
-      mbar_init(bars + 8 * (Lay::kOFree + i), 4);
+      mbar_init(bars + 8 * (Lay::kPFull + i), 8);
+      mbar_init(bars + 8 * (Lay::kOFull + i), 1);
+      mbar_init(bars + 8 * (Lay::kOFree + i), 8);
     }
     mbar_fence_init();
   }
@@ -812,8 +838,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, m.tmem, 0);
   uint32_t issued = 0, cleaned = 0;
   if (run.count > 0) {
-    if (warp < 8) {
-      softmax_role<F>(a, run, smem, tmem, wait, warp >> 2, warp & 3, lane, ws, srows);
+    if (warp < kMmaWarp) {
+      softmax_role<F>(a, run, smem, tmem, wait, warp, lane, ws, srows, m);
       asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp < kLoadWarp) {
       mma_role<F>(a, run, smem, tmem, wait, warp - kMmaWarp, lane);
