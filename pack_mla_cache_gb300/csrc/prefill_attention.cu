@@ -15,20 +15,21 @@
 //
 // A unit: S_i = Q_i K^T (two tiles of 128 x 128, k = 192), weights P_i = exp2(S_i - reference)
 // written over S_i in tensor memory as 16-bit values, O_i += P_i V (128 x 128).  Tensor memory
-// is full: two S and two O of 128 columns.  The two tiles alternate on the tensor core: while
-// one tile's weights are computed, the other tile's products run (1280 of 2560 cycles a unit
-// at 8192 multiply-adds... per tile).
+// is full: two S and two O of 128 columns.  The products of a unit and tile take 1280 cycles;
+// while a tile's weights are computed, the other tile's products run.
 //
-// Shared memory: the two query tiles (96 KB), and a ring of 8 slots of 128 keys x 64 columns
-// (128 bytes a row, 128-byte swizzle) through which K (three slots a unit) and V (two) flow by
-// TMA, a whole unit ahead of their use.
+// Shared memory: the two query tiles (96 KB), and a ring of 8 slots of 16 KB through which K
+// (three slots a unit: 128 keys x 64 columns each) and V (two: 64 keys x 128 columns) flow by
+// TMA, in rows of 128 bytes with the 128-byte swizzle.
 //
-// Roles (20 warps): 8 warps per query tile load the queries, compute weights, two threads a row
-// (64 columns each; running maximum, rescaling O only when a maximum has grown by more than
-// 2^kGrow) and write the output; one per tile issues the products; one loads K and V; one looks after V rows that
-// not every row of an item sees: those behind the sequence are zeroed (they may hold anything),
-// those with a NaN or an infinity too, and noted, so that the sums of the rows that see them
-// become NaN.
+// Roles (12 warps): 4 warps per query tile load the queries, compute weights, a thread a row
+// (running maximum, rescaling O only when a maximum has grown by more than 2^kGrow) and write
+// the output; one per tile issues the products; one plans the CTA's items, describes them to
+// the others in shared memory and loads K and V; one looks after V rows that not every row of
+// an item sees: those behind the sequence are zeroed (they may hold anything), those with a
+// NaN or an infinity too, and noted, so that the sums of the rows that see them become NaN.
+// Each role's code is kept small and in one place: instructions are fetched cold in every
+// launch, at about 40 cycles each where nothing else covers it.
 //
 // Waits are bounded (wait_limit_ns): one that runs out marks the CTA as given up.  Every role
 // leaves at its next wait then, copies and products in flight are waited for (bounded again),
@@ -52,8 +53,10 @@ constexpr int kSlot = kKeys * 128;   // bytes of a ring slot
 constexpr int kSlots = 8;
 constexpr int kUnitSlots = 5;        // 3 of K, 2 of V
 constexpr int kQTile = 3 * kM * 128;
-constexpr int kMmaWarp = 16, kLoadWarp = 18;  // and one more, that looks after V
-constexpr int kWarps = 20, kThreads = kWarps * 32;
+constexpr int kMmaWarp = 8, kLoadWarp = 10;  // and one more, that looks after V
+constexpr int kWarps = 12, kThreads = kWarps * 32;
+constexpr int kItems = 4;            // item descriptions in shared memory
+constexpr int kItemReaders = kWarps - 1;
 constexpr int kMaxCtas = 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -75,13 +78,13 @@ struct Ref {
 struct Lay {
   static constexpr int q = 0;
   static constexpr int ring = 2 * kQTile;
-  static constexpr int red = ring + kSlots * kSlot;  // float [8 pairs of warps][2][32]
-  static constexpr int flags = red + 2048;           // uint32 [4 units][4]: keys with bad V rows
+  static constexpr int items = ring + kSlots * kSlot;     // Item [kItems]
+  static constexpr int flags = items + kItems * 64;       // uint32 [4 units][4]: keys with bad V rows
   static constexpr int bars = flags + 64;
   // Two of each: of units in turn (K and V), of the query tiles; the weights' by tile and half.
   static constexpr int kKFull = 0, kVFull = 2, kKEmpty = 4, kVEmpty = 6, kRaw = 8, kClean = 10,
-                       kQFull = 12, kSFull = 14, kPFull = 16, kOFull = 18, kOFree = 20, kTurn = 22,
-                       kBars = 24;
+                       kQFull = 12, kSFull = 14, kPFull = 16, kOFull = 20, kOFree = 22, kTurn = 24,
+                       kItemFull = 26, kItemFree = kItemFull + kItems, kBars = kItemFree + kItems;
   static constexpr int misc = (bars + kBars * 8 + 15) / 16 * 16;
   static constexpr int bytes = misc + 64;
   static_assert(bytes <= 232448, "shared memory of a CTA");
@@ -91,9 +94,7 @@ struct Lay {
 struct Misc {
   uint32_t tmem;
   uint32_t abort;
-  uint8_t left[16];  // a weights' warp that has given up, for its partner
 };
-static_assert(sizeof(Misc) <= 64, "Misc fits");
 
 // How a tensor map reads row p, columns c.. of key head g: box (x_head * g + c, p, z_head * g).
 struct Maps {
@@ -152,156 +153,271 @@ __device__ __forceinline__ Seq load_seq(const PrefillArgs& a, int s, uint32_t& e
   return q;
 }
 // Key rows that the token of a query row sees.
-__device__ __forceinline__ int seen_of(const PrefillArgs& a, const Seq& q, uint32_t row) {
-  const int64_t n = q.base + (a.causal ? (int64_t)a.by_group(row) : 0);
-  return (int)max((int64_t)0, min(n, (int64_t)q.m));
+__device__ __forceinline__ int seen_of(const PrefillArgs& a, int64_t base, int m, uint32_t row) {
+  const int64_t n = base + (a.causal ? (int64_t)a.by_group(row) : 0);
+  return (int)max((int64_t)0, min(n, (int64_t)m));
 }
 // Key tiles of rows of which the last sees `most` (one even when it sees none: they are still
 // written).
 __device__ __forceinline__ int key_tiles(int most) { return max(1, (most + kKeys - 1) / kKeys); }
 __device__ __forceinline__ int item_tiles(const PrefillArgs& a, const Seq& q, int b) {
-  return key_tiles(seen_of(a, q, min((uint32_t)(b + 1) * kItemRows, q.rows) - 1));
+  return key_tiles(seen_of(a, q.base, q.m, min((uint32_t)(b + 1) * kItemRows, q.rows) - 1));
 }
 
-// A CTA's run of units: where it starts, and what finds the CTA of another unit.  An item is
-// kSwitch units that stand for beginning it, then its key tiles: a run starts before the
-// first of these when kt is negative.
-struct Run {
-  Seq q;
-  int s, head, b, kt, count;
-  int64_t begin, each;
-  int extra;
-};
-
-// Walks the run item by item; every role has its own copy.
-struct Walk {
-  Seq q;
-  int s, head, b, left;
-  bool more;
-  // the present item
-  int kb, ke;              // this CTA's key tiles of it
-  int nkt[2], tiles;       // key tiles of the query tiles (0: the tile has no rows), and of both
-  int least, most;         // rows seen by its first and last row
-  uint32_t row0;
-  int rows;
-  __device__ __forceinline__ void start(const Run& r) {
-    q = r.q;
-    s = r.s;
-    head = r.head;
-    b = r.b;
-    left = r.count + min(r.kt, 0);
-    kb = max(r.kt, 0);
-    more = false;
-  }
-  __device__ __forceinline__ bool next(const PrefillArgs& a) {
-    if (left <= 0) return false;
-    if (more) {
-      kb = 0;
-      if (++b >= q.nb) {
-        b = 0;
-        if (++head >= a.kv_heads) {
-          head = 0;
-          uint32_t ignored = 0;
-          do q = load_seq(a, ++s, ignored);
-          while (q.nb == 0 && s + 1 < a.num_seqs);
-        }
-      }
-      left -= kSwitch;
-      if (left <= 0) return false;
-    }
-    more = true;
-    row0 = (uint32_t)b * kItemRows;
-    rows = (int)min((uint32_t)kItemRows, q.rows - row0);
-    least = seen_of(a, q, row0);
-    most = seen_of(a, q, row0 + rows - 1);
-    tiles = key_tiles(most);
-    nkt[0] = rows > kM ? key_tiles(seen_of(a, q, row0 + kM - 1)) : tiles;
-    nkt[1] = rows > kM ? tiles : 0;
-    ke = min(tiles, kb + left);
-    left -= ke - kb;
-    return true;
-  }
-  // Key tiles of query tile i in this run end here (at kb or before: none).
-  __device__ __forceinline__ int end(int i) const { return min(ke, nkt[i]); }
+// A CTA's part of an item.
+struct Item {
+  int kb, ke;          // its key tiles of it; ke < 0: no more items
+  int end[2];          // where those of the query tiles end (at kb or before: none)
+  int tiles;           // of the whole item
+  int least, most;     // keys seen by its first and last row
+  uint32_t row0;       // first row, among the sequence's of the key head
+  int rows, t0, head;
+  int k0, m;           // the sequence's first key row, and how many exist
+  int64_t base;        // keys that its token t0 sees (before clamping)
   // The first key tile that not every row sees whole.
-  __device__ __forceinline__ int ragged() const { return least / kKeys; }
-  // Units of the item in this run with V rows to be looked after.
-  __device__ __forceinline__ int cleaned() const { return max(0, ke - max(kb, ragged())); }
+  __device__ __forceinline__ int ragged() const { return max(kb, least / kKeys); }
+  // Units with V rows to be looked after.
+  __device__ __forceinline__ int cleaned() const { return max(0, ke - ragged()); }
+};
+static_assert(sizeof(Item) <= 64, "an item's description");
+
+// Reads the descriptions in their order, a whole warp at a time.
+struct Items {
+  uint32_t smem, next;
+  __device__ __forceinline__ bool get(const Waiter& wait, Item& it) {
+    const uint32_t i = next & (kItems - 1);
+    const uint32_t bars = smem + Lay::bars;
+    if (!__all_sync(0xFFFFFFFFu, wait(bars + 8 * (Lay::kItemFull + i), (next / kItems) & 1))) return false;
+    uint4* w = reinterpret_cast<uint4*>(&it);
+#pragma unroll
+    for (int k = 0; k < (int)sizeof(Item) / 16; ++k) w[k] = lds16(smem + Lay::items + i * 64 + 16 * k);
+    if constexpr (sizeof(Item) % 16 != 0) {
+      static_assert(sizeof(Item) % 16 == 8 || sizeof(Item) % 16 == 0, "words of a description");
+      reinterpret_cast<uint2*>(&it)[sizeof(Item) / 8 - 1] =
+          lds8(smem + Lay::items + i * 64 + (int)sizeof(Item) / 8 * 8 - 8);
+    }
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bars + 8 * (Lay::kItemFree + i));
+    ++next;
+    return it.ke >= 0;
+  }
 };
 
 __device__ __forceinline__ uint32_t slot_of(uint32_t unit, int chunk) {
   return (unit * kUnitSlots + chunk) & (kSlots - 1);
 }
 
-__device__ __noinline__ int cta_of(int64_t u, int64_t each, int extra) {
-  const int64_t longer = (each + 1) * extra;
-  return (int)(u < longer ? u / (each + 1) : extra + (u - longer) / each);
+// -------------------------------------------------------------- plan and load
+__device__ __noinline__ int64_t divide(int64_t n, int64_t d) {
+  return (n | d) >> 32 ? n / d : (int64_t)((uint32_t)n / (uint32_t)d);
+}
+__device__ __forceinline__ int64_t scan64(int64_t v, int lane) {  // inclusive, over the warp
+#pragma unroll 1
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
 }
 
-// ------------------------------------------------------------------ the roles
-// K and V by TMA, and where the run ends inside an item, what the join needs.  Returns the
-// copies begun, in K and V of a unit, and the units whose V is looked after.  V of such a unit
-// completes on a barrier of its own (two in turn), which that warp waits for: it does not follow
-// the ring through the units between, and a barrier's parity tells one phase from the next
-// only.
+// The run of one CTA, walked item by item, by one warp.  An item is kSwitch units that stand
+// for beginning it, then its key tiles: a run starts before the first of these when kt is
+// negative.
+struct Plan {
+  Seq q;
+  int s, head, b, kt, left;
+  int64_t begin, each;   // the first unit; units of the CTAs c >= extra (each + 1 of the ones before)
+  int extra, count;
+  __device__ __forceinline__ int cta_of(int64_t u) const {
+    const int64_t longer = (each + 1) * extra;
+    return (int)(u < longer ? divide(u, each + 1) : extra + divide(u - longer, each));
+  }
+  // Where the run starts; pre: scratch for num_seqs numbers.
+  __device__ __forceinline__ void find(const PrefillArgs& a, int64_t* pre, int lane, uint32_t& errbits) {
+    int64_t total = 0;
+    uint32_t ignored = 0;
+#pragma unroll 1
+    for (int s0 = 0; s0 < a.num_seqs; s0 += 32) {
+      int64_t u = 0;
+      int nb = 0;
+      if (s0 + lane < a.num_seqs) {
+        const Seq one = load_seq(a, s0 + lane, errbits);
+        nb = one.nb;
+        if (nb <= 4)
+#pragma unroll 1
+          for (int i = 0; i < nb; ++i) u += kSwitch + item_tiles(a, one, i);
+      }
+      // sequences of many items: by the whole warp
+      for (uint32_t many = __ballot_sync(0xFFFFFFFFu, nb > 4); many; many &= many - 1) {
+        const int from = __ffs(many) - 1;
+        const Seq one = load_seq(a, s0 + from, ignored);
+        int64_t sum = 0;
+#pragma unroll 1
+        for (int i = lane; i < one.nb; i += 32) sum += kSwitch + item_tiles(a, one, i);
+        sum = __shfl_sync(0xFFFFFFFFu, scan64(sum, lane), 31);
+        if (lane == from) u = sum;
+      }
+      u *= a.kv_heads;
+      const int64_t in = scan64(u, lane);
+      if (s0 + lane < a.num_seqs) pre[s0 + lane] = total + in - u;
+      total += __shfl_sync(0xFFFFFFFFu, in, 31);
+    }
+    __syncwarp();
+    const int64_t ctas = max((int64_t)1, min((int64_t)gridDim.x, total / kMinUnits));
+    each = divide(total, ctas);
+    extra = (int)(total - each * ctas);
+    begin = each * blockIdx.x + min((int)blockIdx.x, extra);
+    count = blockIdx.x < ctas ? (int)each + ((int)blockIdx.x < extra ? 1 : 0) : 0;
+    left = 0;
+    if (count == 0) return;
+    // the last sequence that begins at or before the run (those without units begin where the
+    // one behind them does)
+    int lo = 0;
+#pragma unroll 1
+    for (int step = 4096; step > 0; step >>= 1)
+      if (lo + step < a.num_seqs && pre[lo + step] <= begin) lo += step;
+    s = lo;
+    q = load_seq(a, s, ignored);
+    int64_t off = begin - pre[s];
+    const int64_t per = divide((s + 1 < a.num_seqs ? pre[s + 1] : total) - pre[s], a.kv_heads);
+    head = (int)divide(off, per);
+    off -= head * per;
+    int64_t base = 0;
+#pragma unroll 1
+    for (int b0 = 0;; b0 += 32) {
+      const int64_t u = b0 + lane < q.nb ? kSwitch + item_tiles(a, q, b0 + lane) : 0;
+      const int64_t in = scan64(u, lane);
+      const uint32_t hit = __ballot_sync(0xFFFFFFFFu, off < base + in);
+      if (hit) {
+        const int at = __ffs(hit) - 1;
+        b = b0 + at;
+        kt = (int)(off - base - __shfl_sync(0xFFFFFFFFu, in - u, at)) - kSwitch;
+        break;
+      }
+      base += __shfl_sync(0xFFFFFFFFu, in, 31);
+    }
+    left = count + min(kt, 0);
+    kt = max(kt, 0);
+  }
+  // The next item (the first call: the run's first).
+  __device__ __forceinline__ Item next(const PrefillArgs& a) {
+    Item it;
+    it.ke = -1;
+    if (left <= 0) return it;
+    it.kb = kt;
+    it.row0 = (uint32_t)b * kItemRows;
+    it.rows = (int)min((uint32_t)kItemRows, q.rows - it.row0);
+    it.least = seen_of(a, q.base, q.m, it.row0);
+    it.most = seen_of(a, q.base, q.m, it.row0 + it.rows - 1);
+    it.tiles = key_tiles(it.most);
+    it.ke = min(it.tiles, kt + left);
+    const int first = it.rows > kM ? key_tiles(seen_of(a, q.base, q.m, it.row0 + kM - 1)) : it.tiles;
+    it.end[0] = min(it.ke, first);
+    it.end[1] = it.rows > kM ? it.ke : 0;
+    it.t0 = q.t0;
+    it.head = head;
+    it.k0 = q.k0;
+    it.m = q.m;
+    it.base = q.base;
+    left -= it.ke - kt + kSwitch;
+    kt = 0;
+    if (left > 0 && ++b >= q.nb) {
+      b = 0;
+      if (++head >= a.kv_heads) {
+        head = 0;
+        uint32_t ignored = 0;
+#pragma unroll 1
+        do q = load_seq(a, ++s, ignored);
+        while (q.nb == 0 && s + 1 < a.num_seqs);
+      }
+    }
+    return it;
+  }
+};
+
+// Plans the items and describes them, one ahead; K and V by TMA; where the run ends inside an
+// item, what the join needs.  Returns the copies begun, in K and V of a unit, and the units
+// whose V is looked after.  V of such a unit completes on a barrier of its own (two in turn),
+// which that warp waits for: it does not follow the ring through the units between, and a
+// barrier's parity tells one phase from the next only.
 //
 // The ring holds 8/5 units, so a unit's slots are those of K's last third and V of the unit two
 // before, and of the first two thirds of K of the unit before.
-__device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& maps, const Run& run,
+__device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& maps, uint8_t* smem_raw,
                                               uint32_t smem, const Waiter& wait, int lane,
-                                              const Workspace& ws, uint32_t& cleaned) {
+                                              const Workspace& ws, uint32_t& cleaned, uint32_t& errbits) {
   const uint32_t bars = smem + Lay::bars;
+  auto waited = [&](int bar, uint32_t phase) {
+    return __all_sync(0xFFFFFFFFu, wait(bars + 8 * bar, phase & 1));
+  };
   // rows that one item reads leave L2 first
   const uint64_t policy =
       tc::l2_policy((int64_t)a.num_tokens * a.group <= (int64_t)kItemRows * a.num_seqs);
-  Walk w;
-  w.start(run);
-  uint32_t g = 0;
+  Plan plan;
+  plan.find(a, reinterpret_cast<int64_t*>(smem_raw + Lay::ring), lane, errbits);
+  tc::fence_smem_async();  // the scratch is read; copies may write there now
+  __syncwarp();
+  uint32_t g = 0, told = 0;
   cleaned = 0;
-  while (w.next(a)) {
-    const int h = w.head;
+  Item it;
+  it.ke = 0;
+  // The first round only plans.
 #pragma unroll 1
-    for (int kt = w.kb; kt < w.ke; ++kt, ++g) {
-      const int row = w.q.k0 + kt * kKeys;
-      const bool clean = kt >= w.ragged();
-      auto dst = [&](int c) { return smem + Lay::ring + slot_of(g, c) * kSlot; };
-      auto freed = [&](int bar, uint32_t unit) {  // K (V) of that unit is read
-        return __all_sync(0xFFFFFFFFu, wait(bars + 8 * (bar + (unit & 1)), (unit >> 1) & 1));
-      };
-      const uint32_t kf = bars + 8 * (Lay::kKFull + (g & 1));
+  for (bool first = true;; first = false) {
+    const Item nxt = plan.next(a);
+    if (first || it.ke >= 0) {
+      const uint32_t i = told & (kItems - 1);
+      if (told >= kItems && !waited(Lay::kItemFree + i, told / kItems - 1)) return 2 * g;
       if (lane == 0) {
-        mbar_arrive_expect_tx(kf, 3 * kSlot);
-        tc::tma_load3(dst(0), &maps.kn, h * maps.kn_x, row, h * maps.kn_z, kf, policy);
+        *reinterpret_cast<Item*>(smem_raw + Lay::items + i * 64) = nxt;
+        mbar_arrive(bars + 8 * (Lay::kItemFull + i));
       }
       __syncwarp();
-      if (g >= 2 && !freed(Lay::kVEmpty, g - 2)) return 2 * g;
-      if (lane == 0) {
-        tc::tma_load3(dst(1), &maps.kn, h * maps.kn_x + 64, row, h * maps.kn_z, kf, policy);
-        tc::tma_load3(dst(2), &maps.kp, h * maps.kp_x, row, h * maps.kp_z, kf, policy);
-      }
-      __syncwarp();
-      if (g >= 1 && !freed(Lay::kKEmpty, g - 1)) return 2 * g + 1;
-      if (lane == 0) {
-        uint32_t vf = bars + 8 * (Lay::kVFull + (g & 1));
-        if (clean) {
-          mbar_arrive(vf);
-          vf = bars + 8 * (Lay::kRaw + (cleaned & 1));
+      ++told;
+    }
+    if (!first) {
+      if (it.ke < 0) break;
+      const int h = it.head, ragged = it.ragged();
+#pragma unroll 1
+      for (int kt = it.kb; kt < it.ke; ++kt, ++g) {
+        const int row = it.k0 + kt * kKeys;
+        const bool clean = kt >= ragged;
+        auto dst = [&](int c) { return smem + Lay::ring + slot_of(g, c) * kSlot; };
+        const uint32_t kf = bars + 8 * (Lay::kKFull + (g & 1));
+        if (lane == 0) {
+          mbar_arrive_expect_tx(kf, 3 * kSlot);
+          tc::tma_load3(dst(0), &maps.kn, h * maps.kn_x, row, h * maps.kn_z, kf, policy);
         }
-        mbar_arrive_expect_tx(vf, 2 * kSlot);
+        __syncwarp();
+        if (g >= 2 && !waited(Lay::kVEmpty + (g & 1), (g - 2) >> 1)) return 2 * g;
+        if (lane == 0) {
+          tc::tma_load3(dst(1), &maps.kn, h * maps.kn_x + 64, row, h * maps.kn_z, kf, policy);
+          tc::tma_load3(dst(2), &maps.kp, h * maps.kp_x, row, h * maps.kp_z, kf, policy);
+        }
+        __syncwarp();
+        if (g >= 1 && !waited(Lay::kKEmpty + ((g - 1) & 1), (g - 1) >> 1)) return 2 * g + 1;
+        if (lane == 0) {
+          uint32_t vf = bars + 8 * (Lay::kVFull + (g & 1));
+          if (clean) {
+            mbar_arrive(vf);
+            vf = bars + 8 * (Lay::kRaw + (cleaned & 1));
+          }
+          mbar_arrive_expect_tx(vf, 2 * kSlot);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)  // 64 keys x 64 columns each
-          tc::tma_load3(dst(3 + (k >> 1)) + (k & 1) * (kSlot / 2), &maps.v, h * maps.v_x + 64 * (k & 1),
-                        row + 64 * (k >> 1), h * maps.v_z, vf, policy);
+          for (int k = 0; k < 4; ++k)  // 64 keys x 64 columns each
+            tc::tma_load3(dst(3 + (k >> 1)) + (k & 1) * (kSlot / 2), &maps.v, h * maps.v_x + 64 * (k & 1),
+                          row + 64 * (k >> 1), h * maps.v_z, vf, policy);
+        }
+        __syncwarp();
+        cleaned += clean;
       }
-      __syncwarp();
-      cleaned += clean;
+      if (it.ke < it.tiles && lane == 0) {  // the run's last item
+        const int64_t u0 = plan.begin + plan.count - it.ke;  // the unit of its key tile 0
+        const int c0 = plan.cta_of(u0), c1 = plan.cta_of(u0 + it.tiles - 1);
+        ws.split[blockIdx.x] = Split{it.t0, it.row0, it.head, (int16_t)it.rows, (int16_t)(c1 - c0 + 1), c0, {}};
+      }
     }
-    if (w.ke < w.tiles && lane == 0) {  // the run's last item
-      const int64_t u0 = run.begin + run.count - w.ke;  // the unit of its key tile 0
-      const int c0 = cta_of(u0, run.each, run.extra);
-      const int c1 = cta_of(u0 + w.tiles - 1, run.each, run.extra);
-      ws.split[blockIdx.x] = Split{w.q.t0, w.row0, w.head, (int16_t)w.rows, (int16_t)(c1 - c0 + 1), c0, {}};
-    }
+    it = nxt;
   }
   return 2 * g;
 }
@@ -310,39 +426,40 @@ __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& 
 // turn: this role may be one unit ahead of the last look at its barrier, but not two, as V of
 // the next but one waits for the scores of the next.)
 template <int F>
-__device__ __forceinline__ void clean_role(const PrefillArgs& a, const Run& run, uint32_t smem,
-                                           const Waiter& wait, int lane) {
+__device__ __forceinline__ void clean_role(uint32_t smem, const Waiter& wait, int lane) {
   const uint32_t bars = smem + Lay::bars;
-  Walk w;
-  w.start(run);
   uint32_t g = 0, cleaned = 0;
   const int col = lane & 7;
-  while (w.next(a)) {
+  Items items{smem, 0};
+  Item it;
 #pragma unroll 1
-    for (int kt = max(w.kb, w.ragged()); kt < w.ke; ++kt) {
-      const uint32_t u = g + kt - w.kb;
+  while (items.get(wait, it)) {
+#pragma unroll 1
+    for (int kt = it.ragged(); kt < it.ke; ++kt) {
+      const uint32_t u = g + kt - it.kb;
       if (!__all_sync(0xFFFFFFFFu, wait(bars + 8 * (Lay::kRaw + (cleaned & 1)), (cleaned >> 1) & 1)))
         return;
 #pragma unroll 1
       for (int q = 0; q < 4; ++q) {  // 32 keys
         const int p0 = kt * kKeys + q * 32;
         uint32_t bad = 0;
-        if (p0 + 32 > w.least) {
+        if (p0 + 32 > it.least) {
           // 64 keys to a slot: two runs of 64 columns
           const uint32_t v0 = smem + Lay::ring + slot_of(u, 3 + (q >> 1)) * kSlot + (q & 1) * 4096;
-#pragma unroll
+#pragma unroll 2
           for (int n = 0; n < 8; ++n) {
             const int key = 4 * n + (lane >> 3), p = p0 + key;
             const uint32_t at = v0 + key * 128 + col * 16;  // every column of the row, in any order
             const bool sp = any_special<F>(lds16(at)) | any_special<F>(lds16(at + kSlot / 2));
-            const uint32_t votes = __ballot_sync(0xFFFFFFFFu, sp && p >= w.least && p < w.most);
-            if (p >= w.most || votes & (0xFFu << (lane & 24))) {
+            const uint32_t votes = __ballot_sync(0xFFFFFFFFu, sp && p >= it.least && p < it.most);
+            if (p >= it.most || votes & (0xFFu << (lane & 24))) {
               sts16(at, make_uint4(0, 0, 0, 0));
               sts16(at + kSlot / 2, make_uint4(0, 0, 0, 0));
             }
+            if (votes)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (votes & (0xFFu << (8 * k))) bad |= 1u << (4 * n + k);
+              for (int k = 0; k < 4; ++k)
+                if (votes & (0xFFu << (8 * k))) bad |= 1u << (4 * n + k);
           }
         }
         if (lane == 0) sts_u32(smem + Lay::flags + (u & 3) * 16 + q * 4, bad);
@@ -352,10 +469,11 @@ __device__ __forceinline__ void clean_role(const PrefillArgs& a, const Run& run,
       if (lane == 0) mbar_arrive(bars + 8 * (Lay::kClean + (cleaned & 1)));
       ++cleaned;
     }
-    g += w.ke - w.kb;
+    g += it.ke - it.kb;
   }
 }
 
+// ------------------------------------------------------------ matrix products
 template <int F>
 __device__ __forceinline__ void issue_scores(uint32_t smem, uint32_t tmem, bool one, int tile,
                                              uint32_t unit, uint32_t negate) {
@@ -371,94 +489,80 @@ __device__ __forceinline__ void issue_scores(uint32_t smem, uint32_t tmem, bool 
       tc::mma_16bit(one, d, qa + (c * kM * 128 >> 4) + 2 * k, kb + 2 * k, id, c + k > 0);
   }
 }
-// V MN-major (two runs of 64 columns), half of the keys a slot.
+// Half of the keys: a slot of V, MN-major (two runs of 64 columns).
 template <int F>
 __device__ __forceinline__ void issue_outputs(uint32_t smem, uint32_t tmem, bool one, int tile,
-                                              uint32_t unit, bool first) {
+                                              uint32_t unit, int half_, bool first) {
   constexpr uint32_t kId = tc::instr_desc(kM, kV, false, F == kBF16, F == kBF16, true);
   const uint32_t i = __shfl_sync(0xFFFFFFFFu, tile, 0), g = __shfl_sync(0xFFFFFFFFu, unit, 0);
-  const uint32_t p = tmem + i * kKeys, d = tmem + Lay::kO + i * kV;
+  const uint32_t half = __shfl_sync(0xFFFFFFFFu, half_, 0);
+  const uint32_t p = tmem + i * kKeys + half * 32, d = tmem + Lay::kO + i * kV;
+  const uint64_t vb = tc::smem_desc(smem + Lay::ring + slot_of(g, 3 + half) * kSlot, kSlot / 2, 1024);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint64_t vb = tc::smem_desc(smem + Lay::ring + slot_of(g, 3 + h) * kSlot, kSlot / 2, 1024);
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      tc::mma_16bit_ta(one, d, p + h * 32 + 8 * k, vb + k * (2048 >> 4), kId, h + k > 0 || !first);
-  }
+  for (int k = 0; k < 4; ++k)
+    tc::mma_16bit_ta(one, d, p + 8 * k, vb + k * (2048 >> 4), kId, half + k > 0 || !first);
 }
 
 // A warp issues the products of one query tile, whose chain is serial: scores of a unit behind
-// the outputs of the one before, over whose weights they go.  The two warps take turns, so that
-// a tile's weights are computed while the other's products run.  (One warp for both took 4900
-// cycles a unit, most of them its own instructions between the products; two without turns 4600,
-// both tiles waiting for the tensor core and for their weights at the same times.)  K and V of a
-// unit are free when both warps have said so; a warp whose tile has no part in a unit says it
-// when they have come, so that it does not run ahead.
+// the outputs of the one before, over whose weights they go.  The other tile's products fill
+// the gaps.  (One warp for both took 4900 cycles a unit, most of them its own instructions
+// between the products.)  K and V of a unit are free when both warps have said so; a warp whose
+// tile has no part in a unit says it when they have come, so that it does not run ahead.
 template <int F>
-__device__ __forceinline__ void mma_role(const PrefillArgs& a, const Run& run, uint32_t smem,
-                                         uint32_t tmem, const Waiter& waiter, int tile, int lane) {
+__device__ __forceinline__ void mma_role(float scale, uint32_t smem, uint32_t tmem, const Waiter& waiter,
+                                         int tile, int lane) {
   const uint32_t bars = smem + Lay::bars;
   // Looks at barriers without letting itself be suspended: waking takes long.
   auto wait = [&](int bar, uint32_t phase) {
+#pragma unroll 1
     for (int spin = 0; spin < 64; ++spin)
       if (__any_sync(0xFFFFFFFFu, mbar_test(bars + 8 * bar, phase & 1))) return true;
     return (bool)__all_sync(0xFFFFFFFFu, waiter(bars + 8 * bar, phase & 1));
   };
   const bool one = tc::elect();
-  const uint32_t negate = a.softmax_scale < 0.0f ? 1u << 13 : 0u;  // of the scores, by the tensor core
-  Walk w;
-  w.start(run);
+  const uint32_t negate = scale < 0.0f ? 1u << 13 : 0u;  // of the scores, by the tensor core
   uint32_t g = 0, done = 0, opened = 0, cleaned = 0;
+  Items items{smem, 0};
+  Item it;
 #pragma unroll 1
-  while (w.next(a)) {
-    const int e = w.end(tile), from = max(w.kb, w.ragged());
-    if (e > w.kb) {
-      if (!wait(Lay::kQFull + tile, opened)) return;
-      tc::fence_smem_async();  // the queries came by ordinary copies
-    }
+  while (items.get(waiter, it)) {
+    const int e = it.end[tile], kb = it.kb, ke = it.ke, ragged = it.ragged();
+    const uint32_t c0 = cleaned - ragged;
+    cleaned += it.cleaned();
 #pragma unroll 1
-    for (int kt = w.kb; kt < w.ke; ++kt, ++g) {
-      const bool act = kt < e;
-      // the scores of the item's first unit; the others' follow the outputs before, below
-      if (kt == w.kb) {
-        if (!wait(Lay::kKFull + (g & 1), g >> 1)) return;
-        if (act) {
-          tc::fence_after_sync();
-          issue_scores<F>(smem, tmem, one, tile, g, negate);
-          tc::commit(one, bars + 8 * (Lay::kSFull + tile));
-        }
-        tc::commit(one, bars + 8 * (Lay::kKEmpty + (g & 1)));
+    for (int kt = kb; kt < ke; ++kt, ++g) {
+      const bool act = kt < e, begins = kt == kb;
+      if (act && begins) {
+        if (!wait(Lay::kQFull + tile, opened)) return;
+        tc::fence_smem_async();  // the queries came by ordinary copies
       }
-      // All that is usually there is asked for before the weights, which are not.
-      const uint32_t n = cleaned + kt - from;
+      if (!wait(Lay::kKFull + (g & 1), g >> 1)) return;
+      if (act) {
+        tc::fence_after_sync();
+        issue_scores<F>(smem, tmem, one, tile, g, negate);
+        tc::commit(one, bars + 8 * (Lay::kSFull + tile));
+      }
+      tc::commit(one, bars + 8 * (Lay::kKEmpty + (g & 1)));
       if (!wait(Lay::kVFull + (g & 1), g >> 1)) return;
       if (act) {
-        if (kt >= from && !wait(Lay::kClean + (n & 1), n >> 1)) return;
+        if (kt >= ragged && !wait(Lay::kClean + ((c0 + kt) & 1), (c0 + kt) >> 1)) return;
         // the sums of the item before are read
-        if (kt == w.kb && opened++ > 0 && !wait(Lay::kOFree + tile, opened)) return;
-      }
-      if (tile + g > 0 && !wait(Lay::kTurn + tile, tile ? g : g - 1)) return;
-      if (act) {
-        if (!wait(Lay::kPFull + tile, done++)) return;
-        tc::fence_after_sync();
-        issue_outputs<F>(smem, tmem, one, tile, g, kt == w.kb);
+        if (begins && opened++ > 0 && !wait(Lay::kOFree + tile, opened)) return;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          if (!wait(Lay::kPFull + 2 * tile + h, done)) return;
+          tc::fence_after_sync();
+          issue_outputs<F>(smem, tmem, one, tile, g, h, begins);
+        }
+        ++done;
         if (kt + 1 == e) tc::commit(one, bars + 8 * (Lay::kOFull + tile));
       }
       tc::commit(one, bars + 8 * (Lay::kVEmpty + (g & 1)));
-      if (kt + 1 < w.ke && !wait(Lay::kKFull + ((g + 1) & 1), (g + 1) >> 1)) return;
-      if (kt + 1 < e) {
-        tc::fence_after_sync();
-        issue_scores<F>(smem, tmem, one, tile, g + 1, negate);
-        tc::commit(one, bars + 8 * (Lay::kSFull + tile));
-      }
-      if (kt + 1 < w.ke) tc::commit(one, bars + 8 * (Lay::kKEmpty + ((g + 1) & 1)));
-      if (lane == 0) mbar_arrive(bars + 8 * (Lay::kTurn + (tile ^ 1)));
-      __syncwarp();
     }
-    cleaned += w.cleaned();
   }
 }
 
+// -------------------------------------------------------- weights and output
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -469,33 +573,18 @@ __device__ __forceinline__ uint32_t pack16x2(float lo, float hi) {
   if constexpr (F == kF16) return pack_f16x2(lo, hi);
   else return pack_bf16x2(lo, hi);
 }
-// A barrier of the two warps that share 32 rows of a tile, and whether x holds in any of their
-// threads.
-__device__ __forceinline__ void pair_sync(int pair) {
-  asm volatile("bar.sync %0, 64;" ::"r"(1 + pair) : "memory");
-}
-__device__ __forceinline__ bool pair_any(int pair, bool x) {
-  uint32_t any;
-  asm volatile(
-      "{ .reg .pred p, q; setp.ne.u32 q, %2, 0;\n"
-      "  barrier.cta.red.or.pred p, %1, 64, q; selp.u32 %0, 1, 0, p; }"
-      : "=r"(any)
-      : "r"(1 + pair), "r"(x ? 1u : 0u)
-      : "memory");
-  return any != 0;
-}
 
-// The queries of a tile by asynchronous copies, 16 rows by each of its eight warps.
-__device__ __forceinline__ void load_queries(const PrefillArgs& a, const Walk& w, uint32_t smem,
-                                             int tile, int warp8, int lane) {
+// The queries of a tile by asynchronous copies, by the tile's four warps.
+__device__ __forceinline__ void load_queries(const PrefillArgs& a, const Item& it, uint32_t smem,
+                                             int tile, int w4, int lane) {
   const int col = lane & 7;
 #pragma unroll 1
-  for (int r = warp8 * 16 + (lane >> 3); r < warp8 * 16 + 16; r += 4) {
-    const uint32_t row = w.row0 + tile * kM + r;
-    const bool ok = row < w.q.rows;
+  for (int r = w4 * 32 + (lane >> 3); r < w4 * 32 + 32; r += 4) {
+    const bool ok = tile * kM + r < it.rows;
+    const uint32_t row = it.row0 + tile * kM + r;
     const uint32_t dt = ok ? a.by_group(row) : 0;
-    const int64_t t = ok ? w.q.t0 + (int)dt : 0;
-    const int64_t h = ok ? (int64_t)w.head * a.group + (int)(row - dt * a.group) : 0;
+    const int64_t t = ok ? it.t0 + (int)dt : 0;
+    const int64_t h = ok ? (int64_t)it.head * a.group + (int)(row - dt * a.group) : 0;
     const uint8_t* nope = a.q_nope + t * a.qn_ts + h * a.qn_hs + col * 16;
     const uint8_t* pe = a.q_pe + t * a.qp_ts + h * a.qp_hs + col * 16;
     const uint32_t d = smem + Lay::q + tile * kQTile + r * 128 + ((col ^ (r & 7)) << 4);
@@ -506,166 +595,174 @@ __device__ __forceinline__ void load_queries(const PrefillArgs& a, const Walk& w
   tc::cp_async_arrive(smem + Lay::bars + 8 * (Lay::kQFull + tile));
 }
 
-// Weights and output of one query tile: a thread has a row's keys 64 half .. of a key tile (and
-// dims 64 half .. of the output), its partner in another warp the others.  One warp for 32 whole
-// rows took 2300 cycles a tile, mostly waiting for its own instructions.  The queries' place is
-// free when the item's last scores have come: those of the next item are asked for before the
-// output of this one is written.
+// What the weights of an item's units need to know; key tiles count from the part's first.
+struct Part {
+  uint32_t smem, s_at, o_at;  // tensor memory: this warp's scores and sums
+  uint32_t n, g, cleaned;     // units of this tile, of all, and looked after, before the part
+  int tile, count, from;      // key tiles, and the first that not every row sees whole
+  int seen;                   // keys that this thread's row sees, from the first tile on
+  bool live;                  // the warp has rows
+  float c;                    // weights: exp2(c score - reference)
+};
+// The weights of an item's units (a function of its own, so that its loop has the registers to
+// itself): the row's reference and the sum of its weights.  False: given up.
 template <int F>
-__device__ __forceinline__ void softmax_role(const PrefillArgs& a, const Run& run, uint32_t smem,
-                                             uint32_t tmem, const Waiter& waiter, int warp, int lane,
-                                             const Workspace& ws, int srows, Misc& misc) {
+__device__ __noinline__ bool unit_weights(Part s, const Waiter waiter, float& mu_out, float& l_out) {
   using R = Ref<F>;
-  constexpr int kC = kKeys / 2;
-  const int tile = warp >> 3, half = (warp >> 2) & 1, w4 = warp & 3, pair = tile * 4 + w4;
-  const uint32_t bars = smem + Lay::bars;
+  const int lane = threadIdx.x & 31;
   auto wait = [&](int bar, uint32_t phase) {
-    return __all_sync(0xFFFFFFFFu, waiter(bars + 8 * bar, phase & 1));
+    return __all_sync(0xFFFFFFFFu, waiter(s.smem + Lay::bars + 8 * bar, phase & 1));
   };
-  const uint32_t s_at = tmem + tile * kKeys + ((uint32_t)(w4 * 32) << 16);
-  const uint32_t o_at = tmem + Lay::kO + tile * kV + half * 64 + ((uint32_t)(w4 * 32) << 16);
-  const float c = fabsf(a.softmax_scale) * kLog2e;  // (the scores have its sign)
-  const int r = w4 * 32 + lane;
-  const uint32_t red = smem + Lay::red + (pair * 2 + half) * 128 + lane * 4;  // partner: ^ 128
-  volatile uint8_t* left = misc.left + pair * 2;
-  Walk w;
-  w.start(run);
-  uint32_t n = 0, g = 0, cleaned = 0, items = 0;
-  bool more = w.next(a);
-  if (more && w.end(tile) > w.kb) load_queries(a, w, smem, tile, warp & 7, lane);
+  float mu = -INFINITY, l = 0.0f;
 #pragma unroll 1
-  while (more) {
-    const int e = w.end(tile), mine = w.rows - tile * kM;  // rows of this tile (or less than 0)
-    const bool live = w4 * 32 < mine;  // this warp has rows
-    const uint32_t row = w.row0 + tile * kM + r;
-    const bool ok = r < mine;
-    const int seen = ok ? seen_of(a, w.q, row) - half * kC : 0;
-    const int from = max(w.kb, w.ragged());
-    float mu = -INFINITY, l = 0.0f;
-#pragma unroll 1
-    for (int kt = w.kb; kt < e; ++kt, ++n) {
-      bool fine = wait(Lay::kSFull + tile, n);
-      tc::fence_after_sync();
-      if (live) {
-        float x[kC];
-        tc::ld_32x64(s_at + half * kC, reinterpret_cast<uint32_t*>(x));
-        float cs = c;
-        if (__builtin_expect(kt >= from, 0)) {
-          const uint32_t nc = cleaned + kt - from;
-          fine &= wait(Lay::kClean + (nc & 1), nc >> 1);
-          const int lim = seen - kt * kKeys;
-          const uint32_t at = smem + Lay::flags + ((g + kt - w.kb) & 3) * 16 + half * 8;
-          bool bad = false;
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int below = min(max(lim - 32 * k, 0), 32);
-            bad |= (lds_u32(at + 4 * k) & (below == 32 ? 0xFFFFFFFFu : (1u << below) - 1)) != 0;
-          }
-          if (bad) l = NAN;
-#pragma unroll
-          for (int j = 0; j < kC; ++j) x[j] = j < lim ? x[j] * c : -INFINITY;
-          cs = 1.0f;
-        }
-        float t[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-        for (int j = 4; j < kC; j += 8)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            t[k] = j + 4 + k < kC ? fmaxf(t[k], fmaxf(x[j + k], x[j + 4 + k])) : fmaxf(t[k], x[j + k]);
-        float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * cs;
-        // (behind this barrier both warps have their scores: P goes over them)
-        if (__builtin_expect(pair_any(pair, !fine || top > mu + R::kGrow), 0)) {
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(red), "f"(top) : "memory");
-          if (lane == 0) left[half] = !fine;
-          pair_sync(pair);
-          if (left[0] | left[1]) return;  // both
-          top = fmaxf(top, __uint_as_float(lds_u32(red ^ 128)));
-          const float mn = fmaxf(mu, ceilf(top) - R::kTop);
-          const float f = mu == -INFINITY ? 0.0f : ex2(mu - mn);
-          l = l == 0.0f ? 0.0f : l * f;  // (a NaN stays)
-          mu = mn;
-          if (kt > w.kb) {  // the outputs before are done (these scores came behind them)
-#pragma unroll 1
-            for (int k = 0; k < 64; k += 16) {
-              uint32_t y[16];
-              tc::ld_32x16(o_at + k, y);
-#pragma unroll
-              for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
-              tc::st_32x16(o_at + k, y);
-            }
-            tc::wait_st();
-          }
-          pair_sync(pair);  // the maxima are read
-        }
-        const float m0 = mu == -INFINITY ? 0.0f : -mu;
-        const uint64_t c2 = f2(cs, cs), m2 = f2(m0, m0);
-        uint64_t sum[2] = {0, 0};
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {  // (16 words at a time: more do not fit the registers)
-          uint32_t pk[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float2 y = unf2(fma2(f2(x[32 * q + 2 * j], x[32 * q + 2 * j + 1]), c2, m2));
-            const float p0 = ex2(y.x), p1 = ex2(y.y);
-            sum[j & 1] = add2(sum[j & 1], f2(p0, p1));
-            pk[j] = pack16x2<F>(p0, p1);
-          }
-          tc::st_32x16(s_at + half * 32 + q * 16, pk);
-        }
-        const float2 s2 = unf2(add2(sum[0], sum[1]));
-        l += s2.x + s2.y;
-        tc::wait_st();
-      } else if (!fine) {
-        return;
-      }
+  for (int kt = 0; kt < s.count; ++kt, ++s.n) {
+    if (!wait(Lay::kSFull + s.tile, s.n)) return false;
+    tc::fence_after_sync();
+    if (!s.live) {
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bars + 8 * (Lay::kPFull + tile));
+      if (lane < 2) mbar_arrive(s.smem + Lay::bars + 8 * (Lay::kPFull + 2 * s.tile + lane));
+      continue;
     }
+    float x[kKeys];
+    tc::ld_32x64(s.s_at, reinterpret_cast<uint32_t*>(x));
+    tc::ld_32x64(s.s_at + 64, reinterpret_cast<uint32_t*>(x) + 64);
+    float cs = s.c;
+    if (__builtin_expect(kt >= s.from, 0)) {
+      const uint32_t nc = s.cleaned + kt - s.from;
+      if (!wait(Lay::kClean + (nc & 1), nc >> 1)) return false;
+      const int lim = s.seen - kt * kKeys;
+      const uint32_t at = s.smem + Lay::flags + ((s.g + kt) & 3) * 16;
+      bool bad = false;
+#pragma unroll 1
+      for (int k = 0; k < 4; ++k) {
+        const int below = min(max(lim - 32 * k, 0), 32);
+        bad |= (lds_u32(at + 4 * k) & (below == 32 ? 0xFFFFFFFFu : (1u << below) - 1)) != 0;
+      }
+      if (bad) l = NAN;
+#pragma unroll
+      for (int j = 0; j < kKeys; ++j) x[j] = j < lim ? x[j] * s.c : -INFINITY;
+      cs = 1.0f;
+    }
+    float t[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+    for (int j = 4; j < kKeys; j += 8)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        t[k] = j + 4 + k < kKeys ? fmaxf(t[k], fmaxf(x[j + k], x[j + 4 + k])) : fmaxf(t[k], x[j + k]);
+    const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * cs;
+    if (__builtin_expect(__any_sync(0xFFFFFFFFu, top > mu + R::kGrow), 0)) {
+      const float mn = fmaxf(mu, ceilf(top) - R::kTop);
+      const float f = mu == -INFINITY ? 0.0f : ex2(mu - mn);
+      l = l == 0.0f ? 0.0f : l * f;  // (a NaN stays)
+      mu = mn;
+      if (kt > 0) {  // the outputs before are done (these scores came behind them)
+#pragma unroll 1
+        for (int k = 0; k < kV; k += 16) {
+          uint32_t y[16];
+          tc::ld_32x16(s.o_at + k, y);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
+          tc::st_32x16(s.o_at + k, y);
+        }
+        tc::wait_st();
+      }
+    }
+    const float m0 = mu == -INFINITY ? 0.0f : -mu;
+    const uint64_t c2 = f2(cs, cs), m2 = f2(m0, m0);
+    uint64_t sum[2] = {0, 0};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {  // (16 words at a time)
+        uint32_t pk[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int at = 64 * h + 32 * q + 2 * j;
+          const float2 y = unf2(fma2(f2(x[at], x[at + 1]), c2, m2));
+          const float p0 = ex2(y.x), p1 = ex2(y.y);
+          sum[j & 1] = add2(sum[j & 1], f2(p0, p1));
+          pk[j] = pack16x2<F>(p0, p1);
+        }
+        tc::st_32x16(s.s_at + 32 * h + 16 * q, pk);
+      }
+      tc::wait_st();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(s.smem + Lay::bars + 8 * (Lay::kPFull + 2 * s.tile + h));
+    }
+    const float2 s2 = unf2(add2(sum[0], sum[1]));
+    l += s2.x + s2.y;
+  }
+  mu_out = mu;
+  l_out = l;
+  return true;
+}
+
+// Weights and output of one query tile; a thread has a row.  The queries' place is free when the
+// item's last scores have come: those of the next item are asked for before the output of this
+// one is written.
+template <int F>
+__device__ __forceinline__ void softmax_role(const PrefillArgs& a, uint32_t smem, uint32_t tmem,
+                                             const Waiter& waiter, int tile, int w4, int lane,
+                                             const Workspace& ws, int srows) {
+  const uint32_t bars = smem + Lay::bars;
+  const uint32_t s_at = tmem + tile * kKeys + ((uint32_t)(w4 * 32) << 16);
+  const uint32_t o_at = tmem + Lay::kO + tile * kV + ((uint32_t)(w4 * 32) << 16);
+  const int r = w4 * 32 + lane;
+  uint32_t n = 0, g = 0, cleaned = 0, opened = 0;
+  Items items{smem, 0};
+  Item it;
+  bool more = items.get(waiter, it);
+  if (more && it.end[tile] > it.kb) load_queries(a, it, smem, tile, w4, lane);
+#pragma unroll 1
+  while (more) {
+    const int count = max(it.end[tile] - it.kb, 0), mine = it.rows - tile * kM;
+    const bool live = w4 * 32 < mine, ok = r < mine;
+    const uint32_t row = it.row0 + tile * kM + r;
+    const int seen = ok ? seen_of(a, it.base, it.m, row) : 0;
+    float mu, l;
+    if (!unit_weights<F>(Part{smem, s_at, o_at, n, g, cleaned, tile, count, it.ragged() - it.kb,
+                              seen - it.kb * kKeys, live, fabsf(a.softmax_scale) * kLog2e},
+                         waiter, mu, l))
+      return;
+    n += count;
+    g += it.ke - it.kb;
+    cleaned += it.cleaned();
+    const Item past = it;
+    more = items.get(waiter, it);
+    if (more && it.end[tile] > it.kb) load_queries(a, it, smem, tile, w4, lane);
     // ---- the end of this CTA's part of the item
-    const Walk past = w;
-    g += w.ke - w.kb;
-    cleaned += w.cleaned();
-    more = w.next(a);
-    if (more && w.end(tile) > w.kb) load_queries(a, w, smem, tile, warp & 7, lane);
-    const bool any = e > past.kb;
-    bool fine = true;
-    if (any) {
-      fine = wait(Lay::kOFull + tile, items++);
+    if (count > 0) {
+      if (!__all_sync(0xFFFFFFFFu, waiter(bars + 8 * (Lay::kOFull + tile), opened & 1))) return;
+      ++opened;
       tc::fence_after_sync();
     }
     if (live) {
-      asm volatile("st.shared.f32 [%0], %1;" ::"r"(red), "f"(l) : "memory");
-      if (lane == 0) left[half] = !fine;
-      pair_sync(pair);
-      if (left[0] | left[1]) return;  // both
-      l += __uint_as_float(lds_u32(red ^ 128));
       const bool whole = past.kb == 0 && past.ke == past.tiles;
       const int64_t slot = 2 * (int64_t)blockIdx.x + (past.kb == 0 ? 1 : 0);
-      const int64_t at = slot * srows + tile * kM + r;
-      float* part = ws.o + slot * srows * kV + (int64_t)half * 64 * srows + (tile * kM + r) * 4;
+      const int at = tile * kM + r;
       const uint32_t dt = a.by_group(row);
-      const int64_t t = past.q.t0 + (int)dt;
+      const int64_t t = past.t0 + (int)dt;
       const int64_t h = (int64_t)past.head * a.group + (int)(row - dt * a.group);
-      if (ok && half == 0) {
-        if (!whole) {
-          ws.m[at] = mu;
-          ws.l[at] = l;
-        } else if (a.lse) {
-          a.lse[t * a.lse_ts + h * a.lse_hs] = l == 0.0f ? -INFINITY : (mu + __log2f(l)) * kLn2;
-        }
+      if (ok && !whole) {
+        ws.m[slot * srows + at] = mu;
+        ws.l[slot * srows + at] = l;
+      } else if (ok && a.lse) {
+        a.lse[t * a.lse_ts + h * a.lse_hs] = l == 0.0f ? -INFINITY : (mu + __log2f(l)) * kLn2;
       }
       const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
-      uint8_t* out = a.out + t * a.out_ts + h * a.out_hs + half * 128;
-      if (any) {
+      uint8_t* out = a.out + t * a.out_ts + h * a.out_hs;
+      float* part = ws.o + slot * srows * kV + at * 4;  // [dims / 4][rows][4]
+      if (count > 0) {
 #pragma unroll 1
-        for (int k = 0; k < 64; k += 32) {
-          uint32_t y[32];
-          tc::ld_32x32(o_at + k, y);
+        for (int k = 0; k < kV; k += 16) {
+          uint32_t y[16];
+          tc::ld_32x16(o_at + k, y);
           if (!ok) continue;
           if (whole) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
+            for (int j = 0; j < 16; j += 8) {
               uint32_t z[4];
 #pragma unroll
               for (int m = 0; m < 4; ++m)
@@ -675,15 +772,13 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, const Run& ru
             }
           } else {
 #pragma unroll
-            for (int j = 0; j < 32; j += 4)
+            for (int j = 0; j < 16; j += 4)
               st16(part + (int64_t)(k + j) * srows, make_uint4(y[j], y[j + 1], y[j + 2], y[j + 3]));
           }
         }
       }
-    } else if (!fine) {
-      return;
     }
-    if (any) {
+    if (count > 0) {
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + 8 * (Lay::kOFree + tile));
@@ -691,93 +786,7 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, const Run& ru
   }
 }
 
-// ------------------------------------------------------------------ scheduling
-__device__ __forceinline__ int64_t scan64(int64_t v, int lane) {  // inclusive, over the warp
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
-    if (lane >= o) v += u;
-  }
-  return v;
-}
-// This CTA's run, by the whole CTA; the scratch is the (still unused) ring.
-__device__ __noinline__ void schedule(const PrefillArgs& a, uint8_t* scratch, Run& r,
-                                      uint32_t& errbits) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int64_t* pre = reinterpret_cast<int64_t*>(scratch);  // [num_seqs]
-  int64_t* part = pre + a.num_seqs;                    // [kWarps]
-  int64_t* at = part + kWarps;                         // sequence, unit in it, item, key tile
-  for (int s = warp; s < a.num_seqs; s += kWarps) {
-    const Seq q = load_seq(a, s, errbits);
-    int64_t u = 0;
-    for (int b = lane; b < q.nb; b += 32) u += kSwitch + item_tiles(a, q, b);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
-    if (lane == 0) pre[s] = u * a.kv_heads;
-  }
-  __syncthreads();
-  const int run = (a.num_seqs + kThreads - 1) / kThreads;
-  const int s0 = min((int)threadIdx.x * run, a.num_seqs), s1 = min(s0 + run, a.num_seqs);
-  int64_t sum = 0;
-  for (int s = s0; s < s1; ++s) sum += pre[s];
-  const int64_t inc = scan64(sum, lane);
-  if (lane == 31) part[warp] = inc;
-  __syncthreads();
-  int64_t before = inc - sum, total = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += part[w];
-    total += part[w];
-  }
-  const int64_t ctas = max((int64_t)1, min((int64_t)gridDim.x, total / kMinUnits));
-  r.each = total / ctas;
-  r.extra = (int)(total - r.each * ctas);
-  r.begin = r.each * blockIdx.x + min((int)blockIdx.x, r.extra);
-  r.count = blockIdx.x < ctas ? (int)r.each + ((int)blockIdx.x < r.extra ? 1 : 0) : 0;
-  r.kt = 0;
-  if (r.count > 0)
-    for (int s = s0; s < s1; ++s) {
-      const int64_t u = pre[s];
-      if (before <= r.begin && r.begin < before + u) {
-        at[0] = s;
-        at[1] = r.begin - before;
-        at[2] = u;
-      }
-      before += u;
-    }
-  __syncthreads();
-  if (r.count > 0) {
-    uint32_t ignored = 0;
-    r.s = (int)at[0];
-    r.q = load_seq(a, r.s, ignored);
-    const int64_t per = at[2] / a.kv_heads;
-    r.head = (int)(at[1] / per);
-    if (warp == 0) {
-      const int64_t off = at[1] - r.head * per;
-      int64_t base = 0;
-      for (int b0 = 0; b0 < r.q.nb; b0 += 32) {
-        const int64_t u = b0 + lane < r.q.nb ? kSwitch + item_tiles(a, r.q, b0 + lane) : 0;
-        const int64_t in = scan64(u, lane);
-        const uint32_t hit = __ballot_sync(0xFFFFFFFFu, off < base + in);
-        if (hit) {
-          if (lane == __ffs(hit) - 1) {
-            at[3] = b0 + lane;
-            at[4] = off - (base + in - u);
-          }
-          break;
-        }
-        base += __shfl_sync(0xFFFFFFFFu, in, 31);
-      }
-    }
-  }
-  __syncthreads();
-  if (r.count > 0) {
-    r.b = (int)at[3];
-    r.kt = (int)at[4] - kSwitch;
-  }
-  tc::fence_smem_async();  // the scratch is read; copies may write there now
-  __syncthreads();
-}
-
+// ------------------------------------------------------------------ the kernel
 // After giving up: waits, bounded again, for the copies into shared memory, and a
 // millisecond for matrix products in flight (they end by themselves within microseconds).
 __device__ __noinline__ void settle(uint32_t smem, uint32_t issued, uint32_t cleaned, uint64_t limit) {
@@ -803,23 +812,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   Misc& m = *reinterpret_cast<Misc*>(smem_raw + Lay::misc);
   pdl_trigger();
-  if (threadIdx.x == 0) {
-    m.abort = 0;
-    const uint32_t bars = smem + Lay::bars;
-    for (int i = 0; i < 2; ++i) {
-      auto stall = [&](int n) { return blockIdx.x == 0 && a.stall_stage == n ? 1 : 0; };
-      mbar_init(bars + 8 * (Lay::kKFull + i), 1 + stall(i + 1));  // (one arrival too many)
-      mbar_init(bars + 8 * (Lay::kVFull + i), 1 + stall(i + 3));
-      mbar_init(bars + 8 * (Lay::kKEmpty + i), 2);
-      mbar_init(bars + 8 * (Lay::kVEmpty + i), 2);
-      mbar_init(bars + 8 * (Lay::kTurn + i), 1);
-      mbar_init(bars + 8 * (Lay::kRaw + i), 1);
-      mbar_init(bars + 8 * (Lay::kClean + i), 1);
-      mbar_init(bars + 8 * (Lay::kQFull + i), 8 * 32);
-      mbar_init(bars + 8 * (Lay::kSFull + i), 1);
-      mbar_init(bars + 8 * (Lay::kPFull + i), 8);
-      mbar_init(bars + 8 * (Lay::kOFull + i), 1);
-      mbar_init(bars + 8 * (Lay::kOFree + i), 8);
+  if (threadIdx.x == 0) m.abort = 0;
+  if (warp == 0) {
+    // arrivals of a phase, by barrier
+    for (int i = lane; i < Lay::kBars; i += 32) {
+      const int pair = i & ~1;
+      int n = pair == Lay::kKEmpty || pair == Lay::kVEmpty ? 2 : 1;
+      if (pair == Lay::kQFull) n = kM;
+      if (pair == Lay::kPFull || pair == Lay::kPFull + 2 || pair == Lay::kOFree) n = 4;
+      if (i >= Lay::kItemFree) n = kItemReaders;
+      // (testing: one arrival too many)
+      if (blockIdx.x == 0 && i < 4 && a.stall_stage == i + 1) ++n;
+      mbar_init(smem + Lay::bars + 8 * i, n);
     }
     mbar_fence_init();
   }
@@ -828,40 +832,33 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) tc::alloc(smem_addr(&m.tmem), Lay::kTmem);
   const int srows = slot_rows(a.num_tokens, a.group);
   const Workspace ws = workspace_of(a.workspace, gridDim.x, srows);
-  if (threadIdx.x == 0) ws.split[blockIdx.x] = Split{};
-  uint32_t errbits = 0;
-  Run run;
-  schedule(a, smem_raw + Lay::ring, run, errbits);
+  if (threadIdx.x == kLoadWarp * 32) ws.split[blockIdx.x] = Split{};
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, m.tmem, 0);
-  uint32_t issued = 0, cleaned = 0;
-  if (run.count > 0) {
-    if (warp < kMmaWarp) {
-      softmax_role<F>(a, run, smem, tmem, wait, warp, lane, ws, srows, m);
-      asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (warp < kLoadWarp) {
-      mma_role<F>(a, run, smem, tmem, wait, warp - kMmaWarp, lane);
-    } else if (warp == kLoadWarp) {
-      issued = load_role(a, maps, run, smem, wait, lane, ws, cleaned);
-    } else {
-      clean_role<F>(a, run, smem, wait, lane);
-    }
+  uint32_t errbits = 0, issued = 0, cleaned = 0;
+  if (warp < kMmaWarp) {
+    softmax_role<F>(a, smem, tmem, wait, warp >> 2, warp & 3, lane, ws, srows);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp < kLoadWarp) {
+    mma_role<F>(a.softmax_scale, smem, tmem, wait, warp - kMmaWarp, lane);
+  } else if (warp == kLoadWarp) {
+    issued = load_role(a, maps, smem_raw, smem, wait, lane, ws, cleaned, errbits);
+  } else {
+    clean_role<F>(smem, wait, lane);
   }
   __syncwarp();
-  if (a.err) {
+  if (a.err && warp == kLoadWarp) {
     errbits = __reduce_or_sync(0xFFFFFFFFu, errbits);
-    if (lane == 0) {
-      if (wait.given_up()) errbits |= kErrTimeout;
-      if (errbits) atomicOr(a.err, errbits);
-    }
+    if (lane == 0 && errbits) atomicOr(a.err, errbits);
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   if (__builtin_expect(wait.given_up(), 0)) {
     if (warp == kLoadWarp) settle(smem, issued, cleaned, a.wait_limit_ns);
+    if (threadIdx.x == 0 && a.err) atomicOr(a.err, kErrTimeout);
     __syncthreads();
   }
   if (warp == kMmaWarp) tc::dealloc(tmem, Lay::kTmem);
