@@ -22,13 +22,13 @@
 // (three slots a unit: 128 keys x 64 columns each) and V (two: 64 keys x 128 columns) flow by
 // TMA, in rows of 128 bytes with the 128-byte swizzle.
 //
-// Roles (12 warps): 4 warps per query tile load the queries, compute weights, a thread a row
-// (running maximum, rescaling O only when a maximum has grown by more than 2^kGrow) and write
-// the output; one per tile issues the products; one plans the CTA's items, describes them to
-// the others in shared memory and loads K and V; one looks after V rows that not every row of
-// an item sees: those behind the sequence are zeroed (they may hold anything), those with a
-// NaN or an infinity too, and noted, so that the sums of the rows that see them become NaN.
-// Each role's code is kept small and in one place: instructions are fetched cold in every
+// Roles (11 warps): 4 warps per query tile compute weights, a thread a row (running maximum,
+// rescaling O only when a maximum has grown by more than 2^kGrow) and write the output; one per
+// tile issues the products; one plans the CTA's items, describes them to the others in shared
+// memory and loads Q, K and V.  V rows that not every row of an item sees are looked after by
+// the weights' warps before their products: those behind the sequence are zeroed (they may hold
+// anything), those with a NaN or an infinity too, and noted, so that the sums of the rows that
+// see them become NaN.  Each role's code is kept small: instructions are fetched cold in every
 // launch, at about 40 cycles each where nothing else covers it.
 //
 // Waits are bounded (wait_limit_ns): one that runs out marks the CTA as given up.  Every role
@@ -53,8 +53,8 @@ constexpr int kSlot = kKeys * 128;   // bytes of a ring slot
 constexpr int kSlots = 8;
 constexpr int kUnitSlots = 5;        // 3 of K, 2 of V
 constexpr int kQTile = 3 * kM * 128;
-constexpr int kMmaWarp = 8, kLoadWarp = 10;  // and one more, that looks after V
-constexpr int kWarps = 12, kThreads = kWarps * 32;
+constexpr int kMmaWarp = 8, kLoadWarp = 10;
+constexpr int kWarps = 11, kThreads = kWarps * 32;
 constexpr int kItems = 4;            // item descriptions in shared memory
 constexpr int kItemReaders = kWarps - 1;
 constexpr int kMaxCtas = 1024;
@@ -83,7 +83,7 @@ struct Lay {
   static constexpr int bars = flags + 64;
   // Two of each: of units in turn (K and V), of the query tiles; the weights' by tile and half.
   static constexpr int kKFull = 0, kVFull = 2, kKEmpty = 4, kVEmpty = 6, kRaw = 8, kClean = 10,
-                       kQFull = 12, kSFull = 14, kPFull = 16, kOFull = 20, kOFree = 22, kTurn = 24,
+                       kQFull = 12, kQEmpty = 14, kSFull = 16, kPFull = 18, kOFull = 22, kOFree = 24,
                        kItemFull = 26, kItemFree = kItemFull + kItems, kBars = kItemFree + kItems;
   static constexpr int misc = (bars + kBars * 8 + 15) / 16 * 16;
   static constexpr int bytes = misc + 64;
@@ -98,8 +98,10 @@ struct Misc {
 
 // How a tensor map reads row p, columns c.. of key head g: box (x_head * g + c, p, z_head * g).
 struct Maps {
+  CUtensorMap qn, qp;  // (column, head, token); only where q_tokens is not 0
   CUtensorMap kn, kp, v;
   int32_t kn_x, kn_z, kp_x, kp_z, v_x, v_z;
+  int32_t q_tokens;  // tokens of a query tile that comes in boxes; 0: rows are copied one by one
 };
 
 // What the join needs of a split item; written by each CTA whose run ends inside it.  rows 0:
@@ -184,21 +186,21 @@ static_assert(sizeof(Item) <= 64, "an item's description");
 // Reads the descriptions in their order, a whole warp at a time.
 struct Items {
   uint32_t smem, next;
-  __device__ __forceinline__ bool get(const Waiter& wait, Item& it) {
-    const uint32_t i = next & (kItems - 1);
-    const uint32_t bars = smem + Lay::bars;
+  // The next one, left there (peek) or given back.
+  __device__ __forceinline__ bool get(const Waiter& wait, Item& it, bool peek = false) {
+    const uint32_t i = next & (kItems - 1), bars = smem + Lay::bars;
     if (!__all_sync(0xFFFFFFFFu, wait(bars + 8 * (Lay::kItemFull + i), (next / kItems) & 1))) return false;
-    uint4* w = reinterpret_cast<uint4*>(&it);
-#pragma unroll
-    for (int k = 0; k < (int)sizeof(Item) / 16; ++k) w[k] = lds16(smem + Lay::items + i * 64 + 16 * k);
-    if constexpr (sizeof(Item) % 16 != 0) {
-      static_assert(sizeof(Item) % 16 == 8 || sizeof(Item) % 16 == 0, "words of a description");
-      reinterpret_cast<uint2*>(&it)[sizeof(Item) / 8 - 1] =
-          lds8(smem + Lay::items + i * 64 + (int)sizeof(Item) / 8 * 8 - 8);
+    const uint32_t at = smem + Lay::items + i * 64;
+    const uint4 w0 = lds16(at), w1 = lds16(at + 16), w2 = lds16(at + 32), w3 = lds16(at + 48);
+    it.kb = w0.x, it.ke = w0.y, it.end[0] = w0.z, it.end[1] = w0.w;
+    it.tiles = w1.x, it.least = w1.y, it.most = w1.z, it.row0 = w1.w;
+    it.rows = w2.x, it.t0 = w2.y, it.head = w2.z, it.k0 = w2.w;
+    it.m = w3.x, it.base = (int64_t)((uint64_t)w3.w << 32 | w3.z);
+    if (!peek) {
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(bars + 8 * (Lay::kItemFree + i));
+      ++next;
     }
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(bars + 8 * (Lay::kItemFree + i));
-    ++next;
     return it.ke >= 0;
   }
 };
@@ -211,10 +213,11 @@ __device__ __forceinline__ uint32_t slot_of(uint32_t unit, int chunk) {
 __device__ __noinline__ int64_t divide(int64_t n, int64_t d) {
   return (n | d) >> 32 ? n / d : (int64_t)((uint32_t)n / (uint32_t)d);
 }
-__device__ __forceinline__ int64_t scan64(int64_t v, int lane) {  // inclusive, over the warp
-#pragma unroll 1
+template <typename I>
+__device__ __forceinline__ I scan(I v, int lane) {  // inclusive, over the warp
+#pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    const I u = __shfl_up_sync(0xFFFFFFFFu, v, o);
     if (lane >= o) v += u;
   }
   return v;
@@ -222,23 +225,28 @@ __device__ __forceinline__ int64_t scan64(int64_t v, int lane) {  // inclusive, 
 
 // The run of one CTA, walked item by item, by one warp.  An item is kSwitch units that stand
 // for beginning it, then its key tiles: a run starts before the first of these when kt is
-// negative.
+// negative.  I: of numbers of units (32 bits do for all but the largest calls).
+template <typename I>
 struct Plan {
   Seq q;
   int s, head, b, kt, left;
-  int64_t begin, each;   // the first unit; units of the CTAs c >= extra (each + 1 of the ones before)
+  I begin, each;   // the first unit; units of the CTAs c >= extra (each + 1 of the ones before)
   int extra, count;
-  __device__ __forceinline__ int cta_of(int64_t u) const {
-    const int64_t longer = (each + 1) * extra;
-    return (int)(u < longer ? divide(u, each + 1) : extra + divide(u - longer, each));
+  static __device__ __forceinline__ I over(I n, I d) {
+    if constexpr (sizeof(I) == 4) return (uint32_t)n / (uint32_t)d;
+    else return divide(n, d);
+  }
+  __device__ __forceinline__ int cta_of(I u) const {
+    const I longer = (each + 1) * extra;
+    return (int)(u < longer ? over(u, each + 1) : extra + over(u - longer, each));
   }
   // Where the run starts; pre: scratch for num_seqs numbers.
-  __device__ __forceinline__ void find(const PrefillArgs& a, int64_t* pre, int lane, uint32_t& errbits) {
-    int64_t total = 0;
+  __device__ __forceinline__ void find(const PrefillArgs& a, I* pre, int lane, uint32_t& errbits) {
+    I total = 0;
     uint32_t ignored = 0;
 #pragma unroll 1
     for (int s0 = 0; s0 < a.num_seqs; s0 += 32) {
-      int64_t u = 0;
+      I u = 0;
       int nb = 0;
       if (s0 + lane < a.num_seqs) {
         const Seq one = load_seq(a, s0 + lane, errbits);
@@ -251,20 +259,20 @@ struct Plan {
       for (uint32_t many = __ballot_sync(0xFFFFFFFFu, nb > 4); many; many &= many - 1) {
         const int from = __ffs(many) - 1;
         const Seq one = load_seq(a, s0 + from, ignored);
-        int64_t sum = 0;
+        I sum = 0;
 #pragma unroll 1
         for (int i = lane; i < one.nb; i += 32) sum += kSwitch + item_tiles(a, one, i);
-        sum = __shfl_sync(0xFFFFFFFFu, scan64(sum, lane), 31);
+        sum = __shfl_sync(0xFFFFFFFFu, scan<I>(sum, lane), 31);
         if (lane == from) u = sum;
       }
       u *= a.kv_heads;
-      const int64_t in = scan64(u, lane);
+      const I in = scan<I>(u, lane);
       if (s0 + lane < a.num_seqs) pre[s0 + lane] = total + in - u;
       total += __shfl_sync(0xFFFFFFFFu, in, 31);
     }
     __syncwarp();
-    const int64_t ctas = max((int64_t)1, min((int64_t)gridDim.x, total / kMinUnits));
-    each = divide(total, ctas);
+    const I ctas = max((I)1, min((I)gridDim.x, total / (I)kMinUnits));
+    each = over(total, ctas);
     extra = (int)(total - each * ctas);
     begin = each * blockIdx.x + min((int)blockIdx.x, extra);
     count = blockIdx.x < ctas ? (int)each + ((int)blockIdx.x < extra ? 1 : 0) : 0;
@@ -274,19 +282,19 @@ struct Plan {
     // one behind them does)
     int lo = 0;
 #pragma unroll 1
-    for (int step = 4096; step > 0; step >>= 1)
+    for (int step = a.num_seqs > 32 ? 2048 : 16; step > 0; step >>= 1)
       if (lo + step < a.num_seqs && pre[lo + step] <= begin) lo += step;
     s = lo;
     q = load_seq(a, s, ignored);
-    int64_t off = begin - pre[s];
-    const int64_t per = divide((s + 1 < a.num_seqs ? pre[s + 1] : total) - pre[s], a.kv_heads);
-    head = (int)divide(off, per);
+    I off = begin - pre[s];
+    const I per = over((s + 1 < a.num_seqs ? pre[s + 1] : total) - pre[s], a.kv_heads);
+    head = (int)over(off, per);
     off -= head * per;
-    int64_t base = 0;
+    I base = 0;
 #pragma unroll 1
     for (int b0 = 0;; b0 += 32) {
-      const int64_t u = b0 + lane < q.nb ? kSwitch + item_tiles(a, q, b0 + lane) : 0;
-      const int64_t in = scan64(u, lane);
+      const I u = b0 + lane < q.nb ? kSwitch + item_tiles(a, q, b0 + lane) : 0;
+      const I in = scan<I>(u, lane);
       const uint32_t hit = __ballot_sync(0xFFFFFFFFu, off < base + in);
       if (hit) {
         const int at = __ffs(hit) - 1;
@@ -335,14 +343,15 @@ struct Plan {
   }
 };
 
-// Plans the items and describes them, one ahead; K and V by TMA; where the run ends inside an
-// item, what the join needs.  Returns the copies begun, in K and V of a unit, and the units
+// Plans the items and describes them, one ahead; Q, K and V by TMA; where the run ends inside
+// an item, what the join needs.  Returns the copies begun, in K and V of a unit, and the units
 // whose V is looked after.  V of such a unit completes on a barrier of its own (two in turn),
-// which that warp waits for: it does not follow the ring through the units between, and a
-// barrier's parity tells one phase from the next only.
+// for the warps that look after it: they do not follow the ring through the units between, and
+// a barrier's parity tells one phase from the next only.
 //
 // The ring holds 8/5 units, so a unit's slots are those of K's last third and V of the unit two
 // before, and of the first two thirds of K of the unit before.
+template <typename I>
 __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& maps, uint8_t* smem_raw,
                                               uint32_t smem, const Waiter& wait, int lane,
                                               const Workspace& ws, uint32_t& cleaned, uint32_t& errbits) {
@@ -353,11 +362,11 @@ __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& 
   // rows that one item reads leave L2 first
   const uint64_t policy =
       tc::l2_policy((int64_t)a.num_tokens * a.group <= (int64_t)kItemRows * a.num_seqs);
-  Plan plan;
-  plan.find(a, reinterpret_cast<int64_t*>(smem_raw + Lay::ring), lane, errbits);
+  Plan<I> plan;
+  plan.find(a, reinterpret_cast<I*>(smem_raw + Lay::ring), lane, errbits);
   tc::fence_smem_async();  // the scratch is read; copies may write there now
   __syncwarp();
-  uint32_t g = 0, told = 0;
+  uint32_t g = 0, told = 0, filled[2] = {0, 0};
   cleaned = 0;
   Item it;
   it.ke = 0;
@@ -378,6 +387,23 @@ __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& 
     if (!first) {
       if (it.ke < 0) break;
       const int h = it.head, ragged = it.ragged();
+      if (maps.q_tokens != 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (it.end[i] <= it.kb) continue;
+          if (filled[i] > 0 && !waited(Lay::kQEmpty + i, filled[i] - 1)) return 2 * g;
+          ++filled[i];
+          if (lane == 0) {
+            const uint32_t qf = bars + 8 * (Lay::kQFull + i), dst = smem + Lay::q + i * kQTile;
+            const int t = it.t0 + ((int)(it.row0 / (uint32_t)kM) + i) * maps.q_tokens;
+            mbar_arrive_expect_tx(qf, kQTile);
+            tc::tma_load3(dst, &maps.qn, 0, h * a.group, t, qf, policy);
+            tc::tma_load3(dst + kM * 128, &maps.qn, 64, h * a.group, t, qf, policy);
+            tc::tma_load3(dst + 2 * kM * 128, &maps.qp, 0, h * a.group, t, qf, policy);
+          }
+          __syncwarp();
+        }
+      }
 #pragma unroll 1
       for (int kt = it.kb; kt < it.ke; ++kt, ++g) {
         const int row = it.k0 + kt * kKeys;
@@ -412,7 +438,7 @@ __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& 
         cleaned += clean;
       }
       if (it.ke < it.tiles && lane == 0) {  // the run's last item
-        const int64_t u0 = plan.begin + plan.count - it.ke;  // the unit of its key tile 0
+        const I u0 = plan.begin + plan.count - it.ke;  // the unit of its key tile 0
         const int c0 = plan.cta_of(u0), c1 = plan.cta_of(u0 + it.tiles - 1);
         ws.split[blockIdx.x] = Split{it.t0, it.row0, it.head, (int16_t)it.rows, (int16_t)(c1 - c0 + 1), c0, {}};
       }
@@ -420,57 +446,6 @@ __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& 
     it = nxt;
   }
   return 2 * g;
-}
-
-// The V rows that not every row of an item sees.  (Units looked after use two barriers in
-// turn: this role may be one unit ahead of the last look at its barrier, but not two, as V of
-// the next but one waits for the scores of the next.)
-template <int F>
-__device__ __forceinline__ void clean_role(uint32_t smem, const Waiter& wait, int lane) {
-  const uint32_t bars = smem + Lay::bars;
-  uint32_t g = 0, cleaned = 0;
-  const int col = lane & 7;
-  Items items{smem, 0};
-  Item it;
-#pragma unroll 1
-  while (items.get(wait, it)) {
-#pragma unroll 1
-    for (int kt = it.ragged(); kt < it.ke; ++kt) {
-      const uint32_t u = g + kt - it.kb;
-      if (!__all_sync(0xFFFFFFFFu, wait(bars + 8 * (Lay::kRaw + (cleaned & 1)), (cleaned >> 1) & 1)))
-        return;
-#pragma unroll 1
-      for (int q = 0; q < 4; ++q) {  // 32 keys
-        const int p0 = kt * kKeys + q * 32;
-        uint32_t bad = 0;
-        if (p0 + 32 > it.least) {
-          // 64 keys to a slot: two runs of 64 columns
-          const uint32_t v0 = smem + Lay::ring + slot_of(u, 3 + (q >> 1)) * kSlot + (q & 1) * 4096;
-#pragma unroll 2
-          for (int n = 0; n < 8; ++n) {
-            const int key = 4 * n + (lane >> 3), p = p0 + key;
-            const uint32_t at = v0 + key * 128 + col * 16;  // every column of the row, in any order
-            const bool sp = any_special<F>(lds16(at)) | any_special<F>(lds16(at + kSlot / 2));
-            const uint32_t votes = __ballot_sync(0xFFFFFFFFu, sp && p >= it.least && p < it.most);
-            if (p >= it.most || votes & (0xFFu << (lane & 24))) {
-              sts16(at, make_uint4(0, 0, 0, 0));
-              sts16(at + kSlot / 2, make_uint4(0, 0, 0, 0));
-            }
-            if (votes)
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (votes & (0xFFu << (8 * k))) bad |= 1u << (4 * n + k);
-          }
-        }
-        if (lane == 0) sts_u32(smem + Lay::flags + (u & 3) * 16 + q * 4, bad);
-      }
-      tc::fence_smem_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + 8 * (Lay::kClean + (cleaned & 1)));
-      ++cleaned;
-    }
-    g += it.ke - it.kb;
-  }
 }
 
 // ------------------------------------------------------------ matrix products
@@ -510,7 +485,7 @@ __device__ __forceinline__ void issue_outputs(uint32_t smem, uint32_t tmem, bool
 // tile has no part in a unit says it when they have come, so that it does not run ahead.
 template <int F>
 __device__ __forceinline__ void mma_role(float scale, uint32_t smem, uint32_t tmem, const Waiter& waiter,
-                                         int tile, int lane) {
+                                         int tile) {
   const uint32_t bars = smem + Lay::bars;
   // Looks at barriers without letting itself be suspended: waking takes long.
   auto wait = [&](int bar, uint32_t phase) {
@@ -529,35 +504,44 @@ __device__ __forceinline__ void mma_role(float scale, uint32_t smem, uint32_t tm
     const int e = it.end[tile], kb = it.kb, ke = it.ke, ragged = it.ragged();
     const uint32_t c0 = cleaned - ragged;
     cleaned += it.cleaned();
-#pragma unroll 1
-    for (int kt = kb; kt < ke; ++kt, ++g) {
-      const bool act = kt < e, begins = kt == kb;
-      if (act && begins) {
-        if (!wait(Lay::kQFull + tile, opened)) return;
-        tc::fence_smem_async();  // the queries came by ordinary copies
-      }
-      if (!wait(Lay::kKFull + (g & 1), g >> 1)) return;
-      if (act) {
-        tc::fence_after_sync();
+    // Scores of a unit (K has come), and its K given back.
+    auto scores = [&](int kt, uint32_t g) {
+      if (kt < e) {
         issue_scores<F>(smem, tmem, one, tile, g, negate);
         tc::commit(one, bars + 8 * (Lay::kSFull + tile));
+        if (kt + 1 == e) tc::commit(one, bars + 8 * (Lay::kQEmpty + tile));
       }
       tc::commit(one, bars + 8 * (Lay::kKEmpty + (g & 1)));
+    };
+    if (kb < e) {
+      if (!wait(Lay::kQFull + tile, opened)) return;
+      tc::fence_smem_async();  // (the queries may have come by ordinary copies)
+    }
+    if (!wait(Lay::kKFull + (g & 1), g >> 1)) return;
+    tc::fence_after_sync();
+    scores(kb, g);
+#pragma unroll 1
+    for (int kt = kb; kt < ke; ++kt, ++g) {
+      const bool act = kt < e;
       if (!wait(Lay::kVFull + (g & 1), g >> 1)) return;
       if (act) {
         if (kt >= ragged && !wait(Lay::kClean + ((c0 + kt) & 1), (c0 + kt) >> 1)) return;
         // the sums of the item before are read
-        if (begins && opened++ > 0 && !wait(Lay::kOFree + tile, opened)) return;
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          if (!wait(Lay::kPFull + 2 * tile + h, done)) return;
-          tc::fence_after_sync();
-          issue_outputs<F>(smem, tmem, one, tile, g, h, begins);
-        }
-        ++done;
+        if (kt == kb && opened++ > 0 && !wait(Lay::kOFree + tile, opened)) return;
+        if (!wait(Lay::kPFull + 2 * tile, done)) return;
+        tc::fence_after_sync();
+        issue_outputs<F>(smem, tmem, one, tile, g, 0, kt == kb);
+      }
+      // (here, so that nothing stands between the outputs and the next scores)
+      if (kt + 1 < ke && !wait(Lay::kKFull + ((g + 1) & 1), (g + 1) >> 1)) return;
+      if (act) {
+        if (!wait(Lay::kPFull + 2 * tile + 1, done++)) return;
+        tc::fence_after_sync();
+        issue_outputs<F>(smem, tmem, one, tile, g, 1, kt == kb);
         if (kt + 1 == e) tc::commit(one, bars + 8 * (Lay::kOFull + tile));
       }
       tc::commit(one, bars + 8 * (Lay::kVEmpty + (g & 1)));
+      if (kt + 1 < ke) scores(kt + 1, g + 1);
     }
   }
 }
@@ -574,7 +558,8 @@ __device__ __forceinline__ uint32_t pack16x2(float lo, float hi) {
   else return pack_bf16x2(lo, hi);
 }
 
-// The queries of a tile by asynchronous copies, by the tile's four warps.
+// The queries of a tile by asynchronous copies, by the tile's four warps (where they do not come
+// in boxes: a group of query heads that does not divide a tile, or heads with a stride of 0).
 __device__ __forceinline__ void load_queries(const PrefillArgs& a, const Item& it, uint32_t smem,
                                              int tile, int w4, int lane) {
   const int col = lane & 7;
@@ -600,10 +585,38 @@ struct Part {
   uint32_t smem, s_at, o_at;  // tensor memory: this warp's scores and sums
   uint32_t n, g, cleaned;     // units of this tile, of all, and looked after, before the part
   int tile, count, from;      // key tiles, and the first that not every row sees whole
-  int seen;                   // keys that this thread's row sees, from the first tile on
+  int mend;                   // this tile looks after V from this key tile on
+  int least, most;            // keys that the item's first and last row see, from the first tile on
+  int seen;                   // and this thread's
   bool live;                  // the warp has rows
   float c;                    // weights: exp2(c score - reference)
 };
+// This warp's 32 keys of V of a unit: rows from key `most` on (of the tile's) are zeroed, those
+// from `least` on with a NaN or an infinity too, and noted.
+template <int F>
+__device__ __noinline__ void look_after(uint32_t v, uint32_t flag, int least, int most) {
+  const int lane = threadIdx.x & 31, col = lane & 7;
+  uint32_t bad = 0;
+#pragma unroll 2
+  for (int n = 0; n < 8; ++n) {
+    const int key = 4 * n + (lane >> 3);
+    const uint32_t at = v + key * 128 + col * 16;  // every column of the row, in any order
+    const bool sp = any_special<F>(lds16(at)) | any_special<F>(lds16(at + kSlot / 2));
+    const uint32_t votes = __ballot_sync(0xFFFFFFFFu, sp && key >= least && key < most);
+    if (key >= most || votes & (0xFFu << (lane & 24))) {
+      sts16(at, make_uint4(0, 0, 0, 0));
+      sts16(at + kSlot / 2, make_uint4(0, 0, 0, 0));
+    }
+    if (votes)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (votes & (0xFFu << (8 * k))) bad |= 1u << (4 * n + k);
+  }
+  if (lane == 0) sts_u32(flag, bad);
+  tc::fence_smem_async();
+  __syncwarp();
+}
+
 // The weights of an item's units (a function of its own, so that its loop has the registers to
 // itself): the row's reference and the sum of its weights.  False: given up.
 template <int F>
@@ -618,6 +631,17 @@ __device__ __noinline__ bool unit_weights(Part s, const Waiter waiter, float& mu
   for (int kt = 0; kt < s.count; ++kt, ++s.n) {
     if (!wait(Lay::kSFull + s.tile, s.n)) return false;
     tc::fence_after_sync();
+    const uint32_t nc = s.cleaned + kt - s.from, u = s.g + kt;
+    if (__builtin_expect(kt >= s.mend, 0)) {
+      // (behind the scores: the barrier's phase before is past then)
+      const int w4 = (threadIdx.x >> 5) & 3;
+      if (!wait(Lay::kRaw + (nc & 1), nc >> 1)) return false;
+      // 64 keys to a slot: two runs of 64 columns
+      look_after<F>(s.smem + Lay::ring + slot_of(u, 3 + (w4 >> 1)) * kSlot + (w4 & 1) * 4096,
+                    s.smem + Lay::flags + (u & 3) * 16 + w4 * 4, s.least - kt * kKeys - w4 * 32,
+                    s.most - kt * kKeys - w4 * 32);
+      if (lane == 0) mbar_arrive(s.smem + Lay::bars + 8 * (Lay::kClean + (nc & 1)));
+    }
     if (!s.live) {
       tc::fence_before_sync();
       __syncwarp();
@@ -627,12 +651,10 @@ __device__ __noinline__ bool unit_weights(Part s, const Waiter waiter, float& mu
     float x[kKeys];
     tc::ld_32x64(s.s_at, reinterpret_cast<uint32_t*>(x));
     tc::ld_32x64(s.s_at + 64, reinterpret_cast<uint32_t*>(x) + 64);
-    float cs = s.c;
     if (__builtin_expect(kt >= s.from, 0)) {
-      const uint32_t nc = s.cleaned + kt - s.from;
       if (!wait(Lay::kClean + (nc & 1), nc >> 1)) return false;
       const int lim = s.seen - kt * kKeys;
-      const uint32_t at = s.smem + Lay::flags + ((s.g + kt) & 3) * 16;
+      const uint32_t at = s.smem + Lay::flags + (u & 3) * 16;
       bool bad = false;
 #pragma unroll 1
       for (int k = 0; k < 4; ++k) {
@@ -641,8 +663,7 @@ __device__ __noinline__ bool unit_weights(Part s, const Waiter waiter, float& mu
       }
       if (bad) l = NAN;
 #pragma unroll
-      for (int j = 0; j < kKeys; ++j) x[j] = j < lim ? x[j] * s.c : -INFINITY;
-      cs = 1.0f;
+      for (int j = 0; j < kKeys; ++j) x[j] = j < lim ? x[j] : -INFINITY;
     }
     float t[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
@@ -650,7 +671,7 @@ __device__ __noinline__ bool unit_weights(Part s, const Waiter waiter, float& mu
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         t[k] = j + 4 + k < kKeys ? fmaxf(t[k], fmaxf(x[j + k], x[j + 4 + k])) : fmaxf(t[k], x[j + k]);
-    const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * cs;
+    const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * s.c;
     if (__builtin_expect(__any_sync(0xFFFFFFFFu, top > mu + R::kGrow), 0)) {
       const float mn = fmaxf(mu, ceilf(top) - R::kTop);
       const float f = mu == -INFINITY ? 0.0f : ex2(mu - mn);
@@ -669,7 +690,7 @@ __device__ __noinline__ bool unit_weights(Part s, const Waiter waiter, float& mu
       }
     }
     const float m0 = mu == -INFINITY ? 0.0f : -mu;
-    const uint64_t c2 = f2(cs, cs), m2 = f2(m0, m0);
+    const uint64_t c2 = f2(s.c, s.c), m2 = f2(m0, m0);
     uint64_t sum[2] = {0, 0};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -699,11 +720,15 @@ __device__ __noinline__ bool unit_weights(Part s, const Waiter waiter, float& mu
   return true;
 }
 
-// Weights and output of one query tile; a thread has a row.  The queries' place is free when the
-// item's last scores have come: those of the next item are asked for before the output of this
-// one is written.
+__device__ __forceinline__ void st32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+               "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// Weights and output of one query tile; a thread has a row.
 template <int F>
-__device__ __forceinline__ void softmax_role(const PrefillArgs& a, uint32_t smem, uint32_t tmem,
+__device__ __forceinline__ void softmax_role(const PrefillArgs& a, bool boxes, uint32_t smem, uint32_t tmem,
                                              const Waiter& waiter, int tile, int w4, int lane,
                                              const Workspace& ws, int srows) {
   const uint32_t bars = smem + Lay::bars;
@@ -713,25 +738,31 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, uint32_t smem
   uint32_t n = 0, g = 0, cleaned = 0, opened = 0;
   Items items{smem, 0};
   Item it;
-  bool more = items.get(waiter, it);
-  if (more && it.end[tile] > it.kb) load_queries(a, it, smem, tile, w4, lane);
+  // The queries' place is free when the item's last scores have come: those of the next item are
+  // asked for before the output of this one is written.
+  auto queries = [&] {
+    Item nxt;
+    if (!boxes && items.get(waiter, nxt, true) && nxt.end[tile] > nxt.kb)
+      load_queries(a, nxt, smem, tile, w4, lane);
+  };
+  queries();
 #pragma unroll 1
-  while (more) {
+  while (items.get(waiter, it)) {
     const int count = max(it.end[tile] - it.kb, 0), mine = it.rows - tile * kM;
     const bool live = w4 * 32 < mine, ok = r < mine;
     const uint32_t row = it.row0 + tile * kM + r;
-    const int seen = ok ? seen_of(a, it.base, it.m, row) : 0;
+    const int seen = ok ? seen_of(a, it.base, it.m, row) : 0, shift = it.kb * kKeys;
     float mu, l;
     if (!unit_weights<F>(Part{smem, s_at, o_at, n, g, cleaned, tile, count, it.ragged() - it.kb,
-                              seen - it.kb * kKeys, live, fabsf(a.softmax_scale) * kLog2e},
+                              max(it.ragged(), tile ? it.end[0] : 0) - it.kb, it.least - shift,
+                              it.most - shift, seen - shift, live,
+                              fmaxf(fabsf(a.softmax_scale) * kLog2e, 1e-37f)},
                          waiter, mu, l))
       return;
     n += count;
     g += it.ke - it.kb;
     cleaned += it.cleaned();
-    const Item past = it;
-    more = items.get(waiter, it);
-    if (more && it.end[tile] > it.kb) load_queries(a, it, smem, tile, w4, lane);
+    queries();
     // ---- the end of this CTA's part of the item
     if (count > 0) {
       if (!__all_sync(0xFFFFFFFFu, waiter(bars + 8 * (Lay::kOFull + tile), opened & 1))) return;
@@ -739,41 +770,46 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, uint32_t smem
       tc::fence_after_sync();
     }
     if (live) {
-      const bool whole = past.kb == 0 && past.ke == past.tiles;
-      const int64_t slot = 2 * (int64_t)blockIdx.x + (past.kb == 0 ? 1 : 0);
-      const int at = tile * kM + r;
+      const bool whole = it.kb == 0 && it.ke == it.tiles;
       const uint32_t dt = a.by_group(row);
-      const int64_t t = past.t0 + (int)dt;
-      const int64_t h = (int64_t)past.head * a.group + (int)(row - dt * a.group);
+      const int64_t t = it.t0 + (int)dt;
+      const int64_t h = (int64_t)it.head * a.group + (int)(row - dt * a.group);
+      const int64_t slot = (2 * (int64_t)blockIdx.x + (it.kb == 0 ? 1 : 0)) * srows;
+      const int at = tile * kM + r;
       if (ok && !whole) {
-        ws.m[slot * srows + at] = mu;
-        ws.l[slot * srows + at] = l;
+        ws.m[slot + at] = mu;
+        ws.l[slot + at] = l;
       } else if (ok && a.lse) {
         a.lse[t * a.lse_ts + h * a.lse_hs] = l == 0.0f ? -INFINITY : (mu + __log2f(l)) * kLn2;
       }
       const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
-      uint8_t* out = a.out + t * a.out_ts + h * a.out_hs;
-      float* part = ws.o + slot * srows * kV + at * 4;  // [dims / 4][rows][4]
+      // where 32 dims of the row go, and how far the next lie
+      uint8_t* to = whole ? a.out + t * a.out_ts + h * a.out_hs
+                          : reinterpret_cast<uint8_t*>(ws.o + slot * kV + at * 4);  // [dims / 4][rows][4]
       if (count > 0) {
 #pragma unroll 1
-        for (int k = 0; k < kV; k += 16) {
-          uint32_t y[16];
-          tc::ld_32x16(o_at + k, y);
-          if (!ok) continue;
-          if (whole) {
+        for (int k = 0; k < kV; k += 32) {
+          uint32_t y[32];
+          tc::ld_32x32(o_at + k, y);
+          if (ok && whole) {
+            uint32_t z[16];
 #pragma unroll
-            for (int j = 0; j < 16; j += 8) {
-              uint32_t z[4];
+            for (int j = 0; j < 16; ++j)
+              z[j] = pack16x2<F>(__uint_as_float(y[2 * j]) * inv, __uint_as_float(y[2 * j + 1]) * inv);
+            if (a.out_32) {
+              st32(to, z);
+              st32(to + 32, z + 8);
+            } else {
 #pragma unroll
-              for (int m = 0; m < 4; ++m)
-                z[m] = pack16x2<F>(__uint_as_float(y[j + 2 * m]) * inv,
-                                   __uint_as_float(y[j + 2 * m + 1]) * inv);
-              st16(out + (k + j) * 2, make_uint4(z[0], z[1], z[2], z[3]));
+              for (int j = 0; j < 16; j += 4) st16(to + 4 * j, make_uint4(z[j], z[j + 1], z[j + 2], z[j + 3]));
             }
-          } else {
+            to += 64;
+          } else if (ok) {
 #pragma unroll
-            for (int j = 0; j < 16; j += 4)
-              st16(part + (int64_t)(k + j) * srows, make_uint4(y[j], y[j + 1], y[j + 2], y[j + 3]));
+            for (int j = 0; j < 32; j += 4) {
+              st16(to, make_uint4(y[j], y[j + 1], y[j + 2], y[j + 3]));
+              to += (int64_t)srows * 16;
+            }
           }
         }
       }
@@ -818,8 +854,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = lane; i < Lay::kBars; i += 32) {
       const int pair = i & ~1;
       int n = pair == Lay::kKEmpty || pair == Lay::kVEmpty ? 2 : 1;
-      if (pair == Lay::kQFull) n = kM;
-      if (pair == Lay::kPFull || pair == Lay::kPFull + 2 || pair == Lay::kOFree) n = 4;
+      if (pair == Lay::kQFull && maps.q_tokens == 0) n = kM;
+      if (pair == Lay::kPFull || pair == Lay::kPFull + 2 || pair == Lay::kOFree || pair == Lay::kClean) n = 4;
       if (i >= Lay::kItemFree) n = kItemReaders;
       // (testing: one arrival too many)
       if (blockIdx.x == 0 && i < 4 && a.stall_stage == i + 1) ++n;
@@ -839,14 +875,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, m.tmem, 0);
   uint32_t errbits = 0, issued = 0, cleaned = 0;
   if (warp < kMmaWarp) {
-    softmax_role<F>(a, smem, tmem, wait, warp >> 2, warp & 3, lane, ws, srows);
+    softmax_role<F>(a, maps.q_tokens != 0, smem, tmem, wait, warp >> 2, warp & 3, lane, ws, srows);
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp < kLoadWarp) {
-    mma_role<F>(a.softmax_scale, smem, tmem, wait, warp - kMmaWarp, lane);
-  } else if (warp == kLoadWarp) {
-    issued = load_role(a, maps, smem_raw, smem, wait, lane, ws, cleaned, errbits);
+    mma_role<F>(a.softmax_scale, smem, tmem, wait, warp - kMmaWarp);
   } else {
-    clean_role<F>(smem, wait, lane);
+    issued = a.few_units ? load_role<int32_t>(a, maps, smem_raw, smem, wait, lane, ws, cleaned, errbits)
+                         : load_role<int64_t>(a, maps, smem_raw, smem, wait, lane, ws, cleaned, errbits);
   }
   __syncwarp();
   if (a.err && warp == kLoadWarp) {
@@ -867,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // -------------------------------------------------------- join of the split items
 // Block (x, c) looks at what CTA c left.  An item of `parts` CTAs is dealt to the warps of the
 // blocks of all of them but the last: 8 rows x 16 dims a warp, a lane four dims of a row.
-constexpr int kJoinWarps = 8, kJoinBlocks = 8;
+constexpr int kJoinWarps = 8, kJoinBlocks = 32;
 
 template <int F>
 __global__ void __launch_bounds__(kJoinWarps * 32) prefill_join_kernel(const PrefillArgs a) {
@@ -957,8 +992,32 @@ bool make_map(CUtensorMap* map, const void* base, int fmt, int width, int64_t hs
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The queries of a tile as boxes of 64 columns x the key head's query heads x tokens; 0 tokens
+// where there is no such box.
+int query_maps(const PrefillArgs& a, int fmt, Maps* maps) {
+  const TensorMapEncode encode = tensor_map_encode();
+  if (!encode || kM % a.group != 0) return 0;
+  const cuuint32_t box[3] = {64, (cuuint32_t)a.group, (cuuint32_t)(kM / a.group)}, unit[3] = {1, 1, 1};
+  const CUtensorMapDataType type =
+      fmt == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  auto make = [&](CUtensorMap* map, const uint8_t* base, int width, int64_t hs, int64_t ts) {
+    // (strides of dimensions of one are not used, and may be anything)
+    if (a.num_heads == 1) hs = 16 * width;
+    if (a.num_tokens == 1) ts = 16 * width;
+    if (hs <= 0 || ts <= 0 || hs >= (int64_t(1) << 40) || ts >= (int64_t(1) << 40)) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)a.num_heads, (cuuint64_t)a.num_tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)hs, (cuuint64_t)ts};
+    return encode(map, type, 3, const_cast<uint8_t*>(base), dims, strides, box, unit,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  return make(&maps->qn, a.q_nope, 128, a.qn_hs, a.qn_ts) && make(&maps->qp, a.q_pe, 64, a.qp_hs, a.qp_ts)
+             ? kM / a.group
+             : 0;
+}
+
 template <int F>
-cudaError_t launch_tc(const PrefillArgs& a, int ctas, const LaunchCfg& cfg) {
+cudaError_t launch_tc(PrefillArgs a, int ctas, const LaunchCfg& cfg) {
   Maps maps = {};
   const bool none = a.num_kv == 0;
   const int64_t rows = none ? 1 : a.num_kv;
@@ -970,6 +1029,10 @@ cudaError_t launch_tc(const PrefillArgs& a, int ctas, const LaunchCfg& cfg) {
       !make_map(&maps.v, none ? a.q_nope : a.v, F, 128, a.v_hs, heads, a.v_ts, rows, kKeys / 2,
                 &maps.v_x, &maps.v_z))
     return cudaErrorInvalidValue;
+  maps.q_tokens = query_maps(a, F, &maps);
+  a.out_32 = ((reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)a.out_ts | (uintptr_t)a.out_hs) & 31) == 0;
+  const int64_t items = (((int64_t)a.num_tokens * a.group + kItemRows - 1) / kItemRows + a.num_seqs) * a.kv_heads;
+  a.few_units = items * (a.num_kv / kKeys + 2 + kSwitch) < INT32_MAX;
   auto kern = prefill_attention_kernel<F>;
   // the attribute stays with the device's context: set on a device's first call
   static std::atomic<uint64_t> set{0};

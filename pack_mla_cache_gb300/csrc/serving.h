@@ -142,6 +142,7 @@ struct PrefillArgs {
   float softmax_scale;
   const float* kv_scale;  // fp8 keys and values only
   bool causal;
+  bool few_units, out_32;  // units are counted in 32 bits; out rows on 32-byte boundaries (set by the launch)
   uint8_t* out;
   int64_t out_ts, out_hs;
   float* lse;  // may be null
