@@ -7,20 +7,27 @@
 //
 // Shape of the work.  The query rows of a sequence and key head (token-major, the key
 // head's query heads inside) are cut into items of 256 rows, two tiles of 128, its keys
-// into tiles of 128; one unit = (item, key tile).  The units of the whole call, in
+// into tiles of 64; one unit = (item, key tile).  The units of the whole call, in
 // (sequence, key head, item, key tile) order, are cut into equal contiguous runs, one per
 // CTA (one CTA per SM), so ragged and causal batches load every SM alike.  An item whose
 // units fall into several CTAs leaves unnormalised fp32 partial sums in the workspace, which
 // a second launch joins in the order of the CTAs (no atomics: equal calls give equal bits).
 //
-// A unit: S_i = Q_i K^T (two tiles of 128 x 128, k = 192), weights P_i = exp2(S_i - reference)
-// written over S_i in tensor memory as 16-bit values, O_i += P_i V (128 x 128).  Tensor memory
-// is full: two S and two O of 128 columns.  The products of a unit and tile take 1280 cycles;
-// while a tile's weights are computed, the other tile's products run.
+// A unit: S_i = Q_i K^T (two tiles of 128 x 64, k = 192), weights P_i = exp2(S_i - reference)
+// written over S_i in tensor memory as 16-bit values, O_i += P_i V (128 x 128, k = 64).  Tensor
+// memory is full: two S of 64 columns and an O of 128 per query tile.  With two S the scores of
+// the next unit are there when the weights of one are done, and the tensor core does not wait
+// for weights.
 //
-// Shared memory: the two query tiles (96 KB), and a ring of 8 slots of 16 KB through which K
-// (three slots a unit: 128 keys x 64 columns each) and V (two: 64 keys x 128 columns) flow by
-// TMA, in rows of 128 bytes with the 128-byte swizzle.
+// Why 64 keys.  Beside the queries (96 KB) there is room for 1.6 units of 128 keys, and K of a
+// unit came later than the products before it were done (2000 cycles for 32 KB; 16384 tokens
+// 1100 us, in every order of the products tried).  Three stages of 64 keys hold two units ahead.
+// The price: a product 128 x 64 x 16 with both operands in shared memory takes 49 cycles where
+// one of 128 columns takes 64 (shared memory's reads bound it), so a unit of both tiles is 1690
+// cycles of the tensor core where 1280 would do.
+//
+// Shared memory: the two query tiles (96 KB), three stages of K (24 KB: three runs of 64 columns)
+// and of V (16 KB: two), in rows of 128 bytes with the 128-byte swizzle, by TMA.
 //
 // Roles (11 warps): 4 warps per query tile compute weights, a thread a row (running maximum,
 // rescaling O only when a maximum has grown by more than 2^kGrow) and write the output; one per
@@ -47,11 +54,10 @@ namespace {
 constexpr int kSimpleThreads = 256;
 constexpr int kM = 128;              // query rows of a tile
 constexpr int kItemRows = 2 * kM;
-constexpr int kKeys = 128;           // keys of a tile
+constexpr int kKeys = 64;            // keys of a tile
 constexpr int kV = 128;
-constexpr int kSlot = kKeys * 128;   // bytes of a ring slot
-constexpr int kSlots = 8;
-constexpr int kUnitSlots = 5;        // 3 of K, 2 of V
+constexpr int kRun = kKeys * 128;    // bytes of 64 columns of a key tile
+constexpr int kStages = 3;
 constexpr int kQTile = 3 * kM * 128;
 constexpr int kMmaWarp = 8, kLoadWarp = 10;
 constexpr int kWarps = 11, kThreads = kWarps * 32;
@@ -62,8 +68,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // What beginning another item costs a CTA, in units: the runs are cut as if each item had
 // this many more.
-constexpr int kSwitch = 1;
-constexpr int kMinUnits = 2;  // a CTA takes at least this many
+constexpr int kSwitch = 2;
+constexpr int kMinUnits = 4;  // a CTA takes at least this many
 
 // The reference of a row's weights is the next whole number (log2) above its maximum less
 // kTop; a score may pass the reference by kGrow before the sums are rescaled.  fp16 weights:
@@ -77,19 +83,24 @@ struct Ref {
 // shared memory
 struct Lay {
   static constexpr int q = 0;
-  static constexpr int ring = 2 * kQTile;
-  static constexpr int items = ring + kSlots * kSlot;     // Item [kItems]
-  static constexpr int flags = items + kItems * 64;       // uint32 [4 units][4]: keys with bad V rows
-  static constexpr int bars = flags + 64;
-  // Two of each: of units in turn (K and V), of the query tiles; the weights' by tile and half.
-  static constexpr int kKFull = 0, kVFull = 2, kKEmpty = 4, kVEmpty = 6, kRaw = 8, kClean = 10,
-                       kQFull = 12, kQEmpty = 14, kSFull = 16, kPFull = 18, kOFull = 22, kOFree = 24,
-                       kItemFull = 26, kItemFree = kItemFull + kItems, kBars = kItemFree + kItems;
+  static constexpr int k = 2 * kQTile;                    // [kStages][3 runs]
+  static constexpr int v = k + kStages * 3 * kRun;        // [kStages][2 runs]
+  static constexpr int items = v + kStages * 2 * kRun;    // Item [kItems]
+  static constexpr int flags = items + kItems * 64;       // uint32 [4 units][2]: keys with bad V rows
+  static constexpr int bars = flags + 32;
+  // Barriers: of the stages; of units looked after, in turn; of the query tiles (scores, weights
+  // and outputs two each, in turn: the weights' warps may be one unit behind the scores and one
+  // ahead of the outputs, and a phase's parity has to be told from the one before); of the items.
+  static constexpr int kKFull = 0, kVFull = kKFull + kStages, kKEmpty = kVFull + kStages,
+                       kVEmpty = kKEmpty + kStages, kClean = kVEmpty + kStages, kRaw = kClean + 4,
+                       kQFull = kRaw + 2, kQEmpty = kQFull + 2, kSFull = kQEmpty + 2,
+                       kPFull = kSFull + 4, kPvDone = kPFull + 4, kOFree = kPvDone + 4,
+                       kItemFull = kOFree + 2, kItemFree = kItemFull + kItems, kBars = kItemFree + kItems;
   static constexpr int misc = (bars + kBars * 8 + 15) / 16 * 16;
   static constexpr int bytes = misc + 64;
   static_assert(bytes <= 232448, "shared memory of a CTA");
-  // tensor memory columns: S of both tiles (P in their first half), O of both tiles
-  static constexpr int kO = 2 * kKeys, kTmem = 512;
+  // tensor memory columns: two S of each tile (P in their first half), O of both tiles
+  static constexpr int kO = 4 * kKeys, kTmem = 512;
 };
 struct Misc {
   uint32_t tmem;
@@ -205,9 +216,17 @@ struct Items {
   }
 };
 
-__device__ __forceinline__ uint32_t slot_of(uint32_t unit, int chunk) {
-  return (unit * kUnitSlots + chunk) & (kSlots - 1);
-}
+// A place in a ring of kStages: which stage, and the parity of its phase.
+struct Stage {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void step() {
+    if (++at == kStages) {
+      at = 0;
+      phase ^= 1;
+    }
+  }
+};
 
 // -------------------------------------------------------------- plan and load
 __device__ __noinline__ int64_t divide(int64_t n, int64_t d) {
@@ -344,17 +363,11 @@ struct Plan {
 };
 
 // Plans the items and describes them, one ahead; Q, K and V by TMA; where the run ends inside
-// an item, what the join needs.  Returns the copies begun, in K and V of a unit, and the units
-// whose V is looked after.  V of such a unit completes on a barrier of its own (two in turn),
-// for the warps that look after it: they do not follow the ring through the units between, and
-// a barrier's parity tells one phase from the next only.
-//
-// The ring holds 8/5 units, so a unit's slots are those of K's last third and V of the unit two
-// before, and of the first two thirds of K of the unit before.
+// an item, what the join needs.  Returns the copies begun, in K and V of a unit.
 template <typename I>
 __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& maps, uint8_t* smem_raw,
                                               uint32_t smem, const Waiter& wait, int lane,
-                                              const Workspace& ws, uint32_t& cleaned, uint32_t& errbits) {
+                                              const Workspace& ws, uint32_t& errbits) {
   const uint32_t bars = smem + Lay::bars;
   auto waited = [&](int bar, uint32_t phase) {
     return __all_sync(0xFFFFFFFFu, wait(bars + 8 * bar, phase & 1));
@@ -363,11 +376,11 @@ __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& 
   const uint64_t policy =
       tc::l2_policy((int64_t)a.num_tokens * a.group <= (int64_t)kItemRows * a.num_seqs);
   Plan<I> plan;
-  plan.find(a, reinterpret_cast<I*>(smem_raw + Lay::ring), lane, errbits);
+  plan.find(a, reinterpret_cast<I*>(smem_raw + Lay::k), lane, errbits);
   tc::fence_smem_async();  // the scratch is read; copies may write there now
   __syncwarp();
   uint32_t g = 0, told = 0, filled[2] = {0, 0};
-  cleaned = 0;
+  Stage st;
   Item it;
   it.ke = 0;
   // The first round only plans.
@@ -386,7 +399,7 @@ __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& 
     }
     if (!first) {
       if (it.ke < 0) break;
-      const int h = it.head, ragged = it.ragged();
+      const int h = it.head;
       if (maps.q_tokens != 0) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -405,37 +418,25 @@ __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& 
         }
       }
 #pragma unroll 1
-      for (int kt = it.kb; kt < it.ke; ++kt, ++g) {
+      for (int kt = it.kb; kt < it.ke; ++kt, ++g, st.step()) {
         const int row = it.k0 + kt * kKeys;
-        const bool clean = kt >= ragged;
-        auto dst = [&](int c) { return smem + Lay::ring + slot_of(g, c) * kSlot; };
-        const uint32_t kf = bars + 8 * (Lay::kKFull + (g & 1));
+        const uint32_t kf = bars + 8 * (Lay::kKFull + st.at), vf = bars + 8 * (Lay::kVFull + st.at);
+        const uint32_t k = smem + Lay::k + st.at * 3 * kRun, v = smem + Lay::v + st.at * 2 * kRun;
+        if (g >= kStages && !waited(Lay::kKEmpty + st.at, st.phase ^ 1)) return 2 * g;
         if (lane == 0) {
-          mbar_arrive_expect_tx(kf, 3 * kSlot);
-          tc::tma_load3(dst(0), &maps.kn, h * maps.kn_x, row, h * maps.kn_z, kf, policy);
+          mbar_arrive_expect_tx(kf, 3 * kRun);
+          tc::tma_load3(k, &maps.kn, h * maps.kn_x, row, h * maps.kn_z, kf, policy);
+          tc::tma_load3(k + kRun, &maps.kn, h * maps.kn_x + 64, row, h * maps.kn_z, kf, policy);
+          tc::tma_load3(k + 2 * kRun, &maps.kp, h * maps.kp_x, row, h * maps.kp_z, kf, policy);
         }
         __syncwarp();
-        if (g >= 2 && !waited(Lay::kVEmpty + (g & 1), (g - 2) >> 1)) return 2 * g;
+        if (g >= kStages && !waited(Lay::kVEmpty + st.at, st.phase ^ 1)) return 2 * g + 1;
         if (lane == 0) {
-          tc::tma_load3(dst(1), &maps.kn, h * maps.kn_x + 64, row, h * maps.kn_z, kf, policy);
-          tc::tma_load3(dst(2), &maps.kp, h * maps.kp_x, row, h * maps.kp_z, kf, policy);
+          mbar_arrive_expect_tx(vf, 2 * kRun);
+          tc::tma_load3(v, &maps.v, h * maps.v_x, row, h * maps.v_z, vf, policy);
+          tc::tma_load3(v + kRun, &maps.v, h * maps.v_x + 64, row, h * maps.v_z, vf, policy);
         }
         __syncwarp();
-        if (g >= 1 && !waited(Lay::kKEmpty + ((g - 1) & 1), (g - 1) >> 1)) return 2 * g + 1;
-        if (lane == 0) {
-          uint32_t vf = bars + 8 * (Lay::kVFull + (g & 1));
-          if (clean) {
-            mbar_arrive(vf);
-            vf = bars + 8 * (Lay::kRaw + (cleaned & 1));
-          }
-          mbar_arrive_expect_tx(vf, 2 * kSlot);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)  // 64 keys x 64 columns each
-            tc::tma_load3(dst(3 + (k >> 1)) + (k & 1) * (kSlot / 2), &maps.v, h * maps.v_x + 64 * (k & 1),
-                          row + 64 * (k >> 1), h * maps.v_z, vf, policy);
-        }
-        __syncwarp();
-        cleaned += clean;
       }
       if (it.ke < it.tiles && lane == 0) {  // the run's last item
         const I u0 = plan.begin + plan.count - it.ke;  // the unit of its key tile 0
@@ -450,42 +451,43 @@ __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& 
 
 // ------------------------------------------------------------ matrix products
 template <int F>
-__device__ __forceinline__ void issue_scores(uint32_t smem, uint32_t tmem, bool one, int tile,
-                                             uint32_t unit, uint32_t negate) {
+__device__ __forceinline__ void issue_scores(uint32_t smem, uint32_t tmem, bool one, int tile, int stage,
+                                             uint32_t buffer, uint32_t negate) {
   const uint32_t id = negate | tc::instr_desc(kM, kKeys, false, F == kBF16, F == kBF16);
-  const uint32_t i = __shfl_sync(0xFFFFFFFFu, tile, 0), g = __shfl_sync(0xFFFFFFFFu, unit, 0);
+  const uint32_t i = __shfl_sync(0xFFFFFFFFu, tile, 0), st = __shfl_sync(0xFFFFFFFFu, stage, 0);
+  const uint32_t b = __shfl_sync(0xFFFFFFFFu, buffer, 0);
   const uint64_t qa = tc::smem_desc(smem + Lay::q + i * kQTile, 0, 1024);
-  const uint32_t d = tmem + i * kKeys;
+  const uint64_t kb = tc::smem_desc(smem + Lay::k + st * 3 * kRun, 0, 1024);
+  const uint32_t d = tmem + (2 * i + b) * kKeys;
 #pragma unroll
-  for (int c = 0; c < 3; ++c) {
-    const uint64_t kb = tc::smem_desc(smem + Lay::ring + slot_of(g, c) * kSlot, 0, 1024);
+  for (int c = 0; c < 3; ++c)
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      tc::mma_16bit(one, d, qa + (c * kM * 128 >> 4) + 2 * k, kb + 2 * k, id, c + k > 0);
-  }
+      tc::mma_16bit(one, d, qa + (c * kM * 128 >> 4) + 2 * k, kb + (c * kRun >> 4) + 2 * k, id, c + k > 0);
 }
-// Half of the keys: a slot of V, MN-major (two runs of 64 columns).
+// V MN-major (two runs of 64 columns).
 template <int F>
-__device__ __forceinline__ void issue_outputs(uint32_t smem, uint32_t tmem, bool one, int tile,
-                                              uint32_t unit, int half_, bool first) {
+__device__ __forceinline__ void issue_outputs(uint32_t smem, uint32_t tmem, bool one, int tile, int stage,
+                                              uint32_t buffer, bool first) {
   constexpr uint32_t kId = tc::instr_desc(kM, kV, false, F == kBF16, F == kBF16, true);
-  const uint32_t i = __shfl_sync(0xFFFFFFFFu, tile, 0), g = __shfl_sync(0xFFFFFFFFu, unit, 0);
-  const uint32_t half = __shfl_sync(0xFFFFFFFFu, half_, 0);
-  const uint32_t p = tmem + i * kKeys + half * 32, d = tmem + Lay::kO + i * kV;
-  const uint64_t vb = tc::smem_desc(smem + Lay::ring + slot_of(g, 3 + half) * kSlot, kSlot / 2, 1024);
+  const uint32_t i = __shfl_sync(0xFFFFFFFFu, tile, 0), st = __shfl_sync(0xFFFFFFFFu, stage, 0);
+  const uint32_t b = __shfl_sync(0xFFFFFFFFu, buffer, 0);
+  const uint32_t p = tmem + (2 * i + b) * kKeys, d = tmem + Lay::kO + i * kV;
+  const uint64_t vb = tc::smem_desc(smem + Lay::v + st * 2 * kRun, kRun, 1024);
 #pragma unroll
   for (int k = 0; k < 4; ++k)
-    tc::mma_16bit_ta(one, d, p + 8 * k, vb + k * (2048 >> 4), kId, half + k > 0 || !first);
+    tc::mma_16bit_ta(one, d, p + 8 * k, vb + k * (2048 >> 4), kId, k > 0 || !first);
 }
 
-// A warp issues the products of one query tile, whose chain is serial: scores of a unit behind
-// the outputs of the one before, over whose weights they go.  The other tile's products fill
-// the gaps.  (One warp for both took 4900 cycles a unit, most of them its own instructions
-// between the products.)  K and V of a unit are free when both warps have said so; a warp whose
-// tile has no part in a unit says it when they have come, so that it does not run ahead.
+// A warp issues the products of one query tile: the scores of the next unit, then the outputs
+// of this one when its weights have come.  (One warp for both tiles spent most of its time on
+// its own instructions between the products.)  Scores go over the weights of two units before,
+// whose outputs were issued earlier: products are done in the order of their issue.  K and V of
+// a unit are free when both warps have said so; a warp whose tile has no part in a unit says it
+// when they have come, so that it does not run ahead.
 template <int F>
 __device__ __forceinline__ void mma_role(float scale, uint32_t smem, uint32_t tmem, const Waiter& waiter,
-                                         int tile) {
+                                         int tile, int lane) {
   const uint32_t bars = smem + Lay::bars;
   // Looks at barriers without letting itself be suspended: waking takes long.
   auto wait = [&](int bar, uint32_t phase) {
@@ -496,52 +498,53 @@ __device__ __forceinline__ void mma_role(float scale, uint32_t smem, uint32_t tm
   };
   const bool one = tc::elect();
   const uint32_t negate = scale < 0.0f ? 1u << 13 : 0u;  // of the scores, by the tensor core
-  uint32_t g = 0, done = 0, opened = 0, cleaned = 0;
+  uint32_t scored = 0, done = 0, opened = 0, cleaned = 0;  // units (two), items, units looked after
+  Stage sk, sv;
   Items items{smem, 0};
   Item it;
 #pragma unroll 1
   while (items.get(waiter, it)) {
     const int e = it.end[tile], kb = it.kb, ke = it.ke, ragged = it.ragged();
+    const int mine = tile ? max(ragged, it.end[0]) : ragged;  // this tile looks after V from here on
     const uint32_t c0 = cleaned - ragged;
     cleaned += it.cleaned();
-    // Scores of a unit (K has come), and its K given back.
-    auto scores = [&](int kt, uint32_t g) {
-      if (kt < e) {
-        issue_scores<F>(smem, tmem, one, tile, g, negate);
-        tc::commit(one, bars + 8 * (Lay::kSFull + tile));
-        if (kt + 1 == e) tc::commit(one, bars + 8 * (Lay::kQEmpty + tile));
-      }
-      tc::commit(one, bars + 8 * (Lay::kKEmpty + (g & 1)));
-    };
     if (kb < e) {
       if (!wait(Lay::kQFull + tile, opened)) return;
       tc::fence_smem_async();  // (the queries may have come by ordinary copies)
     }
-    if (!wait(Lay::kKFull + (g & 1), g >> 1)) return;
-    tc::fence_after_sync();
-    scores(kb, g);
+    // One round ahead with the scores.
 #pragma unroll 1
-    for (int kt = kb; kt < ke; ++kt, ++g) {
-      const bool act = kt < e;
-      if (!wait(Lay::kVFull + (g & 1), g >> 1)) return;
-      if (act) {
-        if (kt >= ragged && !wait(Lay::kClean + ((c0 + kt) & 1), (c0 + kt) >> 1)) return;
+    for (int kt = kb - 1; kt < ke; ++kt) {
+      if (kt + 1 < ke) {
+        if (!wait(Lay::kKFull + sk.at, sk.phase)) return;
+        tc::fence_after_sync();
+        if (kt + 1 < e) {
+          issue_scores<F>(smem, tmem, one, tile, sk.at, scored & 1, negate);
+          tc::commit(one, bars + 8 * (Lay::kSFull + 2 * tile + (scored & 1)));
+          ++scored;
+          if (kt + 2 == e) tc::commit(one, bars + 8 * (Lay::kQEmpty + tile));
+        }
+        tc::commit(one, bars + 8 * (Lay::kKEmpty + sk.at));
+        sk.step();
+      }
+      if (kt < kb) continue;
+      if (!wait(Lay::kVFull + sv.at, sv.phase)) return;
+      if (kt < e) {
+        if (kt >= ragged) {
+          if (kt >= mine && lane == 0) mbar_arrive(bars + 8 * (Lay::kRaw + tile));
+          __syncwarp();
+          if (!wait(Lay::kClean + ((c0 + kt) & 3), (c0 + kt) >> 2)) return;
+        }
         // the sums of the item before are read
         if (kt == kb && opened++ > 0 && !wait(Lay::kOFree + tile, opened)) return;
-        if (!wait(Lay::kPFull + 2 * tile, done)) return;
+        if (!wait(Lay::kPFull + 2 * tile + (done & 1), done >> 1)) return;
         tc::fence_after_sync();
-        issue_outputs<F>(smem, tmem, one, tile, g, 0, kt == kb);
+        issue_outputs<F>(smem, tmem, one, tile, sv.at, done & 1, kt == kb);
+        tc::commit(one, bars + 8 * (Lay::kPvDone + 2 * tile + (done & 1)));
+        ++done;
       }
-      // (here, so that nothing stands between the outputs and the next scores)
-      if (kt + 1 < ke && !wait(Lay::kKFull + ((g + 1) & 1), (g + 1) >> 1)) return;
-      if (act) {
-        if (!wait(Lay::kPFull + 2 * tile + 1, done++)) return;
-        tc::fence_after_sync();
-        issue_outputs<F>(smem, tmem, one, tile, g, 1, kt == kb);
-        if (kt + 1 == e) tc::commit(one, bars + 8 * (Lay::kOFull + tile));
-      }
-      tc::commit(one, bars + 8 * (Lay::kVEmpty + (g & 1)));
-      if (kt + 1 < ke) scores(kt + 1, g + 1);
+      tc::commit(one, bars + 8 * (Lay::kVEmpty + sv.at));
+      sv.step();
     }
   }
 }
@@ -584,6 +587,8 @@ __device__ __forceinline__ void load_queries(const PrefillArgs& a, const Item& i
 struct Part {
   uint32_t smem, s_at, o_at;  // tensor memory: this warp's scores and sums
   uint32_t n, g, cleaned;     // units of this tile, of all, and looked after, before the part
+  uint32_t mended;            // and looked after by this tile's warps
+  int stage;                  // of V of the part's first unit
   int tile, count, from;      // key tiles, and the first that not every row sees whole
   int mend;                   // this tile looks after V from this key tile on
   int least, most;            // keys that the item's first and last row see, from the first tile on
@@ -591,30 +596,30 @@ struct Part {
   bool live;                  // the warp has rows
   float c;                    // weights: exp2(c score - reference)
 };
-// This warp's 32 keys of V of a unit: rows from key `most` on (of the tile's) are zeroed, those
-// from `least` on with a NaN or an infinity too, and noted.
+// This warp's 16 keys of V of a unit: rows from key `most` on (of these) are zeroed, those from
+// `least` on with a NaN or an infinity too; returns which.
 template <int F>
-__device__ __noinline__ void look_after(uint32_t v, uint32_t flag, int least, int most) {
+__device__ __noinline__ uint32_t look_after(uint32_t v, int least, int most) {
   const int lane = threadIdx.x & 31, col = lane & 7;
   uint32_t bad = 0;
 #pragma unroll 2
-  for (int n = 0; n < 8; ++n) {
+  for (int n = 0; n < 4; ++n) {
     const int key = 4 * n + (lane >> 3);
     const uint32_t at = v + key * 128 + col * 16;  // every column of the row, in any order
-    const bool sp = any_special<F>(lds16(at)) | any_special<F>(lds16(at + kSlot / 2));
+    const bool sp = any_special<F>(lds16(at)) | any_special<F>(lds16(at + kRun));
     const uint32_t votes = __ballot_sync(0xFFFFFFFFu, sp && key >= least && key < most);
     if (key >= most || votes & (0xFFu << (lane & 24))) {
       sts16(at, make_uint4(0, 0, 0, 0));
-      sts16(at + kSlot / 2, make_uint4(0, 0, 0, 0));
+      sts16(at + kRun, make_uint4(0, 0, 0, 0));
     }
     if (votes)
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         if (votes & (0xFFu << (8 * k))) bad |= 1u << (4 * n + k);
   }
-  if (lane == 0) sts_u32(flag, bad);
   tc::fence_smem_async();
   __syncwarp();
+  return bad;
 }
 
 // The weights of an item's units (a function of its own, so that its loop has the registers to
@@ -629,39 +634,38 @@ __device__ __noinline__ bool unit_weights(Part s, const Waiter waiter, float& mu
   float mu = -INFINITY, l = 0.0f;
 #pragma unroll 1
   for (int kt = 0; kt < s.count; ++kt, ++s.n) {
-    if (!wait(Lay::kSFull + s.tile, s.n)) return false;
+    if (!wait(Lay::kSFull + 2 * s.tile + (s.n & 1), s.n >> 1)) return false;
     tc::fence_after_sync();
-    const uint32_t nc = s.cleaned + kt - s.from, u = s.g + kt;
+    const uint32_t bars = s.smem + Lay::bars, nc = s.cleaned + kt - s.from;
+    const uint32_t flags = s.smem + Lay::flags + ((s.g + kt) & 3) * 8;
     if (__builtin_expect(kt >= s.mend, 0)) {
-      // (behind the scores: the barrier's phase before is past then)
       const int w4 = (threadIdx.x >> 5) & 3;
-      if (!wait(Lay::kRaw + (nc & 1), nc >> 1)) return false;
-      // 64 keys to a slot: two runs of 64 columns
-      look_after<F>(s.smem + Lay::ring + slot_of(u, 3 + (w4 >> 1)) * kSlot + (w4 & 1) * 4096,
-                    s.smem + Lay::flags + (u & 3) * 16 + w4 * 4, s.least - kt * kKeys - w4 * 32,
-                    s.most - kt * kKeys - w4 * 32);
-      if (lane == 0) mbar_arrive(s.smem + Lay::bars + 8 * (Lay::kClean + (nc & 1)));
+      if (!wait(Lay::kRaw + s.tile, s.mended++)) return false;
+      const int stage = (s.stage + kt) % kStages;
+      const uint32_t bad = look_after<F>(s.smem + Lay::v + stage * 2 * kRun + w4 * 2048,
+                                         s.least - kt * kKeys - w4 * 16, s.most - kt * kKeys - w4 * 16);
+      if (lane == 0) {
+        sts_u16(flags + w4 * 2, bad);
+        mbar_arrive(bars + 8 * (Lay::kClean + (nc & 3)));
+      }
     }
     if (!s.live) {
       tc::fence_before_sync();
       __syncwarp();
-      if (lane < 2) mbar_arrive(s.smem + Lay::bars + 8 * (Lay::kPFull + 2 * s.tile + lane));
+      if (lane == 0) mbar_arrive(bars + 8 * (Lay::kPFull + 2 * s.tile + (s.n & 1)));
       continue;
     }
+    const uint32_t s_at = s.s_at + (s.n & 1) * kKeys;
     float x[kKeys];
-    tc::ld_32x64(s.s_at, reinterpret_cast<uint32_t*>(x));
-    tc::ld_32x64(s.s_at + 64, reinterpret_cast<uint32_t*>(x) + 64);
+    tc::ld_32x64(s_at, reinterpret_cast<uint32_t*>(x));
     if (__builtin_expect(kt >= s.from, 0)) {
-      if (!wait(Lay::kClean + (nc & 1), nc >> 1)) return false;
+      if (!wait(Lay::kClean + (nc & 3), nc >> 2)) return false;
       const int lim = s.seen - kt * kKeys;
-      const uint32_t at = s.smem + Lay::flags + (u & 3) * 16;
-      bool bad = false;
-#pragma unroll 1
-      for (int k = 0; k < 4; ++k) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
         const int below = min(max(lim - 32 * k, 0), 32);
-        bad |= (lds_u32(at + 4 * k) & (below == 32 ? 0xFFFFFFFFu : (1u << below) - 1)) != 0;
+        if ((lds_u32(flags + 4 * k) & (below == 32 ? 0xFFFFFFFFu : (1u << below) - 1)) != 0) l = NAN;
       }
-      if (bad) l = NAN;
 #pragma unroll
       for (int j = 0; j < kKeys; ++j) x[j] = j < lim ? x[j] : -INFINITY;
     }
@@ -677,7 +681,9 @@ __device__ __noinline__ bool unit_weights(Part s, const Waiter waiter, float& mu
       const float f = mu == -INFINITY ? 0.0f : ex2(mu - mn);
       l = l == 0.0f ? 0.0f : l * f;  // (a NaN stays)
       mu = mn;
-      if (kt > 0) {  // the outputs before are done (these scores came behind them)
+      if (kt > 0) {
+        if (!wait(Lay::kPvDone + 2 * s.tile + ((s.n - 1) & 1), (s.n - 1) >> 1)) return false;
+        tc::fence_after_sync();
 #pragma unroll 1
         for (int k = 0; k < kV; k += 16) {
           uint32_t y[16];
@@ -692,28 +698,21 @@ __device__ __noinline__ bool unit_weights(Part s, const Waiter waiter, float& mu
     const float m0 = mu == -INFINITY ? 0.0f : -mu;
     const uint64_t c2 = f2(s.c, s.c), m2 = f2(m0, m0);
     uint64_t sum[2] = {0, 0};
+    uint32_t* pk = reinterpret_cast<uint32_t*>(x);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {  // (16 words at a time)
-        uint32_t pk[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int at = 64 * h + 32 * q + 2 * j;
-          const float2 y = unf2(fma2(f2(x[at], x[at + 1]), c2, m2));
-          const float p0 = ex2(y.x), p1 = ex2(y.y);
-          sum[j & 1] = add2(sum[j & 1], f2(p0, p1));
-          pk[j] = pack16x2<F>(p0, p1);
-        }
-        tc::st_32x16(s.s_at + 32 * h + 16 * q, pk);
-      }
-      tc::wait_st();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(s.smem + Lay::bars + 8 * (Lay::kPFull + 2 * s.tile + h));
+    for (int j = 0; j < kKeys / 2; ++j) {
+      const float2 y = unf2(fma2(f2(x[2 * j], x[2 * j + 1]), c2, m2));
+      const float p0 = ex2(y.x), p1 = ex2(y.y);
+      sum[j & 1] = add2(sum[j & 1], f2(p0, p1));
+      pk[j] = pack16x2<F>(p0, p1);
     }
+    tc::st_32x32(s_at, pk);
     const float2 s2 = unf2(add2(sum[0], sum[1]));
     l += s2.x + s2.y;
+    tc::wait_st();
+    tc::fence_before_sync();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + 8 * (Lay::kPFull + 2 * s.tile + (s.n & 1)));
   }
   mu_out = mu;
   l_out = l;
@@ -732,10 +731,10 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, bool boxes, u
                                              const Waiter& waiter, int tile, int w4, int lane,
                                              const Workspace& ws, int srows) {
   const uint32_t bars = smem + Lay::bars;
-  const uint32_t s_at = tmem + tile * kKeys + ((uint32_t)(w4 * 32) << 16);
+  const uint32_t s_at = tmem + tile * 2 * kKeys + ((uint32_t)(w4 * 32) << 16);
   const uint32_t o_at = tmem + Lay::kO + tile * kV + ((uint32_t)(w4 * 32) << 16);
   const int r = w4 * 32 + lane;
-  uint32_t n = 0, g = 0, cleaned = 0, opened = 0;
+  uint32_t n = 0, g = 0, cleaned = 0, mended = 0;
   Items items{smem, 0};
   Item it;
   // The queries' place is free when the item's last scores have come: those of the next item are
@@ -752,21 +751,21 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, bool boxes, u
     const bool live = w4 * 32 < mine, ok = r < mine;
     const uint32_t row = it.row0 + tile * kM + r;
     const int seen = ok ? seen_of(a, it.base, it.m, row) : 0, shift = it.kb * kKeys;
+    const int mend = max(it.ragged(), tile ? it.end[0] : 0);
     float mu, l;
-    if (!unit_weights<F>(Part{smem, s_at, o_at, n, g, cleaned, tile, count, it.ragged() - it.kb,
-                              max(it.ragged(), tile ? it.end[0] : 0) - it.kb, it.least - shift,
-                              it.most - shift, seen - shift, live,
-                              fmaxf(fabsf(a.softmax_scale) * kLog2e, 1e-37f)},
+    if (!unit_weights<F>(Part{smem, s_at, o_at, n, g, cleaned, mended, (int)(g % kStages), tile, count,
+                              it.ragged() - it.kb, mend - it.kb, it.least - shift, it.most - shift,
+                              seen - shift, live, fmaxf(fabsf(a.softmax_scale) * kLog2e, 1e-37f)},
                          waiter, mu, l))
       return;
+    mended += max(it.end[tile] - mend, 0);
     n += count;
     g += it.ke - it.kb;
     cleaned += it.cleaned();
     queries();
     // ---- the end of this CTA's part of the item
     if (count > 0) {
-      if (!__all_sync(0xFFFFFFFFu, waiter(bars + 8 * (Lay::kOFull + tile), opened & 1))) return;
-      ++opened;
+      if (!__all_sync(0xFFFFFFFFu, waiter(bars + 8 * (Lay::kPvDone + 2 * tile + ((n - 1) & 1)), ((n - 1) >> 1) & 1))) return;
       tc::fence_after_sync();
     }
     if (live) {
@@ -825,17 +824,13 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, bool boxes, u
 // ------------------------------------------------------------------ the kernel
 // After giving up: waits, bounded again, for the copies into shared memory, and a
 // millisecond for matrix products in flight (they end by themselves within microseconds).
-__device__ __noinline__ void settle(uint32_t smem, uint32_t issued, uint32_t cleaned, uint64_t limit) {
+__device__ __noinline__ void settle(uint32_t smem, uint32_t issued, uint64_t limit) {
   const uint64_t since = global_ns();
-  for (uint32_t i = cleaned > 2 ? cleaned - 2 : 0; i < cleaned; ++i)
-    while (!mbar_try_wait(smem + Lay::bars + 8 * (Lay::kRaw + (i & 1)), (i >> 1) & 1) &&
-           global_ns() - since <= limit) {
+  for (uint32_t i = issued > 2 * kStages ? issued - 2 * kStages : 0; i < issued; ++i) {
+    const uint32_t u = i >> 1, bar = (i & 1 ? Lay::kVFull : Lay::kKFull) + u % kStages;
+    while (!mbar_try_wait(smem + Lay::bars + 8 * bar, (u / kStages) & 1) && global_ns() - since <= limit) {
     }
-  for (uint32_t i = issued > 4 ? issued - 4 : 0; i < issued; ++i)
-    while (!mbar_try_wait(smem + Lay::bars + 8 * ((i & 1 ? Lay::kVFull : Lay::kKFull) + ((i >> 1) & 1)),
-                          (i >> 2) & 1) &&
-           global_ns() - since <= limit) {
-    }
+  }
   while (global_ns() - since <= 1000000) {
   }
 }
@@ -852,13 +847,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // arrivals of a phase, by barrier
     for (int i = lane; i < Lay::kBars; i += 32) {
-      const int pair = i & ~1;
-      int n = pair == Lay::kKEmpty || pair == Lay::kVEmpty ? 2 : 1;
-      if (pair == Lay::kQFull && maps.q_tokens == 0) n = kM;
-      if (pair == Lay::kPFull || pair == Lay::kPFull + 2 || pair == Lay::kOFree || pair == Lay::kClean) n = 4;
+      auto of = [&](int bar, int many) { return i >= bar && i < bar + many; };
+      int n = of(Lay::kKEmpty, 2 * kStages) ? 2 : 1;
+      if (of(Lay::kQFull, 2) && maps.q_tokens == 0) n = kM;
+      if (of(Lay::kPFull, 4) || of(Lay::kOFree, 2) || of(Lay::kClean, 4)) n = 4;
       if (i >= Lay::kItemFree) n = kItemReaders;
       // (testing: one arrival too many)
-      if (blockIdx.x == 0 && i < 4 && a.stall_stage == i + 1) ++n;
+      if (blockIdx.x == 0 && i < 2 * kStages && a.stall_stage == i + 1) ++n;
       mbar_init(smem + Lay::bars + 8 * i, n);
     }
     mbar_fence_init();
@@ -873,15 +868,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, m.tmem, 0);
-  uint32_t errbits = 0, issued = 0, cleaned = 0;
+  uint32_t errbits = 0, issued = 0;
   if (warp < kMmaWarp) {
     softmax_role<F>(a, maps.q_tokens != 0, smem, tmem, wait, warp >> 2, warp & 3, lane, ws, srows);
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp < kLoadWarp) {
-    mma_role<F>(a.softmax_scale, smem, tmem, wait, warp - kMmaWarp);
+    mma_role<F>(a.softmax_scale, smem, tmem, wait, warp - kMmaWarp, lane);
   } else {
-    issued = a.few_units ? load_role<int32_t>(a, maps, smem_raw, smem, wait, lane, ws, cleaned, errbits)
-                         : load_role<int64_t>(a, maps, smem_raw, smem, wait, lane, ws, cleaned, errbits);
+    issued = a.few_units ? load_role<int32_t>(a, maps, smem_raw, smem, wait, lane, ws, errbits)
+                         : load_role<int64_t>(a, maps, smem_raw, smem, wait, lane, ws, errbits);
   }
   __syncwarp();
   if (a.err && warp == kLoadWarp) {
@@ -892,7 +887,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   if (__builtin_expect(wait.given_up(), 0)) {
-    if (warp == kLoadWarp) settle(smem, issued, cleaned, a.wait_limit_ns);
+    if (warp == kLoadWarp) settle(smem, issued, a.wait_limit_ns);
     if (threadIdx.x == 0 && a.err) atomicOr(a.err, kErrTimeout);
     __syncthreads();
   }
@@ -961,10 +956,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefill_join_kernel(const Pre
 
 // ------------------------------------------------------------------ launches
 // Rows of keys (or values) of all heads as a tensor map with boxes of 64 columns and
-// `box_rows` rows.  Heads inside a row are columns of it, so that any head stride does; otherwise (heads
+// 64 rows.  Heads inside a row are columns of it, so that any head stride does; otherwise (heads
 // apart) the third dimension.  `base` stands in for arrays without rows.
 bool make_map(CUtensorMap* map, const void* base, int fmt, int width, int64_t hs, int heads, int64_t ts,
-              int64_t rows, int box_rows, int32_t* x_head, int32_t* z_head) {
+              int64_t rows, int32_t* x_head, int32_t* z_head) {
   const TensorMapEncode encode = tensor_map_encode();
   if (!encode) return false;
   const int es = is16(fmt) ? 2 : 1;
@@ -984,7 +979,7 @@ bool make_map(CUtensorMap* map, const void* base, int fmt, int width, int64_t hs
     }
   }
   if (dims[0] > INT32_MAX) return false;
-  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, unit[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, kKeys, 1}, unit[3] = {1, 1, 1};
   const CUtensorMapDataType type =
       fmt == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   return encode(map, type, 3, const_cast<void*>(base), dims, strides, box, unit,
@@ -1022,11 +1017,11 @@ cudaError_t launch_tc(PrefillArgs a, int ctas, const LaunchCfg& cfg) {
   const bool none = a.num_kv == 0;
   const int64_t rows = none ? 1 : a.num_kv;
   const int heads = none ? 1 : a.kv_heads;
-  if (!make_map(&maps.kn, none ? a.q_nope : a.k_nope, F, 128, a.kn_hs, heads, a.kn_ts, rows, kKeys,
+  if (!make_map(&maps.kn, none ? a.q_nope : a.k_nope, F, 128, a.kn_hs, heads, a.kn_ts, rows,
                 &maps.kn_x, &maps.kn_z) ||
-      !make_map(&maps.kp, none ? a.q_nope : a.k_pe, F, 64, a.kp_hs, heads, a.kp_ts, rows, kKeys,
+      !make_map(&maps.kp, none ? a.q_nope : a.k_pe, F, 64, a.kp_hs, heads, a.kp_ts, rows,
                 &maps.kp_x, &maps.kp_z) ||
-      !make_map(&maps.v, none ? a.q_nope : a.v, F, 128, a.v_hs, heads, a.v_ts, rows, kKeys / 2,
+      !make_map(&maps.v, none ? a.q_nope : a.v, F, 128, a.v_hs, heads, a.v_ts, rows,
                 &maps.v_x, &maps.v_z))
     return cudaErrorInvalidValue;
   maps.q_tokens = query_maps(a, F, &maps);
