@@ -29,9 +29,9 @@
 // Shared memory: the two query tiles (96 KB), three stages of K (24 KB: three runs of 64 columns)
 // and of V (16 KB: two), in rows of 128 bytes with the 128-byte swizzle, by TMA.
 //
-// Roles (11 warps): 4 warps per query tile compute weights, a thread a row (running maximum,
-// rescaling O only when a maximum has grown by more than 2^kGrow) and write the output; one per
-// tile issues the products; one plans the CTA's items, describes them to the others in shared
+// Roles (13 warps): 4 warps per query tile compute weights, a thread a row (running maximum,
+// rescaling O only when a maximum has grown by more than 2^kGrow) and write the output; two per
+// tile issue the products, scores and outputs; one plans the CTA's items, describes them to the others in shared
 // memory and loads Q, K and V.  V rows that not every row of an item sees are looked after by
 // the weights' warps before their products: those behind the sequence are zeroed (they may hold
 // anything), those with a NaN or an infinity too, and noted, so that the sums of the rows that
@@ -59,8 +59,8 @@ constexpr int kV = 128;
 constexpr int kRun = kKeys * 128;    // bytes of 64 columns of a key tile
 constexpr int kStages = 3;
 constexpr int kQTile = 3 * kM * 128;
-constexpr int kMmaWarp = 8, kLoadWarp = 10;
-constexpr int kWarps = 11, kThreads = kWarps * 32;
+constexpr int kScoreWarp = 8, kOutWarp = 10, kLoadWarp = 12;
+constexpr int kWarps = 13, kThreads = kWarps * 32;
 constexpr int kItems = 4;            // item descriptions in shared memory
 constexpr int kItemReaders = kWarps - 1;
 constexpr int kMaxCtas = 1024;
@@ -479,27 +479,63 @@ __device__ __forceinline__ void issue_outputs(uint32_t smem, uint32_t tmem, bool
     tc::mma_16bit_ta(one, d, p + 8 * k, vb + k * (2048 >> 4), kId, k > 0 || !first);
 }
 
-// A warp issues the products of one query tile: the scores of the next unit, then the outputs
-// of this one when its weights have come.  (One warp for both tiles spent most of its time on
-// its own instructions between the products.)  Scores go over the weights of two units before,
-// whose outputs were issued earlier: products are done in the order of their issue.  K and V of
-// a unit are free when both warps have said so; a warp whose tile has no part in a unit says it
-// when they have come, so that it does not run ahead.
-template <int F>
-__device__ __forceinline__ void mma_role(float scale, uint32_t smem, uint32_t tmem, const Waiter& waiter,
-                                         int tile, int lane) {
-  const uint32_t bars = smem + Lay::bars;
-  // Looks at barriers without letting itself be suspended: waking takes long.
-  auto wait = [&](int bar, uint32_t phase) {
+// Four warps issue the products: scores and outputs of a query tile each.  An issue waits for
+// the products before it, and what a warp does between two of its products (looks at barriers,
+// signals) leaves the tensor core idle unless another warp's products are there: 16384 tokens
+// took 1380 us with one warp for all, 1060 with one per tile.  K and V of a unit are free when
+// both tiles' warps have said so; a warp whose tile has no part in a unit says it when they have
+// come, so that it does not run ahead.
+//
+// Looks at a barrier without letting the warp be suspended: waking takes long.
+__device__ __forceinline__ bool spin(const Waiter& waiter, uint32_t bar, uint32_t phase) {
 #pragma unroll 1
-    for (int spin = 0; spin < 64; ++spin)
-      if (__any_sync(0xFFFFFFFFu, mbar_test(bars + 8 * bar, phase & 1))) return true;
-    return (bool)__all_sync(0xFFFFFFFFu, waiter(bars + 8 * bar, phase & 1));
-  };
+  for (int n = 0; n < 64; ++n)
+    if (__any_sync(0xFFFFFFFFu, mbar_test(bar, phase & 1))) return true;
+  return __all_sync(0xFFFFFFFFu, waiter(bar, phase & 1));
+}
+template <int F>
+__device__ __forceinline__ void score_role(float scale, uint32_t smem, uint32_t tmem, const Waiter& waiter,
+                                           int tile) {
+  const uint32_t bars = smem + Lay::bars;
+  auto wait = [&](int bar, uint32_t phase) { return spin(waiter, bars + 8 * bar, phase); };
   const bool one = tc::elect();
   const uint32_t negate = scale < 0.0f ? 1u << 13 : 0u;  // of the scores, by the tensor core
-  uint32_t scored = 0, done = 0, opened = 0, cleaned = 0;  // units (two), items, units looked after
-  Stage sk, sv;
+  uint32_t n = 0, opened = 0;  // units, items of this tile
+  Stage st;
+  Items items{smem, 0};
+  Item it;
+#pragma unroll 1
+  while (items.get(waiter, it)) {
+    const int e = it.end[tile], kb = it.kb, ke = it.ke;
+    if (kb < e) {
+      if (!wait(Lay::kQFull + tile, opened++)) return;
+      tc::fence_smem_async();  // (the queries may have come by ordinary copies)
+    }
+#pragma unroll 1
+    for (int kt = kb; kt < ke; ++kt) {
+      // the outputs of two units before have read the weights that these scores go over
+      if (kt < e && n >= 2 && !wait(Lay::kPvDone + 2 * tile + (n & 1), (n >> 1) - 1)) return;
+      if (!wait(Lay::kKFull + st.at, st.phase)) return;
+      if (kt < e) {
+        tc::fence_after_sync();
+        issue_scores<F>(smem, tmem, one, tile, st.at, n & 1, negate);
+        tc::commit(one, bars + 8 * (Lay::kSFull + 2 * tile + (n & 1)));
+        if (kt + 1 == e) tc::commit(one, bars + 8 * (Lay::kQEmpty + tile));
+        ++n;
+      }
+      tc::commit(one, bars + 8 * (Lay::kKEmpty + st.at));
+      st.step();
+    }
+  }
+}
+template <int F>
+__device__ __forceinline__ void output_role(uint32_t smem, uint32_t tmem, const Waiter& waiter, int tile,
+                                            int lane) {
+  const uint32_t bars = smem + Lay::bars;
+  auto wait = [&](int bar, uint32_t phase) { return spin(waiter, bars + 8 * bar, phase); };
+  const bool one = tc::elect();
+  uint32_t n = 0, opened = 0, cleaned = 0;  // units, items of this tile; units looked after
+  Stage st;
   Items items{smem, 0};
   Item it;
 #pragma unroll 1
@@ -508,43 +544,25 @@ __device__ __forceinline__ void mma_role(float scale, uint32_t smem, uint32_t tm
     const int mine = tile ? max(ragged, it.end[0]) : ragged;  // this tile looks after V from here on
     const uint32_t c0 = cleaned - ragged;
     cleaned += it.cleaned();
-    if (kb < e) {
-      if (!wait(Lay::kQFull + tile, opened)) return;
-      tc::fence_smem_async();  // (the queries may have come by ordinary copies)
-    }
-    // One round ahead with the scores.
+    // the sums of the item before are read
+    if (kb < e && opened++ > 0 && !wait(Lay::kOFree + tile, opened)) return;
 #pragma unroll 1
-    for (int kt = kb - 1; kt < ke; ++kt) {
-      if (kt + 1 < ke) {
-        if (!wait(Lay::kKFull + sk.at, sk.phase)) return;
-        tc::fence_after_sync();
-        if (kt + 1 < e) {
-          issue_scores<F>(smem, tmem, one, tile, sk.at, scored & 1, negate);
-          tc::commit(one, bars + 8 * (Lay::kSFull + 2 * tile + (scored & 1)));
-          ++scored;
-          if (kt + 2 == e) tc::commit(one, bars + 8 * (Lay::kQEmpty + tile));
-        }
-        tc::commit(one, bars + 8 * (Lay::kKEmpty + sk.at));
-        sk.step();
-      }
-      if (kt < kb) continue;
-      if (!wait(Lay::kVFull + sv.at, sv.phase)) return;
+    for (int kt = kb; kt < ke; ++kt) {
+      if (!wait(Lay::kVFull + st.at, st.phase)) return;
       if (kt < e) {
         if (kt >= ragged) {
           if (kt >= mine && lane == 0) mbar_arrive(bars + 8 * (Lay::kRaw + tile));
           __syncwarp();
           if (!wait(Lay::kClean + ((c0 + kt) & 3), (c0 + kt) >> 2)) return;
         }
-        // the sums of the item before are read
-        if (kt == kb && opened++ > 0 && !wait(Lay::kOFree + tile, opened)) return;
-        if (!wait(Lay::kPFull + 2 * tile + (done & 1), done >> 1)) return;
+        if (!wait(Lay::kPFull + 2 * tile + (n & 1), n >> 1)) return;
         tc::fence_after_sync();
-        issue_outputs<F>(smem, tmem, one, tile, sv.at, done & 1, kt == kb);
-        tc::commit(one, bars + 8 * (Lay::kPvDone + 2 * tile + (done & 1)));
-        ++done;
+        issue_outputs<F>(smem, tmem, one, tile, st.at, n & 1, kt == kb);
+        tc::commit(one, bars + 8 * (Lay::kPvDone + 2 * tile + (n & 1)));
+        ++n;
       }
-      tc::commit(one, bars + 8 * (Lay::kVEmpty + sv.at));
-      sv.step();
+      tc::commit(one, bars + 8 * (Lay::kVEmpty + st.at));
+      st.step();
     }
   }
 }
@@ -860,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const Waiter wait{smem_addr(&m.abort), a.wait_limit_ns};
   pdl_wait();
-  if (warp == kMmaWarp) tc::alloc(smem_addr(&m.tmem), Lay::kTmem);
+  if (warp == kScoreWarp) tc::alloc(smem_addr(&m.tmem), Lay::kTmem);
   const int srows = slot_rows(a.num_tokens, a.group);
   const Workspace ws = workspace_of(a.workspace, gridDim.x, srows);
   if (threadIdx.x == kLoadWarp * 32) ws.split[blockIdx.x] = Split{};
@@ -869,11 +887,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, m.tmem, 0);
   uint32_t errbits = 0, issued = 0;
-  if (warp < kMmaWarp) {
+  if (warp < kScoreWarp) {
     softmax_role<F>(a, maps.q_tokens != 0, smem, tmem, wait, warp >> 2, warp & 3, lane, ws, srows);
     asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp < kOutWarp) {
+    score_role<F>(a.softmax_scale, smem, tmem, wait, warp - kScoreWarp);
   } else if (warp < kLoadWarp) {
-    mma_role<F>(a.softmax_scale, smem, tmem, wait, warp - kMmaWarp, lane);
+    output_role<F>(smem, tmem, wait, warp - kOutWarp, lane);
   } else {
     issued = a.few_units ? load_role<int32_t>(a, maps, smem_raw, smem, wait, lane, ws, errbits)
                          : load_role<int64_t>(a, maps, smem_raw, smem, wait, lane, ws, errbits);
@@ -891,7 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0 && a.err) atomicOr(a.err, kErrTimeout);
     __syncthreads();
   }
-  if (warp == kMmaWarp) tc::dealloc(tmem, Lay::kTmem);
+  if (warp == kScoreWarp) tc::dealloc(tmem, Lay::kTmem);
 }
 
 // -------------------------------------------------------- join of the split items
