@@ -29,13 +29,18 @@
 // Shared memory: the two query tiles (96 KB), three stages of K (24 KB: three runs of 64 columns)
 // and of V (16 KB: two), in rows of 128 bytes with the 128-byte swizzle, by TMA.
 //
+// fp8 keys and values are widened to fp16 (exactly) on their way into the stages: two of these
+// then, and two of raw codes (20 KB) in the place of the third.  bf16 queries become fp16 times
+// a power of two per row, in place.
+//
 // Roles (13 warps): 4 warps per query tile compute weights, a thread a row (running maximum,
 // rescaling O only when a maximum has grown by more than 2^kGrow) and write the output; two per
 // tile issue the products, scores and outputs; one plans the CTA's items, describes them to the others in shared
 // memory and loads Q, K and V.  V rows that not every row of an item sees are looked after by
 // the weights' warps before their products: those behind the sequence are zeroed (they may hold
 // anything), those with a NaN or an infinity too, and noted, so that the sums of the rows that
-// see them become NaN.  Each role's code is kept small: instructions are fetched cold in every
+// see them become NaN.  With fp8, three more warps widen the codes and look after V on the way.
+// Each role's code is kept small: instructions are fetched cold in every
 // launch, at about 40 cycles each where nothing else covers it.
 //
 // Waits are bounded (wait_limit_ns): one that runs out marks the CTA as given up.  Every role
@@ -51,18 +56,16 @@
 namespace mla {
 namespace {
 
-constexpr int kSimpleThreads = 256;
 constexpr int kM = 128;              // query rows of a tile
 constexpr int kItemRows = 2 * kM;
 constexpr int kKeys = 64;            // keys of a tile
 constexpr int kV = 128;
 constexpr int kRun = kKeys * 128;    // bytes of 64 columns of a key tile
-constexpr int kStages = 3;
 constexpr int kQTile = 3 * kM * 128;
 constexpr int kScoreWarp = 8, kOutWarp = 10, kLoadWarp = 12;
-constexpr int kWarps = 13, kThreads = kWarps * 32;
+constexpr int kWideWarp = 13, kWideWarps = 3;  // (fp8 only)
+__host__ __device__ constexpr int warps_of(int kf) { return is16(kf) ? 13 : kWideWarp + kWideWarps; }
 constexpr int kItems = 4;            // item descriptions in shared memory
-constexpr int kItemReaders = kWarps - 1;
 constexpr int kMaxCtas = 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -80,28 +83,37 @@ struct Ref {
   static constexpr float kGrow = F == kF16 ? 14.0f : 8.0f;
 };
 
-// shared memory
+// shared memory; KF: format of keys and values
+template <int KF>
 struct Lay {
+  static constexpr bool kF8 = !is16(KF);
+  static constexpr int kStages = kF8 ? 2 : 3;
+  static constexpr int kRawStages = 2;
+  static constexpr int kRawK = kKeys * 192, kRawV = kKeys * 128;  // bytes of a unit's codes
   static constexpr int q = 0;
   static constexpr int k = 2 * kQTile;                    // [kStages][3 runs]
   static constexpr int v = k + kStages * 3 * kRun;        // [kStages][2 runs]
-  static constexpr int items = v + kStages * 2 * kRun;    // Item [kItems]
-  static constexpr int flags = items + kItems * 64;       // uint32 [4 units][2]: keys with bad V rows
-  static constexpr int bars = flags + 32;
+  static constexpr int raw = v + kStages * 2 * kRun;      // [kRawStages][128 + 64 columns of K, V]
+  static constexpr int items = raw + (kF8 ? kRawStages * (kRawK + kRawV) : 0);  // Item [kItems]
+  static constexpr int flags = items + kItems * 64;       // uint8 [4 units][16]: keys with bad V rows,
+                                                          // four to a byte
+  static constexpr int bars = flags + 64;
   // Barriers: of the stages; of units looked after, in turn; of the query tiles (scores, weights
   // and outputs two each, in turn: the weights' warps may be one unit behind the scores and one
   // ahead of the outputs, and a phase's parity has to be told from the one before); of the items.
   static constexpr int kKFull = 0, kVFull = kKFull + kStages, kKEmpty = kVFull + kStages,
-                       kVEmpty = kKEmpty + kStages, kClean = kVEmpty + kStages, kRaw = kClean + 4,
-                       kQFull = kRaw + 2, kQEmpty = kQFull + 2, kSFull = kQEmpty + 2,
-                       kPFull = kSFull + 4, kPvDone = kPFull + 4, kOFree = kPvDone + 4,
-                       kItemFull = kOFree + 2, kItemFree = kItemFull + kItems, kBars = kItemFree + kItems;
+                       kVEmpty = kKEmpty + kStages, kRawFull = kVEmpty + kStages,
+                       kRawEmpty = kRawFull + kRawStages, kClean = kRawEmpty + kRawStages,
+                       kHere = kClean + 4, kQFull = kHere + 2, kQReady = kQFull + 2,
+                       kQEmpty = kQReady + 2, kSFull = kQEmpty + 2, kPFull = kSFull + 4,
+                       kPvDone = kPFull + 4, kOFree = kPvDone + 4, kItemFull = kOFree + 2,
+                       kItemFree = kItemFull + kItems, kBars = kItemFree + kItems;
   static constexpr int misc = (bars + kBars * 8 + 15) / 16 * 16;
   static constexpr int bytes = misc + 64;
   static_assert(bytes <= 232448, "shared memory of a CTA");
-  // tensor memory columns: two S of each tile (P in their first half), O of both tiles
-  static constexpr int kO = 4 * kKeys, kTmem = 512;
 };
+// tensor memory columns: two S of each tile (P in their first half), O of both tiles
+constexpr int kO = 4 * kKeys, kTmem = 512;
 struct Misc {
   uint32_t tmem;
   uint32_t abort;
@@ -195,13 +207,15 @@ struct Item {
 static_assert(sizeof(Item) <= 64, "an item's description");
 
 // Reads the descriptions in their order, a whole warp at a time.
+template <int KF>
 struct Items {
+  using L = Lay<KF>;
   uint32_t smem, next;
   // The next one, left there (peek) or given back.
   __device__ __forceinline__ bool get(const Waiter& wait, Item& it, bool peek = false) {
-    const uint32_t i = next & (kItems - 1), bars = smem + Lay::bars;
-    if (!__all_sync(0xFFFFFFFFu, wait(bars + 8 * (Lay::kItemFull + i), (next / kItems) & 1))) return false;
-    const uint32_t at = smem + Lay::items + i * 64;
+    const uint32_t i = next & (kItems - 1), bars = smem + L::bars;
+    if (!__all_sync(0xFFFFFFFFu, wait(bars + 8 * (L::kItemFull + i), (next / kItems) & 1))) return false;
+    const uint32_t at = smem + L::items + i * 64;
     const uint4 w0 = lds16(at), w1 = lds16(at + 16), w2 = lds16(at + 32), w3 = lds16(at + 48);
     it.kb = w0.x, it.ke = w0.y, it.end[0] = w0.z, it.end[1] = w0.w;
     it.tiles = w1.x, it.least = w1.y, it.most = w1.z, it.row0 = w1.w;
@@ -209,19 +223,20 @@ struct Items {
     it.m = w3.x, it.base = (int64_t)((uint64_t)w3.w << 32 | w3.z);
     if (!peek) {
       __syncwarp();
-      if ((threadIdx.x & 31) == 0) mbar_arrive(bars + 8 * (Lay::kItemFree + i));
+      if ((threadIdx.x & 31) == 0) mbar_arrive(bars + 8 * (L::kItemFree + i));
       ++next;
     }
     return it.ke >= 0;
   }
 };
 
-// A place in a ring of kStages: which stage, and the parity of its phase.
+// A place in a ring of N stages: which stage, and the parity of its phase.
+template <int N>
 struct Stage {
   int at = 0;
   uint32_t phase = 0;
   __device__ __forceinline__ void step() {
-    if (++at == kStages) {
+    if (++at == N) {
       at = 0;
       phase ^= 1;
     }
@@ -363,12 +378,13 @@ struct Plan {
 };
 
 // Plans the items and describes them, one ahead; Q, K and V by TMA; where the run ends inside
-// an item, what the join needs.  Returns the copies begun, in K and V of a unit.
-template <typename I>
+// an item, what the join needs.  Returns the copies begun, in K and V of a unit (fp8: in units).
+template <int KF, typename I>
 __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& maps, uint8_t* smem_raw,
                                               uint32_t smem, const Waiter& wait, int lane,
                                               const Workspace& ws, uint32_t& errbits) {
-  const uint32_t bars = smem + Lay::bars;
+  using L = Lay<KF>;
+  const uint32_t bars = smem + L::bars;
   auto waited = [&](int bar, uint32_t phase) {
     return __all_sync(0xFFFFFFFFu, wait(bars + 8 * bar, phase & 1));
   };
@@ -376,11 +392,11 @@ __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& 
   const uint64_t policy =
       tc::l2_policy((int64_t)a.num_tokens * a.group <= (int64_t)kItemRows * a.num_seqs);
   Plan<I> plan;
-  plan.find(a, reinterpret_cast<I*>(smem_raw + Lay::k), lane, errbits);
+  plan.find(a, reinterpret_cast<I*>(smem_raw + L::k), lane, errbits);
   tc::fence_smem_async();  // the scratch is read; copies may write there now
   __syncwarp();
   uint32_t g = 0, told = 0, filled[2] = {0, 0};
-  Stage st;
+  Stage<L::kF8 ? L::kRawStages : L::kStages> st;
   Item it;
   it.ke = 0;
   // The first round only plans.
@@ -389,10 +405,10 @@ __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& 
     const Item nxt = plan.next(a);
     if (first || it.ke >= 0) {
       const uint32_t i = told & (kItems - 1);
-      if (told >= kItems && !waited(Lay::kItemFree + i, told / kItems - 1)) return 2 * g;
+      if (told >= kItems && !waited(L::kItemFree + i, told / kItems - 1)) return L::kF8 ? g : 2 * g;
       if (lane == 0) {
-        *reinterpret_cast<Item*>(smem_raw + Lay::items + i * 64) = nxt;
-        mbar_arrive(bars + 8 * (Lay::kItemFull + i));
+        *reinterpret_cast<Item*>(smem_raw + L::items + i * 64) = nxt;
+        mbar_arrive(bars + 8 * (L::kItemFull + i));
       }
       __syncwarp();
       ++told;
@@ -404,10 +420,10 @@ __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& 
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (it.end[i] <= it.kb) continue;
-          if (filled[i] > 0 && !waited(Lay::kQEmpty + i, filled[i] - 1)) return 2 * g;
+          if (filled[i] > 0 && !waited(L::kQEmpty + i, filled[i] - 1)) return L::kF8 ? g : 2 * g;
           ++filled[i];
           if (lane == 0) {
-            const uint32_t qf = bars + 8 * (Lay::kQFull + i), dst = smem + Lay::q + i * kQTile;
+            const uint32_t qf = bars + 8 * (L::kQFull + i), dst = smem + L::q + i * kQTile;
             const int t = it.t0 + ((int)(it.row0 / (uint32_t)kM) + i) * maps.q_tokens;
             mbar_arrive_expect_tx(qf, kQTile);
             tc::tma_load3(dst, &maps.qn, 0, h * a.group, t, qf, policy);
@@ -420,9 +436,22 @@ __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& 
 #pragma unroll 1
       for (int kt = it.kb; kt < it.ke; ++kt, ++g, st.step()) {
         const int row = it.k0 + kt * kKeys;
-        const uint32_t kf = bars + 8 * (Lay::kKFull + st.at), vf = bars + 8 * (Lay::kVFull + st.at);
-        const uint32_t k = smem + Lay::k + st.at * 3 * kRun, v = smem + Lay::v + st.at * 2 * kRun;
-        if (g >= kStages && !waited(Lay::kKEmpty + st.at, st.phase ^ 1)) return 2 * g;
+        if constexpr (L::kF8) {
+          const uint32_t rf = bars + 8 * (L::kRawFull + st.at);
+          const uint32_t k = smem + L::raw + st.at * (L::kRawK + L::kRawV);
+          if (g >= L::kRawStages && !waited(L::kRawEmpty + st.at, st.phase ^ 1)) return g;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(rf, L::kRawK + L::kRawV);
+            tc::tma_load3(k, &maps.kn, h * maps.kn_x, row, h * maps.kn_z, rf, policy);
+            tc::tma_load3(k + kKeys * 128, &maps.kp, h * maps.kp_x, row, h * maps.kp_z, rf, policy);
+            tc::tma_load3(k + L::kRawK, &maps.v, h * maps.v_x, row, h * maps.v_z, rf, policy);
+          }
+          __syncwarp();
+          continue;
+        }
+        const uint32_t kf = bars + 8 * (L::kKFull + st.at), vf = bars + 8 * (L::kVFull + st.at);
+        const uint32_t k = smem + L::k + st.at * 3 * kRun, v = smem + L::v + st.at * 2 * kRun;
+        if (g >= L::kStages && !waited(L::kKEmpty + st.at, st.phase ^ 1)) return 2 * g;
         if (lane == 0) {
           mbar_arrive_expect_tx(kf, 3 * kRun);
           tc::tma_load3(k, &maps.kn, h * maps.kn_x, row, h * maps.kn_z, kf, policy);
@@ -430,7 +459,7 @@ __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& 
           tc::tma_load3(k + 2 * kRun, &maps.kp, h * maps.kp_x, row, h * maps.kp_z, kf, policy);
         }
         __syncwarp();
-        if (g >= kStages && !waited(Lay::kVEmpty + st.at, st.phase ^ 1)) return 2 * g + 1;
+        if (g >= L::kStages && !waited(L::kVEmpty + st.at, st.phase ^ 1)) return 2 * g + 1;
         if (lane == 0) {
           mbar_arrive_expect_tx(vf, 2 * kRun);
           tc::tma_load3(v, &maps.v, h * maps.v_x, row, h * maps.v_z, vf, policy);
@@ -446,18 +475,108 @@ __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& 
     }
     it = nxt;
   }
-  return 2 * g;
+  return L::kF8 ? g : 2 * g;
+}
+
+// ------------------------------------------------------------------- widening
+// Two fp8 codes (the low 16 bits) as two fp16 values, exactly.
+template <int KF>
+__device__ __forceinline__ uint32_t widen2(uint32_t w) {
+  uint32_t r;
+  if constexpr (KF == kE4M3) asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)w));
+  else asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(r) : "h"((uint16_t)w));
+  return r;
+}
+// Columns 16 j .. of a row of a tile of runs of 64 columns.
+template <int KF>
+__device__ __forceinline__ void widen16(uint32_t tile, int row, int j, uint4 w) {
+  const uint32_t at = tile + (j >> 2) * kRun + row * 128, u = 2 * (j & 3), x = row & 7;
+  sts16(at + ((u ^ x) << 4), make_uint4(widen2<KF>(w.x), widen2<KF>(w.x >> 16), widen2<KF>(w.y),
+                                        widen2<KF>(w.y >> 16)));
+  sts16(at + (((u + 1) ^ x) << 4), make_uint4(widen2<KF>(w.z), widen2<KF>(w.z >> 16), widen2<KF>(w.w),
+                                              widen2<KF>(w.w >> 16)));
+}
+// fp8 codes of K and V from the raw stages to the fp16 ones; V rows that not every row of an item
+// sees are looked after on the way (as by look_after).
+template <int KF>
+__device__ __forceinline__ void widen_role(uint32_t smem, const Waiter& waiter, int cw, int lane) {
+  using L = Lay<KF>;
+  const uint32_t bars = smem + L::bars;
+  auto wait = [&](int bar, uint32_t phase) {
+    return __all_sync(0xFFFFFFFFu, waiter(bars + 8 * bar, phase & 1));
+  };
+  Stage<L::kRawStages> sr;
+  Stage<L::kStages> st;
+  uint32_t g = 0, cleaned = 0;
+  Items<KF> items{smem, 0};
+  Item it;
+#pragma unroll 1
+  while (items.get(waiter, it)) {
+    const int ragged = it.ragged();
+#pragma unroll 1
+    for (int kt = it.kb; kt < it.ke; ++kt, ++g, sr.step(), st.step()) {
+      const uint32_t raw = smem + L::raw + sr.at * (L::kRawK + L::kRawV);
+      const uint32_t k = smem + L::k + st.at * 3 * kRun, v = smem + L::v + st.at * 2 * kRun;
+      if (!wait(L::kRawFull + sr.at, sr.phase)) return;
+      if (g >= L::kStages && !wait(L::kKEmpty + st.at, st.phase ^ 1)) return;
+      // 8 rows x 8 pieces of 16 columns each (two rounds at once), then the rotary ones 8 x 4
+#pragma unroll 1
+      for (int r = cw * 8 + (lane >> 3); r < kKeys; r += kWideWarps * 8) {
+        const int j = lane & 7;
+        const uint4 w0 = lds16(raw + r * 128 + j * 16), w1 = lds16(raw + (r + 4) * 128 + j * 16);
+        widen16<KF>(k, r, j, w0);
+        widen16<KF>(k, r + 4, j, w1);
+        const int rr = (r & ~7) + (lane >> 2);
+        widen16<KF>(k + 2 * kRun, rr, lane & 3, lds16(raw + kKeys * 128 + rr * 64 + (lane & 3) * 16));
+      }
+      tc::fence_smem_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * (L::kKFull + st.at));
+      if (g >= L::kStages && !wait(L::kVEmpty + st.at, st.phase ^ 1)) return;
+      const uint32_t flags = smem + L::flags + (g & 3) * 16;
+#pragma unroll 1
+      for (int r = cw * 8 + (lane >> 3); r < kKeys; r += kWideWarps * 8) {
+        const int j = lane & 7;
+        uint4 w[2] = {lds16(raw + L::kRawK + r * 128 + j * 16), lds16(raw + L::kRawK + (r + 4) * 128 + j * 16)};
+        if (__builtin_expect(kt >= ragged, 0)) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const int p = kt * kKeys + r + 4 * n;
+            const uint32_t votes =
+                __ballot_sync(0xFFFFFFFFu, any_special<KF>(w[n]) && p >= it.least && p < it.most);
+            if (p >= it.most || votes & (0xFFu << (lane & 24))) w[n] = make_uint4(0, 0, 0, 0);
+            uint32_t bad = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (votes & (0xFFu << (8 * i))) bad |= 1u << i;
+            if (lane == 0) sts_u8(flags + (r >> 2) + n, bad);
+          }
+        }
+        widen16<KF>(v, r, j, w[0]);
+        widen16<KF>(v, r + 4, j, w[1]);
+      }
+      tc::fence_smem_async();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bars + 8 * (L::kVFull + st.at));
+        mbar_arrive(bars + 8 * (L::kRawEmpty + sr.at));
+        if (kt >= ragged) mbar_arrive(bars + 8 * (L::kClean + ((cleaned + kt - ragged) & 3)));
+      }
+    }
+    cleaned += it.cleaned();
+  }
 }
 
 // ------------------------------------------------------------ matrix products
-template <int F>
+template <int F, int KF>
 __device__ __forceinline__ void issue_scores(uint32_t smem, uint32_t tmem, bool one, int tile, int stage,
                                              uint32_t buffer, uint32_t negate) {
+  using L = Lay<KF>;
   const uint32_t id = negate | tc::instr_desc(kM, kKeys, false, F == kBF16, F == kBF16);
   const uint32_t i = __shfl_sync(0xFFFFFFFFu, tile, 0), st = __shfl_sync(0xFFFFFFFFu, stage, 0);
   const uint32_t b = __shfl_sync(0xFFFFFFFFu, buffer, 0);
-  const uint64_t qa = tc::smem_desc(smem + Lay::q + i * kQTile, 0, 1024);
-  const uint64_t kb = tc::smem_desc(smem + Lay::k + st * 3 * kRun, 0, 1024);
+  const uint64_t qa = tc::smem_desc(smem + L::q + i * kQTile, 0, 1024);
+  const uint64_t kb = tc::smem_desc(smem + L::k + st * 3 * kRun, 0, 1024);
   const uint32_t d = tmem + (2 * i + b) * kKeys;
 #pragma unroll
   for (int c = 0; c < 3; ++c)
@@ -466,14 +585,15 @@ __device__ __forceinline__ void issue_scores(uint32_t smem, uint32_t tmem, bool 
       tc::mma_16bit(one, d, qa + (c * kM * 128 >> 4) + 2 * k, kb + (c * kRun >> 4) + 2 * k, id, c + k > 0);
 }
 // V MN-major (two runs of 64 columns).
-template <int F>
+template <int F, int KF>
 __device__ __forceinline__ void issue_outputs(uint32_t smem, uint32_t tmem, bool one, int tile, int stage,
                                               uint32_t buffer, bool first) {
+  using L = Lay<KF>;
   constexpr uint32_t kId = tc::instr_desc(kM, kV, false, F == kBF16, F == kBF16, true);
   const uint32_t i = __shfl_sync(0xFFFFFFFFu, tile, 0), st = __shfl_sync(0xFFFFFFFFu, stage, 0);
   const uint32_t b = __shfl_sync(0xFFFFFFFFu, buffer, 0);
-  const uint32_t p = tmem + (2 * i + b) * kKeys, d = tmem + Lay::kO + i * kV;
-  const uint64_t vb = tc::smem_desc(smem + Lay::v + st * 2 * kRun, kRun, 1024);
+  const uint32_t p = tmem + (2 * i + b) * kKeys, d = tmem + kO + i * kV;
+  const uint64_t vb = tc::smem_desc(smem + L::v + st * 2 * kRun, kRun, 1024);
 #pragma unroll
   for (int k = 0; k < 4; ++k)
     tc::mma_16bit_ta(one, d, p + 8 * k, vb + k * (2048 >> 4), kId, k > 0 || !first);
@@ -493,50 +613,52 @@ __device__ __forceinline__ bool spin(const Waiter& waiter, uint32_t bar, uint32_
     if (__any_sync(0xFFFFFFFFu, mbar_test(bar, phase & 1))) return true;
   return __all_sync(0xFFFFFFFFu, waiter(bar, phase & 1));
 }
-template <int F>
+template <int F, int QF, int KF>
 __device__ __forceinline__ void score_role(float scale, uint32_t smem, uint32_t tmem, const Waiter& waiter,
                                            int tile) {
-  const uint32_t bars = smem + Lay::bars;
+  using L = Lay<KF>;
+  const uint32_t bars = smem + L::bars;
   auto wait = [&](int bar, uint32_t phase) { return spin(waiter, bars + 8 * bar, phase); };
   const bool one = tc::elect();
   const uint32_t negate = scale < 0.0f ? 1u << 13 : 0u;  // of the scores, by the tensor core
   uint32_t n = 0, opened = 0;  // units, items of this tile
-  Stage st;
-  Items items{smem, 0};
+  Stage<L::kStages> st;
+  Items<KF> items{smem, 0};
   Item it;
 #pragma unroll 1
   while (items.get(waiter, it)) {
     const int e = it.end[tile], kb = it.kb, ke = it.ke;
     if (kb < e) {
-      if (!wait(Lay::kQFull + tile, opened++)) return;
-      tc::fence_smem_async();  // (the queries may have come by ordinary copies)
+      if (!wait((F == QF ? L::kQFull : L::kQReady) + tile, opened++)) return;
+      tc::fence_smem_async();  // (the queries may have come by ordinary stores)
     }
 #pragma unroll 1
     for (int kt = kb; kt < ke; ++kt) {
       // the outputs of two units before have read the weights that these scores go over
-      if (kt < e && n >= 2 && !wait(Lay::kPvDone + 2 * tile + (n & 1), (n >> 1) - 1)) return;
-      if (!wait(Lay::kKFull + st.at, st.phase)) return;
+      if (kt < e && n >= 2 && !wait(L::kPvDone + 2 * tile + (n & 1), (n >> 1) - 1)) return;
+      if (!wait(L::kKFull + st.at, st.phase)) return;
       if (kt < e) {
         tc::fence_after_sync();
-        issue_scores<F>(smem, tmem, one, tile, st.at, n & 1, negate);
-        tc::commit(one, bars + 8 * (Lay::kSFull + 2 * tile + (n & 1)));
-        if (kt + 1 == e) tc::commit(one, bars + 8 * (Lay::kQEmpty + tile));
+        issue_scores<F, KF>(smem, tmem, one, tile, st.at, n & 1, negate);
+        tc::commit(one, bars + 8 * (L::kSFull + 2 * tile + (n & 1)));
+        if (kt + 1 == e) tc::commit(one, bars + 8 * (L::kQEmpty + tile));
         ++n;
       }
-      tc::commit(one, bars + 8 * (Lay::kKEmpty + st.at));
+      tc::commit(one, bars + 8 * (L::kKEmpty + st.at));
       st.step();
     }
   }
 }
-template <int F>
+template <int F, int KF>
 __device__ __forceinline__ void output_role(uint32_t smem, uint32_t tmem, const Waiter& waiter, int tile,
                                             int lane) {
-  const uint32_t bars = smem + Lay::bars;
+  using L = Lay<KF>;
+  const uint32_t bars = smem + L::bars;
   auto wait = [&](int bar, uint32_t phase) { return spin(waiter, bars + 8 * bar, phase); };
   const bool one = tc::elect();
   uint32_t n = 0, opened = 0, cleaned = 0;  // units, items of this tile; units looked after
-  Stage st;
-  Items items{smem, 0};
+  Stage<L::kStages> st;
+  Items<KF> items{smem, 0};
   Item it;
 #pragma unroll 1
   while (items.get(waiter, it)) {
@@ -545,23 +667,23 @@ __device__ __forceinline__ void output_role(uint32_t smem, uint32_t tmem, const 
     const uint32_t c0 = cleaned - ragged;
     cleaned += it.cleaned();
     // the sums of the item before are read
-    if (kb < e && opened++ > 0 && !wait(Lay::kOFree + tile, opened)) return;
+    if (kb < e && opened++ > 0 && !wait(L::kOFree + tile, opened)) return;
 #pragma unroll 1
     for (int kt = kb; kt < ke; ++kt) {
-      if (!wait(Lay::kVFull + st.at, st.phase)) return;
+      if (!wait(L::kVFull + st.at, st.phase)) return;
       if (kt < e) {
-        if (kt >= ragged) {
-          if (kt >= mine && lane == 0) mbar_arrive(bars + 8 * (Lay::kRaw + tile));
+        if (!L::kF8 && kt >= ragged) {
+          if (kt >= mine && lane == 0) mbar_arrive(bars + 8 * (L::kHere + tile));
           __syncwarp();
-          if (!wait(Lay::kClean + ((c0 + kt) & 3), (c0 + kt) >> 2)) return;
+          if (!wait(L::kClean + ((c0 + kt) & 3), (c0 + kt) >> 2)) return;
         }
-        if (!wait(Lay::kPFull + 2 * tile + (n & 1), n >> 1)) return;
+        if (!wait(L::kPFull + 2 * tile + (n & 1), n >> 1)) return;
         tc::fence_after_sync();
-        issue_outputs<F>(smem, tmem, one, tile, st.at, n & 1, kt == kb);
-        tc::commit(one, bars + 8 * (Lay::kPvDone + 2 * tile + (n & 1)));
+        issue_outputs<F, KF>(smem, tmem, one, tile, st.at, n & 1, kt == kb);
+        tc::commit(one, bars + 8 * (L::kPvDone + 2 * tile + (n & 1)));
         ++n;
       }
-      tc::commit(one, bars + 8 * (Lay::kVEmpty + st.at));
+      tc::commit(one, bars + 8 * (L::kVEmpty + st.at));
       st.step();
     }
   }
@@ -581,6 +703,7 @@ __device__ __forceinline__ uint32_t pack16x2(float lo, float hi) {
 
 // The queries of a tile by asynchronous copies, by the tile's four warps (where they do not come
 // in boxes: a group of query heads that does not divide a tile, or heads with a stride of 0).
+template <int KF>
 __device__ __forceinline__ void load_queries(const PrefillArgs& a, const Item& it, uint32_t smem,
                                              int tile, int w4, int lane) {
   const int col = lane & 7;
@@ -593,12 +716,42 @@ __device__ __forceinline__ void load_queries(const PrefillArgs& a, const Item& i
     const int64_t h = ok ? (int64_t)it.head * a.group + (int)(row - dt * a.group) : 0;
     const uint8_t* nope = a.q_nope + t * a.qn_ts + h * a.qn_hs + col * 16;
     const uint8_t* pe = a.q_pe + t * a.qp_ts + h * a.qp_hs + col * 16;
-    const uint32_t d = smem + Lay::q + tile * kQTile + r * 128 + ((col ^ (r & 7)) << 4);
+    const uint32_t d = smem + tile * kQTile + r * 128 + ((col ^ (r & 7)) << 4);
     tc::cp_async16(d, nope, ok);
     tc::cp_async16(d + kM * 128, nope + 128, ok);
     tc::cp_async16(d + 2 * kM * 128, pe, ok);
   }
-  tc::cp_async_arrive(smem + Lay::bars + 8 * (Lay::kQFull + tile));
+  tc::cp_async_arrive(smem + Lay<KF>::bars + 8 * (Lay<KF>::kQFull + tile));
+}
+
+// A bf16 query row in shared memory as fp16 times a power of two that puts its largest magnitude
+// into [2^14, 2^15): exact down to 2^-31 of that, off by at most 2^-39 of it below.  Returns the
+// inverse power; NaN for a row with a NaN or an infinity.
+__device__ __noinline__ float narrow_row(uint32_t at, int row) {
+  uint32_t top = 0;
+#pragma unroll 1
+  for (int k = 0; k < 24; k += 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 w = lds16(at + ((k + i) >> 3) * (kM * 128) + ((((k + i) ^ row) & 7) << 4));
+      top = umax16x2(top, umax16x2(umax16x2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                                   umax16x2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu)));
+    }
+  }
+  top = max(top & 0xFFFFu, top >> 16);
+  const uint32_t e = min(max(top >> 7, 15u), 254u);         // exponent of the largest magnitude
+  const float s = __uint_as_float((268u - e) << 23);        // 2^(141 - e)
+#pragma unroll 1
+  for (int k = 0; k < 24; k += 2) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t p = at + ((k + i) >> 3) * (kM * 128) + ((((k + i) ^ row) & 7) << 4);
+      const uint4 w = lds16(p);
+      sts16(p, make_uint4(pack_f16x2(bf16lo(w.x) * s, bf16hi(w.x) * s), pack_f16x2(bf16lo(w.y) * s, bf16hi(w.y) * s),
+                          pack_f16x2(bf16lo(w.z) * s, bf16hi(w.z) * s), pack_f16x2(bf16lo(w.w) * s, bf16hi(w.w) * s)));
+    }
+  }
+  return top >= 0x7F80u ? NAN : __uint_as_float((e - 14u) << 23);  // 2^(e - 141)
 }
 
 // What the weights of an item's units need to know; key tiles count from the part's first.
@@ -619,7 +772,7 @@ struct Part {
 template <int F>
 __device__ __noinline__ uint32_t look_after(uint32_t v, int least, int most) {
   const int lane = threadIdx.x & 31, col = lane & 7;
-  uint32_t bad = 0;
+  uint32_t bad = 0;  // four keys to a byte
 #pragma unroll 2
   for (int n = 0; n < 4; ++n) {
     const int key = 4 * n + (lane >> 3);
@@ -633,7 +786,7 @@ __device__ __noinline__ uint32_t look_after(uint32_t v, int least, int most) {
     if (votes)
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (votes & (0xFFu << (8 * k))) bad |= 1u << (4 * n + k);
+        if (votes & (0xFFu << (8 * k))) bad |= 1u << (8 * n + k);
   }
   tc::fence_smem_async();
   __syncwarp();
@@ -642,48 +795,49 @@ __device__ __noinline__ uint32_t look_after(uint32_t v, int least, int most) {
 
 // The weights of an item's units (a function of its own, so that its loop has the registers to
 // itself): the row's reference and the sum of its weights.  False: given up.
-template <int F>
+template <int F, int KF>
 __device__ __noinline__ bool unit_weights(Part s, const Waiter waiter, float& mu_out, float& l_out) {
   using R = Ref<F>;
+  using L = Lay<KF>;
   const int lane = threadIdx.x & 31;
   auto wait = [&](int bar, uint32_t phase) {
-    return __all_sync(0xFFFFFFFFu, waiter(s.smem + Lay::bars + 8 * bar, phase & 1));
+    return __all_sync(0xFFFFFFFFu, waiter(s.smem + L::bars + 8 * bar, phase & 1));
   };
   float mu = -INFINITY, l = 0.0f;
 #pragma unroll 1
   for (int kt = 0; kt < s.count; ++kt, ++s.n) {
-    if (!wait(Lay::kSFull + 2 * s.tile + (s.n & 1), s.n >> 1)) return false;
+    if (!wait(L::kSFull + 2 * s.tile + (s.n & 1), s.n >> 1)) return false;
     tc::fence_after_sync();
-    const uint32_t bars = s.smem + Lay::bars, nc = s.cleaned + kt - s.from;
-    const uint32_t flags = s.smem + Lay::flags + ((s.g + kt) & 3) * 8;
-    if (__builtin_expect(kt >= s.mend, 0)) {
+    const uint32_t bars = s.smem + L::bars, nc = s.cleaned + kt - s.from;
+    const uint32_t flags = s.smem + L::flags + ((s.g + kt) & 3) * 16;
+    if (!L::kF8 && __builtin_expect(kt >= s.mend, 0)) {
       const int w4 = (threadIdx.x >> 5) & 3;
-      if (!wait(Lay::kRaw + s.tile, s.mended++)) return false;
-      const int stage = (s.stage + kt) % kStages;
-      const uint32_t bad = look_after<F>(s.smem + Lay::v + stage * 2 * kRun + w4 * 2048,
+      if (!wait(L::kHere + s.tile, s.mended++)) return false;
+      const int stage = (s.stage + kt) % L::kStages;
+      const uint32_t bad = look_after<F>(s.smem + L::v + stage * 2 * kRun + w4 * 2048,
                                          s.least - kt * kKeys - w4 * 16, s.most - kt * kKeys - w4 * 16);
       if (lane == 0) {
-        sts_u16(flags + w4 * 2, bad);
-        mbar_arrive(bars + 8 * (Lay::kClean + (nc & 3)));
+        sts_u32(flags + w4 * 4, bad);
+        mbar_arrive(bars + 8 * (L::kClean + (nc & 3)));
       }
     }
     if (!s.live) {
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bars + 8 * (Lay::kPFull + 2 * s.tile + (s.n & 1)));
+      if (lane == 0) mbar_arrive(bars + 8 * (L::kPFull + 2 * s.tile + (s.n & 1)));
       continue;
     }
     const uint32_t s_at = s.s_at + (s.n & 1) * kKeys;
     float x[kKeys];
     tc::ld_32x64(s_at, reinterpret_cast<uint32_t*>(x));
     if (__builtin_expect(kt >= s.from, 0)) {
-      if (!wait(Lay::kClean + (nc & 3), nc >> 2)) return false;
+      if (!wait(L::kClean + (nc & 3), nc >> 2)) return false;
       const int lim = s.seen - kt * kKeys;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int below = min(max(lim - 32 * k, 0), 32);
-        if ((lds_u32(flags + 4 * k) & (below == 32 ? 0xFFFFFFFFu : (1u << below) - 1)) != 0) l = NAN;
-      }
+      const uint4 f = lds16(flags);
+      if (__builtin_expect((f.x | f.y | f.z | f.w) != 0, 0))
+#pragma unroll 1
+        for (int k = 0; k < kKeys; ++k)
+          if (k < lim && lds_u8(flags + (k >> 2)) >> (k & 3) & 1) l = NAN;
 #pragma unroll
       for (int j = 0; j < kKeys; ++j) x[j] = j < lim ? x[j] : -INFINITY;
     }
@@ -700,7 +854,7 @@ __device__ __noinline__ bool unit_weights(Part s, const Waiter waiter, float& mu
       l = l == 0.0f ? 0.0f : l * f;  // (a NaN stays)
       mu = mn;
       if (kt > 0) {
-        if (!wait(Lay::kPvDone + 2 * s.tile + ((s.n - 1) & 1), (s.n - 1) >> 1)) return false;
+        if (!wait(L::kPvDone + 2 * s.tile + ((s.n - 1) & 1), (s.n - 1) >> 1)) return false;
         tc::fence_after_sync();
 #pragma unroll 1
         for (int k = 0; k < kV; k += 16) {
@@ -730,7 +884,7 @@ __device__ __noinline__ bool unit_weights(Part s, const Waiter waiter, float& mu
     tc::wait_st();
     tc::fence_before_sync();
     __syncwarp();
-    if (lane == 0) mbar_arrive(bars + 8 * (Lay::kPFull + 2 * s.tile + (s.n & 1)));
+    if (lane == 0) mbar_arrive(bars + 8 * (L::kPFull + 2 * s.tile + (s.n & 1)));
   }
   mu_out = mu;
   l_out = l;
@@ -744,23 +898,25 @@ __device__ __forceinline__ void st32(void* p, const uint32_t* w) {
 }
 
 // Weights and output of one query tile; a thread has a row.
-template <int F>
+template <int F, int QF, int KF>
 __device__ __forceinline__ void softmax_role(const PrefillArgs& a, bool boxes, uint32_t smem, uint32_t tmem,
                                              const Waiter& waiter, int tile, int w4, int lane,
                                              const Workspace& ws, int srows) {
-  const uint32_t bars = smem + Lay::bars;
+  using L = Lay<KF>;
+  const uint32_t bars = smem + L::bars;
   const uint32_t s_at = tmem + tile * 2 * kKeys + ((uint32_t)(w4 * 32) << 16);
-  const uint32_t o_at = tmem + Lay::kO + tile * kV + ((uint32_t)(w4 * 32) << 16);
+  const uint32_t o_at = tmem + kO + tile * kV + ((uint32_t)(w4 * 32) << 16);
   const int r = w4 * 32 + lane;
-  uint32_t n = 0, g = 0, cleaned = 0, mended = 0;
-  Items items{smem, 0};
+  uint32_t n = 0, g = 0, cleaned = 0, mended = 0, opened = 0;
+  const float ks = L::kF8 ? __ldg(a.kv_scale) : 1.0f;
+  Items<KF> items{smem, 0};
   Item it;
   // The queries' place is free when the item's last scores have come: those of the next item are
   // asked for before the output of this one is written.
   auto queries = [&] {
     Item nxt;
     if (!boxes && items.get(waiter, nxt, true) && nxt.end[tile] > nxt.kb)
-      load_queries(a, nxt, smem, tile, w4, lane);
+      load_queries<KF>(a, nxt, smem, tile, w4, lane);
   };
   queries();
 #pragma unroll 1
@@ -770,10 +926,20 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, bool boxes, u
     const uint32_t row = it.row0 + tile * kM + r;
     const int seen = ok ? seen_of(a, it.base, it.m, row) : 0, shift = it.kb * kKeys;
     const int mend = max(it.ragged(), tile ? it.end[0] : 0);
-    float mu, l;
-    if (!unit_weights<F>(Part{smem, s_at, o_at, n, g, cleaned, mended, (int)(g % kStages), tile, count,
+    float c = fabsf(a.softmax_scale * ks) * kLog2e, mu, l;
+    if constexpr (F != QF) {
+      if (count > 0) {
+        if (!__all_sync(0xFFFFFFFFu, waiter(bars + 8 * (L::kQFull + tile), opened++ & 1))) return;
+        c *= narrow_row(smem + L::q + tile * kQTile + r * 128, r & 7);
+        tc::fence_smem_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + 8 * (L::kQReady + tile));
+      }
+    }
+    c = c < 1e-37f ? 1e-37f : c;  // (a masked score times it is -infinity)
+    if (!unit_weights<F, KF>(Part{smem, s_at, o_at, n, g, cleaned, mended, (int)(g % L::kStages), tile, count,
                               it.ragged() - it.kb, mend - it.kb, it.least - shift, it.most - shift,
-                              seen - shift, live, fmaxf(fabsf(a.softmax_scale) * kLog2e, 1e-37f)},
+                              seen - shift, live, c},
                          waiter, mu, l))
       return;
     mended += max(it.end[tile] - mend, 0);
@@ -783,7 +949,7 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, bool boxes, u
     queries();
     // ---- the end of this CTA's part of the item
     if (count > 0) {
-      if (!__all_sync(0xFFFFFFFFu, waiter(bars + 8 * (Lay::kPvDone + 2 * tile + ((n - 1) & 1)), ((n - 1) >> 1) & 1))) return;
+      if (!__all_sync(0xFFFFFFFFu, waiter(bars + 8 * (L::kPvDone + 2 * tile + ((n - 1) & 1)), ((n - 1) >> 1) & 1))) return;
       tc::fence_after_sync();
     }
     if (live) {
@@ -799,7 +965,7 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, bool boxes, u
       } else if (ok && a.lse) {
         a.lse[t * a.lse_ts + h * a.lse_hs] = l == 0.0f ? -INFINITY : (mu + __log2f(l)) * kLn2;
       }
-      const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
+      const float inv = l == 0.0f ? 0.0f : __fdividef(ks, l);
       // where 32 dims of the row go, and how far the next lie
       uint8_t* to = whole ? a.out + t * a.out_ts + h * a.out_hs
                           : reinterpret_cast<uint8_t*>(ws.o + slot * kV + at * 4);  // [dims / 4][rows][4]
@@ -812,7 +978,7 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, bool boxes, u
             uint32_t z[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-              z[j] = pack16x2<F>(__uint_as_float(y[2 * j]) * inv, __uint_as_float(y[2 * j + 1]) * inv);
+              z[j] = pack16x2<QF>(__uint_as_float(y[2 * j]) * inv, __uint_as_float(y[2 * j + 1]) * inv);
             if (a.out_32) {
               st32(to, z);
               st32(to + 32, z + 8);
@@ -834,7 +1000,7 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, bool boxes, u
     if (count > 0) {
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bars + 8 * (Lay::kOFree + tile));
+      if (lane == 0) mbar_arrive(bars + 8 * (L::kOFree + tile));
     }
   }
 }
@@ -842,43 +1008,55 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, bool boxes, u
 // ------------------------------------------------------------------ the kernel
 // After giving up: waits, bounded again, for the copies into shared memory, and a
 // millisecond for matrix products in flight (they end by themselves within microseconds).
+template <int KF>
 __device__ __noinline__ void settle(uint32_t smem, uint32_t issued, uint64_t limit) {
+  using L = Lay<KF>;
   const uint64_t since = global_ns();
-  for (uint32_t i = issued > 2 * kStages ? issued - 2 * kStages : 0; i < issued; ++i) {
-    const uint32_t u = i >> 1, bar = (i & 1 ? Lay::kVFull : Lay::kKFull) + u % kStages;
-    while (!mbar_try_wait(smem + Lay::bars + 8 * bar, (u / kStages) & 1) && global_ns() - since <= limit) {
+  auto past = [&](int bar, uint32_t phase) {
+    while (!mbar_try_wait(smem + L::bars + 8 * bar, phase & 1) && global_ns() - since <= limit) {
     }
+  };
+  if constexpr (L::kF8) {
+    for (uint32_t u = issued > L::kRawStages ? issued - L::kRawStages : 0; u < issued; ++u)
+      past(L::kRawFull + u % L::kRawStages, u / L::kRawStages);
+  } else {
+    for (uint32_t i = issued > 2 * L::kStages ? issued - 2 * L::kStages : 0; i < issued; ++i)
+      past((i & 1 ? L::kVFull : L::kKFull) + (i >> 1) % L::kStages, (i >> 1) / L::kStages);
   }
   while (global_ns() - since <= 1000000) {
   }
 }
 
-template <int F>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int F, int QF, int KF>
+__global__ void __launch_bounds__(warps_of(KF) * 32, 1)
     prefill_attention_kernel(const PrefillArgs a, const __grid_constant__ Maps maps) {
+  using L = Lay<KF>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t smem = smem_addr(smem_raw);
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  Misc& m = *reinterpret_cast<Misc*>(smem_raw + Lay::misc);
+  Misc& m = *reinterpret_cast<Misc*>(smem_raw + L::misc);
   pdl_trigger();
   if (threadIdx.x == 0) m.abort = 0;
   if (warp == 0) {
     // arrivals of a phase, by barrier
-    for (int i = lane; i < Lay::kBars; i += 32) {
+    for (int i = lane; i < L::kBars; i += 32) {
       auto of = [&](int bar, int many) { return i >= bar && i < bar + many; };
-      int n = of(Lay::kKEmpty, 2 * kStages) ? 2 : 1;
-      if (of(Lay::kQFull, 2) && maps.q_tokens == 0) n = kM;
-      if (of(Lay::kPFull, 4) || of(Lay::kOFree, 2) || of(Lay::kClean, 4)) n = 4;
-      if (i >= Lay::kItemFree) n = kItemReaders;
+      int n = of(L::kKEmpty, 2 * L::kStages) ? 2 : 1;
+      if (L::kF8 && (of(L::kKFull, 2 * L::kStages) || of(L::kRawEmpty, L::kRawStages) || of(L::kClean, 4)))
+        n = kWideWarps;
+      if (!L::kF8 && of(L::kClean, 4)) n = 4;
+      if (of(L::kQFull, 2) && maps.q_tokens == 0) n = kM;
+      if (of(L::kPFull, 4) || of(L::kOFree, 2) || of(L::kQReady, 2)) n = 4;
+      if (of(L::kItemFree, kItems)) n = warps_of(KF) - 1;
       // (testing: one arrival too many)
-      if (blockIdx.x == 0 && i < 2 * kStages && a.stall_stage == i + 1) ++n;
-      mbar_init(smem + Lay::bars + 8 * i, n);
+      if (blockIdx.x == 0 && i < 2 * L::kStages && a.stall_stage == i + 1) ++n;
+      mbar_init(smem + L::bars + 8 * i, n);
     }
     mbar_fence_init();
   }
   const Waiter wait{smem_addr(&m.abort), a.wait_limit_ns};
   pdl_wait();
-  if (warp == kScoreWarp) tc::alloc(smem_addr(&m.tmem), Lay::kTmem);
+  if (warp == kScoreWarp) tc::alloc(smem_addr(&m.tmem), kTmem);
   const int srows = slot_rows(a.num_tokens, a.group);
   const Workspace ws = workspace_of(a.workspace, gridDim.x, srows);
   if (threadIdx.x == kLoadWarp * 32) ws.split[blockIdx.x] = Split{};
@@ -888,15 +1066,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, m.tmem, 0);
   uint32_t errbits = 0, issued = 0;
   if (warp < kScoreWarp) {
-    softmax_role<F>(a, maps.q_tokens != 0, smem, tmem, wait, warp >> 2, warp & 3, lane, ws, srows);
+    softmax_role<F, QF, KF>(a, maps.q_tokens != 0, smem, tmem, wait, warp >> 2, warp & 3, lane, ws, srows);
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp < kOutWarp) {
-    score_role<F>(a.softmax_scale, smem, tmem, wait, warp - kScoreWarp);
+    score_role<F, QF, KF>(L::kF8 ? a.softmax_scale * __ldg(a.kv_scale) : a.softmax_scale, smem, tmem, wait, warp - kScoreWarp);
   } else if (warp < kLoadWarp) {
-    output_role<F>(smem, tmem, wait, warp - kOutWarp, lane);
+    output_role<F, KF>(smem, tmem, wait, warp - kOutWarp, lane);
+  } else if (warp == kLoadWarp) {
+    issued = a.few_units ? load_role<KF, int32_t>(a, maps, smem_raw, smem, wait, lane, ws, errbits)
+                         : load_role<KF, int64_t>(a, maps, smem_raw, smem, wait, lane, ws, errbits);
   } else {
-    issued = a.few_units ? load_role<int32_t>(a, maps, smem_raw, smem, wait, lane, ws, errbits)
-                         : load_role<int64_t>(a, maps, smem_raw, smem, wait, lane, ws, errbits);
+    if constexpr (L::kF8) widen_role<KF>(smem, wait, warp - kWideWarp, lane);
   }
   __syncwarp();
   if (a.err && warp == kLoadWarp) {
@@ -907,11 +1087,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   if (__builtin_expect(wait.given_up(), 0)) {
-    if (warp == kLoadWarp) settle(smem, issued, a.wait_limit_ns);
+    if (warp == kLoadWarp) settle<KF>(smem, issued, a.wait_limit_ns);
     if (threadIdx.x == 0 && a.err) atomicOr(a.err, kErrTimeout);
     __syncthreads();
   }
-  if (warp == kScoreWarp) tc::dealloc(tmem, Lay::kTmem);
+  if (warp == kScoreWarp) tc::dealloc(tmem, kTmem);
 }
 
 // -------------------------------------------------------- join of the split items
@@ -919,7 +1099,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // blocks of all of them but the last: 8 rows x 16 dims a warp, a lane four dims of a row.
 constexpr int kJoinWarps = 8, kJoinBlocks = 32;
 
-template <int F>
+template <int QF>
 __global__ void __launch_bounds__(kJoinWarps * 32) prefill_join_kernel(const PrefillArgs a) {
   pdl_trigger();
   pdl_wait();
@@ -966,17 +1146,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefill_join_kernel(const Pre
     }
     const uint32_t row = sp.row0 + r, dt = a.by_group(row);
     const int64_t t = sp.tok0 + (int)dt, h = (int64_t)sp.head * a.group + (int)(row - dt * a.group);
-    const float inv = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
+    const float inv = sum == 0.0f ? 0.0f : __fdividef(a.kv_scale ? __ldg(a.kv_scale) : 1.0f, sum);
     st8(a.out + t * a.out_ts + h * a.out_hs + quad * 8,
-        make_uint2(pack16x2<F>(acc.x * inv, acc.y * inv), pack16x2<F>(acc.z * inv, acc.w * inv)));
+        make_uint2(pack16x2<QF>(acc.x * inv, acc.y * inv), pack16x2<QF>(acc.z * inv, acc.w * inv)));
     if (quad == 0 && a.lse)
       a.lse[t * a.lse_ts + h * a.lse_hs] = sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * kLn2;
   }
 }
 
 // ------------------------------------------------------------------ launches
-// Rows of keys (or values) of all heads as a tensor map with boxes of 64 columns and
-// 64 rows.  Heads inside a row are columns of it, so that any head stride does; otherwise (heads
+// Rows of keys (or values) of all heads as a tensor map with boxes of 64 columns (fp8: all)
+// and 64 rows.  Heads inside a row are columns of it, so that any head stride does; otherwise (heads
 // apart) the third dimension.  `base` stands in for arrays without rows.
 bool make_map(CUtensorMap* map, const void* base, int fmt, int width, int64_t hs, int heads, int64_t ts,
               int64_t rows, int32_t* x_head, int32_t* z_head) {
@@ -999,11 +1179,12 @@ bool make_map(CUtensorMap* map, const void* base, int fmt, int width, int64_t hs
     }
   }
   if (dims[0] > INT32_MAX) return false;
-  const cuuint32_t box[3] = {64, kKeys, 1}, unit[3] = {1, 1, 1};
-  const CUtensorMapDataType type =
-      fmt == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const cuuint32_t box[3] = {is16(fmt) ? 64u : (cuuint32_t)width, kKeys, 1}, unit[3] = {1, 1, 1};
+  const CUtensorMapDataType type = fmt == kBF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                   : fmt == kF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
   return encode(map, type, 3, const_cast<void*>(base), dims, strides, box, unit,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, is16(fmt) ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1031,38 +1212,38 @@ int query_maps(const PrefillArgs& a, int fmt, Maps* maps) {
              : 0;
 }
 
-template <int F>
+template <int F, int QF, int KF>
 cudaError_t launch_tc(PrefillArgs a, int ctas, const LaunchCfg& cfg) {
   Maps maps = {};
   const bool none = a.num_kv == 0;
   const int64_t rows = none ? 1 : a.num_kv;
   const int heads = none ? 1 : a.kv_heads;
-  if (!make_map(&maps.kn, none ? a.q_nope : a.k_nope, F, 128, a.kn_hs, heads, a.kn_ts, rows,
+  if (!make_map(&maps.kn, none ? a.q_nope : a.k_nope, KF, 128, a.kn_hs, heads, a.kn_ts, rows,
                 &maps.kn_x, &maps.kn_z) ||
-      !make_map(&maps.kp, none ? a.q_nope : a.k_pe, F, 64, a.kp_hs, heads, a.kp_ts, rows,
+      !make_map(&maps.kp, none ? a.q_nope : a.k_pe, KF, 64, a.kp_hs, heads, a.kp_ts, rows,
                 &maps.kp_x, &maps.kp_z) ||
-      !make_map(&maps.v, none ? a.q_nope : a.v, F, 128, a.v_hs, heads, a.v_ts, rows,
+      !make_map(&maps.v, none ? a.q_nope : a.v, KF, 128, a.v_hs, heads, a.v_ts, rows,
                 &maps.v_x, &maps.v_z))
     return cudaErrorInvalidValue;
-  maps.q_tokens = query_maps(a, F, &maps);
+  maps.q_tokens = query_maps(a, QF, &maps);
   a.out_32 = ((reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)a.out_ts | (uintptr_t)a.out_hs) & 31) == 0;
   const int64_t items = (((int64_t)a.num_tokens * a.group + kItemRows - 1) / kItemRows + a.num_seqs) * a.kv_heads;
   a.few_units = items * (a.num_kv / kKeys + 2 + kSwitch) < INT32_MAX;
-  auto kern = prefill_attention_kernel<F>;
+  auto kern = prefill_attention_kernel<F, QF, KF>;
   // the attribute stays with the device's context: set on a device's first call
   static std::atomic<uint64_t> set{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !(set.load(std::memory_order_relaxed) >> dev & 1)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::bytes);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<KF>::bytes);
     if (e != cudaSuccess) return e;
     if (dev < 64) set.fetch_or(uint64_t(1) << dev);
   }
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(ctas);
-  lc.blockDim = dim3(kThreads);
-  lc.dynamicSmemBytes = Lay::bytes;
+  lc.blockDim = dim3(warps_of(KF) * 32);
+  lc.dynamicSmemBytes = Lay<KF>::bytes;
   lc.stream = cfg.stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1074,91 +1255,8 @@ cudaError_t launch_tc(PrefillArgs a, int ctas, const LaunchCfg& cfg) {
   lc.gridDim = dim3(kJoinBlocks, ctas);
   lc.blockDim = dim3(kJoinWarps * 32);
   lc.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&lc, prefill_join_kernel<F>, a);
+  return cudaLaunchKernelEx(&lc, prefill_join_kernel<QF>, a);
 }
-
-template <int F>
-__device__ __forceinline__ float value_at(const uint8_t* row, int i) {
-  if constexpr (F == kBF16) return bf16lo(*reinterpret_cast<const uint16_t*>(row + 2 * i));
-  else if constexpr (F == kF16) return f16lo(*reinterpret_cast<const uint16_t*>(row + 2 * i));
-  else {
-    float x, y;
-    fp8x2_to_f32x2<F>(row[i], x, y);
-    return x;
-  }
-}
-
-template <int F, int KF>
-__global__ void __launch_bounds__(kSimpleThreads) prefill_simple_kernel(const PrefillArgs a) {
-  pdl_trigger();
-  pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t rows = (int64_t)a.num_tokens * a.num_heads;
-  const int64_t warps = ((int64_t)gridDim.x * kSimpleThreads) >> 5;
-  const float ks = KF == kE4M3 || KF == kE5M2 ? *a.kv_scale : 1.0f;
-  uint32_t errbits = 0;
-  for (int64_t row = ((int64_t)blockIdx.x * kSimpleThreads + threadIdx.x) >> 5; row < rows; row += warps) {
-    const int t = (int)(row / a.num_heads), h = (int)(row - (int64_t)t * a.num_heads);
-    int s = -1;
-    for (int i = 0; i < a.num_seqs; ++i)
-      if (a.cu_q[i] <= t && t < a.cu_q[i + 1]) s = i;
-    if (s < 0) continue;
-    const int c1 = a.cu_q[s + 1], k0 = a.cu_kv[s];
-    int64_t m = (int64_t)a.cu_kv[s + 1] - k0;
-    if (a.causal) m += t + 1 - c1;
-    if (k0 < 0 || k0 + m > a.num_kv) {
-      if (m > 0) errbits |= kErrPosOOB;
-      m = k0 < 0 ? 0 : a.num_kv - k0;
-    }
-    const int g = h / a.group;
-    const uint8_t* qn = a.q_nope + t * a.qn_ts + h * a.qn_hs;
-    const uint8_t* qp = a.q_pe + t * a.qp_ts + h * a.qp_hs;
-    float q[6], o[4] = {0, 0, 0, 0}, top = -INFINITY, sum = 0.0f;
-    for (int i = 0; i < 4; ++i) q[i] = value_at<F>(qn, 32 * i + lane);
-    for (int i = 0; i < 2; ++i) q[4 + i] = value_at<F>(qp, 32 * i + lane);
-    for (int64_t p = k0; p < k0 + m; ++p) {
-      const uint8_t* kn = a.k_nope + p * a.kn_ts + g * a.kn_hs;
-      const uint8_t* kp = a.k_pe + p * a.kp_ts + g * a.kp_hs;
-      float x = 0.0f;
-      for (int i = 0; i < 4; ++i) x = fmaf(q[i], value_at<KF>(kn, 32 * i + lane), x);
-      for (int i = 0; i < 2; ++i) x = fmaf(q[4 + i], value_at<KF>(kp, 32 * i + lane), x);
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
-      x *= a.softmax_scale * ks * kLog2e;
-      const float mx = fmaxf(top, x), f = exp2f(top - mx), w = exp2f(x - mx);
-      const uint8_t* v = a.v + p * a.v_ts + g * a.v_hs;
-      for (int i = 0; i < 4; ++i) o[i] = fmaf(o[i], f, w * value_at<KF>(v, 32 * i + lane));
-      sum = fmaf(sum, f, w);
-      top = mx;
-    }
-    for (int i = 0; i < 4; ++i) {
-      const float y = sum == 0.0f ? 0.0f : o[i] * ks / sum;
-      uint16_t b = (uint16_t)pack_bf16x2(y, 0.0f);
-      if (F == kF16) asm("cvt.rn.f16.f32 %0, %1;" : "=h"(b) : "f"(y));
-      *reinterpret_cast<uint16_t*>(a.out + t * a.out_ts + h * a.out_hs + 2 * (32 * i + lane)) = b;
-    }
-    if (a.lse && lane == 0)
-      a.lse[t * a.lse_ts + h * a.lse_hs] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
-  }
-  if (errbits && lane == 0 && a.err) atomicOr(a.err, errbits);
-}
-
-template <int F, int KF>
-cudaError_t launch_simple(const PrefillArgs& a, const LaunchCfg& cfg) {
-  const auto kern = prefill_simple_kernel<F, KF>;
-  cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3(capped_grid(reinterpret_cast<const void*>(kern), kSimpleThreads,
-                                ((int64_t)a.num_tokens * a.num_heads + kSimpleThreads / 32 - 1) / (kSimpleThreads / 32)));
-  lc.blockDim = dim3(kSimpleThreads);
-  lc.stream = cfg.stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  lc.attrs = attr;
-  lc.numAttrs = cfg.pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&lc, kern, a);
-}
-
 
 }  // namespace
 
@@ -1173,11 +1271,11 @@ cudaError_t launch_prefill_attention(const PrefillArgs& a, int fmt, int kv_fmt, 
                                      const LaunchCfg& cfg) {
   const int ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
   if (fmt == kBF16) {
-    if (kv_fmt == kBF16) return launch_tc<kBF16>(a, ctas, cfg);
-    return kv_fmt == kE4M3 ? launch_simple<kBF16, kE4M3>(a, cfg) : launch_simple<kBF16, kE5M2>(a, cfg);
+    if (kv_fmt == kBF16) return launch_tc<kBF16, kBF16, kBF16>(a, ctas, cfg);
+    return kv_fmt == kE4M3 ? launch_tc<kF16, kBF16, kE4M3>(a, ctas, cfg) : launch_tc<kF16, kBF16, kE5M2>(a, ctas, cfg);
   }
-  if (kv_fmt == kF16) return launch_tc<kF16>(a, ctas, cfg);
-  return kv_fmt == kE4M3 ? launch_simple<kF16, kE4M3>(a, cfg) : launch_simple<kF16, kE5M2>(a, cfg);
+  if (kv_fmt == kF16) return launch_tc<kF16, kF16, kF16>(a, ctas, cfg);
+  return kv_fmt == kE4M3 ? launch_tc<kF16, kF16, kE4M3>(a, ctas, cfg) : launch_tc<kF16, kF16, kE5M2>(a, ctas, cfg);
 }
 
 }  // namespace mla
