@@ -218,12 +218,15 @@ __device__ __forceinline__ int seen_of(const LatentAttnArgs& a, const Seq& q, in
   const int64_t n = (int64_t)q.kv + (!TREE && a.causal ? (int64_t)t + 1 - q.c1 : 0);
   return (int)max((int64_t)0, min(n, (int64_t)a.room));
 }
-// TREE: whether token t sees row p >= q.ctx(), a new one.
-__device__ __forceinline__ bool in_tree(const LatentAttnArgs& a, const Seq& q, int t, int p) {
-  const uint32_t node = (uint32_t)p - (uint32_t)q.first;  // (at most 2^31 + kMaxTree)
-  return node < 32u * a.tree_words &&
-         (__ldg(a.tree + (int64_t)t * a.tree_ts + (node >> 5)) >> (node & 31) & 1u) != 0;
-}
+// TREE: row p >= q.ctx(), a new one, among the masks' bits.
+struct Node {
+  uint32_t word, bit;  // bit 0 when no mask has one for it
+  __device__ __forceinline__ Node(const LatentAttnArgs& a, const Seq& q, int p) {
+    const uint32_t n = (uint32_t)p - (uint32_t)q.first;  // (at most 2^31 + kMaxTree)
+    word = min(n >> 5, a.tree_words - 1);
+    bit = n < 32u * a.tree_words ? 1u << (n & 31) : 0u;
+  }
+};
 // Rows that the last (first) row of query tile qt sees: the most (least) of its rows.
 template <int NR, bool TREE>
 __device__ __forceinline__ int most_seen(const LatentAttnArgs& a, const Seq& q, int qt) {
@@ -522,6 +525,17 @@ __device__ __forceinline__ uint32_t produce(const LatentAttnArgs& a, const CUten
         if (L::kHalves > 1 && !freed(1)) break;
         // tokens of the query tile see different rows of this key tile
         const bool mixed = cur.least < cur.most && (cur.kt + 1) * kKeys > cur.least;
+        // the 16-byte parts of this lane: chunk c, and for fp8 the rotary columns of
+        // the last chunk (its upper half) in lanes 4 to 7
+        auto part = [&](int c) { return !L::kF8 || c < 4 ? c * 128 + col * 16 : 512 + (col - 4) * 16; };
+        auto has = [&](int c) { return !L::kF8 || c < 4 || col >= 4; };
+        auto place = [&](int row) { return base + row * 128 + ((col ^ (row & 7)) << 4); };
+        // Rows of mixed tiles are looked at for NaNs and infinities: in shared memory once they are
+        // there, or, in tiles of 16 query rows without masks, where mixed tiles are few, in the
+        // cache before they are stored.  (us with the first and the second: 32 verifications of 4
+        // tokens 45.6, 46.7, chunks of 1024 tokens 633, 641, 16 trees of 61 tokens 241, 286 with the
+        // masks' words loaded one by one; 64 ragged e4m3 decodes, which have no mixed tile, 60.8, 59.7.)
+        constexpr bool kInPlace = TREE || NR > 16;
 #pragma unroll 1
         for (int i = 0; i < kRows; ++i) {
           const int row = row0 + 4 * i;
@@ -529,17 +543,12 @@ __device__ __forceinline__ uint32_t produce(const LatentAttnArgs& a, const CUten
           uint32_t flag;
           const uint8_t* src = row_in(a, cur.kt * kKeys + row, bi, flag);
           if (flag) errbits |= kErrBlockOOB;
-          const uint32_t d = base + row * 128 + ((col ^ (row & 7)) << 4);
-          // the 16-byte parts of this lane: chunk c, and for fp8 the rotary columns of
-          // the last chunk (its upper half) in lanes 4 to 7
-          auto part = [&](int c) { return !L::kF8 || c < 4 ? c * 128 + col * 16 : 512 + (col - 4) * 16; };
-          auto has = [&](int c) { return !L::kF8 || c < 4 || col >= 4; };
-          if (!mixed) {
+          if (kInPlace || !mixed) {
 #pragma unroll
             for (int c = 0; c < L::kChunks; ++c)
-              if (has(c)) tc::cp_async16(d + c * kChunk, src ? src + part(c) : a.cache, src != nullptr);
+              if (has(c)) tc::cp_async16(place(row) + c * kChunk, src ? src + part(c) : a.cache, src != nullptr);
           } else {
-            // once to look for NaNs and infinities, and again to store
+            // once to look, and again to store
             bool sp = false;
 #pragma unroll
             for (int c = 0; c < L::kChunks; ++c)
@@ -549,10 +558,28 @@ __device__ __forceinline__ uint32_t produce(const LatentAttnArgs& a, const CUten
 #pragma unroll 1
             for (int c = 0; c < L::kChunks; ++c)
               if (has(c))
-                sts16(d + c * kChunk,
+                sts16(place(row) + c * kChunk,
                       src && !drop ? ld_shared_ro16(src + part(c)) : make_uint4(0, 0, 0, 0));
           }
           if (col == 0) sts_u8(flags + row, flag);
+        }
+        if (kInPlace && mixed) {
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          __syncwarp();
+#pragma unroll 1
+          for (int i = 0; i < kRows; ++i) {
+            const int row = row0 + 4 * i;
+            bool sp = false;
+#pragma unroll
+            for (int c = 0; c < L::kChunks; ++c)  // (what this lane has copied)
+              if (has(c)) sp |= any_special<FMT>(lds16(place(row) + c * kChunk));
+            if (__ballot_sync(0xFFFFFFFFu, sp) & (0xFFu << (lane & 24))) {
+#pragma unroll 1
+              for (int c = 0; c < L::kChunks; ++c)
+                if (has(c)) sts16(place(row) + c * kChunk, make_uint4(0, 0, 0, 0));
+              if (col == 0) sts_u8(flags + row, kPoison);
+            }
+          }
         }
         __syncwarp();
 #pragma unroll
@@ -847,23 +874,41 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
       for (int i = 0; i < 4; ++i) x[j][i] *= cs[j][i & 1];
     if (__builtin_expect((t.kt + 1) * kKeys > t.least || __any_sync(0xFFFFFFFFu, (f0 | f1) != 0), 0)) {
       const int p = t.kt * kKeys + key0;
+      // a row behind the last one (its query is zeros) copies the last one's view
+      auto token = [&](int j, int e) {
+        const uint32_t row = min((uint32_t)t.qt * NR + col0 + 8 * j + c2 + e,
+                                 (uint32_t)t.ntok * (uint32_t)a.num_heads - 1);
+        return t.t0 + token_of(a, row);
+      };
+      uint32_t in0[kG][2], in1[kG][2];  // TREE: whether the masks name the two rows
+      if constexpr (TREE) {
+        // (all loads at once; those for rows in front of the new tokens are not used)
+        const Node n0(a, walk.q, max(p, t.least)), n1(a, walk.q, max(p + 8, t.least));
+#pragma unroll
+        for (int j = 0; j < kG; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t* m = a.tree + (int64_t)token(j, e) * a.tree_ts;
+            in0[j][e] = __ldg(m + n0.word);
+            in1[j][e] = __ldg(m + n1.word);
+          }
+#pragma unroll
+        for (int j = 0; j < kG; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            in0[j][e] = p < t.least ? 1u : in0[j][e] & n0.bit;
+            in1[j][e] = p + 8 < t.least ? 1u : in1[j][e] & n1.bit;
+          }
+      }
 #pragma unroll
       for (int j = 0; j < kG; ++j)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          // a row behind the last one (its query is zeros) copies the last one's view
-          const uint32_t row = min((uint32_t)t.qt * NR + col0 + 8 * j + c2 + e,
-                                   (uint32_t)t.ntok * (uint32_t)a.num_heads - 1);
-          const int tok = t.t0 + token_of(a, row), seen = seen_of<TREE>(a, walk.q, tok);
+          const int seen = TREE ? t.most : seen_of<TREE>(a, walk.q, token(j, e));
           if (f0 == kPoison) x[j][e] = NAN;
           if (f1 == kPoison) x[j][e + 2] = NAN;
-          bool s0 = p < seen, s1 = p + 8 < seen;
-          if constexpr (TREE) {
-            if (s0 && p >= t.least) s0 = in_tree(a, walk.q, tok, p);
-            if (s1 && p + 8 >= t.least) s1 = in_tree(a, walk.q, tok, p + 8);
-          }
-          if (!s0 || f0 == kAbsent) x[j][e] = -INFINITY;
-          if (!s1 || f1 == kAbsent) x[j][e + 2] = -INFINITY;
+          if (p >= seen || f0 == kAbsent || (TREE && !in0[j][e])) x[j][e] = -INFINITY;
+          if (p + 8 >= seen || f1 == kAbsent || (TREE && !in1[j][e])) x[j][e + 2] = -INFINITY;
         }
     }
     // Only whether a score passes its row's reference by more than 2^kGrow is asked of

@@ -138,7 +138,8 @@ struct Split {
 };
 struct Workspace {
   Split* split;  // [ctas]
-  float *m, *l;  // [2 ctas][slot_rows]: reference (log2) and sum of the weights
+  float *m, *l, *d;  // [2 ctas][slot_rows]: reference (log2), sum of the weights, and what it is
+                     // divided by less that
   float* o;      // [2 ctas][32][slot_rows][4]: 4 dims of a row lie together, so that a thread a
                  // row writes whole lines
 };
@@ -151,7 +152,8 @@ __host__ __device__ inline Workspace workspace_of(uint8_t* p, int ctas, int rows
   w.split = reinterpret_cast<Split*>(p);
   w.m = reinterpret_cast<float*>(p + (int64_t)ctas * sizeof(Split));
   w.l = w.m + (int64_t)ctas * 2 * rows;
-  w.o = w.l + (int64_t)ctas * 2 * rows;
+  w.d = w.l + (int64_t)ctas * 2 * rows;
+  w.o = w.d + (int64_t)ctas * 2 * rows;
   return w;
 }
 
@@ -794,16 +796,20 @@ __device__ __noinline__ uint32_t look_after(uint32_t v, int least, int most) {
 }
 
 // The weights of an item's units (a function of its own, so that its loop has the registers to
-// itself): the row's reference and the sum of its weights.  False: given up.
+// itself): the row's reference, the sum of its weights, and how much more they are as they are
+// rounded.  (The last is counted in the units that not every row sees whole: a row of few keys,
+// all of them there, is divided by the weights that its products had, so that their rounding
+// does not scale it.  In long rows the roundings cancel, and the count would cost each unit.)
+// False: given up.
 template <int F, int KF>
-__device__ __noinline__ bool unit_weights(Part s, const Waiter waiter, float& mu_out, float& l_out) {
+__device__ __noinline__ bool unit_weights(Part s, const Waiter waiter, float& mu_out, float& l_out, float& d_out) {
   using R = Ref<F>;
   using L = Lay<KF>;
   const int lane = threadIdx.x & 31;
   auto wait = [&](int bar, uint32_t phase) {
     return __all_sync(0xFFFFFFFFu, waiter(s.smem + L::bars + 8 * bar, phase & 1));
   };
-  float mu = -INFINITY, l = 0.0f;
+  float mu = -INFINITY, l = 0.0f, d = 0.0f;
 #pragma unroll 1
   for (int kt = 0; kt < s.count; ++kt, ++s.n) {
     if (!wait(L::kSFull + 2 * s.tile + (s.n & 1), s.n >> 1)) return false;
@@ -852,6 +858,7 @@ __device__ __noinline__ bool unit_weights(Part s, const Waiter waiter, float& mu
       const float mn = fmaxf(mu, ceilf(top) - R::kTop);
       const float f = mu == -INFINITY ? 0.0f : ex2(mu - mn);
       l = l == 0.0f ? 0.0f : l * f;  // (a NaN stays)
+      d *= f;
       mu = mn;
       if (kt > 0) {
         if (!wait(L::kPvDone + 2 * s.tile + ((s.n - 1) & 1), (s.n - 1) >> 1)) return false;
@@ -881,6 +888,15 @@ __device__ __noinline__ bool unit_weights(Part s, const Waiter waiter, float& mu
     tc::st_32x32(s_at, pk);
     const float2 s2 = unf2(add2(sum[0], sum[1]));
     l += s2.x + s2.y;
+    if (__builtin_expect(kt >= s.from, 0)) {
+      float r0 = 0.0f, r1 = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kKeys / 2; ++j) {
+        r0 += x16lo<F>(pk[j]);
+        r1 += x16hi<F>(pk[j]);
+      }
+      d += (r0 - s2.x) + (r1 - s2.y);
+    }
     tc::wait_st();
     tc::fence_before_sync();
     __syncwarp();
@@ -888,6 +904,7 @@ __device__ __noinline__ bool unit_weights(Part s, const Waiter waiter, float& mu
   }
   mu_out = mu;
   l_out = l;
+  d_out = d;
   return true;
 }
 
@@ -926,7 +943,7 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, bool boxes, u
     const uint32_t row = it.row0 + tile * kM + r;
     const int seen = ok ? seen_of(a, it.base, it.m, row) : 0, shift = it.kb * kKeys;
     const int mend = max(it.ragged(), tile ? it.end[0] : 0);
-    float c = fabsf(a.softmax_scale * ks) * kLog2e, mu, l;
+    float c = fabsf(a.softmax_scale * ks) * kLog2e, mu, l, d;
     if constexpr (F != QF) {
       if (count > 0) {
         if (!__all_sync(0xFFFFFFFFu, waiter(bars + 8 * (L::kQFull + tile), opened++ & 1))) return;
@@ -940,7 +957,7 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, bool boxes, u
     if (!unit_weights<F, KF>(Part{smem, s_at, o_at, n, g, cleaned, mended, (int)(g % L::kStages), tile, count,
                               it.ragged() - it.kb, mend - it.kb, it.least - shift, it.most - shift,
                               seen - shift, live, c},
-                         waiter, mu, l))
+                         waiter, mu, l, d))
       return;
     mended += max(it.end[tile] - mend, 0);
     n += count;
@@ -962,10 +979,11 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, bool boxes, u
       if (ok && !whole) {
         ws.m[slot + at] = mu;
         ws.l[slot + at] = l;
+        ws.d[slot + at] = d;
       } else if (ok && a.lse) {
         a.lse[t * a.lse_ts + h * a.lse_hs] = l == 0.0f ? -INFINITY : (mu + __log2f(l)) * kLn2;
       }
-      const float inv = l == 0.0f ? 0.0f : __fdividef(ks, l);
+      const float inv = l == 0.0f ? 0.0f : __fdividef(ks, l + d);
       // where 32 dims of the row go, and how far the next lie
       uint8_t* to = whole ? a.out + t * a.out_ts + h * a.out_hs
                           : reinterpret_cast<uint8_t*>(ws.o + slot * kV + at * 4);  // [dims / 4][rows][4]
@@ -1113,20 +1131,21 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefill_join_kernel(const Pre
     const int r = (n >> 3) * 8 + (lane & 7), quad = (n & 7) * 4 + (lane >> 3);
     if (r >= sp.rows) continue;
     float4 acc = make_float4(0, 0, 0, 0);
-    float sum = 0.0f, top = -INFINITY;
+    float sum = 0.0f, more = 0.0f, top = -INFINITY;
     // the first partial lies in the odd slot of the first CTA, the others in the even ones behind
 #pragma unroll 1
     for (int i = 0; i < sp.parts; i += 4) {
       float4 v[4];
-      float lv[4], mv[4];
+      float lv[4], dv[4], mv[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int64_t slot = 2 * (int64_t)(sp.first + i + k) + (i + k == 0 ? 1 : 0);
-        lv[k] = 0.0f;
+        lv[k] = dv[k] = 0.0f;
         mv[k] = -INFINITY;
         v[k] = make_float4(0, 0, 0, 0);
         if (i + k < sp.parts) {
           lv[k] = ws.l[slot * srows + r];
+          dv[k] = ws.d[slot * srows + r];
           mv[k] = ws.m[slot * srows + r];
           v[k] = __ldcs(reinterpret_cast<const float4*>(ws.o + slot * srows * kV) + quad * srows + r);
         }
@@ -1141,12 +1160,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefill_join_kernel(const Pre
         acc.z = fmaf(acc.z, f, w * v[k].z);
         acc.w = fmaf(acc.w, f, w * v[k].w);
         sum = fmaf(sum, f, w * lv[k]);
+        more = fmaf(more, f, w * dv[k]);
         top = m;
       }
     }
     const uint32_t row = sp.row0 + r, dt = a.by_group(row);
     const int64_t t = sp.tok0 + (int)dt, h = (int64_t)sp.head * a.group + (int)(row - dt * a.group);
-    const float inv = sum == 0.0f ? 0.0f : __fdividef(a.kv_scale ? __ldg(a.kv_scale) : 1.0f, sum);
+    const float inv = sum == 0.0f ? 0.0f : __fdividef(a.kv_scale ? __ldg(a.kv_scale) : 1.0f, sum + more);
     st8(a.out + t * a.out_ts + h * a.out_hs + quad * 8,
         make_uint2(pack16x2<QF>(acc.x * inv, acc.y * inv), pack16x2<QF>(acc.z * inv, acc.w * inv)));
     if (quad == 0 && a.lse)
@@ -1264,7 +1284,7 @@ int64_t prefill_attention_workspace(int32_t num_tokens, int32_t num_heads, int32
                                     int num_sms) {
   const int64_t ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
   return ctas * ((int64_t)sizeof(Split) +
-                 2 * slot_rows(num_tokens, num_heads / kv_heads) * (2 + kV) * (int64_t)sizeof(float));
+                 2 * slot_rows(num_tokens, num_heads / kv_heads) * (3 + kV) * (int64_t)sizeof(float));
 }
 
 cudaError_t launch_prefill_attention(const PrefillArgs& a, int fmt, int kv_fmt, int num_sms,
