@@ -190,9 +190,13 @@ struct Seq {
   int32_t t0, ntok;  // tokens t0 .. t0 + ntok - 1 are computed
   int32_t c1, kv;
   int32_t nqt;       // query tiles
-  int32_t first;     // TREE: the row of the first new token (below 0: it has none)
+};
+struct TreeSeq : Seq {
+  int32_t first;     // the row of the first new token (below 0: it has none)
   __device__ __forceinline__ int ctx(const LatentAttnArgs& a) const { return max(0, min(first, a.room)); }
 };
+template <bool TREE>
+using SeqOf = std::conditional_t<TREE, TreeSeq, Seq>;
 
 // Token of a sequence's query row (row < 2^31).
 __device__ __forceinline__ int token_of(const LatentAttnArgs& a, uint32_t row) {
@@ -200,8 +204,8 @@ __device__ __forceinline__ int token_of(const LatentAttnArgs& a, uint32_t row) {
 }
 
 template <int NR, bool TREE>
-__device__ __forceinline__ Seq load_seq(const LatentAttnArgs& a, int s) {
-  Seq q;
+__device__ __forceinline__ SeqOf<TREE> load_seq(const LatentAttnArgs& a, int s) {
+  SeqOf<TREE> q;
   const int32_t c0 = __ldg(a.cu_q + s);
   q.c1 = __ldg(a.cu_q + s + 1);
   q.kv = __ldg(a.kv_lens + s);
@@ -221,7 +225,7 @@ __device__ __forceinline__ int seen_of(const LatentAttnArgs& a, const Seq& q, in
 // TREE: row p >= q.ctx(), a new one, among the masks' bits.
 struct Node {
   uint32_t word, bit;  // bit 0 when no mask has one for it
-  __device__ __forceinline__ Node(const LatentAttnArgs& a, const Seq& q, int p) {
+  __device__ __forceinline__ Node(const LatentAttnArgs& a, const TreeSeq& q, int p) {
     const uint32_t n = (uint32_t)p - (uint32_t)q.first;  // (at most 2^31 + kMaxTree)
     word = min(n >> 5, a.tree_words - 1);
     bit = n < 32u * a.tree_words ? 1u << (n & 31) : 0u;
@@ -252,8 +256,9 @@ struct Tile {
 // A CTA's run of units: where it starts, and what finds the CTA of another unit.  A
 // query tile is kSwitch units that stand for beginning it, then its key tiles: a run
 // starts before the first of these when kt is negative.
+template <bool TREE>
 struct Run {
-  Seq q;               // of sequence s
+  SeqOf<TREE> q;               // of sequence s
   int s, qt, kt, count;
   int64_t begin, each; // the first unit; units of the CTAs c >= extra (each + 1 of the ones before)
   int extra;
@@ -263,17 +268,18 @@ struct Run {
 // Walks the run; every role has its own copy.
 template <int NR, int kSwitch, bool TREE>
 struct Walk {
-  Seq q;
+  SeqOf<TREE> q;
   int s, qt, kt, nkt, most, least;
   int left;
   bool fresh;
   __device__ __forceinline__ void item(const LatentAttnArgs& a) {
     most = most_seen<NR, TREE>(a, q, qt);
-    least = TREE ? min(q.ctx(a), most) : seen_of<TREE>(a, q, q.t0 + token_of(a, (uint32_t)qt * NR));
+    if constexpr (TREE) least = min(q.ctx(a), most);
+    else least = seen_of<TREE>(a, q, q.t0 + token_of(a, (uint32_t)qt * NR));
     nkt = key_tiles(most);
     fresh = true;
   }
-  __device__ __forceinline__ void start(const Run& r) {
+  __device__ __forceinline__ void start(const Run<TREE>& r) {
     q = r.q;
     s = r.s;
     qt = r.qt;
@@ -447,7 +453,7 @@ __device__ __forceinline__ void split_q(const LatentAttnArgs& a, const Tile& q, 
 // Returns the key tiles whose copies were issued.
 template <int FMT, int NR, bool TREE>
 __device__ __forceinline__ uint32_t produce(const LatentAttnArgs& a, const CUtensorMap& map,
-                                        const Run& run, uint32_t smem, const Waiter& wait, int pw,
+                                        const Run<TREE>& run, uint32_t smem, const Waiter& wait, int pw,
                                         int lane, uint32_t& errbits) {
   using L = Lay<FMT, NR>;
   const uint32_t bars = smem + L::bars;
@@ -525,11 +531,6 @@ __device__ __forceinline__ uint32_t produce(const LatentAttnArgs& a, const CUten
         if (L::kHalves > 1 && !freed(1)) break;
         // tokens of the query tile see different rows of this key tile
         const bool mixed = cur.least < cur.most && (cur.kt + 1) * kKeys > cur.least;
-        // the 16-byte parts of this lane: chunk c, and for fp8 the rotary columns of
-        // the last chunk (its upper half) in lanes 4 to 7
-        auto part = [&](int c) { return !L::kF8 || c < 4 ? c * 128 + col * 16 : 512 + (col - 4) * 16; };
-        auto has = [&](int c) { return !L::kF8 || c < 4 || col >= 4; };
-        auto place = [&](int row) { return base + row * 128 + ((col ^ (row & 7)) << 4); };
         // Rows of mixed tiles are looked at for NaNs and infinities: in shared memory once they are
         // there, or, in tiles of 16 query rows without masks, where mixed tiles are few, in the
         // cache before they are stored.  (us with the first and the second: 32 verifications of 4
@@ -543,12 +544,17 @@ __device__ __forceinline__ uint32_t produce(const LatentAttnArgs& a, const CUten
           uint32_t flag;
           const uint8_t* src = row_in(a, cur.kt * kKeys + row, bi, flag);
           if (flag) errbits |= kErrBlockOOB;
+          const uint32_t d = base + row * 128 + ((col ^ (row & 7)) << 4);
+          // the 16-byte parts of this lane: chunk c, and for fp8 the rotary columns of
+          // the last chunk (its upper half) in lanes 4 to 7
+          auto part = [&](int c) { return !L::kF8 || c < 4 ? c * 128 + col * 16 : 512 + (col - 4) * 16; };
+          auto has = [&](int c) { return !L::kF8 || c < 4 || col >= 4; };
           if (kInPlace || !mixed) {
 #pragma unroll
             for (int c = 0; c < L::kChunks; ++c)
-              if (has(c)) tc::cp_async16(place(row) + c * kChunk, src ? src + part(c) : a.cache, src != nullptr);
+              if (has(c)) tc::cp_async16(d + c * kChunk, src ? src + part(c) : a.cache, src != nullptr);
           } else {
-            // once to look, and again to store
+            // once to look for NaNs and infinities, and again to store
             bool sp = false;
 #pragma unroll
             for (int c = 0; c < L::kChunks; ++c)
@@ -558,26 +564,29 @@ __device__ __forceinline__ uint32_t produce(const LatentAttnArgs& a, const CUten
 #pragma unroll 1
             for (int c = 0; c < L::kChunks; ++c)
               if (has(c))
-                sts16(place(row) + c * kChunk,
+                sts16(d + c * kChunk,
                       src && !drop ? ld_shared_ro16(src + part(c)) : make_uint4(0, 0, 0, 0));
           }
           if (col == 0) sts_u8(flags + row, flag);
         }
-        if (kInPlace && mixed) {
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          __syncwarp();
+        if constexpr (kInPlace) {
+          if (mixed) {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncwarp();
 #pragma unroll 1
-          for (int i = 0; i < kRows; ++i) {
-            const int row = row0 + 4 * i;
-            bool sp = false;
+            for (int i = 0; i < kRows; ++i) {
+              const int row = row0 + 4 * i;
+              const uint32_t d = base + row * 128 + ((col ^ (row & 7)) << 4);
+              bool sp = false;
 #pragma unroll
-            for (int c = 0; c < L::kChunks; ++c)  // (what this lane has copied)
-              if (has(c)) sp |= any_special<FMT>(lds16(place(row) + c * kChunk));
-            if (__ballot_sync(0xFFFFFFFFu, sp) & (0xFFu << (lane & 24))) {
+              for (int c = 0; c < L::kChunks; ++c)  // (what this lane has copied)
+                if (!L::kF8 || c < 4 || col >= 4) sp |= any_special<FMT>(lds16(d + c * kChunk));
+              if (__ballot_sync(0xFFFFFFFFu, sp) & (0xFFu << (lane & 24))) {
 #pragma unroll 1
-              for (int c = 0; c < L::kChunks; ++c)
-                if (has(c)) sts16(place(row) + c * kChunk, make_uint4(0, 0, 0, 0));
-              if (col == 0) sts_u8(flags + row, kPoison);
+                for (int c = 0; c < L::kChunks; ++c)
+                  if (!L::kF8 || c < 4 || col >= 4) sts16(d + c * kChunk, make_uint4(0, 0, 0, 0));
+                if (col == 0) sts_u8(flags + row, kPoison);
+              }
             }
           }
         }
@@ -716,7 +725,7 @@ __device__ __noinline__ int cta_of(int64_t u, int64_t each, int extra) {
 // they would wait for the scores of the next tile or for its polls of both (2 chunks of
 // 1024 tokens 726 us from one warp, 695 from two, both before later steps).
 template <int FMT, int NR, bool TREE>
-__device__ __forceinline__ void score_role(const LatentAttnArgs& a, const Run& run, uint32_t smem,
+__device__ __forceinline__ void score_role(const LatentAttnArgs& a, const Run<TREE>& run, uint32_t smem,
                                            uint32_t tmem, const Waiter& waiter) {
   using L = Lay<FMT, NR>;
   const uint32_t bars = smem + L::bars;
@@ -751,7 +760,7 @@ __device__ __forceinline__ void score_role(const LatentAttnArgs& a, const Run& r
 }
 
 template <int FMT, int NR, bool TREE>
-__device__ __forceinline__ void output_role(const LatentAttnArgs& a, const Run& run, uint32_t smem,
+__device__ __forceinline__ void output_role(const LatentAttnArgs& a, const Run<TREE>& run, uint32_t smem,
                                             uint32_t tmem, const Waiter& waiter, int lane,
                                             const Workspace& ws) {
   using L = Lay<FMT, NR>;
@@ -790,7 +799,7 @@ __device__ __forceinline__ void output_role(const LatentAttnArgs& a, const Run& 
 
 // ----------------------------------------------------------- softmax and output
 template <int FMT, int NR, bool TREE>
-__device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, uint32_t smem,
+__device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run<TREE>& run, uint32_t smem,
                                        uint32_t tmem, const Waiter& waiter, int warp, int lane,
                                        const Workspace& ws) {
   using L = Lay<FMT, NR>;
@@ -875,11 +884,6 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
     if (__builtin_expect((t.kt + 1) * kKeys > t.least || __any_sync(0xFFFFFFFFu, (f0 | f1) != 0), 0)) {
       const int p = t.kt * kKeys + key0;
       // a row behind the last one (its query is zeros) copies the last one's view
-      auto token = [&](int j, int e) {
-        const uint32_t row = min((uint32_t)t.qt * NR + col0 + 8 * j + c2 + e,
-                                 (uint32_t)t.ntok * (uint32_t)a.num_heads - 1);
-        return t.t0 + token_of(a, row);
-      };
       uint32_t in0[kG][2], in1[kG][2];  // TREE: whether the masks name the two rows
       if constexpr (TREE) {
         // (all loads at once; those for rows in front of the new tokens are not used)
@@ -888,7 +892,9 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
         for (int j = 0; j < kG; ++j)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const uint32_t* m = a.tree + (int64_t)token(j, e) * a.tree_ts;
+            const uint32_t row = min((uint32_t)t.qt * NR + col0 + 8 * j + c2 + e,
+                                     (uint32_t)t.ntok * (uint32_t)a.num_heads - 1);
+            const uint32_t* m = a.tree + (int64_t)(t.t0 + token_of(a, row)) * a.tree_ts;
             in0[j][e] = __ldg(m + n0.word);
             in1[j][e] = __ldg(m + n1.word);
           }
@@ -896,19 +902,28 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
         for (int j = 0; j < kG; ++j)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            in0[j][e] = p < t.least ? 1u : in0[j][e] & n0.bit;
-            in1[j][e] = p + 8 < t.least ? 1u : in1[j][e] & n1.bit;
+            in0[j][e] = p < t.most && (p < t.least || (in0[j][e] & n0.bit) != 0);
+            in1[j][e] = p + 8 < t.most && (p + 8 < t.least || (in1[j][e] & n1.bit) != 0);
           }
       }
 #pragma unroll
       for (int j = 0; j < kG; ++j)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int seen = TREE ? t.most : seen_of<TREE>(a, walk.q, token(j, e));
-          if (f0 == kPoison) x[j][e] = NAN;
-          if (f1 == kPoison) x[j][e + 2] = NAN;
-          if (p >= seen || f0 == kAbsent || (TREE && !in0[j][e])) x[j][e] = -INFINITY;
-          if (p + 8 >= seen || f1 == kAbsent || (TREE && !in1[j][e])) x[j][e + 2] = -INFINITY;
+          if constexpr (TREE) {
+            if (f0 == kPoison) x[j][e] = NAN;
+            if (f1 == kPoison) x[j][e + 2] = NAN;
+            if (!in0[j][e] || f0 == kAbsent) x[j][e] = -INFINITY;
+            if (!in1[j][e] || f1 == kAbsent) x[j][e + 2] = -INFINITY;
+          } else {
+            const uint32_t row = min((uint32_t)t.qt * NR + col0 + 8 * j + c2 + e,
+                                     (uint32_t)t.ntok * (uint32_t)a.num_heads - 1);
+            const int seen = seen_of<TREE>(a, walk.q, t.t0 + token_of(a, row));
+            if (f0 == kPoison) x[j][e] = NAN;
+            if (f1 == kPoison) x[j][e + 2] = NAN;
+            if (p >= seen || f0 == kAbsent) x[j][e] = -INFINITY;
+            if (p + 8 >= seen || f1 == kAbsent) x[j][e + 2] = -INFINITY;
+          }
         }
     }
     // Only whether a score passes its row's reference by more than 2^kGrow is asked of
@@ -1141,7 +1156,8 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run& run, 
 // The runs of `total` units: the first `extra` CTAs take one unit more than the
 // others; fewer CTAs than the grid has when each would get less than kMinUnits.
 __device__ __noinline__ int64_t divide(int64_t n, int64_t d) { return n / d; }
-__device__ __forceinline__ void cut(int64_t total, Run& r) {
+template <typename R>
+__device__ __forceinline__ void cut(int64_t total, R& r) {
   const uint32_t ctas = total >= (int64_t)gridDim.x * kMinUnits
                             ? gridDim.x
                             : max(1u, (uint32_t)total / (uint32_t)kMinUnits);
@@ -1164,11 +1180,11 @@ __device__ __forceinline__ int64_t scan64(int64_t v, int lane) {  // inclusive, 
 // by itself without a barrier, a lane looking at four neighbouring sequences.
 constexpr int kLaneSeqs = 4, kSmallTiles = 8;
 template <int NR, int kSwitch, bool TREE>
-__device__ __forceinline__ bool schedule_small(const LatentAttnArgs& a, int lane, Run& r,
+__device__ __forceinline__ bool schedule_small(const LatentAttnArgs& a, int lane, Run<TREE>& r,
                                                uint32_t& errbits) {
   if (a.num_seqs > 32 * kLaneSeqs) return false;
   const int per = (a.num_seqs + 31) >> 5, s0 = lane * per;  // this lane's sequences
-  Seq q[kLaneSeqs];
+  SeqOf<TREE> q[kLaneSeqs];
 #pragma unroll
   for (int i = 0; i < kLaneSeqs; ++i) {
     q[i].nqt = 0;
@@ -1223,14 +1239,14 @@ __device__ __forceinline__ bool schedule_small(const LatentAttnArgs& a, int lane
 // Any number of sequences and query tiles, by the whole CTA; the scratch is the
 // (still unused) first key stage.
 template <int NR, int kSwitch, int kWarps, bool TREE>
-__device__ __noinline__ void schedule_large(const LatentAttnArgs& a, uint8_t* scratch, Run& r) {
+__device__ __noinline__ void schedule_large(const LatentAttnArgs& a, uint8_t* scratch, Run<TREE>& r) {
   constexpr int kThreads = kWarps * 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int64_t* pre = reinterpret_cast<int64_t*>(scratch);  // [num_seqs]
   int64_t* part = pre + a.num_seqs;                    // [kWarps]
   int64_t* at = part + kWarps;                         // sequence, unit in it, query tile, key tile
   for (int s = warp; s < a.num_seqs; s += kWarps) {
-    const Seq q = load_seq<NR, TREE>(a, s);
+    const SeqOf<TREE> q = load_seq<NR, TREE>(a, s);
     int64_t u = 0;
     for (int qt = lane; qt < q.nqt; qt += 32)
       u += kSwitch + key_tiles(most_seen<NR, TREE>(a, q, qt));
@@ -1351,9 +1367,9 @@ __global__ void __launch_bounds__(Lay<FMT, NR>::kThreads, 1)
   const Workspace ws = workspace_of<NR>(a.workspace, gridDim.x);
   if (threadIdx.x == 0) ws.split[blockIdx.x] = Split{0, 0, 0, 0, 0};
   uint32_t errbits = 0;
-  Run run;
+  Run<TREE> run;
   if (!schedule_small<NR, L::kSwitch, TREE>(a, lane, run, errbits)) {
-    Run large;  // apart, so that only this branch has it in memory
+    Run<TREE> large;  // apart, so that only this branch has it in memory
     schedule_large<NR, L::kSwitch, L::kWarps, TREE>(a, smem_raw, large);
     run = large;
   }

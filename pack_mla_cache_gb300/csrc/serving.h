@@ -80,9 +80,6 @@ struct LatentAttnArgs {
   float softmax_scale;
   const float* k_scale;  // fp8 caches only
   bool causal;
-  const uint32_t* tree;  // trees only: ancestor bits, tree_words words a token
-  int64_t tree_ts;       // words
-  uint32_t tree_words;   // at most kMaxTree / 32
   uint8_t* out;
   int64_t out_ts, out_hs;
   float* lse;  // may be null
@@ -91,6 +88,9 @@ struct LatentAttnArgs {
   uint32_t* err;
   uint64_t wait_limit_ns;
   int32_t stall_stage;  // testing: this pipeline stage (from 1) of CTA 0 never fills
+  const uint32_t* tree;  // trees only: ancestor bits, tree_words words a token
+  int64_t tree_ts;       // words
+  uint32_t tree_words;   // at most kMaxTree / 32
 };
 
 // Drafted tokens that a tree's masks can name.
