@@ -73,6 +73,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 // this many more.
 constexpr int kSwitch = 2;
 constexpr int kMinUnits = 4;  // a CTA takes at least this many
+// Calls of at most this many key rows, and of no more items than CTAs, give every CTA a whole
+// item: nothing is cut, and nothing has to be joined.
+constexpr int kWholeKeys = 512;
 
 // The reference of a row's weights is the next whole number (log2) above its maximum less
 // kTop; a score may pass the reference by kGrow before the sums are rescaled.  fp16 weights:
@@ -121,8 +124,8 @@ struct Misc {
 
 // How a tensor map reads row p, columns c.. of key head g: box (x_head * g + c, p, z_head * g).
 struct Maps {
-  CUtensorMap qn, qp;  // (column, head, token); only where q_tokens is not 0
   CUtensorMap kn, kp, v;
+  CUtensorMap qn, qp;  // (column, head, token); only where q_tokens is not 0
   int32_t kn_x, kn_z, kp_x, kp_z, v_x, v_z;
   int32_t q_tokens;  // tokens of a query tile that comes in boxes; 0: rows are copied one by one
 };
@@ -189,6 +192,11 @@ __device__ __forceinline__ int seen_of(const PrefillArgs& a, int64_t base, int m
 __device__ __forceinline__ int key_tiles(int most) { return max(1, (most + kKeys - 1) / kKeys); }
 __device__ __forceinline__ int item_tiles(const PrefillArgs& a, const Seq& q, int b) {
   return key_tiles(seen_of(a, q.base, q.m, min((uint32_t)(b + 1) * kItemRows, q.rows) - 1));
+}
+
+// Units of an item; one where a CTA takes whole items.
+__device__ __forceinline__ int item_units(const PrefillArgs& a, const Seq& q, int b) {
+  return a.whole ? 1 : kSwitch + item_tiles(a, q, b);
 }
 
 // A CTA's part of an item.
@@ -289,7 +297,7 @@ struct Plan {
         nb = one.nb;
         if (nb <= 4)
 #pragma unroll 1
-          for (int i = 0; i < nb; ++i) u += kSwitch + item_tiles(a, one, i);
+          for (int i = 0; i < nb; ++i) u += item_units(a, one, i);
       }
       // sequences of many items: by the whole warp
       for (uint32_t many = __ballot_sync(0xFFFFFFFFu, nb > 4); many; many &= many - 1) {
@@ -297,7 +305,7 @@ struct Plan {
         const Seq one = load_seq(a, s0 + from, ignored);
         I sum = 0;
 #pragma unroll 1
-        for (int i = lane; i < one.nb; i += 32) sum += kSwitch + item_tiles(a, one, i);
+        for (int i = lane; i < one.nb; i += 32) sum += item_units(a, one, i);
         sum = __shfl_sync(0xFFFFFFFFu, scan<I>(sum, lane), 31);
         if (lane == from) u = sum;
       }
@@ -307,7 +315,7 @@ struct Plan {
       total += __shfl_sync(0xFFFFFFFFu, in, 31);
     }
     __syncwarp();
-    const I ctas = max((I)1, min((I)gridDim.x, total / (I)kMinUnits));
+    const I ctas = a.whole ? max((I)1, total) : max((I)1, min((I)gridDim.x, total / (I)kMinUnits));
     each = over(total, ctas);
     extra = (int)(total - each * ctas);
     begin = each * blockIdx.x + min((int)blockIdx.x, extra);
@@ -329,7 +337,7 @@ struct Plan {
     I base = 0;
 #pragma unroll 1
     for (int b0 = 0;; b0 += 32) {
-      const I u = b0 + lane < q.nb ? kSwitch + item_tiles(a, q, b0 + lane) : 0;
+      const I u = b0 + lane < q.nb ? item_units(a, q, b0 + lane) : 0;
       const I in = scan<I>(u, lane);
       const uint32_t hit = __ballot_sync(0xFFFFFFFFu, off < base + in);
       if (hit) {
@@ -340,7 +348,7 @@ struct Plan {
       }
       base += __shfl_sync(0xFFFFFFFFu, in, 31);
     }
-    left = count + min(kt, 0);
+    left = a.whole ? item_tiles(a, q, b) : count + min(kt, 0);
     kt = max(kt, 0);
   }
   // The next item (the first call: the run's first).
@@ -1072,6 +1080,8 @@ __global__ void __launch_bounds__(warps_of(KF) * 32, 1)
     }
     mbar_fence_init();
   }
+  if (warp == kLoadWarp && lane < (maps.q_tokens != 0 ? 5 : 3))
+    tc::prefetch_map(reinterpret_cast<const CUtensorMap*>(&maps) + lane);
   const Waiter wait{smem_addr(&m.abort), a.wait_limit_ns};
   pdl_wait();
   if (warp == kScoreWarp) tc::alloc(smem_addr(&m.tmem), kTmem);
@@ -1114,8 +1124,9 @@ __global__ void __launch_bounds__(warps_of(KF) * 32, 1)
 
 // -------------------------------------------------------- join of the split items
 // Block (x, c) looks at what CTA c left.  An item of `parts` CTAs is dealt to the warps of the
-// blocks of all of them but the last: 8 rows x 16 dims a warp, a lane four dims of a row.
-constexpr int kJoinWarps = 8, kJoinBlocks = 32;
+// blocks of all of them but the last: 8 rows x 32 dims a warp, a lane two times four dims of a
+// row.
+constexpr int kJoinWarps = 8, kJoinBlocks = 16;
 
 template <int QF>
 __global__ void __launch_bounds__(kJoinWarps * 32) prefill_join_kernel(const PrefillArgs a) {
@@ -1127,38 +1138,39 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefill_join_kernel(const Pre
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int stride = (sp.parts - 1) * kJoinBlocks * kJoinWarps;
   for (int n = (((int)blockIdx.y - sp.first) * kJoinBlocks + (int)blockIdx.x) * kJoinWarps + warp;
-       n < (sp.rows + 7) / 8 * 8; n += stride) {
-    const int r = (n >> 3) * 8 + (lane & 7), quad = (n & 7) * 4 + (lane >> 3);
+       n < (sp.rows + 7) / 8 * 4; n += stride) {
+    const int r = (n >> 2) * 8 + (lane & 7), quad = (n & 3) * 8 + (lane >> 3);  // and quad + 4
     if (r >= sp.rows) continue;
-    float4 acc = make_float4(0, 0, 0, 0);
+    float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     float sum = 0.0f, more = 0.0f, top = -INFINITY;
     // the first partial lies in the odd slot of the first CTA, the others in the even ones behind
+    constexpr int kAtOnce = 4;
 #pragma unroll 1
-    for (int i = 0; i < sp.parts; i += 4) {
-      float4 v[4];
-      float lv[4], dv[4], mv[4];
+    for (int i = 0; i < sp.parts; i += kAtOnce) {
+      float4 v[kAtOnce][2];
+      float lv[kAtOnce], dv[kAtOnce], mv[kAtOnce];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < kAtOnce; ++k) {
         const int64_t slot = 2 * (int64_t)(sp.first + i + k) + (i + k == 0 ? 1 : 0);
-        lv[k] = dv[k] = 0.0f;
-        mv[k] = -INFINITY;
-        v[k] = make_float4(0, 0, 0, 0);
+        lv[k] = 0.0f;
         if (i + k < sp.parts) {
           lv[k] = ws.l[slot * srows + r];
           dv[k] = ws.d[slot * srows + r];
           mv[k] = ws.m[slot * srows + r];
-          v[k] = __ldcs(reinterpret_cast<const float4*>(ws.o + slot * srows * kV) + quad * srows + r);
+          const float4* o = reinterpret_cast<const float4*>(ws.o + slot * srows * kV) + r;
+          v[k][0] = __ldcs(o + quad * srows);
+          v[k][1] = __ldcs(o + (quad + 4) * srows);
         }
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < kAtOnce; ++k) {
         if (lv[k] == 0.0f) continue;  // nothing seen there (and perhaps nothing written)
         const float m = fmaxf(top, mv[k]), m0 = m == -INFINITY ? 0.0f : m;
         const float f = ex2(top - m0), w = ex2(mv[k] - m0);
-        acc.x = fmaf(acc.x, f, w * v[k].x);
-        acc.y = fmaf(acc.y, f, w * v[k].y);
-        acc.z = fmaf(acc.z, f, w * v[k].z);
-        acc.w = fmaf(acc.w, f, w * v[k].w);
+        const float x[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w,
+                            v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] = fmaf(acc[j], f, w * x[j]);
         sum = fmaf(sum, f, w * lv[k]);
         more = fmaf(more, f, w * dv[k]);
         top = m;
@@ -1166,9 +1178,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefill_join_kernel(const Pre
     }
     const uint32_t row = sp.row0 + r, dt = a.by_group(row);
     const int64_t t = sp.tok0 + (int)dt, h = (int64_t)sp.head * a.group + (int)(row - dt * a.group);
-    const float inv = sum == 0.0f ? 0.0f : __fdividef(a.kv_scale ? __ldg(a.kv_scale) : 1.0f, sum + more);
-    st8(a.out + t * a.out_ts + h * a.out_hs + quad * 8,
-        make_uint2(pack16x2<QF>(acc.x * inv, acc.y * inv), pack16x2<QF>(acc.z * inv, acc.w * inv)));
+    const float ks = a.kv_scale ? __ldg(a.kv_scale) : 1.0f;
+    const float inv = sum == 0.0f ? 0.0f : __fdividef(ks, sum + more);
+    uint8_t* out = a.out + t * a.out_ts + h * a.out_hs + quad * 8;
+#pragma unroll
+    for (int j = 0; j < 8; j += 4)
+      st8(out + j * 8, make_uint2(pack16x2<QF>(acc[j] * inv, acc[j + 1] * inv),
+                                  pack16x2<QF>(acc[j + 2] * inv, acc[j + 3] * inv)));
     if (quad == 0 && a.lse)
       a.lse[t * a.lse_ts + h * a.lse_hs] = sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * kLn2;
   }
@@ -1249,6 +1265,7 @@ cudaError_t launch_tc(PrefillArgs a, int ctas, const LaunchCfg& cfg) {
   a.out_32 = ((reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)a.out_ts | (uintptr_t)a.out_hs) & 31) == 0;
   const int64_t items = (((int64_t)a.num_tokens * a.group + kItemRows - 1) / kItemRows + a.num_seqs) * a.kv_heads;
   a.few_units = items * (a.num_kv / kKeys + 2 + kSwitch) < INT32_MAX;
+  a.whole = items <= ctas && a.num_kv <= kWholeKeys;
   auto kern = prefill_attention_kernel<F, QF, KF>;
   // the attribute stays with the device's context: set on a device's first call
   static std::atomic<uint64_t> set{0};
@@ -1271,7 +1288,7 @@ cudaError_t launch_tc(PrefillArgs a, int ctas, const LaunchCfg& cfg) {
   lc.attrs = attr;
   lc.numAttrs = cfg.pdl ? 1 : 0;
   e = cudaLaunchKernelEx(&lc, kern, a, maps);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || a.whole) return e;
   lc.gridDim = dim3(kJoinBlocks, ctas);
   lc.blockDim = dim3(kJoinWarps * 32);
   lc.dynamicSmemBytes = 0;

@@ -142,7 +142,8 @@ struct PrefillArgs {
   float softmax_scale;
   const float* kv_scale;  // fp8 keys and values only
   bool causal;
-  bool few_units, out_32;  // units are counted in 32 bits; out rows on 32-byte boundaries (set by the launch)
+  // (set by the launch) units are counted in 32 bits; out rows on 32-byte boundaries; an item a CTA
+  bool few_units, out_32, whole;
   uint8_t* out;
   int64_t out_ts, out_hs;
   float* lse;  // may be null

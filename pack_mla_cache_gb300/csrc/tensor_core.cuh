@@ -333,6 +333,10 @@ __device__ __forceinline__ void tma_load3(uint32_t dst, const void* map, int x, 
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
       : "memory");
 }
+// A tensor map on its way to the copy unit.
+__device__ __forceinline__ void prefetch_map(const void* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 // Arrive on `bar` when this thread's cp_async16 so far are done.
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
