@@ -727,9 +727,11 @@ mla_status_t mla_cache_compact_rows(const int64_t* kv_cache_ptrs, int32_t num_la
  * one rounding of the result to dtype.  Weights exp(x_p), relative to a power of two
  * near the largest seen so far, are rounded before their products: to bf16 (2^-8 of
  * themselves) with bf16 keys and values, and to fp16 (2^-11 of themselves, or 2^-34 of
- * the row's largest) with fp16 and fp8 ones; the sum that they are divided by counts
- * them unrounded.  With fp8 keys and bf16 queries, elements of q below 2^-28 of their
- * row's largest magnitude are off by at most 2^-39 of that magnitude.  Results do not
+ * the row's largest) with fp16 and fp8 ones.  The sum that they are divided by counts
+ * them as rounded in a row's last key tiles (from the first tile of 64 that a neighbour
+ * no longer sees whole), and unrounded before these; lse counts them unrounded.  With
+ * fp8 keys and bf16 queries, elements of q below 2^-31 of their row's largest magnitude
+ * (or of 2^-112, where that is more) are off by at most 2^-39 of it.  Results do not
  * depend on other work on the device; the call's sizes, its lengths and the device's
  * number of SMs decide how rows are cut, and results depend on them through fp32
  * roundings only.
@@ -781,8 +783,9 @@ mla_status_t mla_prefill_attention_workspace(int32_t num_tokens, int32_t num_hea
                                              int64_t* bytes);
 
 /* TESTING HOOK for the attentions (mla_latent_attention, mla_latent_tree_attention,
- * mla_prefill_attention), applied to every later call from this process (not for production use).  wait_limit_ns: how long a wait may last before
- * the kernel gives up (0 restores the default of 2 s).  stall_stage >= 1: that stage
+ * mla_prefill_attention), applied to every later call from this process (not for
+ * production use).  wait_limit_ns: how long a wait may last before the kernel gives up
+ * (0 restores the default of 2 s).  stall_stage >= 1: that stage
  * of the first CTA's pipeline never fills, so its waits run out of time; 0 (the
  * default) stalls nothing.  Returns 0. */
 int mla_test_attention_timeout(uint64_t wait_limit_ns, int32_t stall_stage);

@@ -70,11 +70,17 @@ constexpr int kMaxCtas = 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // What beginning another item costs a CTA, in units: the runs are cut as if each item had
-// this many more.
-constexpr int kSwitch = 2;
-constexpr int kMinUnits = 4;  // a CTA takes at least this many
+// this many more.  An item's change takes about 9000 cycles (the last output's way out, then the
+// next queries and scores) where a unit takes 1700 to 2000.  16 ragged prompts: 200 us with 1,
+// 188 with 2, 179.4 with 4, 180.8 with 6, 183 with 8; 16384 tokens 1060, 1055, 1053, 1053, 1056.
+constexpr int kSwitch = 4;
+// A CTA takes at least this many units, so that a short call is not cut into runs that are all
+// beginning and join: 21 prompts of 6 to 503 tokens, 2 heads, 19.6 us with 4 and 24.6 with 8.
+constexpr int kMinUnits = 4;
 // Calls of at most this many key rows, and of no more items than CTAs, give every CTA a whole
-// item: nothing is cut, and nothing has to be joined.
+// item: nothing is cut, and nothing has to be joined.  Whole against cut, 16 heads: 300 tokens
+// 14.7 and 18.7 us, 500 tokens 18.9 and 19.3, 700 tokens 21.3 and 21.4, 1000 tokens 27.8 and
+// 24.8 (one CTA then does 16 units in turn).
 constexpr int kWholeKeys = 512;
 
 // The reference of a row's weights is the next whole number (log2) above its maximum less
@@ -378,9 +384,10 @@ struct Plan {
       if (++head >= a.kv_heads) {
         head = 0;
         uint32_t ignored = 0;
+        q.nb = 0;
 #pragma unroll 1
-        do q = load_seq(a, ++s, ignored);
-        while (q.nb == 0 && s + 1 < a.num_seqs);
+        while (q.nb == 0 && ++s < a.num_seqs) q = load_seq(a, s, ignored);
+        if (q.nb == 0) left = 0;
       }
     }
     return it;
@@ -612,7 +619,7 @@ __device__ __forceinline__ void issue_outputs(uint32_t smem, uint32_t tmem, bool
 // Four warps issue the products: scores and outputs of a query tile each.  An issue waits for
 // the products before it, and what a warp does between two of its products (looks at barriers,
 // signals) leaves the tensor core idle unless another warp's products are there: 16384 tokens
-// took 1380 us with one warp for all, 1060 with one per tile.  K and V of a unit are free when
+// took 1380 us with one warp for all, 1060 with these.  K and V of a unit are free when
 // both tiles' warps have said so; a warp whose tile has no part in a unit says it when they have
 // come, so that it does not run ahead.
 //
@@ -1263,8 +1270,10 @@ cudaError_t launch_tc(PrefillArgs a, int ctas, const LaunchCfg& cfg) {
     return cudaErrorInvalidValue;
   maps.q_tokens = query_maps(a, QF, &maps);
   a.out_32 = ((reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)a.out_ts | (uintptr_t)a.out_hs) & 31) == 0;
-  const int64_t items = (((int64_t)a.num_tokens * a.group + kItemRows - 1) / kItemRows + a.num_seqs) * a.kv_heads;
-  a.few_units = items * (a.num_kv / kKeys + 2 + kSwitch) < INT32_MAX;
+  const int64_t full = ((int64_t)a.num_tokens * a.group + kItemRows - 1) / kItemRows;
+  const int64_t items = (full + a.num_seqs) * a.kv_heads;
+  // (every sequence taken as long as all: whatever the offsets hold, the count does not overflow)
+  a.few_units = full * a.num_seqs * a.kv_heads < INT32_MAX / (a.num_kv / kKeys + 2 + kSwitch);
   a.whole = items <= ctas && a.num_kv <= kWholeKeys;
   auto kern = prefill_attention_kernel<F, QF, KF>;
   // the attribute stays with the device's context: set on a device's first call

@@ -523,15 +523,25 @@ def mla_cache_compact_rows(kv_cache_ptrs, cache_dtype, num_blocks, block_size, b
         _refuse("starts", starts, "contiguous int32")
     if not _is_list(counts, torch.int32, S):
         _refuse("counts", counts, f"contiguous int32 [{S}]")
-    for name, t in (("block_table", block_table), ("rows", rows)):
-        if t.dtype is not torch.int32 or t.ndim != 2 or t.shape[0] < S or \
-                (t.shape[1] > 1 and t.stride(1) != 1):
-            _refuse(name, t, f"int32 [{S}, .] with a unit last stride")
-    _check(lib().mla_cache_compact_rows(
+    if block_table.dtype is not torch.int32 or block_table.ndim != 2:
+        _refuse("block_table", block_table, f"int32 [{S}, W]")
+    tab_S, tab_W = block_table.shape
+    tab_s, tab_e = block_table.stride()
+    if (tab_e != 1 and tab_W > 1) or tab_S < S:
+        _refuse("block_table", block_table, f"int32 [{S}, W] with a unit last stride")
+    if rows.dtype is not torch.int32 or rows.ndim != 2:
+        _refuse("rows", rows, f"int32 [{S}, N]")
+    rows_S, width = rows.shape
+    rows_s, rows_e = rows.stride()
+    if (rows_e != 1 and width > 1) or rows_S < S:
+        _refuse("rows", rows, f"int32 [{S}, N] with a unit last stride")
+    status = lib().mla_cache_compact_rows(
         kv_cache_ptrs.data_ptr(), L, dtype_code(cache_dtype), num_blocks, block_size, block_stride,
-        entry_stride, entry_dim, block_table.data_ptr(), _bt_stride(block_table),
-        starts.data_ptr(), rows.data_ptr(), rows.stride(0), rows.shape[1], counts.data_ptr(), S,
-        _ptr(err_word), _stream(stream)))
+        entry_stride, entry_dim, block_table.data_ptr(), tab_s if tab_S > 1 else tab_W,
+        starts.data_ptr(), rows.data_ptr(), rows_s, width, counts.data_ptr(), S, _ptr(err_word),
+        _stream(stream))
+    if status:
+        _check(status)
 
 
 def mla_prefill_attention_workspace(num_tokens: int, num_heads: int, num_kv_heads: int,
@@ -553,27 +563,36 @@ def mla_prefill_attention(q_nope, q_pe, k_nope, k_pe, v, cu_q_lens, cu_kv_lens, 
     cu_q_lens and cu_kv_lens int32 [S + 1]; workspace: a uint8 tensor of
     ``mla_prefill_attention_workspace`` bytes."""
     T, H, N = q_nope.shape
-    K, G, _ = k_nope.shape
+    K, G, kn_N = k_nope.shape
+    qp_T, qp_H, P = q_pe.shape
+    v_K, v_G, V = v.shape
+    qn_t, qn_h, qn_e = q_nope.stride()
+    qp_t, qp_h, qp_e = q_pe.stride()
+    kn_t, kn_h, kn_e = k_nope.stride()
+    v_t, v_h, v_e = v.stride()
+    out_t, out_h, out_e = out.stride()
+    if k_pe.ndim == 2:
+        (kp_K, kp_P), (kp_t, kp_e) = k_pe.shape, k_pe.stride()
+        kp_G, kp_h = G, 0
+    else:
+        (kp_K, kp_G, kp_P), (kp_t, kp_h, kp_e) = k_pe.shape, k_pe.stride()
     qd, kd = q_nope.dtype, k_nope.dtype
-    P = q_pe.shape[-1]
     if q_pe.dtype is not qd or out.dtype is not qd:
         raise ValueError(f"q_pe and out must have q_nope's dtype ({qd}, got {q_pe.dtype}, {out.dtype})")
     if k_pe.dtype is not kd or v.dtype is not kd:
         raise ValueError(f"k_pe and v must have k_nope's dtype ({kd}, got {k_pe.dtype}, {v.dtype})")
-    if q_pe.ndim != 3 or q_pe.shape[0] != T or q_pe.shape[1] != H:
+    if qp_T != T or qp_H != H:
         _refuse("q_pe", q_pe, f"[{T}, {H}, 64]")
-    if k_pe.shape != ((K, P) if k_pe.ndim == 2 else (K, G, P)):
+    if kp_K != K or kp_G != G or kp_P != P:
         _refuse("k_pe", k_pe, f"[{K}, {P}] or [{K}, {G}, {P}]")
-    if k_nope.shape[2] != N:
+    if kn_N != N:
         _refuse("k_nope", k_nope, f"[{K}, {G}, {N}]")
-    if v.ndim != 3 or v.shape[0] != K or v.shape[1] != G:
+    if v_K != K or v_G != G:
         _refuse("v", v, f"[{K}, {G}, 128]")
-    V = v.shape[2]
     if out.shape != (T, H, V):
         _refuse("out", out, f"[{T}, {H}, {V}]")
-    for t in (q_nope, q_pe, k_nope, k_pe, v, out):
-        if t.stride(-1) != 1:
-            raise ValueError("q_nope, q_pe, k_nope, k_pe, v and out must have a unit last stride")
+    if not qn_e == qp_e == kn_e == kp_e == v_e == out_e == 1:
+        raise ValueError("q_nope, q_pe, k_nope, k_pe, v and out must have a unit last stride")
     lse_t = lse_h = 0
     if lse is not None:
         if lse.dtype is not torch.float32 or lse.shape != (T, H):
@@ -589,13 +608,11 @@ def mla_prefill_attention(q_nope, q_pe, k_nope, k_pe, v, cu_q_lens, cu_kv_lens, 
     if not workspace.is_contiguous():
         _refuse("workspace", workspace, "contiguous")
     status = lib().mla_prefill_attention(
-        q_nope.data_ptr(), q_nope.stride(0), q_nope.stride(1), q_pe.data_ptr(), q_pe.stride(0),
-        q_pe.stride(1), dtype_code(qd), T, H, k_nope.data_ptr(), k_nope.stride(0),
-        k_nope.stride(1), k_pe.data_ptr(), k_pe.stride(0), k_pe.stride(1) if k_pe.ndim == 3 else 0,
-        v.data_ptr(), v.stride(0), v.stride(1), dtype_code(kd), K, G, N, P, V,
-        cu_q_lens.data_ptr(), cu_kv_lens.data_ptr(), S, softmax_scale, _ptr(kv_scale),
-        1 if causal else 0, out.data_ptr(), out.stride(0), out.stride(1), _ptr(lse), lse_t, lse_h,
-        workspace.data_ptr(), workspace.nbytes, _ptr(err_word), _stream(stream))
+        q_nope.data_ptr(), qn_t, qn_h, q_pe.data_ptr(), qp_t, qp_h, dtype_code(qd), T, H,
+        k_nope.data_ptr(), kn_t, kn_h, k_pe.data_ptr(), kp_t, kp_h, v.data_ptr(), v_t, v_h,
+        dtype_code(kd), K, G, N, P, V, cu_q_lens.data_ptr(), cu_kv_lens.data_ptr(), S,
+        softmax_scale, _ptr(kv_scale), 1 if causal else 0, out.data_ptr(), out_t, out_h, _ptr(lse),
+        lse_t, lse_h, workspace.data_ptr(), workspace.nbytes, _ptr(err_word), _stream(stream))
     if status:
         _check(status)
 
