@@ -155,3 +155,24 @@ def test_wide_tables_and_lists_streams_and_graphs():
         c.run(stream=s)
     g.replay()
     c.check()
+
+
+def test_offsets_past_32_bits():
+    """A cache of 6 GB whose used blocks are its last ones."""
+    c = Case([3, 100], [[1, 4, 6], [0, 2, 30]], block=64, layers=1).put()
+    blocks, far = c.blocks, 80000
+    big = torch.empty((far, 64, 576), dtype=torch.int16, device="cuda")
+    big[far - blocks:].copy_(c.cache[0])
+    c.ptrs = torch.tensor([big.data_ptr()], dtype=torch.int64, device="cuda")
+    c.d[0] += far - blocks
+    c.blocks = far
+    c.run()
+    c.cache[0].copy_(big[far - blocks:])
+    c.check()
+
+
+def test_device_refusals():
+    c = Case([3], [[1, 4]]).put()
+    c.d[2] = c.d[2].cpu()
+    with pytest.raises(ops.MlaError, match="rows must be device memory"):
+        c.run()

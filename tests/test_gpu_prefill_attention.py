@@ -384,3 +384,114 @@ def test_long_items_between_others():
     mag = 2.0 ** -8 * (2 + 2.0 ** -6) * 4.5  # |v| stays below 4.5 in all but a few of 10^6 values
     assert c.dv.abs().max() < 6 and (first.double() - ref).abs().max() < mag * 6 / 4.5
     assert (first.double() - ref).norm() < 2.0 ** -8 * ref.norm()
+
+
+@pytest.mark.parametrize("kind,heads,kv_heads", [((BF, E4), 6, 2), ((HF, E5), 5, 1), ((BF, E4), 40, 1), ((HF, HF), 6, 2)], ids=str)
+def test_head_layouts_of_other_types(kind, heads, kv_heads):
+    Call([33, 1, 60], [33, 200, 170], heads, kv_heads, *kind).put().run().check()
+
+
+@pytest.mark.parametrize("seqs,heads,kv_heads,kv", [
+    (150, 1, 1, 512), (150, 1, 1, 513), (151, 1, 1, 450), (4, 32, 32, 512), (4, 32, 32, 520), (1, 256, 1, 512),
+    (1, 256, 2, 513)], ids=str)
+def test_borders_of_whole_items(seqs, heads, kv_heads, kv):
+    """Around the sizes from which items are cut: 512 key rows in all, an item per SM."""
+    lens = [kv // seqs] * (seqs - 1) + [kv - kv // seqs * (seqs - 1)]
+    Call([min(2, n) for n in lens], lens, heads, kv_heads, BF).put().run().check()
+
+
+@pytest.mark.parametrize("kind", [(BF, BF), (HF, HF), (BF, E4)], ids=str)
+@pytest.mark.parametrize("lens", [([300], [300]), ([300, 20], [1300, 400])], ids=str)
+def test_rows_of_out_on_32_bytes(kind, lens):
+    """out without gaps, which is written in wider stores; and the same bits with gaps."""
+    c = Call(*lens, heads=4, dtype=kind[0], kv=kind[1]).put().run()
+    first = c.got()
+    T, H = c.out.shape[:2]
+    out = torch.full((T, H, 128), 7.0, dtype=kind[0], device="cuda")
+    ops.mla_prefill_attention(c.dq[:, :, :128], c.dq[:, :, 128:], c.dk, c.dp, c.dv, c.dcq, c.dck, out, c.ws,
+                              softmax_scale=c.scale, kv_scale=c.ds)
+    torch.cuda.synchronize()
+    assert np.array_equal(R.f64(out.cpu()), first[0])
+
+
+@pytest.mark.parametrize("kind", [(BF, BF), (HF, HF), (BF, E4)], ids=str)
+@pytest.mark.parametrize("scale", [0.0, -R.SCALE, 1e-30])
+def test_scales(kind, scale):
+    Call([70, 200], [70, 330], heads=2, dtype=kind[0], kv=kind[1], scale=scale).put().run().check()
+
+
+@pytest.mark.parametrize("which", ["heads", "tokens"])
+@pytest.mark.parametrize("kind", [(BF, BF), (BF, E4)], ids=str)
+def test_broadcast_queries(kind, which):
+    """Queries whose heads, or tokens, are one row."""
+    c = Call([70, 40], [70, 300], heads=4, dtype=kind[0], kv=kind[1])
+    c.q = (c.q[:, :1].expand(-1, 4, -1) if which == "heads" else c.q[:1].expand(110, -1, -1)).clone()
+    c.put()
+    c.dq = c.dq[:, :1].expand(-1, 4, -1) if which == "heads" else c.dq[:1].expand(110, -1, -1)
+    c.run().check()
+
+
+def test_offsets_past_32_bits():
+    """Rows 16 MiB apart in one buffer of 5 GB: queries, keys, values and results side by side."""
+    c = Call([300], [310], heads=1).put()
+    step, n = 1 << 23, 310
+    big = torch.empty(n * step, dtype=BF, device="cuda")
+    at = lambda off, w, rows: big.as_strided((rows, 1, w), (step, 192, 1), off)
+    q, key, v, out = at(0, 192, 300), at(192, 192, n), at(384, 128, n), at(512, 128, 300)
+    q.copy_(c.dq)
+    key[:, :, :128].copy_(c.dk)
+    key[:, :, 128:].copy_(c.dp)
+    v.copy_(c.dv)
+    ops.mla_prefill_attention(q[:, :, :128], q[:, :, 128:], key[:, :, :128], key[:, :, 128:], v, c.dcq, c.dck, out,
+                              c.ws, softmax_scale=c.scale, lse=c.lse, err_word=c.err)
+    c.out.copy_(out)
+    c.check()
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with its own workspace, repeat what they give alone."""
+    calls = [Call([700, 30], [900, 1500], 8, 2, seed=1).put(), Call([1, 300], [2000, 300], 4, 4, BF, E4, seed=2).put()]
+    alone = [c.run().got()[0] for c in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    for c in calls:
+        c.out.fill_(3.0)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, s in zip(calls, streams):
+            c.run(stream=s)
+    for c, want in zip(calls, alone):
+        assert np.array_equal(c.got()[0], want)
+
+
+def test_device_refusals():
+    c = Call([5], [5]).put()
+    ws = c.ws
+    c.ws = ws[:-16]
+    with pytest.raises(ops.MlaError, match="workspace_bytes must be >="):
+        c.run()
+    c.ws = ws
+    c.dv = c.dv.cpu()
+    with pytest.raises(ops.MlaError, match="v must be device memory"):
+        c.run()
+
+
+@pytest.mark.parametrize("kind,stages", [((BF, BF), 6), ((HF, HF), 6), ((BF, E4), 4)], ids=str)
+def test_waits_that_run_out_return_and_report(kind, stages):
+    """With a 1 ms limit and a stage of the first CTA that never fills (a testing hook), its waits
+    run out: the call returns and says so, the other CTAs' heads are as ever, and the next call is
+    exact.  No fault is involved: only bounded waits that give up."""
+    c = Call([2000], [2000], 8, dtype=kind[0], kv=kind[1]).put()
+    good = c.run().got()[0]
+    for stage in range(1, stages + 1):
+        c.out.fill_(3.0)
+        torch.cuda.synchronize()
+        try:
+            ops.mla_test_attention_timeout(1_000_000, stage)
+            out, _, e = c.run().got()
+        finally:
+            ops.mla_test_attention_timeout()
+        assert e == ops.MLA_ERRBIT_TIMEOUT
+        assert np.array_equal(out[:, 2:], good[:, 2:]) and not np.array_equal(out[:, 0], good[:, 0])
+        c.err.zero_()
+        out, _, e = c.run().got()
+        assert e == 0 and np.array_equal(out, good)

@@ -229,3 +229,53 @@ def test_streams_and_graphs_repeat_to_the_bit():
     c.run(stream=s)
     s.synchronize()
     assert np.array_equal(first[0], c.got()[0])
+
+
+def test_masks_past_32_bits():
+    """Mask rows 2 GB apart."""
+    n, kv = [3], [70]
+    pg = R.paged(kv, 0, 16)
+    c = Call(pg, R.queries(3, 16), cu_of(n), kv, P.tree_masks(n, 4))
+    big = torch.empty(2 * (1 << 29) + 8, dtype=torch.int32, device="cuda")
+    far = big.as_strided(tuple(c.mask.shape), (1 << 29, 1))
+    far.copy_(c.mask)
+    c.mask = far
+    c.run().check()
+
+
+def test_device_refusals():
+    n, kv = [3], [70]
+    c = Call(R.paged(kv, 0, 16), R.queries(3, 16), cu_of(n), kv, P.tree_masks(n, 4))
+    ws = c.ws
+    c.ws = ws[:-16]
+    with pytest.raises(ops.MlaError, match="workspace_bytes must be >="):
+        c.run()
+    c.ws = ws
+    c.mask = c.mask.cpu()
+    with pytest.raises(ops.MlaError, match="tree_mask must be device memory"):
+        c.run()
+
+
+@pytest.mark.parametrize("stage", [1, 2])
+@pytest.mark.parametrize("fmt,heads", [(0, 16), (1, 16), (0, 128)])
+def test_waits_that_run_out_return_and_report(fmt, heads, stage):
+    """With a 1 ms limit and a pipeline stage of the first CTA that never fills (a testing hook),
+    its waits run out: the call returns and says so, the other CTAs' sequences are as ever, and
+    the next call is exact.  No fault is involved: only bounded waits that give up."""
+    n = [2] * 200
+    kv = [1500] + [64 * (i % 5 + 1) for i in range(199)]
+    pg = R.paged(kv, fmt, 64, seed=19)
+    c = Call(pg, R.queries(400, heads), cu_of(n), kv, P.tree_masks(n, 4)).run()
+    good = c.got()[0]
+    c.out.fill_(3.0)
+    torch.cuda.synchronize()
+    try:
+        ops.mla_test_attention_timeout(1_000_000, stage)
+        out, _, e = c.run().got()
+    finally:
+        ops.mla_test_attention_timeout()
+    assert e == ops.MLA_ERRBIT_TIMEOUT
+    assert np.array_equal(out[80:], good[80:]) and not np.array_equal(out[:2], good[:2])
+    c.err.zero_()
+    out, _, e = c.run().got()
+    assert e == 0 and np.array_equal(out, good)
