@@ -37,9 +37,10 @@
 // rescaling O only when a maximum has grown by more than 2^kGrow) and write the output; two per
 // tile issue the products, scores and outputs; one plans the CTA's items, describes them to the others in shared
 // memory and loads Q, K and V.  V rows that not every row of an item sees are looked after by
-// the weights' warps before their products: those behind the sequence are zeroed (they may hold
-// anything), those with a NaN or an infinity too, and noted, so that the sums of the rows that
-// see them become NaN.  With fp8, three more warps widen the codes and look after V on the way.
+// the outputs' warps while the weights are computed (300 tokens 13.2 us and 16 ragged prompts 159;
+// by the weights' warps, before these, 14.7 and 180): those behind the sequence are zeroed (they may
+// hold anything), those with a NaN or an infinity too, and noted, so that the sums of the rows
+// that see them become NaN.  With fp8, three more warps widen the codes and look after V on the way.
 // Each role's code is kept small: instructions are fetched cold in every
 // launch, at about 40 cycles each where nothing else covers it.
 //
@@ -104,8 +105,8 @@ struct Lay {
   static constexpr int v = k + kStages * 3 * kRun;        // [kStages][2 runs]
   static constexpr int raw = v + kStages * 2 * kRun;      // [kRawStages][128 + 64 columns of K, V]
   static constexpr int items = raw + (kF8 ? kRawStages * (kRawK + kRawV) : 0);  // Item [kItems]
-  static constexpr int flags = items + kItems * 64;       // uint8 [4 units][16]: keys with bad V rows,
-                                                          // four to a byte
+  static constexpr int flags = items + kItems * 64;       // [4 units][16 bytes]: keys with bad V rows, a bit
+                                                          // each; fp8: four to a byte
   static constexpr int bars = flags + 64;
   // Barriers: of the stages; of units looked after, in turn; of the query tiles (scores, weights
   // and outputs two each, in turn: the weights' warps may be one unit behind the scores and one
@@ -113,7 +114,7 @@ struct Lay {
   static constexpr int kKFull = 0, kVFull = kKFull + kStages, kKEmpty = kVFull + kStages,
                        kVEmpty = kKEmpty + kStages, kRawFull = kVEmpty + kStages,
                        kRawEmpty = kRawFull + kRawStages, kClean = kRawEmpty + kRawStages,
-                       kHere = kClean + 4, kQFull = kHere + 2, kQReady = kQFull + 2,
+                       kQFull = kClean + 4, kQReady = kQFull + 2,
                        kQEmpty = kQReady + 2, kSFull = kQEmpty + 2, kPFull = kSFull + 4,
                        kPvDone = kPFull + 4, kOFree = kPvDone + 4, kItemFull = kOFree + 2,
                        kItemFree = kItemFull + kItems, kBars = kItemFree + kItems;
@@ -666,6 +667,41 @@ __device__ __forceinline__ void score_role(float scale, uint32_t smem, uint32_t 
     }
   }
 }
+// V of a unit (of its keys): rows from `most` on are zeroed, those from `least` on with a NaN or an
+// infinity too, and noted in flags, a bit each.  By one warp, a lane a row at a time.
+template <int F>
+__device__ __noinline__ void look_after(uint32_t v, uint32_t flags, int least, int most) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int k = 0; k < kKeys; k += 32) {
+    uint32_t bad = 0;
+    if (k + 32 > least) {
+      const int key = k + lane;
+      const uint32_t at = v + key * 128;
+      uint32_t top = 0;
+#pragma unroll 1
+      for (int c = 0; c < 8; c += 2) {  // every column of the row, in any order
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 w = lds16(at + (i & 1) * kRun + (((c + (i >> 1)) ^ (lane & 7)) << 4));
+          top = umax16x2(top, umax16x2(umax16x2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                                       umax16x2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu)));
+        }
+      }
+      const bool sp = max(top & 0xFFFFu, top >> 16) >= (F == kBF16 ? 0x7F80u : 0x7C00u);
+      bad = __ballot_sync(0xFFFFFFFFu, sp && key >= least && key < most);
+      if (key >= most || bad >> lane & 1)
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 16) {
+          sts16(at + c, make_uint4(0, 0, 0, 0));
+          sts16(at + kRun + c, make_uint4(0, 0, 0, 0));
+        }
+    }
+    if (lane == 0) sts_u32(flags + k / 8, bad);
+  }
+  tc::fence_smem_async();
+  __syncwarp();
+}
 template <int F, int KF>
 __device__ __forceinline__ void output_role(uint32_t smem, uint32_t tmem, const Waiter& waiter, int tile,
                                             int lane) {
@@ -673,25 +709,27 @@ __device__ __forceinline__ void output_role(uint32_t smem, uint32_t tmem, const 
   const uint32_t bars = smem + L::bars;
   auto wait = [&](int bar, uint32_t phase) { return spin(waiter, bars + 8 * bar, phase); };
   const bool one = tc::elect();
-  uint32_t n = 0, opened = 0, cleaned = 0;  // units, items of this tile; units looked after
+  uint32_t n = 0, g = 0, opened = 0, cleaned = 0;  // units of this tile, and of all; items; units looked after
   Stage<L::kStages> st;
   Items<KF> items{smem, 0};
   Item it;
 #pragma unroll 1
   while (items.get(waiter, it)) {
     const int e = it.end[tile], kb = it.kb, ke = it.ke, ragged = it.ragged();
-    const int mine = tile ? max(ragged, it.end[0]) : ragged;  // this tile looks after V from here on
+    const int mine = tile ? max(ragged, it.end[0]) : ragged;  // this warp looks after V from here on
     const uint32_t c0 = cleaned - ragged;
     cleaned += it.cleaned();
     // the sums of the item before are read
     if (kb < e && opened++ > 0 && !wait(L::kOFree + tile, opened)) return;
 #pragma unroll 1
-    for (int kt = kb; kt < ke; ++kt) {
+    for (int kt = kb; kt < ke; ++kt, ++g) {
       if (!wait(L::kVFull + st.at, st.phase)) return;
       if (kt < e) {
-        if (!L::kF8 && kt >= ragged) {
-          if (kt >= mine && lane == 0) mbar_arrive(bars + 8 * (L::kHere + tile));
-          __syncwarp();
+        if (!L::kF8 && kt >= mine) {
+          look_after<F>(smem + L::v + st.at * 2 * kRun, smem + L::flags + (g & 3) * 16, it.least - kt * kKeys,
+                        it.most - kt * kKeys);
+          if (lane == 0) mbar_arrive(bars + 8 * (L::kClean + ((c0 + kt) & 3)));
+        } else if (!L::kF8 && kt >= ragged) {
           if (!wait(L::kClean + ((c0 + kt) & 3), (c0 + kt) >> 2)) return;
         }
         if (!wait(L::kPFull + 2 * tile + (n & 1), n >> 1)) return;
@@ -775,41 +813,11 @@ __device__ __noinline__ float narrow_row(uint32_t at, int row) {
 struct Part {
   uint32_t smem, s_at, o_at;  // tensor memory: this warp's scores and sums
   uint32_t n, g, cleaned;     // units of this tile, of all, and looked after, before the part
-  uint32_t mended;            // and looked after by this tile's warps
-  int stage;                  // of V of the part's first unit
   int tile, count, from;      // key tiles, and the first that not every row sees whole
-  int mend;                   // this tile looks after V from this key tile on
-  int least, most;            // keys that the item's first and last row see, from the first tile on
-  int seen;                   // and this thread's
+  int seen;                   // keys that this thread's row sees, from the first tile on
   bool live;                  // the warp has rows
   float c;                    // weights: exp2(c score - reference)
 };
-// This warp's 16 keys of V of a unit: rows from key `most` on (of these) are zeroed, those from
-// `least` on with a NaN or an infinity too; returns which.
-template <int F>
-__device__ __noinline__ uint32_t look_after(uint32_t v, int least, int most) {
-  const int lane = threadIdx.x & 31, col = lane & 7;
-  uint32_t bad = 0;  // four keys to a byte
-#pragma unroll 2
-  for (int n = 0; n < 4; ++n) {
-    const int key = 4 * n + (lane >> 3);
-    const uint32_t at = v + key * 128 + col * 16;  // every column of the row, in any order
-    const bool sp = any_special<F>(lds16(at)) | any_special<F>(lds16(at + kRun));
-    const uint32_t votes = __ballot_sync(0xFFFFFFFFu, sp && key >= least && key < most);
-    if (key >= most || votes & (0xFFu << (lane & 24))) {
-      sts16(at, make_uint4(0, 0, 0, 0));
-      sts16(at + kRun, make_uint4(0, 0, 0, 0));
-    }
-    if (votes)
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (votes & (0xFFu << (8 * k))) bad |= 1u << (8 * n + k);
-  }
-  tc::fence_smem_async();
-  __syncwarp();
-  return bad;
-}
-
 // The weights of an item's units (a function of its own, so that its loop has the registers to
 // itself): the row's reference, the sum of its weights, and how much more they are as they are
 // rounded.  (The last is counted in the units that not every row sees whole: a row of few keys,
@@ -829,19 +837,7 @@ __device__ __noinline__ bool unit_weights(Part s, const Waiter waiter, float& mu
   for (int kt = 0; kt < s.count; ++kt, ++s.n) {
     if (!wait(L::kSFull + 2 * s.tile + (s.n & 1), s.n >> 1)) return false;
     tc::fence_after_sync();
-    const uint32_t bars = s.smem + L::bars, nc = s.cleaned + kt - s.from;
-    const uint32_t flags = s.smem + L::flags + ((s.g + kt) & 3) * 16;
-    if (!L::kF8 && __builtin_expect(kt >= s.mend, 0)) {
-      const int w4 = (threadIdx.x >> 5) & 3;
-      if (!wait(L::kHere + s.tile, s.mended++)) return false;
-      const int stage = (s.stage + kt) % L::kStages;
-      const uint32_t bad = look_after<F>(s.smem + L::v + stage * 2 * kRun + w4 * 2048,
-                                         s.least - kt * kKeys - w4 * 16, s.most - kt * kKeys - w4 * 16);
-      if (lane == 0) {
-        sts_u32(flags + w4 * 4, bad);
-        mbar_arrive(bars + 8 * (L::kClean + (nc & 3)));
-      }
-    }
+    const uint32_t bars = s.smem + L::bars;
     if (!s.live) {
       tc::fence_before_sync();
       __syncwarp();
@@ -852,13 +848,7 @@ __device__ __noinline__ bool unit_weights(Part s, const Waiter waiter, float& mu
     float x[kKeys];
     tc::ld_32x64(s_at, reinterpret_cast<uint32_t*>(x));
     if (__builtin_expect(kt >= s.from, 0)) {
-      if (!wait(L::kClean + (nc & 3), nc >> 2)) return false;
       const int lim = s.seen - kt * kKeys;
-      const uint4 f = lds16(flags);
-      if (__builtin_expect((f.x | f.y | f.z | f.w) != 0, 0))
-#pragma unroll 1
-        for (int k = 0; k < kKeys; ++k)
-          if (k < lim && lds_u8(flags + (k >> 2)) >> (k & 3) & 1) l = NAN;
 #pragma unroll
       for (int j = 0; j < kKeys; ++j) x[j] = j < lim ? x[j] : -INFINITY;
     }
@@ -916,6 +906,21 @@ __device__ __noinline__ bool unit_weights(Part s, const Waiter waiter, float& mu
     tc::fence_before_sync();
     __syncwarp();
     if (lane == 0) mbar_arrive(bars + 8 * (L::kPFull + 2 * s.tile + (s.n & 1)));
+    if (__builtin_expect(kt >= s.from, 0)) {
+      const uint32_t nc = s.cleaned + kt - s.from, flags = s.smem + L::flags + ((s.g + kt) & 3) * 16;
+      if (!wait(L::kClean + (nc & 3), nc >> 2)) return false;
+      const int lim = s.seen - kt * kKeys;
+      const uint4 f = lds16(flags);
+      if constexpr (L::kF8) {
+        if (__builtin_expect((f.x | f.y | f.z | f.w) != 0, 0))
+#pragma unroll 1
+          for (int k = 0; k < kKeys; ++k)
+            if (k < lim && lds_u8(flags + (k >> 2)) >> (k & 3) & 1) l = NAN;
+      } else if (__builtin_expect((f.x | f.y) != 0, 0)) {
+        const uint64_t bits = (uint64_t)f.y << 32 | f.x;
+        if (lim > 0 && bits << (kKeys - min(lim, kKeys))) l = NAN;
+      }
+    }
   }
   mu_out = mu;
   l_out = l;
@@ -939,7 +944,7 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, bool boxes, u
   const uint32_t s_at = tmem + tile * 2 * kKeys + ((uint32_t)(w4 * 32) << 16);
   const uint32_t o_at = tmem + kO + tile * kV + ((uint32_t)(w4 * 32) << 16);
   const int r = w4 * 32 + lane;
-  uint32_t n = 0, g = 0, cleaned = 0, mended = 0, opened = 0;
+  uint32_t n = 0, g = 0, cleaned = 0, opened = 0;
   const float ks = L::kF8 ? __ldg(a.kv_scale) : 1.0f;
   Items<KF> items{smem, 0};
   Item it;
@@ -957,7 +962,6 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, bool boxes, u
     const bool live = w4 * 32 < mine, ok = r < mine;
     const uint32_t row = it.row0 + tile * kM + r;
     const int seen = ok ? seen_of(a, it.base, it.m, row) : 0, shift = it.kb * kKeys;
-    const int mend = max(it.ragged(), tile ? it.end[0] : 0);
     float c = fabsf(a.softmax_scale * ks) * kLog2e, mu, l, d;
     if constexpr (F != QF) {
       if (count > 0) {
@@ -969,12 +973,10 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, bool boxes, u
       }
     }
     c = c < 1e-37f ? 1e-37f : c;  // (a masked score times it is -infinity)
-    if (!unit_weights<F, KF>(Part{smem, s_at, o_at, n, g, cleaned, mended, (int)(g % L::kStages), tile, count,
-                              it.ragged() - it.kb, mend - it.kb, it.least - shift, it.most - shift,
-                              seen - shift, live, c},
+    if (!unit_weights<F, KF>(Part{smem, s_at, o_at, n, g, cleaned, tile, count, it.ragged() - it.kb, seen - shift,
+                              live, c},
                          waiter, mu, l, d))
       return;
-    mended += max(it.end[tile] - mend, 0);
     n += count;
     g += it.ke - it.kb;
     cleaned += it.cleaned();
@@ -1077,7 +1079,6 @@ __global__ void __launch_bounds__(warps_of(KF) * 32, 1)
       int n = of(L::kKEmpty, 2 * L::kStages) ? 2 : 1;
       if (L::kF8 && (of(L::kKFull, 2 * L::kStages) || of(L::kRawEmpty, L::kRawStages) || of(L::kClean, 4)))
         n = kWideWarps;
-      if (!L::kF8 && of(L::kClean, 4)) n = 4;
       if (of(L::kQFull, 2) && maps.q_tokens == 0) n = kM;
       if (of(L::kPFull, 4) || of(L::kOFree, 2) || of(L::kQReady, 2)) n = 4;
       if (of(L::kItemFree, kItems)) n = warps_of(KF) - 1;
