@@ -847,8 +847,9 @@ __device__ __noinline__ bool unit_weights(Part s, const Waiter waiter, float& mu
     const uint32_t s_at = s.s_at + (s.n & 1) * kKeys;
     float x[kKeys];
     tc::ld_32x64(s_at, reinterpret_cast<uint32_t*>(x));
-    if (__builtin_expect(kt >= s.from, 0)) {
-      const int lim = s.seen - kt * kKeys;
+    const int lim = s.seen - kt * kKeys;
+    const bool cut = kt >= s.from && __any_sync(0xFFFFFFFFu, lim < kKeys);
+    if (__builtin_expect(cut, 0)) {
 #pragma unroll
       for (int j = 0; j < kKeys; ++j) x[j] = j < lim ? x[j] : -INFINITY;
     }
@@ -893,7 +894,7 @@ __device__ __noinline__ bool unit_weights(Part s, const Waiter waiter, float& mu
     tc::st_32x32(s_at, pk);
     const float2 s2 = unf2(add2(sum[0], sum[1]));
     l += s2.x + s2.y;
-    if (__builtin_expect(kt >= s.from, 0)) {
+    if (__builtin_expect(cut, 0)) {
       float r0 = 0.0f, r1 = 0.0f;
 #pragma unroll
       for (int j = 0; j < kKeys / 2; ++j) {
@@ -909,7 +910,6 @@ __device__ __noinline__ bool unit_weights(Part s, const Waiter waiter, float& mu
     if (__builtin_expect(kt >= s.from, 0)) {
       const uint32_t nc = s.cleaned + kt - s.from, flags = s.smem + L::flags + ((s.g + kt) & 3) * 16;
       if (!wait(L::kClean + (nc & 3), nc >> 2)) return false;
-      const int lim = s.seen - kt * kKeys;
       const uint4 f = lds16(flags);
       if constexpr (L::kF8) {
         if (__builtin_expect((f.x | f.y | f.z | f.w) != 0, 0))
