@@ -434,23 +434,23 @@ __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& 
     if (!first) {
       if (it.ke < 0) break;
       const int h = it.head;
-      if (maps.q_tokens != 0) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (it.end[i] <= it.kb) continue;
-          if (filled[i] > 0 && !waited(L::kQEmpty + i, filled[i] - 1)) return L::kF8 ? g : 2 * g;
-          ++filled[i];
-          if (lane == 0) {
-            const uint32_t qf = bars + 8 * (L::kQFull + i), dst = smem + L::q + i * kQTile;
-            const int t = it.t0 + ((int)(it.row0 / (uint32_t)kM) + i) * maps.q_tokens;
-            mbar_arrive_expect_tx(qf, kQTile);
-            tc::tma_load3(dst, &maps.qn, 0, h * a.group, t, qf, policy);
-            tc::tma_load3(dst + kM * 128, &maps.qn, 64, h * a.group, t, qf, policy);
-            tc::tma_load3(dst + 2 * kM * 128, &maps.qp, 0, h * a.group, t, qf, policy);
-          }
-          __syncwarp();
+      // the queries of a tile; they come behind the item's first keys, so that the first scores
+      // wait for no more than they need
+      auto queries = [&](int i) {
+        if (maps.q_tokens == 0 || it.end[i] <= it.kb) return true;
+        if (filled[i] > 0 && !waited(L::kQEmpty + i, filled[i] - 1)) return false;
+        ++filled[i];
+        if (lane == 0) {
+          const uint32_t qf = bars + 8 * (L::kQFull + i), dst = smem + L::q + i * kQTile;
+          const int t = it.t0 + ((int)(it.row0 / (uint32_t)kM) + i) * maps.q_tokens;
+          mbar_arrive_expect_tx(qf, kQTile);
+          tc::tma_load3(dst, &maps.qn, 0, h * a.group, t, qf, policy);
+          tc::tma_load3(dst + kM * 128, &maps.qn, 64, h * a.group, t, qf, policy);
+          tc::tma_load3(dst + 2 * kM * 128, &maps.qp, 0, h * a.group, t, qf, policy);
         }
-      }
+        __syncwarp();
+        return true;
+      };
 #pragma unroll 1
       for (int kt = it.kb; kt < it.ke; ++kt, ++g, st.step()) {
         const int row = it.k0 + kt * kKeys;
@@ -465,6 +465,7 @@ __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& 
             tc::tma_load3(k + L::kRawK, &maps.v, h * maps.v_x, row, h * maps.v_z, rf, policy);
           }
           __syncwarp();
+          if (kt == it.kb && !(queries(0) && queries(1))) return g + 1;
           continue;
         }
         const uint32_t kf = bars + 8 * (L::kKFull + st.at), vf = bars + 8 * (L::kVFull + st.at);
@@ -477,6 +478,7 @@ __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& 
           tc::tma_load3(k + 2 * kRun, &maps.kp, h * maps.kp_x, row, h * maps.kp_z, kf, policy);
         }
         __syncwarp();
+        if (kt == it.kb && !queries(0)) return 2 * g + 1;
         if (g >= L::kStages && !waited(L::kVEmpty + st.at, st.phase ^ 1)) return 2 * g + 1;
         if (lane == 0) {
           mbar_arrive_expect_tx(vf, 2 * kRun);
@@ -484,6 +486,7 @@ __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& 
           tc::tma_load3(v + kRun, &maps.v, h * maps.v_x + 64, row, h * maps.v_z, vf, policy);
         }
         __syncwarp();
+        if (kt == it.kb && !queries(1)) return 2 * g + 2;
       }
       if (it.ke < it.tiles && lane == 0) {  // the run's last item
         const I u0 = plan.begin + plan.count - it.ke;  // the unit of its key tile 0
@@ -672,23 +675,26 @@ __device__ __forceinline__ void score_role(float scale, uint32_t smem, uint32_t 
 template <int F>
 __device__ __noinline__ void look_after(uint32_t v, uint32_t flags, int least, int most) {
   const int lane = threadIdx.x & 31;
+  bool written = false;
 #pragma unroll 1
   for (int k = 0; k < kKeys; k += 32) {
     uint32_t bad = 0;
     if (k + 32 > least) {
       const int key = k + lane;
       const uint32_t at = v + key * 128;
-      uint32_t top = 0;
+      uint32_t top[4] = {0, 0, 0, 0};
 #pragma unroll 1
-      for (int c = 0; c < 8; c += 2) {  // every column of the row, in any order
+      for (int c = 0; c < 8; c += 4) {  // every column of the row, in any order
+        uint4 w[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 w = lds16(at + (i & 1) * kRun + (((c + (i >> 1)) ^ (lane & 7)) << 4));
-          top = umax16x2(top, umax16x2(umax16x2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
-                                       umax16x2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu)));
-        }
+        for (int i = 0; i < 8; ++i) w[i] = lds16(at + (i & 1) * kRun + (((c + (i >> 1)) ^ (lane & 7)) << 4));
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          top[i & 3] = umax16x2(top[i & 3], umax16x2(umax16x2(w[i].x & 0x7FFF7FFFu, w[i].y & 0x7FFF7FFFu),
+                                                     umax16x2(w[i].z & 0x7FFF7FFFu, w[i].w & 0x7FFF7FFFu)));
       }
-      const bool sp = max(top & 0xFFFFu, top >> 16) >= (F == kBF16 ? 0x7F80u : 0x7C00u);
+      const uint32_t all = umax16x2(umax16x2(top[0], top[1]), umax16x2(top[2], top[3]));
+      const bool sp = max(all & 0xFFFFu, all >> 16) >= (F == kBF16 ? 0x7F80u : 0x7C00u);
       bad = __ballot_sync(0xFFFFFFFFu, sp && key >= least && key < most);
       if (key >= most || bad >> lane & 1)
 #pragma unroll 1
@@ -696,10 +702,11 @@ __device__ __noinline__ void look_after(uint32_t v, uint32_t flags, int least, i
           sts16(at + c, make_uint4(0, 0, 0, 0));
           sts16(at + kRun + c, make_uint4(0, 0, 0, 0));
         }
+      written |= bad != 0 || k + 32 > most;
     }
     if (lane == 0) sts_u32(flags + k / 8, bad);
   }
-  tc::fence_smem_async();
+  if (written) tc::fence_smem_async();  // (takes as long as looking)
   __syncwarp();
 }
 template <int F, int KF>
@@ -982,52 +989,51 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, bool boxes, u
     cleaned += it.cleaned();
     queries();
     // ---- the end of this CTA's part of the item
+    // (what needs no sums, while the last of them are added up)
+    const bool whole = it.kb == 0 && it.ke == it.tiles;
+    const uint32_t dt = a.by_group(row);
+    const int64_t t = it.t0 + (int)dt;
+    const int64_t h = (int64_t)it.head * a.group + (int)(row - dt * a.group);
+    const int64_t slot = (2 * (int64_t)blockIdx.x + (it.kb == 0 ? 1 : 0)) * srows;
+    const int at = tile * kM + r;
+    if (ok && !whole) {
+      ws.m[slot + at] = mu;
+      ws.l[slot + at] = l;
+      ws.d[slot + at] = d;
+    } else if (ok && a.lse) {
+      a.lse[t * a.lse_ts + h * a.lse_hs] = l == 0.0f ? -INFINITY : (mu + __log2f(l)) * kLn2;
+    }
+    const float inv = l == 0.0f ? 0.0f : __fdividef(ks, l + d);
+    // where 32 dims of the row go, and how far the next lie
+    uint8_t* to = whole ? a.out + t * a.out_ts + h * a.out_hs
+                        : reinterpret_cast<uint8_t*>(ws.o + slot * kV + at * 4);  // [dims / 4][rows][4]
     if (count > 0) {
       if (!__all_sync(0xFFFFFFFFu, waiter(bars + 8 * (L::kPvDone + 2 * tile + ((n - 1) & 1)), ((n - 1) >> 1) & 1))) return;
       tc::fence_after_sync();
     }
-    if (live) {
-      const bool whole = it.kb == 0 && it.ke == it.tiles;
-      const uint32_t dt = a.by_group(row);
-      const int64_t t = it.t0 + (int)dt;
-      const int64_t h = (int64_t)it.head * a.group + (int)(row - dt * a.group);
-      const int64_t slot = (2 * (int64_t)blockIdx.x + (it.kb == 0 ? 1 : 0)) * srows;
-      const int at = tile * kM + r;
-      if (ok && !whole) {
-        ws.m[slot + at] = mu;
-        ws.l[slot + at] = l;
-        ws.d[slot + at] = d;
-      } else if (ok && a.lse) {
-        a.lse[t * a.lse_ts + h * a.lse_hs] = l == 0.0f ? -INFINITY : (mu + __log2f(l)) * kLn2;
-      }
-      const float inv = l == 0.0f ? 0.0f : __fdividef(ks, l + d);
-      // where 32 dims of the row go, and how far the next lie
-      uint8_t* to = whole ? a.out + t * a.out_ts + h * a.out_hs
-                          : reinterpret_cast<uint8_t*>(ws.o + slot * kV + at * 4);  // [dims / 4][rows][4]
-      if (count > 0) {
+    if (count > 0 && live) {
 #pragma unroll 1
-        for (int k = 0; k < kV; k += 32) {
-          uint32_t y[32];
-          tc::ld_32x32(o_at + k, y);
-          if (ok && whole) {
-            uint32_t z[16];
+      for (int k = 0; k < kV; k += 32) {
+        uint32_t y[32];
+        tc::ld_32x32(o_at + k, y);
+        if (ok && whole) {
+          uint32_t z[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              z[j] = pack16x2<QF>(__uint_as_float(y[2 * j]) * inv, __uint_as_float(y[2 * j + 1]) * inv);
-            if (a.out_32) {
-              st32(to, z);
-              st32(to + 32, z + 8);
-            } else {
+          for (int j = 0; j < 16; ++j)
+            z[j] = pack16x2<QF>(__uint_as_float(y[2 * j]) * inv, __uint_as_float(y[2 * j + 1]) * inv);
+          if (a.out_32) {
+            st32(to, z);
+            st32(to + 32, z + 8);
+          } else {
 #pragma unroll
-              for (int j = 0; j < 16; j += 4) st16(to + 4 * j, make_uint4(z[j], z[j + 1], z[j + 2], z[j + 3]));
-            }
-            to += 64;
-          } else if (ok) {
+            for (int j = 0; j < 16; j += 4) st16(to + 4 * j, make_uint4(z[j], z[j + 1], z[j + 2], z[j + 3]));
+          }
+          to += 64;
+        } else if (ok) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              st16(to, make_uint4(y[j], y[j + 1], y[j + 2], y[j + 3]));
-              to += (int64_t)srows * 16;
-            }
+          for (int j = 0; j < 32; j += 4) {
+            st16(to, make_uint4(y[j], y[j + 1], y[j + 2], y[j + 3]));
+            to += (int64_t)srows * 16;
           }
         }
       }
