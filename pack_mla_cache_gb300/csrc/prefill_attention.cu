@@ -67,6 +67,7 @@ constexpr int kScoreWarp = 8, kOutWarp = 10, kLoadWarp = 12;
 constexpr int kWideWarp = 13, kWideWarps = 3;  // (fp8 only)
 __host__ __device__ constexpr int warps_of(int kf) { return is16(kf) ? 13 : kWideWarp + kWideWarps; }
 constexpr int kItems = 4;            // item descriptions in shared memory
+constexpr int kLooks = 8;            // notes of units whose V was looked after
 constexpr int kMaxCtas = 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -105,16 +106,16 @@ struct Lay {
   static constexpr int v = k + kStages * 3 * kRun;        // [kStages][2 runs]
   static constexpr int raw = v + kStages * 2 * kRun;      // [kRawStages][128 + 64 columns of K, V]
   static constexpr int items = raw + (kF8 ? kRawStages * (kRawK + kRawV) : 0);  // Item [kItems]
-  static constexpr int flags = items + kItems * 64;       // [4 units][16 bytes]: keys with bad V rows, a bit
+  static constexpr int flags = items + kItems * 64;       // [kLooks][16 bytes]: keys with bad V rows, a bit
                                                           // each; fp8: four to a byte
-  static constexpr int bars = flags + 64;
+  static constexpr int bars = flags + kLooks * 16;
   // Barriers: of the stages; of units looked after, in turn; of the query tiles (scores, weights
   // and outputs two each, in turn: the weights' warps may be one unit behind the scores and one
   // ahead of the outputs, and a phase's parity has to be told from the one before); of the items.
   static constexpr int kKFull = 0, kVFull = kKFull + kStages, kKEmpty = kVFull + kStages,
                        kVEmpty = kKEmpty + kStages, kRawFull = kVEmpty + kStages,
                        kRawEmpty = kRawFull + kRawStages, kClean = kRawEmpty + kRawStages,
-                       kQFull = kClean + 4, kQReady = kQFull + 2,
+                       kQFull = kClean + kLooks, kQReady = kQFull + 2,
                        kQEmpty = kQReady + 2, kSFull = kQEmpty + 2, kPFull = kSFull + 4,
                        kPvDone = kPFull + 4, kOFree = kPvDone + 4, kItemFull = kOFree + 2,
                        kItemFree = kItemFull + kItems, kBars = kItemFree + kItems;
@@ -554,7 +555,7 @@ __device__ __forceinline__ void widen_role(uint32_t smem, const Waiter& waiter, 
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + 8 * (L::kKFull + st.at));
       if (g >= L::kStages && !wait(L::kVEmpty + st.at, st.phase ^ 1)) return;
-      const uint32_t flags = smem + L::flags + (g & 3) * 16;
+      const uint32_t flags = smem + L::flags + (g & (kLooks - 1)) * 16;
 #pragma unroll 1
       for (int r = cw * 8 + (lane >> 3); r < kKeys; r += kWideWarps * 8) {
         const int j = lane & 7;
@@ -581,7 +582,7 @@ __device__ __forceinline__ void widen_role(uint32_t smem, const Waiter& waiter, 
       if (lane == 0) {
         mbar_arrive(bars + 8 * (L::kVFull + st.at));
         mbar_arrive(bars + 8 * (L::kRawEmpty + sr.at));
-        if (kt >= ragged) mbar_arrive(bars + 8 * (L::kClean + ((cleaned + kt - ragged) & 3)));
+        if (kt >= ragged) mbar_arrive(bars + 8 * (L::kClean + ((cleaned + kt - ragged) & (kLooks - 1))));
       }
     }
     cleaned += it.cleaned();
@@ -634,6 +635,41 @@ __device__ __forceinline__ bool spin(const Waiter& waiter, uint32_t bar, uint32_
     if (__any_sync(0xFFFFFFFFu, mbar_test(bar, phase & 1))) return true;
   return __all_sync(0xFFFFFFFFu, waiter(bar, phase & 1));
 }
+// 32 rows of V of a unit, a lane each: those from `most` on are zeroed, those from `least` on with a
+// NaN or an infinity too, and noted in flags, a bit each.
+template <int F>
+__device__ __noinline__ void look_after(uint32_t v, uint32_t flags, int least, int most) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t at = v + lane * 128;
+  uint32_t bad = 0;
+  if (least < 32) {
+    uint32_t top[4] = {0, 0, 0, 0};
+#pragma unroll 1
+    for (int c = 0; c < 8; c += 4) {  // every column of the row, in any order
+      uint4 w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = lds16(at + (i & 1) * kRun + (((c + (i >> 1)) ^ (lane & 7)) << 4));
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        top[i & 3] = umax16x2(top[i & 3], umax16x2(umax16x2(w[i].x & 0x7FFF7FFFu, w[i].y & 0x7FFF7FFFu),
+                                                   umax16x2(w[i].z & 0x7FFF7FFFu, w[i].w & 0x7FFF7FFFu)));
+    }
+    const uint32_t all = umax16x2(umax16x2(top[0], top[1]), umax16x2(top[2], top[3]));
+    const bool sp = max(all & 0xFFFFu, all >> 16) >= (F == kBF16 ? 0x7F80u : 0x7C00u);
+    bad = __ballot_sync(0xFFFFFFFFu, sp && lane >= least && lane < most);
+    if (bad != 0 || most < 32) {
+      if (lane >= most || bad >> lane & 1)
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 16) {
+          sts16(at + c, make_uint4(0, 0, 0, 0));
+          sts16(at + kRun + c, make_uint4(0, 0, 0, 0));
+        }
+      tc::fence_smem_async();
+    }
+  }
+  if (lane == 0) sts_u32(flags, bad);
+  __syncwarp();
+}
 template <int F, int QF, int KF>
 __device__ __forceinline__ void score_role(float scale, uint32_t smem, uint32_t tmem, const Waiter& waiter,
                                            int tile) {
@@ -642,19 +678,19 @@ __device__ __forceinline__ void score_role(float scale, uint32_t smem, uint32_t 
   auto wait = [&](int bar, uint32_t phase) { return spin(waiter, bars + 8 * bar, phase); };
   const bool one = tc::elect();
   const uint32_t negate = scale < 0.0f ? 1u << 13 : 0u;  // of the scores, by the tensor core
-  uint32_t n = 0, opened = 0;  // units, items of this tile
+  uint32_t n = 0, g = 0, opened = 0, cleaned = 0;  // units of this tile, and of all; items; units looked after
   Stage<L::kStages> st;
   Items<KF> items{smem, 0};
   Item it;
 #pragma unroll 1
   while (items.get(waiter, it)) {
-    const int e = it.end[tile], kb = it.kb, ke = it.ke;
+    const int e = it.end[tile], kb = it.kb, ke = it.ke, ragged = it.ragged();
     if (kb < e) {
       if (!wait((F == QF ? L::kQFull : L::kQReady) + tile, opened++)) return;
       tc::fence_smem_async();  // (the queries may have come by ordinary stores)
     }
 #pragma unroll 1
-    for (int kt = kb; kt < ke; ++kt) {
+    for (int kt = kb; kt < ke; ++kt, ++g) {
       // the outputs of two units before have read the weights that these scores go over
       if (kt < e && n >= 2 && !wait(L::kPvDone + 2 * tile + (n & 1), (n >> 1) - 1)) return;
       if (!wait(L::kKFull + st.at, st.phase)) return;
@@ -666,79 +702,41 @@ __device__ __forceinline__ void score_role(float scale, uint32_t smem, uint32_t 
         ++n;
       }
       tc::commit(one, bars + 8 * (L::kKEmpty + st.at));
+      if (!L::kF8 && kt >= ragged) {  // half of V each
+        if (!wait(L::kVFull + st.at, st.phase)) return;
+        const int row = kt * kKeys + tile * 32;
+        look_after<F>(smem + L::v + st.at * 2 * kRun + tile * 32 * 128,
+                      smem + L::flags + (g & (kLooks - 1)) * 16 + tile * 4, it.least - row, it.most - row);
+        if ((threadIdx.x & 31) == 0) mbar_arrive(bars + 8 * (L::kClean + (cleaned & (kLooks - 1))));
+        ++cleaned;
+      }
       st.step();
     }
   }
 }
-// V of a unit (of its keys): rows from `most` on are zeroed, those from `least` on with a NaN or an
-// infinity too, and noted in flags, a bit each.  By one warp, a lane a row at a time.
-template <int F>
-__device__ __noinline__ void look_after(uint32_t v, uint32_t flags, int least, int most) {
-  const int lane = threadIdx.x & 31;
-  bool written = false;
-#pragma unroll 1
-  for (int k = 0; k < kKeys; k += 32) {
-    uint32_t bad = 0;
-    if (k + 32 > least) {
-      const int key = k + lane;
-      const uint32_t at = v + key * 128;
-      uint32_t top[4] = {0, 0, 0, 0};
-#pragma unroll 1
-      for (int c = 0; c < 8; c += 4) {  // every column of the row, in any order
-        uint4 w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = lds16(at + (i & 1) * kRun + (((c + (i >> 1)) ^ (lane & 7)) << 4));
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          top[i & 3] = umax16x2(top[i & 3], umax16x2(umax16x2(w[i].x & 0x7FFF7FFFu, w[i].y & 0x7FFF7FFFu),
-                                                     umax16x2(w[i].z & 0x7FFF7FFFu, w[i].w & 0x7FFF7FFFu)));
-      }
-      const uint32_t all = umax16x2(umax16x2(top[0], top[1]), umax16x2(top[2], top[3]));
-      const bool sp = max(all & 0xFFFFu, all >> 16) >= (F == kBF16 ? 0x7F80u : 0x7C00u);
-      bad = __ballot_sync(0xFFFFFFFFu, sp && key >= least && key < most);
-      if (key >= most || bad >> lane & 1)
-#pragma unroll 1
-        for (int c = 0; c < 128; c += 16) {
-          sts16(at + c, make_uint4(0, 0, 0, 0));
-          sts16(at + kRun + c, make_uint4(0, 0, 0, 0));
-        }
-      written |= bad != 0 || k + 32 > most;
-    }
-    if (lane == 0) sts_u32(flags + k / 8, bad);
-  }
-  if (written) tc::fence_smem_async();  // (takes as long as looking)
-  __syncwarp();
-}
 template <int F, int KF>
-__device__ __forceinline__ void output_role(uint32_t smem, uint32_t tmem, const Waiter& waiter, int tile,
-                                            int lane) {
+__device__ __forceinline__ void output_role(uint32_t smem, uint32_t tmem, const Waiter& waiter, int tile) {
   using L = Lay<KF>;
   const uint32_t bars = smem + L::bars;
   auto wait = [&](int bar, uint32_t phase) { return spin(waiter, bars + 8 * bar, phase); };
   const bool one = tc::elect();
-  uint32_t n = 0, g = 0, opened = 0, cleaned = 0;  // units of this tile, and of all; items; units looked after
+  uint32_t n = 0, opened = 0, cleaned = 0;  // units, items of this tile; units looked after
   Stage<L::kStages> st;
   Items<KF> items{smem, 0};
   Item it;
 #pragma unroll 1
   while (items.get(waiter, it)) {
     const int e = it.end[tile], kb = it.kb, ke = it.ke, ragged = it.ragged();
-    const int mine = tile ? max(ragged, it.end[0]) : ragged;  // this warp looks after V from here on
     const uint32_t c0 = cleaned - ragged;
     cleaned += it.cleaned();
     // the sums of the item before are read
     if (kb < e && opened++ > 0 && !wait(L::kOFree + tile, opened)) return;
 #pragma unroll 1
-    for (int kt = kb; kt < ke; ++kt, ++g) {
+    for (int kt = kb; kt < ke; ++kt) {
       if (!wait(L::kVFull + st.at, st.phase)) return;
       if (kt < e) {
-        if (!L::kF8 && kt >= mine) {
-          look_after<F>(smem + L::v + st.at * 2 * kRun, smem + L::flags + (g & 3) * 16, it.least - kt * kKeys,
-                        it.most - kt * kKeys);
-          if (lane == 0) mbar_arrive(bars + 8 * (L::kClean + ((c0 + kt) & 3)));
-        } else if (!L::kF8 && kt >= ragged) {
-          if (!wait(L::kClean + ((c0 + kt) & 3), (c0 + kt) >> 2)) return;
-        }
+        const uint32_t nc = c0 + kt;
+        if (!L::kF8 && kt >= ragged && !wait(L::kClean + (nc & (kLooks - 1)), nc / kLooks)) return;
         if (!wait(L::kPFull + 2 * tile + (n & 1), n >> 1)) return;
         tc::fence_after_sync();
         issue_outputs<F, KF>(smem, tmem, one, tile, st.at, n & 1, kt == kb);
@@ -915,8 +913,8 @@ __device__ __noinline__ bool unit_weights(Part s, const Waiter waiter, float& mu
     __syncwarp();
     if (lane == 0) mbar_arrive(bars + 8 * (L::kPFull + 2 * s.tile + (s.n & 1)));
     if (__builtin_expect(kt >= s.from, 0)) {
-      const uint32_t nc = s.cleaned + kt - s.from, flags = s.smem + L::flags + ((s.g + kt) & 3) * 16;
-      if (!wait(L::kClean + (nc & 3), nc >> 2)) return false;
+      const uint32_t nc = s.cleaned + kt - s.from, flags = s.smem + L::flags + ((s.g + kt) & (kLooks - 1)) * 16;
+      if (!wait(L::kClean + (nc & (kLooks - 1)), nc / kLooks)) return false;
       const uint4 f = lds16(flags);
       if constexpr (L::kF8) {
         if (__builtin_expect((f.x | f.y | f.z | f.w) != 0, 0))
@@ -1083,8 +1081,9 @@ __global__ void __launch_bounds__(warps_of(KF) * 32, 1)
     for (int i = lane; i < L::kBars; i += 32) {
       auto of = [&](int bar, int many) { return i >= bar && i < bar + many; };
       int n = of(L::kKEmpty, 2 * L::kStages) ? 2 : 1;
-      if (L::kF8 && (of(L::kKFull, 2 * L::kStages) || of(L::kRawEmpty, L::kRawStages) || of(L::kClean, 4)))
+      if (L::kF8 && (of(L::kKFull, 2 * L::kStages) || of(L::kRawEmpty, L::kRawStages) || of(L::kClean, kLooks)))
         n = kWideWarps;
+      if (!L::kF8 && of(L::kClean, kLooks)) n = 2;
       if (of(L::kQFull, 2) && maps.q_tokens == 0) n = kM;
       if (of(L::kPFull, 4) || of(L::kOFree, 2) || of(L::kQReady, 2)) n = 4;
       if (of(L::kItemFree, kItems)) n = warps_of(KF) - 1;
@@ -1113,7 +1112,7 @@ __global__ void __launch_bounds__(warps_of(KF) * 32, 1)
   } else if (warp < kOutWarp) {
     score_role<F, QF, KF>(L::kF8 ? a.softmax_scale * __ldg(a.kv_scale) : a.softmax_scale, smem, tmem, wait, warp - kScoreWarp);
   } else if (warp < kLoadWarp) {
-    output_role<F, KF>(smem, tmem, wait, warp - kOutWarp, lane);
+    output_role<F, KF>(smem, tmem, wait, warp - kOutWarp);
   } else if (warp == kLoadWarp) {
     issued = a.few_units ? load_role<KF, int32_t>(a, maps, smem_raw, smem, wait, lane, ws, errbits)
                          : load_role<KF, int64_t>(a, maps, smem_raw, smem, wait, lane, ws, errbits);
