@@ -728,9 +728,9 @@ mla_status_t mla_cache_compact_rows(const int64_t* kv_cache_ptrs, int32_t num_la
  * near the largest seen so far, are rounded before their products: to bf16 (2^-8 of
  * themselves) with bf16 keys and values, and to fp16 (2^-11 of themselves, or 2^-34 of
  * the row's largest) with fp16 and fp8 ones.  The sum that they are divided by counts
- * them as rounded in a row's last key tiles (from the first tile of 64 that a neighbour
- * no longer sees whole), and unrounded before these; lse counts them unrounded.  With
- * fp8 keys and bf16 queries, elements of q below 2^-31 of their row's largest magnitude
+ * them as rounded among the first 64 keys of tokens that see no more (and of some
+ * beside them), and unrounded elsewhere; lse counts them unrounded.  With fp8 keys and
+ * bf16 queries, elements of q below 2^-31 of their row's largest magnitude
  * (or of 2^-112, where that is more) are off by at most 2^-39 of it.  Results do not
  * depend on other work on the device; the call's sizes, its lengths and the device's
  * number of SMs decide how rows are cut, and results depend on them through fp32

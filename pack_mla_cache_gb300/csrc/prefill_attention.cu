@@ -79,6 +79,10 @@ constexpr int kSwitch = 4;
 // A CTA takes at least this many units, so that a short call is not cut into runs that are all
 // beginning and join: 21 prompts of 6 to 503 tokens, 2 heads, 19.6 us with 4 and 24.6 with 8.
 constexpr int kMinUnits = 4;
+// A sequence of at most this many items (of a key head) is counted by one lane, beside 31 others; a
+// longer one by the whole warp.  16 prompts of up to 8 items: 154.0 us with 4, 152.2 with 12 or 24;
+// 4 of 22 to 47: 187.7, 186.4, 189.9.
+constexpr int kFewItems = 12;
 // Calls of at most this many key rows, and of no more items than CTAs, give every CTA a whole
 // item: nothing is cut, and nothing has to be joined.  Whole against cut, 16 heads: 300 tokens
 // 14.7 and 18.7 us, 500 tokens 18.9 and 19.3, 700 tokens 21.3 and 21.4, 1000 tokens 27.8 and
@@ -303,12 +307,12 @@ struct Plan {
       if (s0 + lane < a.num_seqs) {
         const Seq one = load_seq(a, s0 + lane, errbits);
         nb = one.nb;
-        if (nb <= 4)
+        if (nb <= kFewItems)
 #pragma unroll 1
           for (int i = 0; i < nb; ++i) u += item_units(a, one, i);
       }
       // sequences of many items: by the whole warp
-      for (uint32_t many = __ballot_sync(0xFFFFFFFFu, nb > 4); many; many &= many - 1) {
+      for (uint32_t many = __ballot_sync(0xFFFFFFFFu, nb > kFewItems); many; many &= many - 1) {
         const int from = __ffs(many) - 1;
         const Seq one = load_seq(a, s0 + from, ignored);
         I sum = 0;
@@ -821,13 +825,14 @@ struct Part {
   int tile, count, from;      // key tiles, and the first that not every row sees whole
   int seen;                   // keys that this thread's row sees, from the first tile on
   bool live;                  // the warp has rows
+  bool head;                  // the part begins with the item's first key tile
   float c;                    // weights: exp2(c score - reference)
 };
 // The weights of an item's units (a function of its own, so that its loop has the registers to
 // itself): the row's reference, the sum of its weights, and how much more they are as they are
-// rounded.  (The last is counted in the units that not every row sees whole: a row of few keys,
-// all of them there, is divided by the weights that its products had, so that their rounding
-// does not scale it.  In long rows the roundings cancel, and the count would cost each unit.)
+// rounded.  (The last is counted in an item's first key tile, by warps with a row that ends there:
+// a row of few keys is divided by the weights that its products had, so that their rounding does
+// not scale it.  In longer rows the roundings cancel, and the count would cost each unit.)
 // False: given up.
 template <int F, int KF>
 __device__ __noinline__ bool unit_weights(Part s, const Waiter waiter, float& mu_out, float& l_out, float& d_out) {
@@ -899,7 +904,7 @@ __device__ __noinline__ bool unit_weights(Part s, const Waiter waiter, float& mu
     tc::st_32x32(s_at, pk);
     const float2 s2 = unf2(add2(sum[0], sum[1]));
     l += s2.x + s2.y;
-    if (__builtin_expect(cut, 0)) {
+    if (__builtin_expect(cut && s.head && kt == 0, 0)) {
       float r0 = 0.0f, r1 = 0.0f;
 #pragma unroll
       for (int j = 0; j < kKeys / 2; ++j) {
@@ -950,7 +955,7 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, bool boxes, u
   const uint32_t o_at = tmem + kO + tile * kV + ((uint32_t)(w4 * 32) << 16);
   const int r = w4 * 32 + lane;
   uint32_t n = 0, g = 0, cleaned = 0, opened = 0;
-  const float ks = L::kF8 ? __ldg(a.kv_scale) : 1.0f;
+  const float ks = L::kF8 ? __ldg(a.kv_scale) : 1.0f, scale = fabsf(a.softmax_scale * ks) * kLog2e;
   Items<KF> items{smem, 0};
   Item it;
   // The queries' place is free when the item's last scores have come: those of the next item are
@@ -967,7 +972,7 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, bool boxes, u
     const bool live = w4 * 32 < mine, ok = r < mine;
     const uint32_t row = it.row0 + tile * kM + r;
     const int seen = ok ? seen_of(a, it.base, it.m, row) : 0, shift = it.kb * kKeys;
-    float c = fabsf(a.softmax_scale * ks) * kLog2e, mu, l, d;
+    float c = scale, mu, l, d;
     if constexpr (F != QF) {
       if (count > 0) {
         if (!__all_sync(0xFFFFFFFFu, waiter(bars + 8 * (L::kQFull + tile), opened++ & 1))) return;
@@ -979,7 +984,7 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, bool boxes, u
     }
     c = c < 1e-37f ? 1e-37f : c;  // (a masked score times it is -infinity)
     if (!unit_weights<F, KF>(Part{smem, s_at, o_at, n, g, cleaned, tile, count, it.ragged() - it.kb, seen - shift,
-                              live, c},
+                              live, it.kb == 0, c},
                          waiter, mu, l, d))
       return;
     n += count;
@@ -989,22 +994,21 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, bool boxes, u
     // ---- the end of this CTA's part of the item
     // (what needs no sums, while the last of them are added up)
     const bool whole = it.kb == 0 && it.ke == it.tiles;
-    const uint32_t dt = a.by_group(row);
-    const int64_t t = it.t0 + (int)dt;
-    const int64_t h = (int64_t)it.head * a.group + (int)(row - dt * a.group);
-    const int64_t slot = (2 * (int64_t)blockIdx.x + (it.kb == 0 ? 1 : 0)) * srows;
-    const int at = tile * kM + r;
-    if (ok && !whole) {
-      ws.m[slot + at] = mu;
-      ws.l[slot + at] = l;
-      ws.d[slot + at] = d;
-    } else if (ok && a.lse) {
-      a.lse[t * a.lse_ts + h * a.lse_hs] = l == 0.0f ? -INFINITY : (mu + __log2f(l)) * kLn2;
-    }
     const float inv = l == 0.0f ? 0.0f : __fdividef(ks, l + d);
-    // where 32 dims of the row go, and how far the next lie
-    uint8_t* to = whole ? a.out + t * a.out_ts + h * a.out_hs
-                        : reinterpret_cast<uint8_t*>(ws.o + slot * kV + at * 4);  // [dims / 4][rows][4]
+    uint8_t* to;  // where the row goes
+    if (whole) {
+      const uint32_t dt = a.by_group(row), t = it.t0 + dt, h = it.head * a.group + (row - dt * a.group);
+      to = a.out + t * a.out_ts + h * a.out_hs;
+      if (ok && a.lse) a.lse[t * a.lse_ts + h * a.lse_hs] = l == 0.0f ? -INFINITY : (mu + __log2f(l)) * kLn2;
+    } else {
+      const uint32_t slot = (2 * blockIdx.x + (it.kb == 0 ? 1 : 0)) * srows, at = slot + tile * kM + r;
+      to = reinterpret_cast<uint8_t*>(ws.o + (int64_t)slot * kV + (tile * kM + r) * 4);  // [dims / 4][rows][4]
+      if (ok) {
+        ws.m[at] = mu;
+        ws.l[at] = l;
+        ws.d[at] = d;
+      }
+    }
     if (count > 0) {
       if (!__all_sync(0xFFFFFFFFu, waiter(bars + 8 * (L::kPvDone + 2 * tile + ((n - 1) & 1)), ((n - 1) >> 1) & 1))) return;
       tc::fence_after_sync();
