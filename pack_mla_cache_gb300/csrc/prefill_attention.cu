@@ -221,6 +221,8 @@ struct Item {
   int rows, t0, head;
   int k0, m;           // the sequence's first key row, and how many exist
   int64_t base;        // keys that its token t0 sees (before clamping)
+  // (an index that is not known would put the whole description into local memory)
+  __device__ __forceinline__ int end_of(int tile) const { return tile ? end[1] : end[0]; }
   // The first key tile that not every row sees whole.
   __device__ __forceinline__ int ragged() const { return max(kb, least / kKeys); }
   // Units with V rows to be looked after.
@@ -688,7 +690,7 @@ __device__ __forceinline__ void score_role(float scale, uint32_t smem, uint32_t 
   Item it;
 #pragma unroll 1
   while (items.get(waiter, it)) {
-    const int e = it.end[tile], kb = it.kb, ke = it.ke, ragged = it.ragged();
+    const int e = it.end_of(tile), kb = it.kb, ke = it.ke, ragged = it.ragged();
     if (kb < e) {
       if (!wait((F == QF ? L::kQFull : L::kQReady) + tile, opened++)) return;
       tc::fence_smem_async();  // (the queries may have come by ordinary stores)
@@ -730,7 +732,7 @@ __device__ __forceinline__ void output_role(uint32_t smem, uint32_t tmem, const 
   Item it;
 #pragma unroll 1
   while (items.get(waiter, it)) {
-    const int e = it.end[tile], kb = it.kb, ke = it.ke, ragged = it.ragged();
+    const int e = it.end_of(tile), kb = it.kb, ke = it.ke, ragged = it.ragged();
     const uint32_t c0 = cleaned - ragged;
     cleaned += it.cleaned();
     // the sums of the item before are read
@@ -828,14 +830,13 @@ struct Part {
   bool head;                  // the part begins with the item's first key tile
   float c;                    // weights: exp2(c score - reference)
 };
-// The weights of an item's units (a function of its own, so that its loop has the registers to
-// itself): the row's reference, the sum of its weights, and how much more they are as they are
-// rounded.  (The last is counted in an item's first key tile, by warps with a row that ends there:
+// The weights of an item's units: the row's reference, the sum of its weights, and how much more
+// they are as they are rounded.  (The last is counted in an item's first key tile, by warps with a row that ends there:
 // a row of few keys is divided by the weights that its products had, so that their rounding does
 // not scale it.  In longer rows the roundings cancel, and the count would cost each unit.)
 // False: given up.
 template <int F, int KF>
-__device__ __noinline__ bool unit_weights(Part s, const Waiter waiter, float& mu_out, float& l_out, float& d_out) {
+__device__ __forceinline__ bool unit_weights(Part s, const Waiter waiter, float& mu_out, float& l_out, float& d_out) {
   using R = Ref<F>;
   using L = Lay<KF>;
   const int lane = threadIdx.x & 31;
@@ -962,13 +963,13 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, bool boxes, u
   // asked for before the output of this one is written.
   auto queries = [&] {
     Item nxt;
-    if (!boxes && items.get(waiter, nxt, true) && nxt.end[tile] > nxt.kb)
+    if (!boxes && items.get(waiter, nxt, true) && nxt.end_of(tile) > nxt.kb)
       load_queries<KF>(a, nxt, smem, tile, w4, lane);
   };
   queries();
 #pragma unroll 1
   while (items.get(waiter, it)) {
-    const int count = max(it.end[tile] - it.kb, 0), mine = it.rows - tile * kM;
+    const int count = max(it.end_of(tile) - it.kb, 0), mine = it.rows - tile * kM;
     const bool live = w4 * 32 < mine, ok = r < mine;
     const uint32_t row = it.row0 + tile * kM + r;
     const int seen = ok ? seen_of(a, it.base, it.m, row) : 0, shift = it.kb * kKeys;
