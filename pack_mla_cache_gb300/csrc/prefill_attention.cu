@@ -72,9 +72,9 @@ constexpr int kMaxCtas = 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // What beginning another item costs a CTA, in units: the runs are cut as if each item had
-// this many more.  An item's change takes about 9000 cycles (the last output's way out, then the
-// next queries and scores) where a unit takes 1700 to 2000.  16 ragged prompts: 200 us with 1,
-// 188 with 2, 179.4 with 4, 180.8 with 6, 183 with 8; 16384 tokens 1060, 1055, 1053, 1053, 1056.
+// this many more.  An item's change takes about 7000 cycles (the last output's way out, then the
+// next scores' weights) where a unit takes 1700 to 2000.  16 ragged prompts 144.7 us with 2, 142.4
+// with 3 and 4; 16384 tokens 1004, 993, 989; 6 chunks over up to 4109 rows 27.2, 26.7, 25.8.
 constexpr int kSwitch = 4;
 // A CTA takes at least this many units, so that a short call is not cut into runs that are all
 // beginning and join: 21 prompts of 6 to 503 tokens, 2 heads, 19.6 us with 4 and 24.6 with 8.
