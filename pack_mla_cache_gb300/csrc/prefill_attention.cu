@@ -536,20 +536,21 @@ __device__ __forceinline__ void widen_role(uint32_t smem, const Waiter& waiter, 
   Stage<L::kRawStages> sr;
   Stage<L::kStages> st;
   uint32_t g = 0, cleaned = 0;
+  int turn = cw;  // the 8 groups of 8 rows are dealt to three warps: who has two of them changes
   Items<KF> items{smem, 0};
   Item it;
 #pragma unroll 1
   while (items.get(waiter, it)) {
     const int ragged = it.ragged();
 #pragma unroll 1
-    for (int kt = it.kb; kt < it.ke; ++kt, ++g, sr.step(), st.step()) {
+    for (int kt = it.kb; kt < it.ke; ++kt, ++g, sr.step(), st.step(), turn = turn == 2 ? 0 : turn + 1) {
       const uint32_t raw = smem + L::raw + sr.at * (L::kRawK + L::kRawV);
       const uint32_t k = smem + L::k + st.at * 3 * kRun, v = smem + L::v + st.at * 2 * kRun;
       if (!wait(L::kRawFull + sr.at, sr.phase)) return;
       if (g >= L::kStages && !wait(L::kKEmpty + st.at, st.phase ^ 1)) return;
       // 8 rows x 8 pieces of 16 columns each (two rounds at once), then the rotary ones 8 x 4
 #pragma unroll 1
-      for (int r = cw * 8 + (lane >> 3); r < kKeys; r += kWideWarps * 8) {
+      for (int r = turn * 8 + (lane >> 3); r < kKeys; r += kWideWarps * 8) {
         const int j = lane & 7;
         const uint4 w0 = lds16(raw + r * 128 + j * 16), w1 = lds16(raw + (r + 4) * 128 + j * 16);
         widen16<KF>(k, r, j, w0);
@@ -563,7 +564,7 @@ __device__ __forceinline__ void widen_role(uint32_t smem, const Waiter& waiter, 
       if (g >= L::kStages && !wait(L::kVEmpty + st.at, st.phase ^ 1)) return;
       const uint32_t flags = smem + L::flags + (g & (kLooks - 1)) * 16;
 #pragma unroll 1
-      for (int r = cw * 8 + (lane >> 3); r < kKeys; r += kWideWarps * 8) {
+      for (int r = (turn == 2 ? 0 : turn + 1) * 8 + (lane >> 3); r < kKeys; r += kWideWarps * 8) {
         const int j = lane & 7;
         uint4 w[2] = {lds16(raw + L::kRawK + r * 128 + j * 16), lds16(raw + L::kRawK + (r + 4) * 128 + j * 16)};
         if (__builtin_expect(kt >= ragged, 0)) {
