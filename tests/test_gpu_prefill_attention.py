@@ -495,3 +495,22 @@ def test_waits_that_run_out_return_and_report(kind, stages):
         c.err.zero_()
         out, _, e = c.run().got()
         assert e == 0 and np.array_equal(out, good)
+
+
+@pytest.mark.parametrize("kind", [(BF, BF), (HF, HF), (BF, E4)], ids=str)
+def test_heads_outside_of_tokens(kind):
+    """[head, token, element] arrays, seen as [token, head, element]: queries, keys, values, results."""
+    c = Call([150, 40], [280, 300], 4, 2, *kind).put()
+    swap = lambda t: t.transpose(0, 1).contiguous().transpose(0, 1)
+    c.dq, c.dv = swap(c.dq), swap(c.dv)
+    key = swap(torch.cat([c.dk.view(torch.uint8), c.dp.view(torch.uint8)], -1)).view(kind[1])
+    c.dk, c.dp = key[:, :, :128], key[:, :, 128:]
+    full = torch.full((4, 191, 136), 7.0, dtype=kind[0], device="cuda")
+    c.out_full, c.out = full.transpose(0, 1), full.transpose(0, 1)[:190, :, :128]
+    c.run().check()
+
+
+def test_lists_that_are_not_whole():
+    """Sequences without keys, without tokens, and with fewer keys than tokens, next to each other."""
+    Call([0, 9, 0, 300, 2, 0, 70], [5, 0, 0, 200, 0, 900, 1], 3, 1).put().run().check()
+    Call([9, 0, 0, 1], [0, 0, 70, 0], 2, 2, HF, E5, causal=False).put().run().check()
