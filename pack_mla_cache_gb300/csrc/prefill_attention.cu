@@ -14,10 +14,9 @@
 // a second launch joins in the order of the CTAs (no atomics: equal calls give equal bits).
 //
 // A unit: S_i = Q_i K^T (two tiles of 128 x 64, k = 192), weights P_i = exp2(S_i - reference)
-// written over S_i in tensor memory as 16-bit values, O_i += P_i V (128 x 128, k = 64).  Tensor
-// memory is full: two S of 64 columns and an O of 128 per query tile.  With two S the scores of
-// the next unit are there when the weights of one are done, and the tensor core does not wait
-// for weights.
+// written to tensor memory as 16-bit values, O_i += P_i V (128 x 128, k = 64).  Tensor memory is
+// full: per query tile S of 64 columns, P of 32, O of 128 and the queries' rotary columns, 32.  The
+// weights' warps read the whole of S before they compute, so that the next scores come meanwhile.
 //
 // Measured (replayed from a graph, 16 heads): one prompt of 16384 tokens 980 us (1400 TFLOP/s), of
 // 300 tokens 11.4 us; 16 prompts of 37 to 2048 tokens 142 us; 1024 new tokens of 2 sequences over
@@ -29,16 +28,17 @@
 // 1100 us, in every order of the products tried).  Three stages of 64 keys hold two units ahead.
 // The price: shared memory's reads bound the scores.  A product 128 x 64 x 16 with both operands
 // there takes 49 cycles (6 KB at 128 bytes a cycle) where one of 128 columns takes 64, so a unit
-// of both tiles, 176 KB of operands and 40 KB that arrive, is 1690 cycles where 1280 of the tensor
-// core would do.  Long prompts come to 1700 to 2000 a unit, at the clock that the power limit
-// leaves (1.84 GHz).
+// of both tiles would be 1690 cycles where 1280 of the tensor core would do.  The queries' rotary
+// third in tensor memory takes 32 KB of a unit's 216 away (grouped heads 182.6 us without, 173.6
+// with it; 2048 tokens 35.5, 34.4; 300 tokens 11.4, 11.7).  Long prompts come to 1600 to 2000 a
+// unit, at the clock that the power limit leaves (1.84 GHz).
 //
 // Shared memory: the two query tiles (96 KB), three stages of K (24 KB: three runs of 64 columns)
 // and of V (16 KB: two), in rows of 128 bytes with the 128-byte swizzle, by TMA.
 //
 // fp8 keys and values are widened to fp16 (exactly) on their way into the stages: two of these
 // then, and two of raw codes (20 KB) in the place of the third.  That is another 80 KB of shared
-// memory's traffic a unit, 2050 cycles in all; a unit takes 2200.  bf16 queries become fp16 times a
+// memory's traffic a unit, 2000 cycles in all; a unit takes 2200.  bf16 queries become fp16 times a
 // power of two per row, in place.
 //
 // Roles (13 warps): 4 warps per query tile compute weights, a thread a row (running maximum,
@@ -124,21 +124,21 @@ struct Lay {
                                                           // each; fp8: four to a byte
   static constexpr int bars = flags + kLooks * 16;
   // Barriers: of the stages; of units looked after, in turn; of the query tiles (scores, weights
-  // and outputs two each, in turn: the weights' warps may be one unit behind the scores and one
-  // ahead of the outputs, and a phase's parity has to be told from the one before); of the items.
+  // and outputs two each, in turn: a warp may wait for a unit's before all have seen the one
+  // before, and a phase's parity has to be told from the last); of the items.
   static constexpr int kKFull = 0, kVFull = kKFull + kStages, kKEmpty = kVFull + kStages,
                        kVEmpty = kKEmpty + kStages, kRawFull = kVEmpty + kStages,
                        kRawEmpty = kRawFull + kRawStages, kClean = kRawEmpty + kRawStages,
                        kQFull = kClean + kLooks, kQReady = kQFull + 2,
-                       kQEmpty = kQReady + 2, kSFull = kQEmpty + 2, kPFull = kSFull + 4,
+                       kQEmpty = kQReady + 2, kSFull = kQEmpty + 2, kSFree = kSFull + 4, kPFull = kSFree + 2,
                        kPvDone = kPFull + 4, kOFree = kPvDone + 4, kItemFull = kOFree + 2,
                        kItemFree = kItemFull + kItems, kBars = kItemFree + kItems;
   static constexpr int misc = (bars + kBars * 8 + 15) / 16 * 16;
   static constexpr int bytes = misc + 64;
   static_assert(bytes <= 232448, "shared memory of a CTA");
 };
-// tensor memory columns: two S of each tile (P in their first half), O of both tiles
-constexpr int kO = 4 * kKeys, kTmem = 512;
+// tensor memory columns: S of both tiles, P, the queries' rotary columns, O
+constexpr int kP = 2 * kKeys, kQr = 3 * kKeys, kO = 4 * kKeys, kTmem = 512;
 struct Misc {
   uint32_t tmem;
   uint32_t abort;
@@ -607,31 +607,40 @@ __device__ __forceinline__ void widen_role(uint32_t smem, const Waiter& waiter, 
 }
 
 // ------------------------------------------------------------ matrix products
+// A query tile's rotary columns to tensor memory, where every unit's scores read them.
+template <int KF>
+__device__ __forceinline__ void move_rotary(uint32_t smem, uint32_t tmem, bool one, int tile) {
+  const uint32_t i = __shfl_sync(0xFFFFFFFFu, tile, 0);
+  const uint64_t qr = tc::smem_desc(smem + Lay<KF>::q + i * kQTile + 2 * kM * 128, 0, 1024);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) tc::copy_k16(one, tmem + kQr + i * (kKeys / 2) + 8 * k, qr + 2 * k);
+}
 template <int F, int KF>
 __device__ __forceinline__ void issue_scores(uint32_t smem, uint32_t tmem, bool one, int tile, int stage,
-                                             uint32_t buffer, uint32_t negate) {
+                                             uint32_t negate) {
   using L = Lay<KF>;
   const uint32_t id = negate | tc::instr_desc(kM, kKeys, false, F == kBF16, F == kBF16);
   const uint32_t i = __shfl_sync(0xFFFFFFFFu, tile, 0), st = __shfl_sync(0xFFFFFFFFu, stage, 0);
-  const uint32_t b = __shfl_sync(0xFFFFFFFFu, buffer, 0);
   const uint64_t qa = tc::smem_desc(smem + L::q + i * kQTile, 0, 1024);
   const uint64_t kb = tc::smem_desc(smem + L::k + st * 3 * kRun, 0, 1024);
-  const uint32_t d = tmem + (2 * i + b) * kKeys;
+  const uint32_t d = tmem + i * kKeys;
 #pragma unroll
-  for (int c = 0; c < 3; ++c)
+  for (int c = 0; c < 2; ++c)
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       tc::mma_16bit(one, d, qa + (c * kM * 128 >> 4) + 2 * k, kb + (c * kRun >> 4) + 2 * k, id, c + k > 0);
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    tc::mma_16bit_ta(one, d, tmem + kQr + i * (kKeys / 2) + 8 * k, kb + (2 * kRun >> 4) + 2 * k, id, true);
 }
 // V MN-major (two runs of 64 columns).
 template <int F, int KF>
 __device__ __forceinline__ void issue_outputs(uint32_t smem, uint32_t tmem, bool one, int tile, int stage,
-                                              uint32_t buffer, bool first) {
+                                              bool first) {
   using L = Lay<KF>;
   constexpr uint32_t kId = tc::instr_desc(kM, kV, false, F == kBF16, F == kBF16, true);
   const uint32_t i = __shfl_sync(0xFFFFFFFFu, tile, 0), st = __shfl_sync(0xFFFFFFFFu, stage, 0);
-  const uint32_t b = __shfl_sync(0xFFFFFFFFu, buffer, 0);
-  const uint32_t p = tmem + (2 * i + b) * kKeys, d = tmem + kO + i * kV;
+  const uint32_t p = tmem + kP + i * (kKeys / 2), d = tmem + kO + i * kV;
   const uint64_t vb = tc::smem_desc(smem + L::v + st * 2 * kRun, kRun, 1024);
 #pragma unroll
   for (int k = 0; k < 4; ++k)
@@ -705,15 +714,18 @@ __device__ __forceinline__ void score_role(float scale, uint32_t smem, uint32_t 
     if (kb < e) {
       if (!wait((F == QF ? L::kQFull : L::kQReady) + tile, opened++)) return;
       tc::fence_smem_async();  // (the queries may have come by ordinary stores)
+      // (the item before's last scores are done, or these queries would not have come)
+      tc::fence_after_sync();
+      move_rotary<KF>(smem, tmem, one, tile);
     }
 #pragma unroll 1
     for (int kt = kb; kt < ke; ++kt, ++g) {
-      // the outputs of two units before have read the weights that these scores go over
-      if (kt < e && n >= 2 && !wait(L::kPvDone + 2 * tile + (n & 1), (n >> 1) - 1)) return;
+      // the scores before these are read
+      if (kt < e && n >= 1 && !wait(L::kSFree + tile, n - 1)) return;
       if (!wait(L::kKFull + st.at, st.phase)) return;
       if (kt < e) {
         tc::fence_after_sync();
-        issue_scores<F, KF>(smem, tmem, one, tile, st.at, n & 1, negate);
+        issue_scores<F, KF>(smem, tmem, one, tile, st.at, negate);
         tc::commit(one, bars + 8 * (L::kSFull + 2 * tile + (n & 1)));
         if (kt + 1 == e) tc::commit(one, bars + 8 * (L::kQEmpty + tile));
         ++n;
@@ -756,7 +768,7 @@ __device__ __forceinline__ void output_role(uint32_t smem, uint32_t tmem, const 
         if (!L::kF8 && kt >= ragged && !wait(L::kClean + (nc & (kLooks - 1)), nc / kLooks)) return;
         if (!wait(L::kPFull + 2 * tile + (n & 1), n >> 1)) return;
         tc::fence_after_sync();
-        issue_outputs<F, KF>(smem, tmem, one, tile, st.at, n & 1, kt == kb);
+        issue_outputs<F, KF>(smem, tmem, one, tile, st.at, kt == kb);
         tc::commit(one, bars + 8 * (L::kPvDone + 2 * tile + (n & 1)));
         ++n;
       }
@@ -833,7 +845,7 @@ __device__ __noinline__ float narrow_row(uint32_t at, int row) {
 
 // What the weights of an item's units need to know; key tiles count from the part's first.
 struct Part {
-  uint32_t smem, s_at, o_at;  // tensor memory: this warp's scores and sums
+  uint32_t smem, s_at, p_at, o_at;  // tensor memory: this warp's scores, weights and sums
   uint32_t n, g, cleaned;     // units of this tile, of all, and looked after, before the part
   int tile, count, from;      // key tiles, and the first that not every row sees whole
   int seen;                   // keys that this thread's row sees, from the first tile on
@@ -842,9 +854,10 @@ struct Part {
   float c;                    // weights: exp2(c score - reference)
 };
 // The weights of an item's units: the row's reference, the sum of its weights, and how much more
-// they are as they are rounded.  (The last is counted in an item's first key tile, by warps with a row that ends there:
-// a row of few keys is divided by the weights that its products had, so that their rounding does
-// not scale it.  In longer rows the roundings cancel, and the count would cost each unit.)
+// they are as they are rounded.  (The last is counted in an item's first key tile, by warps with a
+// row that ends there: a row of few keys is divided by the weights that its products had, so that
+// their rounding does not scale it.  In longer rows the roundings cancel, and the count would cost
+// each unit.)
 // False: given up.
 template <int F, int KF>
 __device__ __forceinline__ bool unit_weights(Part s, const Waiter waiter, float& mu_out, float& l_out, float& d_out) {
@@ -863,12 +876,17 @@ __device__ __forceinline__ bool unit_weights(Part s, const Waiter waiter, float&
     if (!s.live) {
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bars + 8 * (L::kPFull + 2 * s.tile + (s.n & 1)));
+      if (lane == 0) {
+        mbar_arrive(bars + 8 * (L::kSFree + s.tile));
+        mbar_arrive(bars + 8 * (L::kPFull + 2 * s.tile + (s.n & 1)));
+      }
       continue;
     }
-    const uint32_t s_at = s.s_at + (s.n & 1) * kKeys;
     float x[kKeys];
-    tc::ld_32x64(s_at, reinterpret_cast<uint32_t*>(x));
+    tc::ld_32x64(s.s_at, reinterpret_cast<uint32_t*>(x));
+    tc::fence_before_sync();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + 8 * (L::kSFree + s.tile));
     const int lim = s.seen - kt * kKeys;
     const bool cut = kt >= s.from && __any_sync(0xFFFFFFFFu, lim < kKeys);
     if (__builtin_expect(cut, 0)) {
@@ -913,7 +931,10 @@ __device__ __forceinline__ bool unit_weights(Part s, const Waiter waiter, float&
       sum[j & 1] = add2(sum[j & 1], f2(p0, p1));
       pk[j] = pack16x2<F>(p0, p1);
     }
-    tc::st_32x32(s_at, pk);
+    // the weights before these are read
+    if (kt > 0 && !wait(L::kPvDone + 2 * s.tile + ((s.n - 1) & 1), (s.n - 1) >> 1)) return false;
+    tc::fence_after_sync();
+    tc::st_32x32(s.p_at, pk);
     const float2 s2 = unf2(add2(sum[0], sum[1]));
     l += s2.x + s2.y;
     if (__builtin_expect(cut && s.head && kt == 0, 0)) {
@@ -963,7 +984,8 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, bool boxes, u
                                              const Workspace& ws, int srows) {
   using L = Lay<KF>;
   const uint32_t bars = smem + L::bars;
-  const uint32_t s_at = tmem + tile * 2 * kKeys + ((uint32_t)(w4 * 32) << 16);
+  const uint32_t s_at = tmem + tile * kKeys + ((uint32_t)(w4 * 32) << 16);
+  const uint32_t p_at = tmem + kP + tile * (kKeys / 2) + ((uint32_t)(w4 * 32) << 16);
   const uint32_t o_at = tmem + kO + tile * kV + ((uint32_t)(w4 * 32) << 16);
   const int r = w4 * 32 + lane;
   uint32_t n = 0, g = 0, cleaned = 0, opened = 0;
@@ -995,9 +1017,9 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, bool boxes, u
       }
     }
     c = c < 1e-37f ? 1e-37f : c;  // (a masked score times it is -infinity)
-    if (!unit_weights<F, KF>(Part{smem, s_at, o_at, n, g, cleaned, tile, count, it.ragged() - it.kb, seen - shift,
-                              live, it.kb == 0, c},
-                         waiter, mu, l, d))
+    if (!unit_weights<F, KF>(Part{smem, s_at, p_at, o_at, n, g, cleaned, tile, count,
+                                  it.ragged() - it.kb, seen - shift, live, it.kb == 0, c},
+                             waiter, mu, l, d))
       return;
     n += count;
     g += it.ke - it.kb;
@@ -1101,7 +1123,7 @@ __global__ void __launch_bounds__(warps_of(KF) * 32, 1)
         n = kWideWarps;
       if (!L::kF8 && of(L::kClean, kLooks)) n = 2;
       if (of(L::kQFull, 2) && maps.q_tokens == 0) n = kM;
-      if (of(L::kPFull, 4) || of(L::kOFree, 2) || of(L::kQReady, 2)) n = 4;
+      if (of(L::kSFree, 2) || of(L::kPFull, 4) || of(L::kOFree, 2) || of(L::kQReady, 2)) n = 4;
       if (of(L::kItemFree, kItems)) n = warps_of(KF) - 1;
       // (testing: one arrival too many)
       if (blockIdx.x == 0 && i < 2 * L::kStages && a.stall_stage == i + 1) ++n;

@@ -181,6 +181,15 @@ __device__ __forceinline__ void mma_fp8(bool lane, uint32_t d, uint64_t a, uint6
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(lane ? 1u : 0u)
       : "memory");
 }
+// One k step of 16 of a K-major operand of 128 rows, from shared memory to 8 columns of tensor
+// memory, ahead of the matrix instructions that the lane issues later.
+__device__ __forceinline__ void copy_k16(bool lane, uint32_t d, uint64_t a) {
+  asm volatile(
+      "{ .reg .pred q; setp.ne.u32 q, %2, 0;\n"
+      "  @q tcgen05.cp.cta_group::1.128x256b [%0], %1; }" ::"r"(d),
+      "l"(a), "r"(lane ? 1u : 0u)
+      : "memory");
+}
 // Arrive on `bar` when every matrix instruction that lane has issued is done.
 __device__ __forceinline__ void commit(bool lane, uint32_t bar) {
   asm volatile(
