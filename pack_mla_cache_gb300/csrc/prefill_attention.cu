@@ -18,10 +18,10 @@
 // full: per query tile S of 64 columns, P of 32, O of 128 and the queries' rotary columns, 32.  The
 // weights' warps read the whole of S before they compute, so that the next scores come meanwhile.
 //
-// Measured (replayed from a graph, 16 heads): one prompt of 16384 tokens 980 us (1400 TFLOP/s), of
-// 300 tokens 11.4 us; 16 prompts of 37 to 2048 tokens 142 us; 1024 new tokens of 2 sequences over
-// 8192 e4m3 rows each 149 us (1150 TFLOP/s); single tokens of 32 sequences over 500 to 4096 rows
-// 133 us (5.8 TB/s).
+// Measured (replayed from a graph, 16 heads): one prompt of 16384 tokens 970 us (1420 TFLOP/s), of
+// 300 tokens 12.0 us; 16 prompts of 37 to 2048 tokens 142 us; 1024 new tokens of 2 sequences over
+// 8192 e4m3 rows each 150 us (1140 TFLOP/s); single tokens of 32 sequences over 500 to 4096 rows
+// 131 us (5.9 TB/s).
 //
 // Why 64 keys.  Beside the queries (96 KB) there is room for 1.6 units of 128 keys, and K of a
 // unit came later than the products before it were done (2000 cycles for 32 KB; 16384 tokens
@@ -730,9 +730,13 @@ __device__ __forceinline__ void score_role(float scale, uint32_t smem, uint32_t 
         if (kt + 1 == e) tc::commit(one, bars + 8 * (L::kQEmpty + tile));
         ++n;
       }
+      // V of every unit is seen to come, though only some are looked after: a wait for one must know
+      // that the stage's last has come (or it would take that phase for its own: a tile without rows
+      // in an item is held back by nothing else), and the stage's next must not have come (it does
+      // not before this K is free).
+      if (!L::kF8 && !wait(L::kVFull + st.at, st.phase)) return;
       tc::commit(one, bars + 8 * (L::kKEmpty + st.at));
       if (!L::kF8 && kt >= ragged) {  // half of V each
-        if (!wait(L::kVFull + st.at, st.phase)) return;
         const int row = kt * kKeys + tile * 32;
         look_after<F>(smem + L::v + st.at * 2 * kRun + tile * 32 * 128,
                       smem + L::flags + (g & (kLooks - 1)) * 16 + tile * 4, it.least - row, it.most - row);
@@ -946,10 +950,7 @@ __device__ __forceinline__ bool unit_weights(Part s, const Waiter waiter, float&
       }
       d += (r0 - s2.x) + (r1 - s2.y);
     }
-    tc::wait_st();
-    tc::fence_before_sync();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bars + 8 * (L::kPFull + 2 * s.tile + (s.n & 1)));
+    // (before the weights are handed on, without which no note is written over)
     if (__builtin_expect(kt >= s.from, 0)) {
       const uint32_t nc = s.cleaned + kt - s.from, flags = s.smem + L::flags + ((s.g + kt) & (kLooks - 1)) * 16;
       if (!wait(L::kClean + (nc & (kLooks - 1)), nc / kLooks)) return false;
@@ -964,6 +965,10 @@ __device__ __forceinline__ bool unit_weights(Part s, const Waiter waiter, float&
         if (lim > 0 && bits << (kKeys - min(lim, kKeys))) l = NAN;
       }
     }
+    tc::wait_st();
+    tc::fence_before_sync();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + 8 * (L::kPFull + 2 * s.tile + (s.n & 1)));
   }
   mu_out = mu;
   l_out = l;
