@@ -131,7 +131,7 @@ struct Lay {
                        kRawEmpty = kRawFull + kRawStages, kClean = kRawEmpty + kRawStages,
                        kQFull = kClean + kLooks, kQReady = kQFull + 2,
                        kQEmpty = kQReady + 2, kSFull = kQEmpty + 2, kSFree = kSFull + 4, kPFull = kSFree + 2,
-                       kPvDone = kPFull + 4, kOFree = kPvDone + 4, kItemFull = kOFree + 2,
+                       kPvDone = kPFull + 4, kItemFull = kPvDone + 4,
                        kItemFree = kItemFull + kItems, kBars = kItemFree + kItems;
   static constexpr int misc = (bars + kBars * 8 + 15) / 16 * 16;
   static constexpr int bytes = misc + 64;
@@ -753,7 +753,7 @@ __device__ __forceinline__ void output_role(uint32_t smem, uint32_t tmem, const 
   const uint32_t bars = smem + L::bars;
   auto wait = [&](int bar, uint32_t phase) { return spin(waiter, bars + 8 * bar, phase); };
   const bool one = tc::elect();
-  uint32_t n = 0, opened = 0, cleaned = 0;  // units, items of this tile; units looked after
+  uint32_t n = 0, cleaned = 0;  // units of this tile; units looked after
   Stage<L::kStages> st;
   Items<KF> items{smem, 0};
   Item it;
@@ -762,14 +762,13 @@ __device__ __forceinline__ void output_role(uint32_t smem, uint32_t tmem, const 
     const int e = it.end_of(tile), kb = it.kb, ke = it.ke, ragged = it.ragged();
     const uint32_t c0 = cleaned - ragged;
     cleaned += it.cleaned();
-    // the sums of the item before are read
-    if (kb < e && opened++ > 0 && !wait(L::kOFree + tile, opened)) return;
 #pragma unroll 1
     for (int kt = kb; kt < ke; ++kt) {
       if (!wait(L::kVFull + st.at, st.phase)) return;
       if (kt < e) {
         const uint32_t nc = c0 + kt;
         if (!L::kF8 && kt >= ragged && !wait(L::kClean + (nc & (kLooks - 1)), nc / kLooks)) return;
+        // (an item's first weights: each warp has read its sums of the item before, too)
         if (!wait(L::kPFull + 2 * tile + (n & 1), n >> 1)) return;
         tc::fence_after_sync();
         issue_outputs<F, KF>(smem, tmem, one, tile, st.at, kt == kb);
@@ -880,10 +879,10 @@ __device__ __forceinline__ bool unit_weights(Part s, const Waiter waiter, float&
     if (!s.live) {
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bars + 8 * (L::kSFree + s.tile));
-        mbar_arrive(bars + 8 * (L::kPFull + 2 * s.tile + (s.n & 1)));
-      }
+      if (lane == 0) mbar_arrive(bars + 8 * (L::kSFree + s.tile));
+      // (every warp waits for every unit's outputs, so that none mistakes a phase later on)
+      if (kt > 0 && !wait(L::kPvDone + 2 * s.tile + ((s.n - 1) & 1), (s.n - 1) >> 1)) return false;
+      if (lane == 0) mbar_arrive(bars + 8 * (L::kPFull + 2 * s.tile + (s.n & 1)));
       continue;
     }
     float x[kKeys];
@@ -1079,11 +1078,6 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, bool boxes, u
         }
       }
     }
-    if (count > 0) {
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + 8 * (L::kOFree + tile));
-    }
   }
 }
 
@@ -1128,7 +1122,7 @@ __global__ void __launch_bounds__(warps_of(KF) * 32, 1)
         n = kWideWarps;
       if (!L::kF8 && of(L::kClean, kLooks)) n = 2;
       if (of(L::kQFull, 2) && maps.q_tokens == 0) n = kM;
-      if (of(L::kSFree, 2) || of(L::kPFull, 4) || of(L::kOFree, 2) || of(L::kQReady, 2)) n = 4;
+      if (of(L::kSFree, 2) || of(L::kPFull, 4) || of(L::kQReady, 2)) n = 4;
       if (of(L::kItemFree, kItems)) n = warps_of(KF) - 1;
       // (testing: one arrival too many)
       if (blockIdx.x == 0 && i < 2 * L::kStages && a.stall_stage == i + 1) ++n;
