@@ -18,10 +18,10 @@
 // full: per query tile S of 64 columns, P of 32, O of 128 and the queries' rotary columns, 32.  The
 // weights' warps read the whole of S before they compute, so that the next scores come meanwhile.
 //
-// Measured (replayed from a graph, 16 heads): one prompt of 16384 tokens 970 us (1420 TFLOP/s), of
-// 300 tokens 12.0 us; 16 prompts of 37 to 2048 tokens 142 us; 1024 new tokens of 2 sequences over
+// Measured (replayed from a graph, 16 heads): one prompt of 16384 tokens 961 us (1430 TFLOP/s), of
+// 300 tokens 11.8 us; 16 prompts of 37 to 2048 tokens 141 us; 1024 new tokens of 2 sequences over
 // 8192 e4m3 rows each 150 us (1140 TFLOP/s); single tokens of 32 sequences over 500 to 4096 rows
-// 131 us (5.9 TB/s).
+// 133 us (5.8 TB/s).
 //
 // Why 64 keys.  Beside the queries (96 KB) there is room for 1.6 units of 128 keys, and K of a
 // unit came later than the products before it were done (2000 cycles for 32 KB; 16384 tokens
