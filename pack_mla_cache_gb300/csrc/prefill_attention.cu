@@ -83,21 +83,20 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // What beginning another item costs a CTA, in units: the runs are cut as if each item had
 // this many more.  An item's change takes about 7000 cycles (the last output's way out, then the
-// next scores' weights) where a unit takes 1700 to 2000.  16 ragged prompts 144.7 us with 2, 142.4
-// with 3 and 4; 16384 tokens 1004, 993, 989; 6 chunks over up to 4109 rows 27.2, 26.7, 25.8.
+// next scores' weights) where a unit takes 1600 to 2000.  4 ragged prompts of grouped heads 183 us
+// with 2 and 172 with 4, 16 ragged prompts 143 and 140, 16384 tokens 949 and 941.
 constexpr int kSwitch = 4;
 // A CTA takes at least this many units, so that a short call is not cut into runs that are all
-// beginning and join: 21 prompts of 6 to 503 tokens, 2 heads, 19.6 us with 4 and 24.6 with 8.
+// beginning and join: 21 prompts of 6 to 503 tokens, 2 heads, 18.1 us with 4 and 20.3 with 8.
 constexpr int kMinUnits = 4;
 // A sequence of at most this many items (of a key head) is counted by one lane, beside 31 others; a
-// longer one by the whole warp.  16 prompts of up to 8 items: 154.0 us with 4, 152.2 with 12 or 24;
-// 4 of 22 to 47: 187.7, 186.4, 189.9.
+// longer one by the whole warp.  16 prompts of up to 8 items: 141.9 us with 4, 140.1 with 12.
 constexpr int kFewItems = 12;
 // Calls of at most this many key rows, and of no more items than CTAs, give every CTA a whole
 // item: nothing is cut, and nothing has to be joined.  Whole against cut, 16 heads: 300 tokens
-// 14.7 and 18.7 us, 500 tokens 18.9 and 19.3, 700 tokens 21.3 and 21.4, 1000 tokens 27.8 and
-// 24.8 (one CTA then does 16 units in turn).
-constexpr int kWholeKeys = 512;
+// 11.8 and 15.6 us, 500 tokens 15.2 and 16.4, 700 tokens 17.1 and 18.5, 1000 tokens 22.4 and 21.5
+// (one CTA then does 16 units in turn).
+constexpr int kWholeKeys = 768;
 
 // The reference of a row's weights is the next whole number (log2) above its maximum less
 // kTop; a score may pass the reference by kGrow before the sums are rescaled.  fp16 weights:

@@ -393,9 +393,10 @@ def test_head_layouts_of_other_types(kind, heads, kv_heads):
 
 @pytest.mark.parametrize("seqs,heads,kv_heads,kv", [
     (150, 1, 1, 512), (150, 1, 1, 513), (151, 1, 1, 450), (4, 32, 32, 512), (4, 32, 32, 520), (1, 256, 1, 512),
-    (1, 256, 2, 513)], ids=str)
+    (1, 256, 2, 513), (150, 1, 1, 768), (150, 1, 1, 769), (151, 1, 1, 700), (1, 256, 1, 768), (1, 256, 2, 769)],
+    ids=str)
 def test_borders_of_whole_items(seqs, heads, kv_heads, kv):
-    """Around the sizes from which items are cut: 512 key rows in all, an item per SM."""
+    """Around the sizes from which items are cut: 768 key rows in all, an item per SM."""
     lens = [kv // seqs] * (seqs - 1) + [kv - kv // seqs * (seqs - 1)]
     Call([min(2, n) for n in lens], lens, heads, kv_heads, BF).put().run().check()
 
