@@ -1019,7 +1019,8 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, bool boxes, u
         if (lane == 0) mbar_arrive(bars + 8 * (L::kQReady + tile));
       }
     }
-    c = c < 1e-37f ? 1e-37f : c;  // (a masked score times it is -infinity)
+    // (a masked score times it is -infinity, also where a row that sees nothing asks with a NaN)
+    c = c < 1e-37f || seen <= shift ? 1e-37f : c;
     if (!unit_weights<F, KF>(Part{smem, s_at, p_at, o_at, n, g, cleaned, tile, count,
                                   it.ragged() - it.kb, seen - shift, live, it.kb == 0, c},
                              waiter, mu, l, d))

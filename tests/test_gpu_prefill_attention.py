@@ -530,3 +530,23 @@ def test_many_calls_give_the_same_bits(kind, causal):
         c.run()
         differ |= (c.out.view(torch.int16) != first.view(torch.int16)).any() | (c.lse != lse).any()
     assert not differ.item() and c.err.item() == 0
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=str)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("kv_lens", [[70, 0, 200], [400, 0, 900]], ids=str)
+def test_bad_queries_that_see_no_row(kind, bad, kv_lens):
+    """A token that sees nothing has 0 and -infinity, whatever its query holds (a padded batch's
+    rows): more tokens than rows, no rows at all, and those beside them as ever."""
+    lens = [100, 30, 210] if kv_lens[0] == 70 else [430, 30, 905]
+    none = np.zeros(sum(lens), bool)
+    none[:30] = none[lens[0]:lens[0] + 30] = True
+    none[lens[0] + 30:lens[0] + 30 + lens[2] - kv_lens[2]] = True
+    good = Call(lens, kv_lens, 3, 1, *kind).put().run()
+    good.check()
+    want = good.got()
+    c = Call(lens, kv_lens, 3, 1, *kind)
+    c.q[torch.from_numpy(none)] = bad
+    out, lse, e = c.put().run().got()
+    assert (out[none] == 0).all() and np.isneginf(lse[none]).all() and e == 0
+    assert np.array_equal(out, want[0]) and np.array_equal(lse, want[1])

@@ -279,3 +279,22 @@ def test_waits_that_run_out_return_and_report(fmt, heads, stage):
     c.err.zero_()
     out, _, e = c.run().got()
     assert e == 0 and np.array_equal(out, good)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("fmt", [0, 1, 2])
+def test_bad_queries_that_see_no_row(fmt, bad):
+    """A token whose mask names nothing and that has no context has 0 and -infinity, whatever its
+    query holds; the others are as ever."""
+    n = [12, 30]
+    pg = R.paged(n, fmt, 16, seed=8)
+    masks = P.tree_masks(n, 2)
+    none = np.zeros(42, bool)
+    none[[0, 5, 11, 12, 13, 14, 15, 40]] = True
+    masks[none] = False
+    q = R.queries(42, 16)
+    c = Call(pg, q, cu_of(n), n, masks).run().check()
+    want = c.got()
+    c.q[torch.from_numpy(none).cuda()] = bad
+    out, lse, e = c.run().got()
+    assert np.array_equal(out, want[0]) and np.array_equal(lse, want[1]) and e == 0
