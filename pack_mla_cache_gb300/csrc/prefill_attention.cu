@@ -41,8 +41,8 @@
 // memory's traffic a unit, 2000 cycles in all; a unit takes 2200.  bf16 queries become fp16 times a
 // power of two per row, in place.
 //
-// Roles (13 warps): 4 warps per query tile compute weights, a thread a row (running maximum,
-// rescaling O only when a maximum has grown by more than 2^kGrow) and write the output; two per
+// Roles (13 warps): 4 warps per query tile compute weights, a thread a row (running maximum;
+// O is rescaled only when one has grown by more than 2^kGrow, and only that row's) and write the output; two per
 // tile issue the products, scores and outputs; one plans the CTA's items, describes them to the
 // others in shared memory and loads Q, K and V.  V rows that not every row of an item sees are
 // looked after by the scores' warps, half a tile each, ahead of their products (16 ragged prompts
@@ -903,8 +903,11 @@ __device__ __forceinline__ bool unit_weights(Part s, const Waiter waiter, float&
         t[k] = j + 4 + k < kKeys ? fmaxf(t[k], fmaxf(x[j + k], x[j + 4 + k])) : fmaxf(t[k], x[j + k]);
     const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * s.c;
     if (__builtin_expect(__any_sync(0xFFFFFFFFu, top > mu + R::kGrow), 0)) {
-      const float mn = fmaxf(mu, ceilf(top) - R::kTop);
-      const float f = mu == -INFINITY ? 0.0f : ex2(mu - mn);
+      // Only the rows that have grown: with the others' references a row's roundings would depend
+      // on keys that it does not see, and on the queries behind the sequence's last.
+      const bool up = top > mu + R::kGrow;
+      const float mn = up ? ceilf(top) - R::kTop : mu;
+      const float f = up ? ex2(mu - mn) : 1.0f;
       l = l == 0.0f ? 0.0f : l * f;  // (a NaN stays)
       d *= f;
       mu = mn;

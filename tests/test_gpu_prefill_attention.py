@@ -550,3 +550,45 @@ def test_bad_queries_that_see_no_row(kind, bad, kv_lens):
     out, lse, e = c.put().run().got()
     assert (out[none] == 0).all() and np.isneginf(lse[none]).all() and e == 0
     assert np.array_equal(out, want[0]) and np.array_equal(lse, want[1])
+
+
+def _same_bits(a, b):
+    """Results of `got`, NaNs among them."""
+    return all(np.array_equal(x, y, equal_nan=True) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=str)
+@pytest.mark.parametrize("ctx", [160, 900])
+def test_a_large_key_moves_no_row_that_does_not_see_it(kind, ctx):
+    """Tokens 25 to 63 see a key whose scores dwarf the others; the tokens before them, some of them
+    rows of the same warp, keep every bit.  The key lies behind a tile of smaller ones (of the
+    block's part of the sum, too, where that is cut), so its reader's reference has to move."""
+    p = ctx + 25
+    got = []
+    for mul in (1.0, 20.0 if kind[1] not in R.FP8 else 10.0):
+        c = Call([64], [ctx + 64], 4, dtype=kind[0], kv=kind[1])
+        key = c.key.float()
+        key[:p // 64 * 64] *= 0.5
+        key[p] *= mul
+        c.key = (key.clamp(-448, 448) if kind[1] is E4 else key).to(kind[1])
+        c.put().run().check()
+        got.append(c.got()[:2])
+    assert _same_bits([x[:25] for x in got[0]], [x[:25] for x in got[1]])
+    assert not np.array_equal(got[0][1][25:], got[1][1][25:])
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=str)
+def test_queries_of_the_next_sequence_move_no_row(kind):
+    """Tokens of the next sequence that share a warp's rows with this one's last tokens: whatever
+    they ask, this sequence keeps every bit."""
+    got = []
+    for mul in (1.0, 40.0, float("nan")):
+        c = Call([20, 200], [300, 300], 2, dtype=kind[0], kv=kind[1])
+        key = c.key.float()
+        key[:128] *= 0.5
+        c.key = key.to(kind[1])
+        c.q[20:] *= mul
+        c.put().run()
+        got.append(c.got()[:2])
+    for other in got[1:]:
+        assert _same_bits([x[:20] for x in got[0]], [x[:20] for x in other])
