@@ -579,8 +579,9 @@ mla_status_t mla_cache_copy_blocks(const int64_t* kv_cache_ptrs, int32_t num_lay
  *   out[t,h]  = sum_p exp(x_p - lse[t,h]) * row_p[0:kv_lora_rank]
  * where row_p is the stored bf16 row, or an fp8 row's values times *k_scale.  A
  * token that sees no row has out = 0 and lse = -infinity.  A row that a token
- * does not see has no influence on its result, whatever the row holds; the
- * result of a token that sees a row with a NaN or an infinity is not specified.
+ * does not see has no influence on its result but through the fp32 roundings
+ * named below, whatever the row holds; the result of a token that sees a row
+ * with a NaN or an infinity is not specified.
  *
  * Arithmetic: exact products summed in fp32, softmax in fp32, one rounding of the
  * result to bf16.  Two operands are rounded before their products:
@@ -593,7 +594,8 @@ mla_status_t mla_cache_copy_blocks(const int64_t* kv_cache_ptrs, int32_t num_lay
  * Results do not depend on other work on the device.  The call's shape (num_tokens,
  * num_seqs, num_heads), its lengths and the device's number of SMs decide how the
  * rows are cut; results depend on them through fp32 roundings only (the order of
- * sums, and a score's distance to the power of two of the rows around it).
+ * sums, and a score's distance to a power of two that moves when the score of any
+ * of the up to 32 query rows beside it has grown).
  *
  *   q_c, q_pe           bf16; element (t, h, e) at t * token_stride +
  *                       h * head_stride + e; rows start on 16-byte boundaries.
@@ -657,7 +659,8 @@ mla_status_t mla_latent_attention(
  *                       words apart.
  *   mask_words          1 to 1024.
  * Every other argument and rule is that of mla_latent_attention, its workspace
- * (mla_latent_attention_workspace) too.
+ * (mla_latent_attention_workspace) too; but a query row's power of two moves with its
+ * own scores alone, so a row that a token does not see leaves every bit of its result.
  */
 mla_status_t mla_latent_tree_attention(
     const void* q_c, int64_t qc_token_stride, int64_t qc_head_stride, const void* q_pe,

@@ -977,8 +977,17 @@ __device__ __forceinline__ void soften(const LatentAttnArgs& a, const Run<TREE>&
         float f[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float mn = fmaxf(mu[j][e], ceilf(tm[j][e]) - L::kTop);
-          f[e] = mu[j][e] == -INFINITY ? 0.0f : ex2(mu[j][e] - mn);
+          float mn;
+          if constexpr (TREE) {
+            // only the rows that have grown: with the others' references a token's roundings would
+            // depend on rows that its mask does not name
+            const bool up = tm[j][e] > mu[j][e] + L::kGrow;
+            mn = up ? ceilf(tm[j][e]) - L::kTop : mu[j][e];
+            f[e] = up ? ex2(mu[j][e] - mn) : 1.0f;
+          } else {
+            mn = fmaxf(mu[j][e], ceilf(tm[j][e]) - L::kTop);
+            f[e] = mu[j][e] == -INFINITY ? 0.0f : ex2(mu[j][e] - mn);
+          }
           l[j][e] *= f[e];
           mu[j][e] = mn;
         }

@@ -298,3 +298,42 @@ def test_bad_queries_that_see_no_row(fmt, bad):
     c.q[torch.from_numpy(none).cuda()] = bad
     out, lse, e = c.run().got()
     assert np.array_equal(out, want[0]) and np.array_equal(lse, want[1]) and e == 0
+
+
+def _times(pg, s, p, mul):
+    """Row p of sequence s of a paged cache times a factor, cut to what the format holds."""
+    o = int(pg.table[s, p // pg.block]) * pg.block_stride + (p % pg.block) * pg.entry_stride
+    row = pg.cache[o:o + R.ENTRY]
+    if pg.fmt == 0:
+        pg.cache[o:o + R.ENTRY] = R.orc.bf16_from_f32_array((R.orc.bf16_bits_to_f64(row) * mul).astype(np.float32))
+    else:
+        x = np.clip(R.orc.fp8_decode(row, pg.fmt).astype(np.float32) * np.float32(mul), -440, 440)
+        pg.cache[o:o + R.ENTRY] = R.orc.fp8_encode(x, pg.fmt)
+
+
+@pytest.mark.parametrize("fmt", [0, 1, 2])
+@pytest.mark.parametrize("heads", [1, 4, 16])
+def test_a_large_row_moves_no_token_that_does_not_name_it(fmt, heads):
+    """The masks of every other token name a drafted row whose scores dwarf the others; the tokens
+    between, rows of the same query tile, keep every bit.  The row lies behind tiles of smaller
+    ones, so its readers' references have to move; enough sequences (over the same blocks) that most
+    are not cut in front of it."""
+    S, n, ctx = 300, 8, 200
+    masks = P.tree_masks([n] * S, 3)
+    masks[:, 4] = np.arange(S * n) % 2 == 1
+    got = []
+    for mul in (1.0, 20.0):
+        pg = R.paged([ctx + n], fmt, 64, seed=4)
+        for p in range(192):
+            _times(pg, 0, p, 0.5)
+        _times(pg, 0, ctx + 4, mul)
+        pg.table = np.repeat(pg.table, S, 0)
+        c = Call(pg, R.queries(S * n, heads, mul=2.0), cu_of([n] * S), [ctx + n] * S, masks).run()
+        got.append(c.got())
+        assert got[-1][2] == 0
+        if mul > 1:
+            c.check()
+    sees = masks[:, 4]
+    for a, b in zip(got[0][:2], got[1][:2]):
+        assert np.array_equal(a[~sees], b[~sees])
+    assert not np.array_equal(got[0][1][sees], got[1][1][sees])
