@@ -1246,7 +1246,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefill_join_kernel(const Pre
 // ------------------------------------------------------------------ launches
 // Rows of keys (or values) of all heads as a tensor map with boxes of 64 columns (fp8: all)
 // and 64 rows.  Heads inside a row are columns of it, so that any head stride does; otherwise (heads
-// apart) the third dimension.  `base` stands in for arrays without rows.
+// apart, or more columns than 31 bits count) the third dimension.  `base` stands in for arrays
+// without rows.
 bool make_map(CUtensorMap* map, const void* base, int fmt, int width, int64_t hs, int heads, int64_t ts,
               int64_t rows, int32_t* x_head, int32_t* z_head) {
   const TensorMapEncode encode = tensor_map_encode();
@@ -1255,12 +1256,14 @@ bool make_map(CUtensorMap* map, const void* base, int fmt, int width, int64_t hs
   *x_head = *z_head = 0;
   const int64_t flat = (heads - 1) * hs + (int64_t)width * es;
   cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)rows, 1};
-  cuuint64_t strides[2] = {(cuuint64_t)ts, (cuuint64_t)ts};
-  if (rows <= 1) strides[0] = strides[1] = (cuuint64_t)((flat + 15) / 16 * 16);
+  // (strides of dimensions of one are not used, and may be anything)
+  cuuint64_t strides[2] = {(cuuint64_t)(rows > 1 ? ts : width * es), 0};
+  strides[1] = strides[0];
   if (heads > 1 && hs > 0) {
-    if (rows <= 1 || flat <= ts) {
+    if ((rows <= 1 || flat <= ts) && flat / es <= INT32_MAX) {
       dims[0] = (cuuint64_t)(flat / es);
       *x_head = (int32_t)(hs / es);
+      if (rows <= 1) strides[0] = strides[1] = (cuuint64_t)((flat + 15) / 16 * 16);
     } else {
       dims[2] = (cuuint64_t)heads;
       strides[1] = (cuuint64_t)hs;

@@ -592,3 +592,17 @@ def test_queries_of_the_next_sequence_move_no_row(kind):
         got.append(c.got()[:2])
     for other in got[1:]:
         assert _same_bits([x[:20] for x in got[0]], [x[:20] for x in other])
+
+
+@pytest.mark.parametrize("kind", [(BF, BF), (HF, HF), (BF, E4)], ids=str)
+@pytest.mark.parametrize("rows", [1, 2])
+def test_heads_far_apart(kind, rows):
+    """Heads 2^30 elements apart: the columns of three of them are more than 2^31, outside of the one
+    row that there is, or (two rows) inside of rows that are farther apart still."""
+    heads, step = 3, (1 << 30) + 64
+    c = Call([5], [rows], heads, dtype=kind[0], kv=kind[1]).put()
+    big = torch.empty((rows - 1) * (3 * step) + 2 * step + 128, dtype=kind[1], device="cuda")
+    far = big.as_strided((rows, heads, 128), (3 * step, step, 1))
+    far.view(torch.uint8).copy_(c.dk.contiguous().view(torch.uint8))
+    c.dk = far
+    c.run().check()
