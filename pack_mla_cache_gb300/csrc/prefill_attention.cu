@@ -412,11 +412,13 @@ struct Plan {
 };
 
 // Plans the items and describes them, one ahead; Q, K and V by TMA; where the run ends inside
-// an item, what the join needs.  Returns the copies begun, in K and V of a unit (fp8: in units).
+// an item, what the join needs.  Returns the copies begun, in K and V of a unit (fp8: in units);
+// filled: how often the queries' boxes of each tile.
 template <int KF, typename I>
 __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& maps, uint8_t* smem_raw,
                                               uint32_t smem, const Waiter& wait, int lane,
-                                              const Workspace& ws, uint32_t& errbits) {
+                                              const Workspace& ws, uint32_t& errbits,
+                                              uint32_t (&filled)[2]) {
   using L = Lay<KF>;
   const uint32_t bars = smem + L::bars;
   auto waited = [&](int bar, uint32_t phase) {
@@ -429,7 +431,7 @@ __device__ __forceinline__ uint32_t load_role(const PrefillArgs& a, const Maps& 
   plan.find(a, reinterpret_cast<I*>(smem_raw + L::k), lane, errbits);
   tc::fence_smem_async();  // the scratch is read; copies may write there now
   __syncwarp();
-  uint32_t g = 0, told = 0, filled[2] = {0, 0};
+  uint32_t g = 0, told = 0;
   Stage<L::kF8 ? L::kRawStages : L::kStages> st;
   Item it;
   it.ke = 0;
@@ -1085,10 +1087,12 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, bool boxes, u
 }
 
 // ------------------------------------------------------------------ the kernel
-// After giving up: waits, bounded again, for the copies into shared memory, and a
-// millisecond for matrix products in flight (they end by themselves within microseconds).
+// After giving up: waits, bounded again, for the copies into shared memory (keys, values and the
+// queries' boxes; another CTA may own it next), and a millisecond for matrix products in flight
+// (they end by themselves within microseconds).
 template <int KF>
-__device__ __noinline__ void settle(uint32_t smem, uint32_t issued, uint64_t limit) {
+__device__ __noinline__ void settle(uint32_t smem, uint32_t issued, uint32_t filled0, uint32_t filled1,
+                                    uint64_t limit) {
   using L = Lay<KF>;
   const uint64_t since = global_ns();
   auto past = [&](int bar, uint32_t phase) {
@@ -1102,6 +1106,8 @@ __device__ __noinline__ void settle(uint32_t smem, uint32_t issued, uint64_t lim
     for (uint32_t i = issued > 2 * L::kStages ? issued - 2 * L::kStages : 0; i < issued; ++i)
       past((i & 1 ? L::kVFull : L::kKFull) + (i >> 1) % L::kStages, (i >> 1) / L::kStages);
   }
+  if (filled0 > 0) past(L::kQFull, filled0 - 1);
+  if (filled1 > 0) past(L::kQFull + 1, filled1 - 1);
   while (global_ns() - since <= 1000000) {
   }
 }
@@ -1145,7 +1151,7 @@ __global__ void __launch_bounds__(warps_of(KF) * 32, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, m.tmem, 0);
-  uint32_t errbits = 0, issued = 0;
+  uint32_t errbits = 0, issued = 0, filled[2] = {0, 0};
   if (warp < kScoreWarp) {
     softmax_role<F, QF, KF>(a, maps.q_tokens != 0, smem, tmem, wait, warp >> 2, warp & 3, lane, ws, srows);
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -1154,8 +1160,8 @@ __global__ void __launch_bounds__(warps_of(KF) * 32, 1)
   } else if (warp < kLoadWarp) {
     output_role<F, KF>(smem, tmem, wait, warp - kOutWarp);
   } else if (warp == kLoadWarp) {
-    issued = a.few_units ? load_role<KF, int32_t>(a, maps, smem_raw, smem, wait, lane, ws, errbits)
-                         : load_role<KF, int64_t>(a, maps, smem_raw, smem, wait, lane, ws, errbits);
+    issued = a.few_units ? load_role<KF, int32_t>(a, maps, smem_raw, smem, wait, lane, ws, errbits, filled)
+                         : load_role<KF, int64_t>(a, maps, smem_raw, smem, wait, lane, ws, errbits, filled);
   } else {
     if constexpr (L::kF8) widen_role<KF>(smem, wait, warp - kWideWarp, lane);
   }
@@ -1168,7 +1174,7 @@ __global__ void __launch_bounds__(warps_of(KF) * 32, 1)
   __syncthreads();
   tc::fence_after_sync();
   if (__builtin_expect(wait.given_up(), 0)) {
-    if (warp == kLoadWarp) settle<KF>(smem, issued, a.wait_limit_ns);
+    if (warp == kLoadWarp) settle<KF>(smem, issued, filled[0], filled[1], a.wait_limit_ns);
     if (threadIdx.x == 0 && a.err) atomicOr(a.err, kErrTimeout);
     __syncthreads();
   }

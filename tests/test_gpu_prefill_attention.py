@@ -606,3 +606,27 @@ def test_heads_far_apart(kind, rows):
     far.view(torch.uint8).copy_(c.dk.contiguous().view(torch.uint8))
     c.dk = far
     c.run().check()
+
+
+@pytest.mark.parametrize("kind,stages", [((BF, BF), 6), ((HF, E5), 4)], ids=str)
+def test_waits_that_run_out_with_queries_on_their_way(kind, stages):
+    """As above, with many short items, so that query boxes of both tiles come again and again (also
+    of tiles without rows): the call ends, says so, and the next one, launched right behind it, is
+    exact."""
+    lens = [130, 20, 300, 129, 70, 256] * 40
+    c = Call(lens, lens, 4, 2, *kind).put()
+    good = c.run().got()[0]
+    for stage in range(1, stages + 1):
+        c.out.fill_(3.0)
+        torch.cuda.synchronize()
+        try:
+            ops.mla_test_attention_timeout(1_000_000, stage)
+            c.run()
+        finally:
+            ops.mla_test_attention_timeout()
+        first = c.out.clone()
+        c.run()
+        out, _, e = c.got()
+        assert e == ops.MLA_ERRBIT_TIMEOUT and np.array_equal(out, good)
+        assert not np.array_equal(R.f64(first.cpu())[:130, :2], good[:130, :2])
+        c.err.zero_()
