@@ -655,11 +655,12 @@ __device__ __forceinline__ void issue_outputs(uint32_t smem, uint32_t tmem, bool
 // both tiles' warps have said so; a warp whose tile has no part in a unit says it when they have
 // come, so that it does not run ahead.
 //
-// Looks at a barrier without letting the warp be suspended: waking takes long.
+// Looks at a barrier without letting the warp be suspended: waking takes long.  Every lane has
+// to see the phase complete: the lane that issues, and those that read what has come.
 __device__ __forceinline__ bool spin(const Waiter& waiter, uint32_t bar, uint32_t phase) {
 #pragma unroll 1
   for (int n = 0; n < 64; ++n)
-    if (__any_sync(0xFFFFFFFFu, mbar_test(bar, phase & 1))) return true;
+    if (__all_sync(0xFFFFFFFFu, mbar_test(bar, phase & 1))) return true;
   return __all_sync(0xFFFFFFFFu, waiter(bar, phase & 1));
 }
 // 32 rows of V of a unit, a lane each: those from `most` on are zeroed, those from `least` on with a

@@ -630,3 +630,25 @@ def test_waits_that_run_out_with_queries_on_their_way(kind, stages):
         assert e == ops.MLA_ERRBIT_TIMEOUT and np.array_equal(out, good)
         assert not np.array_equal(R.f64(first.cpu())[:130, :2], good[:130, :2])
         c.err.zero_()
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_many_calls_of_many_shapes_give_the_same_bits(seed):
+    """12 x 10 random batches, 400 calls of each: what a call gives does not depend on when its warps
+    come by."""
+    rng = np.random.default_rng(900 + seed)
+    for i in range(10):
+        n, G = int(rng.choice([1, 3, 12, 60, 150])), int(rng.choice([1, 2, 4]))
+        H = G * int(rng.choice([1, 2, 3, 8]))
+        most = max(2, min(1200, 40000 // (n * H)))
+        ql = [int(rng.choice([0, 1, 2, 60, 127, 130, int(rng.integers(1, most + 1))])) for _ in range(n)]
+        ql[0] = max(1, ql[0])
+        kind = KINDS[int(rng.integers(0, len(KINDS)))]
+        c = Call(ql, [x + int(rng.choice([0, 1, 30, 64, 700 // n])) for x in ql], H, G, *kind, seed=i,
+                 causal=bool(rng.integers(0, 2))).put().run()
+        out, lse = c.out.clone(), c.lse.clone()
+        differ = torch.zeros((), dtype=torch.bool, device="cuda")
+        for _ in range(400):
+            c.run()
+            differ |= (c.out.view(torch.int16) != out.view(torch.int16)).any() | (c.lse != lse).any()
+        assert not differ.item() and c.err.item() == 0, (i, ql, H, G, kind)
