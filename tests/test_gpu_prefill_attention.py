@@ -652,3 +652,45 @@ def test_many_calls_of_many_shapes_give_the_same_bits(seed):
             c.run()
             differ |= (c.out.view(torch.int16) != out.view(torch.int16)).any() | (c.lse != lse).any()
         assert not differ.item() and c.err.item() == 0, (i, ql, H, G, kind)
+
+
+@pytest.mark.parametrize("kind", [(BF, BF), (HF, HF), (BF, E4), (HF, E5)], ids=str)
+def test_batches_whose_units_are_counted_in_64_bits(kind):
+    """4096 sequences, nearly all empty: by an estimate from their number the units could pass 32
+    bits.  The same four sequences alone stay below it; nothing else differs, so the bits agree, and
+    tokens of each agree with 64-bit arithmetic."""
+    lens, kvs, at = [1300, 1, 499, 200], [9000, 4000, 5000, 2000], [0, 17, 2000, 4095]
+    H, G = 256, 64
+    T, K = sum(lens), sum(kvs)
+    q = R.values((T, H, 192), kind[0], 1, 1.5).cuda()
+    mul = 30.0 if kind[1] in R.FP8 else 1.0
+    key, v = R.values((K, 1, 192), kind[1], 2, mul).cuda(), R.values((K, 1, 128), kind[1], 3, mul).cuda()
+    key, v = key.expand(-1, G, -1), v.expand(-1, G, -1)
+    ks = torch.tensor([0.03], device="cuda") if kind[1] in R.FP8 else None
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    got = []
+    for n in (4, 4096):
+        ql, kl = np.zeros(n, int), np.zeros(n, int)
+        where = range(4) if n == 4 else at
+        for s, a, b in zip(where, lens, kvs):
+            ql[s], kl[s] = a, b
+        out, lse = torch.full((T, H, 128), 7.0, dtype=kind[0], device="cuda"), torch.full((T, H), 7.0, device="cuda")
+        ws = torch.full((ops.mla_prefill_attention_workspace(T, H, G, n),), 0xFF, dtype=torch.uint8, device="cuda")
+        ops.mla_prefill_attention(q[:, :, :128], q[:, :, 128:], key[:, :, :128], key[:, :, 128:], v, i32(cu_of(ql)),
+                                  i32(cu_of(kl)), out, ws, softmax_scale=R.SCALE, kv_scale=ks, lse=lse, err_word=err)
+        torch.cuda.synchronize()
+        got.append((out, lse))
+    assert torch.equal(got[0][0].view(torch.int16), got[1][0].view(torch.int16)) and torch.equal(got[0][1], got[1][1])
+    assert err.item() == 0
+    c = 1.0 if ks is None else float(np.float32(0.03))
+    cq, ck = cu_of(lens), cu_of(kvs)
+    for s in range(4):
+        for t in {0, lens[s] // 2, lens[s] - 1}:
+            m = kvs[s] - lens[s] + 1 + t
+            rows = slice(ck[s], ck[s] + m)
+            r = R.attend(R.f64(q[cq[s] + t:cq[s] + t + 1, ::17].cpu()), c * R.f64(key[rows, :1].cpu()),
+                         c * R.f64(v[rows, :1].cpu()), [0, 1], [0, m], R.SCALE, False)
+            bo, bl = R.bounds(r, kind[0], kind[1])
+            assert (np.abs(R.f64(got[1][0][cq[s] + t:cq[s] + t + 1, ::17].cpu()) - r.out) <= bo).all()
+            assert (np.abs(R.f64(got[1][1][cq[s] + t:cq[s] + t + 1, ::17].cpu()) - r.lse) <= bl).all()

@@ -337,3 +337,21 @@ def test_a_large_row_moves_no_token_that_does_not_name_it(fmt, heads):
     for a, b in zip(got[0][:2], got[1][:2]):
         assert np.array_equal(a[~sees], b[~sees])
     assert not np.array_equal(got[0][1][sees], got[1][1][sees])
+
+
+@pytest.mark.parametrize("fmt", [0, 1, 2])
+@pytest.mark.parametrize("case", [([5, 9, 1], [300, 9, 700], 16), ([1] * 40, list(range(1, 2400, 60)), 16),
+                                  ([64, 3], [1200, 5000], 4)], ids=["short", "single", "long"])
+def test_chains_meet_the_definition_both_ways(fmt, case):
+    """Trees of one branch by masks and as causal tokens: each within the bound of the one definition."""
+    n, kv, H = case
+    pg = R.paged(kv, fmt, 64)
+    q = R.queries(sum(n), H)
+    masks = np.concatenate([np.tril(np.ones((x, max(n)), bool)) for x in n])
+    c = Call(pg, q, cu_of(n), kv, masks).run().check()
+    c.out.fill_(7.0)
+    c.lse.fill_(7.0)
+    ops.mla_latent_attention(c.q[:, :, :512], c.q[:, :, 512:], c.cache, pg.fmt, pg.num_blocks, pg.block,
+                             pg.block_stride, pg.entry_stride, c.table, c.cu_t, c.kv_t, c.out, c.ws,
+                             softmax_scale=R.SCALE, k_scale=c.k_scale, lse=c.lse, causal=True)
+    c.check()
