@@ -692,7 +692,8 @@ mla_status_t mla_latent_tree_attention(
  *   rows                int32 device [num_seqs, max_rows], lists rows_stride elements
  *                       apart, each strictly increasing over its first counts[s]
  *                       elements and not below 0.  max_rows at most 1024.
- *   counts              int32 device [num_seqs]; 0 moves nothing.
+ *   counts              int32 device [num_seqs]; 0 moves nothing.  (A call with
+ *                       max_rows 0 launches nothing, and reports no counts.)
  * A sequence whose list is not of that form, or whose start or count is negative or
  * count above max_rows, is left as it is (MLA_ERRBIT_POS_OOB); so is one with a row
  * behind its table's or in a block whose id is out of range (MLA_ERRBIT_BLOCK_OOB).

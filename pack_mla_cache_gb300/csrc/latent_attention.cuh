@@ -20,7 +20,7 @@
 // Measured (replayed from a graph, without the profiler; 16 heads, 64-row blocks): one
 // new token of 4 sequences over 131072 bf16 rows 101 us (5.97 TB/s), of 64 over 130 to
 // 16384 e4m3 rows 60.3 us (5.2 TB/s), of one over 2047 bf16 rows 10.2 us; 1024 new
-// tokens of 2 over 8192 bf16 rows 643 us (852 TFLOP/s).  About 10 us of a call are fixed
+// tokens of 2 over 8192 bf16 rows 632 us (867 TFLOP/s).  About 10 us of a call are fixed
 // (finding the run and the first rows 3, filling and draining the pipeline 4, the join 3).
 //
 // Both products are computed transposed, so that few query rows (a decode
@@ -70,8 +70,8 @@
 // Trees (TREE): the rows before a sequence's new tokens are seen by all of them, so only
 // the tiles from the first new row on are mixed, and there a token's mask bits stand in
 // place of the comparison with the number of rows that it sees.  Measured, 16 heads: one tree of 8
-// tokens over 2047 bf16 rows 15.0 us; 32 of 5 to 16 over 700 to 8192 e4m3 rows 110 us; 16 of 61
-// over 1025 to 8191 bf16 rows 242 us (650 TFLOP/s).
+// tokens over 2047 bf16 rows 15.0 us; 32 of 5 to 16 over 700 to 8192 e4m3 rows 112 us; 16 of 61
+// over 1025 to 8191 bf16 rows 240 us (660 TFLOP/s).
 //
 // Waits are bounded (wait_limit_ns): one that runs out marks the CTA as given up.
 // Every role leaves at its next wait then, copies and products in flight are waited
@@ -122,8 +122,8 @@ struct Lay {
   // Halves of a stage (chunks 0 to 3 and the rest) that fill and are freed by
   // themselves.  At 64 query rows the chain load, scores, weights, outputs of the two
   // stages is what takes the time, and a half's load overlaps the outputs of the other
-  // (2 chunks of 1024 tokens over 8192 rows: 645 us, 689 with whole stages; 16 decodes of
-  // 128 heads 46.1, 47.7).
+  // (2 chunks of 1024 tokens over 8192 rows: 632 us, 675 with whole stages; 16 decodes of
+  // 128 heads 43.5, 44.5).
   static constexpr int kHalves = NR == 64 ? 2 : 1;
   static constexpr int kQBufs = NR <= (kF8 ? 16 : 32) ? 2 : 1;
   static constexpr int kQ = kChunks * kN * 128;
@@ -137,13 +137,13 @@ struct Lay {
   // What beginning another query tile costs a CTA, in key tiles (its queries, the sums
   // of the one before): the runs are cut as if each query tile had this many more.
   // us with 0, 1, 2, 3, 4 and 6 of them (r. = ragged, 16 heads):
-  //   fp8  16  64 r. e4m3 decodes           62.1 61.2 60.8 60.2 60.0 61.0
-  //   fp8  32  32 r. verifications of 4     56.6 55.2 53.3 52.4 50.6 48.2
-  //            32 r. verifications of 2     37.0 36.8 35.5 34.4 33.9 31.9
-  //   bf16 16  64 r. decodes               103.7 103.5 103.7 104.1 104.4 105.3
-  //   bf16 32  32 r. verifications of 2     45.5 45.4 43.1 42.2 41.8 42.6
-  //   bf16 64  16 r. decodes, 128 heads     48.1 47.4 46.1 47.1 47.0 46.3
-  //            32 r. verifications of 4     55.7 55.7 53.1 52.0 50.9 51.2
+  //   fp8  16  64 r. e4m3 decodes           62.4 60.9 60.3 59.6 59.5 60.3
+  //   fp8  32  32 r. verifications of 4     51.4 50.6 48.1 46.5 45.7 45.3
+  //            32 r. verifications of 2     33.7 32.6 31.4 30.7 30.4 30.0
+  //   bf16 16  64 r. decodes               104.9 104.7 105.1 105.6 106.1 106.7
+  //   bf16 32  32 r. verifications of 2     41.4 40.6 40.3 40.6 40.6 41.0
+  //   bf16 64  16 r. decodes, 128 heads     46.0 44.9 43.5 44.2 44.2 44.1
+  //            32 r. verifications of 4     48.9 48.0 46.3 45.8 46.0 47.2
   static constexpr int kSwitch = kF8 ? (NR == 16 ? 3 : 6) : (NR == 16 ? 1 : 2);
   // The reference of a row's weights is the next whole number (log2) above its maximum
   // less kTop; a score may pass the reference by kGrow before the sums are rescaled.
@@ -536,8 +536,9 @@ __device__ __forceinline__ uint32_t produce(const LatentAttnArgs& a, const CUten
         // Rows of mixed tiles are looked at for NaNs and infinities: in shared memory once they are
         // there, or, in tiles of 16 query rows without masks, where mixed tiles are few, in the
         // cache before they are stored.  (us with the first and the second: 32 verifications of 4
-        // tokens 45.6, 46.7, chunks of 1024 tokens 633, 641, 16 trees of 61 tokens 241, 286 with the
-        // masks' words loaded one by one; 64 ragged e4m3 decodes, which have no mixed tile, 60.8, 59.7.)
+        // tokens 46.3, 49.7, e5m2 45.3, 46.5, chunks of 1024 tokens 632, 641, 16 trees of 61 tokens
+        // 241, 286 with the masks' words loaded one by one; 64 ragged e4m3 decodes, which have no
+        // mixed tile, 60.9, 59.7.)
         constexpr bool kInPlace = TREE || NR > 16;
 #pragma unroll 1
         for (int i = 0; i < kRows; ++i) {
@@ -1425,8 +1426,8 @@ __global__ void __launch_bounds__(Lay<FMT, NR>::kThreads, 1)
 // for every row).  So a block mostly costs two dependent loads, whatever the batch, and
 // the grid, NR / 8 blocks per CTA, is one to four rounds of resident blocks.  With NR / 4
 // and the rows of few partials left to the first CTA's, most blocks found nothing to do:
-// 32 verifications took 48.5 us (48.2 now), 16 decodes of 128 heads 47.3 (46.1), one
-// decode 10.7 (10.3).
+// 32 verifications took 48.5 us instead of 48.2, 16 decodes of 128 heads 47.3 instead of
+// 46.1, one decode 10.7 instead of 10.3 (all before later steps).
 constexpr int kJoinGroups = 4;
 constexpr int kJoinThreads = kJoinGroups * 128;
 constexpr int kFewParts = 8;
@@ -1568,11 +1569,11 @@ cudaError_t launch_f(LatentAttnArgs a, int ctas, const LaunchCfg& cfg) {
   for (int rows = a.box_rows; rows != 0 && rows < kKeys; rows *= 2) ++a.box_shift;
   const int nr = attention_tile_rows(a.num_tokens, a.num_heads, a.num_seqs, kF8);
   // Cache rows that up to four query tiles of a sequence read (at about the same time) are
-  // the first to leave L2: 64 ragged decodes 60.5 us (62.9 without the hint), in bf16 103.5
-  // (107.3), 32 verifications 48.2 (50.5), 16 decodes of 128 heads 46.1 (46.9).  The many
-  // query tiles of a prefill want them kept: 2 chunks of 1024 tokens 645 us (699 with the
-  // hint).  16 bf16 sequences over 8192 rows at 2, 4, 8 and 16 query tiles each: 73.7, 121.8,
-  // 219.7 and 415 us with it, 74.0, 121.4, 213.6 and 391 without.
+  // the first to leave L2: 64 ragged decodes 59.7 us (62.6 without the hint), in bf16 104.7
+  // (108.5), 32 verifications 45.3 (46.0), in bf16 46.3 (50.6), 16 decodes of 128 heads 43.5
+  // (44.2).  The many query tiles of a prefill want them kept: 2 chunks of 1024 tokens 632 us
+  // (678 with the hint).  16 bf16 sequences over 8192 rows at 2, 4, 8 and 16 query tiles each:
+  // 65.6, 112.4, 207.7 and 409 us with it, 66.0, 114.9, 207.8 and 381 without.
   a.stream_rows = (int64_t)a.num_tokens * a.num_heads <= (int64_t)4 * nr * a.num_seqs;
   switch (nr) {
     case 16: return launch_t<FMT, 16, TREE>(a, map, ctas, cfg);

@@ -18,10 +18,11 @@
 // full: per query tile S of 64 columns, P of 32, O of 128 and the queries' rotary columns, 32.  The
 // weights' warps read the whole of S before they compute, so that the next scores come meanwhile.
 //
-// Measured (replayed from a graph, 16 heads): one prompt of 16384 tokens 961 us (1430 TFLOP/s), of
-// 300 tokens 11.8 us; 16 prompts of 37 to 2048 tokens 141 us; 1024 new tokens of 2 sequences over
-// 8192 e4m3 rows each 150 us (1140 TFLOP/s); single tokens of 32 sequences over 500 to 4096 rows
-// 133 us (5.8 TB/s).
+// Measured (replayed from a graph, 16 heads): one prompt of 16384 tokens 950 us (1450 TFLOP/s; 950
+// to 990 from one GPU to another), of 300 tokens 11.9 us; 16 prompts of 37 to 2048 tokens 142 us;
+// 1024 new tokens of 2 sequences over 8192 e4m3 rows each 151 us (1140 TFLOP/s); single tokens of
+// 32 sequences over 500 to 4096 rows 133 us (5.8 TB/s), over as many e4m3 rows 149 us (2.6 TB/s:
+// a unit of one query row still pays the widening and products of 128 rows).
 //
 // Why 64 keys.  Beside the queries (96 KB) there is room for 1.6 units of 128 keys, and K of a
 // unit came later than the products before it were done (2000 cycles for 32 KB; 16384 tokens
@@ -42,14 +43,20 @@
 // power of two per row, in place.
 //
 // Roles (13 warps): 4 warps per query tile compute weights, a thread a row (running maximum;
-// O is rescaled only when one has grown by more than 2^kGrow, and only that row's) and write the output; two per
-// tile issue the products, scores and outputs; one plans the CTA's items, describes them to the
-// others in shared memory and loads Q, K and V.  V rows that not every row of an item sees are
-// looked after by the scores' warps, half a tile each, ahead of their products (16 ragged prompts
-// 154 us; 156 by the outputs' warps; 180 by the weights' warps, before the weights): those behind
-// the sequence are zeroed (they may hold anything), those with a NaN or an infinity too, and noted,
-// so that the sums of the rows that see them become NaN.  With fp8, three more warps widen the
-// codes and look after V on the way.
+// O is rescaled only when one has grown by more than 2^kGrow, and only that row's) and write the
+// output; two per tile issue the products, scores and outputs; one plans the CTA's items, describes
+// them to the others in shared memory and loads Q, K and V.  V rows that not every row of an item
+// sees are looked after by the scores' warps, half a tile each, ahead of their products (16 ragged
+// prompts 154 us; 156 by the outputs' warps; 180 by the weights' warps, before the weights): those
+// behind the sequence are zeroed (they may hold anything), those with a NaN or an infinity too, and
+// noted, so that the sums of the rows that see them become NaN.  With fp8, three more warps widen
+// the codes and look after V on the way.
+//
+// Weights are 16-bit operands, as the tensor core takes them beside 16-bit values: bf16 ones (2^-8
+// of themselves, as the bf16 result) beside bf16, fp16 ones (2^-11) beside fp16 and widened fp8.
+// Against 64 bits a bf16 call is off by 0.0021 to 0.0024, relative, where weights in 32 bits would
+// give 0.0016; a second bf16 part of each weight would be another product per unit.  Scores, sums
+// and references are fp32.
 //
 // Code that runs once an item is as short as it can be: the roles' loops push it out of the
 // instruction caches, and each of its instructions takes about 40 cycles.
@@ -83,19 +90,29 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // What beginning another item costs a CTA, in units: the runs are cut as if each item had
 // this many more.  An item's change takes about 7000 cycles (the last output's way out, then the
-// next scores' weights) where a unit takes 1600 to 2000.  4 ragged prompts of grouped heads 183 us
-// with 2 and 172 with 4, 16 ragged prompts 143 and 140, 16384 tokens 949 and 941.
+// next scores' weights) where a unit takes 1600 to 2000.  With 2 and 4, medians of 5: 4 ragged
+// prompts of grouped heads 182 us (180 to 183) and 175 (174 to 178), 16 ragged prompts 144.8 and
+// 142.2, 6 chunks of 300 to 900 tokens over up to 4109 rows 92.0 and 90.3, 32 single tokens over
+// e4m3 rows 150.7 and 149.4; where items are long or few the other way round, and less: 24 fp16
+// prompts of up to 1300 tokens, 8 heads, 72.6 and 73.7, 21 of up to 503, 2 heads, 17.2 and 17.7.
 constexpr int kSwitch = 4;
 // A CTA takes at least this many units, so that a short call is not cut into runs that are all
-// beginning and join: 21 prompts of 6 to 503 tokens, 2 heads, 18.1 us with 4 and 20.3 with 8.
+// beginning and join: 21 prompts of 6 to 503 tokens, 2 heads, 17.7 us with 4 and 19.7 with 8.
 constexpr int kMinUnits = 4;
 // A sequence of at most this many items (of a key head) is counted by one lane, beside 31 others; a
-// longer one by the whole warp.  16 prompts of up to 8 items: 141.9 us with 4, 140.1 with 12.
+// longer one by the whole warp.  With 4 and 12: 16 prompts of up to 8 items 144.0 and 142.2 us, 24
+// of up to 6 75.0 and 73.7; 4 of 22 to 47 items, which neither deals to a lane, the same within
+// their spread (172 to 178).
 constexpr int kFewItems = 12;
 // Calls of at most this many key rows, and of no more items than CTAs, give every CTA a whole
-// item: nothing is cut, and nothing has to be joined.  Whole against cut, 16 heads: 300 tokens
-// 11.8 and 15.6 us, 500 tokens 15.2 and 16.4, 700 tokens 17.1 and 18.5, 1000 tokens 22.4 and 21.5
-// (one CTA then does 16 units in turn).
+// item: nothing is cut, and nothing has to be joined.  Whole against cut, one prompt (us):
+//   tokens       100         300         500         600         700         768
+//   1 head    7.9  11.4  11.5  13.8  14.6  15.5  14.9  15.0  16.0  15.0  18.0  15.7
+//   4 heads   8.0  11.7  11.5  15.3  15.1  15.9  15.3  16.1  16.5  15.8  18.1  16.0
+//   16 heads  8.2  12.0  11.9  15.9  15.4  16.5  15.8  18.0  17.1  18.4  19.2  18.3
+// and 8 prompts of 40 to 96, 1 head 8.3 and 12.1.  (With few heads a limit of 600 would do better
+// by up to 2 us, with 16 worse by 1.4: whole items are one CTA's units in turn, cut ones a second
+// launch and, with many heads, more of them than CTAs.)
 constexpr int kWholeKeys = 768;
 
 // The reference of a row's weights is the next whole number (log2) above its maximum less
@@ -1277,7 +1294,6 @@ bool make_map(CUtensorMap* map, const void* base, int fmt, int width, int64_t hs
       *z_head = 1;
     }
   }
-  if (dims[0] > INT32_MAX) return false;
   const cuuint32_t box[3] = {is16(fmt) ? 64u : (cuuint32_t)width, kKeys, 1}, unit[3] = {1, 1, 1};
   const CUtensorMapDataType type = fmt == kBF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                    : fmt == kF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
